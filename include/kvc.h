@@ -57,7 +57,7 @@
 extern "C" {
 #endif
 
-#define KVC_VERSION 10100  /* major*10000 + minor*100 + patch */
+#define KVC_VERSION 10200  /* major*10000 + minor*100 + patch */
 
 /* Exported symbols (the library is built with hidden default visibility). */
 #if defined(__GNUC__)
@@ -488,6 +488,163 @@ KVC_API kvc_status kvc_decode_attend_noalloc(const kvc_params *p, int32_t t,
                                              const kvc_cache *cache, float *lse,
                                              float *f_all, double *probs,
                                              int32_t *device_status, void *stream);
+
+/* ------------------------------------------------------------------ */
+/* drafted tokens (speculative decoding over the budgeted cache)        */
+/* ------------------------------------------------------------------ */
+
+/*
+ * One verification of a tree of drafted tokens takes three calls:
+ *   kvc_tree_attend   every drafted token attends over the cache and the
+ *                     drafted tokens its mask shows; the cache does not
+ *                     change;
+ *   (the caller samples and accepts a path of the tree)
+ *   kvc_tree_weights  the attention weight the accepted tokens gave to every
+ *                     slot (from the lse of the first call);
+ *   kvc_tree_commit   appends the accepted tokens, updates the utilities with
+ *                     those weights and evicts down to the budget.
+ * The pages decode one token per step; a verification step of several tokens
+ * is this library's own extension of their definitions, cited per call.
+ * A tree belongs to a sequence: `units` consecutive units (NL * Hkv of one
+ * call, Hkv when the layers are called one by one) share its mask and path.
+ * The calls may alternate with kvc_decode_step on the same cache.
+ */
+typedef struct {
+    int32_t T;              /* drafted tokens per tree, 1..64: the row stride of
+                               q, k_tree, v_tree, o, lse and mask            */
+    int32_t units;          /* units per tree; unit u belongs to tree
+                               u / units; U is a multiple of units           */
+    const uint64_t *mask;   /* DEVICE [U/units][T]: bit j of token i's word is
+                               set when i attends drafted token j (its
+                               ancestors and itself; any mask is allowed)    */
+    const int32_t *n;       /* DEVICE [U/units] live tokens of each tree, 0..T,
+                               or NULL = T.  Tokens at or behind it do not
+                               exist: their rows of the inputs are not used
+                               (they may hold anything, NaN included), their
+                               rows of the outputs are left as they were     */
+} kvc_tree;
+
+typedef struct {
+    int32_t A;              /* row stride of token and row_weight, 1..T      */
+    const int32_t *token;   /* DEVICE [U/units][A] the accepted tokens, in the
+                               order they are appended (root first)          */
+    const int32_t *n;       /* DEVICE [U/units] accepted tokens, 0..A        */
+    const int32_t *pos;     /* DEVICE [U/units] position of the first of them;
+                               the j-th has pos + j                          */
+} kvc_path;
+
+/* Bytes of workspace kvc_tree_attend and kvc_tree_weights need for trees of
+ * T tokens (0: invalid parameters).  Its first 256 bytes hold the status word
+ * kvc_get_device_status reads: zero them once before the first call.  The
+ * rest is scratch of one call; calls that overlap on the GPU need a workspace
+ * each. */
+KVC_API size_t kvc_tree_workspace_size(const kvc_params *p, int32_t T);
+
+/*
+ * kvc_tree_attend -- attention of drafted tokens over the cache and their
+ * tree, with the normalization correction.
+ *
+ * Defined by: MomentKV sec 2 and KeepKV eq 6 as in kvc_decode_attend;
+ * MomentKV sec 4.1 eq 9, sec 4.2 eqs 10-12, App. C.2 as in kvc_correct.
+ * For unit u (n = len[u]), live drafted token t and query head h:
+ *   x_i = q_th . k_i / sqrt(d) + ln p_i      cache slots i in [0, n)
+ *   y_j = q_th . k_tree_j / sqrt(d)          live j with bit j of mask[t]
+ *   lse = log(sum_i exp(x_i) + sum_j exp(y_j)),
+ *   f   = (sum_i exp(x_i) v_i + sum_j exp(y_j) v_tree_j) / exp(lse)
+ *   o   = f without moments (mom NULL, p->correction = KVC_CORR_OFF, or
+ *         n_e[u] = 0); otherwise w f + (1 - w) fhat, with
+ *         fhat = mu_v + C q / sqrt(d)  (KVC_CORR_ZERO_ORDER: mu_v),
+ *         w = 1 / (1 + exp(ln n_e + q . mu_k / sqrt(d) - lse)).
+ *   A row that sees nothing (empty cache, no bit) has lse = -inf, f = 0 (and
+ *   o = fhat with moments).
+ * What a row does not see does not reach it, NaN and infinities included.
+ * q [U][T][G][d], k_tree, v_tree [U][T][d] bf16; o [U][T][G][d] bf16 (the
+ * type the output projection reads; fp32 until that one rounding, the
+ * softmax weights rounded to bf16 for the tensor cores), lse [U][T][G] fp32.
+ * Reads K, V, votes and len of the cache.  max_len >= len[u] bounds the
+ * launch.  Device-side errors, which leave the unit's outputs untouched:
+ * KVC_ERR_SHAPE (len[u] outside [0, max_len]), KVC_ERR_INVALID_ARG (live
+ * tokens outside [0, T]).
+ */
+KVC_API kvc_status kvc_tree_attend(const kvc_params *p, int32_t max_len, const kvc_tree *tree,
+                                   const uint16_t *q, const uint16_t *k_tree,
+                                   const uint16_t *v_tree, const kvc_cache *cache,
+                                   const kvc_moments *mom, uint16_t *o, float *lse, void *ws,
+                                   size_t ws_bytes, void *stream);
+
+/*
+ * kvc_tree_weights -- accumulated attention weight of the accepted tokens.
+ *
+ * Defined by: InertiaKV sec 3.1 eq 1 (head-mean probability), summed over the
+ * accepted tokens with weights w_j = row_weight[j] (KeepKV reading notes eq
+ * 15 has such a windowed sum; NULL = 1, the plain accumulation).
+ * With the accepted tokens c_0 .. c_{a-1} of unit u's tree and lse from
+ * kvc_tree_attend of the same tree:
+ *   S[u][i]     = sum_j w_j (1/G) sum_h exp(x_{c_j h i} - lse_{c_j h}),
+ *                 i in [0, n) with x as above;
+ *   S[u][n + r] = sum over the j whose mask shows c_r of
+ *                 w_j (1/G) sum_h exp(q_{c_j h} . k_tree_{c_r} / sqrt(d)
+ *                 - lse_{c_j h}),  r in [0, a)
+ * (where kvc_tree_commit appends c_r).  Entries from n + a on are left as
+ * they were; a = 0 gives S = 0 on [0, n).  Rows with lse = -inf give nothing.
+ * row_weight: DEVICE [U/units][A] fp32, >= 0 (a negative weight gives NaN).
+ * S [U][cap] fp32; a weight below fp32's range is 0.  The logits are formed
+ * again from the keys (256 bytes per slot): which rows count is known only
+ * after the verification, and keeping all T G logits per slot would move
+ * more.  max_len >= len[u].  Device-side errors, which leave the unit's
+ * entries untouched: KVC_ERR_SHAPE (len[u] outside [0, max_len], or len[u] +
+ * a > cap), KVC_ERR_INVALID_ARG (a outside [0, A], an accepted token that is
+ * not live, live tokens outside [0, T]).
+ */
+KVC_API kvc_status kvc_tree_weights(const kvc_params *p, int32_t max_len, const kvc_tree *tree,
+                                    const kvc_path *path, const float *row_weight,
+                                    const uint16_t *q, const uint16_t *k_tree, const float *lse,
+                                    const kvc_cache *cache, float *S, void *ws, size_t ws_bytes,
+                                    void *stream);
+
+/*
+ * kvc_tree_commit -- append the accepted tokens and evict by accumulated
+ * attention weight.
+ *
+ * Defined by: InertiaKV sec 3.1 eqs 2-4 and MomentKV Algorithm 1 as in
+ * kvc_aggregate_evict, kvc_moment_update and kvc_compact, for a step that
+ * appends a >= 0 tokens: the verification is one observation of weight S.
+ * For unit u, n = len[u]:
+ *   slots n .. n+a-1 receive the accepted tokens (k_tree, v_tree rows, vote
+ *     1, positions pos + j, unscored);
+ *   with S (from kvc_tree_weights): util of every slot i < n + a becomes S_i
+ *     when unscored or under KVC_RULE_SINGLE, util + S_i (KVC_RULE_CUMULATIVE)
+ *     or alpha util + (1 - alpha) S_i (KVC_RULE_EMA).  Without (S = NULL, a
+ *     verification that does not refresh): utilities stay, the accepted
+ *     tokens are unscored (protected);
+ *   k = max(0, n + a - budget) victims: the lowest (util, pos) pairs among
+ *     the scored slots, ties of both to the lower slot; evict_idx / evict_pos
+ *     (optional, [U][kmax]) receive their slots and positions in ascending
+ *     slot order, n_evict[u] = k;
+ *   the victims are folded into the moments, weighted by their votes (mom
+ *     NULL: they are dropped);
+ *   with n' = n + a - k: the r-th victim slot below n' receives the r-th
+ *     other slot at or above n' (kvc_compact's rule), len[u] = n'.  Slots at
+ *     or behind n' are not written, except that the utilities of slots below
+ *     the old n are updated.
+ * Not combined with merging, KVC_RULE_MI (its score is not an attention
+ * weight alone) or KVC_RULE_EMA_CHAINED (KVC_ERR_UNSUPPORTED).  kmax in
+ * [1, 64] (KVC_ERR_UNSUPPORTED above: bring a cache that far over its budget
+ * down with kvc_decode_step or kvc_aggregate_evict first).  max_len >=
+ * len[u] on entry.  ws: the decode stream's workspace
+ * (kvc_decode_workspace_size); the victim queue it keeps for lazy steps is
+ * dropped.  Device-side errors, which leave the unit as it was with
+ * n_evict = 0: KVC_ERR_SHAPE (len[u] outside [0, max_len], len[u] + a > cap,
+ * budget[u] outside [1, L], k > kmax), KVC_ERR_INVALID_ARG (the path, as in
+ * kvc_tree_weights; fewer than k scored slots, which is seen once the
+ * utilities are updated).
+ */
+KVC_API kvc_status kvc_tree_commit(const kvc_params *p, int32_t max_len, const kvc_tree *tree,
+                                   const kvc_path *path, const uint16_t *k_tree,
+                                   const uint16_t *v_tree, const float *S,
+                                   const kvc_cache *cache, const kvc_moments *mom, int32_t kmax,
+                                   int32_t *evict_idx, int32_t *evict_pos, int32_t *n_evict,
+                                   void *ws, size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------------ */
 /* prefill -> decode hand-off                                           */

@@ -1,0 +1,64 @@
+// kvc_tree.h -- shared by the drafted-token entry points (kvc_tree_attend,
+// kvc_tree_weights, kvc_tree_commit): device-side checks, workspace carve-up
+// and launchers.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "kvc_common.cuh"
+#include "kvc_internal.h"
+
+namespace kvc {
+
+constexpr int kTreeMax = 64;          // drafted tokens per tree (one mask word)
+
+// Device views of a tree and of an accepted path.
+struct TreeArgs {
+    const uint64_t *mask;             // [trees][T]
+    const int32_t *n;                 // [trees] or NULL
+    int T, units;
+};
+
+struct PathArgs {
+    const int32_t *token, *n, *pos;   // [trees][A], [trees], [trees]
+    int A;
+};
+
+// Live drafted tokens of unit u's tree, or -1 when outside [0, T].
+__device__ __forceinline__ int tree_live(const TreeArgs &t, int u)
+{
+    const int n = t.n ? t.n[u / t.units] : t.T;
+    return n < 0 || n > t.T ? -1 : n;
+}
+
+// Accepted tokens of unit u's path, or -1 when the path is not one: a count
+// outside [0, A] or a token that is not live.  Warp-wide; every lane gets the
+// answer.
+__device__ __forceinline__ int path_count(const TreeArgs &t, const PathArgs &p, int u, int lane)
+{
+    const int b = u / t.units, live = tree_live(t, u), a = p.n[b];
+    if (live < 0 || a < 0 || a > p.A) return -1;
+    bool bad = false;
+    for (int j = lane; j < a; j += 32) {
+        const int c = p.token[(size_t)b * p.A + j];
+        bad |= c < 0 || c >= live;
+    }
+    return __any_sync(kFull, bad) ? -1 : a;
+}
+
+cudaError_t launch_tree_attend(const kvc_params &p, int max_len, const TreeArgs &t,
+                               const uint16_t *q, const uint16_t *kt, const uint16_t *vt,
+                               const kvc_cache &c, const kvc_moments *m, uint16_t *o, float *lse,
+                               void *ws, cudaStream_t st);
+cudaError_t launch_tree_weights(const kvc_params &p, int max_len, const TreeArgs &t,
+                                const PathArgs &a, const float *row_weight, const uint16_t *q,
+                                const uint16_t *kt, const float *lse, const kvc_cache &c, float *S,
+                                void *ws, cudaStream_t st);
+cudaError_t launch_tree_commit(const kvc_params &p, int max_len, const TreeArgs &t,
+                               const PathArgs &a, const uint16_t *kt, const uint16_t *vt,
+                               const float *S, const kvc_cache &c, const kvc_moments *m, int kmax,
+                               int32_t *evict_idx, int32_t *evict_pos, int32_t *n_evict,
+                               const DecodeWs &ws, cudaStream_t st);
+size_t tree_ws_bytes(const kvc_params &p, int T);
+
+}  // namespace kvc

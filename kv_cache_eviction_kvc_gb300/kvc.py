@@ -23,6 +23,7 @@ STATUS_NAMES = {0: "KVC_OK", 1: "KVC_ERR_INVALID_ARG", 2: "KVC_ERR_SHAPE",
 RULE_SINGLE, RULE_CUMULATIVE, RULE_EMA, RULE_MI, RULE_EMA_CHAINED = 0, 1, 2, 3, 4
 CORR_OFF, CORR_ZERO_ORDER, CORR_FIRST_ORDER = 0, 1, 2
 ALLOC_GLOBAL, ALLOC_LAYER, ALLOC_HEAD = 0, 1, 2
+TREE_MAX = 64      # most drafted tokens per tree, most victims per commit
 
 EXPORTED = (
     "kvc_version", "kvc_last_error", "kvc_status_string",
@@ -31,6 +32,7 @@ EXPORTED = (
     "kvc_compact", "kvc_zip_merge", "kvc_mi_scores", "kvc_mi_evict", "kvc_decode_step", "kvc_decode_attend_noalloc", "kvc_prefill_prepare",
     "kvc_prefill_workspace_size", "kvc_prefill_score", "kvc_prefill_window_attention",
     "kvc_prefill_snapkv", "kvc_prefill_handoff_workspace_size", "kvc_prefill_handoff",
+    "kvc_tree_workspace_size", "kvc_tree_attend", "kvc_tree_weights", "kvc_tree_commit",
 )
 
 
@@ -59,6 +61,16 @@ class kvc_moments(ctypes.Structure):
                 ("mu_v", ctypes.c_void_p), ("C", ctypes.c_void_p)]
 
 
+class kvc_tree(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("units", ctypes.c_int32), ("mask", ctypes.c_void_p),
+                ("n", ctypes.c_void_p)]
+
+
+class kvc_path(ctypes.Structure):
+    _fields_ = [("A", ctypes.c_int32), ("token", ctypes.c_void_p), ("n", ctypes.c_void_p),
+                ("pos", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -79,6 +91,7 @@ def load(build: bool = True):
     PP = ctypes.POINTER(kvc_params)
     PC = ctypes.POINTER(kvc_cache)
     PM = ctypes.POINTER(kvc_moments)
+    PT, PA = ctypes.POINTER(kvc_tree), ctypes.POINTER(kvc_path)
     sigs = {
         "kvc_version": (I32, []),
         "kvc_last_error": (ctypes.c_char_p, []),
@@ -106,6 +119,10 @@ def load(build: bool = True):
         "kvc_prefill_handoff": (I32, [PP, I32, P, P, P, P, P, PC, PM, P, P, SZ, P]),
         "kvc_prefill_snapkv": (I32, [I32, I32, I32, I32, I32, I32, I64, I32, I32, P, P, P, P, P,
                                      P, P, SZ, P]),
+        "kvc_tree_workspace_size": (SZ, [PP, I32]),
+        "kvc_tree_attend": (I32, [PP, I32, PT, P, P, P, PC, PM, P, P, P, SZ, P]),
+        "kvc_tree_weights": (I32, [PP, I32, PT, PA, P, P, P, P, PC, P, P, SZ, P]),
+        "kvc_tree_commit": (I32, [PP, I32, PT, PA, P, P, P, PC, PM, I32, P, P, P, P, SZ, P]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -302,6 +319,111 @@ def kvc_decode_attend_noalloc(p, t, new_pos, max_len, q, k_new, v_new, cache: kv
         _ptr(lse, torch.float32, "lse"), _ptr(f_all, torch.float32, "f_all"),
         _ptr(probs, torch.float64, "probs", optional=True),
         _ptr(device_status, torch.int32, "device_status", optional=True), _stream(stream)))
+
+
+# ------------------------------------------------------------------ drafted tokens
+
+def _sized(t, dtype, name, numel, device, optional=False):
+    """_ptr with the element count and the device checked: a row stride or a
+    unit count that does not fit the tensor is an error here, not a read out
+    of range on the device."""
+    ptr = _ptr(t, dtype, name, optional)
+    if t is not None:
+        if t.numel() < numel:
+            raise ValueError(f"{name} has {t.numel()} elements, needs {numel}")
+        if t.device.index != device:
+            raise ValueError(f"{name} must live on the current device cuda:{device}, not {t.device}")
+    return ptr
+
+
+def make_tree(T, units, mask, n=None) -> kvc_tree:
+    """A tree of T drafted tokens per sequence, shared by `units` consecutive
+    units.  mask: int64 [trees][T], bit j of row i set when token i attends
+    drafted token j; n: int32 [trees] live tokens or None (= T).  The tensors
+    are kept alive with the structure."""
+    T, units = int(T), int(units)
+    if mask is None or mask.dim() != 2 or mask.shape[1] != T:
+        raise ValueError(f"mask must be [trees][T = {T}]")
+    trees, dev = mask.shape[0], mask.device.index
+    tr = kvc_tree(T, units, _sized(mask, torch.int64, "mask", trees * T, dev),
+                  _sized(n, torch.int32, "n", trees, dev, optional=True))
+    tr.trees, tr.keep = trees, (mask, n)
+    return tr
+
+
+def make_path(A, token, n, pos) -> kvc_path:
+    """The accepted tokens of every tree: token int32 [trees][A] (root first),
+    n int32 [trees] how many of them, pos int32 [trees] the position of the
+    first.  The tensors are kept alive with the structure."""
+    A = int(A)
+    if token is None or token.dim() != 2 or token.shape[1] != A:
+        raise ValueError(f"token must be [trees][A = {A}]")
+    trees, dev, i32 = token.shape[0], token.device.index, torch.int32
+    pa = kvc_path(A, _sized(token, i32, "token", trees * A, dev),
+                  _sized(n, i32, "n", trees, dev), _sized(pos, i32, "pos", trees, dev))
+    pa.trees, pa.keep = trees, (token, n, pos)
+    return pa
+
+
+def _tree_device(p, tree, path=None):
+    """The current device; the tree (and path) must live there and cover the units."""
+    dev = torch.cuda.current_device()
+    for x in (tree, path) if path is not None else (tree,):
+        if x.keep[0].device.index != dev:
+            raise ValueError(f"the tree and path must live on the current device cuda:{dev}")
+        if tree.units < 1 or x.trees * tree.units < p.U:
+            raise ValueError(f"{x.trees} trees of {tree.units} units do not cover U = {p.U}")
+    return dev
+
+
+def kvc_tree_workspace_size(p: kvc_params, T: int) -> int:
+    return int(load().kvc_tree_workspace_size(ctypes.byref(p), int(T)))
+
+
+def kvc_tree_attend(p, max_len, tree: kvc_tree, q, k_tree, v_tree, cache: kvc_cache, mom, o, lse,
+                    ws, stream=None):
+    """mom: kvc_moments or None (no correction)."""
+    bf, dev = torch.bfloat16, _tree_device(p, tree)
+    rows = p.U * tree.T
+    _check(load().kvc_tree_attend(
+        ctypes.byref(p), int(max_len), ctypes.byref(tree),
+        _sized(q, bf, "q", rows * p.G * p.d, dev), _sized(k_tree, bf, "k_tree", rows * p.d, dev),
+        _sized(v_tree, bf, "v_tree", rows * p.d, dev), ctypes.byref(cache),
+        None if mom is None else ctypes.byref(mom), _sized(o, bf, "o", rows * p.G * p.d, dev),
+        _sized(lse, torch.float32, "lse", rows * p.G, dev), _sized(ws, torch.uint8, "ws", 0, dev),
+        ws.numel(), _stream(stream)))
+
+
+def kvc_tree_weights(p, max_len, tree: kvc_tree, path: kvc_path, row_weight, q, k_tree, lse,
+                     cache: kvc_cache, S, ws, stream=None):
+    """row_weight: fp32 [trees][A] or None (all 1)."""
+    bf, f32, dev = torch.bfloat16, torch.float32, _tree_device(p, tree, path)
+    rows = p.U * tree.T
+    _check(load().kvc_tree_weights(
+        ctypes.byref(p), int(max_len), ctypes.byref(tree), ctypes.byref(path),
+        _sized(row_weight, f32, "row_weight", p.U // tree.units * path.A, dev, optional=True),
+        _sized(q, bf, "q", rows * p.G * p.d, dev), _sized(k_tree, bf, "k_tree", rows * p.d, dev),
+        _sized(lse, f32, "lse", rows * p.G, dev), ctypes.byref(cache),
+        _sized(S, f32, "S", p.U * p.cap, dev), _sized(ws, torch.uint8, "ws", 0, dev), ws.numel(),
+        _stream(stream)))
+
+
+def kvc_tree_commit(p, max_len, tree: kvc_tree, path: kvc_path, k_tree, v_tree, S,
+                    cache: kvc_cache, mom, kmax, evict_idx, evict_pos, n_evict, ws, stream=None):
+    """S: fp32 [U][cap] from kvc_tree_weights or None (no refresh); mom:
+    kvc_moments or None; evict_idx, evict_pos: int32 [U][kmax] or None."""
+    bf, i32, dev = torch.bfloat16, torch.int32, _tree_device(p, tree, path)
+    rows = p.U * tree.T
+    _check(load().kvc_tree_commit(
+        ctypes.byref(p), int(max_len), ctypes.byref(tree), ctypes.byref(path),
+        _sized(k_tree, bf, "k_tree", rows * p.d, dev),
+        _sized(v_tree, bf, "v_tree", rows * p.d, dev),
+        _sized(S, torch.float32, "S", p.U * p.cap, dev, optional=True), ctypes.byref(cache),
+        None if mom is None else ctypes.byref(mom), int(kmax),
+        _sized(evict_idx, i32, "evict_idx", p.U * int(kmax), dev, optional=True),
+        _sized(evict_pos, i32, "evict_pos", p.U * int(kmax), dev, optional=True),
+        _sized(n_evict, i32, "n_evict", p.U, dev), _sized(ws, torch.uint8, "ws", 0, dev),
+        ws.numel(), _stream(stream)))
 
 
 # ------------------------------------------------------------------ prefill

@@ -1,0 +1,609 @@
+"""GPU tests of the drafted-token calls (kvc_tree_attend, kvc_tree_weights,
+kvc_tree_commit) against their definitions in 64 bits (tree_ref.py): head
+layouts, lengths from zero on, ragged trees and budgets, masks that leave rows
+empty, NaN where nothing looks, ties, every rule; then runs of the three
+together against the one-token calls, streams and graphs."""
+import numpy as np
+import pytest
+import torch
+
+import tree_ref as R
+from kv_cache_eviction_kvc_gb300 import kvc as K
+from kv_cache_eviction_kvc_gb300.state import DecodeState
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+DEV = "cuda"
+NAN = float("nan")
+
+
+def bf(x):
+    return torch.from_numpy(np.ascontiguousarray(x, dtype=np.float32)).to(torch.bfloat16)
+
+
+def f64(t):
+    return t.detach().cpu().to(torch.float64).numpy()
+
+
+def tree_masks(rng, B, T, kind):
+    out = np.zeros((B, T), dtype=np.uint64)
+    for b in range(B):
+        for i in range(T):
+            own = np.uint64(1) << np.uint64(i)
+            if kind == "chain":
+                out[b, i] = (out[b, i - 1] if i else np.uint64(0)) | own
+            elif kind == "tree":
+                out[b, i] = (out[b, rng.integers(max(0, i - 4), i)] if i else np.uint64(0)) | own
+            elif kind == "none":
+                out[b, i] = 0
+            else:                                      # any bits, rows without one among them
+                out[b, i] = np.uint64(rng.integers(0, 1 << 63)) if rng.random() < 0.8 else 0
+    return out
+
+
+class Case:
+    """Inputs of one verification on both sides; rows nobody may look at are NaN."""
+
+    def __init__(self, seed, per, G, T, lens, kind="tree", live=None, votes=False, moments=False,
+                 correction=K.CORR_FIRST_ORDER, cap=None, rule="ema", L=None, budget=None,
+                 q_scale=1.5, unscored=False):
+        rng = self.rng = np.random.default_rng(seed)
+        U = self.U = len(lens)
+        B = self.B = U // per
+        self.per, self.G, self.T, self.lens = per, G, T, list(lens)
+        cap = self.cap = cap or max(lens) + T + 3
+        self.live = list(live) if live is not None else [T] * B
+        self.mask = tree_masks(rng, B, T, kind)
+        D = R.D
+        off = rng.standard_normal((U, 1, D))
+        self.K = off + rng.standard_normal((U, cap, D))
+        self.V = 0.5 + rng.standard_normal((U, cap, D))
+        self.kt = off + rng.standard_normal((U, T, D))
+        self.vt = 0.5 + rng.standard_normal((U, T, D))
+        self.q = q_scale * rng.standard_normal((U, T, G, D))
+        for u in range(U):
+            self.K[u, lens[u]:], self.V[u, lens[u]:] = NAN, NAN
+            t = self.live[u // per]
+            self.kt[u, t:], self.vt[u, t:], self.q[u, t:] = NAN, NAN, NAN
+        self.votes = rng.integers(1, 9, (U, cap)).astype(np.int32) if votes else None
+        self.pos = np.stack([rng.permutation(cap) for _ in range(U)]).astype(np.int32)
+        self.util = np.exp(rng.standard_normal((U, cap)) * 2)
+        if unscored:
+            self.util[rng.random((U, cap)) < 0.3] = np.inf
+        self.mom = None
+        if moments:
+            n = rng.integers(0, 50, U).astype(np.float32)
+            self.mom = [n, (off[:, 0] + 0.1 * rng.standard_normal((U, D))).astype(np.float32),
+                        rng.standard_normal((U, D)).astype(np.float32),
+                        (0.3 * rng.standard_normal((U, D, D))).astype(np.float32)]
+        t = {}
+        for name in ("K", "V", "kt", "vt", "q"):
+            t[name] = bf(getattr(self, name)).to(DEV)
+            setattr(self, name, f64(t[name]))
+        t["votes"] = None if self.votes is None else torch.from_numpy(self.votes).to(DEV)
+        t["pos"], t["util"] = torch.from_numpy(self.pos).to(DEV), torch.from_numpy(self.util).to(DEV)
+        t["len"] = torch.tensor(self.lens, dtype=torch.int32, device=DEV)
+        t["mom"] = None if self.mom is None else [torch.from_numpy(x).to(DEV) for x in self.mom]
+        t["mask"] = torch.from_numpy(self.mask.view(np.int64)).to(DEV)
+        t["live"] = torch.tensor(self.live, dtype=torch.int32, device=DEV)
+        t["budget"] = None if budget is None else torch.tensor(budget, dtype=torch.int32, device=DEV)
+        self.t = t
+        self.budget = budget if budget is not None else [L or cap - 1] * U
+        self.rule, self.correction = rule, correction
+        code = {"single": K.RULE_SINGLE, "cumulative": K.RULE_CUMULATIVE, "ema": K.RULE_EMA}[rule]
+        self.p = K.make_params(U, G, cap, L or cap - 1, rule=code, alpha=0.75, correction=correction,
+                               budget=t["budget"])
+        self.cache = K.make_cache(t["K"], t["V"], t["votes"], t["pos"], t["util"], t["len"])
+        self.moments = None if self.mom is None else K.make_moments(*t["mom"])
+        self.tree = K.make_tree(T, per, t["mask"], t["live"])
+        self.ws = torch.zeros(K.kvc_tree_workspace_size(self.p, T), dtype=torch.uint8, device=DEV)
+        self.dws = torch.empty(K.kvc_decode_workspace_size(self.p), dtype=torch.uint8, device=DEV)
+        K.kvc_decode_workspace_init(self.p, self.dws)
+        self.max_len = max(1, max(lens))
+
+    def path(self, counts, A):
+        """Paths along the visible ancestors of a live token where there are enough, else any
+        live tokens."""
+        tok = np.zeros((self.B, A), np.int32)
+        for b, a in enumerate(counts):
+            rows = sorted(range(self.live[b]), key=lambda i: -bin(int(self.mask[b, i])).count("1"))
+            anc = [j for j in range(self.live[b]) if rows and int(self.mask[b, rows[0]]) >> j & 1]
+            rest = [j for j in range(self.live[b]) if j not in anc]
+            tok[b, :a] = (anc + rest)[:a]
+        self.tok, self.counts = tok, list(counts)
+        self.pos0 = (self.cap + 10 * np.arange(self.B)).astype(np.int32)
+        self.t["tok"] = torch.from_numpy(tok).to(DEV)
+        self.t["np"] = torch.tensor(self.counts, dtype=torch.int32, device=DEV)
+        self.t["pos0"] = torch.from_numpy(self.pos0).to(DEV)
+        self.accept = K.make_path(A, self.t["tok"], self.t["np"], self.t["pos0"])
+
+    # ---------------------------------------------------------------- attend
+    def run_attend(self, max_len=None):
+        o = torch.full((self.U, self.T, self.G, R.D), 7.0, dtype=torch.bfloat16, device=DEV)
+        lse = torch.full((self.U, self.T, self.G), 7.0, device=DEV)
+        K.kvc_tree_attend(self.p, max_len or self.max_len, self.tree, self.t["q"], self.t["kt"],
+                          self.t["vt"], self.cache, self.moments, o, lse, self.ws)
+        self.o, self.lse = o, lse
+        return o, lse
+
+    def ref_attend(self, u):
+        b = u // self.per
+        mom = None if self.mom is None else [np.float64(x[u]) for x in self.mom]
+        return R.attend(self.q[u], self.K[u], self.V[u],
+                        None if self.votes is None else self.votes[u], self.lens[u], self.kt[u],
+                        self.vt[u], self.mask[b], self.live[b], mom,
+                        self.correction == K.CORR_FIRST_ORDER,
+                        mom is not None and self.correction != K.CORR_OFF)
+
+    def check_attend(self):
+        o, lse = f64(self.o), f64(self.lse)
+        for u in range(self.U):
+            t = self.live[u // self.per]
+            ro, rl, bo, bl = self.ref_attend(u)
+            assert (o[u, t:] == 7).all() and (lse[u, t:] == 7).all(), "dead rows written"
+            fin = np.isfinite(rl)
+            assert (np.isneginf(lse[u, :t]) == ~fin).all()
+            assert (np.abs(lse[u, :t][fin] - rl[fin]) <= bl[fin]).all(), (
+                u, np.abs(lse[u, :t][fin] - rl[fin]).max(), bl[fin].min())
+            err = np.abs(o[u, :t] - ro)
+            assert np.isfinite(o[u, :t]).all()
+            assert (err <= bo).all(), (u, err.max(), (err / bo).max())
+
+
+ATTEND = [
+    # per, G, T, lens, keywords
+    (1, 1, 1, [0, 1, 2, 7], {}),
+    (2, 4, 1, [64, 63, 65, 1], {}),
+    (2, 4, 7, [127, 128, 129, 0], dict(live=[7, 3])),
+    (2, 8, 5, [255, 256, 257, 300], dict(votes=True)),
+    (1, 2, 64, [130, 1, 400], dict(kind="chain")),
+    (1, 1, 64, [96, 33], dict(kind="any")),
+    (2, 4, 33, [200, 511, 513, 90], dict(live=[33, 0], kind="any")),
+    (1, 8, 64, [150, 700], dict(kind="any", live=[64, 50])),
+    (1, 4, 63, [385, 640], dict(votes=True, moments=True)),
+    (3, 4, 16, [0, 1, 300, 77, 128, 5], dict(moments=True, live=[16, 9])),
+    (3, 2, 9, [0, 40, 130], dict(moments=True, correction=K.CORR_ZERO_ORDER)),
+    (3, 2, 9, [0, 40, 130], dict(moments=True, correction=K.CORR_OFF)),
+    (1, 4, 6, [0, 0, 5], dict(kind="none")),
+    (1, 4, 6, [0, 0, 5], dict(kind="none", moments=True)),
+    (1, 8, 17, [900, 1000, 3], dict(q_scale=30.0)),          # sharp attention
+    (4, 1, 24, [100, 200, 300, 400] * 45, dict()),           # more units than SMs
+]
+
+
+@pytest.mark.parametrize("i", range(len(ATTEND)))
+def test_attend(i):
+    per, G, T, lens, kw = ATTEND[i]
+    c = Case(100 + i, per, G, T, lens, **kw)
+    c.run_attend()
+    assert K.kvc_get_device_status(c.ws) == 0
+    c.check_attend()
+
+
+def test_attend_bounds_looser_than_the_lengths():
+    c = Case(3, 1, 4, 5, [17, 140], cap=1000)
+    c.run_attend(max_len=1000)
+    c.check_attend()
+
+
+@pytest.mark.parametrize("where", ["k", "v", "both"])
+@pytest.mark.parametrize("value", [NAN, float("inf")])
+def test_attend_masked_branch_does_not_leak(where, value):
+    """Token 1's branch is not finite: the rows that do not see it are as
+    they are without it; the rows that see it are not finite."""
+    ok = Case(5, 1, 4, 6, [50], kind="tree")
+    mask = np.array([[1, 3, 5, 7, 17, 63]], dtype=np.uint64)
+    outs = []
+    for bad in (False, True):
+        c = ok
+        c.t["mask"].copy_(torch.from_numpy(mask.view(np.int64)))
+        if bad and where in ("k", "both"):
+            c.t["kt"][0, 1] = value
+        if bad and where in ("v", "both"):
+            c.t["vt"][0, 1] = value
+        outs.append([x.clone() for x in c.run_attend()])
+    clean = [t for t in range(6) if not int(mask[0, t]) >> 1 & 1]
+    seen = [t for t in range(6) if int(mask[0, t]) >> 1 & 1]
+    for a, b in zip(*outs):
+        assert torch.equal(a[0, clean], b[0, clean])
+    if where != "k" or value != value:
+        assert not torch.isfinite(outs[1][0][0, seen].float()).all(-1).any()
+
+
+def test_attend_refused_on_the_device():
+    c = Case(6, 1, 4, 4, [50, 60, 40], live=[4, 4, 4])
+    c.t["live"].copy_(torch.tensor([4, 5, 4]))
+    o, lse = c.run_attend()
+    assert K.kvc_get_device_status(c.ws) == 1 and K.kvc_get_device_status(c.ws) == 0
+    assert (o[1] == 7).all() and (lse[1] == 7).all() and (lse[0] != 7).all()
+    c.t["live"].fill_(4)
+    o, lse = c.run_attend(max_len=50)
+    assert K.kvc_get_device_status(c.ws) == 2
+    assert (o[1] == 7).all() and (lse[1] == 7).all() and (lse[[0, 2]] != 7).all()
+
+
+# --------------------------------------------------------------------- weights
+
+WEIGHTS = [
+    (1, 1, 1, [0, 1, 2], [1, 1, 0], 1, {}),
+    (2, 4, 7, [127, 128, 129, 0], [3, 2], 3, {}),
+    (2, 8, 5, [255, 256, 257, 300], [5, 1], 5, dict(votes=True)),
+    (1, 2, 64, [130, 1, 400], [64, 64, 7], 64, dict(kind="chain")),
+    (1, 8, 64, [200, 129], [64, 30], 64, dict(kind="chain")),
+    (1, 1, 20, [96, 33], [20, 3], 20, dict(kind="any")),
+    (1, 4, 33, [700, 511], [17, 4], 17, dict(live=[33, 20], votes=True)),
+    (1, 4, 6, [0, 0, 5], [2, 3, 1], 3, dict(kind="none")),
+    (4, 1, 24, [100, 200, 300, 400] * 45, [i % 7 for i in range(45)], 6, {}),
+    (1, 4, 9, [300], [5], 5, dict(q_scale=30.0)),
+]
+
+
+@pytest.mark.parametrize("given", [False, True])
+@pytest.mark.parametrize("i", range(len(WEIGHTS)))
+def test_weights(i, given):
+    per, G, T, lens, counts, A, kw = WEIGHTS[i]
+    c = Case(200 + i, per, G, T, lens, **kw)
+    c.path(counts, A)
+    _, lse = c.run_attend()
+    w = c.rng.random((c.B, A)).astype(np.float32) if given else np.ones((c.B, A), np.float32)
+    if given:
+        w[0, 0] = 0.0
+    S = torch.full((c.U, c.cap), -3.0, device=DEV)
+    K.kvc_tree_weights(c.p, c.max_len, c.tree, c.accept,
+                       torch.from_numpy(w).to(DEV) if given else None, c.t["q"], c.t["kt"], lse,
+                       c.cache, S, c.ws)
+    assert K.kvc_get_device_status(c.ws) == 0
+    S, lse = f64(S), f64(lse)
+    for u in range(c.U):
+        b = u // per
+        a = counts[b]
+        ref, bound = R.weights(c.q[u], c.K[u], None if c.votes is None else c.votes[u], lens[u],
+                               c.kt[u], c.mask[b], [int(x) for x in c.tok[b, :a]],
+                               w[b].astype(np.float64), lse[u])
+        got = S[u, :lens[u] + a]
+        assert (np.abs(got - ref) <= bound).all(), (u, (np.abs(got - ref) / bound).max())
+        assert (S[u, lens[u] + a:] == -3).all(), "entries behind the last written"
+
+
+def test_weights_sum_to_the_accepted_tokens():
+    """Each accepted row's probabilities add up to 1 over the cache and its ancestors."""
+    c = Case(7, 1, 4, 12, [333, 20], kind="chain", votes=True)
+    c.path([9, 12], 12)
+    _, lse = c.run_attend()
+    S = torch.zeros(c.U, c.cap, device=DEV)
+    K.kvc_tree_weights(c.p, c.max_len, c.tree, c.accept, None, c.t["q"], c.t["kt"], lse, c.cache, S,
+                       c.ws)
+    # each of a sums has the logits' error (64 bits of slack for the longest one here)
+    assert torch.allclose(S.double().sum(1).cpu(), torch.tensor([9.0, 12.0]).double(), rtol=1e-4)
+
+
+def test_weights_refused_on_the_device():
+    c = Case(8, 1, 4, 6, [50, 60, 40, 30], live=[6, 6, 4, 6], cap=62)
+    c.path([2, 3, 2, 3], 3)
+    c.t["tok"][2, 1] = 4                               # not live
+    c.t["np"][3] = 4                                   # more than A
+    c.run_attend()
+    S = torch.full((4, c.cap), -3.0, device=DEV)
+    K.kvc_tree_weights(c.p, 60, c.tree, c.accept, None, c.t["q"], c.t["kt"], c.lse, c.cache, S, c.ws)
+    assert K.kvc_get_device_status(c.ws) in (1, 2)
+    assert (S[1:] == -3).all() and (S[0, :52] >= 0).all()   # unit 1: 60 + 3 > cap
+
+
+# ---------------------------------------------------------------------- commit
+
+def run_commit(c, S, kmax, mom=True):
+    ei = torch.full((c.U, kmax), -9, dtype=torch.int32, device=DEV)
+    ep = torch.full((c.U, kmax), -9, dtype=torch.int32, device=DEV)
+    ne = torch.full((c.U,), -9, dtype=torch.int32, device=DEV)
+    K.kvc_tree_commit(c.p, c.max_len, c.tree, c.accept, c.t["kt"], c.t["vt"],
+                      None if S is None else torch.from_numpy(S).to(DEV), c.cache,
+                      c.moments if mom else None, kmax, ei, ep, ne, c.dws)
+    return ei.cpu().numpy(), ep.cpu().numpy(), ne.cpu().numpy()
+
+
+def check_commit(c, S, kmax):
+    ei, ep, ne = run_commit(c, S, kmax)
+    assert K.kvc_get_device_status(c.dws) == 0
+    got = {n: f64(c.t[n]) for n in ("K", "V")}
+    pos, util, ln = c.t["pos"].cpu().numpy(), c.t["util"].cpu().numpy(), c.t["len"].tolist()
+    votes = None if c.votes is None else c.t["votes"].cpu().numpy()
+    for u in range(c.U):
+        b = u // c.per
+        a = c.counts[b]
+        mom = None if c.mom is None else [np.float64(x[u]) for x in c.mom]
+        ref = R.commit(c.K[u], c.V[u], None if c.votes is None else c.votes[u], c.pos[u], c.util[u],
+                       c.lens[u], c.budget[u], c.rule, 0.75,
+                       None if S is None else S[u, :c.lens[u] + a].astype(np.float64), c.kt[u],
+                       c.vt[u], [int(x) for x in c.tok[b, :a]], int(c.pos0[b]), mom)
+        k = ref["n_evict"]
+        assert ne[u] == k and ei[u, :k].tolist() == ref["evict_idx"]
+        assert ep[u, :k].tolist() == ref["evict_pos"]
+        assert (ei[u, k:] == -9).all() and (ep[u, k:] == -9).all()
+        assert ln[u] == ref["len"]
+        assert np.array_equal(got["K"][u], ref["K"], equal_nan=True)
+        assert np.array_equal(got["V"][u], ref["V"], equal_nan=True)
+        assert np.array_equal(pos[u], ref["pos"])
+        # one multiplication and one addition in 64 bits, fused or not
+        np.testing.assert_allclose(util[u], ref["util"], rtol=4 * 2.0 ** -53)
+        if votes is not None:
+            assert np.array_equal(votes[u], ref["votes"])
+        if mom is not None and k:
+            n1, mk, mv, C = (f64(x[u]) for x in c.t["mom"])
+            assert n1 == ref["n"]
+            assert (np.abs(mk - ref["mu_k"]) <= ref["bound_mu"] * ref["scale_k"]).all()
+            assert (np.abs(mv - ref["mu_v"]) <= ref["bound_mu"] * ref["scale_v"]).all()
+            assert (np.abs(C - ref["C"]) <= ref["bound_C"]).all(), (
+                np.abs(C - ref["C"]) / ref["bound_C"]).max()
+
+
+COMMIT = [
+    # per, T, lens, counts, A, keywords, scored weights given
+    (1, 4, [0, 1, 2, 9], [1, 2, 0, 4], 4, dict(budget=[1, 1, 9, 9], L=9), True),
+    (2, 7, [64, 63, 60, 64], [3, 5], 5, dict(L=64, votes=True, moments=True), True),
+    (1, 8, [100, 100], [8, 0], 8, dict(L=100, rule="cumulative", moments=True), True),
+    (1, 64, [200, 130], [64, 33], 64, dict(L=200, kind="chain", rule="single", moments=True), True),
+    (1, 8, [120, 128], [3, 8], 8, dict(budget=[77, 100], L=128, votes=True, moments=True), True),
+    (1, 8, [500, 90], [5, 2], 8, dict(budget=[500, 88], L=500, unscored=True, moments=True), True),
+    (1, 8, [500, 90], [5, 2], 8, dict(budget=[500, 88], L=500, unscored=True, moments=True), False),
+    (4, 6, [3000, 1025, 4096, 8200], [6], 6, dict(budget=[3000, 1024, 4096, 8200], L=8200), True),
+    (1, 3, [5, 5], [3, 3], 3, dict(L=9), True),                        # room left: nothing goes
+    (4, 24, [100, 200, 300, 400] * 45, [i % 7 for i in range(45)], 6,
+     dict(budget=[100, 200, 300, 400] * 45, L=400), True),
+]
+
+
+@pytest.mark.parametrize("i", range(len(COMMIT)))
+def test_commit(i):
+    per, T, lens, counts, A, kw, scored = COMMIT[i]
+    c = Case(300 + i, per, 1, T, lens, cap=max(lens) + A + 2, **kw)
+    c.path(counts, A)
+    S = np.exp(c.rng.standard_normal((c.U, c.cap)) * 2).astype(np.float32) if scored else None
+    kmax = max(1, max(max(0, c.lens[u] + counts[u // per] - c.budget[u]) for u in range(c.U)))
+    check_commit(c, S, kmax)
+
+
+@pytest.mark.parametrize("n", [70, 1500, 6000])
+@pytest.mark.parametrize("ties", ["zero", "few", "stride"])
+def test_commit_ties(n, ties):
+    """Weights that underflowed, few distinct ones, and the lowest all in
+    slots of one residue: the lowest positions go."""
+    c = Case(400 + n, 1, 1, 40, [n, n], cap=n + 44, L=n, rule="single", moments=True, kind="chain")
+    c.path([40, 17], 40)
+    S = np.zeros((2, c.cap), np.float32)
+    if ties == "few":
+        S = c.rng.integers(0, 3, S.shape).astype(np.float32)
+    elif ties == "stride":
+        S = (1 + c.rng.random(S.shape)).astype(np.float32)
+        S[:, ::512] = 0.25
+        S[:, 1:3000:3] = 0.5
+    check_commit(c, S, 40)
+
+
+def test_commit_same_position_and_weight_goes_by_slot():
+    c = Case(9, 1, 1, 4, [50], cap=60, L=50, rule="single")
+    c.t["pos"].fill_(3)
+    c.pos[:] = 3
+    c.path([4], 4)
+    c.pos0[:] = 0
+    c.t["pos0"].zero_()
+    check_commit(c, np.ones((1, 60), np.float32), 4)
+
+
+def test_commit_refused_on_the_device():
+    """Every refused unit is as it was; the others go on."""
+    c = Case(10, 1, 1, 6, [50, 60, 40, 30, 20, 45], cap=64, live=[6, 6, 4, 6, 6, 6], moments=True,
+             budget=[50, 60, 40, 30, 20, 0], L=60)
+    c.path([2, 5, 2, 3, 3, 1], 5)
+    c.t["tok"][2, 1] = 4                               # not live
+    c.t["np"][3] = 6                                   # more than A
+    c.t["len"][4] = 61                                 # beyond max_len
+    before = {n: c.t[n].clone() for n in ("K", "V", "pos", "util", "len")}
+    mom = [x.clone() for x in c.t["mom"]]
+    ei, ep, ne = run_commit(c, np.ones((6, 64), np.float32), 5)
+    assert K.kvc_get_device_status(c.dws) in (1, 2)
+    assert ne.tolist() == [2, 0, 0, 0, 0, 0]           # unit 1: 60 + 5 > cap; unit 5: budget 0
+    for n, x in before.items():
+        assert torch.equal(c.t[n][1:].view(torch.uint8), x[1:].view(torch.uint8)), n
+    for x, y in zip(c.t["mom"], mom):
+        assert torch.equal(x[1:], y[1:])
+    assert c.t["len"][0] == 50
+
+
+def test_commit_more_victims_than_room_and_too_few_scored():
+    c = Case(11, 1, 1, 6, [50, 50], cap=64, budget=[45, 50], L=50)
+    c.path([2, 2], 2)
+    ei, ep, ne = run_commit(c, np.ones((2, 64), np.float32), 2)       # unit 0 needs 7
+    assert K.kvc_get_device_status(c.dws) == 2 and ne.tolist() == [0, 2]
+    c = Case(12, 1, 1, 6, [50, 50], cap=64, L=50)
+    c.t["util"][0, 1:] = float("inf")
+    c.path([2, 2], 2)
+    util = c.t["util"].clone()
+    ei, ep, ne = run_commit(c, None, 2)                               # one scored, two to go
+    assert K.kvc_get_device_status(c.dws) == 1 and ne.tolist() == [0, 2]
+    assert torch.equal(c.t["util"][0], util[0]) and c.t["len"].tolist() == [50, 50]
+
+
+# --------------------------------------------------------------------- together
+
+def _stream(seed, U, G, n, cap, L, steps, **kw):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+
+    def rnd(*s):
+        return torch.randn(*s, generator=g, device=DEV)
+
+    st = DecodeState(U, G, cap, L, rule=K.RULE_CUMULATIVE, **kw)
+    st.load_prefill(rnd(U, n, 128).bfloat16(), rnd(U, n, 128).bfloat16(),
+                    None, torch.arange(n, dtype=torch.int32, device=DEV).repeat(U, 1),
+                    torch.full((U,), n, dtype=torch.int32, device=DEV))
+    return st, rnd
+
+
+def test_one_token_trees_are_decode_steps():
+    """A drafted token accepted alone, with its weight as the utility's
+    observation, does what the one-token calls do: the same outputs, victims
+    and moments, step by step."""
+    U, G, n, L = 6, 4, 90, 64
+    a, rnd = _stream(1, U, G, n, n + 4, L, 8)
+    b, _ = _stream(1, U, G, n, n + 4, L, 8)
+    one = torch.ones(1, 1, dtype=torch.int64, device=DEV)
+    zero = torch.zeros(1, 1, dtype=torch.int32, device=DEV)
+    for t in range(1, 9):
+        q, k, v = rnd(U, G, 128).bfloat16(), rnd(U, 128).bfloat16(), rnd(U, 128).bfloat16()
+        max_len = n + 1 if t == 1 else L + 1
+        b.step_calls(t, n + t - 1, q, k, v, max_len)
+        if t == 1:       # the prompt goes down to the budget in the one-token calls
+            a.step_calls(t, n + t - 1, q, k, v, max_len)
+            continue
+        tree = K.make_tree(1, U, one)
+        path = K.make_path(1, zero, torch.ones(1, dtype=torch.int32, device=DEV),
+                           torch.full((1,), n + t - 1, dtype=torch.int32, device=DEV))
+        o, lse = a.verify(tree, q, k, v, L)
+        a.accept(tree, path, q, k, v, L)
+        assert a.tree_status() == 0 and a.device_status() == 0
+        # the attention over every slot of the step, before the eviction
+        assert torch.allclose(lse[:, 0], b.lse, atol=2e-5)
+        assert torch.equal(a.n_evict, b.n_evict)
+        assert torch.equal(a.tree_evict[1][:, 0], b.evict_pos[:, 0])
+        assert torch.equal(a.pos[:, :L].sort(1)[0], b.pos[:, :L].sort(1)[0])
+        assert torch.equal(a.n, b.n)
+        assert torch.allclose(a.C, b.C, atol=1e-5)
+
+
+def test_verification_run_matches_the_reference():
+    """Verifications of trees with ragged acceptance on a budgeted cache, each
+    against the 64-bit definitions from the state before it."""
+    U, per, G, T, A, L = 8, 4, 4, 10, 5, 96
+    st, rnd = _stream(2, U, G, L, L + T + 2, L, 6)
+    rng = np.random.default_rng(0)
+    for step in range(6):
+        mask = tree_masks(rng, 2, T, "chain")
+        counts = [int(x) for x in rng.integers(0, A + 1, 2)]
+        tok = np.tile(np.arange(A, dtype=np.int32), (2, 1))
+        tree = K.make_tree(T, per, torch.from_numpy(mask.view(np.int64)).to(DEV))
+        path = K.make_path(A, torch.from_numpy(tok).to(DEV),
+                           torch.tensor(counts, dtype=torch.int32, device=DEV),
+                           torch.tensor([1000 + 10 * step] * 2, dtype=torch.int32, device=DEV))
+        q, k, v = (rnd(U, T, G, 128).bfloat16(), rnd(U, T, 128).bfloat16(), rnd(U, T, 128).bfloat16())
+        old = {x: f64(getattr(st, x)) for x in ("K", "V", "util", "n", "mu_k", "mu_v", "C")}
+        pos, lens = st.pos.cpu().numpy(), st.len.tolist()
+        o, lse = (x.clone() for x in st.verify(tree, q, k, v, L))
+        st.accept(tree, path, q, k, v, L)
+        assert st.tree_status() == 0 and st.device_status() == 0
+        S = f64(st.tree_S)
+        for u in range(U):
+            a = counts[u // per]
+            mom = [old[x][u] for x in ("n", "mu_k", "mu_v", "C")]
+            ro, rl, bo, bl = R.attend(f64(q[u]), old["K"][u], old["V"][u], None, lens[u], f64(k[u]),
+                                      f64(v[u]), mask[u // per], T, mom, True, True)
+            assert (np.abs(f64(o[u]) - ro) <= bo).all() and (np.abs(f64(lse[u]) - rl) <= bl).all()
+            p = list(range(a))
+            rs, bs = R.weights(f64(q[u]), old["K"][u], None, lens[u], f64(k[u]), mask[u // per], p,
+                               np.ones(A), f64(lse[u]))
+            assert (np.abs(S[u, :lens[u] + a] - rs) <= bs).all()
+            ref = R.commit(old["K"][u], old["V"][u], None, pos[u], old["util"][u], lens[u], L,
+                           "cumulative", 0.0, S[u, :lens[u] + a], f64(k[u]), f64(v[u]), p,
+                           1000 + 10 * step, mom)
+            assert np.array_equal(f64(st.K[u]), ref["K"]) and np.array_equal(f64(st.V[u]), ref["V"])
+            assert st.len[u] == ref["len"] and st.n_evict[u] == ref["n_evict"]
+            if ref["n_evict"]:
+                assert (np.abs(f64(st.C[u]) - ref["C"]) <= ref["bound_C"]).all()
+    # the stream goes on with a one-token step on the same cache
+    assert st.len.tolist() == [L] * U
+    st.step(2, 5000, rnd(U, G, 128).bfloat16(), rnd(U, 128).bfloat16(), rnd(U, 128).bfloat16(), L + 1)
+    assert st.device_status() == 0 and st.len.tolist() == [L] * U
+
+
+def _graph_case(seed):
+    c = Case(seed, 2, 4, 9, [700, 90, 33, 400], votes=True, moments=True)
+    c.path([4, 2], 4)
+    c.o = torch.zeros(c.U, c.T, c.G, R.D, dtype=torch.bfloat16, device=DEV)
+    c.lse = torch.zeros(c.U, c.T, c.G, device=DEV)
+    c.S = torch.zeros(c.U, c.cap, device=DEV)
+
+    def call(stream=None):
+        K.kvc_tree_attend(c.p, c.max_len, c.tree, c.t["q"], c.t["kt"], c.t["vt"], c.cache, c.moments,
+                          c.o, c.lse, c.ws, stream)
+        K.kvc_tree_weights(c.p, c.max_len, c.tree, c.accept, None, c.t["q"], c.t["kt"], c.lse, c.cache,
+                           c.S, c.ws, stream)
+    c.call = call
+    return c
+
+
+def test_graphs_that_share_a_workspace_and_another_stream():
+    a, b = _graph_case(21), _graph_case(22)
+    b.ws = a.ws
+    want = []
+    for c in (a, b):
+        c.call()
+        want.append([x.clone() for x in (c.o, c.lse, c.S)])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    a.call(side)                                       # the caller's stream, not the current one
+    graphs = []
+    for c in (a, b):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.call()
+        graphs.append(g)
+    torch.cuda.current_stream().wait_stream(side)
+    for _ in range(3):
+        for c, g, w in zip((a, b), graphs, want):
+            for x in (c.o, c.lse, c.S):
+                x.zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            for x, y in zip((c.o, c.lse, c.S), w):
+                assert torch.equal(x, y)               # the same bits, run after run
+
+
+def test_offsets_past_32_bits():
+    """A cache of more than 2^32 bytes (and 2^31 elements) of keys: the last
+    unit is where it should be."""
+    U, cap, n, T, G = 34, 1 << 19, 300, 3, 2
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB of device memory")
+    Kc = torch.zeros(U, cap, 128, dtype=torch.bfloat16, device=DEV)
+    Vc = torch.zeros(U, cap, 128, dtype=torch.bfloat16, device=DEV)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(5)
+
+    def rnd(*s):
+        return torch.randn(*s, generator=g, device=DEV).bfloat16()
+
+    Kc[-1, :n], Vc[-1, :n] = rnd(n, 128), rnd(n, 128)
+    pos = torch.arange(cap, dtype=torch.int32, device=DEV).repeat(U, 1)
+    util = torch.rand(U, cap, generator=g, device=DEV, dtype=torch.float64)
+    ln = torch.full((U,), n, dtype=torch.int32, device=DEV)
+    p = K.make_params(U, G, cap, n, rule=K.RULE_SINGLE)
+    cache = K.make_cache(Kc, Vc, None, pos, util, ln)
+    mask = torch.tensor([[1, 3, 7]], dtype=torch.int64, device=DEV)
+    tree = K.make_tree(T, U, mask)
+    path = K.make_path(2, torch.tensor([[0, 1]], dtype=torch.int32, device=DEV),
+                       torch.tensor([2], dtype=torch.int32, device=DEV),
+                       torch.tensor([9000], dtype=torch.int32, device=DEV))
+    q, k, v = rnd(U, T, G, 128), rnd(U, T, 128), rnd(U, T, 128)
+    o = torch.zeros(U, T, G, 128, dtype=torch.bfloat16, device=DEV)
+    lse = torch.zeros(U, T, G, device=DEV)
+    S = torch.zeros(U, cap, device=DEV)
+    ws = torch.zeros(K.kvc_tree_workspace_size(p, T), dtype=torch.uint8, device=DEV)
+    dws = torch.empty(K.kvc_decode_workspace_size(p), dtype=torch.uint8, device=DEV)
+    K.kvc_decode_workspace_init(p, dws)
+    K.kvc_tree_attend(p, n, tree, q, k, v, cache, None, o, lse, ws)
+    K.kvc_tree_weights(p, n, tree, path, None, q, k, lse, cache, S, ws)
+    ne = torch.zeros(U, dtype=torch.int32, device=DEV)
+    rk, rv = f64(Kc[-1, :n]), f64(Vc[-1, :n])
+    K.kvc_tree_commit(p, n, tree, path, k, v, S, cache, None, 2, None, None, ne, dws)
+    assert K.kvc_get_device_status(ws) == 0 and K.kvc_get_device_status(dws) == 0
+    ro, rl, bo, bl = R.attend(f64(q[-1]), rk, rv, None, n, f64(k[-1]), f64(v[-1]), [1, 3, 7], T,
+                              None, False, False)
+    assert (np.abs(f64(o[-1]) - ro) <= bo).all() and (np.abs(f64(lse[-1]) - rl) <= bl).all()
+    rs, bs = R.weights(f64(q[-1]), rk, None, n, f64(k[-1]), [1, 3, 7], [0, 1], np.ones(2), f64(lse[-1]))
+    assert (np.abs(f64(S[-1, :n + 2]) - rs) <= bs).all()
+    ref = R.commit(rk, rv, None, np.arange(n), np.zeros(n), n, n, "single", 0, f64(S[-1, :n + 2]),
+                   f64(k[-1]), f64(v[-1]), [0, 1], 9000, None)
+    assert np.array_equal(f64(Kc[-1, :n]), ref["K"]) and np.array_equal(f64(Vc[-1, :n]), ref["V"])
+    assert ne.tolist() == [2] * U
