@@ -7,6 +7,7 @@
 
 #include "kvc_common.cuh"
 #include "kvc_internal.h"
+#include "kvc_tma.cuh"
 
 namespace kvc {
 
@@ -44,6 +45,42 @@ __device__ __forceinline__ int path_count(const TreeArgs &t, const PathArgs &p, 
         bad |= c < 0 || c >= live;
     }
     return __any_sync(kFull, bad) ? -1 : a;
+}
+
+// 3D copies of a box of 64 columns x 64 rows of one unit.
+__device__ __forceinline__ void tma_3d(void *dst, const CUtensorMap *map, int x, int y, int z,
+                                       uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_3d_hint(void *dst, const CUtensorMap *map, int x, int y, int z,
+                                            uint64_t *bar, uint64_t policy)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+
+// [units][rows][128] bf16, boxes of 64 columns x 64 rows of a unit with the
+// 128-byte swizzle; rows past a unit's last read as zero.  A unit index and a
+// row index fit 32 bits where their product does not.
+inline bool make_unit_map(CUtensorMap *m, const void *base, uint64_t units, uint64_t rows)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)kD, (cuuint64_t)rows, (cuuint64_t)units};
+    const cuuint64_t strides[2] = {(cuuint64_t)(kD * 2), (cuuint64_t)(rows * kD * 2)};
+    const cuuint32_t box[3] = {64u, 64u, 1u}, estr[3] = {1u, 1u, 1u};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 cudaError_t launch_tree_attend(const kvc_params &p, int max_len, const TreeArgs &t,

@@ -1,103 +1,929 @@
 // kvc_tree_attend.cu -- attention of a tree of drafted tokens over the cache
 // and the tree itself, with the normalization correction.
 //
-// One warp per query row (drafted token, head): a lane holds four dimensions
-// of q and of the output, one pass over the slots with the running maximum
-// and sum of the softmax.
+// The T G query rows of a unit share its keys and values, so a unit is one
+// matrix product per tile of 128 slots each way: S = Q K^T (tcgen05, rows on
+// the tensor-memory lanes), a softmax with a running maximum and sum (one
+// thread per row), O += P V (P from tensor memory).  Up to 256 rows are bound
+// by the 512 bytes per slot that stream from HBM (128 rows take 1024 tensor
+// clocks per tile against about 2800 for its bytes at one SM's share of the
+// bandwidth), so everything else is laid out to keep the loads going.
+//
+// Work split: the tiles of all (unit, block of 256 rows) items form one line
+// that is cut into equal parts, one per CTA (a persistent CTA per SM).  An
+// item inside one part is finished there; an item that a cut crosses leaves
+// partial sums (maximum, sum, output) per part, which tree_join_kernel adds.
+// The drafted tokens are the item's last tile.
+//
+// 320 threads:
+//   warps 0-3, 4-7  two softmax groups, each with its own S, P and O in tensor
+//                   memory.  Items of more than 128 rows give each group 128
+//                   of them; otherwise the groups take alternate tiles of the
+//                   same rows and add their sums at the end
+//   warp 8          producer (TMA into a ring of 32 KB key and value tiles)
+//   warp 9          tensor-memory owner and MMA issuer
+// Tensor memory: O of group w at column 128 w, S at 256 + 128 w; P (bf16)
+// overlays the first half of S.
+//
+// What a row must not see: slots behind len and hidden drafted tokens are
+// masked in S by selection (never by adding -inf to what may be NaN).  The
+// value rows behind len are zeroed in shared memory up to the next multiple of
+// 16 (the MMA reads 16 slots at a time).  Drafted tokens whose value is not
+// finite are zeroed as well and added afterwards to the rows that see them.
+// Every wait is bounded (~2 s); a wait that ran out records KVC_ERR_TIMEOUT.
 #include "kvc_tree.h"
+#include "kvc_umma.cuh"
+
+#include <stddef.h>
 
 namespace kvc {
 namespace {
 
+constexpr int kTile = 128;                       // slots per tile
+constexpr int kRows = 256;                       // query rows per item
+constexpr int kSlot = kTile * kD * 2;            // 32 KB: a tile of keys or values
+constexpr int kHalf = kSlot / 2;                 // its 64-column half
+constexpr int kRing = 5;
+constexpr int kThreads = 320;
+constexpr int kProd = 8, kMma = 9;
+constexpr int kGrid = 152;                       // CTAs: one per SM
+constexpr uint32_t kColS = 256;
+constexpr float kLog2e = 1.4426950408889634f;
+// the running maximum moves once a new one is above it by this much (in
+// powers of two): weights stay below 2^8 and most tiles rescale nothing
+constexpr float kSlack = 8.f;
+
+constexpr uint32_t kIdescS = umma_idesc_bf16(128, 128);
+constexpr uint32_t kIdescS64 = umma_idesc_bf16(128, 64);
+constexpr uint32_t kIdescO = umma_idesc_bf16(128, 128) | (1u << 16);   // B (values) MN-major
+
 struct AttArgs {
     TreeArgs t;
-    const uint16_t *q, *kt, *vt, *K, *V;
     const int32_t *votes, *len;
-    const float *mn, *mu_k, *mu_v, *C;
+    const uint16_t *vt;
     uint16_t *o;
     float *lse;
+    float *part;            // [items + CTAs][rows][128]
+    float2 *ml;             // [items + CTAs][rows]
+    int *first;             // [items + 1] tiles before each item
     int32_t *status;
-    int G, cap, max_len, first;
+    int U, RB, TG, G, cap, max_len, rows, whole, join_all;
+    float scale;            // log2(e) / sqrt(d)
 };
 
-__device__ __forceinline__ uint32_t bf2(float a, float b)
+struct AttSmem {
+    union {                 // read as float4
+        float bias[kTile];  // ln p of a tile's slots
+        float2 ml[kTile];   // at an item's end: the rows' maxima and sums
+    } g[2];
+    uint64_t full[kRing], empty[kRing];
+    uint64_t drain;
+    uint64_t qfull[2], qempty[2], sfull[2], pready[2], pvdone[2];
+    uint64_t odd[2];        // drafted tokens with a value that is not finite
+    int scan[40];
+    int start_item, start_base, total;
+    int bad;
+    uint32_t tmem;
+};
+
+// Bounded wait.  Once one has run out every wait ends at once: each role then
+// walks its loops to the end (so that the barriers among them stay matched)
+// without issuing copies or MMAs.
+__device__ __forceinline__ bool tree_wait(uint64_t *b, uint32_t parity, volatile int *bad)
+{
+    if (mbar_try_wait(b, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_try_wait(b, parity)) {
+        if (*bad) return false;
+        if (clock64() - t0 > kWaitCycles) {
+            *bad = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
+// Everything is dynamic shared memory: the tiles fill all of it but 3 KB.
+constexpr size_t kDyn = (size_t)(2 + kRing) * kSlot + sizeof(AttSmem);
+static_assert(kDyn <= 227 * 1024, "one block's shared memory");
+static_assert(offsetof(AttSmem, g) % 16 == 0 && offsetof(AttSmem, full) % 8 == 0, "alignment");
+
+// Value operand: 128 slots of two 64-dimension boxes; leading byte offset
+// between the boxes, stride byte offset between 8-slot groups, version 1,
+// 128-byte swizzle.
+__device__ __forceinline__ uint64_t v_desc(uint32_t saddr)
+{
+    uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
+    d |= (uint64_t)((uint32_t)kHalf >> 4) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1u << 46;
+    d |= (uint64_t)2u << 61;
+    return d;
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc)
+{
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+        "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15,%16};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st()
+{
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 {
     uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
 
-__global__ void __launch_bounds__(256) tree_attend_kernel(AttArgs a)
+template <int kBar, int kCount>
+__device__ __forceinline__ void bar_sync()
 {
-    const int u = blockIdx.x, lane = threadIdx.x & 31;
-    const int row = blockIdx.y * 8 + (threadIdx.x >> 5);
-    const int n = a.len[u], live = tree_live(a.t, u);
-    if (n < 0 || n > a.max_len || live < 0) {
-        if (threadIdx.x == 0) record_status(a.status, live < 0 ? KVC_ERR_INVALID_ARG : KVC_ERR_SHAPE);
-        return;
+    asm volatile("bar.sync %0, %1;" ::"n"(kBar), "n"(kCount) : "memory");
+}
+
+// Barrier of one softmax group (2 + w) over its 128 threads.
+__device__ __forceinline__ void group_sync(int w)
+{
+    if (w == 0) bar_sync<2, 128>();
+    else bar_sync<3, 128>();
+}
+
+// Tiles of an item: the cache's and, last, the drafted tokens'; none when it
+// has no live row or the unit is refused.
+__device__ __forceinline__ int item_tiles(const AttArgs &a, int n, int live, int rb)
+{
+    if (n < 0 || n > a.max_len || live < 0 || live * a.G <= rb * kRows) return 0;
+    return (n + kTile - 1) / kTile + 1;
+}
+
+// The line is cut into as many parts as there are CTAs, none of them empty.
+__device__ __forceinline__ int parts_of(int grid, int total) { return min(grid, total); }
+
+// The part of one item that this CTA takes.
+struct Seg {
+    int item, u, rb, n, live, nt;   // nt: tiles of the item
+    int t0, t1;                     // this CTA's tiles of it
+    int rows;                       // live rows of the item
+};
+
+struct Walk {
+    const AttArgs &a;
+    int item, base, lo, hi;
+    int n_next, live_next;
+
+    __device__ Walk(const AttArgs &a_, int item_, int base_, int lo_, int hi_)
+        : a(a_), item(item_), base(base_), lo(lo_), hi(hi_)
+    {
+        peek(item);
     }
-    if (row >= live * a.G) return;
-    const size_t tb = (size_t)u * a.t.T, cb = (size_t)u * a.cap, qr = tb * a.G + row;
-    const float scale = rsqrtf((float)kD);
-    const uint2 qw = reinterpret_cast<const uint2 *>(a.q + qr * kD)[lane];
-    const float q0 = bf_lo(qw.x), q1 = bf_hi(qw.x), q2 = bf_lo(qw.y), q3 = bf_hi(qw.y);
-    float m = -INFINITY, l = 0.f, f0 = 0.f, f1 = 0.f, f2 = 0.f, f3 = 0.f;
-    auto take = [&](const uint16_t *kp, const uint16_t *vp, float bias) {
-        const uint2 kw = reinterpret_cast<const uint2 *>(kp)[lane];
-        const uint2 vw = reinterpret_cast<const uint2 *>(vp)[lane];
-        const float x = warp_sum(q0 * bf_lo(kw.x) + q1 * bf_hi(kw.x) + q2 * bf_lo(kw.y) +
-                                 q3 * bf_hi(kw.y)) * scale + bias;
-        const float mx = fmaxf(m, x);
-        const float c = m == -INFINITY ? 0.f : expf(m - mx), e = x == -INFINITY ? 0.f : expf(x - mx);
-        l = l * c + e;
-        f0 = f0 * c + e * bf_lo(vw.x);
-        f1 = f1 * c + e * bf_hi(vw.x);
-        f2 = f2 * c + e * bf_lo(vw.y);
-        f3 = f3 * c + e * bf_hi(vw.y);
-        m = mx;
-    };
-    for (int i = 0; i < n; i++)
-        take(a.K + (cb + i) * kD, a.V + (cb + i) * kD,
-             a.votes ? logf((float)a.votes[cb + i]) : 0.f);
-    uint64_t w = a.t.mask[(size_t)(u / a.t.units) * a.t.T + row / a.G];
-    for (int j = 0; j < live; j++)
-        if (w >> j & 1) take(a.kt + (tb + j) * kD, a.vt + (tb + j) * kD, 0.f);
-    const bool none = l == 0.f;
-    const float lse = none ? -INFINITY : m + logf(l);
-    const float inv = none ? 0.f : 1.f / l;
-    float f[4] = {f0 * inv, f1 * inv, f2 * inv, f3 * inv};
-    const float ne = a.mn ? a.mn[u] : 0.f;
-    if (ne > 0.f) {
-        const float4 mk = reinterpret_cast<const float4 *>(a.mu_k + (size_t)u * kD)[lane];
-        const float ze = logf(ne) + scale * warp_sum(q0 * mk.x + q1 * mk.y + q2 * mk.z + q3 * mk.w);
-        const float wr = 1.f / (1.f + expf(ze - lse));
-        for (int i = 0; i < kD; i++) {
-            float g = a.mu_v[(size_t)u * kD + i];
-            if (a.first) {
-                const float4 c =
-                    reinterpret_cast<const float4 *>(a.C + ((size_t)u * kD + i) * kD)[lane];
-                g += scale * warp_sum(q0 * c.x + q1 * c.y + q2 * c.z + q3 * c.w);
-            }
-            if (lane == i >> 2) f[i & 3] = wr * f[i & 3] + (1.f - wr) * g;
+    __device__ void peek(int i)
+    {
+        if (i < a.U * a.RB) {
+            const int u = i / a.RB;
+            n_next = a.len[u];
+            live_next = tree_live(a.t, u);
         }
     }
-    reinterpret_cast<uint2 *>(a.o + qr * kD)[lane] = make_uint2(bf2(f[0], f[1]), bf2(f[2], f[3]));
-    if (lane == 0) a.lse[qr] = lse;
+    __device__ bool next(Seg &s)
+    {
+        while (base < hi && item < a.U * a.RB) {
+            s.item = item;
+            s.u = item / a.RB;
+            s.rb = item - s.u * a.RB;
+            s.n = n_next;
+            s.live = live_next;
+            s.nt = item_tiles(a, s.n, s.live, s.rb);
+            peek(item + 1);
+            const int b = base;
+            base += s.nt;
+            item++;
+            s.t0 = max(0, lo - b);
+            s.t1 = min(s.nt, hi - b);
+            if (s.t1 > s.t0) {
+                s.rows = min(kRows, s.live * a.G - s.rb * kRows);
+                return true;
+            }
+        }
+        return false;
+    }
+};
+
+// valid slots of tile t (the drafted tokens' tile: the live ones)
+__device__ __forceinline__ int tile_valid(const Seg &s, int t)
+{
+    return t == s.nt - 1 ? s.live : min(kTile, s.n - t * kTile);
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CUtensorMap tmK,
+                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmQ,
+                   const __grid_constant__ CUtensorMap tmKt, const __grid_constant__ CUtensorMap tmVt)
+{
+    extern __shared__ __align__(1024) unsigned char dyn[];
+    unsigned char *qbuf = dyn, *ring = qbuf + 2 * kSlot;
+    AttSmem &S = *reinterpret_cast<AttSmem *>(ring + kRing * kSlot);
+    if (smem_u32(dyn) & 1023) {                  // the swizzle counts on it
+        if (threadIdx.x == 0) record_status(a.status, KVC_ERR_CUDA);
+        return;
+    }
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int items = a.U * a.RB;
+
+    if (tid == 0) {
+        S.bad = 0;
+        for (int i = 0; i < kRing; i++) {
+            mbar_init(&S.full[i], 1);
+            mbar_init(&S.empty[i], 1);
+        }
+        mbar_init(&S.drain, 1);
+        for (int i = 0; i < 2; i++) {
+            mbar_init(&S.qfull[i], 1);
+            mbar_init(&S.qempty[i], 1);
+            mbar_init(&S.sfull[i], 1);
+            mbar_init(&S.pready[i], 4);
+            mbar_init(&S.pvdone[i], 1);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kMma) tmem_alloc(&S.tmem, 512);
+
+    // the line of tiles: every CTA counts it and finds where its part starts
+    int lo, hi;
+    {
+        const int per = (items + kThreads - 1) / kThreads;
+        const int i0 = min(items, tid * per), i1 = min(items, i0 + per);
+        int sum = 0;
+        for (int i = i0; i < i1; i++) {
+            const int u = i / a.RB, n = a.len[u], live = tree_live(a.t, u);
+            if (blockIdx.x == 0 && (n < 0 || n > a.max_len || live < 0) && i == u * a.RB)
+                record_status(a.status, live < 0 ? KVC_ERR_INVALID_ARG : KVC_ERR_SHAPE);
+            sum += item_tiles(a, n, live, i - u * a.RB);
+        }
+        int total;
+        int base = block_exscan(sum, S.scan, &total);
+        if (a.whole) {
+            // parts of whole items: nothing to join
+            const int c0 = (int)((long long)items * blockIdx.x / gridDim.x);
+            const int c1 = (int)((long long)items * (blockIdx.x + 1) / gridDim.x);
+            for (int i = i0, b = base; i < i1; i++) {
+                const int u = i / a.RB;
+                if (i == c0) { S.start_item = i; S.start_base = b; }
+                b += item_tiles(a, a.len[u], tree_live(a.t, u), i - u * a.RB);
+                if (i == c1 - 1) S.total = b;
+            }
+            __syncthreads();
+            lo = c0 < c1 ? S.start_base : 0;
+            hi = c0 < c1 ? S.total : 0;
+        } else {
+            const int g = parts_of(gridDim.x, total), c = min((int)blockIdx.x, g);
+            lo = g ? (int)((long long)total * c / g) : 0;
+            hi = g ? (int)((long long)total * min(c + 1, g) / g) : 0;
+            for (int i = i0, b = base; i < i1; i++) {
+                const int u = i / a.RB;
+                const int nt = item_tiles(a, a.len[u], tree_live(a.t, u), i - u * a.RB);
+                if (blockIdx.x == 0) a.first[i] = b;
+                if (lo >= b && lo < b + nt) { S.start_item = i; S.start_base = b; }
+                b += nt;
+                if (blockIdx.x == 0 && i == items - 1) a.first[items] = b;
+            }
+            __syncthreads();
+        }
+    }
+    tc_fence_after();
+    const uint32_t tmem = S.tmem;
+    Walk walk(a, lo < hi ? S.start_item : items, S.start_base, lo, hi);
+    Seg s;
+
+    if (warp == kProd) {
+        // ------------------------------------------------------- producer
+        if (lane == 0) {
+            int k = 0, nseg = 0, qn[2] = {0, 0};
+            bool ok = true;
+            const uint64_t pol = l2_policy_evict_first();
+            auto load = [&](const CUtensorMap *m, int u, int row, int rows, bool stream) {
+                const int slot = k % kRing;
+                if (k >= kRing) ok = tree_wait(&S.empty[slot], ((k / kRing) - 1) & 1, &S.bad);
+                if (!ok) return;
+                unsigned char *d = ring + slot * kSlot;
+                const int boxes = rows > 64 ? 2 : 1;
+                mbar_expect_tx(&S.full[slot], boxes * kHalf);
+                for (int h = 0; h < 2; h++)
+                    for (int b = 0; b < boxes; b++) {
+                        if (stream)
+                            tma_3d_hint(d + h * kHalf + b * (kHalf / 2), m, 64 * h, row + 64 * b, u,
+                                        &S.full[slot], pol);
+                        else
+                            tma_3d(d + h * kHalf + b * (kHalf / 2), m, 64 * h, row + 64 * b, u,
+                                   &S.full[slot]);
+                    }
+                k++;
+            };
+            auto load_q = [&](int half, int u, int row, int rows) {
+                if (qn[half] > 0) ok = ok && tree_wait(&S.qempty[half], (qn[half] - 1) & 1, &S.bad);
+                if (!ok) return;
+                const int boxes = rows > 64 ? 2 : 1;
+                unsigned char *d = qbuf + half * kSlot;
+                mbar_expect_tx(&S.qfull[half], boxes * kHalf);
+                for (int h = 0; h < 2; h++)
+                    for (int b = 0; b < boxes; b++)
+                        tma_3d(d + h * kHalf + b * (kHalf / 2), &tmQ, 64 * h, row + 64 * b, u,
+                               &S.qfull[half]);
+                qn[half]++;
+            };
+            while (ok && walk.next(s)) {
+                const int qrow = s.rb * kRows;
+                if (s.rows > 128) {
+                    load_q(0, s.u, qrow, 128);
+                    load_q(1, s.u, qrow + 128, s.rows - 128);
+                } else {
+                    // the halves alternate, so the next item's rows load early;
+                    // an item of two halves takes both, whichever was last
+                    load_q(nseg & 1, s.u, qrow, s.rows);
+                }
+                nseg++;
+                for (int t = s.t0; ok && t < s.t1; t++) {
+                    const int nv = tile_valid(s, t);
+                    if (t == s.nt - 1) {
+                        load(&tmKt, s.u, 0, 64, false);
+                        if (ok) load(&tmVt, s.u, 0, 64, false);
+                    } else {
+                        load(&tmK, s.u, t * kTile, nv, a.RB == 1);
+                        if (ok) load(&tmV, s.u, t * kTile, nv, a.RB == 1);
+                    }
+                }
+            }
+            if (!ok) {
+                S.bad = 1;
+                // the copies in flight land before the block ends
+                for (int i = max(0, k - kRing); i < k; i++)
+                    mbar_wait(&S.full[i % kRing], (i / kRing) & 1);
+                for (int h = 0; h < 2; h++)
+                    if (qn[h]) mbar_wait(&S.qfull[h], (qn[h] - 1) & 1);
+            }
+        }
+        __syncwarp();
+    } else if (warp == kMma) {
+        // ------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            bool ok = true;
+            int k0 = 0, nseg = 0;              // ring index of the segment's first tile
+            int qn[2] = {0, 0}, sn[2] = {0, 0}, pn[2] = {0, 0};
+            while (ok && walk.next(s)) {
+                const bool dual = s.rows > 128;
+                const int nq = s.t1 - s.t0, jobs = dual ? 2 * nq : nq;
+                const int qh = nseg & 1;
+                nseg++;
+                int last_pv[2] = {-1, -1};
+                auto tile_of = [&](int j) { return dual ? j >> 1 : j; };
+                auto issue_s = [&](int j) {
+                    const int t = tile_of(j), w = j & 1, half = dual ? w : qh;
+                    const int kk = k0 + 2 * t, slot = kk % kRing;
+                    if (j < (dual ? 2 : 1)) {
+                        ok = ok && tree_wait(&S.qfull[half], qn[half] & 1, &S.bad);
+                        qn[half]++;
+                    }
+                    if (!dual || w == 0) ok = ok && tree_wait(&S.full[slot], (kk / kRing) & 1, &S.bad);
+                    // the group's earlier weights, which S overlays, are used up
+                    if (pn[w] > 0) ok = ok && tree_wait(&S.pvdone[w], (pn[w] - 1) & 1, &S.bad);
+                    if (!ok) return;
+                    tc_fence_after();
+                    const bool small = tile_valid(s, s.t0 + t) <= 64;
+                    const uint64_t qd = umma_sdesc(smem_u32(qbuf + half * kSlot));
+                    const uint64_t kd = umma_sdesc(smem_u32(ring + slot * kSlot));
+#pragma unroll
+                    for (int ks = 0; ks < 8; ks++)
+                        umma_bf16(tmem + kColS + 128 * w, umma_sdesc_step(qd, ks),
+                                  umma_sdesc_step(kd, ks), small ? kIdescS64 : kIdescS, ks > 0);
+                    umma_commit(&S.sfull[w]);
+                    sn[w]++;
+                    if (!dual || w == 1) umma_commit(&S.empty[slot]);
+                    if (j >= jobs - (dual ? 2 : 1)) umma_commit(&S.qempty[half]);
+                };
+                auto issue_o = [&](int j) {
+                    const int t = tile_of(j), w = j & 1;
+                    const int kk = k0 + 2 * t + 1, slot = kk % kRing;
+                    ok = ok && tree_wait(&S.pready[w], pn[w] & 1, &S.bad);
+                    if (!dual || w == 0) ok = ok && tree_wait(&S.full[slot], (kk / kRing) & 1, &S.bad);
+                    if (!ok) return;
+                    tc_fence_after();
+                    const int steps = (tile_valid(s, s.t0 + t) + 15) >> 4;
+                    const uint64_t vd = v_desc(smem_u32(ring + slot * kSlot));
+                    const uint32_t p = tmem + kColS + 128 * w;
+                    for (int ks = 0; ks < steps; ks++)
+                        umma_ts(tmem + 128 * w, p + 8 * ks, vd + (uint64_t)(ks * (2048 >> 4)), kIdescO,
+                                ks > 0 || last_pv[w] >= 0);
+                    last_pv[w] = j;
+                    umma_commit(&S.pvdone[w]);
+                    pn[w]++;
+                    if (!dual || w == 1) umma_commit(&S.empty[slot]);
+                };
+                issue_s(0);
+                if (ok && jobs > 1) issue_s(1);
+                for (int j = 0; ok && j < jobs; j++) {
+                    issue_o(j);
+                    if (ok && j + 2 < jobs) issue_s(j + 2);
+                }
+                k0 += 2 * nq;
+            }
+            if (!ok) {
+                // the MMAs in flight are done before tensor memory goes back
+                S.bad = 1;
+                umma_commit(&S.drain);
+                mbar_wait(&S.drain, 0);
+            }
+        }
+        __syncwarp();
+    } else {
+        // --------------------------------------------------------- softmax
+        const int w = warp >> 2, wl = warp & 3, r = wl * 32 + lane;   // row of the group's 128
+        const uint32_t lanes = (uint32_t)(wl * 32) << 16;
+        const uint32_t tS = tmem + lanes + kColS + 128 * w, tO = tmem + lanes + 128 * w;
+        bool ok = true;
+        int k0 = 0, sn = 0, pn = 0, ntree = 0;
+        while (walk.next(s)) {
+            const bool dual = s.rows > 128;
+            const int nq = s.t1 - s.t0;
+            const int row = (dual ? 128 * w : 0) + r;        // row of the item
+            const bool mine = row < s.rows;
+            const bool busy = (dual ? 128 * w : 0) + wl * 32 < s.rows;   // the warp has rows
+            const int grow = s.rb * kRows + row;             // row of the unit
+            float m = -INFINITY, l = 0.f;
+            int done = 0;                                    // this group's tiles so far
+            uint64_t odd = 0;                                // drafted tokens added by hand
+            uint64_t see = 0;
+            if (mine)
+                see = a.t.mask[(size_t)(s.u / a.t.units) * a.t.T + grow / a.G] &
+                      (s.live >= 64 ? ~0ull : (1ull << s.live) - 1);
+            for (int t = dual ? 0 : w; t < nq; t += dual ? 1 : 2) {
+                const int tile = s.t0 + t, nv = tile_valid(s, tile);
+                const bool tree = tile == s.nt - 1;
+                const int kv = k0 + 2 * t + 1, slot = kv % kRing;
+                const bool votes = a.votes != nullptr && !tree;
+                if (votes) {
+                    group_sync(w);                           // the last tile's are read
+                    const int i = tile * kTile + r;
+                    S.g[w].bias[r] = i < s.n ? log2f((float)a.votes[(size_t)s.u * a.cap + i]) : 0.f;
+                    group_sync(w);
+                }
+                // value rows the MMA reads that are no slot: zero
+                if (!dual || w == 0) {
+                    if (nv & 15 || tree) {
+                        ok = tree_wait(&S.full[slot], (kv / kRing) & 1, &S.bad) && ok;
+                        unsigned char *v = ring + slot * kSlot;
+                        const int stop = (nv + 15) & ~15;
+                        if (tree && r < 64) {
+                            // thread r has row r: what is not finite is zeroed here and
+                            // added to the rows that see it at the end
+                            bool bad = false;
+                            if (r < stop)
+                                for (int c = 0; c < 16; c++) {
+                                    unsigned char *p = v + (c >> 3) * kHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+                                    const uint4 x = lds_v4(p);
+                                    uint32_t q[4] = {x.x, x.y, x.z, x.w};
+                                    bool hit = r >= nv;
+#pragma unroll
+                                    for (int e = 0; e < 4; e++) {
+                                        const bool lo = (q[e] & 0x7f80u) == 0x7f80u;
+                                        const bool hi = (q[e] & 0x7f800000u) == 0x7f800000u;
+                                        hit |= lo || hi;
+                                        if (lo || r >= nv) q[e] &= 0xffff0000u;
+                                        if (hi || r >= nv) q[e] &= 0x0000ffffu;
+                                    }
+                                    if (hit)
+                                        *reinterpret_cast<uint4 *>(p) = make_uint4(q[0], q[1], q[2], q[3]);
+                                    bad |= hit;
+                                }
+                            const uint32_t bits = __ballot_sync(kFull, bad && r < nv);
+                            if (lane == 0) reinterpret_cast<uint32_t *>(&S.odd[ntree & 1])[wl] = bits;
+                        } else if (!tree && r >= nv && r < stop) {
+                            for (int c = 0; c < 16; c++)
+                                *reinterpret_cast<uint4 *>(v + (c >> 3) * kHalf + r * 128 +
+                                                           ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        group_sync(w);
+                    }
+                }
+                if (tree && dual) bar_sync<1, 256>();        // both groups see the odd tokens
+                if (tree) odd = S.odd[ntree & 1];
+                ok = tree_wait(&S.sfull[w], sn & 1, &S.bad) && ok;
+                sn++;
+                tc_fence_after();
+                if (busy) {
+                    float x[128];
+                    tmem_ld128(tS, x);
+                    if (votes) {
+#pragma unroll
+                        for (int j = 0; j < 128; j += 4) {
+                            const float4 b4 = *reinterpret_cast<const float4 *>(&S.g[w].bias[j]);
+                            x[j] = fmaf(x[j], a.scale, b4.x);
+                            x[j + 1] = fmaf(x[j + 1], a.scale, b4.y);
+                            x[j + 2] = fmaf(x[j + 2], a.scale, b4.z);
+                            x[j + 3] = fmaf(x[j + 3], a.scale, b4.w);
+                        }
+                    }
+                    if (nv < kTile || tree) {
+                        uint64_t lo64 = see, hi64 = 0;
+                        if (!tree) {
+                            lo64 = nv >= 64 ? ~0ull : (1ull << nv) - 1;
+                            hi64 = nv <= 64 ? 0ull : (1ull << (nv - 64)) - 1;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 64; j++) {
+                            x[j] = lo64 >> j & 1 ? x[j] : -INFINITY;
+                            x[64 + j] = hi64 >> j & 1 ? x[64 + j] : -INFINITY;
+                        }
+                    }
+                    float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                    for (int j = 4; j < 128; j += 4) {
+                        mx[0] = fmaxf(mx[0], x[j]);
+                        mx[1] = fmaxf(mx[1], x[j + 1]);
+                        mx[2] = fmaxf(mx[2], x[j + 2]);
+                        mx[3] = fmaxf(mx[3], x[j + 3]);
+                    }
+                    const float c = votes ? 1.f : a.scale;
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                    const bool move = top > m + kSlack || (m == -INFINITY && top > m);
+                    if (__any_sync(kFull, move)) {
+                        float f = 1.f;
+                        if (move) {
+                            f = m == -INFINITY ? 0.f : ex2_approx(m - top);
+                            m = top;
+                            l *= f;
+                        }
+                        if (done > 0) {
+#pragma unroll 1
+                            for (int h = 0; h < 4; h++) {
+                                uint32_t y[32];
+                                tmem_ld32_async(tO + 32 * h, y);
+                                tmem_wait_ld();
+                                tmem_bind(y);
+#pragma unroll
+                                for (int j = 0; j < 32; j++)
+                                    y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
+                                tmem_st32(tO + 32 * h, y);
+                            }
+                            tmem_wait_st();
+                        }
+                    }
+                    const float ref = m == -INFINITY ? 0.f : m;
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int h = 0; h < 4; h++) {
+                        uint32_t p[16];
+#pragma unroll
+                        for (int j = 0; j < 16; j++) {
+                            const float e0 = ex2_approx(fmaf(x[32 * h + 2 * j], c, -ref));
+                            const float e1 = ex2_approx(fmaf(x[32 * h + 2 * j + 1], c, -ref));
+                            sum[j & 1] += e0;
+                            sum[2 + (j & 1)] += e1;
+                            p[j] = pack_bf16(e0, e1);
+                        }
+                        tmem_st16(tS + 16 * h, p);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tmem_wait_st();
+                }
+                done++;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&S.pready[w]);
+                pn++;
+            }
+            k0 += 2 * nq;
+            // ------------------------------------------------------ outputs
+            if (done > 0) ok = tree_wait(&S.pvdone[w], (pn - 1) & 1, &S.bad) && ok;
+            tc_fence_after();
+            const bool all = s.t1 - s.t0 == s.nt;            // nothing to join
+            const bool direct = all && !a.join_all;
+            float c0 = 1.f, c1 = 0.f, M = m, Lsum = l;       // weights of the groups' sums
+            if (!dual) {
+                S.g[w].ml[r] = make_float2(m, l);
+                tc_fence_before();
+                bar_sync<1, 256>();
+                tc_fence_after();
+                odd = S.odd[ntree & 1];          // written by the group that had the tokens' tile
+                const float2 p0 = S.g[0].ml[r], p1 = S.g[1].ml[r];
+                M = fmaxf(p0.x, p1.x);
+                const float ref = M == -INFINITY ? 0.f : M;
+                c0 = ex2_approx(p0.x - ref);
+                c1 = ex2_approx(p1.x - ref);
+                Lsum = p0.y * c0 + p1.y * c1;
+            }
+            const size_t sid = (size_t)s.item + blockIdx.x;
+            const size_t orow = (size_t)s.u * a.TG + grow;
+            const float inv = Lsum == 0.f ? 0.f : 1.f / Lsum;
+            const float k_0 = direct ? c0 * inv : c0, k_1 = direct ? c1 * inv : c1;
+            const bool has_tree = s.t1 == s.nt;
+            const uint64_t by_hand = has_tree ? odd & see : 0;
+            ntree += has_tree;
+            // a group writes its rows whole, or (alternate tiles) half of the columns
+            if (busy) {
+                const int q0 = dual ? 0 : 2 * w, q1 = dual ? 4 : 2 * w + 2;
+#pragma unroll 1
+                for (int q = q0; q < q1; q++) {
+                    uint32_t y[32], z[32];
+                    tmem_ld32_async(tmem + lanes + (dual ? 128 * w : 0) + 32 * q, y);
+                    if (!dual && nq > 1) tmem_ld32_async(tmem + lanes + 128 + 32 * q, z);
+                    tmem_wait_ld();
+                    tmem_bind(y);
+                    float f[32];
+#pragma unroll
+                    for (int j = 0; j < 32; j++) f[j] = __uint_as_float(y[j]) * k_0;
+                    if (!dual && nq > 1) {
+                        tmem_bind(z);
+#pragma unroll
+                        for (int j = 0; j < 32; j++) f[j] = fmaf(__uint_as_float(z[j]), k_1, f[j]);
+                    }
+                    if (by_hand) {
+                        // a visible value that is not finite: whatever its weight, the
+                        // output is what weight x value gives, not finite
+                        for (uint64_t rest = by_hand; rest; rest &= rest - 1) {
+                            const int jt = __ffsll((long long)rest) - 1;
+                            const uint16_t *vr = a.vt + ((size_t)s.u * a.t.T + jt) * kD + 32 * q;
+#pragma unroll
+                            for (int j = 0; j < 32; j++) {
+                                const float v = bf2f(vr[j]);
+                                f[j] += isfinite(v) ? 0.f : v;
+                            }
+                        }
+                    }
+                    if (mine && ok) {
+                        if (direct) {
+                            uint4 *d = reinterpret_cast<uint4 *>(a.o + orow * kD + 32 * q);
+#pragma unroll
+                            for (int j = 0; j < 4; j++)
+                                d[j] = make_uint4(pack_bf16(f[8 * j], f[8 * j + 1]),
+                                                  pack_bf16(f[8 * j + 2], f[8 * j + 3]),
+                                                  pack_bf16(f[8 * j + 4], f[8 * j + 5]),
+                                                  pack_bf16(f[8 * j + 6], f[8 * j + 7]));
+                        } else {
+                            float4 *d = reinterpret_cast<float4 *>(
+                                a.part + (sid * a.rows + row) * kD + 32 * q);
+#pragma unroll
+                            for (int j = 0; j < 8; j++)
+                                d[j] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+                        }
+                    }
+                }
+                if (mine && ok && (dual || w == 0)) {
+                    if (direct)
+                        a.lse[orow] = Lsum == 0.f ? -INFINITY
+                                                  : (M + log2f(Lsum)) * 0.6931471805599453f;
+                    else
+                        a.ml[sid * a.rows + row] = make_float2(M, Lsum);
+                }
+            }
+            // the other group reads this one's sums: both are done before either goes on
+            tc_fence_before();
+            if (!dual) bar_sync<1, 256>();
+        }
+    }
+    __syncthreads();
+    if (warp == kMma) tmem_dealloc(tmem, 512);
+    if (tid == 0 && S.bad) record_status(a.status, KVC_ERR_TIMEOUT);
+}
+
+// The sums of an item's parts added and normalised, and (kMom) mixed with the
+// evicted set's estimate, C q on tensor cores (mma.sync, C as two bf16 terms).
+// One CTA per item and `chunk` rows, 16 rows at a time; warp w has the output
+// columns [16 w, 16 w + 16), in the MMA's accumulator layout.
+struct JoinArgs {
+    AttArgs a;
+    const uint16_t *q;
+    const float *mn, *mu_k, *mu_v, *C;
+    int first_order, chunk, grid;
+};
+
+template <bool kMom>
+__global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ JoinArgs j)
+{
+    const AttArgs &a = j.a;
+    __shared__ float zs[16];
+    const int item = blockIdx.x, u = item / a.RB, rb = item - u * a.RB;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int n = a.len[u], live = tree_live(a.t, u);
+    if (n < 0 || n > a.max_len || live < 0) return;
+    const int rows = min(kRows, live * a.G - rb * kRows);
+    const int r_end = min(rows, (int)(blockIdx.y + 1) * j.chunk);
+    int r0 = blockIdx.y * j.chunk;
+    if (r0 >= r_end) return;
+    int c0, c1;
+    if (a.whole) {
+        c0 = c1 = (int)((((long long)item + 1) * j.grid - 1) / (a.U * a.RB));
+    } else {
+        // tile x is in part ((x + 1) g - 1) / W
+        const long long b = a.first[item], e = a.first[item + 1], W = a.first[a.U * a.RB];
+        const int g = parts_of(j.grid, (int)W);
+        c0 = (int)(((b + 1) * g - 1) / W);
+        c1 = (int)((e * g - 1) / W);
+    }
+    if (!kMom && c0 == c1) return;               // finished by its CTA
+    const float ne = kMom ? j.mn[u] : 0.f;
+    const bool mix = kMom && ne > 0.f;
+    const int g = lane >> 2, c = 16 * warp + 2 * (lane & 3);   // row of 8, column of the pair
+    uint32_t bh[2][8][2], bl[2][8][2];
+    if (kMom && mix && j.first_order) {
+        const float *C = j.C + (size_t)u * kD * kD;
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+#pragma unroll
+            for (int ks = 0; ks < 8; ks++)
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    const float2 x = *reinterpret_cast<const float2 *>(
+                        C + (16 * warp + 8 * i + g) * kD + 16 * ks + 8 * h + 2 * (lane & 3));
+                    uint16_t h0, l0, h1, l1;
+                    split_bf16(x.x, h0, l0);
+                    split_bf16(x.y, h1, l1);
+                    bh[i][ks][h] = h0 | (uint32_t)h1 << 16;
+                    bl[i][ks][h] = l0 | (uint32_t)l1 << 16;
+                }
+    }
+    const size_t ubase = (size_t)u * a.TG + (size_t)rb * kRows;
+    for (; r0 < r_end; r0 += 16) {
+        const int ra[2] = {r0 + g, r0 + g + 8};
+        float M[2] = {-INFINITY, -INFINITY}, L[2] = {0.f, 0.f}, f[2][2][2] = {};
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const int r = min(ra[h], rows - 1);
+            for (int k = c0; k <= c1; k++)
+                M[h] = fmaxf(M[h], a.ml[((size_t)item + k) * a.rows + r].x);
+            const float ref = M[h] == -INFINITY ? 0.f : M[h];
+            for (int k = c0; k <= c1; k++) {
+                const size_t at = ((size_t)item + k) * a.rows + r;
+                const float2 ml = a.ml[at];
+                const float s = ex2_approx(ml.x - ref);
+                L[h] += ml.y * s;
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    const float2 p = *reinterpret_cast<const float2 *>(a.part + at * kD + c + 8 * i);
+                    f[h][i][0] = fmaf(p.x, s, f[h][i][0]);
+                    f[h][i][1] = fmaf(p.y, s, f[h][i][1]);
+                }
+            }
+        }
+        float lse[2];
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            lse[h] = L[h] == 0.f ? -INFINITY : (M[h] + log2f(L[h])) * 0.6931471805599453f;
+            const float inv = L[h] == 0.f ? 0.f : 1.f / L[h];
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                f[h][i][0] *= inv;
+                f[h][i][1] *= inv;
+            }
+        }
+        if (kMom && mix) {
+            const float sd = rsqrtf((float)kD);
+            __syncthreads();
+            for (int h = 0; h < 2; h++) {
+                const int r = min(r0 + 2 * warp + h, rows - 1);
+                const uint2 qw = reinterpret_cast<const uint2 *>(j.q + (ubase + r) * kD)[lane];
+                const float *mk = j.mu_k + (size_t)u * kD + 4 * lane;
+                const float z = warp_sum(bf_lo(qw.x) * mk[0] + bf_hi(qw.x) * mk[1] +
+                                         bf_lo(qw.y) * mk[2] + bf_hi(qw.y) * mk[3]);
+                if (lane == 0) zs[2 * warp + h] = logf(ne) + sd * z;
+            }
+            __syncthreads();
+            float d[2][4] = {};
+            if (j.first_order) {
+                const uint32_t *qa = reinterpret_cast<const uint32_t *>(
+                    j.q + (ubase + min(ra[0], rows - 1)) * kD) + (lane & 3);
+                const uint32_t *qb = reinterpret_cast<const uint32_t *>(
+                    j.q + (ubase + min(ra[1], rows - 1)) * kD) + (lane & 3);
+#pragma unroll
+                for (int ks = 0; ks < 8; ks++) {
+                    const uint32_t a0 = qa[8 * ks], a1 = qb[8 * ks], a2 = qa[8 * ks + 4],
+                                   a3 = qb[8 * ks + 4];
+#pragma unroll
+                    for (int i = 0; i < 2; i++) {
+                        mma16816(d[i], a0, a1, a2, a3, bl[i][ks][0], bl[i][ks][1]);
+                        mma16816(d[i], a0, a1, a2, a3, bh[i][ks][0], bh[i][ks][1]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const float w = 1.f / (1.f + expf(zs[g + 8 * h] - lse[h]));
+#pragma unroll
+                for (int i = 0; i < 2; i++)
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {
+                        const float m = j.mu_v[(size_t)u * kD + c + 8 * i + e] + sd * d[i][2 * h + e];
+                        f[h][i][e] = w * f[h][i][e] + (1.f - w) * m;
+                    }
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            if (ra[h] >= r_end) continue;
+            const size_t row = ubase + ra[h];
+#pragma unroll
+            for (int i = 0; i < 2; i++)
+                *reinterpret_cast<uint32_t *>(a.o + row * kD + c + 8 * i) =
+                    pack_bf16(f[h][i][0], f[h][i][1]);
+            if (warp == 0 && (lane & 3) == 0) a.lse[row] = lse[h];
+        }
+    }
+}
+
+struct TreeWs {
+    int32_t *status;
+    int *first;
+    float2 *ml;
+    float *part;
+    size_t bytes;
+};
+
+TreeWs tree_ws(const kvc_params &p, int T, void *base)
+{
+    TreeWs w{};
+    char *b = static_cast<char *>(base);
+    size_t off = 0;
+    auto take = [&](size_t n) {
+        char *r = b ? b + off : nullptr;
+        off += align_up(n);
+        return r;
+    };
+    const size_t TG = (size_t)T * p.G, items = (size_t)p.U * ((TG + kRows - 1) / kRows);
+    const size_t rows = TG < (size_t)kRows ? TG : (size_t)kRows;
+    w.status = reinterpret_cast<int32_t *>(take(sizeof(WsHeader)));
+    w.first = reinterpret_cast<int *>(take((items + 1) * sizeof(int)));
+    w.ml = reinterpret_cast<float2 *>(take((items + kGrid) * rows * sizeof(float2)));
+    w.part = reinterpret_cast<float *>(take((items + kGrid) * rows * kD * sizeof(float)));
+    w.bytes = off;
+    return w;
 }
 
 }  // namespace
 
-size_t tree_ws_bytes(const kvc_params &, int) { return align_up(sizeof(WsHeader)); }
+size_t tree_ws_bytes(const kvc_params &p, int T) { return tree_ws(p, T, nullptr).bytes; }
 
 cudaError_t launch_tree_attend(const kvc_params &p, int max_len, const TreeArgs &t,
                                const uint16_t *q, const uint16_t *kt, const uint16_t *vt,
                                const kvc_cache &c, const kvc_moments *m, uint16_t *o, float *lse,
                                void *ws, cudaStream_t st)
 {
-    AttArgs a{t, q, kt, vt, c.K, c.V, c.votes, c.len, m ? m->n : nullptr, m ? m->mu_k : nullptr,
-              m ? m->mu_v : nullptr, m ? m->C : nullptr, o, lse, static_cast<int32_t *>(ws), p.G,
-              p.cap, max_len, p.correction == KVC_CORR_FIRST_ORDER};
-    tree_attend_kernel<<<dim3(p.U, (t.T * p.G + 7) / 8), 256, 0, st>>>(a);
+    const TreeWs w = tree_ws(p, t.T, ws);
+    const int TG = t.T * p.G, RB = (TG + kRows - 1) / kRows;
+    const long long items = (long long)p.U * RB, tmax = (max_len + kTile - 1) / kTile + 1;
+    if (items * tmax > 0x7fffffffll) return cudaErrorInvalidValue;
+    CUtensorMap mk, mv, mq, mkt, mvt;
+    if (!make_unit_map(&mk, c.K, p.U, p.cap) || !make_unit_map(&mv, c.V, p.U, p.cap) ||
+        !make_unit_map(&mq, q, p.U, TG) || !make_unit_map(&mkt, kt, p.U, t.T) ||
+        !make_unit_map(&mvt, vt, p.U, t.T))
+        return cudaErrorInvalidValue;
+    const bool whole = tmax <= 4 || items >= 8 * kGrid;
+    long long grid = whole ? items : (items * tmax + 3) / 4;
+    if (grid < items) grid = items;
+    if (grid > kGrid) grid = kGrid;
+    AttArgs a{t, c.votes, c.len, vt, o, lse, w.part, w.ml, w.first, w.status, p.U, RB, TG, p.G, p.cap,
+              max_len, TG < kRows ? TG : kRows, whole, m != nullptr, kLog2e / sqrtf((float)kD)};
+    cudaError_t e = cudaFuncSetAttribute(tree_attend_kernel,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDyn);
+    if (e != cudaSuccess) return e;
+    tree_attend_kernel<<<(int)grid, kThreads, kDyn, st>>>(a, mk, mv, mq, mkt, mvt);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (m == nullptr && whole) return cudaSuccess;
+    const int chunk = m && items >= kGrid ? 64 : 16;
+    JoinArgs j{a, q, m ? m->n : nullptr, m ? m->mu_k : nullptr, m ? m->mu_v : nullptr,
+               m ? m->C : nullptr, p.correction == KVC_CORR_FIRST_ORDER, chunk, (int)grid};
+    const dim3 jg((unsigned)items, (a.rows + chunk - 1) / chunk);
+    if (m) tree_join_kernel<true><<<jg, 256, 0, st>>>(j);
+    else tree_join_kernel<false><<<jg, 256, 0, st>>>(j);
     return cudaGetLastError();
 }
 
