@@ -245,6 +245,136 @@ __device__ __forceinline__ int tile_valid(const Seg &s, int t)
     return t == s.nt - 1 ? s.live : min(kTile, s.n - t * kTile);
 }
 
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<const uint64_t &>(a)), "l"(reinterpret_cast<const uint64_t &>(b)),
+          "l"(reinterpret_cast<const uint64_t &>(c)));
+    return d;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<const uint64_t &>(a)), "l"(reinterpret_cast<const uint64_t &>(b)));
+    return d;
+}
+
+// Logits (in powers of two) of 32 slots of the thread's row: raw products in,
+// scaled, biased and masked.  Without a bias the scale is applied later.
+template <bool kMask>
+__device__ __forceinline__ void logits32(uint32_t (&y)[32], float scale, const float *bias,
+                                         uint32_t keep)
+{
+    if (bias) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+            const float4 b = *reinterpret_cast<const float4 *>(bias + j);
+            y[j] = __float_as_uint(fmaf(__uint_as_float(y[j]), scale, b.x));
+            y[j + 1] = __float_as_uint(fmaf(__uint_as_float(y[j + 1]), scale, b.y));
+            y[j + 2] = __float_as_uint(fmaf(__uint_as_float(y[j + 2]), scale, b.z));
+            y[j + 3] = __float_as_uint(fmaf(__uint_as_float(y[j + 3]), scale, b.w));
+        }
+    }
+    if (kMask) {
+#pragma unroll
+        for (int j = 0; j < 32; j++) y[j] = keep >> j & 1 ? y[j] : 0xff800000u;   // -inf
+    }
+}
+
+// One tile of the thread's row: S (128 columns at tS) is read twice, 32
+// columns at a time with the next 32 in flight (all 128 held at once spill),
+// for the maximum and for the weights, which replace it as bf16 pairs.
+template <bool kMask>
+__device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float scale,
+                                             const float *bias, uint64_t lo64, uint64_t hi64,
+                                             bool rescale, float &m, float &l)
+{
+    const float c = bias ? 1.f : scale;
+    uint32_t ya[32], yb[32];
+    float mx[2] = {-INFINITY, -INFINITY};
+    auto top_of = [&](uint32_t (&y)[32], int h, uint32_t keep) {
+        logits32<kMask>(y, scale, bias ? bias + 32 * h : nullptr, keep);
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+            mx[0] = fmaxf(fmaxf(mx[0], __uint_as_float(y[j])), __uint_as_float(y[j + 1]));
+            mx[1] = fmaxf(fmaxf(mx[1], __uint_as_float(y[j + 2])), __uint_as_float(y[j + 3]));
+        }
+    };
+    tmem_ld32_async(tS, ya);
+#pragma unroll 1
+    for (int hh = 0; hh < 2; hh++) {
+        const uint64_t keep = hh ? hi64 : lo64;
+        tmem_wait_ld();
+        tmem_bind(ya);
+        tmem_ld32_async(tS + 64 * hh + 32, yb);
+        top_of(ya, 2 * hh, (uint32_t)keep);
+        tmem_wait_ld();
+        tmem_bind(yb);
+        if (hh == 0) tmem_ld32_async(tS + 64, ya);
+        else tmem_ld32_async(tS, ya);                      // the second pass's first
+        top_of(yb, 2 * hh + 1, (uint32_t)(keep >> 32));
+    }
+    const float top = fmaxf(mx[0], mx[1]) * c;
+    const bool move = top > m + kSlack || (m == -INFINITY && top > m);
+    if (__any_sync(kFull, move)) {
+        tmem_wait_ld();
+        tmem_bind(ya);
+        float f = 1.f;
+        if (move) {
+            f = m == -INFINITY ? 0.f : ex2_approx(m - top);
+            m = top;
+            l *= f;
+        }
+        if (rescale) {
+#pragma unroll 1
+            for (int h = 0; h < 4; h++) {
+                uint32_t y[32];
+                tmem_ld32_async(tO + 32 * h, y);
+                tmem_wait_ld();
+                tmem_bind(y);
+#pragma unroll
+                for (int j = 0; j < 32; j++) y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
+                tmem_st32(tO + 32 * h, y);
+            }
+        }
+    }
+    const float nref = m == -INFINITY ? 0.f : -m;
+    const float2 c2 = make_float2(c, c), r2 = make_float2(nref, nref);
+    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    auto weights = [&](uint32_t (&y)[32], int h, uint32_t keep) {
+        logits32<kMask>(y, scale, bias ? bias + 32 * h : nullptr, keep);
+        uint32_t p[16];
+#pragma unroll
+        for (int j = 0; j < 16; j++) {
+            const float2 x = make_float2(__uint_as_float(y[2 * j]), __uint_as_float(y[2 * j + 1]));
+            const float2 t = fma2(x, c2, r2);
+            const float2 e = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+            sum[j & 1] = add2(sum[j & 1], e);
+            p[j] = pack_bf16(e.x, e.y);
+        }
+        tmem_st16(tS + 16 * h, p);                          // over columns already read
+    };
+#pragma unroll 1
+    for (int hh = 0; hh < 2; hh++) {
+        const uint64_t keep = hh ? hi64 : lo64;
+        tmem_wait_ld();
+        tmem_bind(ya);
+        tmem_ld32_async(tS + 64 * hh + 32, yb);
+        weights(ya, 2 * hh, (uint32_t)keep);
+        tmem_wait_ld();
+        tmem_bind(yb);
+        if (hh == 0) tmem_ld32_async(tS + 64, ya);
+        weights(yb, 2 * hh + 1, (uint32_t)(keep >> 32));
+    }
+    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+    tmem_wait_st();
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
 tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmQ,
@@ -397,56 +527,76 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
         // ------------------------------------------------------ MMA issuer
         if (lane == 0) {
             bool ok = true;
-            int k0 = 0, nseg = 0;              // ring index of the segment's first tile
-            int qn[2] = {0, 0}, sn[2] = {0, 0}, pn[2] = {0, 0};
+            // slot and phase of the ring's next key and value tile; phases of
+            // the groups' barriers as bits
+            int ks_slot = 0, vs_slot = 1;
+            uint32_t ks_ph = 0, vs_ph = 0, q_ph = 0, p_ph = 0, begun = 0, nseg = 0;
+            const uint64_t q0 = umma_sdesc(smem_u32(qbuf)), k0 = umma_sdesc(smem_u32(ring));
+            const uint64_t v0 = v_desc(smem_u32(ring));
+            constexpr uint32_t kStep = kSlot >> 4;           // a slot in descriptor units
             while (ok && walk.next(s)) {
                 const bool dual = s.rows > 128;
                 const int nq = s.t1 - s.t0, jobs = dual ? 2 * nq : nq;
-                const int qh = nseg & 1;
-                nseg++;
-                int last_pv[2] = {-1, -1};
-                auto tile_of = [&](int j) { return dual ? j >> 1 : j; };
+                const uint32_t qh = nseg++ & 1;
+                uint32_t fresh = 3;                          // groups whose O starts anew
                 auto issue_s = [&](int j) {
-                    const int t = tile_of(j), w = j & 1, half = dual ? w : qh;
-                    const int kk = k0 + 2 * t, slot = kk % kRing;
+                    const uint32_t w = j & 1, half = dual ? w : qh;
+                    const int t = dual ? j >> 1 : j;
                     if (j < (dual ? 2 : 1)) {
-                        ok = ok && tree_wait(&S.qfull[half], qn[half] & 1, &S.bad);
-                        qn[half]++;
+                        ok = ok && tree_wait(&S.qfull[half], q_ph >> half & 1, &S.bad);
+                        q_ph ^= 1u << half;
                     }
-                    if (!dual || w == 0) ok = ok && tree_wait(&S.full[slot], (kk / kRing) & 1, &S.bad);
+                    if (!dual || w == 0) ok = ok && tree_wait(&S.full[ks_slot], ks_ph, &S.bad);
                     // the group's earlier weights, which S overlays, are used up
-                    if (pn[w] > 0) ok = ok && tree_wait(&S.pvdone[w], (pn[w] - 1) & 1, &S.bad);
+                    if (begun >> w & 1)
+                        ok = ok && tree_wait(&S.pvdone[w], (p_ph >> w & 1) ^ 1, &S.bad);
                     if (!ok) return;
                     tc_fence_after();
-                    const bool small = tile_valid(s, s.t0 + t) <= 64;
-                    const uint64_t qd = umma_sdesc(smem_u32(qbuf + half * kSlot));
-                    const uint64_t kd = umma_sdesc(smem_u32(ring + slot * kSlot));
+                    const uint32_t idesc =
+                        tile_valid(s, s.t0 + t) <= 64 ? kIdescS64 : kIdescS;
+                    const uint64_t qd = q0 + half * kStep, kd = k0 + (uint32_t)ks_slot * kStep;
+                    const uint32_t d = tmem + kColS + 128 * w;
 #pragma unroll
                     for (int ks = 0; ks < 8; ks++)
-                        umma_bf16(tmem + kColS + 128 * w, umma_sdesc_step(qd, ks),
-                                  umma_sdesc_step(kd, ks), small ? kIdescS64 : kIdescS, ks > 0);
+                        umma_bf16(d, umma_sdesc_step(qd, ks), umma_sdesc_step(kd, ks), idesc, ks > 0);
                     umma_commit(&S.sfull[w]);
-                    sn[w]++;
-                    if (!dual || w == 1) umma_commit(&S.empty[slot]);
                     if (j >= jobs - (dual ? 2 : 1)) umma_commit(&S.qempty[half]);
+                    if (!dual || w == 1) {
+                        umma_commit(&S.empty[ks_slot]);
+                        ks_slot += 2;
+                        if (ks_slot >= kRing) { ks_slot -= kRing; ks_ph ^= 1; }
+                    }
                 };
                 auto issue_o = [&](int j) {
-                    const int t = tile_of(j), w = j & 1;
-                    const int kk = k0 + 2 * t + 1, slot = kk % kRing;
-                    ok = ok && tree_wait(&S.pready[w], pn[w] & 1, &S.bad);
-                    if (!dual || w == 0) ok = ok && tree_wait(&S.full[slot], (kk / kRing) & 1, &S.bad);
+                    const uint32_t w = j & 1;
+                    const int t = dual ? j >> 1 : j;
+                    ok = ok && tree_wait(&S.pready[w], p_ph >> w & 1, &S.bad);
+                    if (!dual || w == 0) ok = ok && tree_wait(&S.full[vs_slot], vs_ph, &S.bad);
                     if (!ok) return;
                     tc_fence_after();
                     const int steps = (tile_valid(s, s.t0 + t) + 15) >> 4;
-                    const uint64_t vd = v_desc(smem_u32(ring + slot * kSlot));
-                    const uint32_t p = tmem + kColS + 128 * w;
-                    for (int ks = 0; ks < steps; ks++)
-                        umma_ts(tmem + 128 * w, p + 8 * ks, vd + (uint64_t)(ks * (2048 >> 4)), kIdescO,
-                                ks > 0 || last_pv[w] >= 0);
-                    last_pv[w] = j;
+                    const uint64_t vd = v0 + (uint32_t)vs_slot * kStep;
+                    const uint32_t d = tmem + 128 * w, p = tmem + kColS + 128 * w;
+                    const bool keep = !(fresh >> w & 1);
+                    if (steps == 8) {
+#pragma unroll
+                        for (int ks = 0; ks < 8; ks++)
+                            umma_ts(d, p + 8 * ks, vd + (uint64_t)(ks * (2048 >> 4)), kIdescO,
+                                    ks > 0 || keep);
+                    } else {
+                        for (int ks = 0; ks < steps; ks++)
+                            umma_ts(d, p + 8 * ks, vd + (uint64_t)(ks * (2048 >> 4)), kIdescO,
+                                    ks > 0 || keep);
+                    }
                     umma_commit(&S.pvdone[w]);
-                    pn[w]++;
-                    if (!dual || w == 1) umma_commit(&S.empty[slot]);
+                    fresh &= ~(1u << w);
+                    begun |= 1u << w;
+                    p_ph ^= 1u << w;
+                    if (!dual || w == 1) {
+                        umma_commit(&S.empty[vs_slot]);
+                        vs_slot += 2;
+                        if (vs_slot >= kRing) { vs_slot -= kRing; vs_ph ^= 1; }
+                    }
                 };
                 issue_s(0);
                 if (ok && jobs > 1) issue_s(1);
@@ -454,7 +604,6 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                     issue_o(j);
                     if (ok && j + 2 < jobs) issue_s(j + 2);
                 }
-                k0 += 2 * nq;
             }
             if (!ok) {
                 // the MMAs in flight are done before tensor memory goes back
@@ -541,80 +690,19 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                 sn++;
                 tc_fence_after();
                 if (busy) {
-                    float x[128];
-                    tmem_ld128(tS, x);
-                    if (votes) {
-#pragma unroll
-                        for (int j = 0; j < 128; j += 4) {
-                            const float4 b4 = *reinterpret_cast<const float4 *>(&S.g[w].bias[j]);
-                            x[j] = fmaf(x[j], a.scale, b4.x);
-                            x[j + 1] = fmaf(x[j + 1], a.scale, b4.y);
-                            x[j + 2] = fmaf(x[j + 2], a.scale, b4.z);
-                            x[j + 3] = fmaf(x[j + 3], a.scale, b4.w);
-                        }
+                    uint64_t lo64 = ~0ull, hi64 = ~0ull;     // slots the row may see
+                    if (tree) {
+                        lo64 = see;
+                        hi64 = 0;
+                    } else if (nv < kTile) {
+                        lo64 = nv >= 64 ? ~0ull : (1ull << nv) - 1;
+                        hi64 = nv <= 64 ? 0ull : (1ull << (nv - 64)) - 1;
                     }
-                    if (nv < kTile || tree) {
-                        uint64_t lo64 = see, hi64 = 0;
-                        if (!tree) {
-                            lo64 = nv >= 64 ? ~0ull : (1ull << nv) - 1;
-                            hi64 = nv <= 64 ? 0ull : (1ull << (nv - 64)) - 1;
-                        }
-#pragma unroll
-                        for (int j = 0; j < 64; j++) {
-                            x[j] = lo64 >> j & 1 ? x[j] : -INFINITY;
-                            x[64 + j] = hi64 >> j & 1 ? x[64 + j] : -INFINITY;
-                        }
-                    }
-                    float mx[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-                    for (int j = 4; j < 128; j += 4) {
-                        mx[0] = fmaxf(mx[0], x[j]);
-                        mx[1] = fmaxf(mx[1], x[j + 1]);
-                        mx[2] = fmaxf(mx[2], x[j + 2]);
-                        mx[3] = fmaxf(mx[3], x[j + 3]);
-                    }
-                    const float c = votes ? 1.f : a.scale;
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-                    const bool move = top > m + kSlack || (m == -INFINITY && top > m);
-                    if (__any_sync(kFull, move)) {
-                        float f = 1.f;
-                        if (move) {
-                            f = m == -INFINITY ? 0.f : ex2_approx(m - top);
-                            m = top;
-                            l *= f;
-                        }
-                        if (done > 0) {
-#pragma unroll 1
-                            for (int h = 0; h < 4; h++) {
-                                uint32_t y[32];
-                                tmem_ld32_async(tO + 32 * h, y);
-                                tmem_wait_ld();
-                                tmem_bind(y);
-#pragma unroll
-                                for (int j = 0; j < 32; j++)
-                                    y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
-                                tmem_st32(tO + 32 * h, y);
-                            }
-                            tmem_wait_st();
-                        }
-                    }
-                    const float ref = m == -INFINITY ? 0.f : m;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int h = 0; h < 4; h++) {
-                        uint32_t p[16];
-#pragma unroll
-                        for (int j = 0; j < 16; j++) {
-                            const float e0 = ex2_approx(fmaf(x[32 * h + 2 * j], c, -ref));
-                            const float e1 = ex2_approx(fmaf(x[32 * h + 2 * j + 1], c, -ref));
-                            sum[j & 1] += e0;
-                            sum[2 + (j & 1)] += e1;
-                            p[j] = pack_bf16(e0, e1);
-                        }
-                        tmem_st16(tS + 16 * h, p);
-                    }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                    tmem_wait_st();
+                    const float *bias = votes ? S.g[w].bias : nullptr;
+                    if (tree || nv < kTile)
+                        softmax_tile<true>(tS, tO, a.scale, bias, lo64, hi64, done > 0, m, l);
+                    else
+                        softmax_tile<false>(tS, tO, a.scale, bias, lo64, hi64, done > 0, m, l);
                 }
                 done++;
                 tc_fence_before();
