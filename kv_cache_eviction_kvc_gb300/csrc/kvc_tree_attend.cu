@@ -13,7 +13,9 @@
 // that is cut into equal parts, one per CTA (a persistent CTA per SM).  An
 // item inside one part is finished there; an item that a cut crosses leaves
 // partial sums (maximum, sum, output) per part, which tree_join_kernel adds.
-// The drafted tokens are the item's last tile.
+// With moments every item leaves its sums, and tree_moment_kernel mixes them
+// with the evicted set's estimate.  The drafted tokens are the item's last
+// tile.
 //
 // 320 threads:
 //   warps 0-3, 4-7  two softmax groups, each with its own S, P and O in tensor
@@ -73,7 +75,7 @@ struct AttArgs {
 
 struct AttSmem {
     union {                 // read as float4
-        float bias[kTile];  // ln p of a tile's slots
+        float vote[kTile];  // votes of a tile's slots
         float2 ml[kTile];   // at an item's end: the rows' maxima and sums
     } g[2];
     uint64_t full[kRing], empty[kRing];
@@ -85,6 +87,15 @@ struct AttSmem {
     int bad;
     uint32_t tmem;
 };
+
+// True on one lane of a converged warp; the compiler keeps what the branch
+// issues (descriptors and all) in uniform registers.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
 
 // Bounded wait.  Once one has run out every wait ends at once: each role then
 // walks its loops to the end (so that the barriers among them stay matched)
@@ -264,41 +275,27 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
     return d;
 }
 
-// Logits (in powers of two) of 32 slots of the thread's row: raw products in,
-// scaled, biased and masked.  Without a bias the scale is applied later.
-template <bool kMask>
-__device__ __forceinline__ void logits32(uint32_t (&y)[32], float scale, const float *bias,
-                                         uint32_t keep)
+// Hidden slots of 32 raw products: -inf.
+__device__ __forceinline__ void hide32(uint32_t (&y)[32], uint32_t keep)
 {
-    if (bias) {
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-            const float4 b = *reinterpret_cast<const float4 *>(bias + j);
-            y[j] = __float_as_uint(fmaf(__uint_as_float(y[j]), scale, b.x));
-            y[j + 1] = __float_as_uint(fmaf(__uint_as_float(y[j + 1]), scale, b.y));
-            y[j + 2] = __float_as_uint(fmaf(__uint_as_float(y[j + 2]), scale, b.z));
-            y[j + 3] = __float_as_uint(fmaf(__uint_as_float(y[j + 3]), scale, b.w));
-        }
-    }
-    if (kMask) {
-#pragma unroll
-        for (int j = 0; j < 32; j++) y[j] = keep >> j & 1 ? y[j] : 0xff800000u;   // -inf
-    }
+    for (int j = 0; j < 32; j++) y[j] = keep >> j & 1 ? y[j] : 0xff800000u;
 }
 
 // One tile of the thread's row: S (128 columns at tS) is read twice, 32
 // columns at a time with the next 32 in flight (all 128 held at once spill),
-// for the maximum and for the weights, which replace it as bf16 pairs.
+// for the maximum and for the weights, which replace it as bf16 pairs.  A
+// slot's vote multiplies its weight (exp(x + ln p) = p exp(x)), so the first
+// pass does not see it.
 template <bool kMask>
 __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float scale,
-                                             const float *bias, uint64_t lo64, uint64_t hi64,
+                                             const float *vote, uint64_t lo64, uint64_t hi64,
                                              bool rescale, float &m, float &l)
 {
-    const float c = bias ? 1.f : scale;
     uint32_t ya[32], yb[32];
     float mx[2] = {-INFINITY, -INFINITY};
-    auto top_of = [&](uint32_t (&y)[32], int h, uint32_t keep) {
-        logits32<kMask>(y, scale, bias ? bias + 32 * h : nullptr, keep);
+    auto top_of = [&](uint32_t (&y)[32], uint32_t keep) {
+        if (kMask) hide32(y, keep);
 #pragma unroll
         for (int j = 0; j < 32; j += 4) {
             mx[0] = fmaxf(fmaxf(mx[0], __uint_as_float(y[j])), __uint_as_float(y[j + 1]));
@@ -312,14 +309,14 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float sca
         tmem_wait_ld();
         tmem_bind(ya);
         tmem_ld32_async(tS + 64 * hh + 32, yb);
-        top_of(ya, 2 * hh, (uint32_t)keep);
+        top_of(ya, (uint32_t)keep);
         tmem_wait_ld();
         tmem_bind(yb);
         if (hh == 0) tmem_ld32_async(tS + 64, ya);
         else tmem_ld32_async(tS, ya);                      // the second pass's first
-        top_of(yb, 2 * hh + 1, (uint32_t)(keep >> 32));
+        top_of(yb, (uint32_t)(keep >> 32));
     }
-    const float top = fmaxf(mx[0], mx[1]) * c;
+    const float top = fmaxf(mx[0], mx[1]) * scale;
     const bool move = top > m + kSlack || (m == -INFINITY && top > m);
     if (__any_sync(kFull, move)) {
         tmem_wait_ld();
@@ -344,18 +341,33 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float sca
         }
     }
     const float nref = m == -INFINITY ? 0.f : -m;
-    const float2 c2 = make_float2(c, c), r2 = make_float2(nref, nref);
+    const float2 c2 = make_float2(scale, scale), r2 = make_float2(nref, nref);
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     auto weights = [&](uint32_t (&y)[32], int h, uint32_t keep) {
-        logits32<kMask>(y, scale, bias ? bias + 32 * h : nullptr, keep);
+        if (kMask) hide32(y, keep);
         uint32_t p[16];
 #pragma unroll
-        for (int j = 0; j < 16; j++) {
-            const float2 x = make_float2(__uint_as_float(y[2 * j]), __uint_as_float(y[2 * j + 1]));
-            const float2 t = fma2(x, c2, r2);
-            const float2 e = make_float2(ex2_approx(t.x), ex2_approx(t.y));
-            sum[j & 1] = add2(sum[j & 1], e);
-            p[j] = pack_bf16(e.x, e.y);
+        for (int j = 0; j < 16; j += 2) {
+            float2 e[2];
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                const float2 x = make_float2(__uint_as_float(y[2 * (j + i)]),
+                                             __uint_as_float(y[2 * (j + i) + 1]));
+                const float2 t = fma2(x, c2, r2);
+                e[i] = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+            }
+            if (vote) {
+                const float4 v = *reinterpret_cast<const float4 *>(vote + 32 * h + 2 * j);
+                e[0].x *= v.x;
+                e[0].y *= v.y;
+                e[1].x *= v.z;
+                e[1].y *= v.w;
+            }
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                sum[i] = add2(sum[i], e[i]);
+                p[j + i] = pack_bf16(e[i].x, e[i].y);
+            }
         }
         tmem_st16(tS + 16 * h, p);                          // over columns already read
     };
@@ -525,7 +537,8 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
         __syncwarp();
     } else if (warp == kMma) {
         // ------------------------------------------------------ MMA issuer
-        if (lane == 0) {
+        // the whole warp walks and waits, one lane issues
+        {
             bool ok = true;
             // slot and phase of the ring's next key and value tile; phases of
             // the groups' barriers as bits
@@ -550,19 +563,23 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                     // the group's earlier weights, which S overlays, are used up
                     if (begun >> w & 1)
                         ok = ok && tree_wait(&S.pvdone[w], (p_ph >> w & 1) ^ 1, &S.bad);
+                    ok = __all_sync(kFull, ok);
                     if (!ok) return;
                     tc_fence_after();
                     const uint32_t idesc =
                         tile_valid(s, s.t0 + t) <= 64 ? kIdescS64 : kIdescS;
                     const uint64_t qd = q0 + half * kStep, kd = k0 + (uint32_t)ks_slot * kStep;
                     const uint32_t d = tmem + kColS + 128 * w;
+                    if (elect_one()) {
 #pragma unroll
-                    for (int ks = 0; ks < 8; ks++)
-                        umma_bf16(d, umma_sdesc_step(qd, ks), umma_sdesc_step(kd, ks), idesc, ks > 0);
-                    umma_commit(&S.sfull[w]);
-                    if (j >= jobs - (dual ? 2 : 1)) umma_commit(&S.qempty[half]);
+                        for (int ks = 0; ks < 8; ks++)
+                            umma_bf16(d, umma_sdesc_step(qd, ks), umma_sdesc_step(kd, ks), idesc, ks > 0);
+                        umma_commit(&S.sfull[w]);
+                        if (j >= jobs - (dual ? 2 : 1)) umma_commit(&S.qempty[half]);
+                        if (!dual || w == 1) umma_commit(&S.empty[ks_slot]);
+                    }
+                    __syncwarp();
                     if (!dual || w == 1) {
-                        umma_commit(&S.empty[ks_slot]);
                         ks_slot += 2;
                         if (ks_slot >= kRing) { ks_slot -= kRing; ks_ph ^= 1; }
                     }
@@ -572,28 +589,32 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                     const int t = dual ? j >> 1 : j;
                     ok = ok && tree_wait(&S.pready[w], p_ph >> w & 1, &S.bad);
                     if (!dual || w == 0) ok = ok && tree_wait(&S.full[vs_slot], vs_ph, &S.bad);
+                    ok = __all_sync(kFull, ok);
                     if (!ok) return;
                     tc_fence_after();
                     const int steps = (tile_valid(s, s.t0 + t) + 15) >> 4;
                     const uint64_t vd = v0 + (uint32_t)vs_slot * kStep;
                     const uint32_t d = tmem + 128 * w, p = tmem + kColS + 128 * w;
                     const bool keep = !(fresh >> w & 1);
-                    if (steps == 8) {
+                    if (elect_one()) {
+                        if (steps == 8) {
 #pragma unroll
-                        for (int ks = 0; ks < 8; ks++)
-                            umma_ts(d, p + 8 * ks, vd + (uint64_t)(ks * (2048 >> 4)), kIdescO,
-                                    ks > 0 || keep);
-                    } else {
-                        for (int ks = 0; ks < steps; ks++)
-                            umma_ts(d, p + 8 * ks, vd + (uint64_t)(ks * (2048 >> 4)), kIdescO,
-                                    ks > 0 || keep);
+                            for (int ks = 0; ks < 8; ks++)
+                                umma_ts(d, p + 8 * ks, vd + (uint64_t)(ks * (2048 >> 4)), kIdescO,
+                                        ks > 0 || keep);
+                        } else {
+                            for (int ks = 0; ks < steps; ks++)
+                                umma_ts(d, p + 8 * ks, vd + (uint64_t)(ks * (2048 >> 4)), kIdescO,
+                                        ks > 0 || keep);
+                        }
+                        umma_commit(&S.pvdone[w]);
+                        if (!dual || w == 1) umma_commit(&S.empty[vs_slot]);
                     }
-                    umma_commit(&S.pvdone[w]);
+                    __syncwarp();
                     fresh &= ~(1u << w);
                     begun |= 1u << w;
                     p_ph ^= 1u << w;
                     if (!dual || w == 1) {
-                        umma_commit(&S.empty[vs_slot]);
                         vs_slot += 2;
                         if (vs_slot >= kRing) { vs_slot -= kRing; vs_ph ^= 1; }
                     }
@@ -608,8 +629,10 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
             if (!ok) {
                 // the MMAs in flight are done before tensor memory goes back
                 S.bad = 1;
-                umma_commit(&S.drain);
-                mbar_wait(&S.drain, 0);
+                if (lane == 0) {
+                    umma_commit(&S.drain);
+                    mbar_wait(&S.drain, 0);
+                }
             }
         }
         __syncwarp();
@@ -634,6 +657,11 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
             if (mine)
                 see = a.t.mask[(size_t)(s.u / a.t.units) * a.t.T + grow / a.G] &
                       (s.live >= 64 ? ~0ull : (1ull << s.live) - 1);
+            int vote_next = 0;                               // loaded a tile ahead
+            if (a.votes) {
+                const int i = (s.t0 + (dual ? 0 : w)) * kTile + r;
+                if (i < s.n) vote_next = a.votes[(size_t)s.u * a.cap + i];
+            }
             for (int t = dual ? 0 : w; t < nq; t += dual ? 1 : 2) {
                 const int tile = s.t0 + t, nv = tile_valid(s, tile);
                 const bool tree = tile == s.nt - 1;
@@ -641,8 +669,9 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                 const bool votes = a.votes != nullptr && !tree;
                 if (votes) {
                     group_sync(w);                           // the last tile's are read
-                    const int i = tile * kTile + r;
-                    S.g[w].bias[r] = i < s.n ? log2f((float)a.votes[(size_t)s.u * a.cap + i]) : 0.f;
+                    S.g[w].vote[r] = (float)vote_next;
+                    const int i = (tile + (dual ? 1 : 2)) * kTile + r;
+                    if (i < s.n) vote_next = a.votes[(size_t)s.u * a.cap + i];
                     group_sync(w);
                 }
                 // value rows the MMA reads that are no slot: zero
@@ -698,11 +727,11 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                         lo64 = nv >= 64 ? ~0ull : (1ull << nv) - 1;
                         hi64 = nv <= 64 ? 0ull : (1ull << (nv - 64)) - 1;
                     }
-                    const float *bias = votes ? S.g[w].bias : nullptr;
+                    const float *vote = votes ? S.g[w].vote : nullptr;
                     if (tree || nv < kTile)
-                        softmax_tile<true>(tS, tO, a.scale, bias, lo64, hi64, done > 0, m, l);
+                        softmax_tile<true>(tS, tO, a.scale, vote, lo64, hi64, done > 0, m, l);
                     else
-                        softmax_tile<false>(tS, tO, a.scale, bias, lo64, hi64, done > 0, m, l);
+                        softmax_tile<false>(tS, tO, a.scale, vote, lo64, hi64, done > 0, m, l);
                 }
                 done++;
                 tc_fence_before();
@@ -804,10 +833,6 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
     if (tid == 0 && S.bad) record_status(a.status, KVC_ERR_TIMEOUT);
 }
 
-// The sums of an item's parts added and normalised, and (kMom) mixed with the
-// evicted set's estimate, C q on tensor cores (mma.sync, C as two bf16 terms).
-// One CTA per item and `chunk` rows, 16 rows at a time; warp w has the output
-// columns [16 w, 16 w + 16), in the MMA's accumulator layout.
 struct JoinArgs {
     AttArgs a;
     const uint16_t *q;
@@ -815,20 +840,17 @@ struct JoinArgs {
     int first_order, chunk, grid;
 };
 
-template <bool kMom>
-__global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ JoinArgs j)
+// The parts [c0, c1] of an item, and its rows; false when it has none.
+__device__ __forceinline__ bool join_item(const JoinArgs &j, int item, int &u, int &rb, int &rows,
+                                          int &c0, int &c1)
 {
     const AttArgs &a = j.a;
-    __shared__ float zs[16];
-    const int item = blockIdx.x, u = item / a.RB, rb = item - u * a.RB;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    u = item / a.RB;
+    rb = item - u * a.RB;
     const int n = a.len[u], live = tree_live(a.t, u);
-    if (n < 0 || n > a.max_len || live < 0) return;
-    const int rows = min(kRows, live * a.G - rb * kRows);
-    const int r_end = min(rows, (int)(blockIdx.y + 1) * j.chunk);
-    int r0 = blockIdx.y * j.chunk;
-    if (r0 >= r_end) return;
-    int c0, c1;
+    if (n < 0 || n > a.max_len || live < 0) return false;
+    rows = min(kRows, live * a.G - rb * kRows);
+    if (rows <= 0) return false;
     if (a.whole) {
         c0 = c1 = (int)((((long long)item + 1) * j.grid - 1) / (a.U * a.RB));
     } else {
@@ -838,112 +860,192 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
         c0 = (int)(((b + 1) * g - 1) / W);
         c1 = (int)((e * g - 1) / W);
     }
-    if (!kMom && c0 == c1) return;               // finished by its CTA
-    const float ne = kMom ? j.mn[u] : 0.f;
-    const bool mix = kMom && ne > 0.f;
-    const int g = lane >> 2, c = 16 * warp + 2 * (lane & 3);   // row of 8, column of the pair
-    uint32_t bh[2][8][2], bl[2][8][2];
-    if (kMom && mix && j.first_order) {
-        const float *C = j.C + (size_t)u * kD * kD;
+    return true;
+}
+
+// The sums of an item's parts added: one warp per row, a lane has four
+// columns.  The result is the output, or (kKeep, when the moments follow) the
+// first part's place takes it.  grid (items, rows / 8).
+template <bool kKeep>
+__global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ JoinArgs j)
+{
+    const AttArgs &a = j.a;
+    const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
+    int u, rb, rows, c0, c1;
+    if (!join_item(j, blockIdx.x, u, rb, rows, c0, c1) || r >= rows || c0 == c1) return;
+    const size_t at = ((size_t)blockIdx.x + c0) * a.rows + r, step = (size_t)a.rows;
+    const int np = c1 - c0 + 1;
+    float M = -INFINITY;
+    for (int k = lane; k < np; k += 32) M = fmaxf(M, a.ml[at + k * step].x);
+    M = warp_max(M);
+    const float ref = M == -INFINITY ? 0.f : M;
+    float L = 0.f;
+    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < np; k0 += 32) {
+        float s = 0.f;
+        if (k0 + lane < np) {
+            const float2 ml = a.ml[at + (k0 + lane) * step];
+            s = ex2_approx(ml.x - ref);
+            L += ml.y * s;
+        }
+        const int m = min(32, np - k0);
+#pragma unroll 8
+        for (int k = 0; k < m; k++) {
+            const float c = __shfl_sync(kFull, s, k);
+            const float4 p =
+                reinterpret_cast<const float4 *>(a.part + (at + (k0 + k) * step) * kD)[lane];
+            f.x = fmaf(p.x, c, f.x);
+            f.y = fmaf(p.y, c, f.y);
+            f.z = fmaf(p.z, c, f.z);
+            f.w = fmaf(p.w, c, f.w);
+        }
+    }
+    L = warp_sum(L);
+    if (kKeep) {
+        reinterpret_cast<float4 *>(a.part + at * kD)[lane] = f;
+        if (lane == 0) a.ml[at] = make_float2(M, L);
+        return;
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const size_t row = (size_t)u * a.TG + (size_t)rb * kRows + r;
+    reinterpret_cast<uint2 *>(a.o + row * kD)[lane] =
+        make_uint2(pack_bf16(f.x * inv, f.y * inv), pack_bf16(f.z * inv, f.w * inv));
+    if (lane == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+}
+
+// The normalization correction: every row's sum normalised and mixed with the
+// evicted set's estimate.  C q runs on tensor cores (mma.sync) with C as two
+// bf16 terms (2^-16 of a product) in shared memory, 128-byte swizzled; a warp
+// has 16 rows, a CTA `chunk` rows of an item.
+constexpr int kMomWarps = 4;
+constexpr size_t kMomDyn = 2 * (size_t)kSlot;
+
+__global__ void __launch_bounds__(kMomWarps * 32) tree_moment_kernel(const __grid_constant__ JoinArgs j)
+{
+    const AttArgs &a = j.a;
+    extern __shared__ __align__(1024) unsigned char cs[];   // C: high terms, low terms
+    __shared__ float muk[kD], muv[kD];
+    int u, rb, rows, c0, c1;
+    if (!join_item(j, blockIdx.x, u, rb, rows, c0, c1)) return;
+    const int r_end = min(rows, (int)(blockIdx.y + 1) * j.chunk);
+    if ((int)blockIdx.y * j.chunk >= r_end) return;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    const float ne = j.mn[u];
+    const bool mix = ne > 0.f;
+    if (mix) {
+        muk[tid] = j.mu_k[(size_t)u * kD + tid];
+        muv[tid] = j.mu_v[(size_t)u * kD + tid];
+        if (j.first_order) {
+            const float4 *C = reinterpret_cast<const float4 *>(j.C + (size_t)u * kD * kD);
+            // 16 bytes of bf16 per step: 8 elements of a row
+#pragma unroll 4
+            for (int i = 0; i < kD * 16 / (kMomWarps * 32); i++) {
+                const int e = i * kMomWarps * 32 + tid, row = e >> 4, ch = e & 15;
+                const float4 x = C[2 * e], y = C[2 * e + 1];
+                const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+                uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int i = 0; i < 2; i++)
+                for (int k = 0; k < 4; k++) {
+                    uint16_t h0, l0, h1, l1;
+                    split_bf16(v[2 * k], h0, l0);
+                    split_bf16(v[2 * k + 1], h1, l1);
+                    hi[k] = h0 | (uint32_t)h1 << 16;
+                    lo[k] = l0 | (uint32_t)l1 << 16;
+                }
+                unsigned char *d = cs + sw_off_t<128>(row, ch);
+                *reinterpret_cast<uint4 *>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4 *>(d + kSlot) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+        }
+    }
+    __syncthreads();
+    const size_t ubase = (size_t)u * a.TG + (size_t)rb * kRows;
+    const size_t pbase = ((size_t)blockIdx.x + c0) * a.rows;
+    const float sd = rsqrtf((float)kD);
+    for (int r0 = blockIdx.y * j.chunk + 16 * warp; r0 < r_end; r0 += 16 * kMomWarps) {
+        const int ra = min(r0 + g, rows - 1), rb8 = min(r0 + g + 8, rows - 1);
+        const float2 ml[2] = {a.ml[pbase + ra], a.ml[pbase + rb8]};
+        uint32_t qa[8][4];
+        float z[2] = {0.f, 0.f};
+        float d[16][4];
+#pragma unroll
+        for (int i = 0; i < 16; i++) d[i][0] = d[i][1] = d[i][2] = d[i][3] = 0.f;
+        if (mix) {
+            const uint32_t *pa = reinterpret_cast<const uint32_t *>(j.q + (ubase + ra) * kD) + t;
+            const uint32_t *pb = reinterpret_cast<const uint32_t *>(j.q + (ubase + rb8) * kD) + t;
+#pragma unroll
+            for (int ks = 0; ks < 8; ks++) {
+                qa[ks][0] = pa[8 * ks];
+                qa[ks][1] = pb[8 * ks];
+                qa[ks][2] = pa[8 * ks + 4];
+                qa[ks][3] = pb[8 * ks + 4];
+            }
 #pragma unroll
             for (int ks = 0; ks < 8; ks++)
 #pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    const float2 x = *reinterpret_cast<const float2 *>(
-                        C + (16 * warp + 8 * i + g) * kD + 16 * ks + 8 * h + 2 * (lane & 3));
-                    uint16_t h0, l0, h1, l1;
-                    split_bf16(x.x, h0, l0);
-                    split_bf16(x.y, h1, l1);
-                    bh[i][ks][h] = h0 | (uint32_t)h1 << 16;
-                    bl[i][ks][h] = l0 | (uint32_t)l1 << 16;
+                for (int h = 0; h < 4; h++) {
+                    const int k = 16 * ks + 8 * (h >> 1) + 2 * t;
+                    z[h & 1] += bf_lo(qa[ks][h]) * muk[k] + bf_hi(qa[ks][h]) * muk[k + 1];
                 }
-    }
-    const size_t ubase = (size_t)u * a.TG + (size_t)rb * kRows;
-    for (; r0 < r_end; r0 += 16) {
-        const int ra[2] = {r0 + g, r0 + g + 8};
-        float M[2] = {-INFINITY, -INFINITY}, L[2] = {0.f, 0.f}, f[2][2][2] = {};
-#pragma unroll
-        for (int h = 0; h < 2; h++) {
-            const int r = min(ra[h], rows - 1);
-            for (int k = c0; k <= c1; k++)
-                M[h] = fmaxf(M[h], a.ml[((size_t)item + k) * a.rows + r].x);
-            const float ref = M[h] == -INFINITY ? 0.f : M[h];
-            for (int k = c0; k <= c1; k++) {
-                const size_t at = ((size_t)item + k) * a.rows + r;
-                const float2 ml = a.ml[at];
-                const float s = ex2_approx(ml.x - ref);
-                L[h] += ml.y * s;
-#pragma unroll
-                for (int i = 0; i < 2; i++) {
-                    const float2 p = *reinterpret_cast<const float2 *>(a.part + at * kD + c + 8 * i);
-                    f[h][i][0] = fmaf(p.x, s, f[h][i][0]);
-                    f[h][i][1] = fmaf(p.y, s, f[h][i][1]);
-                }
-            }
-        }
-        float lse[2];
-#pragma unroll
-        for (int h = 0; h < 2; h++) {
-            lse[h] = L[h] == 0.f ? -INFINITY : (M[h] + log2f(L[h])) * 0.6931471805599453f;
-            const float inv = L[h] == 0.f ? 0.f : 1.f / L[h];
-#pragma unroll
-            for (int i = 0; i < 2; i++) {
-                f[h][i][0] *= inv;
-                f[h][i][1] *= inv;
-            }
-        }
-        if (kMom && mix) {
-            const float sd = rsqrtf((float)kD);
-            __syncthreads();
-            for (int h = 0; h < 2; h++) {
-                const int r = min(r0 + 2 * warp + h, rows - 1);
-                const uint2 qw = reinterpret_cast<const uint2 *>(j.q + (ubase + r) * kD)[lane];
-                const float *mk = j.mu_k + (size_t)u * kD + 4 * lane;
-                const float z = warp_sum(bf_lo(qw.x) * mk[0] + bf_hi(qw.x) * mk[1] +
-                                         bf_lo(qw.y) * mk[2] + bf_hi(qw.y) * mk[3]);
-                if (lane == 0) zs[2 * warp + h] = logf(ne) + sd * z;
-            }
-            __syncthreads();
-            float d[2][4] = {};
             if (j.first_order) {
-                const uint32_t *qa = reinterpret_cast<const uint32_t *>(
-                    j.q + (ubase + min(ra[0], rows - 1)) * kD) + (lane & 3);
-                const uint32_t *qb = reinterpret_cast<const uint32_t *>(
-                    j.q + (ubase + min(ra[1], rows - 1)) * kD) + (lane & 3);
+                // a quarter-warp's address of ldmatrix: columns (rows of C) i .. i + 7,
+                // k-chunks of two steps
+                const uint32_t base = smem_u32(cs);
 #pragma unroll
-                for (int ks = 0; ks < 8; ks++) {
-                    const uint32_t a0 = qa[8 * ks], a1 = qb[8 * ks], a2 = qa[8 * ks + 4],
-                                   a3 = qb[8 * ks + 4];
+                for (int i = 0; i < 16; i++) {
 #pragma unroll
-                    for (int i = 0; i < 2; i++) {
-                        mma16816(d[i], a0, a1, a2, a3, bl[i][ks][0], bl[i][ks][1]);
-                        mma16816(d[i], a0, a1, a2, a3, bh[i][ks][0], bh[i][ks][1]);
+                    for (int k4 = 0; k4 < 4; k4++) {
+                        const uint32_t off = sw_off_t<128>(8 * i + (lane & 7), 4 * k4 + (lane >> 3));
+                        uint32_t b[4];
+                        ldsm_x4(base + kSlot + off, b[0], b[1], b[2], b[3]);
+                        mma16816(d[i], qa[2 * k4][0], qa[2 * k4][1], qa[2 * k4][2], qa[2 * k4][3], b[0], b[1]);
+                        mma16816(d[i], qa[2 * k4 + 1][0], qa[2 * k4 + 1][1], qa[2 * k4 + 1][2],
+                                 qa[2 * k4 + 1][3], b[2], b[3]);
+                        ldsm_x4(base + off, b[0], b[1], b[2], b[3]);
+                        mma16816(d[i], qa[2 * k4][0], qa[2 * k4][1], qa[2 * k4][2], qa[2 * k4][3], b[0], b[1]);
+                        mma16816(d[i], qa[2 * k4 + 1][0], qa[2 * k4 + 1][1], qa[2 * k4 + 1][2],
+                                 qa[2 * k4 + 1][3], b[2], b[3]);
                     }
                 }
             }
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-                const float w = 1.f / (1.f + expf(zs[g + 8 * h] - lse[h]));
-#pragma unroll
-                for (int i = 0; i < 2; i++)
-#pragma unroll
-                    for (int e = 0; e < 2; e++) {
-                        const float m = j.mu_v[(size_t)u * kD + c + 8 * i + e] + sd * d[i][2 * h + e];
-                        f[h][i][e] = w * f[h][i][e] + (1.f - w) * m;
-                    }
-            }
         }
+        float wf[2], we[2], lse[2];
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-            if (ra[h] >= r_end) continue;
-            const size_t row = ubase + ra[h];
+            lse[h] = ml[h].y == 0.f ? -INFINITY : (ml[h].x + log2f(ml[h].y)) * 0.6931471805599453f;
+            float w = 1.f;
+            if (mix) {
+                float x = z[h];
+                x += __shfl_xor_sync(kFull, x, 1);
+                x += __shfl_xor_sync(kFull, x, 2);
+                w = 1.f / (1.f + expf(logf(ne) + sd * x - lse[h]));
+            }
+            wf[h] = ml[h].y == 0.f ? 0.f : w / ml[h].y;
+            we[h] = 1.f - w;
+        }
+        const float *p0 = a.part + (pbase + ra) * kD + 2 * t, *p1 = a.part + (pbase + rb8) * kD + 2 * t;
+        uint32_t *o0 = reinterpret_cast<uint32_t *>(a.o + (ubase + ra) * kD + 2 * t);
+        uint32_t *o1 = reinterpret_cast<uint32_t *>(a.o + (ubase + rb8) * kD + 2 * t);
 #pragma unroll
-            for (int i = 0; i < 2; i++)
-                *reinterpret_cast<uint32_t *>(a.o + row * kD + c + 8 * i) =
-                    pack_bf16(f[h][i][0], f[h][i][1]);
-            if (warp == 0 && (lane & 3) == 0) a.lse[row] = lse[h];
+        for (int i = 0; i < 16; i++) {
+            const float2 x = *reinterpret_cast<const float2 *>(p0 + 8 * i);
+            const float2 y = *reinterpret_cast<const float2 *>(p1 + 8 * i);
+            float m0 = 0.f, m1 = 0.f;
+            if (mix) {
+                m0 = muv[8 * i + 2 * t];
+                m1 = muv[8 * i + 2 * t + 1];
+            }
+            const uint32_t a0 = pack_bf16(wf[0] * x.x + (mix ? we[0] * (m0 + sd * d[i][0]) : 0.f),
+                                          wf[0] * x.y + (mix ? we[0] * (m1 + sd * d[i][1]) : 0.f));
+            const uint32_t a1 = pack_bf16(wf[1] * y.x + (mix ? we[1] * (m0 + sd * d[i][2]) : 0.f),
+                                          wf[1] * y.y + (mix ? we[1] * (m1 + sd * d[i][3]) : 0.f));
+            if (r0 + g < r_end) o0[4 * i] = a0;
+            if (r0 + g + 8 < r_end) o1[4 * i] = a1;
+        }
+        if (t == 0) {
+            if (r0 + g < r_end) a.lse[ubase + ra] = lse[0];
+            if (r0 + g + 8 < r_end) a.lse[ubase + rb8] = lse[1];
         }
     }
 }
@@ -1006,12 +1108,23 @@ cudaError_t launch_tree_attend(const kvc_params &p, int max_len, const TreeArgs 
     tree_attend_kernel<<<(int)grid, kThreads, kDyn, st>>>(a, mk, mv, mq, mkt, mvt);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (m == nullptr && whole) return cudaSuccess;
-    const int chunk = m && items >= kGrid ? 64 : 16;
+    // enough CTAs to fill the SMs, else as many rows per copy of C as there are
+    const int chunk = items >= 2 * kGrid ? kRows : 64;
     JoinArgs j{a, q, m ? m->n : nullptr, m ? m->mu_k : nullptr, m ? m->mu_v : nullptr,
                m ? m->C : nullptr, p.correction == KVC_CORR_FIRST_ORDER, chunk, (int)grid};
-    const dim3 jg((unsigned)items, (a.rows + chunk - 1) / chunk);
-    if (m) tree_join_kernel<true><<<jg, 256, 0, st>>>(j);
-    else tree_join_kernel<false><<<jg, 256, 0, st>>>(j);
+    if (!whole) {
+        const dim3 g((unsigned)items, (a.rows + 7) / 8);
+        if (m) tree_join_kernel<true><<<g, 256, 0, st>>>(j);
+        else tree_join_kernel<false><<<g, 256, 0, st>>>(j);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    if (m) {
+        e = cudaFuncSetAttribute(tree_moment_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)kMomDyn);
+        if (e != cudaSuccess) return e;
+        const dim3 g((unsigned)items, (a.rows + chunk - 1) / chunk);
+        tree_moment_kernel<<<g, kMomWarps * 32, kMomDyn, st>>>(j);
+    }
     return cudaGetLastError();
 }
 
