@@ -17,15 +17,19 @@
 // with the evicted set's estimate.  The drafted tokens are the item's last
 // tile.
 //
-// 320 threads:
-//   warps 0-3, 4-7  two softmax groups, each with its own S, P and O in tensor
+// 576 threads:
+//   warps 0-7, 8-15 two softmax groups, each with its own S, P and O in tensor
 //                   memory.  Items of more than 128 rows give each group 128
 //                   of them; otherwise the groups take alternate tiles of the
-//                   same rows and add their sums at the end
-//   warp 8          producer (TMA into a ring of 32 KB key and value tiles)
-//   warp 9          tensor-memory owner and MMA issuer
+//                   same rows and add their sums at the end.  Two warps share
+//                   32 rows: each has 64 of a tile's 128 slots, which halves
+//                   the time from S to P that every tile waits for
+//   warp 16         producer (TMA into a ring of 32 KB key and value tiles)
+//   warp 17         tensor-memory owner and MMA issuer
 // Tensor memory: O of group w at column 128 w, S at 256 + 128 w; P (bf16)
-// overlays the first half of S.
+// overlays S, 32 columns at the start of each half.  The MMAs of one thread execute in the order
+// of their issue, so the S that overwrites a P follows the product that reads
+// it without a wait.
 //
 // What a row must not see: slots behind len and hidden drafted tokens are
 // masked in S by selection (never by adding -inf to what may be NaN).  The
@@ -46,8 +50,8 @@ constexpr int kRows = 256;                       // query rows per item
 constexpr int kSlot = kTile * kD * 2;            // 32 KB: a tile of keys or values
 constexpr int kHalf = kSlot / 2;                 // its 64-column half
 constexpr int kRing = 5;
-constexpr int kThreads = 320;
-constexpr int kProd = 8, kMma = 9;
+constexpr int kThreads = 576;
+constexpr int kProd = 16, kMma = 17;
 constexpr int kGrid = 152;                       // CTAs: one per SM
 constexpr uint32_t kColS = 256;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -68,6 +72,7 @@ struct AttArgs {
     float *part;            // [items + CTAs][rows][128]
     float2 *ml;             // [items + CTAs][rows]
     int *first;             // [items + 1] tiles before each item
+    int4 *cut;              // [CTAs] the item a part begins inside of: item, first and last part
     int32_t *status;
     int U, RB, TG, G, cap, max_len, rows, whole, join_all;
     float scale;            // log2(e) / sqrt(d)
@@ -75,9 +80,13 @@ struct AttArgs {
 
 struct AttSmem {
     union {                 // read as float4
-        float vote[kTile];  // votes of a tile's slots
+        struct {
+            float vote[kTile];               // votes of a tile's slots
+            __nv_bfloat16 top[2][kTile];     // the halves' maxima
+        };
         float2 ml[kTile];   // at an item's end: the rows' maxima and sums
     } g[2];
+    int4 cut;
     uint64_t full[kRing], empty[kRing];
     uint64_t drain;
     uint64_t qfull[2], qempty[2], sfull[2], pready[2], pvdone[2];
@@ -142,19 +151,6 @@ __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32])
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-        "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-        "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-        "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
-}
-
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16])
 {
     asm volatile(
@@ -163,6 +159,34 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16_async(uint32_t addr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(addr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_bind16(uint32_t (&r)[16])
+{
+    asm volatile(""
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                   "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                   "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
 
 __device__ __forceinline__ void tmem_wait_st()
@@ -183,11 +207,55 @@ __device__ __forceinline__ void bar_sync()
     asm volatile("bar.sync %0, %1;" ::"n"(kBar), "n"(kCount) : "memory");
 }
 
-// Barrier of one softmax group (2 + w) over its 128 threads.
+// Barrier of one softmax group (2 + w) over its 256 threads.
 __device__ __forceinline__ void group_sync(int w)
 {
-    if (w == 0) bar_sync<2, 128>();
-    else bar_sync<3, 128>();
+    if (w == 0) bar_sync<2, 256>();
+    else bar_sync<3, 256>();
+}
+
+// Barrier of the two warps that share rows (ids 4 .. 11); the second form
+// tells both whether either said yes.
+__device__ __forceinline__ void pair_sync(int id)
+{
+    asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
+}
+
+__device__ __forceinline__ bool pair_any(int id, bool x)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n bar.red.or.pred q, %1, 64, p;\n"
+        " selp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(r)
+        : "r"(id), "r"((uint32_t)x)
+        : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ void tmem_st1(uint32_t addr, float x)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(addr),
+                 "r"(__float_as_uint(x))
+                 : "memory");
+}
+
+__device__ __forceinline__ float tmem_ld1(uint32_t addr)
+{
+    uint32_t a;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\ntcgen05.wait::ld.sync.aligned;"
+                 : "=r"(a)
+                 : "r"(addr)
+                 : "memory");
+    return __uint_as_float(a);
+}
+
+// 32-byte stores: a whole sector per lane.
+__device__ __forceinline__ void st_v8(void *p, const uint32_t *r)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 
 // Tiles of an item: the cache's and, last, the drafted tokens'; none when it
@@ -275,79 +343,88 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
     return d;
 }
 
-// Hidden slots of 32 raw products: -inf.
-__device__ __forceinline__ void hide32(uint32_t (&y)[32], uint32_t keep)
+// Hidden slots of 16 raw products: -inf.
+__device__ __forceinline__ void hide16(uint32_t (&y)[16], uint32_t keep)
 {
 #pragma unroll
-    for (int j = 0; j < 32; j++) y[j] = keep >> j & 1 ? y[j] : 0xff800000u;
+    for (int j = 0; j < 16; j++) y[j] = keep >> j & 1 ? y[j] : 0xff800000u;
 }
 
-// One tile of the thread's row: S (128 columns at tS) is read twice, 32
-// columns at a time with the next 32 in flight (all 128 held at once spill),
-// for the maximum and for the weights, which replace it as bf16 pairs.  A
-// slot's vote multiplies its weight (exp(x + ln p) = p exp(x)), so the first
-// pass does not see it.
+// Half a tile of the thread's row (64 of 128 slots; `half`): the row's maximum
+// so far, the weights, which replace S as bf16 pairs, and their sum.  S is
+// read twice, 16 columns at a time with the next 16 in flight: 64 held at once
+// spill at 96 registers, and spills go through the memory that feeds the MMAs.
+// A slot's vote multiplies its weight (exp(x + ln p) = p exp(x)).  The two
+// halves agree on the maximum in shared memory, only when one of them has to
+// move it, and as bf16: any reference near the maximum will do.  On the
+// group's last tile of an item `last` l becomes the sum of both halves
+// (through a column of S that is read by then).
 template <bool kMask>
-__device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float scale,
-                                             const float *vote, uint64_t lo64, uint64_t hi64,
-                                             bool rescale, float &m, float &l)
+__device__ __forceinline__ void softmax_half(uint32_t tS, uint32_t tO, int half, int pair,
+                                             float scale, const float *vote, uint64_t keep,
+                                             __nv_bfloat16 (&xm)[2][kTile], int r, bool rescale,
+                                             bool last, float &m, float &l)
 {
-    uint32_t ya[32], yb[32];
+    uint32_t y0[16], y1[16];
     float mx[2] = {-INFINITY, -INFINITY};
-    auto top_of = [&](uint32_t (&y)[32], uint32_t keep) {
-        if (kMask) hide32(y, keep);
+    const uint32_t at = tS + 64 * half;
+    auto top_of = [&](uint32_t (&y)[16], uint32_t k) {
+        if (kMask) hide16(y, k);
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
+        for (int j = 0; j < 16; j += 4) {
             mx[0] = fmaxf(fmaxf(mx[0], __uint_as_float(y[j])), __uint_as_float(y[j + 1]));
             mx[1] = fmaxf(fmaxf(mx[1], __uint_as_float(y[j + 2])), __uint_as_float(y[j + 3]));
         }
     };
-    tmem_ld32_async(tS, ya);
-#pragma unroll 1
-    for (int hh = 0; hh < 2; hh++) {
-        const uint64_t keep = hh ? hi64 : lo64;
+    tmem_ld16_async(at, y0);
+#pragma unroll
+    for (int q = 0; q < 2; q++) {
+        const uint32_t k = (uint32_t)(keep >> (32 * q));
         tmem_wait_ld();
-        tmem_bind(ya);
-        tmem_ld32_async(tS + 64 * hh + 32, yb);
-        top_of(ya, (uint32_t)keep);
+        tmem_bind16(y0);
+        tmem_ld16_async(at + 32 * q + 16, y1);
+        top_of(y0, k);
         tmem_wait_ld();
-        tmem_bind(yb);
-        if (hh == 0) tmem_ld32_async(tS + 64, ya);
-        else tmem_ld32_async(tS, ya);                      // the second pass's first
-        top_of(yb, (uint32_t)(keep >> 32));
+        tmem_bind16(y1);
+        tmem_ld16_async(q ? at : at + 32, y0);              // the last: the second pass's first
+        top_of(y1, k >> 16);
     }
-    const float top = fmaxf(mx[0], mx[1]) * scale;
-    const bool move = top > m + kSlack || (m == -INFINITY && top > m);
-    if (__any_sync(kFull, move)) {
+    float top = fmaxf(mx[0], mx[1]) * scale;
+    if (pair_any(pair, top > m + kSlack || (m == -INFINITY && top > m))) {
         tmem_wait_ld();
-        tmem_bind(ya);
+        tmem_bind16(y0);
+        xm[half][r] = __float2bfloat16_rn(top);
+        pair_sync(pair);
+        top = fmaxf(__bfloat162float(xm[0][r]), __bfloat162float(xm[1][r]));
+        const bool move = top > m + kSlack || (m == -INFINITY && top > m);
         float f = 1.f;
         if (move) {
             f = m == -INFINITY ? 0.f : ex2_approx(m - top);
             m = top;
             l *= f;
         }
-        if (rescale) {
+        if (rescale && __any_sync(kFull, move)) {
 #pragma unroll 1
             for (int h = 0; h < 4; h++) {
-                uint32_t y[32];
-                tmem_ld32_async(tO + 32 * h, y);
+                uint32_t y[16];
+                const uint32_t o = tO + 64 * half + 16 * h;
+                tmem_ld16_async(o, y);
                 tmem_wait_ld();
-                tmem_bind(y);
+                tmem_bind16(y);
 #pragma unroll
-                for (int j = 0; j < 32; j++) y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
-                tmem_st32(tO + 32 * h, y);
+                for (int j = 0; j < 16; j++) y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
+                tmem_st16(o, y);
             }
         }
     }
     const float nref = m == -INFINITY ? 0.f : -m;
     const float2 c2 = make_float2(scale, scale), r2 = make_float2(nref, nref);
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-    auto weights = [&](uint32_t (&y)[32], int h, uint32_t keep) {
-        if (kMask) hide32(y, keep);
-        uint32_t p[16];
+    auto weights = [&](uint32_t (&y)[16], int h, uint32_t k) {
+        if (kMask) hide16(y, k);
+        uint32_t p[8];
 #pragma unroll
-        for (int j = 0; j < 16; j += 2) {
+        for (int j = 0; j < 8; j += 2) {
             float2 e[2];
 #pragma unroll
             for (int i = 0; i < 2; i++) {
@@ -357,7 +434,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float sca
                 e[i] = make_float2(ex2_approx(t.x), ex2_approx(t.y));
             }
             if (vote) {
-                const float4 v = *reinterpret_cast<const float4 *>(vote + 32 * h + 2 * j);
+                const float4 v = *reinterpret_cast<const float4 *>(vote + 64 * half + 16 * h + 2 * j);
                 e[0].x *= v.x;
                 e[0].y *= v.y;
                 e[1].x *= v.z;
@@ -369,22 +446,29 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float sca
                 p[j + i] = pack_bf16(e[i].x, e[i].y);
             }
         }
-        tmem_st16(tS + 16 * h, p);                          // over columns already read
+        tmem_st8(at + 8 * h, p);                             // over columns already read
     };
-#pragma unroll 1
-    for (int hh = 0; hh < 2; hh++) {
-        const uint64_t keep = hh ? hi64 : lo64;
+#pragma unroll
+    for (int q = 0; q < 2; q++) {
+        const uint32_t k = (uint32_t)(keep >> (32 * q));
         tmem_wait_ld();
-        tmem_bind(ya);
-        tmem_ld32_async(tS + 64 * hh + 32, yb);
-        weights(ya, 2 * hh, (uint32_t)keep);
+        tmem_bind16(y0);
+        tmem_ld16_async(at + 32 * q + 16, y1);
+        weights(y0, 2 * q, k);
         tmem_wait_ld();
-        tmem_bind(yb);
-        if (hh == 0) tmem_ld32_async(tS + 64, ya);
-        weights(yb, 2 * hh + 1, (uint32_t)(keep >> 32));
+        tmem_bind16(y1);
+        if (q == 0) tmem_ld16_async(at + 32, y0);
+        weights(y1, 2 * q + 1, k >> 16);
     }
     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+    if (last) tmem_st1(at + 32, l);
     tmem_wait_st();
+    if (last) {
+        tc_fence_before();
+        pair_sync(pair);
+        tc_fence_after();
+        l += tmem_ld1(tS + 64 * (half ^ 1) + 32);
+    }
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -413,7 +497,7 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
             mbar_init(&S.qfull[i], 1);
             mbar_init(&S.qempty[i], 1);
             mbar_init(&S.sfull[i], 1);
-            mbar_init(&S.pready[i], 4);
+            mbar_init(&S.pready[i], 8);
             mbar_init(&S.pvdone[i], 1);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -451,15 +535,24 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
             const int g = parts_of(gridDim.x, total), c = min((int)blockIdx.x, g);
             lo = g ? (int)((long long)total * c / g) : 0;
             hi = g ? (int)((long long)total * min(c + 1, g) / g) : 0;
+            if (tid == 0) S.cut = make_int4(-1, 0, 0, 0);
+            __syncthreads();
             for (int i = i0, b = base; i < i1; i++) {
                 const int u = i / a.RB;
                 const int nt = item_tiles(a, a.len[u], tree_live(a.t, u), i - u * a.RB);
                 if (blockIdx.x == 0) a.first[i] = b;
-                if (lo >= b && lo < b + nt) { S.start_item = i; S.start_base = b; }
+                if (lo >= b && lo < b + nt) {
+                    S.start_item = i;
+                    S.start_base = b;
+                    // the part before has the item's start: this CTA names its parts
+                    if (lo > b && b >= (long long)total * (c - 1) / g)
+                        S.cut = make_int4(i, c - 1, (int)(((long long)(b + nt) * g - 1) / total), 0);
+                }
                 b += nt;
                 if (blockIdx.x == 0 && i == items - 1) a.first[items] = b;
             }
             __syncthreads();
+            if (tid == 0) a.cut[blockIdx.x] = S.cut;
         }
     }
     tc_fence_after();
@@ -467,15 +560,16 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
     Walk walk(a, lo < hi ? S.start_item : items, S.start_base, lo, hi);
     Seg s;
 
+
     if (warp == kProd) {
         // ------------------------------------------------------- producer
-        if (lane == 0) {
-            int k = 0, nseg = 0, qn[2] = {0, 0};
+        if (elect_one()) {
+            int k = 0, slot = 0, nseg = 0, qn[2] = {0, 0};
+            uint32_t ph = 1;                     // phase of the slot's last release
             bool ok = true;
             const uint64_t pol = l2_policy_evict_first();
             auto load = [&](const CUtensorMap *m, int u, int row, int rows, bool stream) {
-                const int slot = k % kRing;
-                if (k >= kRing) ok = tree_wait(&S.empty[slot], ((k / kRing) - 1) & 1, &S.bad);
+                if (k >= kRing) ok = tree_wait(&S.empty[slot], ph, &S.bad);
                 if (!ok) return;
                 unsigned char *d = ring + slot * kSlot;
                 const int boxes = rows > 64 ? 2 : 1;
@@ -490,6 +584,7 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                                    &S.full[slot]);
                     }
                 k++;
+                if (++slot == kRing) { slot = 0; ph ^= 1; }
             };
             auto load_q = [&](int half, int u, int row, int rows) {
                 if (qn[half] > 0) ok = ok && tree_wait(&S.qempty[half], (qn[half] - 1) & 1, &S.bad);
@@ -537,108 +632,120 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
         __syncwarp();
     } else if (warp == kMma) {
         // ------------------------------------------------------ MMA issuer
-        // the whole warp walks and waits, one lane issues
-        {
+        if (elect_one()) {
             bool ok = true;
             // slot and phase of the ring's next key and value tile; phases of
             // the groups' barriers as bits
             int ks_slot = 0, vs_slot = 1;
-            uint32_t ks_ph = 0, vs_ph = 0, q_ph = 0, p_ph = 0, begun = 0, nseg = 0;
+            uint32_t ks_ph = 0, vs_ph = 0, q_ph = 0, p_ph = 0, nseg = 0;
             const uint64_t q0 = umma_sdesc(smem_u32(qbuf)), k0 = umma_sdesc(smem_u32(ring));
             const uint64_t v0 = v_desc(smem_u32(ring));
             constexpr uint32_t kStep = kSlot >> 4;           // a slot in descriptor units
+            // S of group w from tile t; the key tile is waited for by its first
+            // reader and given back by its last
+            auto issue_s = [&](uint32_t w, uint32_t half, bool small, bool first, bool last_q) {
+                if (first) ok = ok && tree_wait(&S.full[ks_slot], ks_ph, &S.bad);
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t idesc = small ? kIdescS64 : kIdescS, d = tmem + kColS + 128 * w;
+                const uint64_t qd = q0 + half * kStep, kd = k0 + (uint32_t)ks_slot * kStep;
+#pragma unroll
+                for (int ks = 0; ks < 8; ks++)
+                    umma_bf16(d, umma_sdesc_step(qd, ks), umma_sdesc_step(kd, ks), idesc, ks > 0);
+                umma_commit(&S.sfull[w]);
+                if (last_q) umma_commit(&S.qempty[half]);
+            };
+            auto free_k = [&] {
+                if (!ok) return;
+                umma_commit(&S.empty[ks_slot]);
+                ks_slot += 2;
+                if (ks_slot >= kRing) { ks_slot -= kRing; ks_ph ^= 1; }
+            };
+            auto issue_o = [&](uint32_t w, int nv, bool first, bool keep) {
+                if (first) ok = ok && tree_wait(&S.full[vs_slot], vs_ph, &S.bad);
+                ok = ok && tree_wait(&S.pready[w], p_ph >> w & 1, &S.bad);
+                p_ph ^= 1u << w;
+                if (!ok) return;
+                tc_fence_after();
+                const uint64_t vd = v0 + (uint32_t)vs_slot * kStep;
+                const uint32_t d = tmem + 128 * w, p = tmem + kColS + 128 * w;
+                if (nv > kTile - 16) {
+#pragma unroll
+                    for (int ks = 0; ks < 8; ks++)
+                        umma_ts(d, p + 8 * ks + 32 * (ks >> 2), vd + (uint64_t)(ks * (2048 >> 4)),
+                                kIdescO, ks > 0 || keep);
+                } else {
+                    for (int ks = 0; 16 * ks < nv; ks++)
+                        umma_ts(d, p + 8 * ks + 32 * (ks >> 2), vd + (uint64_t)(ks * (2048 >> 4)),
+                                kIdescO, ks > 0 || keep);
+                }
+                umma_commit(&S.pvdone[w]);
+            };
+            auto free_v = [&] {
+                if (!ok) return;
+                umma_commit(&S.empty[vs_slot]);
+                vs_slot += 2;
+                if (vs_slot >= kRing) { vs_slot -= kRing; vs_ph ^= 1; }
+            };
+            auto wait_q = [&](uint32_t half) {
+                ok = ok && tree_wait(&S.qfull[half], q_ph >> half & 1, &S.bad);
+                q_ph ^= 1u << half;
+            };
             while (ok && walk.next(s)) {
-                const bool dual = s.rows > 128;
-                const int nq = s.t1 - s.t0, jobs = dual ? 2 * nq : nq;
+                const int nq = s.t1 - s.t0;
                 const uint32_t qh = nseg++ & 1;
-                uint32_t fresh = 3;                          // groups whose O starts anew
-                auto issue_s = [&](int j) {
-                    const uint32_t w = j & 1, half = dual ? w : qh;
-                    const int t = dual ? j >> 1 : j;
-                    if (j < (dual ? 2 : 1)) {
-                        ok = ok && tree_wait(&S.qfull[half], q_ph >> half & 1, &S.bad);
-                        q_ph ^= 1u << half;
-                    }
-                    if (!dual || w == 0) ok = ok && tree_wait(&S.full[ks_slot], ks_ph, &S.bad);
-                    // the group's earlier weights, which S overlays, are used up
-                    if (begun >> w & 1)
-                        ok = ok && tree_wait(&S.pvdone[w], (p_ph >> w & 1) ^ 1, &S.bad);
-                    ok = __all_sync(kFull, ok);
-                    if (!ok) return;
-                    tc_fence_after();
-                    const uint32_t idesc =
-                        tile_valid(s, s.t0 + t) <= 64 ? kIdescS64 : kIdescS;
-                    const uint64_t qd = q0 + half * kStep, kd = k0 + (uint32_t)ks_slot * kStep;
-                    const uint32_t d = tmem + kColS + 128 * w;
-                    if (elect_one()) {
-#pragma unroll
-                        for (int ks = 0; ks < 8; ks++)
-                            umma_bf16(d, umma_sdesc_step(qd, ks), umma_sdesc_step(kd, ks), idesc, ks > 0);
-                        umma_commit(&S.sfull[w]);
-                        if (j >= jobs - (dual ? 2 : 1)) umma_commit(&S.qempty[half]);
-                        if (!dual || w == 1) umma_commit(&S.empty[ks_slot]);
-                    }
-                    __syncwarp();
-                    if (!dual || w == 1) {
-                        ks_slot += 2;
-                        if (ks_slot >= kRing) { ks_slot -= kRing; ks_ph ^= 1; }
-                    }
-                };
-                auto issue_o = [&](int j) {
-                    const uint32_t w = j & 1;
-                    const int t = dual ? j >> 1 : j;
-                    ok = ok && tree_wait(&S.pready[w], p_ph >> w & 1, &S.bad);
-                    if (!dual || w == 0) ok = ok && tree_wait(&S.full[vs_slot], vs_ph, &S.bad);
-                    ok = __all_sync(kFull, ok);
-                    if (!ok) return;
-                    tc_fence_after();
-                    const int steps = (tile_valid(s, s.t0 + t) + 15) >> 4;
-                    const uint64_t vd = v0 + (uint32_t)vs_slot * kStep;
-                    const uint32_t d = tmem + 128 * w, p = tmem + kColS + 128 * w;
-                    const bool keep = !(fresh >> w & 1);
-                    if (elect_one()) {
-                        if (steps == 8) {
-#pragma unroll
-                            for (int ks = 0; ks < 8; ks++)
-                                umma_ts(d, p + 8 * ks, vd + (uint64_t)(ks * (2048 >> 4)), kIdescO,
-                                        ks > 0 || keep);
-                        } else {
-                            for (int ks = 0; ks < steps; ks++)
-                                umma_ts(d, p + 8 * ks, vd + (uint64_t)(ks * (2048 >> 4)), kIdescO,
-                                        ks > 0 || keep);
+                if (s.rows > 128) {
+                    wait_q(0);
+                    wait_q(1);
+                    bool small = tile_valid(s, s.t0) <= 64;
+                    issue_s(0, 0, small, true, nq == 1);
+                    issue_s(1, 1, small, false, nq == 1);
+                    free_k();
+                    for (int t = 0; ok && t < nq; t++) {
+                        const int nv = tile_valid(s, s.t0 + t);
+                        const bool more = t + 1 < nq, end = t + 2 == nq;
+                        small = more && tile_valid(s, s.t0 + t + 1) <= 64;
+                        issue_o(0, nv, true, t > 0);
+                        if (more) issue_s(0, 0, small, true, end);
+                        issue_o(1, nv, false, t > 0);
+                        free_v();
+                        if (more) {
+                            issue_s(1, 1, small, false, end);
+                            free_k();
                         }
-                        umma_commit(&S.pvdone[w]);
-                        if (!dual || w == 1) umma_commit(&S.empty[vs_slot]);
                     }
-                    __syncwarp();
-                    fresh &= ~(1u << w);
-                    begun |= 1u << w;
-                    p_ph ^= 1u << w;
-                    if (!dual || w == 1) {
-                        vs_slot += 2;
-                        if (vs_slot >= kRing) { vs_slot -= kRing; vs_ph ^= 1; }
+                } else {
+                    wait_q(qh);
+                    issue_s(0, qh, tile_valid(s, s.t0) <= 64, true, nq == 1);
+                    free_k();
+                    if (nq > 1) {
+                        issue_s(1, qh, tile_valid(s, s.t0 + 1) <= 64, true, nq == 2);
+                        free_k();
                     }
-                };
-                issue_s(0);
-                if (ok && jobs > 1) issue_s(1);
-                for (int j = 0; ok && j < jobs; j++) {
-                    issue_o(j);
-                    if (ok && j + 2 < jobs) issue_s(j + 2);
+                    for (int t = 0; ok && t < nq; t++) {
+                        const uint32_t w = t & 1;
+                        issue_o(w, tile_valid(s, s.t0 + t), true, t > 1);
+                        free_v();
+                        if (t + 2 < nq) {
+                            issue_s(w, qh, tile_valid(s, s.t0 + t + 2) <= 64, true, t + 3 == nq);
+                            free_k();
+                        }
+                    }
                 }
             }
             if (!ok) {
                 // the MMAs in flight are done before tensor memory goes back
                 S.bad = 1;
-                if (lane == 0) {
-                    umma_commit(&S.drain);
-                    mbar_wait(&S.drain, 0);
-                }
+                umma_commit(&S.drain);
+                mbar_wait(&S.drain, 0);
             }
         }
         __syncwarp();
-    } else {
+    } else if (warp < kProd) {
         // --------------------------------------------------------- softmax
-        const int w = warp >> 2, wl = warp & 3, r = wl * 32 + lane;   // row of the group's 128
+        const int w = warp >> 3, half = warp >> 2 & 1, wl = warp & 3;
+        const int r = wl * 32 + lane;                    // row of the group's 128
+        const int pair = 4 + 4 * w + wl;
         const uint32_t lanes = (uint32_t)(wl * 32) << 16;
         const uint32_t tS = tmem + lanes + kColS + 128 * w, tO = tmem + lanes + 128 * w;
         bool ok = true;
@@ -658,7 +765,7 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                 see = a.t.mask[(size_t)(s.u / a.t.units) * a.t.T + grow / a.G] &
                       (s.live >= 64 ? ~0ull : (1ull << s.live) - 1);
             int vote_next = 0;                               // loaded a tile ahead
-            if (a.votes) {
+            if (a.votes && half == 0) {
                 const int i = (s.t0 + (dual ? 0 : w)) * kTile + r;
                 if (i < s.n) vote_next = a.votes[(size_t)s.u * a.cap + i];
             }
@@ -669,9 +776,9 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                 const bool votes = a.votes != nullptr && !tree;
                 if (votes) {
                     group_sync(w);                           // the last tile's are read
-                    S.g[w].vote[r] = (float)vote_next;
+                    if (half == 0) S.g[w].vote[r] = (float)vote_next;
                     const int i = (tile + (dual ? 1 : 2)) * kTile + r;
-                    if (i < s.n) vote_next = a.votes[(size_t)s.u * a.cap + i];
+                    if (half == 0 && i < s.n) vote_next = a.votes[(size_t)s.u * a.cap + i];
                     group_sync(w);
                 }
                 // value rows the MMA reads that are no slot: zero
@@ -680,7 +787,7 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                         ok = tree_wait(&S.full[slot], (kv / kRing) & 1, &S.bad) && ok;
                         unsigned char *v = ring + slot * kSlot;
                         const int stop = (nv + 15) & ~15;
-                        if (tree && r < 64) {
+                        if (tree && half == 0 && r < 64) {
                             // thread r has row r: what is not finite is zeroed here and
                             // added to the rows that see it at the end
                             bool bad = false;
@@ -704,7 +811,7 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                                 }
                             const uint32_t bits = __ballot_sync(kFull, bad && r < nv);
                             if (lane == 0) reinterpret_cast<uint32_t *>(&S.odd[ntree & 1])[wl] = bits;
-                        } else if (!tree && r >= nv && r < stop) {
+                        } else if (!tree && half == 0 && r >= nv && r < stop) {
                             for (int c = 0; c < 16; c++)
                                 *reinterpret_cast<uint4 *>(v + (c >> 3) * kHalf + r * 128 +
                                                            ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
@@ -713,25 +820,28 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                         group_sync(w);
                     }
                 }
-                if (tree && dual) bar_sync<1, 256>();        // both groups see the odd tokens
+                if (tree && dual) bar_sync<1, 512>();        // both groups see the odd tokens
                 if (tree) odd = S.odd[ntree & 1];
                 ok = tree_wait(&S.sfull[w], sn & 1, &S.bad) && ok;
                 sn++;
                 tc_fence_after();
                 if (busy) {
-                    uint64_t lo64 = ~0ull, hi64 = ~0ull;     // slots the row may see
-                    if (tree) {
-                        lo64 = see;
-                        hi64 = 0;
-                    } else if (nv < kTile) {
-                        lo64 = nv >= 64 ? ~0ull : (1ull << nv) - 1;
-                        hi64 = nv <= 64 ? 0ull : (1ull << (nv - 64)) - 1;
-                    }
                     const float *vote = votes ? S.g[w].vote : nullptr;
-                    if (tree || nv < kTile)
-                        softmax_tile<true>(tS, tO, a.scale, vote, lo64, hi64, done > 0, m, l);
-                    else
-                        softmax_tile<false>(tS, tO, a.scale, vote, lo64, hi64, done > 0, m, l);
+                    const bool last = t + (dual ? 1 : 2) >= nq;
+                    if (tree || nv < kTile) {
+                        uint64_t keep = 0;                   // slots the row may see
+                        if (tree) {
+                            keep = half ? 0 : see;
+                        } else {
+                            const int k = nv - 64 * half;
+                            keep = k >= 64 ? ~0ull : k <= 0 ? 0ull : (1ull << k) - 1;
+                        }
+                        softmax_half<true>(tS, tO, half, pair, a.scale, vote, keep, S.g[w].top, r,
+                                           done > 0, last, m, l);
+                    } else {
+                        softmax_half<false>(tS, tO, half, pair, a.scale, vote, ~0ull, S.g[w].top, r,
+                                            done > 0, last, m, l);
+                    }
                 }
                 done++;
                 tc_fence_before();
@@ -747,9 +857,9 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
             const bool direct = all && !a.join_all;
             float c0 = 1.f, c1 = 0.f, M = m, Lsum = l;       // weights of the groups' sums
             if (!dual) {
-                S.g[w].ml[r] = make_float2(m, l);
+                if (half == 0) S.g[w].ml[r] = make_float2(m, l);
                 tc_fence_before();
-                bar_sync<1, 256>();
+                bar_sync<1, 512>();
                 tc_fence_after();
                 odd = S.odd[ntree & 1];          // written by the group that had the tokens' tile
                 const float2 p0 = S.g[0].ml[r], p1 = S.g[1].ml[r];
@@ -766,32 +876,32 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
             const bool has_tree = s.t1 == s.nt;
             const uint64_t by_hand = has_tree ? odd & see : 0;
             ntree += has_tree;
-            // a group writes its rows whole, or (alternate tiles) half of the columns
+            // a warp writes 64 columns of its rows, or (alternate tiles) 32
             if (busy) {
-                const int q0 = dual ? 0 : 2 * w, q1 = dual ? 4 : 2 * w + 2;
+                const int q0 = dual ? 2 * half : 2 * w + half, q1 = dual ? q0 + 2 : q0 + 1;
 #pragma unroll 1
-                for (int q = q0; q < q1; q++) {
-                    uint32_t y[32], z[32];
-                    tmem_ld32_async(tmem + lanes + (dual ? 128 * w : 0) + 32 * q, y);
-                    if (!dual && nq > 1) tmem_ld32_async(tmem + lanes + 128 + 32 * q, z);
+                for (int q = 2 * q0; q < 2 * q1; q++) {      // 16 columns at a time
+                    uint32_t y[16], z[16];
+                    tmem_ld16_async(tmem + lanes + (dual ? 128 * w : 0) + 16 * q, y);
+                    if (!dual && nq > 1) tmem_ld16_async(tmem + lanes + 128 + 16 * q, z);
                     tmem_wait_ld();
-                    tmem_bind(y);
-                    float f[32];
+                    tmem_bind16(y);
+                    float f[16];
 #pragma unroll
-                    for (int j = 0; j < 32; j++) f[j] = __uint_as_float(y[j]) * k_0;
+                    for (int j = 0; j < 16; j++) f[j] = __uint_as_float(y[j]) * k_0;
                     if (!dual && nq > 1) {
-                        tmem_bind(z);
+                        tmem_bind16(z);
 #pragma unroll
-                        for (int j = 0; j < 32; j++) f[j] = fmaf(__uint_as_float(z[j]), k_1, f[j]);
+                        for (int j = 0; j < 16; j++) f[j] = fmaf(__uint_as_float(z[j]), k_1, f[j]);
                     }
                     if (by_hand) {
                         // a visible value that is not finite: whatever its weight, the
                         // output is what weight x value gives, not finite
                         for (uint64_t rest = by_hand; rest; rest &= rest - 1) {
                             const int jt = __ffsll((long long)rest) - 1;
-                            const uint16_t *vr = a.vt + ((size_t)s.u * a.t.T + jt) * kD + 32 * q;
+                            const uint16_t *vr = a.vt + ((size_t)s.u * a.t.T + jt) * kD + 16 * q;
 #pragma unroll
-                            for (int j = 0; j < 32; j++) {
+                            for (int j = 0; j < 16; j++) {
                                 const float v = bf2f(vr[j]);
                                 f[j] += isfinite(v) ? 0.f : v;
                             }
@@ -799,23 +909,20 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                     }
                     if (mine && ok) {
                         if (direct) {
-                            uint4 *d = reinterpret_cast<uint4 *>(a.o + orow * kD + 32 * q);
+                            uint32_t h[8];
 #pragma unroll
-                            for (int j = 0; j < 4; j++)
-                                d[j] = make_uint4(pack_bf16(f[8 * j], f[8 * j + 1]),
-                                                  pack_bf16(f[8 * j + 2], f[8 * j + 3]),
-                                                  pack_bf16(f[8 * j + 4], f[8 * j + 5]),
-                                                  pack_bf16(f[8 * j + 6], f[8 * j + 7]));
+                            for (int j = 0; j < 8; j++) h[j] = pack_bf16(f[2 * j], f[2 * j + 1]);
+                            uint4 *d = reinterpret_cast<uint4 *>(a.o + orow * kD + 16 * q);
+                            d[0] = make_uint4(h[0], h[1], h[2], h[3]);
+                            d[1] = make_uint4(h[4], h[5], h[6], h[7]);
                         } else {
-                            float4 *d = reinterpret_cast<float4 *>(
-                                a.part + (sid * a.rows + row) * kD + 32 * q);
-#pragma unroll
-                            for (int j = 0; j < 8; j++)
-                                d[j] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+                            float *d = a.part + (sid * a.rows + row) * kD + 16 * q;
+                            st_v8(d, reinterpret_cast<const uint32_t *>(f));
+                            st_v8(d + 8, reinterpret_cast<const uint32_t *>(f + 8));
                         }
                     }
                 }
-                if (mine && ok && (dual || w == 0)) {
+                if (mine && ok && half == 0 && (dual || w == 0)) {
                     if (direct)
                         a.lse[orow] = Lsum == 0.f ? -INFINITY
                                                   : (M + log2f(Lsum)) * 0.6931471805599453f;
@@ -825,7 +932,7 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
             }
             // the other group reads this one's sums: both are done before either goes on
             tc_fence_before();
-            if (!dual) bar_sync<1, 256>();
+            if (!dual) bar_sync<1, 512>();
         }
     }
     __syncthreads();
@@ -837,44 +944,24 @@ struct JoinArgs {
     AttArgs a;
     const uint16_t *q;
     const float *mn, *mu_k, *mu_v, *C;
-    int first_order, chunk, grid;
+    int first_order, grid;
 };
 
-// The parts [c0, c1] of an item, and its rows; false when it has none.
-__device__ __forceinline__ bool join_item(const JoinArgs &j, int item, int &u, int &rb, int &rows,
-                                          int &c0, int &c1)
-{
-    const AttArgs &a = j.a;
-    u = item / a.RB;
-    rb = item - u * a.RB;
-    const int n = a.len[u], live = tree_live(a.t, u);
-    if (n < 0 || n > a.max_len || live < 0) return false;
-    rows = min(kRows, live * a.G - rb * kRows);
-    if (rows <= 0) return false;
-    if (a.whole) {
-        c0 = c1 = (int)((((long long)item + 1) * j.grid - 1) / (a.U * a.RB));
-    } else {
-        // tile x is in part ((x + 1) g - 1) / W
-        const long long b = a.first[item], e = a.first[item + 1], W = a.first[a.U * a.RB];
-        const int g = parts_of(j.grid, (int)W);
-        c0 = (int)(((b + 1) * g - 1) / W);
-        c1 = (int)((e * g - 1) / W);
-    }
-    return true;
-}
-
-// The sums of an item's parts added: one warp per row, a lane has four
+// The sums of a cut item's parts added: one warp per row, a lane has four
 // columns.  The result is the output, or (kKeep, when the moments follow) the
-// first part's place takes it.  grid (items, rows / 8).
+// first part's place takes it.  grid (CTAs of the attention, rows / 8): block
+// x takes the item whose first cut is the start of part x.
 template <bool kKeep>
 __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ JoinArgs j)
 {
     const AttArgs &a = j.a;
+    const int4 cut = a.cut[blockIdx.x];
+    if (cut.x < 0) return;
     const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
-    int u, rb, rows, c0, c1;
-    if (!join_item(j, blockIdx.x, u, rb, rows, c0, c1) || r >= rows || c0 == c1) return;
-    const size_t at = ((size_t)blockIdx.x + c0) * a.rows + r, step = (size_t)a.rows;
-    const int np = c1 - c0 + 1;
+    const int u = cut.x / a.RB, rb = cut.x - u * a.RB;
+    if (r >= min(kRows, tree_live(a.t, u) * a.G - rb * kRows)) return;
+    const size_t at = ((size_t)cut.x + cut.y) * a.rows + r, step = (size_t)a.rows;
+    const int np = cut.z - cut.y + 1;
     float M = -INFINITY;
     for (int k = lane; k < np; k += 32) M = fmaxf(M, a.ml[at + k * step].x);
     M = warp_max(M);
@@ -902,6 +989,7 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
     }
     L = warp_sum(L);
     if (kKeep) {
+        __syncwarp();
         reinterpret_cast<float4 *>(a.part + at * kD)[lane] = f;
         if (lane == 0) a.ml[at] = make_float2(M, L);
         return;
@@ -915,144 +1003,139 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
 
 // The normalization correction: every row's sum normalised and mixed with the
 // evicted set's estimate.  C q runs on tensor cores (mma.sync) with C as two
-// bf16 terms (2^-16 of a product) in shared memory, 128-byte swizzled; a warp
-// has 16 rows, a CTA `chunk` rows of an item.
-constexpr int kMomWarps = 4;
+// bf16 terms (2^-16 of a product) in shared memory, 128-byte swizzled.  A CTA
+// has 64 rows of an item, a warp 16 rows and half of the columns; grid
+// (items, rows / 64).
+constexpr int kMomRows = 64;
 constexpr size_t kMomDyn = 2 * (size_t)kSlot;
 
-__global__ void __launch_bounds__(kMomWarps * 32) tree_moment_kernel(const __grid_constant__ JoinArgs j)
+__global__ void __launch_bounds__(256, 2) tree_moment_kernel(const __grid_constant__ JoinArgs j)
 {
     const AttArgs &a = j.a;
     extern __shared__ __align__(1024) unsigned char cs[];   // C: high terms, low terms
     __shared__ float muk[kD], muv[kD];
-    int u, rb, rows, c0, c1;
-    if (!join_item(j, blockIdx.x, u, rb, rows, c0, c1)) return;
-    const int r_end = min(rows, (int)(blockIdx.y + 1) * j.chunk);
-    if ((int)blockIdx.y * j.chunk >= r_end) return;
+    const int item = blockIdx.x, u = item / a.RB, rb = item - u * a.RB;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int g = lane >> 2, t = lane & 3;
+    const int g = lane >> 2, t = lane & 3, n0 = 64 * (warp & 1);
+    const int n = a.len[u], live = tree_live(a.t, u);
     const float ne = j.mn[u];
     const bool mix = ne > 0.f;
-    if (mix) {
+    const int rows = min(kRows, live * a.G - rb * kRows), r0 = blockIdx.y * kMomRows + 16 * (warp >> 1);
+    // the part that has the item's start (its place has the joined sums)
+    int c0;
+    if (a.whole) {
+        c0 = (int)((((long long)item + 1) * j.grid - 1) / (a.U * a.RB));
+    } else {
+        const int W = a.first[a.U * a.RB];
+        c0 = W ? (int)(((a.first[item] + 1ll) * parts_of(j.grid, W) - 1) / W) : 0;
+    }
+    if (n < 0 || n > a.max_len || live < 0 || (int)blockIdx.y * kMomRows >= rows) return;
+    if (mix && j.first_order) {
+        const float4 *C = reinterpret_cast<const float4 *>(j.C + (size_t)u * kD * kD);
+        // 8 elements of a row of C a step, 16 bytes each of high and low terms
+#pragma unroll 4
+        for (int i = 0; i < kD * 16 / 256; i++) {
+            const int e = i * 256 + tid, row = e >> 4, ch = e & 15;
+            const float4 x = C[2 * e], y = C[2 * e + 1];
+            const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                hi[k] = pack_bf16(v[2 * k], v[2 * k + 1]);
+                lo[k] = pack_bf16(v[2 * k] - bf_lo(hi[k]), v[2 * k + 1] - bf_hi(hi[k]));
+            }
+            unsigned char *d = cs + sw_off_t<128>(row, ch);
+            *reinterpret_cast<uint4 *>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4 *>(d + kSlot) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+    }
+    if (mix && tid < kD) {
         muk[tid] = j.mu_k[(size_t)u * kD + tid];
         muv[tid] = j.mu_v[(size_t)u * kD + tid];
-        if (j.first_order) {
-            const float4 *C = reinterpret_cast<const float4 *>(j.C + (size_t)u * kD * kD);
-            // 16 bytes of bf16 per step: 8 elements of a row
-#pragma unroll 4
-            for (int i = 0; i < kD * 16 / (kMomWarps * 32); i++) {
-                const int e = i * kMomWarps * 32 + tid, row = e >> 4, ch = e & 15;
-                const float4 x = C[2 * e], y = C[2 * e + 1];
-                const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-                uint32_t hi[4], lo[4];
+    }
+    const size_t ubase = (size_t)u * a.TG + (size_t)rb * kRows;
+    const size_t pbase = ((size_t)item + c0) * a.rows;
+    const int ra[2] = {min(r0 + g, rows - 1), min(r0 + g + 8, rows - 1)};
+    const float2 ml[2] = {a.ml[pbase + ra[0]], a.ml[pbase + ra[1]]};
+    const float sd = rsqrtf((float)kD);
+    uint32_t qa[8][4];
+    if (mix) {
 #pragma unroll
-                for (int k = 0; k < 4; k++) {
-                    uint16_t h0, l0, h1, l1;
-                    split_bf16(v[2 * k], h0, l0);
-                    split_bf16(v[2 * k + 1], h1, l1);
-                    hi[k] = h0 | (uint32_t)h1 << 16;
-                    lo[k] = l0 | (uint32_t)l1 << 16;
-                }
-                unsigned char *d = cs + sw_off_t<128>(row, ch);
-                *reinterpret_cast<uint4 *>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4 *>(d + kSlot) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        for (int h = 0; h < 2; h++) {
+            const uint32_t *p = reinterpret_cast<const uint32_t *>(j.q + (ubase + ra[h]) * kD) + t;
+#pragma unroll
+            for (int ks = 0; ks < 8; ks++) {
+                qa[ks][h] = p[8 * ks];
+                qa[ks][2 + h] = p[8 * ks + 4];
             }
         }
     }
     __syncthreads();
-    const size_t ubase = (size_t)u * a.TG + (size_t)rb * kRows;
-    const size_t pbase = ((size_t)blockIdx.x + c0) * a.rows;
-    const float sd = rsqrtf((float)kD);
-    for (int r0 = blockIdx.y * j.chunk + 16 * warp; r0 < r_end; r0 += 16 * kMomWarps) {
-        const int ra = min(r0 + g, rows - 1), rb8 = min(r0 + g + 8, rows - 1);
-        const float2 ml[2] = {a.ml[pbase + ra], a.ml[pbase + rb8]};
-        uint32_t qa[8][4];
-        float z[2] = {0.f, 0.f};
-        float d[16][4];
+    float z[2] = {0.f, 0.f};
+    float d[8][4];
 #pragma unroll
-        for (int i = 0; i < 16; i++) d[i][0] = d[i][1] = d[i][2] = d[i][3] = 0.f;
+    for (int i = 0; i < 8; i++) d[i][0] = d[i][1] = d[i][2] = d[i][3] = 0.f;
+    if (mix) {
+#pragma unroll
+        for (int ks = 0; ks < 8; ks++)
+#pragma unroll
+            for (int h = 0; h < 4; h++) {
+                const int k = 16 * ks + 8 * (h >> 1) + 2 * t;
+                z[h & 1] += bf_lo(qa[ks][h]) * muk[k] + bf_hi(qa[ks][h]) * muk[k + 1];
+            }
+        if (j.first_order) {
+            // ldmatrix: a quarter-warp has the addresses of rows n0 + 8 i .. + 7 of C
+            // in one 8-column chunk; four chunks are two k-steps
+            const uint32_t base = smem_u32(cs);
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+#pragma unroll
+                for (int k4 = 0; k4 < 4; k4++) {
+                    const uint32_t off = sw_off_t<128>(n0 + 8 * i + (lane & 7), 4 * k4 + (lane >> 3));
+                    uint32_t b[4], c[4];
+                    ldsm_x4(base + kSlot + off, b[0], b[1], b[2], b[3]);
+                    ldsm_x4(base + off, c[0], c[1], c[2], c[3]);
+                    const uint32_t(&q0)[4] = qa[2 * k4], (&q1)[4] = qa[2 * k4 + 1];
+                    mma16816(d[i], q0[0], q0[1], q0[2], q0[3], b[0], b[1]);
+                    mma16816(d[i], q1[0], q1[1], q1[2], q1[3], b[2], b[3]);
+                    mma16816(d[i], q0[0], q0[1], q0[2], q0[3], c[0], c[1]);
+                    mma16816(d[i], q1[0], q1[1], q1[2], q1[3], c[2], c[3]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        const float lse = ml[h].y == 0.f ? -INFINITY : (ml[h].x + log2f(ml[h].y)) * 0.6931471805599453f;
+        float w = 1.f;
         if (mix) {
-            const uint32_t *pa = reinterpret_cast<const uint32_t *>(j.q + (ubase + ra) * kD) + t;
-            const uint32_t *pb = reinterpret_cast<const uint32_t *>(j.q + (ubase + rb8) * kD) + t;
-#pragma unroll
-            for (int ks = 0; ks < 8; ks++) {
-                qa[ks][0] = pa[8 * ks];
-                qa[ks][1] = pb[8 * ks];
-                qa[ks][2] = pa[8 * ks + 4];
-                qa[ks][3] = pb[8 * ks + 4];
-            }
-#pragma unroll
-            for (int ks = 0; ks < 8; ks++)
-#pragma unroll
-                for (int h = 0; h < 4; h++) {
-                    const int k = 16 * ks + 8 * (h >> 1) + 2 * t;
-                    z[h & 1] += bf_lo(qa[ks][h]) * muk[k] + bf_hi(qa[ks][h]) * muk[k + 1];
-                }
-            if (j.first_order) {
-                // a quarter-warp's address of ldmatrix: columns (rows of C) i .. i + 7,
-                // k-chunks of two steps
-                const uint32_t base = smem_u32(cs);
-#pragma unroll
-                for (int i = 0; i < 16; i++) {
-#pragma unroll
-                    for (int k4 = 0; k4 < 4; k4++) {
-                        const uint32_t off = sw_off_t<128>(8 * i + (lane & 7), 4 * k4 + (lane >> 3));
-                        uint32_t b[4];
-                        ldsm_x4(base + kSlot + off, b[0], b[1], b[2], b[3]);
-                        mma16816(d[i], qa[2 * k4][0], qa[2 * k4][1], qa[2 * k4][2], qa[2 * k4][3], b[0], b[1]);
-                        mma16816(d[i], qa[2 * k4 + 1][0], qa[2 * k4 + 1][1], qa[2 * k4 + 1][2],
-                                 qa[2 * k4 + 1][3], b[2], b[3]);
-                        ldsm_x4(base + off, b[0], b[1], b[2], b[3]);
-                        mma16816(d[i], qa[2 * k4][0], qa[2 * k4][1], qa[2 * k4][2], qa[2 * k4][3], b[0], b[1]);
-                        mma16816(d[i], qa[2 * k4 + 1][0], qa[2 * k4 + 1][1], qa[2 * k4 + 1][2],
-                                 qa[2 * k4 + 1][3], b[2], b[3]);
-                    }
-                }
-            }
+            float x = z[h];
+            x += __shfl_xor_sync(kFull, x, 1);
+            x += __shfl_xor_sync(kFull, x, 2);
+            w = 1.f / (1.f + expf(logf(ne) + sd * x - lse));
         }
-        float wf[2], we[2], lse[2];
+        const float wf = ml[h].y == 0.f ? 0.f : w / ml[h].y, we = 1.f - w;
+        const float *p = a.part + (pbase + ra[h]) * kD + n0 + 2 * t;
+        uint32_t *o = reinterpret_cast<uint32_t *>(a.o + (ubase + ra[h]) * kD + n0 + 2 * t);
+        const bool mine = r0 + g + 8 * h < rows;
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-            lse[h] = ml[h].y == 0.f ? -INFINITY : (ml[h].x + log2f(ml[h].y)) * 0.6931471805599453f;
-            float w = 1.f;
+        for (int i = 0; i < 8; i++) {
+            const float2 x = *reinterpret_cast<const float2 *>(p + 8 * i);
+            float f0 = wf * x.x, f1 = wf * x.y;
             if (mix) {
-                float x = z[h];
-                x += __shfl_xor_sync(kFull, x, 1);
-                x += __shfl_xor_sync(kFull, x, 2);
-                w = 1.f / (1.f + expf(logf(ne) + sd * x - lse[h]));
+                f0 += we * (muv[n0 + 8 * i + 2 * t] + sd * d[i][2 * h]);
+                f1 += we * (muv[n0 + 8 * i + 2 * t + 1] + sd * d[i][2 * h + 1]);
             }
-            wf[h] = ml[h].y == 0.f ? 0.f : w / ml[h].y;
-            we[h] = 1.f - w;
+            if (mine) o[4 * i] = pack_bf16(f0, f1);
         }
-        const float *p0 = a.part + (pbase + ra) * kD + 2 * t, *p1 = a.part + (pbase + rb8) * kD + 2 * t;
-        uint32_t *o0 = reinterpret_cast<uint32_t *>(a.o + (ubase + ra) * kD + 2 * t);
-        uint32_t *o1 = reinterpret_cast<uint32_t *>(a.o + (ubase + rb8) * kD + 2 * t);
-#pragma unroll
-        for (int i = 0; i < 16; i++) {
-            const float2 x = *reinterpret_cast<const float2 *>(p0 + 8 * i);
-            const float2 y = *reinterpret_cast<const float2 *>(p1 + 8 * i);
-            float m0 = 0.f, m1 = 0.f;
-            if (mix) {
-                m0 = muv[8 * i + 2 * t];
-                m1 = muv[8 * i + 2 * t + 1];
-            }
-            const uint32_t a0 = pack_bf16(wf[0] * x.x + (mix ? we[0] * (m0 + sd * d[i][0]) : 0.f),
-                                          wf[0] * x.y + (mix ? we[0] * (m1 + sd * d[i][1]) : 0.f));
-            const uint32_t a1 = pack_bf16(wf[1] * y.x + (mix ? we[1] * (m0 + sd * d[i][2]) : 0.f),
-                                          wf[1] * y.y + (mix ? we[1] * (m1 + sd * d[i][3]) : 0.f));
-            if (r0 + g < r_end) o0[4 * i] = a0;
-            if (r0 + g + 8 < r_end) o1[4 * i] = a1;
-        }
-        if (t == 0) {
-            if (r0 + g < r_end) a.lse[ubase + ra] = lse[0];
-            if (r0 + g + 8 < r_end) a.lse[ubase + rb8] = lse[1];
-        }
+        if (mine && t == 0 && n0 == 0) a.lse[ubase + ra[h]] = lse;
     }
 }
 
 struct TreeWs {
     int32_t *status;
     int *first;
+    int4 *cut;
     float2 *ml;
     float *part;
     size_t bytes;
@@ -1072,6 +1155,7 @@ TreeWs tree_ws(const kvc_params &p, int T, void *base)
     const size_t rows = TG < (size_t)kRows ? TG : (size_t)kRows;
     w.status = reinterpret_cast<int32_t *>(take(sizeof(WsHeader)));
     w.first = reinterpret_cast<int *>(take((items + 1) * sizeof(int)));
+    w.cut = reinterpret_cast<int4 *>(take(kGrid * sizeof(int4)));
     w.ml = reinterpret_cast<float2 *>(take((items + kGrid) * rows * sizeof(float2)));
     w.part = reinterpret_cast<float *>(take((items + kGrid) * rows * kD * sizeof(float)));
     w.bytes = off;
@@ -1100,7 +1184,7 @@ cudaError_t launch_tree_attend(const kvc_params &p, int max_len, const TreeArgs 
     long long grid = whole ? items : (items * tmax + 3) / 4;
     if (grid < items) grid = items;
     if (grid > kGrid) grid = kGrid;
-    AttArgs a{t, c.votes, c.len, vt, o, lse, w.part, w.ml, w.first, w.status, p.U, RB, TG, p.G, p.cap,
+    AttArgs a{t, c.votes, c.len, vt, o, lse, w.part, w.ml, w.first, w.cut, w.status, p.U, RB, TG, p.G, p.cap,
               max_len, TG < kRows ? TG : kRows, whole, m != nullptr, kLog2e / sqrtf((float)kD)};
     cudaError_t e = cudaFuncSetAttribute(tree_attend_kernel,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDyn);
@@ -1108,12 +1192,10 @@ cudaError_t launch_tree_attend(const kvc_params &p, int max_len, const TreeArgs 
     tree_attend_kernel<<<(int)grid, kThreads, kDyn, st>>>(a, mk, mv, mq, mkt, mvt);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (m == nullptr && whole) return cudaSuccess;
-    // enough CTAs to fill the SMs, else as many rows per copy of C as there are
-    const int chunk = items >= 2 * kGrid ? kRows : 64;
     JoinArgs j{a, q, m ? m->n : nullptr, m ? m->mu_k : nullptr, m ? m->mu_v : nullptr,
-               m ? m->C : nullptr, p.correction == KVC_CORR_FIRST_ORDER, chunk, (int)grid};
+               m ? m->C : nullptr, p.correction == KVC_CORR_FIRST_ORDER, (int)grid};
     if (!whole) {
-        const dim3 g((unsigned)items, (a.rows + 7) / 8);
+        const dim3 g((unsigned)grid, (a.rows + 7) / 8);
         if (m) tree_join_kernel<true><<<g, 256, 0, st>>>(j);
         else tree_join_kernel<false><<<g, 256, 0, st>>>(j);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
@@ -1122,8 +1204,8 @@ cudaError_t launch_tree_attend(const kvc_params &p, int max_len, const TreeArgs 
         e = cudaFuncSetAttribute(tree_moment_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)kMomDyn);
         if (e != cudaSuccess) return e;
-        const dim3 g((unsigned)items, (a.rows + chunk - 1) / chunk);
-        tree_moment_kernel<<<g, kMomWarps * 32, kMomDyn, st>>>(j);
+        const dim3 g((unsigned)items, (a.rows + kMomRows - 1) / kMomRows);
+        tree_moment_kernel<<<g, 256, kMomDyn, st>>>(j);
     }
     return cudaGetLastError();
 }
