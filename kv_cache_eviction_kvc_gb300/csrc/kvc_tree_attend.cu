@@ -17,15 +17,17 @@
 // with the evicted set's estimate.  The drafted tokens are the item's last
 // tile.
 //
-// 576 threads:
-//   warps 0-7, 8-15 two softmax groups, each with its own S, P and O in tensor
+// 352 threads:
+//   warps 0-3, 4-7  two softmax groups, each with its own S, P and O in tensor
 //                   memory.  Items of more than 128 rows give each group 128
 //                   of them; otherwise the groups take alternate tiles of the
-//                   same rows and add their sums at the end.  Two warps share
-//                   32 rows: each has 64 of a tile's 128 slots, which halves
-//                   the time from S to P that every tile waits for
-//   warp 16         producer (TMA into a ring of 32 KB key and value tiles)
-//   warp 17         tensor-memory owner and MMA issuer
+//                   same rows and add their sums at the end
+//   warp 8          producer (TMA into a ring of 32 KB key and value tiles)
+//   warp 9          tensor-memory owner and MMA issuer
+//   warp 10         walks the CTA's items ahead of the others and tells them
+//                   through a ring in shared memory
+// (168 registers a thread: spills would go through the few KB of L1 that the
+// tiles leave, to L2.)
 // Tensor memory: O of group w at column 128 w, S at 256 + 128 w; P (bf16)
 // overlays S, 32 columns at the start of each half.  The MMAs of one thread execute in the order
 // of their issue, so the S that overwrites a P follows the product that reads
@@ -50,8 +52,9 @@ constexpr int kRows = 256;                       // query rows per item
 constexpr int kSlot = kTile * kD * 2;            // 32 KB: a tile of keys or values
 constexpr int kHalf = kSlot / 2;                 // its 64-column half
 constexpr int kRing = 5;
-constexpr int kThreads = 576;
-constexpr int kProd = 16, kMma = 17;
+constexpr int kThreads = 352;
+constexpr int kProd = 8, kMma = 9, kWalk = 10;
+constexpr int kSegs = 4;                         // items told ahead
 constexpr int kGrid = 152;                       // CTAs: one per SM
 constexpr uint32_t kColS = 256;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -62,6 +65,21 @@ constexpr float kSlack = 8.f;
 constexpr uint32_t kIdescS = umma_idesc_bf16(128, 128);
 constexpr uint32_t kIdescS64 = umma_idesc_bf16(128, 64);
 constexpr uint32_t kIdescO = umma_idesc_bf16(128, 128) | (1u << 16);   // B (values) MN-major
+
+// x / d for 0 <= x < 2^31 as a multiplication (Granlund and Montgomery, 1994)
+struct FastDiv {
+    uint32_t mul, shift;
+    explicit FastDiv(uint32_t d = 1)
+    {
+        shift = 0;
+        while ((1u << shift) < d) shift++;               // d <= 2^31
+        mul = (uint32_t)(((1ull << 32) * ((1ull << shift) - d)) / d + 1);
+    }
+    __device__ __forceinline__ int operator()(int x) const
+    {
+        return (int)((__umulhi((uint32_t)x, mul) + (uint32_t)x) >> shift);
+    }
+};
 
 struct AttArgs {
     TreeArgs t;
@@ -74,25 +92,40 @@ struct AttArgs {
     int *first;             // [items + 1] tiles before each item
     int4 *cut;              // [CTAs] the item a part begins inside of: item, first and last part
     int32_t *status;
-    int U, RB, TG, G, cap, max_len, rows, whole, join_all;
+    int U, RB, TG, gshift, cap, max_len, rows, whole, join_all;
+    FastDiv by_rb, by_units;
     float scale;            // log2(e) / sqrt(d)
+
+    __device__ __forceinline__ int live(int u) const
+    {
+        const int n = t.n ? t.n[by_units(u)] : t.T;
+        return n < 0 || n > t.T ? -1 : n;
+    }
+};
+
+// The part of one item that this CTA takes; rows = 0: there is none left.
+struct __align__(16) Seg {
+    int item, u, rb, n, live, nt;   // nt: tiles of the item
+    int t0, t1;                     // this CTA's tiles of it
+    int rows;                       // live rows of the item
+    int k0;                         // the CTA's tiles before
+    int trees;                      // drafted tokens' tiles before
 };
 
 struct AttSmem {
     union {                 // read as float4
-        struct {
-            float vote[kTile];               // votes of a tile's slots
-            __nv_bfloat16 top[2][kTile];     // the halves' maxima
-        };
+        float vote[kTile];  // votes of a tile's slots
         float2 ml[kTile];   // at an item's end: the rows' maxima and sums
     } g[2];
+    Seg seg[kSegs];
     int4 cut;
     uint64_t full[kRing], empty[kRing];
-    uint64_t drain;
+    uint64_t segfull[kSegs], segempty[kSegs];
     uint64_t qfull[2], qempty[2], sfull[2], pready[2], pvdone[2];
+    uint64_t gsync[2], xsync, drain;
     uint64_t odd[2];        // drafted tokens with a value that is not finite
-    int scan[40];
-    int start_item, start_base, total;
+    int scan[kThreads / 32];
+    int start_item, start_base;
     int bad;
     uint32_t tmem;
 };
@@ -106,9 +139,8 @@ __device__ __forceinline__ bool elect_one()
     return p != 0;
 }
 
-// Bounded wait.  Once one has run out every wait ends at once: each role then
-// walks its loops to the end (so that the barriers among them stay matched)
-// without issuing copies or MMAs.
+// Bounded wait.  Once one has run out every wait ends at once and each role
+// leaves its loop (all synchronisation among them is by such waits).
 __device__ __forceinline__ bool tree_wait(uint64_t *b, uint32_t parity, volatile int *bad)
 {
     if (mbar_try_wait(b, parity)) return true;
@@ -161,14 +193,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8])
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-        : "memory");
-}
-
 __device__ __forceinline__ void tmem_ld16_async(uint32_t addr, uint32_t (&r)[16])
 {
     asm volatile(
@@ -201,55 +225,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return r;
 }
 
-template <int kBar, int kCount>
-__device__ __forceinline__ void bar_sync()
-{
-    asm volatile("bar.sync %0, %1;" ::"n"(kBar), "n"(kCount) : "memory");
-}
-
-// Barrier of one softmax group (2 + w) over its 256 threads.
-__device__ __forceinline__ void group_sync(int w)
-{
-    if (w == 0) bar_sync<2, 256>();
-    else bar_sync<3, 256>();
-}
-
-// Barrier of the two warps that share rows (ids 4 .. 11); the second form
-// tells both whether either said yes.
-__device__ __forceinline__ void pair_sync(int id)
-{
-    asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
-}
-
-__device__ __forceinline__ bool pair_any(int id, bool x)
-{
-    uint32_t r;
-    asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n bar.red.or.pred q, %1, 64, p;\n"
-        " selp.u32 %0, 1, 0, q;\n}\n"
-        : "=r"(r)
-        : "r"(id), "r"((uint32_t)x)
-        : "memory");
-    return r != 0;
-}
-
-__device__ __forceinline__ void tmem_st1(uint32_t addr, float x)
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(addr),
-                 "r"(__float_as_uint(x))
-                 : "memory");
-}
-
-__device__ __forceinline__ float tmem_ld1(uint32_t addr)
-{
-    uint32_t a;
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\ntcgen05.wait::ld.sync.aligned;"
-                 : "=r"(a)
-                 : "r"(addr)
-                 : "memory");
-    return __uint_as_float(a);
-}
-
 // 32-byte stores: a whole sector per lane.
 __device__ __forceinline__ void st_v8(void *p, const uint32_t *r)
 {
@@ -262,59 +237,31 @@ __device__ __forceinline__ void st_v8(void *p, const uint32_t *r)
 // has no live row or the unit is refused.
 __device__ __forceinline__ int item_tiles(const AttArgs &a, int n, int live, int rb)
 {
-    if (n < 0 || n > a.max_len || live < 0 || live * a.G <= rb * kRows) return 0;
-    return (n + kTile - 1) / kTile + 1;
+    if (n < 0 || n > a.max_len || live < 0 || (live << a.gshift) <= rb * kRows) return 0;
+    return ((n + kTile - 1) >> 7) + 1;
 }
 
-// The line is cut into as many parts as there are CTAs, none of them empty.
-__device__ __forceinline__ int parts_of(int grid, int total) { return min(grid, total); }
+__device__ __forceinline__ void check_unit(const AttArgs &a, int u)
+{
+    const int n = a.len[u], live = a.live(u);
+    if (live < 0) record_status(a.status, KVC_ERR_INVALID_ARG);
+    else if (n < 0 || n > a.max_len) record_status(a.status, KVC_ERR_SHAPE);
+}
 
-// The part of one item that this CTA takes.
-struct Seg {
-    int item, u, rb, n, live, nt;   // nt: tiles of the item
-    int t0, t1;                     // this CTA's tiles of it
-    int rows;                       // live rows of the item
-};
-
-struct Walk {
-    const AttArgs &a;
-    int item, base, lo, hi;
-    int n_next, live_next;
-
-    __device__ Walk(const AttArgs &a_, int item_, int base_, int lo_, int hi_)
-        : a(a_), item(item_), base(base_), lo(lo_), hi(hi_)
+// The line of `total` tiles is cut into min(grid, total) parts, the first
+// total % parts of them one tile longer.
+struct Cuts {
+    int parts, q, rem;
+    __device__ __forceinline__ Cuts(int grid, int total)
+        : parts(min(grid, total)), q(parts ? (uint32_t)total / (uint32_t)parts : 0), rem(total - q * parts)
     {
-        peek(item);
     }
-    __device__ void peek(int i)
+    __device__ __forceinline__ int start(int c) const { return c * q + min(c, rem); }
+    __device__ __forceinline__ int part(int tile) const        // that has the tile
     {
-        if (i < a.U * a.RB) {
-            const int u = i / a.RB;
-            n_next = a.len[u];
-            live_next = tree_live(a.t, u);
-        }
-    }
-    __device__ bool next(Seg &s)
-    {
-        while (base < hi && item < a.U * a.RB) {
-            s.item = item;
-            s.u = item / a.RB;
-            s.rb = item - s.u * a.RB;
-            s.n = n_next;
-            s.live = live_next;
-            s.nt = item_tiles(a, s.n, s.live, s.rb);
-            peek(item + 1);
-            const int b = base;
-            base += s.nt;
-            item++;
-            s.t0 = max(0, lo - b);
-            s.t1 = min(s.nt, hi - b);
-            if (s.t1 > s.t0) {
-                s.rows = min(kRows, s.live * a.G - s.rb * kRows);
-                return true;
-            }
-        }
-        return false;
+        const int longer = rem * (q + 1);
+        return tile < longer ? (uint32_t)tile / (uint32_t)(q + 1)
+                             : rem + (int)((uint32_t)(tile - longer) / (uint32_t)q);
     }
 };
 
@@ -343,88 +290,82 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
     return d;
 }
 
-// Hidden slots of 16 raw products: -inf.
-__device__ __forceinline__ void hide16(uint32_t (&y)[16], uint32_t keep)
+// Hidden slots of 32 raw products: -inf.
+template <bool kMask>
+__device__ __forceinline__ void hide32(uint32_t (&y)[32], uint32_t keep)
 {
+    if (kMask)
 #pragma unroll
-    for (int j = 0; j < 16; j++) y[j] = keep >> j & 1 ? y[j] : 0xff800000u;
+        for (int j = 0; j < 32; j++) y[j] = keep >> j & 1 ? y[j] : 0xff800000u;
 }
 
-// Half a tile of the thread's row (64 of 128 slots; `half`): the row's maximum
-// so far, the weights, which replace S as bf16 pairs, and their sum.  S is
-// read twice, 16 columns at a time with the next 16 in flight: 64 held at once
-// spill at 96 registers, and spills go through the memory that feeds the MMAs.
-// A slot's vote multiplies its weight (exp(x + ln p) = p exp(x)).  The two
-// halves agree on the maximum in shared memory, only when one of them has to
-// move it, and as bf16: any reference near the maximum will do.  On the
-// group's last tile of an item `last` l becomes the sum of both halves
-// (through a column of S that is read by then).
-template <bool kMask>
-__device__ __forceinline__ void softmax_half(uint32_t tS, uint32_t tO, int half, int pair,
-                                             float scale, const float *vote, uint64_t keep,
-                                             __nv_bfloat16 (&xm)[2][kTile], int r, bool rescale,
-                                             bool last, float &m, float &l)
+// One tile of the thread's row: the row's maximum so far, the weights, which
+// replace S as bf16 pairs, and their sum.  A slot's vote multiplies its weight
+// (exp(x + ln p) = p exp(x)).  All 128 columns are read for the maximum (a
+// read takes about 140 clocks and 10 more per 16 columns); the upper 64 stay
+// in registers for the weights and the lower 64 are read again meanwhile, which
+// is what fits without spills.  So P takes 32 columns at the start of each
+// half of S.
+template <bool kMask, bool kVotes>
+__device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float scale,
+                                             const float *vote, uint64_t keep0, uint64_t keep1,
+                                             bool rescale, float &m, float &l)
 {
-    uint32_t y0[16], y1[16];
-    float mx[2] = {-INFINITY, -INFINITY};
-    const uint32_t at = tS + 64 * half;
-    auto top_of = [&](uint32_t (&y)[16], uint32_t k) {
-        if (kMask) hide16(y, k);
+    float top;
+    uint32_t c[32], d[32];
+    {
+        uint32_t a[32], b[32];
+        tmem_ld32_async(tS, a);
+        tmem_ld32_async(tS + 32, b);
+        tmem_ld32_async(tS + 64, c);
+        tmem_ld32_async(tS + 96, d);
+        tmem_wait_ld();
+        tmem_bind(a);
+        tmem_bind(b);
+        tmem_bind(c);
+        tmem_bind(d);
+        hide32<kMask>(a, (uint32_t)keep0);
+        hide32<kMask>(b, (uint32_t)(keep0 >> 32));
+        hide32<kMask>(c, (uint32_t)keep1);
+        hide32<kMask>(d, (uint32_t)(keep1 >> 32));
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-            mx[0] = fmaxf(fmaxf(mx[0], __uint_as_float(y[j])), __uint_as_float(y[j + 1]));
-            mx[1] = fmaxf(fmaxf(mx[1], __uint_as_float(y[j + 2])), __uint_as_float(y[j + 3]));
+        for (int j = 0; j < 32; j += 2) {
+            mx[0] = fmaxf(fmaxf(mx[0], __uint_as_float(a[j])), __uint_as_float(a[j + 1]));
+            mx[1] = fmaxf(fmaxf(mx[1], __uint_as_float(b[j])), __uint_as_float(b[j + 1]));
+            mx[2] = fmaxf(fmaxf(mx[2], __uint_as_float(c[j])), __uint_as_float(c[j + 1]));
+            mx[3] = fmaxf(fmaxf(mx[3], __uint_as_float(d[j])), __uint_as_float(d[j + 1]));
         }
-    };
-    tmem_ld16_async(at, y0);
-#pragma unroll
-    for (int q = 0; q < 2; q++) {
-        const uint32_t k = (uint32_t)(keep >> (32 * q));
-        tmem_wait_ld();
-        tmem_bind16(y0);
-        tmem_ld16_async(at + 32 * q + 16, y1);
-        top_of(y0, k);
-        tmem_wait_ld();
-        tmem_bind16(y1);
-        tmem_ld16_async(q ? at : at + 32, y0);              // the last: the second pass's first
-        top_of(y1, k >> 16);
+        top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
     }
-    float top = fmaxf(mx[0], mx[1]) * scale;
-    if (pair_any(pair, top > m + kSlack || (m == -INFINITY && top > m))) {
-        tmem_wait_ld();
-        tmem_bind16(y0);
-        xm[half][r] = __float2bfloat16_rn(top);
-        pair_sync(pair);
-        top = fmaxf(__bfloat162float(xm[0][r]), __bfloat162float(xm[1][r]));
-        const bool move = top > m + kSlack || (m == -INFINITY && top > m);
+    const bool move = top > m + kSlack || (m == -INFINITY && top > m);
+    if (__any_sync(kFull, move)) {
         float f = 1.f;
         if (move) {
             f = m == -INFINITY ? 0.f : ex2_approx(m - top);
             m = top;
             l *= f;
         }
-        if (rescale && __any_sync(kFull, move)) {
+        if (rescale) {
 #pragma unroll 1
-            for (int h = 0; h < 4; h++) {
-                uint32_t y[16];
-                const uint32_t o = tO + 64 * half + 16 * h;
-                tmem_ld16_async(o, y);
+            for (int h = 0; h < 8; h++) {
+                uint32_t z[16];
+                tmem_ld16_async(tO + 16 * h, z);
                 tmem_wait_ld();
-                tmem_bind16(y);
+                tmem_bind16(z);
 #pragma unroll
-                for (int j = 0; j < 16; j++) y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
-                tmem_st16(o, y);
+                for (int j = 0; j < 16; j++) z[j] = __float_as_uint(__uint_as_float(z[j]) * f);
+                tmem_st16(tO + 16 * h, z);
             }
         }
     }
     const float nref = m == -INFINITY ? 0.f : -m;
     const float2 c2 = make_float2(scale, scale), r2 = make_float2(nref, nref);
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-    auto weights = [&](uint32_t (&y)[16], int h, uint32_t k) {
-        if (kMask) hide16(y, k);
-        uint32_t p[8];
+    auto weights = [&](uint32_t (&y)[32], uint32_t at, const float *v) {
+        uint32_t p[16];
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
+        for (int j = 0; j < 16; j += 2) {
             float2 e[2];
 #pragma unroll
             for (int i = 0; i < 2; i++) {
@@ -433,12 +374,12 @@ __device__ __forceinline__ void softmax_half(uint32_t tS, uint32_t tO, int half,
                 const float2 t = fma2(x, c2, r2);
                 e[i] = make_float2(ex2_approx(t.x), ex2_approx(t.y));
             }
-            if (vote) {
-                const float4 v = *reinterpret_cast<const float4 *>(vote + 64 * half + 16 * h + 2 * j);
-                e[0].x *= v.x;
-                e[0].y *= v.y;
-                e[1].x *= v.z;
-                e[1].y *= v.w;
+            if (kVotes) {
+                const float4 w = *reinterpret_cast<const float4 *>(v + 2 * j);
+                e[0].x *= w.x;
+                e[0].y *= w.y;
+                e[1].x *= w.z;
+                e[1].y *= w.w;
             }
 #pragma unroll
             for (int i = 0; i < 2; i++) {
@@ -446,31 +387,25 @@ __device__ __forceinline__ void softmax_half(uint32_t tS, uint32_t tO, int half,
                 p[j + i] = pack_bf16(e[i].x, e[i].y);
             }
         }
-        tmem_st8(at + 8 * h, p);                             // over columns already read
+        tmem_st16(at, p);
     };
-#pragma unroll
-    for (int q = 0; q < 2; q++) {
-        const uint32_t k = (uint32_t)(keep >> (32 * q));
-        tmem_wait_ld();
-        tmem_bind16(y0);
-        tmem_ld16_async(at + 32 * q + 16, y1);
-        weights(y0, 2 * q, k);
-        tmem_wait_ld();
-        tmem_bind16(y1);
-        if (q == 0) tmem_ld16_async(at + 32, y0);
-        weights(y1, 2 * q + 1, k >> 16);
-    }
+    uint32_t a[32], b[32];
+    tmem_ld32_async(tS, a);
+    weights(c, tS + 64, vote + 64);
+    tmem_ld32_async(tS + 32, b);
+    weights(d, tS + 80, vote + 96);
+    tmem_wait_ld();
+    tmem_bind(a);
+    tmem_bind(b);
+    hide32<kMask>(a, (uint32_t)keep0);
+    hide32<kMask>(b, (uint32_t)(keep0 >> 32));
+    weights(a, tS, vote);
+    weights(b, tS + 16, vote + 32);
     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-    if (last) tmem_st1(at + 32, l);
     tmem_wait_st();
-    if (last) {
-        tc_fence_before();
-        pair_sync(pair);
-        tc_fence_after();
-        l += tmem_ld1(tS + 64 * (half ^ 1) + 32);
-    }
 }
 
+template <bool kVotes>
 __global__ void __launch_bounds__(kThreads, 1)
 tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmQ,
@@ -486,102 +421,156 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int items = a.U * a.RB;
 
+    if (warp == kProd && lane < 5) {
+        const CUtensorMap *m = lane == 0 ? &tmK : lane == 1 ? &tmV : lane == 2 ? &tmQ
+                               : lane == 3 ? &tmKt : &tmVt;
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+    }
     if (tid == 0) {
         S.bad = 0;
         for (int i = 0; i < kRing; i++) {
             mbar_init(&S.full[i], 1);
             mbar_init(&S.empty[i], 1);
         }
-        mbar_init(&S.drain, 1);
+        for (int i = 0; i < kSegs; i++) {
+            mbar_init(&S.segfull[i], 1);
+            mbar_init(&S.segempty[i], 10);       // eight softmax warps, producer, issuer
+        }
         for (int i = 0; i < 2; i++) {
             mbar_init(&S.qfull[i], 1);
             mbar_init(&S.qempty[i], 1);
             mbar_init(&S.sfull[i], 1);
-            mbar_init(&S.pready[i], 8);
+            mbar_init(&S.pready[i], 4);
             mbar_init(&S.pvdone[i], 1);
+            mbar_init(&S.gsync[i], 4);
         }
+        mbar_init(&S.xsync, 8);
+        mbar_init(&S.drain, 1);
+        S.cut = make_int4(-1, 0, 0, 0);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kMma) tmem_alloc(&S.tmem, 512);
 
-    // the line of tiles: every CTA counts it and finds where its part starts
-    int lo, hi;
-    {
+    // this CTA's items [item0, item1) and tiles [lo, hi) of the line
+    int item0, item1, base0, lo, hi;
+    if (a.whole) {
+        // parts of whole items: nothing to count, nothing to join
+        const Cuts c(gridDim.x, items);
+        item0 = c.start(blockIdx.x);
+        item1 = c.start(blockIdx.x + 1);
+        base0 = lo = 0;
+        hi = 0x7fffffff;
+        if (blockIdx.x == 0)
+            for (int u = tid; u < a.U; u += kThreads) check_unit(a, u);
+    } else {
+        // every CTA counts the line and finds where its part starts
         const int per = (items + kThreads - 1) / kThreads;
         const int i0 = min(items, tid * per), i1 = min(items, i0 + per);
         int sum = 0;
         for (int i = i0; i < i1; i++) {
-            const int u = i / a.RB, n = a.len[u], live = tree_live(a.t, u);
-            if (blockIdx.x == 0 && (n < 0 || n > a.max_len || live < 0) && i == u * a.RB)
-                record_status(a.status, live < 0 ? KVC_ERR_INVALID_ARG : KVC_ERR_SHAPE);
-            sum += item_tiles(a, n, live, i - u * a.RB);
+            const int u = a.by_rb(i);
+            sum += item_tiles(a, a.len[u], a.live(u), i - u * a.RB);
+            if (blockIdx.x == 0 && i == u * a.RB) check_unit(a, u);
         }
-        int total;
-        int base = block_exscan(sum, S.scan, &total);
-        if (a.whole) {
-            // parts of whole items: nothing to join
-            const int c0 = (int)((long long)items * blockIdx.x / gridDim.x);
-            const int c1 = (int)((long long)items * (blockIdx.x + 1) / gridDim.x);
-            for (int i = i0, b = base; i < i1; i++) {
-                const int u = i / a.RB;
-                if (i == c0) { S.start_item = i; S.start_base = b; }
-                b += item_tiles(a, a.len[u], tree_live(a.t, u), i - u * a.RB);
-                if (i == c1 - 1) S.total = b;
-            }
-            __syncthreads();
-            lo = c0 < c1 ? S.start_base : 0;
-            hi = c0 < c1 ? S.total : 0;
-        } else {
-            const int g = parts_of(gridDim.x, total), c = min((int)blockIdx.x, g);
-            lo = g ? (int)((long long)total * c / g) : 0;
-            hi = g ? (int)((long long)total * min(c + 1, g) / g) : 0;
-            if (tid == 0) S.cut = make_int4(-1, 0, 0, 0);
-            __syncthreads();
-            for (int i = i0, b = base; i < i1; i++) {
-                const int u = i / a.RB;
-                const int nt = item_tiles(a, a.len[u], tree_live(a.t, u), i - u * a.RB);
-                if (blockIdx.x == 0) a.first[i] = b;
-                if (lo >= b && lo < b + nt) {
-                    S.start_item = i;
-                    S.start_base = b;
-                    // the part before has the item's start: this CTA names its parts
-                    if (lo > b && b >= (long long)total * (c - 1) / g)
-                        S.cut = make_int4(i, c - 1, (int)(((long long)(b + nt) * g - 1) / total), 0);
-                }
-                b += nt;
-                if (blockIdx.x == 0 && i == items - 1) a.first[items] = b;
-            }
-            __syncthreads();
-            if (tid == 0) a.cut[blockIdx.x] = S.cut;
+        int incl = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int t = __shfl_up_sync(kFull, incl, d);
+            if (lane >= d) incl += t;
         }
+        if (lane == 31) S.scan[warp] = incl;
+        __syncthreads();
+        const int of = lane < kThreads / 32 ? S.scan[lane] : 0;
+        const int total = warp_isum(of);
+        int b = incl - sum + warp_isum(lane < warp ? of : 0);
+        const Cuts c(gridDim.x, total);
+        const int bid = min((int)blockIdx.x, c.parts);
+        lo = c.start(bid);
+        hi = c.start(min(bid + 1, c.parts));
+        for (int i = i0; i < i1; i++) {
+            const int u = a.by_rb(i);
+            const int nt = item_tiles(a, a.len[u], a.live(u), i - u * a.RB);
+            if (blockIdx.x == 0) a.first[i] = b;
+            if (lo >= b && lo < b + nt) {
+                S.start_item = i;
+                S.start_base = b;
+                // the part before has the item's start: this CTA names its parts
+                if (lo > b && b >= c.start(bid - 1)) S.cut = make_int4(i, bid - 1, c.part(b + nt - 1), 0);
+            }
+            b += nt;
+            if (blockIdx.x == 0 && i == items - 1) a.first[items] = b;
+        }
+        __syncthreads();
+        if (tid == 0) a.cut[blockIdx.x] = S.cut;
+        item0 = lo < hi ? S.start_item : items;
+        item1 = items;
+        base0 = S.start_base;
     }
+    __syncthreads();
     tc_fence_after();
     const uint32_t tmem = S.tmem;
-    Walk walk(a, lo < hi ? S.start_item : items, S.start_base, lo, hi);
-    Seg s;
 
-
-    if (warp == kProd) {
+    if (warp == kWalk) {
+        // --------------------------------------------------------- walker
+        if (elect_one()) {
+            int item = item0, base = base0, k0 = 0, trees = 0, n = 0, live = 0;
+            bool ok = true;
+            if (item < item1) {
+                n = a.len[a.by_rb(item)];
+                live = a.live(a.by_rb(item));
+            }
+            for (int i = 0; ok; ) {
+                Seg s;
+                s.rows = 0;
+                if (item < item1 && base < hi) {
+                    s.item = item;
+                    s.u = a.by_rb(item);
+                    s.rb = item - s.u * a.RB;
+                    s.n = n;
+                    s.live = live;
+                    s.nt = item_tiles(a, n, live, s.rb);
+                    s.t0 = max(0, lo - base);
+                    s.t1 = min(s.nt, hi - base);
+                    s.k0 = k0;
+                    s.trees = trees;
+                    base += a.whole ? 0 : s.nt;
+                    if (++item < item1) {
+                        n = a.len[a.by_rb(item)];
+                        live = a.live(a.by_rb(item));
+                    }
+                    if (s.t1 <= s.t0) continue;
+                    s.rows = min(kRows, (s.live << a.gshift) - s.rb * kRows);
+                    k0 += s.t1 - s.t0;
+                    trees += s.t1 == s.nt;
+                }
+                if (i >= kSegs) ok = tree_wait(&S.segempty[i % kSegs], (i / kSegs - 1) & 1, &S.bad);
+                if (!ok) break;
+                S.seg[i % kSegs] = s;
+                mbar_arrive(&S.segfull[i % kSegs]);
+                i++;
+                if (s.rows == 0) break;
+            }
+        }
+        __syncwarp();
+    } else if (warp == kProd) {
         // ------------------------------------------------------- producer
         if (elect_one()) {
-            int k = 0, slot = 0, nseg = 0, qn[2] = {0, 0};
+            int k = 0, slot = 0, qn[2] = {0, 0};
             uint32_t ph = 1;                     // phase of the slot's last release
             bool ok = true;
             const uint64_t pol = l2_policy_evict_first();
             auto load = [&](const CUtensorMap *m, int u, int row, int rows, bool stream) {
-                if (k >= kRing) ok = tree_wait(&S.empty[slot], ph, &S.bad);
+                if (k >= kRing) ok = ok && tree_wait(&S.empty[slot], ph, &S.bad);
                 if (!ok) return;
                 unsigned char *d = ring + slot * kSlot;
                 const int boxes = rows > 64 ? 2 : 1;
                 mbar_expect_tx(&S.full[slot], boxes * kHalf);
+#pragma unroll
                 for (int h = 0; h < 2; h++)
                     for (int b = 0; b < boxes; b++) {
-                        if (stream)
-                            tma_3d_hint(d + h * kHalf + b * (kHalf / 2), m, 64 * h, row + 64 * b, u,
-                                        &S.full[slot], pol);
-                        else
-                            tma_3d(d + h * kHalf + b * (kHalf / 2), m, 64 * h, row + 64 * b, u,
-                                   &S.full[slot]);
+                        unsigned char *at = d + h * kHalf + b * (kHalf / 2);
+                        if (stream) tma_3d_hint(at, m, 64 * h, row + 64 * b, u, &S.full[slot], pol);
+                        else tma_3d(at, m, 64 * h, row + 64 * b, u, &S.full[slot]);
                     }
                 k++;
                 if (++slot == kRing) { slot = 0; ph ^= 1; }
@@ -598,7 +587,12 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                                &S.qfull[half]);
                 qn[half]++;
             };
-            while (ok && walk.next(s)) {
+            for (int i = 0; ok; i++) {
+                ok = tree_wait(&S.segfull[i % kSegs], (i / kSegs) & 1, &S.bad);
+                if (!ok) break;
+                const Seg s = S.seg[i % kSegs];
+                mbar_arrive(&S.segempty[i % kSegs]);
+                if (s.rows == 0) break;
                 const int qrow = s.rb * kRows;
                 if (s.rows > 128) {
                     load_q(0, s.u, qrow, 128);
@@ -606,18 +600,14 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                 } else {
                     // the halves alternate, so the next item's rows load early;
                     // an item of two halves takes both, whichever was last
-                    load_q(nseg & 1, s.u, qrow, s.rows);
+                    load_q(i & 1, s.u, qrow, s.rows);
                 }
-                nseg++;
                 for (int t = s.t0; ok && t < s.t1; t++) {
-                    const int nv = tile_valid(s, t);
-                    if (t == s.nt - 1) {
-                        load(&tmKt, s.u, 0, 64, false);
-                        if (ok) load(&tmVt, s.u, 0, 64, false);
-                    } else {
-                        load(&tmK, s.u, t * kTile, nv, a.RB == 1);
-                        if (ok) load(&tmV, s.u, t * kTile, nv, a.RB == 1);
-                    }
+                    const bool tree = t == s.nt - 1;
+                    const int nv = tree ? 64 : s.n - t * kTile, row = tree ? 0 : t * kTile;
+                    const bool stream = !tree && a.RB == 1;
+                    load(tree ? &tmKt : &tmK, s.u, row, nv, stream);
+                    load(tree ? &tmVt : &tmV, s.u, row, nv, stream);
                 }
             }
             if (!ok) {
@@ -637,13 +627,14 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
             // slot and phase of the ring's next key and value tile; phases of
             // the groups' barriers as bits
             int ks_slot = 0, vs_slot = 1;
-            uint32_t ks_ph = 0, vs_ph = 0, q_ph = 0, p_ph = 0, nseg = 0;
+            uint32_t ks_ph = 0, vs_ph = 0, q_ph = 0, p_ph = 0;
             const uint64_t q0 = umma_sdesc(smem_u32(qbuf)), k0 = umma_sdesc(smem_u32(ring));
             const uint64_t v0 = v_desc(smem_u32(ring));
             constexpr uint32_t kStep = kSlot >> 4;           // a slot in descriptor units
-            // S of group w from tile t; the key tile is waited for by its first
-            // reader and given back by its last
-            auto issue_s = [&](uint32_t w, uint32_t half, bool small, bool first, bool last_q) {
+            // S of group w; the key tile is waited for by its first reader
+            // and given back by its last
+            auto issue_s = [&](uint32_t w, uint32_t half, bool small, bool first, bool last,
+                               bool last_q) {
                 if (first) ok = ok && tree_wait(&S.full[ks_slot], ks_ph, &S.bad);
                 if (!ok) return;
                 tc_fence_after();
@@ -654,14 +645,13 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                     umma_bf16(d, umma_sdesc_step(qd, ks), umma_sdesc_step(kd, ks), idesc, ks > 0);
                 umma_commit(&S.sfull[w]);
                 if (last_q) umma_commit(&S.qempty[half]);
+                if (last) {
+                    umma_commit(&S.empty[ks_slot]);
+                    ks_slot += 2;
+                    if (ks_slot >= kRing) { ks_slot -= kRing; ks_ph ^= 1; }
+                }
             };
-            auto free_k = [&] {
-                if (!ok) return;
-                umma_commit(&S.empty[ks_slot]);
-                ks_slot += 2;
-                if (ks_slot >= kRing) { ks_slot -= kRing; ks_ph ^= 1; }
-            };
-            auto issue_o = [&](uint32_t w, int nv, bool first, bool keep) {
+            auto issue_o = [&](uint32_t w, int nv, bool first, bool last, bool keep) {
                 if (first) ok = ok && tree_wait(&S.full[vs_slot], vs_ph, &S.bad);
                 ok = ok && tree_wait(&S.pready[w], p_ph >> w & 1, &S.bad);
                 p_ph ^= 1u << w;
@@ -680,56 +670,42 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                                 kIdescO, ks > 0 || keep);
                 }
                 umma_commit(&S.pvdone[w]);
-            };
-            auto free_v = [&] {
-                if (!ok) return;
-                umma_commit(&S.empty[vs_slot]);
-                vs_slot += 2;
-                if (vs_slot >= kRing) { vs_slot -= kRing; vs_ph ^= 1; }
+                if (last) {
+                    umma_commit(&S.empty[vs_slot]);
+                    vs_slot += 2;
+                    if (vs_slot >= kRing) { vs_slot -= kRing; vs_ph ^= 1; }
+                }
             };
             auto wait_q = [&](uint32_t half) {
                 ok = ok && tree_wait(&S.qfull[half], q_ph >> half & 1, &S.bad);
                 q_ph ^= 1u << half;
             };
-            while (ok && walk.next(s)) {
+            for (int i = 0; ok; i++) {
+                ok = tree_wait(&S.segfull[i % kSegs], (i / kSegs) & 1, &S.bad);
+                if (!ok) break;
+                const Seg s = S.seg[i % kSegs];
+                mbar_arrive(&S.segempty[i % kSegs]);
+                if (s.rows == 0) break;
                 const int nq = s.t1 - s.t0;
-                const uint32_t qh = nseg++ & 1;
-                if (s.rows > 128) {
+                const uint32_t dual = s.rows > 128, jobs = nq << dual;
+                // job j: tile j of the group j & 1, or with two halves of rows
+                // tile j / 2 of the half j & 1
+                if (dual) {
                     wait_q(0);
                     wait_q(1);
-                    bool small = tile_valid(s, s.t0) <= 64;
-                    issue_s(0, 0, small, true, nq == 1);
-                    issue_s(1, 1, small, false, nq == 1);
-                    free_k();
-                    for (int t = 0; ok && t < nq; t++) {
-                        const int nv = tile_valid(s, s.t0 + t);
-                        const bool more = t + 1 < nq, end = t + 2 == nq;
-                        small = more && tile_valid(s, s.t0 + t + 1) <= 64;
-                        issue_o(0, nv, true, t > 0);
-                        if (more) issue_s(0, 0, small, true, end);
-                        issue_o(1, nv, false, t > 0);
-                        free_v();
-                        if (more) {
-                            issue_s(1, 1, small, false, end);
-                            free_k();
-                        }
-                    }
                 } else {
-                    wait_q(qh);
-                    issue_s(0, qh, tile_valid(s, s.t0) <= 64, true, nq == 1);
-                    free_k();
-                    if (nq > 1) {
-                        issue_s(1, qh, tile_valid(s, s.t0 + 1) <= 64, true, nq == 2);
-                        free_k();
+                    wait_q(i & 1);
+                }
+                for (uint32_t j = 0; ok && j < jobs + 2; j++) {
+                    const uint32_t w = j & 1, first = !dual || !w, last = !dual || w;
+                    if (j >= 2) {
+                        const int t = (int)((j - 2) >> dual);
+                        issue_o(w, tile_valid(s, s.t0 + t), first, last, j - 2 >= 2);
                     }
-                    for (int t = 0; ok && t < nq; t++) {
-                        const uint32_t w = t & 1;
-                        issue_o(w, tile_valid(s, s.t0 + t), true, t > 1);
-                        free_v();
-                        if (t + 2 < nq) {
-                            issue_s(w, qh, tile_valid(s, s.t0 + t + 2) <= 64, true, t + 3 == nq);
-                            free_k();
-                        }
+                    if (j < jobs) {
+                        const int t = (int)(j >> dual);
+                        issue_s(w, dual ? w : i & 1, tile_valid(s, s.t0 + t) <= 64, first, last,
+                                dual ? t == nq - 1 : j == jobs - 1);
                     }
                 }
             }
@@ -741,199 +717,213 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
             }
         }
         __syncwarp();
-    } else if (warp < kProd) {
+    } else {
         // --------------------------------------------------------- softmax
-        const int w = warp >> 3, half = warp >> 2 & 1, wl = warp & 3;
-        const int r = wl * 32 + lane;                    // row of the group's 128
-        const int pair = 4 + 4 * w + wl;
-        const uint32_t lanes = (uint32_t)(wl * 32) << 16;
+        const int w = warp >> 2, r = tid & 127;              // group, row of its 128
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lanes + kColS + 128 * w, tO = tmem + lanes + 128 * w;
+        uint32_t job = 0, gph = 0, xph = 0;                  // jobs so far; barrier phases
         bool ok = true;
-        int k0 = 0, sn = 0, pn = 0, ntree = 0;
-        while (walk.next(s)) {
-            const bool dual = s.rows > 128;
-            const int nq = s.t1 - s.t0;
+        auto wait = [&](uint64_t *b, uint32_t ph) {
+            const bool x = tree_wait(b, ph, &S.bad);
+            ok = __all_sync(kFull, x);
+        };
+        // barriers of the group's 128 threads and of all 256
+        auto group_sync = [&] {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.gsync[w]);
+            wait(&S.gsync[w], gph);
+            gph ^= 1;
+        };
+        auto all_sync = [&] {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.xsync);
+            wait(&S.xsync, xph);
+            xph ^= 1;
+            tc_fence_after();
+        };
+        for (int i = 0; ok; i++) {
+            wait(&S.segfull[i % kSegs], (i / kSegs) & 1);
+            if (!ok) break;
+            const volatile Seg &s = S.seg[i % kSegs];
+            const int rows = s.rows;
+            if (rows == 0) break;
+            const bool dual = rows > 128;
+            const int step = dual ? 1 : 2;
             const int row = (dual ? 128 * w : 0) + r;        // row of the item
-            const bool mine = row < s.rows;
-            const bool busy = (dual ? 128 * w : 0) + wl * 32 < s.rows;   // the warp has rows
-            const int grow = s.rb * kRows + row;             // row of the unit
+            const bool busy = row - lane < rows;             // the warp has rows
             float m = -INFINITY, l = 0.f;
-            int done = 0;                                    // this group's tiles so far
-            uint64_t odd = 0;                                // drafted tokens added by hand
-            uint64_t see = 0;
-            if (mine)
-                see = a.t.mask[(size_t)(s.u / a.t.units) * a.t.T + grow / a.G] &
-                      (s.live >= 64 ? ~0ull : (1ull << s.live) - 1);
+            bool begun = false;                              // O has a tile's product
+            uint64_t see = 0;                                // drafted tokens the row sees
             int vote_next = 0;                               // loaded a tile ahead
-            if (a.votes && half == 0) {
-                const int i = (s.t0 + (dual ? 0 : w)) * kTile + r;
-                if (i < s.n) vote_next = a.votes[(size_t)s.u * a.cap + i];
+            {
+                const int live = s.live, u = s.u;
+                if (row < rows)
+                    see = a.t.mask[(size_t)a.by_units(u) * a.t.T + ((s.rb * kRows + row) >> a.gshift)] &
+                          (live >= 64 ? ~0ull : (1ull << live) - 1);
+                if (kVotes) {
+                    const int at = (s.t0 + (dual ? 0 : w)) * kTile + r;
+                    if (at < s.n) vote_next = a.votes[(size_t)u * a.cap + at];
+                }
             }
-            for (int t = dual ? 0 : w; t < nq; t += dual ? 1 : 2) {
-                const int tile = s.t0 + t, nv = tile_valid(s, tile);
+            for (int tile = s.t0 + (dual ? 0 : w); tile < s.t1; tile += step) {
                 const bool tree = tile == s.nt - 1;
-                const int kv = k0 + 2 * t + 1, slot = kv % kRing;
-                const bool votes = a.votes != nullptr && !tree;
-                if (votes) {
-                    group_sync(w);                           // the last tile's are read
-                    if (half == 0) S.g[w].vote[r] = (float)vote_next;
-                    const int i = (tile + (dual ? 1 : 2)) * kTile + r;
-                    if (half == 0 && i < s.n) vote_next = a.votes[(size_t)s.u * a.cap + i];
-                    group_sync(w);
+                const int nv = tree ? s.live : min(kTile, s.n - tile * kTile);
+                if (kVotes) {
+                    group_sync();                            // the last tile's are read
+                    S.g[w].vote[r] = tree ? 1.f : (float)vote_next;
+                    const int at = (tile + step) * kTile + r;
+                    if (at < s.n) vote_next = a.votes[(size_t)s.u * a.cap + at];
+                    group_sync();
+                    if (!ok) break;
                 }
                 // value rows the MMA reads that are no slot: zero
-                if (!dual || w == 0) {
-                    if (nv & 15 || tree) {
-                        ok = tree_wait(&S.full[slot], (kv / kRing) & 1, &S.bad) && ok;
-                        unsigned char *v = ring + slot * kSlot;
-                        const int stop = (nv + 15) & ~15;
-                        if (tree && half == 0 && r < 64) {
-                            // thread r has row r: what is not finite is zeroed here and
-                            // added to the rows that see it at the end
-                            bool bad = false;
-                            if (r < stop)
-                                for (int c = 0; c < 16; c++) {
-                                    unsigned char *p = v + (c >> 3) * kHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-                                    const uint4 x = lds_v4(p);
-                                    uint32_t q[4] = {x.x, x.y, x.z, x.w};
-                                    bool hit = r >= nv;
+                if ((tree || nv & 15) && (!dual || w == 0)) {
+                    const int kv = 2 * (s.k0 + tile - s.t0) + 1, slot = kv % kRing;
+                    wait(&S.full[slot], (kv / kRing) & 1);
+                    if (!ok) break;
+                    unsigned char *v = ring + slot * kSlot;
+                    const int stop = (nv + 15) & ~15;
+                    bool odd = false;
+                    if (r < stop && (tree || r >= nv)) {
+                        // thread r has slot r; of a drafted token, what is not finite is
+                        // zeroed here and added to the rows that see it at the end
+#pragma unroll 2
+                        for (int c = 0; c < 16; c++) {
+                            uint4 *p = reinterpret_cast<uint4 *>(
+                                v + (c >> 3) * kHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+                            uint32_t x[4] = {0, 0, 0, 0};
+                            if (r < nv) {
+                                const uint4 y = *p;
+                                x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
+                            }
+                            bool hit = r >= nv;
 #pragma unroll
-                                    for (int e = 0; e < 4; e++) {
-                                        const bool lo = (q[e] & 0x7f80u) == 0x7f80u;
-                                        const bool hi = (q[e] & 0x7f800000u) == 0x7f800000u;
-                                        hit |= lo || hi;
-                                        if (lo || r >= nv) q[e] &= 0xffff0000u;
-                                        if (hi || r >= nv) q[e] &= 0x0000ffffu;
-                                    }
-                                    if (hit)
-                                        *reinterpret_cast<uint4 *>(p) = make_uint4(q[0], q[1], q[2], q[3]);
-                                    bad |= hit;
-                                }
-                            const uint32_t bits = __ballot_sync(kFull, bad && r < nv);
-                            if (lane == 0) reinterpret_cast<uint32_t *>(&S.odd[ntree & 1])[wl] = bits;
-                        } else if (!tree && half == 0 && r >= nv && r < stop) {
-                            for (int c = 0; c < 16; c++)
-                                *reinterpret_cast<uint4 *>(v + (c >> 3) * kHalf + r * 128 +
-                                                           ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                            for (int e = 0; e < 4; e++) {
+                                if ((x[e] & 0x7f80u) == 0x7f80u) { x[e] &= 0xffff0000u; hit = true; }
+                                if ((x[e] & 0x7f800000u) == 0x7f800000u) { x[e] &= 0x0000ffffu; hit = true; }
+                            }
+                            if (hit) *p = make_uint4(x[0], x[1], x[2], x[3]);
+                            odd |= hit;
                         }
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        group_sync(w);
                     }
+                    if (tree && warp - 4 * w < 2) {
+                        const uint32_t bits = __ballot_sync(kFull, odd && r < nv);
+                        if (lane == 0)
+                            reinterpret_cast<uint32_t *>(&S.odd[s.trees & 1])[warp - 4 * w] = bits;
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
-                if (tree && dual) bar_sync<1, 512>();        // both groups see the odd tokens
-                if (tree) odd = S.odd[ntree & 1];
-                ok = tree_wait(&S.sfull[w], sn & 1, &S.bad) && ok;
-                sn++;
+                wait(&S.sfull[w], job & 1);
+                if (!ok) break;
                 tc_fence_after();
                 if (busy) {
-                    const float *vote = votes ? S.g[w].vote : nullptr;
-                    const bool last = t + (dual ? 1 : 2) >= nq;
                     if (tree || nv < kTile) {
-                        uint64_t keep = 0;                   // slots the row may see
-                        if (tree) {
-                            keep = half ? 0 : see;
-                        } else {
-                            const int k = nv - 64 * half;
-                            keep = k >= 64 ? ~0ull : k <= 0 ? 0ull : (1ull << k) - 1;
+                        uint64_t keep0 = see, keep1 = 0;     // the slots the row may see
+                        if (!tree) {
+                            keep0 = nv >= 64 ? ~0ull : (1ull << nv) - 1;
+                            keep1 = nv <= 64 ? 0ull : (1ull << (nv - 64)) - 1;
                         }
-                        softmax_half<true>(tS, tO, half, pair, a.scale, vote, keep, S.g[w].top, r,
-                                           done > 0, last, m, l);
+                        softmax_tile<true, kVotes>(tS, tO, a.scale, S.g[w].vote, keep0, keep1, begun, m, l);
                     } else {
-                        softmax_half<false>(tS, tO, half, pair, a.scale, vote, ~0ull, S.g[w].top, r,
-                                            done > 0, last, m, l);
+                        softmax_tile<false, kVotes>(tS, tO, a.scale, S.g[w].vote, 0, 0, begun, m, l);
                     }
                 }
-                done++;
+                begun = true;
+                job++;
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&S.pready[w]);
-                pn++;
             }
-            k0 += 2 * nq;
             // ------------------------------------------------------ outputs
-            if (done > 0) ok = tree_wait(&S.pvdone[w], (pn - 1) & 1, &S.bad) && ok;
+            if (ok && begun) wait(&S.pvdone[w], (job - 1) & 1);
+            if (!ok) break;
             tc_fence_after();
-            const bool all = s.t1 - s.t0 == s.nt;            // nothing to join
-            const bool direct = all && !a.join_all;
-            float c0 = 1.f, c1 = 0.f, M = m, Lsum = l;       // weights of the groups' sums
+            const int u = s.u, nq = s.t1 - s.t0;
+            const bool direct = nq == s.nt && !a.join_all;   // nothing to join
+            const bool has_tree = s.t1 == s.nt;
+            float c0 = 1.f, c1 = 0.f, M = m, L = l;          // weights of the groups' sums
+            if (!dual) S.g[w].ml[r] = make_float2(m, l);
+            if (!dual || has_tree) {                         // has_tree: S.odd is written
+                all_sync();
+                if (!ok) break;
+            }
             if (!dual) {
-                if (half == 0) S.g[w].ml[r] = make_float2(m, l);
-                tc_fence_before();
-                bar_sync<1, 512>();
-                tc_fence_after();
-                odd = S.odd[ntree & 1];          // written by the group that had the tokens' tile
                 const float2 p0 = S.g[0].ml[r], p1 = S.g[1].ml[r];
                 M = fmaxf(p0.x, p1.x);
                 const float ref = M == -INFINITY ? 0.f : M;
                 c0 = ex2_approx(p0.x - ref);
                 c1 = ex2_approx(p1.x - ref);
-                Lsum = p0.y * c0 + p1.y * c1;
+                L = p0.y * c0 + p1.y * c1;
             }
-            const size_t sid = (size_t)s.item + blockIdx.x;
-            const size_t orow = (size_t)s.u * a.TG + grow;
-            const float inv = Lsum == 0.f ? 0.f : 1.f / Lsum;
-            const float k_0 = direct ? c0 * inv : c0, k_1 = direct ? c1 * inv : c1;
-            const bool has_tree = s.t1 == s.nt;
-            const uint64_t by_hand = has_tree ? odd & see : 0;
-            ntree += has_tree;
-            // a warp writes 64 columns of its rows, or (alternate tiles) 32
+            const size_t part = ((size_t)s.item + blockIdx.x) * a.rows + row;
+            const size_t orow = (size_t)u * a.TG + (size_t)(s.rb * kRows + row);
+            if (direct) {
+                const float inv = L == 0.f ? 0.f : 1.f / L;
+                c0 *= inv;
+                c1 *= inv;
+            }
+            const uint64_t by_hand = has_tree ? S.odd[s.trees & 1] & see : 0;
+            // a group writes its rows whole, or (alternate tiles) half of the columns
+            const int q0 = dual ? 0 : 4 * w, q1 = dual ? 8 : q0 + 4;
+            const bool two = !dual && nq > 1, mine = row < rows;
             if (busy) {
-                const int q0 = dual ? 2 * half : 2 * w + half, q1 = dual ? q0 + 2 : q0 + 1;
 #pragma unroll 1
-                for (int q = 2 * q0; q < 2 * q1; q++) {      // 16 columns at a time
+                for (int q = q0; q < q1; q++) {              // 16 columns at a time
                     uint32_t y[16], z[16];
                     tmem_ld16_async(tmem + lanes + (dual ? 128 * w : 0) + 16 * q, y);
-                    if (!dual && nq > 1) tmem_ld16_async(tmem + lanes + 128 + 16 * q, z);
+                    if (two) tmem_ld16_async(tmem + lanes + 128 + 16 * q, z);
                     tmem_wait_ld();
                     tmem_bind16(y);
                     float f[16];
 #pragma unroll
-                    for (int j = 0; j < 16; j++) f[j] = __uint_as_float(y[j]) * k_0;
-                    if (!dual && nq > 1) {
+                    for (int j = 0; j < 16; j++) f[j] = __uint_as_float(y[j]) * c0;
+                    if (two) {
                         tmem_bind16(z);
 #pragma unroll
-                        for (int j = 0; j < 16; j++) f[j] = fmaf(__uint_as_float(z[j]), k_1, f[j]);
+                        for (int j = 0; j < 16; j++) f[j] = fmaf(__uint_as_float(z[j]), c1, f[j]);
                     }
-                    if (by_hand) {
-                        // a visible value that is not finite: whatever its weight, the
-                        // output is what weight x value gives, not finite
-                        for (uint64_t rest = by_hand; rest; rest &= rest - 1) {
-                            const int jt = __ffsll((long long)rest) - 1;
-                            const uint16_t *vr = a.vt + ((size_t)s.u * a.t.T + jt) * kD + 16 * q;
-#pragma unroll
-                            for (int j = 0; j < 16; j++) {
-                                const float v = bf2f(vr[j]);
-                                f[j] += isfinite(v) ? 0.f : v;
-                            }
-                        }
-                    }
-                    if (mine && ok) {
+                    if (mine) {
                         if (direct) {
-                            uint32_t h[8];
-#pragma unroll
-                            for (int j = 0; j < 8; j++) h[j] = pack_bf16(f[2 * j], f[2 * j + 1]);
                             uint4 *d = reinterpret_cast<uint4 *>(a.o + orow * kD + 16 * q);
-                            d[0] = make_uint4(h[0], h[1], h[2], h[3]);
-                            d[1] = make_uint4(h[4], h[5], h[6], h[7]);
+                            d[0] = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
+                                              pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+                            d[1] = make_uint4(pack_bf16(f[8], f[9]), pack_bf16(f[10], f[11]),
+                                              pack_bf16(f[12], f[13]), pack_bf16(f[14], f[15]));
                         } else {
-                            float *d = a.part + (sid * a.rows + row) * kD + 16 * q;
+                            float *d = a.part + part * kD + 16 * q;
                             st_v8(d, reinterpret_cast<const uint32_t *>(f));
                             st_v8(d + 8, reinterpret_cast<const uint32_t *>(f + 8));
                         }
                     }
                 }
-                if (mine && ok && half == 0 && (dual || w == 0)) {
+                // drafted tokens that the row sees and whose value is not finite: whatever
+                // their weight, the output of such a column is not finite
+                if (mine)
+                    for (uint64_t rest = by_hand; rest; rest &= rest - 1) {
+                        const uint16_t *vr = a.vt + ((size_t)u * a.t.T + __ffsll((long long)rest) - 1) * kD;
+#pragma unroll 1
+                        for (int c = 16 * q0; c < 16 * q1; c++) {
+                            const float v = bf2f(vr[c]);
+                            if (isfinite(v)) continue;
+                            if (direct) a.o[orow * kD + c] = pack_bf16(bf2f(a.o[orow * kD + c]) + v, 0.f);
+                            else a.part[part * kD + c] += v;
+                        }
+                    }
+                if (mine && (dual || w == 0)) {
                     if (direct)
-                        a.lse[orow] = Lsum == 0.f ? -INFINITY
-                                                  : (M + log2f(Lsum)) * 0.6931471805599453f;
+                        a.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
                     else
-                        a.ml[sid * a.rows + row] = make_float2(M, Lsum);
+                        a.ml[part] = make_float2(M, L);
                 }
             }
             // the other group reads this one's sums: both are done before either goes on
-            tc_fence_before();
-            if (!dual) bar_sync<1, 512>();
+            if (!dual) all_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.segempty[i % kSegs]);
         }
+        if (!ok && lane == 0) S.bad = 1;
     }
     __syncthreads();
     if (warp == kMma) tmem_dealloc(tmem, 512);
@@ -958,8 +948,8 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
     const int4 cut = a.cut[blockIdx.x];
     if (cut.x < 0) return;
     const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
-    const int u = cut.x / a.RB, rb = cut.x - u * a.RB;
-    if (r >= min(kRows, tree_live(a.t, u) * a.G - rb * kRows)) return;
+    const int u = a.by_rb(cut.x), rb = cut.x - u * a.RB;
+    if (r >= min(kRows, (a.live(u) << a.gshift) - rb * kRows)) return;
     const size_t at = ((size_t)cut.x + cut.y) * a.rows + r, step = (size_t)a.rows;
     const int np = cut.z - cut.y + 1;
     float M = -INFINITY;
@@ -1014,20 +1004,21 @@ __global__ void __launch_bounds__(256, 2) tree_moment_kernel(const __grid_consta
     const AttArgs &a = j.a;
     extern __shared__ __align__(1024) unsigned char cs[];   // C: high terms, low terms
     __shared__ float muk[kD], muv[kD];
-    const int item = blockIdx.x, u = item / a.RB, rb = item - u * a.RB;
+    const int item = blockIdx.x, u = a.by_rb(item), rb = item - u * a.RB;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3, n0 = 64 * (warp & 1);
-    const int n = a.len[u], live = tree_live(a.t, u);
+    const int n = a.len[u], live = a.live(u);
     const float ne = j.mn[u];
     const bool mix = ne > 0.f;
-    const int rows = min(kRows, live * a.G - rb * kRows), r0 = blockIdx.y * kMomRows + 16 * (warp >> 1);
+    const int rows = min(kRows, (live << a.gshift) - rb * kRows), r0 = blockIdx.y * kMomRows + 16 * (warp >> 1);
     // the part that has the item's start (its place has the joined sums)
     int c0;
     if (a.whole) {
-        c0 = (int)((((long long)item + 1) * j.grid - 1) / (a.U * a.RB));
+        c0 = Cuts(j.grid, a.U * a.RB).part(item);
     } else {
-        const int W = a.first[a.U * a.RB];
-        c0 = W ? (int)(((a.first[item] + 1ll) * parts_of(j.grid, W) - 1) / W) : 0;
+        const int W = a.first[a.U * a.RB], b = a.first[item];
+        if (W == 0) return;
+        c0 = Cuts(j.grid, W).part(min(b, W - 1));
     }
     if (n < 0 || n > a.max_len || live < 0 || (int)blockIdx.y * kMomRows >= rows) return;
     if (mix && j.first_order) {
@@ -1180,16 +1171,17 @@ cudaError_t launch_tree_attend(const kvc_params &p, int max_len, const TreeArgs 
         !make_unit_map(&mq, q, p.U, TG) || !make_unit_map(&mkt, kt, p.U, t.T) ||
         !make_unit_map(&mvt, vt, p.U, t.T))
         return cudaErrorInvalidValue;
-    const bool whole = tmax <= 4 || items >= 8 * kGrid;
+    const bool whole = tmax <= 4 || items >= 6 * kGrid;
     long long grid = whole ? items : (items * tmax + 3) / 4;
     if (grid < items) grid = items;
     if (grid > kGrid) grid = kGrid;
-    AttArgs a{t, c.votes, c.len, vt, o, lse, w.part, w.ml, w.first, w.cut, w.status, p.U, RB, TG, p.G, p.cap,
-              max_len, TG < kRows ? TG : kRows, whole, m != nullptr, kLog2e / sqrtf((float)kD)};
-    cudaError_t e = cudaFuncSetAttribute(tree_attend_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDyn);
+    AttArgs a{t, c.votes, c.len, vt, o, lse, w.part, w.ml, w.first, w.cut, w.status, p.U, RB, TG,
+              p.G == 1 ? 0 : p.G == 2 ? 1 : p.G == 4 ? 2 : 3, p.cap, max_len, TG < kRows ? TG : kRows,
+              whole, m != nullptr, FastDiv(RB), FastDiv(t.units), kLog2e / sqrtf((float)kD)};
+    auto *kernel = c.votes ? tree_attend_kernel<true> : tree_attend_kernel<false>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDyn);
     if (e != cudaSuccess) return e;
-    tree_attend_kernel<<<(int)grid, kThreads, kDyn, st>>>(a, mk, mv, mq, mkt, mvt);
+    kernel<<<(int)grid, kThreads, kDyn, st>>>(a, mk, mv, mq, mkt, mvt);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (m == nullptr && whole) return cudaSuccess;
     JoinArgs j{a, q, m ? m->n : nullptr, m ? m->mu_k : nullptr, m ? m->mu_v : nullptr,
