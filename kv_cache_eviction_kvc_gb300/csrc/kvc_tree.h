@@ -68,6 +68,20 @@ __device__ __forceinline__ void tma_3d_hint(void *dst, const CUtensorMap *map, i
         : "memory");
 }
 
+// [units][rows][128] fp32, boxes of 32 columns x box_rows rows of a unit with
+// the 128-byte swizzle.
+inline bool make_f32_map(CUtensorMap *m, const void *base, uint64_t units, uint64_t rows, int box_rows)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)kD, (cuuint64_t)rows, (cuuint64_t)units};
+    const cuuint64_t strides[2] = {(cuuint64_t)(kD * 4), (cuuint64_t)(rows * kD * 4)};
+    const cuuint32_t box[3] = {32u, (cuuint32_t)box_rows, 1u}, estr[3] = {1u, 1u, 1u};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void *>(base), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // [units][rows][128] bf16, boxes of 64 columns x 64 rows of a unit with the
 // 128-byte swizzle; rows past a unit's last read as zero.  A unit index and a
 // row index fit 32 bits where their product does not.

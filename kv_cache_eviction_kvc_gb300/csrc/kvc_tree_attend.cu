@@ -90,7 +90,7 @@ struct AttArgs {
     float *part;            // [items + CTAs][rows][128]
     float2 *ml;             // [items + CTAs][rows]
     int *first;             // [items + 1] tiles before each item
-    int4 *cut;              // [CTAs] the item a part begins inside of: item, first and last part
+    int4 *cut;              // [CTAs] the item a part begins inside of: item, first and last part, rows
     int32_t *status;
     int U, RB, TG, gshift, cap, max_len, rows, whole, join_all;
     FastDiv by_rb, by_units;
@@ -114,7 +114,7 @@ struct __align__(16) Seg {
 
 struct AttSmem {
     union {                 // read as float4
-        float vote[kTile];  // votes of a tile's slots
+        float vote[2][kTile];   // votes of a tile's slots, and the next one's
         float2 ml[kTile];   // at an item's end: the rows' maxima and sums
     } g[2];
     Seg seg[kSegs];
@@ -495,7 +495,9 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                 S.start_item = i;
                 S.start_base = b;
                 // the part before has the item's start: this CTA names its parts
-                if (lo > b && b >= c.start(bid - 1)) S.cut = make_int4(i, bid - 1, c.part(b + nt - 1), 0);
+                if (lo > b && b >= c.start(bid - 1)) S.cut = make_int4(
+                        i, bid - 1, c.part(b + nt - 1),
+                        min(kRows, (a.live(u) << a.gshift) - (i - u * a.RB) * kRows));
             }
             b += nt;
             if (blockIdx.x == 0 && i == items - 1) a.first[items] = b;
@@ -756,27 +758,32 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
             float m = -INFINITY, l = 0.f;
             bool begun = false;                              // O has a tile's product
             uint64_t see = 0;                                // drafted tokens the row sees
-            int vote_next = 0;                               // loaded a tile ahead
+            int vote_next = 0;                               // votes: loaded two tiles ahead,
+                                                             // in shared memory one ahead
             {
                 const int live = s.live, u = s.u;
                 if (row < rows)
                     see = a.t.mask[(size_t)a.by_units(u) * a.t.T + ((s.rb * kRows + row) >> a.gshift)] &
                           (live >= 64 ? ~0ull : (1ull << live) - 1);
-                if (kVotes) {
+                // (a group without a tile here must not write: the maxima and sums of the
+                // item's end share the space, and only tiles order the group's warps)
+                if (kVotes && s.t0 + (dual ? 0 : w) < s.t1) {
                     const int at = (s.t0 + (dual ? 0 : w)) * kTile + r;
-                    if (at < s.n) vote_next = a.votes[(size_t)u * a.cap + at];
+                    const int32_t *v = a.votes + (size_t)u * a.cap + at;
+                    S.g[w].vote[job & 1][r] = at < s.n ? (float)v[0] : 1.f;
+                    if (at + step * kTile < s.n) vote_next = v[step * kTile];
                 }
             }
             for (int tile = s.t0 + (dual ? 0 : w); tile < s.t1; tile += step) {
                 const bool tree = tile == s.nt - 1;
                 const int nv = tree ? s.live : min(kTile, s.n - tile * kTile);
                 if (kVotes) {
-                    group_sync();                            // the last tile's are read
-                    S.g[w].vote[r] = tree ? 1.f : (float)vote_next;
-                    const int at = (tile + step) * kTile + r;
-                    if (at < s.n) vote_next = a.votes[(size_t)s.u * a.cap + at];
-                    group_sync();
+                    group_sync();        // this tile's votes are there, the last one's are read
                     if (!ok) break;
+                    const int at = (tile + step) * kTile + r;
+                    S.g[w].vote[(job + 1) & 1][r] = at < s.n ? (float)vote_next : 1.f;
+                    if (at + step * kTile < s.n)
+                        vote_next = a.votes[(size_t)s.u * a.cap + at + step * kTile];
                 }
                 // value rows the MMA reads that are no slot: zero
                 if ((tree || nv & 15) && (!dual || w == 0)) {
@@ -825,9 +832,9 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                             keep0 = nv >= 64 ? ~0ull : (1ull << nv) - 1;
                             keep1 = nv <= 64 ? 0ull : (1ull << (nv - 64)) - 1;
                         }
-                        softmax_tile<true, kVotes>(tS, tO, a.scale, S.g[w].vote, keep0, keep1, begun, m, l);
+                        softmax_tile<true, kVotes>(tS, tO, a.scale, S.g[w].vote[job & 1], keep0, keep1, begun, m, l);
                     } else {
-                        softmax_tile<false, kVotes>(tS, tO, a.scale, S.g[w].vote, 0, 0, begun, m, l);
+                        softmax_tile<false, kVotes>(tS, tO, a.scale, S.g[w].vote[job & 1], 0, 0, begun, m, l);
                     }
                 }
                 begun = true;
@@ -932,195 +939,260 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
 
 struct JoinArgs {
     AttArgs a;
-    const uint16_t *q;
-    const float *mn, *mu_k, *mu_v, *C;
+    const float *mn, *mu_k, *mu_v;
     int first_order, grid;
 };
 
-// The sums of a cut item's parts added: one warp per row, a lane has four
-// columns.  The result is the output, or (kKeep, when the moments follow) the
-// first part's place takes it.  grid (CTAs of the attention, rows / 8): block
-// x takes the item whose first cut is the start of part x.
+// The sums of a cut item's parts added.  A warp has four rows, a lane four of
+// their columns; the loads of four parts are in flight together.  The result
+// is the output, or (kKeep, when the moments follow) the first part's place
+// takes it.  grid (CTAs of the attention, rows / 32): block x takes the item
+// whose first cut is the start of part x.
 template <bool kKeep>
 __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ JoinArgs j)
 {
     const AttArgs &a = j.a;
-    const int4 cut = a.cut[blockIdx.x];
-    if (cut.x < 0) return;
-    const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
+    const int4 cut = a.cut[blockIdx.x];                     // item, first and last part, rows
+    const int lane = threadIdx.x & 31, r0 = blockIdx.y * 32 + 4 * (threadIdx.x >> 5);
+    if (cut.x < 0 || r0 >= cut.w) return;
+    const int nr = min(4, cut.w - r0), np = cut.z - cut.y + 1;
+    const size_t at = ((size_t)cut.x + cut.y) * a.rows + r0, step = (size_t)a.rows;
+    float M[4], L[4];
+    float4 f[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        M[i] = -INFINITY;
+        L[i] = 0.f;
+        f[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int k0 = 0; k0 < np; k0 += 4) {
+        // places past the last part or row are read again and weigh nothing
+        float2 ml[4][4];
+        float4 p[4][4];
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const size_t x = at + min(k0 + k, np - 1) * step + min(i, nr - 1);
+                ml[k][i] = a.ml[x];
+                p[k][i] = reinterpret_cast<const float4 *>(a.part + x * kD)[lane];
+            }
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const float m = fmaxf(M[i], ml[k][i].x), ref = m == -INFINITY ? 0.f : m;
+                const float c = ex2_approx(M[i] - ref);
+                if (k0 + k >= np) continue;
+                const float e = ex2_approx(ml[k][i].x - ref);
+                M[i] = m;
+                L[i] = fmaf(L[i], c, ml[k][i].y * e);
+                f[i].x = fmaf(f[i].x, c, p[k][i].x * e);
+                f[i].y = fmaf(f[i].y, c, p[k][i].y * e);
+                f[i].z = fmaf(f[i].z, c, p[k][i].z * e);
+                f[i].w = fmaf(f[i].w, c, p[k][i].w * e);
+            }
+    }
     const int u = a.by_rb(cut.x), rb = cut.x - u * a.RB;
-    if (r >= min(kRows, (a.live(u) << a.gshift) - rb * kRows)) return;
-    const size_t at = ((size_t)cut.x + cut.y) * a.rows + r, step = (size_t)a.rows;
-    const int np = cut.z - cut.y + 1;
-    float M = -INFINITY;
-    for (int k = lane; k < np; k += 32) M = fmaxf(M, a.ml[at + k * step].x);
-    M = warp_max(M);
-    const float ref = M == -INFINITY ? 0.f : M;
-    float L = 0.f;
-    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = 0; k0 < np; k0 += 32) {
-        float s = 0.f;
-        if (k0 + lane < np) {
-            const float2 ml = a.ml[at + (k0 + lane) * step];
-            s = ex2_approx(ml.x - ref);
-            L += ml.y * s;
-        }
-        const int m = min(32, np - k0);
-#pragma unroll 8
-        for (int k = 0; k < m; k++) {
-            const float c = __shfl_sync(kFull, s, k);
-            const float4 p =
-                reinterpret_cast<const float4 *>(a.part + (at + (k0 + k) * step) * kD)[lane];
-            f.x = fmaf(p.x, c, f.x);
-            f.y = fmaf(p.y, c, f.y);
-            f.z = fmaf(p.z, c, f.z);
-            f.w = fmaf(p.w, c, f.w);
+    const size_t row = (size_t)u * a.TG + (size_t)rb * kRows + r0;
+    if (kKeep) __syncwarp();                                // all lanes have read ml
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        if (i >= nr) break;
+        if (kKeep) {
+            reinterpret_cast<float4 *>(a.part + (at + i) * kD)[lane] = f[i];
+            if (lane == 0) a.ml[at + i] = make_float2(M[i], L[i]);
+        } else {
+            const float inv = L[i] == 0.f ? 0.f : 1.f / L[i];
+            reinterpret_cast<uint2 *>(a.o + (row + i) * kD)[lane] =
+                make_uint2(pack_bf16(f[i].x * inv, f[i].y * inv), pack_bf16(f[i].z * inv, f[i].w * inv));
+            if (lane == 0)
+                a.lse[row + i] = L[i] == 0.f ? -INFINITY : (M[i] + log2f(L[i])) * 0.6931471805599453f;
         }
     }
-    L = warp_sum(L);
-    if (kKeep) {
-        __syncwarp();
-        reinterpret_cast<float4 *>(a.part + at * kD)[lane] = f;
-        if (lane == 0) a.ml[at] = make_float2(M, L);
-        return;
-    }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    const size_t row = (size_t)u * a.TG + (size_t)rb * kRows + r;
-    reinterpret_cast<uint2 *>(a.o + row * kD)[lane] =
-        make_uint2(pack_bf16(f.x * inv, f.y * inv), pack_bf16(f.z * inv, f.w * inv));
-    if (lane == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
 // The normalization correction: every row's sum normalised and mixed with the
-// evicted set's estimate.  C q runs on tensor cores (mma.sync) with C as two
-// bf16 terms (2^-16 of a product) in shared memory, 128-byte swizzled.  A CTA
-// has 64 rows of an item, a warp 16 rows and half of the columns; grid
-// (items, rows / 64).
+// evicted set's estimate.  Bound by bytes: 64 KB of C per unit, 1 KB per row.
+// A persistent CTA per SM takes 64 rows of an item at a time; C, the rows' q
+// and their sums come by TMA into two stages (128-byte swizzle, so that the
+// fragment reads below hit all banks).  C q runs on mma.sync with C as two
+// bf16 terms (2^-16 of a product) taken apart as its fragments are read; warp
+// w has 16 rows and half of the columns.
 constexpr int kMomRows = 64;
-constexpr size_t kMomDyn = 2 * (size_t)kSlot;
+constexpr int kMomC = kD * kD * 4, kMomQ = kMomRows * kD * 2, kMomF = kMomRows * kD * 4;
+constexpr int kMomStage = kMomC + kMomQ + kMomF;
+constexpr size_t kMomDyn = 2 * (size_t)kMomStage;
 
-__global__ void __launch_bounds__(256, 2) tree_moment_kernel(const __grid_constant__ JoinArgs j)
+// Byte offset of columns (c, c + 1) of row r: boxes of 32 fp32 columns x kRows.
+template <int kRowsOfBox>
+__device__ __forceinline__ uint32_t mom_off(int r, int c)
+{
+    return (uint32_t)((c >> 5) * kRowsOfBox * 128 + r * 128 + ((((c & 31) >> 2) ^ (r & 7)) << 4) +
+                      (c & 3) * 4);
+}
+
+__global__ void __launch_bounds__(256, 1)
+tree_moment_kernel(const __grid_constant__ JoinArgs j, const __grid_constant__ CUtensorMap tmQ,
+                   const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmF)
 {
     const AttArgs &a = j.a;
-    extern __shared__ __align__(1024) unsigned char cs[];   // C: high terms, low terms
-    __shared__ float muk[kD], muv[kD];
-    const int item = blockIdx.x, u = a.by_rb(item), rb = item - u * a.RB;
+    extern __shared__ __align__(1024) unsigned char dyn[];
+    __shared__ uint64_t full[2];
+    __shared__ int bad;
+    if (smem_u32(dyn) & 1023) {
+        if (threadIdx.x == 0) record_status(a.status, KVC_ERR_CUDA);
+        return;
+    }
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int g = lane >> 2, t = lane & 3, n0 = 64 * (warp & 1);
-    const int n = a.len[u], live = a.live(u);
-    const float ne = j.mn[u];
-    const bool mix = ne > 0.f;
-    const int rows = min(kRows, (live << a.gshift) - rb * kRows), r0 = blockIdx.y * kMomRows + 16 * (warp >> 1);
-    // the part that has the item's start (its place has the joined sums)
-    int c0;
-    if (a.whole) {
-        c0 = Cuts(j.grid, a.U * a.RB).part(item);
-    } else {
-        const int W = a.first[a.U * a.RB], b = a.first[item];
-        if (W == 0) return;
-        c0 = Cuts(j.grid, W).part(min(b, W - 1));
-    }
-    if (n < 0 || n > a.max_len || live < 0 || (int)blockIdx.y * kMomRows >= rows) return;
-    if (mix && j.first_order) {
-        const float4 *C = reinterpret_cast<const float4 *>(j.C + (size_t)u * kD * kD);
-        // 8 elements of a row of C a step, 16 bytes each of high and low terms
-#pragma unroll 4
-        for (int i = 0; i < kD * 16 / 256; i++) {
-            const int e = i * 256 + tid, row = e >> 4, ch = e & 15;
-            const float4 x = C[2 * e], y = C[2 * e + 1];
-            const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int k = 0; k < 4; k++) {
-                hi[k] = pack_bf16(v[2 * k], v[2 * k + 1]);
-                lo[k] = pack_bf16(v[2 * k] - bf_lo(hi[k]), v[2 * k + 1] - bf_hi(hi[k]));
-            }
-            unsigned char *d = cs + sw_off_t<128>(row, ch);
-            *reinterpret_cast<uint4 *>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4 *>(d + kSlot) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
-    }
-    if (mix && tid < kD) {
-        muk[tid] = j.mu_k[(size_t)u * kD + tid];
-        muv[tid] = j.mu_v[(size_t)u * kD + tid];
-    }
-    const size_t ubase = (size_t)u * a.TG + (size_t)rb * kRows;
-    const size_t pbase = ((size_t)item + c0) * a.rows;
-    const int ra[2] = {min(r0 + g, rows - 1), min(r0 + g + 8, rows - 1)};
-    const float2 ml[2] = {a.ml[pbase + ra[0]], a.ml[pbase + ra[1]]};
+    const int g = lane >> 2, t = lane & 3, n0 = 64 * (warp & 1), m0 = 16 * (warp >> 1);
+    const int items = a.U * a.RB, per = (a.rows + kMomRows - 1) / kMomRows;
     const float sd = rsqrtf((float)kD);
-    uint32_t qa[8][4];
-    if (mix) {
-#pragma unroll
-        for (int h = 0; h < 2; h++) {
-            const uint32_t *p = reinterpret_cast<const uint32_t *>(j.q + (ubase + ra[h]) * kD) + t;
-#pragma unroll
-            for (int ks = 0; ks < 8; ks++) {
-                qa[ks][h] = p[8 * ks];
-                qa[ks][2 + h] = p[8 * ks + 4];
-            }
-        }
+    if (tid == 0) {
+        bad = 0;
+        mbar_init(&full[0], 1);
+        mbar_init(&full[1], 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    const int W = a.whole ? 0 : a.first[items];
+    const Cuts cuts(j.grid, a.whole ? items : W);
+    // job -> item, first row, rows; 0 rows: nothing to do
+    auto job_of = [&](int job, int &item, int &u, int &r0, int &nr, int &sid) {
+        item = job / per;
+        u = a.by_rb(item);
+        const int rb = item - u * a.RB;
+        r0 = (job - item * per) * kMomRows;
+        const int n = a.len[u], live = a.live(u);
+        nr = n < 0 || n > a.max_len || live < 0
+                 ? 0 : min(kMomRows, min(kRows, (live << a.gshift) - rb * kRows) - r0);
+        // the part that has the item's start (its place has the joined sums)
+        if (nr > 0) sid = item + cuts.part(a.whole ? item : a.first[item]);
+    };
+    auto load = [&](int job, int st) {
+        int item, u, r0, nr, sid;
+        job_of(job, item, u, r0, nr, sid);
+        if (nr <= 0) {
+            mbar_arrive(&full[st]);
+            return;
+        }
+        const bool mix = j.mn[u] > 0.f, c = mix && j.first_order;
+        unsigned char *d = dyn + st * kMomStage;
+        mbar_expect_tx(&full[st], kMomF + (mix ? kMomQ : 0) + (c ? kMomC : 0));
+        if (c)
+            for (int i = 0; i < 4; i++) tma_3d(d + i * (kMomC / 4), &tmC, 32 * i, 0, u, &full[st]);
+        if (mix)
+            for (int i = 0; i < 2; i++)
+                tma_3d(d + kMomC + i * (kMomQ / 2), &tmQ, 64 * i, (item - u * a.RB) * kRows + r0, u, &full[st]);
+        for (int i = 0; i < 4; i++)
+            tma_3d(d + kMomC + kMomQ + i * (kMomF / 4), &tmF, 32 * i, r0, sid, &full[st]);
+    };
     __syncthreads();
-    float z[2] = {0.f, 0.f};
-    float d[8][4];
+    const int jobs = items * per;
+    if (tid == 0)
+        for (int i = 0; i < 2; i++)
+            if ((int)(blockIdx.x + i * gridDim.x) < jobs) load(blockIdx.x + i * gridDim.x, i);
+    int k = 0;
+    for (int job = blockIdx.x; job < jobs; job += gridDim.x, k++) {
+        const int st = k & 1;
+        int item, u, r0, nr, sid;
+        job_of(job, item, u, r0, nr, sid);
+        const unsigned char *cs = dyn + st * kMomStage, *qs = cs + kMomC, *fs = qs + kMomQ;
+        const float ne = nr > 0 ? j.mn[u] : 0.f;
+        const bool mix = ne > 0.f;
+        float2 ml[2];
+        float z[2] = {0.f, 0.f}, mk[8][4], mv[8][2];
+        if (nr > m0) {
 #pragma unroll
-    for (int i = 0; i < 8; i++) d[i][0] = d[i][1] = d[i][2] = d[i][3] = 0.f;
-    if (mix) {
+            for (int h = 0; h < 2; h++)
+                ml[h] = a.ml[(size_t)sid * a.rows + r0 + min(m0 + g + 8 * h, nr - 1)];
+            if (mix) {
 #pragma unroll
-        for (int ks = 0; ks < 8; ks++)
-#pragma unroll
-            for (int h = 0; h < 4; h++) {
-                const int k = 16 * ks + 8 * (h >> 1) + 2 * t;
-                z[h & 1] += bf_lo(qa[ks][h]) * muk[k] + bf_hi(qa[ks][h]) * muk[k + 1];
-            }
-        if (j.first_order) {
-            // ldmatrix: a quarter-warp has the addresses of rows n0 + 8 i .. + 7 of C
-            // in one 8-column chunk; four chunks are two k-steps
-            const uint32_t base = smem_u32(cs);
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-#pragma unroll
-                for (int k4 = 0; k4 < 4; k4++) {
-                    const uint32_t off = sw_off_t<128>(n0 + 8 * i + (lane & 7), 4 * k4 + (lane >> 3));
-                    uint32_t b[4], c[4];
-                    ldsm_x4(base + kSlot + off, b[0], b[1], b[2], b[3]);
-                    ldsm_x4(base + off, c[0], c[1], c[2], c[3]);
-                    const uint32_t(&q0)[4] = qa[2 * k4], (&q1)[4] = qa[2 * k4 + 1];
-                    mma16816(d[i], q0[0], q0[1], q0[2], q0[3], b[0], b[1]);
-                    mma16816(d[i], q1[0], q1[1], q1[2], q1[3], b[2], b[3]);
-                    mma16816(d[i], q0[0], q0[1], q0[2], q0[3], c[0], c[1]);
-                    mma16816(d[i], q1[0], q1[1], q1[2], q1[3], c[2], c[3]);
+                for (int i = 0; i < 8; i++) {
+                    const float *v = j.mu_v + (size_t)u * kD + n0 + 8 * i + 2 * t;
+                    mv[i][0] = v[0];
+                    mv[i][1] = v[1];
+                    const float *mu = j.mu_k + (size_t)u * kD + 16 * i + 2 * t;
+                    mk[i][0] = mu[0];
+                    mk[i][1] = mu[1];
+                    mk[i][2] = mu[8];
+                    mk[i][3] = mu[9];
                 }
             }
         }
-    }
+        if (!tree_wait(&full[st], (k >> 1) & 1, &bad)) bad = 1;
+        if (nr > m0) {
+            float d[8][4];
 #pragma unroll
-    for (int h = 0; h < 2; h++) {
-        const float lse = ml[h].y == 0.f ? -INFINITY : (ml[h].x + log2f(ml[h].y)) * 0.6931471805599453f;
-        float w = 1.f;
-        if (mix) {
-            float x = z[h];
-            x += __shfl_xor_sync(kFull, x, 1);
-            x += __shfl_xor_sync(kFull, x, 2);
-            w = 1.f / (1.f + expf(logf(ne) + sd * x - lse));
-        }
-        const float wf = ml[h].y == 0.f ? 0.f : w / ml[h].y, we = 1.f - w;
-        const float *p = a.part + (pbase + ra[h]) * kD + n0 + 2 * t;
-        uint32_t *o = reinterpret_cast<uint32_t *>(a.o + (ubase + ra[h]) * kD + n0 + 2 * t);
-        const bool mine = r0 + g + 8 * h < rows;
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const float2 x = *reinterpret_cast<const float2 *>(p + 8 * i);
-            float f0 = wf * x.x, f1 = wf * x.y;
+            for (int i = 0; i < 8; i++) d[i][0] = d[i][1] = d[i][2] = d[i][3] = 0.f;
             if (mix) {
-                f0 += we * (muv[n0 + 8 * i + 2 * t] + sd * d[i][2 * h]);
-                f1 += we * (muv[n0 + 8 * i + 2 * t + 1] + sd * d[i][2 * h + 1]);
+                uint32_t q[8][4];
+#pragma unroll
+                for (int ks = 0; ks < 8; ks++) {
+                    // ldmatrix: rows m0 .. m0 + 15 in the two 8-column chunks of the step
+                    const int row = m0 + (lane & 15), ch = 2 * ks + (lane >> 4);
+                    ldsm_x4(smem_u32(qs) + sw_off_t<64>(row, ch), q[ks][0], q[ks][1], q[ks][2], q[ks][3]);
+                    // q . mu_k of rows g and g + 8
+#pragma unroll
+                    for (int h = 0; h < 4; h++)
+                        z[h & 1] += bf_lo(q[ks][h]) * mk[ks][h & 2] + bf_hi(q[ks][h]) * mk[ks][(h & 2) + 1];
+                }
+                if (j.first_order) {
+#pragma unroll
+                    for (int ks = 0; ks < 8; ks++)
+#pragma unroll
+                        for (int i = 0; i < 8; i++) {
+                            uint32_t hi[2], lo[2];
+#pragma unroll
+                            for (int h = 0; h < 2; h++) {
+                                const float2 x = *reinterpret_cast<const float2 *>(
+                                    cs + mom_off<kD>(n0 + 8 * i + g, 16 * ks + 8 * h + 2 * t));
+                                hi[h] = pack_bf16(x.x, x.y);
+                                lo[h] = pack_bf16(x.x - bf_lo(hi[h]), x.y - bf_hi(hi[h]));
+                            }
+                            mma16816(d[i], q[ks][0], q[ks][1], q[ks][2], q[ks][3], lo[0], lo[1]);
+                            mma16816(d[i], q[ks][0], q[ks][1], q[ks][2], q[ks][3], hi[0], hi[1]);
+                        }
+                }
             }
-            if (mine) o[4 * i] = pack_bf16(f0, f1);
+            const size_t ubase = (size_t)u * a.TG + (size_t)(item - u * a.RB) * kRows + r0;
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const int row = m0 + g + 8 * h;
+                const float lse = ml[h].y == 0.f ? -INFINITY : (ml[h].x + log2f(ml[h].y)) * 0.6931471805599453f;
+                float w = 1.f;
+                if (mix) {
+                    float x = z[h];
+                    x += __shfl_xor_sync(kFull, x, 1);
+                    x += __shfl_xor_sync(kFull, x, 2);
+                    w = 1.f / (1.f + expf(logf(ne) + sd * x - lse));
+                }
+                const float wf = ml[h].y == 0.f ? 0.f : w / ml[h].y, we = 1.f - w;
+                uint32_t *o = reinterpret_cast<uint32_t *>(a.o + (ubase + row) * kD + n0 + 2 * t);
+                if (row < nr && !bad) {
+#pragma unroll
+                    for (int i = 0; i < 8; i++) {
+                        const float2 x = *reinterpret_cast<const float2 *>(
+                            fs + mom_off<kMomRows>(row, n0 + 8 * i + 2 * t));
+                        float f0 = wf * x.x, f1 = wf * x.y;
+                        if (mix) {
+                            f0 += we * (mv[i][0] + sd * d[i][2 * h]);
+                            f1 += we * (mv[i][1] + sd * d[i][2 * h + 1]);
+                        }
+                        o[4 * i] = pack_bf16(f0, f1);
+                    }
+                    if (t == 0 && n0 == 0) a.lse[ubase + row] = lse;
+                }
+            }
         }
-        if (mine && t == 0 && n0 == 0) a.lse[ubase + ra[h]] = lse;
+        __syncthreads();                                     // the stage is read
+        if (bad) {
+            // the copies in flight land before the block ends
+            if (tid == 0) mbar_wait(&full[st ^ 1], ((k + 1) >> 1) & 1);
+            break;
+        }
+        if (tid == 0 && job + 2 * (int)gridDim.x < jobs) load(job + 2 * gridDim.x, st);
     }
+    if (tid == 0 && bad) record_status(a.status, KVC_ERR_TIMEOUT);
 }
 
 struct TreeWs {
@@ -1184,20 +1256,24 @@ cudaError_t launch_tree_attend(const kvc_params &p, int max_len, const TreeArgs 
     kernel<<<(int)grid, kThreads, kDyn, st>>>(a, mk, mv, mq, mkt, mvt);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (m == nullptr && whole) return cudaSuccess;
-    JoinArgs j{a, q, m ? m->n : nullptr, m ? m->mu_k : nullptr, m ? m->mu_v : nullptr,
-               m ? m->C : nullptr, p.correction == KVC_CORR_FIRST_ORDER, (int)grid};
+    JoinArgs j{a, m ? m->n : nullptr, m ? m->mu_k : nullptr, m ? m->mu_v : nullptr,
+               p.correction == KVC_CORR_FIRST_ORDER, (int)grid};
     if (!whole) {
-        const dim3 g((unsigned)grid, (a.rows + 7) / 8);
+        const dim3 g((unsigned)grid, (a.rows + 31) / 32);
         if (m) tree_join_kernel<true><<<g, 256, 0, st>>>(j);
         else tree_join_kernel<false><<<g, 256, 0, st>>>(j);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     if (m) {
+        CUtensorMap mc, mf;
+        if (!make_f32_map(&mc, m->C, p.U, kD, kD) ||
+            !make_f32_map(&mf, w.part, items + kGrid, a.rows, kMomRows))
+            return cudaErrorInvalidValue;
         e = cudaFuncSetAttribute(tree_moment_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)kMomDyn);
         if (e != cudaSuccess) return e;
-        const dim3 g((unsigned)items, (a.rows + kMomRows - 1) / kMomRows);
-        tree_moment_kernel<<<g, 256, kMomDyn, st>>>(j);
+        const long long jobs = items * ((a.rows + kMomRows - 1) / kMomRows);
+        tree_moment_kernel<<<(int)(jobs < kGrid ? jobs : kGrid), 256, kMomDyn, st>>>(j, mq, mc, mf);
     }
     return cudaGetLastError();
 }
