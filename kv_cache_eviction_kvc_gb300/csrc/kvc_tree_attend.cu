@@ -225,6 +225,41 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return r;
 }
 
+// 32 columns of 16 lanes: thread t has columns 8 b + 2 (t % 4) and the next of
+// lane t / 4 in r[4 b], r[4 b + 1], and of lane t / 4 + 8 in the two after.
+__device__ __forceinline__ void tmem_ld_16x256(uint32_t addr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(addr)
+        : "memory");
+}
+
+// Pairs f[2 j], f[2 j + 1] of the four lanes of a quad as a 4 x 4 matrix,
+// transposed: lane i's pair j becomes lane j's pair i.
+__device__ __forceinline__ void quad_transpose(float (&f)[8], int lane)
+{
+#pragma unroll
+    for (int s = 1; s < 4; s <<= 1) {
+        const bool up = lane & s;
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            if (j & s) continue;
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                float &x = f[2 * j + e], &y = f[2 * (j + s) + e];
+                const float got = __shfl_xor_sync(kFull, up ? x : y, s);
+                if (up) x = got;
+                else y = got;
+            }
+        }
+    }
+}
+
 // 32-byte stores: a whole sector per lane.
 __device__ __forceinline__ void st_v8(void *p, const uint32_t *r)
 {
@@ -873,51 +908,64 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
             }
             const uint64_t by_hand = has_tree ? S.odd[s.trees & 1] & see : 0;
             // a group writes its rows whole, or (alternate tiles) half of the columns
-            const int q0 = dual ? 0 : 4 * w, q1 = dual ? 8 : q0 + 4;
+            const int q0 = dual ? 0 : 2 * w, q1 = dual ? 4 : q0 + 2;
             const bool two = !dual && nq > 1, mine = row < rows;
             if (busy) {
+                // 32 columns of 16 rows at a time, in the layout that gives a thread two
+                // columns of every eight; a transposition in each quad of lanes leaves it
+                // eight in a row, so that a store covers whole lines
+                const uint32_t t0 = tmem + lanes + (dual ? 128 * w : 0);
 #pragma unroll 1
-                for (int q = q0; q < q1; q++) {              // 16 columns at a time
+                for (int q = 2 * q0; q < 2 * q1; q++) {
+                    const int h = q & 1, col = 32 * (q >> 1) + 8 * (lane & 3);
                     uint32_t y[16], z[16];
-                    tmem_ld16_async(tmem + lanes + (dual ? 128 * w : 0) + 16 * q, y);
-                    if (two) tmem_ld16_async(tmem + lanes + 128 + 16 * q, z);
+                    tmem_ld_16x256(t0 + ((uint32_t)(16 * h) << 16) + 32 * (q >> 1), y);
+                    if (two) tmem_ld_16x256(tmem + lanes + 128 + ((uint32_t)(16 * h) << 16) + 32 * (q >> 1), z);
                     tmem_wait_ld();
                     tmem_bind16(y);
-                    float f[16];
+                    if (two) tmem_bind16(z);
 #pragma unroll
-                    for (int j = 0; j < 16; j++) f[j] = __uint_as_float(y[j]) * c0;
-                    if (two) {
-                        tmem_bind16(z);
+                    for (int k = 0; k < 2; k++) {            // rows (lane / 4) and 8 more
+                        const int of = 16 * h + 8 * k + (lane >> 2), r2 = row - lane + of;
+                        const float a0 = __shfl_sync(kFull, c0, of), a1 = __shfl_sync(kFull, c1, of);
+                        float f[8];
 #pragma unroll
-                        for (int j = 0; j < 16; j++) f[j] = fmaf(__uint_as_float(z[j]), c1, f[j]);
-                    }
-                    if (mine) {
+                        for (int j = 0; j < 4; j++)
+#pragma unroll
+                            for (int e = 0; e < 2; e++) {
+                                f[2 * j + e] = __uint_as_float(y[4 * j + 2 * k + e]) * a0;
+                                if (two) f[2 * j + e] = fmaf(__uint_as_float(z[4 * j + 2 * k + e]), a1, f[2 * j + e]);
+                            }
+                        quad_transpose(f, lane);
+                        if (r2 >= rows) continue;
                         if (direct) {
-                            uint4 *d = reinterpret_cast<uint4 *>(a.o + orow * kD + 16 * q);
-                            d[0] = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
-                                              pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
-                            d[1] = make_uint4(pack_bf16(f[8], f[9]), pack_bf16(f[10], f[11]),
-                                              pack_bf16(f[12], f[13]), pack_bf16(f[14], f[15]));
+                            *reinterpret_cast<uint4 *>(a.o + (orow - lane + of) * kD + col) =
+                                make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
+                                           pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
                         } else {
-                            float *d = a.part + part * kD + 16 * q;
-                            st_v8(d, reinterpret_cast<const uint32_t *>(f));
-                            st_v8(d + 8, reinterpret_cast<const uint32_t *>(f + 8));
+                            st_v8(a.part + (part - lane + of) * kD + col, reinterpret_cast<const uint32_t *>(f));
                         }
                     }
                 }
                 // drafted tokens that the row sees and whose value is not finite: whatever
                 // their weight, the output of such a column is not finite
-                if (mine)
-                    for (uint64_t rest = by_hand; rest; rest &= rest - 1) {
-                        const uint16_t *vr = a.vt + ((size_t)u * a.t.T + __ffsll((long long)rest) - 1) * kD;
+                if (__any_sync(kFull, by_hand != 0)) {
+                    __syncwarp();                            // what other lanes wrote of this row
+                    if (mine)
+                        for (uint64_t rest = by_hand; rest; rest &= rest - 1) {
+                            const uint16_t *vr =
+                                a.vt + ((size_t)u * a.t.T + __ffsll((long long)rest) - 1) * kD;
 #pragma unroll 1
-                        for (int c = 16 * q0; c < 16 * q1; c++) {
-                            const float v = bf2f(vr[c]);
-                            if (isfinite(v)) continue;
-                            if (direct) a.o[orow * kD + c] = pack_bf16(bf2f(a.o[orow * kD + c]) + v, 0.f);
-                            else a.part[part * kD + c] += v;
+                            for (int c = 32 * q0; c < 32 * q1; c++) {
+                                const float v = bf2f(vr[c]);
+                                if (isfinite(v)) continue;
+                                volatile uint16_t *o = a.o + orow * kD + c;
+                                volatile float *p = a.part + part * kD + c;
+                                if (direct) *o = (uint16_t)pack_bf16(bf2f(*o) + v, 0.f);
+                                else *p = *p + v;
+                            }
                         }
-                    }
+                }
                 if (mine && (dual || w == 0)) {
                     if (direct)
                         a.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
@@ -943,36 +991,38 @@ struct JoinArgs {
     int first_order, grid;
 };
 
-// The sums of a cut item's parts added.  A warp has four rows, a lane four of
+// The sums of a cut item's parts added.  A warp has two rows, a lane four of
 // their columns; the loads of four parts are in flight together.  The result
 // is the output, or (kKeep, when the moments follow) the first part's place
-// takes it.  grid (CTAs of the attention, rows / 32): block x takes the item
+// takes it.  grid (CTAs of the attention, rows / 16): block x takes the item
 // whose first cut is the start of part x.
+constexpr int kJoinRows = 2;
+
 template <bool kKeep>
 __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ JoinArgs j)
 {
     const AttArgs &a = j.a;
     const int4 cut = a.cut[blockIdx.x];                     // item, first and last part, rows
-    const int lane = threadIdx.x & 31, r0 = blockIdx.y * 32 + 4 * (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, r0 = kJoinRows * (blockIdx.y * 8 + (threadIdx.x >> 5));
     if (cut.x < 0 || r0 >= cut.w) return;
-    const int nr = min(4, cut.w - r0), np = cut.z - cut.y + 1;
+    const int nr = min(kJoinRows, cut.w - r0), np = cut.z - cut.y + 1;
     const size_t at = ((size_t)cut.x + cut.y) * a.rows + r0, step = (size_t)a.rows;
-    float M[4], L[4];
-    float4 f[4];
+    float M[kJoinRows], L[kJoinRows];
+    float4 f[kJoinRows];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
+    for (int i = 0; i < kJoinRows; i++) {
         M[i] = -INFINITY;
         L[i] = 0.f;
         f[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     for (int k0 = 0; k0 < np; k0 += 4) {
         // places past the last part or row are read again and weigh nothing
-        float2 ml[4][4];
-        float4 p[4][4];
+        float2 ml[4][kJoinRows];
+        float4 p[4][kJoinRows];
 #pragma unroll
         for (int k = 0; k < 4; k++)
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
+            for (int i = 0; i < kJoinRows; i++) {
                 const size_t x = at + min(k0 + k, np - 1) * step + min(i, nr - 1);
                 ml[k][i] = a.ml[x];
                 p[k][i] = reinterpret_cast<const float4 *>(a.part + x * kD)[lane];
@@ -980,11 +1030,10 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
 #pragma unroll
         for (int k = 0; k < 4; k++)
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const float m = fmaxf(M[i], ml[k][i].x), ref = m == -INFINITY ? 0.f : m;
-                const float c = ex2_approx(M[i] - ref);
+            for (int i = 0; i < kJoinRows; i++) {
                 if (k0 + k >= np) continue;
-                const float e = ex2_approx(ml[k][i].x - ref);
+                const float m = fmaxf(M[i], ml[k][i].x), ref = m == -INFINITY ? 0.f : m;
+                const float c = ex2_approx(M[i] - ref), e = ex2_approx(ml[k][i].x - ref);
                 M[i] = m;
                 L[i] = fmaf(L[i], c, ml[k][i].y * e);
                 f[i].x = fmaf(f[i].x, c, p[k][i].x * e);
@@ -997,7 +1046,7 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
     const size_t row = (size_t)u * a.TG + (size_t)rb * kRows + r0;
     if (kKeep) __syncwarp();                                // all lanes have read ml
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
+    for (int i = 0; i < kJoinRows; i++) {
         if (i >= nr) break;
         if (kKeep) {
             reinterpret_cast<float4 *>(a.part + (at + i) * kD)[lane] = f[i];
@@ -1259,7 +1308,7 @@ cudaError_t launch_tree_attend(const kvc_params &p, int max_len, const TreeArgs 
     JoinArgs j{a, m ? m->n : nullptr, m ? m->mu_k : nullptr, m ? m->mu_v : nullptr,
                p.correction == KVC_CORR_FIRST_ORDER, (int)grid};
     if (!whole) {
-        const dim3 g((unsigned)grid, (a.rows + 31) / 32);
+        const dim3 g((unsigned)grid, (a.rows + 8 * kJoinRows - 1) / (8 * kJoinRows));
         if (m) tree_join_kernel<true><<<g, 256, 0, st>>>(j);
         else tree_join_kernel<false><<<g, 256, 0, st>>>(j);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
