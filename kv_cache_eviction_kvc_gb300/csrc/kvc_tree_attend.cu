@@ -639,12 +639,19 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                     // an item of two halves takes both, whichever was last
                     load_q(i & 1, s.u, qrow, s.rows);
                 }
-                for (int t = s.t0; ok && t < s.t1; t++) {
+                auto load_tile = [&](bool keys, int t) {
                     const bool tree = t == s.nt - 1;
                     const int nv = tree ? 64 : s.n - t * kTile, row = tree ? 0 : t * kTile;
-                    const bool stream = !tree && a.RB == 1;
-                    load(tree ? &tmKt : &tmK, s.u, row, nv, stream);
-                    load(tree ? &tmVt : &tmV, s.u, row, nv, stream);
+                    load(keys ? (tree ? &tmKt : &tmK) : (tree ? &tmVt : &tmV), s.u, row, nv,
+                         !tree && a.RB == 1);
+                };
+                // in the order of their use, so that no tile waits in the ring for
+                // one behind it: alternate tiles have two S before the first O
+                const int ahead = s.rows > 128 ? 1 : 2, nq = s.t1 - s.t0;
+                for (int t = 0; ok && t < nq + ahead; t++) {
+                    if (ahead == 2 && t >= ahead) load_tile(false, s.t0 + t - ahead);
+                    if (t < nq) load_tile(true, s.t0 + t);
+                    if (ahead == 1 && t < nq) load_tile(false, s.t0 + t);
                 }
             }
             if (!ok) {
@@ -661,18 +668,22 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
         // ------------------------------------------------------ MMA issuer
         if (elect_one()) {
             bool ok = true;
-            // slot and phase of the ring's next key and value tile; phases of
-            // the groups' barriers as bits
-            int ks_slot = 0, vs_slot = 1;
-            uint32_t ks_ph = 0, vs_ph = 0, q_ph = 0, p_ph = 0;
+            // next ring entry and its phase; the entries in use by S and by O
+            int slot = 0, ks_slot = 0, vs_slot = 0;
+            uint32_t ph = 0, q_ph = 0, p_ph = 0;             // phases; the groups' as bits
             const uint64_t q0 = umma_sdesc(smem_u32(qbuf)), k0 = umma_sdesc(smem_u32(ring));
             const uint64_t v0 = v_desc(smem_u32(ring));
             constexpr uint32_t kStep = kSlot >> 4;           // a slot in descriptor units
+            auto take = [&](int &of) {                       // the next entry, once it is there
+                ok = ok && tree_wait(&S.full[slot], ph, &S.bad);
+                of = slot;
+                if (++slot == kRing) { slot = 0; ph ^= 1; }
+            };
             // S of group w; the key tile is waited for by its first reader
             // and given back by its last
             auto issue_s = [&](uint32_t w, uint32_t half, bool small, bool first, bool last,
                                bool last_q) {
-                if (first) ok = ok && tree_wait(&S.full[ks_slot], ks_ph, &S.bad);
+                if (first) take(ks_slot);
                 if (!ok) return;
                 tc_fence_after();
                 const uint32_t idesc = small ? kIdescS64 : kIdescS, d = tmem + kColS + 128 * w;
@@ -681,15 +692,11 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                 for (int ks = 0; ks < 8; ks++)
                     umma_bf16(d, umma_sdesc_step(qd, ks), umma_sdesc_step(kd, ks), idesc, ks > 0);
                 umma_commit(&S.sfull[w]);
+                if (last) umma_commit(&S.empty[ks_slot]);
                 if (last_q) umma_commit(&S.qempty[half]);
-                if (last) {
-                    umma_commit(&S.empty[ks_slot]);
-                    ks_slot += 2;
-                    if (ks_slot >= kRing) { ks_slot -= kRing; ks_ph ^= 1; }
-                }
             };
             auto issue_o = [&](uint32_t w, int nv, bool first, bool last, bool keep) {
-                if (first) ok = ok && tree_wait(&S.full[vs_slot], vs_ph, &S.bad);
+                if (first) take(vs_slot);
                 ok = ok && tree_wait(&S.pready[w], p_ph >> w & 1, &S.bad);
                 p_ph ^= 1u << w;
                 if (!ok) return;
@@ -707,11 +714,7 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                                 kIdescO, ks > 0 || keep);
                 }
                 umma_commit(&S.pvdone[w]);
-                if (last) {
-                    umma_commit(&S.empty[vs_slot]);
-                    vs_slot += 2;
-                    if (vs_slot >= kRing) { vs_slot -= kRing; vs_ph ^= 1; }
-                }
+                if (last) umma_commit(&S.empty[vs_slot]);
             };
             auto wait_q = [&](uint32_t half) {
                 ok = ok && tree_wait(&S.qfull[half], q_ph >> half & 1, &S.bad);
@@ -822,7 +825,9 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                 }
                 // value rows the MMA reads that are no slot: zero
                 if ((tree || nv & 15) && (!dual || w == 0)) {
-                    const int kv = 2 * (s.k0 + tile - s.t0) + 1, slot = kv % kRing;
+                    const int t = tile - s.t0;
+                    const int kv = 2 * s.k0 + t + (dual ? t + 1 : min(t + 2, s.t1 - s.t0));
+                    const int slot = kv % kRing;
                     wait(&S.full[slot], (kv / kRing) & 1);
                     if (!ok) break;
                     unsigned char *v = ring + slot * kSlot;
