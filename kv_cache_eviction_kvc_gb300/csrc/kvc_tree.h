@@ -8,6 +8,7 @@
 #include "kvc_common.cuh"
 #include "kvc_internal.h"
 #include "kvc_tma.cuh"
+#include "kvc_umma.cuh"
 
 namespace kvc {
 
@@ -45,6 +46,83 @@ __device__ __forceinline__ int path_count(const TreeArgs &t, const PathArgs &p, 
         bad |= c < 0 || c >= live;
     }
     return __any_sync(kFull, bad) ? -1 : a;
+}
+
+// x / d for 0 <= x < 2^31 as a multiplication (Granlund and Montgomery, 1994)
+struct FastDiv {
+    uint32_t mul, shift;
+    FastDiv(uint32_t d = 1)
+    {
+        shift = 0;
+        while ((1u << shift) < d) shift++;               // d <= 2^31
+        mul = (uint32_t)(((1ull << 32) * ((1ull << shift) - d)) / d + 1);
+    }
+    __device__ __forceinline__ int operator()(int x) const
+    {
+        return (int)((__umulhi((uint32_t)x, mul) + (uint32_t)x) >> shift);
+    }
+};
+
+// The line of `total` tiles is cut into min(grid, total) parts, the first
+// total % parts of them one tile longer.
+struct LineCuts {
+    int parts, q, rem;
+    __device__ __forceinline__ LineCuts(int grid, int total)
+        : parts(min(grid, total)), q(parts ? (uint32_t)total / (uint32_t)parts : 0), rem(total - q * parts)
+    {
+    }
+    __device__ __forceinline__ int start(int c) const { return c * q + min(c, rem); }
+    __device__ __forceinline__ int part(int tile) const        // that has the tile
+    {
+        const int longer = rem * (q + 1);
+        return tile < longer ? (uint32_t)tile / (uint32_t)(q + 1)
+                             : rem + (int)((uint32_t)(tile - longer) / (uint32_t)q);
+    }
+};
+
+// True on one lane of a converged warp; the compiler keeps what the branch
+// issues (descriptors and all) in uniform registers.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
+
+// Bounded wait.  Once one has run out every wait ends at once and each role
+// leaves its loop (all synchronisation among them is by such waits).
+__device__ __forceinline__ bool tree_wait(uint64_t *b, uint32_t parity, volatile int *bad)
+{
+    if (mbar_try_wait(b, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_try_wait(b, parity)) {
+        if (*bad) return false;
+        if (clock64() - t0 > kWaitCycles) {
+            *bad = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
+__device__ __forceinline__ void tmem_ld16_async(uint32_t addr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(addr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_bind16(uint32_t (&r)[16])
+{
+    asm volatile(""
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                   "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                   "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
 
 // 3D copies of a box of 64 columns x 64 rows of one unit.

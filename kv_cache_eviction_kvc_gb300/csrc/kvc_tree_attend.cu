@@ -66,21 +66,6 @@ constexpr uint32_t kIdescS = umma_idesc_bf16(128, 128);
 constexpr uint32_t kIdescS64 = umma_idesc_bf16(128, 64);
 constexpr uint32_t kIdescO = umma_idesc_bf16(128, 128) | (1u << 16);   // B (values) MN-major
 
-// x / d for 0 <= x < 2^31 as a multiplication (Granlund and Montgomery, 1994)
-struct FastDiv {
-    uint32_t mul, shift;
-    explicit FastDiv(uint32_t d = 1)
-    {
-        shift = 0;
-        while ((1u << shift) < d) shift++;               // d <= 2^31
-        mul = (uint32_t)(((1ull << 32) * ((1ull << shift) - d)) / d + 1);
-    }
-    __device__ __forceinline__ int operator()(int x) const
-    {
-        return (int)((__umulhi((uint32_t)x, mul) + (uint32_t)x) >> shift);
-    }
-};
-
 struct AttArgs {
     TreeArgs t;
     const int32_t *votes, *len;
@@ -130,31 +115,6 @@ struct AttSmem {
     uint32_t tmem;
 };
 
-// True on one lane of a converged warp; the compiler keeps what the branch
-// issues (descriptors and all) in uniform registers.
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t p;
-    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
-    return p != 0;
-}
-
-// Bounded wait.  Once one has run out every wait ends at once and each role
-// leaves its loop (all synchronisation among them is by such waits).
-__device__ __forceinline__ bool tree_wait(uint64_t *b, uint32_t parity, volatile int *bad)
-{
-    if (mbar_try_wait(b, parity)) return true;
-    const long long t0 = clock64();
-    while (!mbar_try_wait(b, parity)) {
-        if (*bad) return false;
-        if (clock64() - t0 > kWaitCycles) {
-            *bad = 1;
-            return false;
-        }
-    }
-    return true;
-}
-
 // Everything is dynamic shared memory: the tiles fill all of it but 3 KB.
 constexpr size_t kDyn = (size_t)(2 + kRing) * kSlot + sizeof(AttSmem);
 static_assert(kDyn <= 227 * 1024, "one block's shared memory");
@@ -191,26 +151,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
-}
-
-__device__ __forceinline__ void tmem_ld16_async(uint32_t addr, uint32_t (&r)[16])
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-        "%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15])
-        : "r"(addr)
-        : "memory");
-}
-
-__device__ __forceinline__ void tmem_bind16(uint32_t (&r)[16])
-{
-    asm volatile(""
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
-                   "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
-                   "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
 
 __device__ __forceinline__ void tmem_wait_st()
@@ -282,23 +222,6 @@ __device__ __forceinline__ void check_unit(const AttArgs &a, int u)
     if (live < 0) record_status(a.status, KVC_ERR_INVALID_ARG);
     else if (n < 0 || n > a.max_len) record_status(a.status, KVC_ERR_SHAPE);
 }
-
-// The line of `total` tiles is cut into min(grid, total) parts, the first
-// total % parts of them one tile longer.
-struct Cuts {
-    int parts, q, rem;
-    __device__ __forceinline__ Cuts(int grid, int total)
-        : parts(min(grid, total)), q(parts ? (uint32_t)total / (uint32_t)parts : 0), rem(total - q * parts)
-    {
-    }
-    __device__ __forceinline__ int start(int c) const { return c * q + min(c, rem); }
-    __device__ __forceinline__ int part(int tile) const        // that has the tile
-    {
-        const int longer = rem * (q + 1);
-        return tile < longer ? (uint32_t)tile / (uint32_t)(q + 1)
-                             : rem + (int)((uint32_t)(tile - longer) / (uint32_t)q);
-    }
-};
 
 // valid slots of tile t (the drafted tokens' tile: the live ones)
 __device__ __forceinline__ int tile_valid(const Seg &s, int t)
@@ -490,7 +413,7 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
     int item0, item1, base0, lo, hi;
     if (a.whole) {
         // parts of whole items: nothing to count, nothing to join
-        const Cuts c(gridDim.x, items);
+        const LineCuts c(gridDim.x, items);
         item0 = c.start(blockIdx.x);
         item1 = c.start(blockIdx.x + 1);
         base0 = lo = 0;
@@ -518,7 +441,7 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
         const int of = lane < kThreads / 32 ? S.scan[lane] : 0;
         const int total = warp_isum(of);
         int b = incl - sum + warp_isum(lane < warp ? of : 0);
-        const Cuts c(gridDim.x, total);
+        const LineCuts c(gridDim.x, total);
         const int bid = min((int)blockIdx.x, c.parts);
         lo = c.start(bid);
         hi = c.start(min(bid + 1, c.parts));
@@ -1109,7 +1032,7 @@ tree_moment_kernel(const __grid_constant__ JoinArgs j, const __grid_constant__ C
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     const int W = a.whole ? 0 : a.first[items];
-    const Cuts cuts(j.grid, a.whole ? items : W);
+    const LineCuts cuts(j.grid, a.whole ? items : W);
     // job -> item, first row, rows; 0 rows: nothing to do
     auto job_of = [&](int job, int &item, int &u, int &r0, int &nr, int &sid) {
         item = job / per;

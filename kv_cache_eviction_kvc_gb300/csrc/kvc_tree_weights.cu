@@ -1,54 +1,457 @@
 // kvc_tree_weights.cu -- the attention weight that the accepted tokens gave
 // to every slot of the cache and to the accepted tokens themselves.
 //
-// One thread per slot (the accepted tokens behind the cache's), over the
-// accepted tokens and heads.
+// The sum runs over the query rows (accepted token, head), so the product is
+// taken the other way round from the attention: D = K Q^T (tcgen05), 128
+// slots on the tensor-memory lanes, the rows along the columns.  A thread has
+// a slot and adds its columns up: no exchange between threads, no maximum (the
+// lse is known), S written in whole lines.  exp(x - lse) w / G is one
+// exponential, exp2(x' - c_row) with c_row = lse log2(e) - log2(w / G).
+//
+// Bound by the 256 bytes of key per slot up to about 128 rows (128 x 128
+// exponentials take 512 clocks of the special-function units, a tile's 32 KB
+// about 1200 of one SM's share of the bandwidth).  The 128-slot tiles of all
+// units form one line, cut into equal parts for a persistent CTA per SM; every
+// tile stands alone, so nothing is joined.
+//
+// 416 threads:
+//   warps 0-7   two groups on alternate tiles, a thread per slot
+//   warp 8      producer (TMA, a ring of 32 KB key tiles)
+//   warp 9      tensor-memory owner and MMA issuer (up to four tiles ahead)
+//   warp 10     walks the CTA's units ahead of the others
+//   warp 11     gathers a unit's accepted rows of q (two buffers when they fit)
+//   warp 12     the accepted tokens' own entries, a few dot products per unit
+//               (mma.sync), unit by unit over the grid
+// Every wait is bounded (~2 s); a wait that ran out records KVC_ERR_TIMEOUT.
 #include "kvc_tree.h"
+#include "kvc_umma.cuh"
+
+#include <stddef.h>
 
 namespace kvc {
 namespace {
+
+constexpr int kTile = 128;
+constexpr int kSlot = kTile * kD * 2;            // 32 KB: a tile of keys
+constexpr int kHalf = kSlot / 2;
+constexpr int kMaxRing = 6, kSegs = 3, kMaxRows = kTreeMax * 8;
+constexpr int kThreads = 416;
+constexpr int kProd = 8, kMma = 9, kWalk = 10, kGather = 11, kTail = 12;
+constexpr int kGrid = 152;
+constexpr float kLog2e = 1.4426950408889634f;
 
 struct WtArgs {
     TreeArgs t;
     PathArgs p;
     const float *w;
-    const uint16_t *q, *kt, *K;
+    const uint16_t *q, *kt;
     const float *lse;
     const int32_t *votes, *len;
     float *S;
     int32_t *status;
-    int G, cap, max_len;
+    int U, G, cap, max_len;
+    int rows, qbufs, ring, dbufs, dcols;   // rows of q per buffer (a multiple of 16); tiles in flight
+    FastDiv by_units;
+    float scale;                           // log2(e) / sqrt(d)
 };
 
-__global__ void __launch_bounds__(256) tree_weights_kernel(WtArgs a)
+// The tiles of a unit that this CTA takes; tiles = 0: there is none left.
+struct __align__(16) Seg {
+    int u, n, t0, tiles, acc, b;
+};
+
+struct WtSmem {
+    float c[2][kMaxRows];                  // c_row of a buffer's rows; read as float4
+    Seg seg[kSegs];
+    uint64_t full[kMaxRing], empty[kMaxRing];
+    uint64_t segfull[kSegs], segempty[kSegs];
+    uint64_t qfull[2], qempty[2], dfull[4], dempty[4];
+    uint64_t drain;
+    int scan[kThreads / 32];
+    int start_unit, start_base;
+    int bad;
+    uint32_t tmem;
+};
+constexpr size_t kCtl = sizeof(WtSmem) + 1024;
+
+// Accepted tokens of unit u, or -1 when the unit is refused.
+__device__ __forceinline__ int unit_acc(const WtArgs &a, int u, int n, int32_t *err)
 {
-    const int u = blockIdx.y, i = blockIdx.x * 256 + threadIdx.x, b = u / a.t.units;
-    const int n = a.len[u], acc = path_count(a.t, a.p, u, threadIdx.x & 31);
-    if (n < 0 || n > a.max_len || acc < 0 || n + acc > a.cap) {
-        if (i == 0) record_status(a.status, acc < 0 ? KVC_ERR_INVALID_ARG : KVC_ERR_SHAPE);
+    const int b = a.by_units(u);
+    const int live = a.t.n ? a.t.n[b] : a.t.T, acc = a.p.n[b];
+    *err = KVC_ERR_INVALID_ARG;
+    if (live < 0 || live > a.t.T || acc < 0 || acc > a.p.A) return -1;
+    for (int j = 0; j < acc; j++) {
+        const int c = a.p.token[(size_t)b * a.p.A + j];
+        if (c < 0 || c >= live) return -1;
+    }
+    *err = KVC_ERR_SHAPE;
+    if (n < 0 || n > a.max_len || n + acc > a.cap) return -1;
+    return acc;
+}
+
+__device__ __forceinline__ int unit_tiles(const WtArgs &a, int u)
+{
+    int32_t err;
+    const int n = a.len[u];
+    return unit_acc(a, u, n, &err) < 0 ? 0 : (n + kTile - 1) >> 7;
+}
+
+// c_row: a row that weighs nothing (or saw nothing) has +inf.
+__device__ __forceinline__ float row_c(const WtArgs &a, size_t qrow, int b, int j)
+{
+    const float lse = a.lse[qrow];
+    const float w = (a.w ? a.w[(size_t)b * a.p.A + j] : 1.f) / (float)a.G;
+    return lse == -INFINITY ? INFINITY : lse * kLog2e - log2f(w);
+}
+
+// exp2(x - c_row); nothing for a row of c = +inf, whatever its product is.
+__device__ __forceinline__ float weight(uint32_t x, float scale, float c)
+{
+    const float e = ex2_approx(fmaf(__uint_as_float(x), scale, -c));
+    return c == INFINITY ? 0.f : e;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+tree_weights_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUtensorMap tmK)
+{
+    extern __shared__ __align__(1024) unsigned char dyn[];
+    const uint32_t qbytes = (uint32_t)a.rows * 256;      // a buffer: two halves of 64 columns
+    unsigned char *ring = dyn, *qbuf = dyn + a.ring * kSlot;
+    WtSmem &S = *reinterpret_cast<WtSmem *>(qbuf + a.qbufs * qbytes);
+    if (smem_u32(dyn) & 1023) {                          // the swizzle counts on it
+        if (threadIdx.x == 0) record_status(a.status, KVC_ERR_CUDA);
         return;
     }
-    if (i >= n + acc) return;
-    const int32_t *tok = a.p.token + (size_t)b * a.p.A;
-    const size_t tb = (size_t)u * a.t.T, slot = (size_t)u * a.cap + i;
-    const bool old = i < n;
-    const int self = old ? 0 : tok[i - n];
-    const uint16_t *k = old ? a.K + slot * kD : a.kt + (tb + self) * kD;
-    const float scale = rsqrtf((float)kD);
-    float s = 0.f;
-    for (int j = 0; j < acc; j++) {
-        const int c = tok[j];
-        if (!old && !(a.t.mask[(size_t)b * a.t.T + c] >> self & 1)) continue;
-        const float w = a.w ? a.w[(size_t)b * a.p.A + j] : 1.f;
-        for (int h = 0; h < a.G; h++) {
-            const size_t qr = (tb + c) * a.G + h;
-            float x = 0.f;
-            for (int d = 0; d < kD; d++) x += bf2f(a.q[qr * kD + d]) * bf2f(k[d]);
-            const float lse = a.lse[qr];
-            if (lse != -INFINITY) s += w / a.G * expf(x * scale - lse);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (warp == kProd && lane == 0)
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmK)) : "memory");
+    if (tid == 0) {
+        S.bad = 0;
+        for (int i = 0; i < kMaxRing; i++) {
+            mbar_init(&S.full[i], 1);
+            mbar_init(&S.empty[i], 1);
+        }
+        for (int i = 0; i < kSegs; i++) {
+            mbar_init(&S.segfull[i], 1);
+            mbar_init(&S.segempty[i], 11);       // eight slot warps, producer, issuer, gatherer
+        }
+        for (int i = 0; i < 2; i++) {
+            mbar_init(&S.qfull[i], 1);
+            mbar_init(&S.qempty[i], 9);          // eight slot warps, issuer
+        }
+        for (int i = 0; i < 4; i++) {
+            mbar_init(&S.dfull[i], 1);
+            mbar_init(&S.dempty[i], 4);
+        }
+        mbar_init(&S.drain, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kMma) tmem_alloc(&S.tmem, 512);
+
+    // the line of tiles: every CTA counts it and finds where its part starts
+    int lo, hi;
+    {
+        const int per = (a.U + kThreads - 1) / kThreads;
+        const int u0 = min(a.U, tid * per), u1 = min(a.U, u0 + per);
+        int sum = 0;
+        for (int u = u0; u < u1; u++) {
+            sum += unit_tiles(a, u);
+            int32_t err;
+            if (blockIdx.x == 0 && unit_acc(a, u, a.len[u], &err) < 0) record_status(a.status, err);
+        }
+        int incl = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int t = __shfl_up_sync(kFull, incl, d);
+            if (lane >= d) incl += t;
+        }
+        if (lane == 31) S.scan[warp] = incl;
+        __syncthreads();
+        const int of = lane < kThreads / 32 ? S.scan[lane] : 0;
+        const int total = warp_isum(of);
+        int b = incl - sum + warp_isum(lane < warp ? of : 0);
+        const LineCuts c(gridDim.x, total);
+        const int bid = min((int)blockIdx.x, c.parts);
+        lo = c.start(bid);
+        hi = c.start(min(bid + 1, c.parts));
+        if (sum > 0 && lo < b + sum && lo >= b)
+            for (int u = u0; u < u1; u++) {
+                const int nt = unit_tiles(a, u);
+                if (lo >= b && lo < b + nt) {
+                    S.start_unit = u;
+                    S.start_base = b;
+                }
+                b += nt;
+            }
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = S.tmem;
+
+    if (warp == kWalk) {
+        // --------------------------------------------------------- walker
+        if (elect_one()) {
+            int u = lo < hi ? S.start_unit : a.U, base = S.start_base;
+            bool ok = true;
+            for (int i = 0; ok;) {
+                Seg s;
+                s.tiles = 0;
+                if (u < a.U && base < hi) {
+                    int32_t err;
+                    s.u = u;
+                    s.n = a.len[u];
+                    s.b = a.by_units(u);
+                    s.acc = unit_acc(a, u, s.n, &err);
+                    const int nt = s.acc < 0 ? 0 : (s.n + kTile - 1) >> 7;
+                    s.t0 = max(0, lo - base);
+                    s.tiles = min(nt, hi - base) - s.t0;
+                    base += nt;
+                    u++;
+                    if (s.tiles <= 0) continue;
+                }
+                if (i >= kSegs) ok = tree_wait(&S.segempty[i % kSegs], (i / kSegs - 1) & 1, &S.bad);
+                if (!ok) break;
+                S.seg[i % kSegs] = s;
+                mbar_arrive(&S.segfull[i % kSegs]);
+                i++;
+                if (s.tiles == 0) break;
+            }
+        }
+        __syncwarp();
+    } else if (warp == kProd) {
+        // ------------------------------------------------------- producer
+        if (elect_one()) {
+            int k = 0, slot = 0;
+            uint32_t ph = 1;
+            bool ok = true;
+            const uint64_t pol = l2_policy_evict_first();
+            for (int i = 0; ok; i++) {
+                ok = tree_wait(&S.segfull[i % kSegs], (i / kSegs) & 1, &S.bad);
+                if (!ok) break;
+                const Seg s = S.seg[i % kSegs];
+                mbar_arrive(&S.segempty[i % kSegs]);
+                if (s.tiles == 0) break;
+                for (int t = s.t0; t < s.t0 + s.tiles; t++) {
+                    if (k >= a.ring) ok = tree_wait(&S.empty[slot], ph, &S.bad);
+                    if (!ok) break;
+                    unsigned char *d = ring + slot * kSlot;
+                    const int boxes = s.n - t * kTile > 64 ? 2 : 1;
+                    mbar_expect_tx(&S.full[slot], boxes * kHalf);
+#pragma unroll
+                    for (int h = 0; h < 2; h++)
+                        for (int b = 0; b < boxes; b++)
+                            tma_3d_hint(d + h * kHalf + b * (kHalf / 2), &tmK, 64 * h, t * kTile + 64 * b,
+                                        s.u, &S.full[slot], pol);
+                    k++;
+                    if (++slot == a.ring) { slot = 0; ph ^= 1; }
+                }
+            }
+            if (!ok) {
+                S.bad = 1;
+                // the copies in flight land before the block ends
+                for (int i = max(0, k - a.ring); i < k; i++)
+                    mbar_wait(&S.full[i % a.ring], (i / a.ring) & 1);
+            }
+        }
+        __syncwarp();
+    } else if (warp == kMma) {
+        // ------------------------------------------------------ MMA issuer
+        if (elect_one()) {
+            bool ok = true;
+            int slot = 0, db = 0, k = 0;
+            uint32_t ph = 0, dph = 1;
+            const uint64_t k0 = umma_sdesc(smem_u32(ring)), q0 = umma_sdesc(smem_u32(qbuf));
+            for (int i = 0; ok; i++) {
+                ok = tree_wait(&S.segfull[i % kSegs], (i / kSegs) & 1, &S.bad);
+                if (!ok) break;
+                const Seg s = S.seg[i % kSegs];
+                mbar_arrive(&S.segempty[i % kSegs]);
+                if (s.tiles == 0) break;
+                const int qb = i % a.qbufs;
+                ok = tree_wait(&S.qfull[qb], (i / a.qbufs) & 1, &S.bad);
+                const int cols = max(16, (s.acc * a.G + 15) & ~15);
+                const int n1 = min(cols, 256), n2 = cols - n1;
+                const uint32_t id1 = umma_idesc_bf16(128, n1), id2 = umma_idesc_bf16(128, n2);
+                const uint64_t qd = q0 + (uint64_t)(qb * qbytes >> 4);
+                for (int t = 0; ok && t < s.tiles; t++) {
+                    ok = tree_wait(&S.full[slot], ph, &S.bad);
+                    if (k >= a.dbufs) ok = ok && tree_wait(&S.dempty[db], dph, &S.bad);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t kd = k0 + (uint64_t)(slot * (kSlot >> 4));
+                    const uint32_t d = tmem + db * a.dcols;
+#pragma unroll
+                    for (int ks = 0; ks < 8; ks++) {
+                        const uint64_t b = qd + (uint64_t)((ks >> 2) * (a.rows * 8) + (ks & 3) * 2);
+                        umma_bf16(d, umma_sdesc_step(kd, ks), b, id1, ks > 0);
+                        if (n2) umma_bf16(d + 256, umma_sdesc_step(kd, ks), b + 256 * 8, id2, ks > 0);
+                    }
+                    umma_commit(&S.dfull[db]);
+                    umma_commit(&S.empty[slot]);
+                    if (t + 1 == s.tiles) umma_commit(&S.qempty[qb]);
+                    if (++slot == a.ring) { slot = 0; ph ^= 1; }
+                    if (++db == a.dbufs) { db = 0; dph ^= 1; }
+                    k++;
+                }
+            }
+            if (!ok) {
+                // the MMAs in flight are done before tensor memory goes back
+                S.bad = 1;
+                umma_commit(&S.drain);
+                mbar_wait(&S.drain, 0);
+            }
+        }
+        __syncwarp();
+    } else if (warp == kGather) {
+        // ------------------------------------------------- accepted rows of q
+        bool ok = true;
+        for (int i = 0; ok; i++) {
+            ok = __all_sync(kFull, tree_wait(&S.segfull[i % kSegs], (i / kSegs) & 1, &S.bad));
+            if (!ok) break;
+            const Seg s = S.seg[i % kSegs];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.segempty[i % kSegs]);
+            if (s.tiles == 0) break;
+            const int qb = i % a.qbufs;
+            if (i >= a.qbufs)
+                ok = __all_sync(kFull, tree_wait(&S.qempty[qb], (i / a.qbufs - 1) & 1, &S.bad));
+            if (!ok) break;
+            const int rows = s.acc * a.G, cols = max(16, (rows + 15) & ~15);
+            unsigned char *d = qbuf + qb * qbytes;
+            const int32_t *tok = a.p.token + (size_t)s.b * a.p.A;
+            // two rows of 16 chunks a step, four steps in flight
+            for (int r0 = 0; r0 < cols; r0 += 8) {
+                uint4 v[4];
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const int r = r0 + 2 * e + (lane >> 4), j = r / a.G;
+                    v[e] = make_uint4(0, 0, 0, 0);
+                    if (r < rows)
+                        v[e] = reinterpret_cast<const uint4 *>(
+                            a.q + (((size_t)s.u * a.t.T + tok[j]) * a.G + (r - j * a.G)) * kD)[lane & 15];
+                }
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const int r = r0 + 2 * e + (lane >> 4), c = lane & 15;
+                    *reinterpret_cast<uint4 *>(d + (c >> 3) * (a.rows * 128) + r * 128 +
+                                               (((c & 7) ^ (r & 7)) << 4)) = v[e];
+                }
+            }
+            for (int r = lane; r < cols; r += 32) {
+                const int j = r / a.G;
+                S.c[qb][r] = r < rows ? row_c(a, ((size_t)s.u * a.t.T + tok[j]) * a.G + (r - j * a.G), s.b, j)
+                                      : INFINITY;
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.qfull[qb]);
+        }
+    } else if (warp == kTail) {
+        // --------------------------------- the accepted tokens' own entries
+        for (int u = blockIdx.x; u < a.U; u += gridDim.x) {
+            int32_t err;
+            const int n = a.len[u], acc = unit_acc(a, u, n, &err), b = a.by_units(u);
+            if (acc <= 0) continue;
+            const int32_t *tok = a.p.token + (size_t)b * a.p.A;
+            const int g = lane >> 2, t = lane & 3, rows = acc * a.G;
+            for (int m0 = 0; m0 < acc; m0 += 16) {           // 16 accepted tokens' keys
+                uint32_t ka[8][4];
+                int c[2];
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    c[h] = tok[min(m0 + g + 8 * h, acc - 1)];
+                    const uint32_t *p = reinterpret_cast<const uint32_t *>(
+                        a.kt + ((size_t)u * a.t.T + c[h]) * kD) + t;
+#pragma unroll
+                    for (int ks = 0; ks < 8; ks++) {
+                        ka[ks][h] = p[8 * ks];
+                        ka[ks][2 + h] = p[8 * ks + 4];
+                    }
+                }
+                float sum[2] = {0.f, 0.f};
+                for (int r0 = 0; r0 < rows; r0 += 8) {       // eight rows of q
+                    const int r = min(r0 + g, rows - 1), j = r / a.G;
+                    const uint32_t *p = reinterpret_cast<const uint32_t *>(
+                        a.q + (((size_t)u * a.t.T + tok[j]) * a.G + (r - j * a.G)) * kD) + t;
+                    float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int ks = 0; ks < 8; ks++)
+                        mma16816(d, ka[ks][0], ka[ks][1], ka[ks][2], ka[ks][3], p[8 * ks], p[8 * ks + 4]);
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {            // the columns of the thread
+                        const int rr = r0 + 2 * t + e, jj = rr / a.G;
+                        if (rr >= rows) continue;
+                        const int ct = tok[jj];
+                        const float cr = row_c(a, ((size_t)u * a.t.T + ct) * a.G + (rr - jj * a.G), b, jj);
+                        const uint64_t see = a.t.mask[(size_t)b * a.t.T + ct];
+#pragma unroll
+                        for (int h = 0; h < 2; h++)
+                            if (see >> c[h] & 1) sum[h] += weight(__float_as_uint(d[2 * h + e]), a.scale, cr);
+                    }
+                }
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    sum[h] += __shfl_xor_sync(kFull, sum[h], 1);
+                    sum[h] += __shfl_xor_sync(kFull, sum[h], 2);
+                    if (t == 0 && m0 + g + 8 * h < acc) a.S[(size_t)u * a.cap + n + m0 + g + 8 * h] = sum[h];
+                }
+            }
+        }
+    } else {
+        // ---------------------------------------------------------- slots
+        const int w = warp >> 2, r = tid & 127;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        bool ok = true;
+        int k = 0;                                           // the CTA's tiles so far
+        for (int i = 0; ok; i++) {
+            ok = __all_sync(kFull, tree_wait(&S.segfull[i % kSegs], (i / kSegs) & 1, &S.bad));
+            if (!ok) break;
+            const Seg s = S.seg[i % kSegs];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.segempty[i % kSegs]);
+            if (s.tiles == 0) break;
+            const int qb = i % a.qbufs, cols = max(16, (s.acc * a.G + 15) & ~15);
+            ok = __all_sync(kFull, tree_wait(&S.qfull[qb], (i / a.qbufs) & 1, &S.bad));
+            for (int t = (k ^ w) & 1; ok && t < s.tiles; t += 2) {
+                const int at = (s.t0 + t) * kTile + r, kk = k + t, db = kk % a.dbufs;
+                const size_t slot = (size_t)s.u * a.cap + at;
+                float vote = 1.f;
+                if (a.votes && at < s.n) vote = (float)a.votes[slot];
+                ok = __all_sync(kFull, tree_wait(&S.dfull[db], (kk / a.dbufs) & 1, &S.bad));
+                if (!ok) break;
+                tc_fence_after();
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                for (int c0 = 0; c0 < cols; c0 += 16) {
+                    uint32_t y[16];
+                    tmem_ld16_async(tmem + lanes + db * a.dcols + c0, y);
+                    float4 c[4];
+#pragma unroll
+                    for (int j = 0; j < 4; j++) c[j] = *reinterpret_cast<const float4 *>(&S.c[qb][c0 + 4 * j]);
+                    tmem_wait_ld();
+                    tmem_bind16(y);
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        sum[0] += weight(y[4 * j], a.scale, c[j].x);
+                        sum[1] += weight(y[4 * j + 1], a.scale, c[j].y);
+                        sum[2] += weight(y[4 * j + 2], a.scale, c[j].z);
+                        sum[3] += weight(y[4 * j + 3], a.scale, c[j].w);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&S.dempty[db]);
+                if (at < s.n) a.S[slot] = ((sum[0] + sum[1]) + (sum[2] + sum[3])) * vote;
+            }
+            k += s.tiles;
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(&S.qempty[qb]);
         }
     }
-    a.S[slot] = old && a.votes ? s * (float)a.votes[slot] : s;
+    __syncthreads();
+    if (warp == kMma) tmem_dealloc(tmem, 512);
+    if (tid == 0 && S.bad) record_status(a.status, KVC_ERR_TIMEOUT);
 }
 
 }  // namespace
@@ -58,10 +461,27 @@ cudaError_t launch_tree_weights(const kvc_params &p, int max_len, const TreeArgs
                                 const uint16_t *kt, const float *lse, const kvc_cache &c, float *S,
                                 void *ws, cudaStream_t st)
 {
-    WtArgs a{t, pa, row_weight, q, kt, c.K, lse, c.votes, c.len, S, static_cast<int32_t *>(ws), p.G,
+    const long long tmax = (max_len + kTile - 1) / kTile, tiles = p.U * tmax;
+    if (tiles > 0x7fffffffll) return cudaErrorInvalidValue;
+    CUtensorMap mk;
+    if (!make_unit_map(&mk, c.K, p.U, p.cap)) return cudaErrorInvalidValue;
+    WtArgs a{t, pa, row_weight, q, kt, lse, c.votes, c.len, S, static_cast<int32_t *>(ws), p.U, p.G,
              p.cap, max_len};
-    const int top = max_len + pa.A < p.cap ? max_len + pa.A : p.cap;
-    tree_weights_kernel<<<dim3((top + 255) / 256, p.U), 256, 0, st>>>(a);
+    a.rows = (pa.A * p.G + 15) & ~15;
+    a.qbufs = a.rows <= 128 ? 2 : 1;
+    a.dcols = a.rows <= 128 ? 128 : a.rows <= 256 ? 256 : 512;
+    a.dbufs = 512 / a.dcols;
+    a.ring = (int)((227 * 1024 - kCtl - (size_t)a.qbufs * a.rows * 256) / kSlot);
+    if (a.ring > kMaxRing) a.ring = kMaxRing;
+    a.by_units = FastDiv(t.units);
+    a.scale = kLog2e / sqrtf((float)kD);
+    const size_t smem = (size_t)a.ring * kSlot + (size_t)a.qbufs * a.rows * 256 + sizeof(WtSmem);
+    cudaError_t e = cudaFuncSetAttribute(tree_weights_kernel,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    long long grid = tiles > p.U ? tiles : p.U;
+    if (grid > kGrid) grid = kGrid;
+    tree_weights_kernel<<<(int)grid, kThreads, smem, st>>>(a, mk);
     return cudaGetLastError();
 }
 
