@@ -2,28 +2,40 @@
 // the weight every slot gathered, evict the lowest (utility, position) pairs
 // down to the budget into the moments, close the gaps.
 //
-// One CTA per unit, one pass over the utilities:
-//   1. update in place; consecutive slots form groups (a power of two of
-//      them, about 256 groups or more) whose lowest utility goes to shared
-//      memory;
+// Bound by bytes: 20 per slot (utility read and written, weight read), 128 KB
+// per unit for C, and the rows that go and come.  One CTA of 256 threads per
+// unit, several of them per SM, so that one's loads run under another's
+// selection:
+//   1. the utilities are updated in place; every thread keeps the lowest of
+//      its slots;
 //   2. at least k slots are at or below the k-th smallest minimum of any
 //      partition of the slots, so it bounds the k-th lowest utility: the
-//      groups are folded into 128 sets whose minima are ranked;
-//   3. the scored slots at or below the bound (in groups whose minimum is)
-//      are the candidates, about 1.4 k of them, ranked by (utility, position,
-//      slot) against one another.
+//      threads are folded into 32 sets (128 for k > 16) whose minima are
+//      ranked;
+//   3. the slots at or below the bound, about 1.4 k of them, are looked up by
+//      the threads that have one and ranked by (utility, position, slot)
+//      against one another;
+//   4. rows move, C is read and written in whole lines (prefetched to L2 at
+//      the start).
+// Units of more than kLong slots are updated by a kernel of their own over
+// the whole grid, which leaves the lowest utility of every 32 slots; step 1 is
+// then a pass over those.
+//
 // Many equal utilities (weights that underflow to 0) can make every slot a
 // candidate: then the bound is taken again over whole (utility, position,
 // slot) keys, which are distinct; and if the lowest keys sit in so few sets
 // that even these are too many, the k lowest are found one after another.
 #include "kvc_tree.h"
 
+#include <stddef.h>
+
 namespace kvc {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kSets = 128;               // minima ranked for the bound
+constexpr int kThreads = 256;
 constexpr int kCand = 1024;              // candidates held
+constexpr int kLong = 8192;              // slots of a unit that one CTA updates
+constexpr int kChunk = 2048;             // slots per CTA of the update kernel
 
 struct Key {
     uint64_t u, t;                       // utility; position and slot
@@ -36,20 +48,14 @@ __device__ __forceinline__ bool key_less(const Key &a, const Key &b)
 
 __device__ __forceinline__ Key key_min(const Key &a, const Key &b) { return key_less(b, a) ? b : a; }
 
-__device__ __forceinline__ Key key_shfl(const Key &k, int m)
-{
-    return Key{__shfl_xor_sync(kFull, (unsigned long long)k.u, m),
-               __shfl_xor_sync(kFull, (unsigned long long)k.t, m)};
-}
-
 // No key: above every scored slot's.
-__device__ __forceinline__ Key key_none() { return Key{~0ull, ~0ull}; }
+constexpr uint64_t kNone = ~0ull;
 
 // Unscored slots (infinite utilities) are protected: they have no key.
 __device__ __forceinline__ uint64_t util_key(double m)
 {
     const uint64_t b = (uint64_t)__double_as_longlong(m);
-    if ((b & 0x7fffffffffffffffull) == 0x7ff0000000000000ull) return ~0ull;
+    if ((b & 0x7fffffffffffffffull) == 0x7ff0000000000000ull) return kNone;
     return double_key(m);
 }
 
@@ -69,23 +75,57 @@ struct ComArgs {
     const int32_t *budget;
     float *mn, *mu_k, *mu_v, *C;
     int32_t *evict_idx, *evict_pos, *n_evict, *status, *pend;
+    uint64_t *gmin;                      // [U][cap] lowest key of every 32 slots (long units)
     double alpha;
-    int cap, L, rule, kmax, max_len, gshift;
+    int cap, L, rule, kmax, max_len;
+    FastDiv by_units;
 };
 
 struct ComSmem {
-    float kv[2][kTreeMax][kD];           // the victims' keys and values
     Key cand[kCand];
-    Key set[kSets];
+    Key set[128];
+    Key bound;
     double fresh[kTreeMax];              // utilities of the accepted tokens
     float bar[2][kD], del[2][kD];        // batch means; their distance from the moments'
     float w[kTreeMax];
     int32_t tok[kTreeMax];
-    int vic[kTreeMax], src[kTreeMax], dst[kTreeMax];
+    int vic[kTreeMax], src[kTreeMax], gone[kTreeMax];
     int scan[40];
-    Key bound;
-    int n_cand, n_move;
+    int n_cand, n_hole;
+    alignas(16) float kv[4];             // [2][kmax][kD]: the victims' keys and values
 };
+static_assert(offsetof(ComSmem, kv) % 16 == 0 && offsetof(ComSmem, bar) % 16 == 0 &&
+                  offsetof(ComSmem, del) % 16 == 0, "read as float4");
+
+// What a unit does: its lengths and counts, or why it is refused.  Warp-wide.
+struct Plan {
+    int n, acc, total, k, err;
+};
+
+__device__ __forceinline__ Plan plan_unit(const ComArgs &a, int u, int lane)
+{
+    const int b = a.by_units(u);
+    Plan p;
+    p.n = a.len[u];
+    const int L = a.budget ? a.budget[u] : a.L;
+    const int live = a.t.n ? a.t.n[b] : a.t.T;
+    p.acc = a.p.n[b];
+    // every entry of the row is read at once: which of them count is known with n
+    int c0 = 0, c1 = 0;
+    const int32_t *tok = a.p.token + (size_t)b * a.p.A;
+    if (lane < a.p.A) c0 = tok[lane];
+    if (lane + 32 < a.p.A) c1 = tok[lane + 32];
+    const bool bad = (lane < p.acc && (c0 < 0 || c0 >= live)) ||
+                     (lane + 32 < p.acc && (c1 < 0 || c1 >= live));
+    p.total = p.n + p.acc;
+    p.k = max(0, p.total - L);
+    p.err = KVC_OK;
+    if (p.n < 0 || p.n > a.max_len) p.err = KVC_ERR_SHAPE;
+    else if (live < 0 || live > a.t.T || p.acc < 0 || p.acc > a.p.A || __any_sync(kFull, bad))
+        p.err = KVC_ERR_INVALID_ARG;
+    else if (p.total > a.cap || L < 1 || L > a.L || p.k > a.kmax) p.err = KVC_ERR_SHAPE;
+    return p;
+}
 
 __device__ __forceinline__ double new_util(const ComArgs &a, double m, double s)
 {
@@ -94,21 +134,79 @@ __device__ __forceinline__ double new_util(const ComArgs &a, double m, double s)
     return a.rule == KVC_RULE_CUMULATIVE ? m + s : a.alpha * m + (1.0 - a.alpha) * s;
 }
 
-// The k-th smallest of the sets' minima into s.bound (none when fewer than k
-// sets have a key).  `mine`: the thread's own minimum; four lanes are a set.
-__device__ void rank_sets(ComSmem &s, Key mine, int k)
+// Long units: the utilities of kChunk slots, and the lowest key of every 32.
+// grid (chunks, U)
+__global__ void __launch_bounds__(kThreads) tree_update_kernel(ComArgs a)
 {
-    mine = key_min(mine, key_shfl(mine, 1));
-    mine = key_min(mine, key_shfl(mine, 2));
-    if ((threadIdx.x & 3) == 0) s.set[threadIdx.x >> 2] = mine;
-    if (threadIdx.x == 0) s.n_cand = 0;
+    const int u = blockIdx.y, lane = threadIdx.x & 31;
+    const Plan p = plan_unit(a, u, lane);
+    if (p.err != KVC_OK) return;
+    const size_t cb = (size_t)u * a.cap;
+    const int i0 = blockIdx.x * kChunk + threadIdx.x;
+    if (i0 - (int)threadIdx.x >= p.n) return;
+    constexpr int kPer = kChunk / kThreads;
+    double m[kPer];
+    float s[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; j++) {
+        const int i = i0 + j * kThreads;
+        m[j] = i < p.n ? a.util[cb + i] : __longlong_as_double(0x7ff0000000000000ll);
+        s[j] = a.S && i < p.n ? a.S[cb + i] : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; j++) {
+        const int i = i0 + j * kThreads;
+        if (a.S && i < p.n) {
+            m[j] = new_util(a, m[j], (double)s[j]);
+            a.util[cb + i] = m[j];
+        }
+        uint64_t x = util_key(m[j]);
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1)
+            x = min((unsigned long long)x, __shfl_xor_sync(kFull, (unsigned long long)x, d));
+        if (lane == 0 && i < p.n) a.gmin[cb / 32 + u + (i >> 5)] = x;
+    }
+}
+
+// The k-th smallest of the sets' minima into s.bound.u (kNone when fewer than
+// k sets have a key); `mine` is the thread's own minimum.
+__device__ __forceinline__ void rank_utils(ComSmem &s, uint64_t mine, int k)
+{
+    const int tid = threadIdx.x, fold = k <= 16 ? 8 : 2, sets = kThreads / fold;
+    uint64_t *set = reinterpret_cast<uint64_t *>(s.set);
+    for (int d = 1; d < fold; d <<= 1)
+        mine = min((unsigned long long)mine, __shfl_xor_sync(kFull, (unsigned long long)mine, d));
+    if (tid % fold == 0) set[tid / fold] = mine;
+    if (tid == 0) s.n_cand = 0;
     __syncthreads();
-    if (threadIdx.x < kSets) {
-        const Key x = s.set[threadIdx.x];
+    if (tid < sets) {
+        const uint64_t x = set[tid];
         int r = 0;
-        for (int j = 0; j < kSets; j++) {
+#pragma unroll 8
+        for (int j = 0; j < sets; j++) {
+            const uint64_t y = set[j];
+            r += y < x || (y == x && j < tid);
+        }
+        if (r == k - 1) s.bound = Key{x, kNone};
+    }
+    __syncthreads();
+}
+
+// The same over whole keys, 128 sets.
+__device__ void rank_keys(ComSmem &s, Key mine, int k)
+{
+    const int tid = threadIdx.x;
+    mine = key_min(mine, Key{__shfl_xor_sync(kFull, (unsigned long long)mine.u, 1),
+                             __shfl_xor_sync(kFull, (unsigned long long)mine.t, 1)});
+    if (tid % 2 == 0) s.set[tid / 2] = mine;
+    if (tid == 0) s.n_cand = 0;
+    __syncthreads();
+    if (tid < 128) {
+        const Key x = s.set[tid];
+        int r = 0;
+        for (int j = 0; j < 128; j++) {
             const Key y = s.set[j];
-            r += key_less(y, x) || (j < (int)threadIdx.x && !key_less(x, y));
+            r += key_less(y, x) || (j < tid && !key_less(x, y));
         }
         if (r == k - 1) s.bound = x;
     }
@@ -121,112 +219,132 @@ __device__ __forceinline__ void add_candidate(ComSmem &s, const Key &k)
     if (c < kCand) s.cand[c] = k;
 }
 
+template <bool kSplit>
 __global__ void __launch_bounds__(kThreads) tree_commit_kernel(ComArgs a)
 {
     extern __shared__ __align__(16) unsigned char raw[];
     ComSmem &s = *reinterpret_cast<ComSmem *>(raw);
-    uint64_t *gmin = reinterpret_cast<uint64_t *>(raw + sizeof(ComSmem));
     const int u = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int b = u / a.t.units;
-    const int n = a.len[u], acc = path_count(a.t, a.p, u, lane);
-    const int L = a.budget ? a.budget[u] : a.L;
-    const int total = n + acc, k = max(0, total - L);
-    int err = KVC_OK;
-    if (n < 0 || n > a.max_len) err = KVC_ERR_SHAPE;
-    else if (acc < 0) err = KVC_ERR_INVALID_ARG;
-    else if (total > a.cap || L < 1 || L > a.L || k > a.kmax) err = KVC_ERR_SHAPE;
-    if (err != KVC_OK) {
+    const Plan p = plan_unit(a, u, lane);
+    if (p.err != KVC_OK) {
         if (tid == 0) {
             a.n_evict[u] = 0;
-            record_status(a.status, err);
+            record_status(a.status, p.err);
         }
         return;
     }
+    const int n = p.n, acc = p.acc, total = p.total, k = p.k, b = a.by_units(u);
     const size_t cb = (size_t)u * a.cap, tb = (size_t)u * a.t.T;
     double *util = a.util + cb;
     int32_t *pos = a.pos + cb;
     const float *S = a.S ? a.S + cb : nullptr;
-    const int pos0 = a.p.pos[b];
+    const uint64_t *gmin = a.gmin + cb / 32 + u;
+    const int pos0 = a.p.pos[b], groups = (n + 31) >> 5;
+    float *C = a.C + (size_t)u * kD * kD;
+    if (a.C && k > 0) {
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(C + (tid + i * kThreads) * 32) : "memory");
+    }
     if (tid < acc) {
         s.tok[tid] = a.p.token[(size_t)b * a.p.A + tid];
         s.fresh[tid] = S ? (double)S[n + tid] : __longlong_as_double(0x7ff0000000000000ll);
     }
-    // 1. utilities; the lowest of each group of 2^gshift consecutive slots
-    const int groups = (n + (1 << a.gshift) - 1) >> a.gshift;
-    int scored = 0;
-    for (int i0 = 0; i0 < n; i0 += kThreads) {
-        const int i = i0 + tid;
-        uint64_t x = ~0ull;
-        if (i < n) {
-            double m = util[i];
-            if (S) {
-                m = new_util(a, m, S[i]);
-                util[i] = m;
+    // 1. the lowest key of the thread's slots (long units: of its groups of 32)
+    uint64_t mine = kNone;
+    if (kSplit) {
+#pragma unroll 4
+        for (int g = tid; g < groups; g += kThreads) mine = min((unsigned long long)mine, (unsigned long long)gmin[g]);
+    } else {
+        for (int i0 = tid; i0 < n; i0 += 4 * kThreads) {
+            double m[4];
+            float x[4];
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const int i = i0 + j * kThreads;
+                m[j] = i < n ? util[i] : __longlong_as_double(0x7ff0000000000000ll);
+                x[j] = S && i < n ? S[i] : 0.f;
             }
-            x = util_key(m);
-            scored += x != ~0ull;
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const int i = i0 + j * kThreads;
+                if (S && i < n) {
+                    m[j] = new_util(a, m[j], (double)x[j]);
+                    util[i] = m[j];
+                }
+                mine = min((unsigned long long)mine, (unsigned long long)util_key(m[j]));
+            }
         }
-        for (int d = 1; d < 1 << a.gshift; d <<= 1)
-            x = min((unsigned long long)x, __shfl_xor_sync(kFull, (unsigned long long)x, d));
-        if (i < n && (i & ((1 << a.gshift) - 1)) == 0) gmin[i >> a.gshift] = x;
     }
-    if (tid < acc) scored += util_key(s.fresh[tid]) != ~0ull;
-    int all;
-    block_exscan(scored, s.scan, &all);
-    if (all < k) {
-        if (tid == 0) {
-            a.n_evict[u] = 0;
-            record_status(a.status, KVC_ERR_INVALID_ARG);
+    // fewer scored slots than victims?  Minima of k threads answer it
+    if (__syncthreads_count(mine != kNone) < k) {
+        int c = tid < acc && util_key(s.fresh[tid]) != kNone, all;
+        for (int i = tid; i < n; i += kThreads) c += util_key(util[i]) != kNone;
+        block_exscan(c, s.scan, &all);
+        if (all < k) {
+            if (tid == 0) {
+                a.n_evict[u] = 0;
+                record_status(a.status, KVC_ERR_INVALID_ARG);
+            }
+            return;
         }
-        return;
     }
+    const int end = total - k;
     if (k > 0) {
         // 2., 3.
-        Key mine = key_none();
-        for (int g = tid; g < groups; g += kThreads) mine = key_min(mine, Key{gmin[g], ~0ull});
-        rank_sets(s, mine, k);
+        rank_utils(s, mine, k);
         const uint64_t top = s.bound.u;
-        if (tid < acc && util_key(s.fresh[tid]) != ~0ull)
-            add_candidate(s, Key{util_key(s.fresh[tid]), tie_key(pos0 + tid, n + tid)});
-        for (int g = warp; g < groups; g += kThreads / 32) {
-            if (gmin[g] > top || gmin[g] == ~0ull) continue;
-            const int i = (g << a.gshift) + lane;
-            if (lane < 1 << a.gshift && i < n) {
+        if (tid < acc) {
+            const uint64_t x = util_key(s.fresh[tid]);
+            if (x != kNone) add_candidate(s, Key{x, tie_key(pos0 + tid, n + tid)});
+        }
+        if (kSplit) {
+            // a warp looks through the groups that one of its threads found low
+            for (int g0 = 32 * warp; g0 < groups; g0 += kThreads) {
+                const int g = g0 + lane;
+                const uint64_t x = g < groups ? gmin[g] : kNone;
+                for (unsigned todo = __ballot_sync(kFull, x != kNone && x <= top); todo; todo &= todo - 1) {
+                    const int i = 32 * (g0 + __ffs(todo) - 1) + lane;
+                    const uint64_t y = i < n ? util_key(util[i]) : kNone;
+                    if (y != kNone && y <= top) add_candidate(s, Key{y, tie_key(pos[i], i)});
+                }
+            }
+        } else if (mine != kNone && mine <= top) {
+#pragma unroll 4
+            for (int i = tid; i < n; i += kThreads) {
                 const uint64_t x = util_key(util[i]);
-                if (x <= top && x != ~0ull) add_candidate(s, Key{x, tie_key(pos[i], i)});
+                if (x != kNone && x <= top) add_candidate(s, Key{x, tie_key(pos[i], i)});
             }
         }
         __syncthreads();
         auto key_at = [&](int i) {
             const uint64_t x = util_key(i < n ? util[i] : s.fresh[i - n]);
-            return x == ~0ull ? key_none()
+            return x == kNone ? Key{kNone, kNone}
                               : Key{x, tie_key(i < n ? pos[i] : pos0 + i - n, i)};
         };
         if (s.n_cand > kCand) {
             __syncthreads();
-            mine = key_none();
-            for (int i = tid; i < total; i += kThreads) mine = key_min(mine, key_at(i));
-            rank_sets(s, mine, k);
+            Key low{kNone, kNone};
+            for (int i = tid; i < total; i += kThreads) low = key_min(low, key_at(i));
+            rank_keys(s, low, k);
             const Key top2 = s.bound;
             for (int i = tid; i < total; i += kThreads) {
                 const Key x = key_at(i);
-                if (x.u != ~0ull && !key_less(top2, x)) add_candidate(s, x);
+                if (x.u != kNone && !key_less(top2, x)) add_candidate(s, x);
             }
             __syncthreads();
         }
         if (s.n_cand > kCand) {
             Key last{0, 0};
-            bool any = false;
             for (int r = 0; r < k; r++) {
-                mine = key_none();
+                Key low{kNone, kNone};
                 for (int i = tid; i < total; i += kThreads) {
                     const Key x = key_at(i);
-                    if (!any || key_less(last, x)) mine = key_min(mine, x);
+                    if (r == 0 || key_less(last, x)) low = key_min(low, x);
                 }
                 __syncthreads();
-                rank_sets(s, mine, 1);
+                rank_keys(s, low, 1);
                 last = s.bound;
-                any = true;
                 __syncthreads();
                 if (tid == 0) s.vic[r] = (int)(uint32_t)last.t;
             }
@@ -236,75 +354,72 @@ __global__ void __launch_bounds__(kThreads) tree_commit_kernel(ComArgs a)
             for (int i = tid; i < c; i += kThreads) {
                 const Key x = s.cand[i];
                 int r = 0;
+#pragma unroll 4
                 for (int j = 0; j < c; j++) r += key_less(s.cand[j], x);
                 if (r < k) s.vic[r] = (int)(uint32_t)x.t;
             }
         }
+        if (tid < k) s.gone[tid] = 0;
+        if (tid == 0) s.n_hole = 0;
         __syncthreads();
-        // into ascending slot order
+        // into ascending slot order; which of the slots from `end` on go
         int v = 0, r = 0;
         if (tid < k) {
             v = s.vic[tid];
             for (int j = 0; j < k; j++) r += s.vic[j] < v;
+            if (v >= end) s.gone[v - end] = 1;
         }
-        __syncthreads();
-        if (tid < k) s.vic[r] = v;
         __syncthreads();
         if (tid < k) {
-            const int e = s.vic[tid];
-            if (a.evict_idx) a.evict_idx[(size_t)u * a.kmax + tid] = e;
-            if (a.evict_pos) a.evict_pos[(size_t)u * a.kmax + tid] = e < n ? pos[e] : pos0 + e - n;
-            s.w[tid] = e < n && a.votes ? (float)a.votes[cb + e] : 1.f;
+            s.vic[r] = v;
+            if (v < end) atomicAdd(&s.n_hole, 1);
+            if (a.evict_idx) a.evict_idx[(size_t)u * a.kmax + r] = v;
+            if (a.evict_pos) a.evict_pos[(size_t)u * a.kmax + r] = v < n ? pos[v] : pos0 + v - n;
+            s.w[r] = v < n && a.votes ? (float)a.votes[cb + v] : 1.f;
+            // the r-th hole below `end` takes the r-th slot at or above it that stays
+            if (!s.gone[tid]) {
+                int before = 0;
+                for (int j = 0; j < tid; j++) before += !s.gone[j];
+                s.src[before] = end + tid;
+            }
         }
+        __syncthreads();
+        // the victims' rows, before any of them is overwritten
+        if (a.C)
+            for (int e = tid; e < k * 32; e += kThreads) {
+                const int j = e >> 5, ch = e & 15, which = e >> 4 & 1, i = s.vic[j];
+                const uint16_t *row = i < n ? (which ? a.V : a.K) + (cb + i) * kD
+                                            : (which ? a.vt : a.kt) + (tb + s.tok[i - n]) * kD;
+                float f[8];
+                unpack8(reinterpret_cast<const uint4 *>(row)[ch], f);
+                float4 *d = reinterpret_cast<float4 *>(s.kv + (which * a.kmax + j) * kD + ch * 8);
+                d[0] = make_float4(f[0], f[1], f[2], f[3]);
+                d[1] = make_float4(f[4], f[5], f[6], f[7]);
+            }
+    } else if (tid == 0) {
+        s.n_hole = 0;
     }
-    const int end = total - k;
-    // the holes below `end` take the slots at or above it that stay; both
-    // lists ascend.  Accepted tokens below `end` that stay go where they are
-    if (tid == 0) {
-        int nm = 0, v = 0;
-        while (v < k && s.vic[v] < end) v++;
-        for (int i = end; i < total; i++) {
-            if (v < k && s.vic[v] == i) { v++; continue; }
-            s.src[nm] = i;
-            s.dst[nm] = s.vic[nm];
-            nm++;
-        }
-        s.n_move = nm;
-    }
-    // the victims' rows, before any of them is overwritten
-    if (a.C)
-        for (int e = tid; e < k * 32; e += kThreads) {
-            const int j = e >> 5, ch = e & 15, which = e >> 4 & 1, i = s.vic[j];
-            const uint16_t *r = i < n ? (which ? a.V : a.K) + (cb + i) * kD
-                                      : (which ? a.vt : a.kt) + (tb + s.tok[i - n]) * kD;
-            float f[8];
-            unpack8(reinterpret_cast<const uint4 *>(r)[ch], f);
-#pragma unroll
-            for (int d = 0; d < 8; d++) s.kv[which][j][ch * 8 + d] = f[d];
-        }
     __syncthreads();
-    // rows: first the moves (sources at or above `end`, destinations below),
-    // then the accepted tokens that stay where they were appended
-    const int nm = s.n_move;
-    auto is_victim = [&](int i) {
-        for (int j = 0; j < k; j++)
-            if (s.vic[j] == i) return true;
-        return false;
-    };
+    // rows: the moves (sources at or above `end`, destinations below), and the
+    // accepted tokens below `end` that stay where they are appended
+    const int nm = s.n_hole;
     for (int e = tid; e < (nm + acc) * 32; e += kThreads) {
         const int j = e >> 5, ch = e & 15, which = e >> 4 & 1;
         int from, to;
         if (j < nm) {
             from = s.src[j];
-            to = s.dst[j];
+            to = s.vic[j];
         } else {
             from = to = n + j - nm;
-            if (to >= end || is_victim(to)) continue;
+            if (to >= end) continue;
+            bool victim = false;
+            for (int i = nm - 1; i >= 0 && s.vic[i] >= to; i--) victim |= s.vic[i] == to;
+            if (victim) continue;
         }
-        const uint16_t *r = from < n ? (which ? a.V : a.K) + (cb + from) * kD
-                                     : (which ? a.vt : a.kt) + (tb + s.tok[from - n]) * kD;
-        uint4 *w = reinterpret_cast<uint4 *>((which ? a.V : a.K) + (cb + to) * kD);
-        w[ch] = reinterpret_cast<const uint4 *>(r)[ch];
+        const uint16_t *row = from < n ? (which ? a.V : a.K) + (cb + from) * kD
+                                       : (which ? a.vt : a.kt) + (tb + s.tok[from - n]) * kD;
+        reinterpret_cast<uint4 *>((which ? a.V : a.K) + (cb + to) * kD)[ch] =
+            reinterpret_cast<const uint4 *>(row)[ch];
         if ((e & 31) == 0) {
             util[to] = from < n ? util[from] : s.fresh[from - n];
             pos[to] = from < n ? pos[from] : pos0 + from - n;
@@ -319,39 +434,60 @@ __global__ void __launch_bounds__(kThreads) tree_commit_kernel(ComArgs a)
     if (!a.C || k == 0) return;
     // the moments: the batch's weighted means and co-moment, merged (Chan,
     // Golub and LeVeque, 1979)
-    float nb = 0.f;
-    for (int j = 0; j < k; j++) nb += s.w[j];
-    const float n0 = a.mn[u], n1 = n0 + nb;
-    if (tid < 2 * kD) {
-        const int which = tid >> 7, d = tid & 127;
-        float x = 0.f;
-        for (int j = 0; j < k; j++) x += s.w[j] * s.kv[which][j][d];
-        float *mu = (which ? a.mu_v : a.mu_k) + (size_t)u * kD + d;
-        x /= nb;
-        s.bar[which][d] = x;
-        s.del[which][d] = x - *mu;
-        *mu += (x - *mu) * (nb / n1);
-    }
-    __syncthreads();
-    const int r0 = 4 * (tid >> 4), c0 = 8 * (tid & 15);
-    float m[4][8] = {};
+    const int which = tid >> 7, d = tid & 127;
+    const float *kv = s.kv, *vv = s.kv + a.kmax * kD;
+    float *mu = (which ? a.mu_v : a.mu_k) + (size_t)u * kD + d;
+    const float mu0 = *mu, n0 = a.mn[u];
+    float nb = 0.f, x = 0.f;
     for (int j = 0; j < k; j++) {
+        nb += s.w[j];
+        x += s.w[j] * (which ? vv : kv)[j * kD + d];
+    }
+    const float n1 = n0 + nb;
+    x /= nb;
+    s.bar[which][d] = x;
+    s.del[which][d] = x - mu0;
+    *mu = mu0 + (x - mu0) * (nb / n1);
+    __syncthreads();
+    // warp w: rows (value dimensions) 16 w .., four columns a lane
+    const float4 kb = reinterpret_cast<const float4 *>(s.bar[0])[lane];
+    const float4 dk = reinterpret_cast<const float4 *>(s.del[0])[lane];
+    const float cross = n0 * (nb / n1) / n1, keep = n0 / n1, inv = 1.f / n1;
 #pragma unroll
-        for (int x = 0; x < 4; x++) {
-            const float v = s.w[j] * (s.kv[1][j][r0 + x] - s.bar[1][r0 + x]);
+    for (int r0 = 0; r0 < 16; r0 += 8) {
+        const int row = 16 * warp + r0;
+        float4 *c = reinterpret_cast<float4 *>(C + row * kD) + lane;
+        float4 old[8], m[8];
 #pragma unroll
-            for (int y = 0; y < 8; y++) m[x][y] += v * (s.kv[0][j][c0 + y] - s.bar[0][c0 + y]);
+        for (int i = 0; i < 8; i++) {
+            old[i] = c[i * (kD / 4)];
+            m[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        for (int j = 0; j < k; j++) {
+            float4 y = reinterpret_cast<const float4 *>(kv + j * kD)[lane];
+            y.x -= kb.x;
+            y.y -= kb.y;
+            y.z -= kb.z;
+            y.w -= kb.w;
+            const float w = s.w[j];
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const float v = w * (vv[j * kD + row + i] - s.bar[1][row + i]);
+                m[i].x = fmaf(v, y.x, m[i].x);
+                m[i].y = fmaf(v, y.y, m[i].y);
+                m[i].z = fmaf(v, y.z, m[i].z);
+                m[i].w = fmaf(v, y.w, m[i].w);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const float dv = cross * s.del[1][row + i];
+            c[i * (kD / 4)] = make_float4(fmaf(dv, dk.x, fmaf(keep, old[i].x, m[i].x * inv)),
+                                          fmaf(dv, dk.y, fmaf(keep, old[i].y, m[i].y * inv)),
+                                          fmaf(dv, dk.z, fmaf(keep, old[i].z, m[i].z * inv)),
+                                          fmaf(dv, dk.w, fmaf(keep, old[i].w, m[i].w * inv)));
         }
     }
-    float *C = a.C + (size_t)u * kD * kD;
-    const float cross = n0 * (nb / n1) / n1;
-#pragma unroll
-    for (int x = 0; x < 4; x++)
-#pragma unroll
-        for (int y = 0; y < 8; y++) {
-            float *c = C + (r0 + x) * kD + c0 + y;
-            *c = (n0 * *c + m[x][y]) / n1 + cross * s.del[1][r0 + x] * s.del[0][c0 + y];
-        }
     if (tid == 0) a.mn[u] = n1;
 }
 
@@ -363,17 +499,22 @@ cudaError_t launch_tree_commit(const kvc_params &p, int max_len, const TreeArgs 
                                int32_t *evict_idx, int32_t *evict_pos, int32_t *n_evict,
                                const DecodeWs &ws, cudaStream_t st)
 {
-    int gshift = 0;
-    while (gshift < 5 && (max_len >> gshift) > 512) gshift++;
-    const size_t smem = sizeof(ComSmem) + ((size_t)(max_len >> gshift) + 1) * sizeof(uint64_t);
-    cudaError_t e = cudaFuncSetAttribute(tree_commit_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
     ComArgs a{t, pa, kt, vt, S, c.K, c.V, c.votes, c.pos, c.len, c.util, p.budget,
               m ? m->n : nullptr, m ? m->mu_k : nullptr, m ? m->mu_v : nullptr, m ? m->C : nullptr,
-              evict_idx, evict_pos, n_evict, ws.status, ws.pend, (double)p.alpha, p.cap, p.L, p.rule,
-              kmax, max_len, gshift};
-    tree_commit_kernel<<<p.U, kThreads, smem, st>>>(a);
+              evict_idx, evict_pos, n_evict, ws.status, ws.pend,
+              reinterpret_cast<uint64_t *>(ws.probs), (double)p.alpha, p.cap, p.L, p.rule, kmax,
+              max_len, FastDiv(t.units)};
+    const bool split = max_len > kLong;
+    const size_t smem = sizeof(ComSmem) + (m ? 2 * (size_t)kmax * kD * sizeof(float) : 0);
+    auto *kernel = split ? tree_commit_kernel<true> : tree_commit_kernel<false>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    if (split) {
+        if (p.U > 65535) return cudaErrorInvalidValue;
+        tree_update_kernel<<<dim3((max_len + kChunk - 1) / kChunk, p.U), kThreads, 0, st>>>(a);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    kernel<<<p.U, kThreads, smem, st>>>(a);
     return cudaGetLastError();
 }
 
