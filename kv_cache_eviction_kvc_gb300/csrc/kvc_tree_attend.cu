@@ -746,7 +746,12 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                     if (at + step * kTile < s.n)
                         vote_next = a.votes[(size_t)s.u * a.cap + at + step * kTile];
                 }
-                // value rows the MMA reads that are no slot: zero
+                wait(&S.sfull[w], job & 1);
+                if (!ok) break;
+                tc_fence_after();
+                // value rows the MMA reads that are no slot: zero.  (After S: the issuer has
+                // then taken the ring entry that used the slot before, so that the parity
+                // below cannot be that of an earlier phase.)
                 if ((tree || nv & 15) && (!dual || w == 0)) {
                     const int t = tile - s.t0;
                     const int kv = 2 * s.k0 + t + (dual ? t + 1 : min(t + 2, s.t1 - s.t0));
@@ -785,9 +790,6 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
-                wait(&S.sfull[w], job & 1);
-                if (!ok) break;
-                tc_fence_after();
                 if (busy) {
                     if (tree || nv < kTile) {
                         uint64_t keep0 = see, keep1 = 0;     // the slots the row may see

@@ -34,7 +34,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kCand = 1024;              // candidates held
-constexpr int kLong = 8192;              // slots of a unit that one CTA updates
+constexpr int kLong = 32 * kThreads;     // slots of a unit that one CTA updates
 constexpr int kChunk = 2048;             // slots per CTA of the update kernel
 
 struct Key {
@@ -76,7 +76,7 @@ struct ComArgs {
     float *mn, *mu_k, *mu_v, *C;
     int32_t *evict_idx, *evict_pos, *n_evict, *status, *pend;
     uint64_t *gmin;                      // [U][cap] lowest key of every 32 slots (long units)
-    double alpha;
+    double alpha, beta;                  // EMA: alpha util + beta weight
     int cap, L, rule, kmax, max_len;
     FastDiv by_units;
 };
@@ -127,11 +127,23 @@ __device__ __forceinline__ Plan plan_unit(const ComArgs &a, int u, int lane)
     return p;
 }
 
-__device__ __forceinline__ double new_util(const ComArgs &a, double m, double s)
+// An fp32 as fp64 by integer operations: conversions run on the fp64 pipe,
+// which is narrow on this part (about one operation a clock per SM) and the
+// bound of step 1.  Zeros and normal numbers; the rest is converted.
+__device__ __forceinline__ double widen(float x)
 {
+    const uint32_t b = __float_as_uint(x), e = b >> 23 & 255;
+    if (e - 1u < 254u)
+        return __hiloint2double((int)((b & 0x80000000u) | ((b & 0x7fffffffu) >> 3) + (896u << 20)), (int)(b << 29));
+    return (b & 0x7fffffffu) == 0 ? __hiloint2double((int)b, 0) : (double)x;
+}
+
+__device__ __forceinline__ double new_util(const ComArgs &a, double m, float weight)
+{
+    const double s = widen(weight);
     const uint64_t b = (uint64_t)__double_as_longlong(m);
     if ((b & 0x7fffffffffffffffull) == 0x7ff0000000000000ull || a.rule == KVC_RULE_SINGLE) return s;
-    return a.rule == KVC_RULE_CUMULATIVE ? m + s : a.alpha * m + (1.0 - a.alpha) * s;
+    return a.rule == KVC_RULE_CUMULATIVE ? m + s : fma(a.alpha, m, a.beta * s);
 }
 
 // Long units: the utilities of kChunk slots, and the lowest key of every 32.
@@ -157,7 +169,7 @@ __global__ void __launch_bounds__(kThreads) tree_update_kernel(ComArgs a)
     for (int j = 0; j < kPer; j++) {
         const int i = i0 + j * kThreads;
         if (a.S && i < p.n) {
-            m[j] = new_util(a, m[j], (double)s[j]);
+            m[j] = new_util(a, m[j], s[j]);
             a.util[cb + i] = m[j];
         }
         uint64_t x = util_key(m[j]);
@@ -220,7 +232,7 @@ __device__ __forceinline__ void add_candidate(ComSmem &s, const Key &k)
 }
 
 template <bool kSplit>
-__global__ void __launch_bounds__(kThreads) tree_commit_kernel(ComArgs a)
+__global__ void __launch_bounds__(kThreads, 4) tree_commit_kernel(ComArgs a)
 {
     extern __shared__ __align__(16) unsigned char raw[];
     ComSmem &s = *reinterpret_cast<ComSmem *>(raw);
@@ -269,7 +281,7 @@ __global__ void __launch_bounds__(kThreads) tree_commit_kernel(ComArgs a)
             for (int j = 0; j < 4; j++) {
                 const int i = i0 + j * kThreads;
                 if (S && i < n) {
-                    m[j] = new_util(a, m[j], (double)x[j]);
+                    m[j] = new_util(a, m[j], x[j]);
                     util[i] = m[j];
                 }
                 mine = min((unsigned long long)mine, (unsigned long long)util_key(m[j]));
@@ -309,10 +321,12 @@ __global__ void __launch_bounds__(kThreads) tree_commit_kernel(ComArgs a)
                     if (y != kNone && y <= top) add_candidate(s, Key{y, tie_key(pos[i], i)});
                 }
             }
-        } else if (mine != kNone && mine <= top) {
-#pragma unroll 4
-            for (int i = tid; i < n; i += kThreads) {
-                const uint64_t x = util_key(util[i]);
+        } else {
+            // a warp looks through the slots of each of its threads that found one low
+            // (every kThreads-th slot: at most 32 of them)
+            for (unsigned todo = __ballot_sync(kFull, mine != kNone && mine <= top); todo; todo &= todo - 1) {
+                const int i = 32 * warp + __ffs(todo) - 1 + kThreads * lane;
+                const uint64_t x = i < n ? util_key(util[i]) : kNone;
                 if (x != kNone && x <= top) add_candidate(s, Key{x, tie_key(pos[i], i)});
             }
         }
@@ -453,34 +467,37 @@ __global__ void __launch_bounds__(kThreads) tree_commit_kernel(ComArgs a)
     const float4 kb = reinterpret_cast<const float4 *>(s.bar[0])[lane];
     const float4 dk = reinterpret_cast<const float4 *>(s.del[0])[lane];
     const float cross = n0 * (nb / n1) / n1, keep = n0 / n1, inv = 1.f / n1;
-#pragma unroll
-    for (int r0 = 0; r0 < 16; r0 += 8) {
+#pragma unroll 1
+    for (int r0 = 0; r0 < 16; r0 += 4) {
         const int row = 16 * warp + r0;
         float4 *c = reinterpret_cast<float4 *>(C + row * kD) + lane;
-        float4 old[8], m[8];
+        float4 old[4], m[4];
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
+        for (int i = 0; i < 4; i++) {
             old[i] = c[i * (kD / 4)];
             m[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
+        const float4 vb = *reinterpret_cast<const float4 *>(&s.bar[1][row]);
+#pragma unroll 2
         for (int j = 0; j < k; j++) {
             float4 y = reinterpret_cast<const float4 *>(kv + j * kD)[lane];
+            const float4 x4 = *reinterpret_cast<const float4 *>(vv + j * kD + row);
+            const float w = s.w[j];
             y.x -= kb.x;
             y.y -= kb.y;
             y.z -= kb.z;
             y.w -= kb.w;
-            const float w = s.w[j];
+            const float v[4] = {w * (x4.x - vb.x), w * (x4.y - vb.y), w * (x4.z - vb.z), w * (x4.w - vb.w)};
 #pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const float v = w * (vv[j * kD + row + i] - s.bar[1][row + i]);
-                m[i].x = fmaf(v, y.x, m[i].x);
-                m[i].y = fmaf(v, y.y, m[i].y);
-                m[i].z = fmaf(v, y.z, m[i].z);
-                m[i].w = fmaf(v, y.w, m[i].w);
+            for (int i = 0; i < 4; i++) {
+                m[i].x = fmaf(v[i], y.x, m[i].x);
+                m[i].y = fmaf(v[i], y.y, m[i].y);
+                m[i].z = fmaf(v[i], y.z, m[i].z);
+                m[i].w = fmaf(v[i], y.w, m[i].w);
             }
         }
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
+        for (int i = 0; i < 4; i++) {
             const float dv = cross * s.del[1][row + i];
             c[i * (kD / 4)] = make_float4(fmaf(dv, dk.x, fmaf(keep, old[i].x, m[i].x * inv)),
                                           fmaf(dv, dk.y, fmaf(keep, old[i].y, m[i].y * inv)),
@@ -502,7 +519,7 @@ cudaError_t launch_tree_commit(const kvc_params &p, int max_len, const TreeArgs 
     ComArgs a{t, pa, kt, vt, S, c.K, c.V, c.votes, c.pos, c.len, c.util, p.budget,
               m ? m->n : nullptr, m ? m->mu_k : nullptr, m ? m->mu_v : nullptr, m ? m->C : nullptr,
               evict_idx, evict_pos, n_evict, ws.status, ws.pend,
-              reinterpret_cast<uint64_t *>(ws.probs), (double)p.alpha, p.cap, p.L, p.rule, kmax,
+              reinterpret_cast<uint64_t *>(ws.probs), (double)p.alpha, 1.0 - (double)p.alpha, p.cap, p.L, p.rule, kmax,
               max_len, FastDiv(t.units)};
     const bool split = max_len > kLong;
     const size_t smem = sizeof(ComSmem) + (m ? 2 * (size_t)kmax * kD * sizeof(float) : 0);

@@ -413,7 +413,10 @@ tree_weights_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CU
             if (s.tiles == 0) break;
             const int qb = i % a.qbufs, cols = max(16, (s.acc * a.G + 15) & ~15);
             ok = __all_sync(kFull, tree_wait(&S.qfull[qb], (i / a.qbufs) & 1, &S.bad));
-            for (int t = (k ^ w) & 1; ok && t < s.tiles; t += 2) {
+            // alternate tiles; with a single accumulator one group takes them all (a wait
+            // for a phase must not begin before the phase ahead of it is over)
+            const int step = a.dbufs > 1 ? 2 : 1;
+            for (int t = step == 2 ? (k ^ w) & 1 : w ? s.tiles : 0; ok && t < s.tiles; t += step) {
                 const int at = (s.t0 + t) * kTile + r, kk = k + t, db = kk % a.dbufs;
                 const size_t slot = (size_t)s.u * a.cap + at;
                 float vote = 1.f;

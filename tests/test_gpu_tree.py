@@ -189,6 +189,21 @@ def test_attend_bounds_looser_than_the_lengths():
     c.check_attend()
 
 
+@pytest.mark.parametrize("i", [6, 8, 9, 15])
+def test_attend_gives_the_same_bits_again(i):
+    """Run after run, with the caches cold and warm: nothing depends on what lands first."""
+    per, G, T, lens, kw = ATTEND[i]
+    c = Case(100 + i, per, G, T, lens, **kw)
+    first = [x.clone() for x in c.run_attend()]
+    c.check_attend()
+    flush = torch.empty(64 << 20, dtype=torch.int32, device=DEV)
+    for r in range(40):
+        if r & 1:
+            flush.fill_(r)
+        for x, y in zip(first, c.run_attend()):
+            assert torch.equal(x, y)
+
+
 @pytest.mark.parametrize("where", ["k", "v", "both"])
 @pytest.mark.parametrize("value", [NAN, float("inf")])
 def test_attend_masked_branch_does_not_leak(where, value):
@@ -266,6 +281,41 @@ def test_weights(i, given):
         got = S[u, :lens[u] + a]
         assert (np.abs(got - ref) <= bound).all(), (u, (np.abs(got - ref) / bound).max())
         assert (S[u, lens[u] + a:] == -3).all(), "entries behind the last written"
+
+
+def test_weights_of_512_rows_over_many_tiles():
+    """64 accepted tokens of 8 heads fill the accumulator: several tiles per CTA through one."""
+    U, n, T, G = 2, 20100, 64, 8
+    g = torch.Generator(device=DEV)
+    g.manual_seed(1)
+
+    def rnd(*s):
+        return torch.randn(*s, generator=g, device=DEV).bfloat16()
+
+    Kc, q, kt = rnd(U, n + 70, 128), rnd(U, T, G, 128), rnd(U, T, 128)
+    ln = torch.full((U,), n, dtype=torch.int32, device=DEV)
+    pos = torch.zeros(U, n + 70, dtype=torch.int32, device=DEV)
+    util = torch.zeros(U, n + 70, dtype=torch.float64, device=DEV)
+    p = K.make_params(U, G, n + 70, n)
+    cache = K.make_cache(Kc, Kc, None, pos, util, ln)
+    mask = torch.from_numpy(tree_masks(np.random.default_rng(0), 1, T, "chain").view(np.int64)).to(DEV)
+    tree = K.make_tree(T, U, mask)
+    path = K.make_path(T, torch.arange(T, dtype=torch.int32, device=DEV)[None],
+                       torch.tensor([T], dtype=torch.int32, device=DEV),
+                       torch.zeros(1, dtype=torch.int32, device=DEV))
+    # any normalization will do: the log of the sum over the cache
+    x = torch.einsum("uthd,und->uthn", q.double(), Kc[:, :n].double()) * R.SCALE
+    lse = torch.logsumexp(x, -1).float()
+    S = torch.zeros(U, n + 70, device=DEV)
+    ws = torch.zeros(K.kvc_tree_workspace_size(p, T), dtype=torch.uint8, device=DEV)
+    K.kvc_tree_weights(p, n, tree, path, None, q, kt, lse, cache, S, ws)
+    assert K.kvc_get_device_status(ws) == 0
+    ref = torch.exp(x - lse.double().unsqueeze(-1)).mean(2).sum(1)
+    # every term is off by the logit's error (128 additions of products, |q||k| sums to
+    # about 100 here, and 16 half steps of a logarithm near 14), the sum by 512 additions
+    rel = (2 * 128 + 4) * R.E32 * float((q.double().abs().amax(-1).max() * 128 * R.SCALE
+                                         * Kc[:, :n].double().abs().amax())) + (16 * 14 + 512) * R.E32
+    assert float(((S[:, :n].double() - ref).abs() / ref).max()) <= rel
 
 
 def test_weights_sum_to_the_accepted_tokens():
