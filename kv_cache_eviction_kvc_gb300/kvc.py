@@ -324,9 +324,12 @@ def kvc_decode_attend_noalloc(p, t, new_pos, max_len, q, k_new, v_new, cache: kv
 # ------------------------------------------------------------------ drafted tokens
 
 def _sized(t, dtype, name, numel, device, optional=False):
-    """_ptr with the element count and the device checked: a row stride or a
-    unit count that does not fit the tensor is an error here, not a read out
-    of range on the device."""
+    """The address of a tensor, as _ptr, with the element count and the device
+    checked too: a row stride or a unit count that does not fit the tensor is
+    an error here, not a read out of range on the device."""
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == device
+            and t.is_contiguous() and t.numel() >= numel):
+        return t.data_ptr()
     ptr = _ptr(t, dtype, name, optional)
     if t is not None:
         if t.numel() < numel:
@@ -334,6 +337,16 @@ def _sized(t, dtype, name, numel, device, optional=False):
         if t.device.index != device:
             raise ValueError(f"{name} must live on the current device cuda:{device}, not {t.device}")
     return ptr
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_on(stream, device):
+    """_stream, without building a Stream object where torch gives the handle."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device)
+    return _stream(stream)
 
 
 def make_tree(T, units, mask, n=None) -> kvc_tree:
@@ -368,11 +381,11 @@ def make_path(A, token, n, pos) -> kvc_path:
 def _tree_device(p, tree, path=None):
     """The current device; the tree (and path) must live there and cover the units."""
     dev = torch.cuda.current_device()
-    for x in (tree, path) if path is not None else (tree,):
-        if x.keep[0].device.index != dev:
-            raise ValueError(f"the tree and path must live on the current device cuda:{dev}")
-        if tree.units < 1 or x.trees * tree.units < p.U:
-            raise ValueError(f"{x.trees} trees of {tree.units} units do not cover U = {p.U}")
+    if tree.keep[0].get_device() != dev or (path is not None and path.keep[0].get_device() != dev):
+        raise ValueError(f"the tree and path must live on the current device cuda:{dev}")
+    if tree.units < 1 or tree.trees * tree.units < p.U or (
+            path is not None and path.trees * tree.units < p.U):
+        raise ValueError(f"the trees of {tree.units} units do not cover U = {p.U}")
     return dev
 
 
@@ -391,7 +404,7 @@ def kvc_tree_attend(p, max_len, tree: kvc_tree, q, k_tree, v_tree, cache: kvc_ca
         _sized(v_tree, bf, "v_tree", rows * p.d, dev), ctypes.byref(cache),
         None if mom is None else ctypes.byref(mom), _sized(o, bf, "o", rows * p.G * p.d, dev),
         _sized(lse, torch.float32, "lse", rows * p.G, dev), _sized(ws, torch.uint8, "ws", 0, dev),
-        ws.numel(), _stream(stream)))
+        ws.numel(), _stream_on(stream, dev)))
 
 
 def kvc_tree_weights(p, max_len, tree: kvc_tree, path: kvc_path, row_weight, q, k_tree, lse,
@@ -405,7 +418,7 @@ def kvc_tree_weights(p, max_len, tree: kvc_tree, path: kvc_path, row_weight, q, 
         _sized(q, bf, "q", rows * p.G * p.d, dev), _sized(k_tree, bf, "k_tree", rows * p.d, dev),
         _sized(lse, f32, "lse", rows * p.G, dev), ctypes.byref(cache),
         _sized(S, f32, "S", p.U * p.cap, dev), _sized(ws, torch.uint8, "ws", 0, dev), ws.numel(),
-        _stream(stream)))
+        _stream_on(stream, dev)))
 
 
 def kvc_tree_commit(p, max_len, tree: kvc_tree, path: kvc_path, k_tree, v_tree, S,
@@ -423,7 +436,7 @@ def kvc_tree_commit(p, max_len, tree: kvc_tree, path: kvc_path, k_tree, v_tree, 
         _sized(evict_idx, i32, "evict_idx", p.U * int(kmax), dev, optional=True),
         _sized(evict_pos, i32, "evict_pos", p.U * int(kmax), dev, optional=True),
         _sized(n_evict, i32, "n_evict", p.U, dev), _sized(ws, torch.uint8, "ws", 0, dev),
-        ws.numel(), _stream(stream)))
+        ws.numel(), _stream_on(stream, dev)))
 
 
 # ------------------------------------------------------------------ prefill
