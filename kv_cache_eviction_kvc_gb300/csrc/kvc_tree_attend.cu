@@ -917,7 +917,7 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
 
 struct JoinArgs {
     AttArgs a;
-    const float *mn, *mu_k, *mu_v;
+    const float *mn, *mu_k, *mu_v, *C;
     int first_order, grid;
 };
 
@@ -993,185 +993,333 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
 
 // The normalization correction: every row's sum normalised and mixed with the
 // evicted set's estimate.  Bound by bytes: 64 KB of C per unit, 1 KB per row.
-// A persistent CTA per SM takes 64 rows of an item at a time; C, the rows' q
-// and their sums come by TMA into two stages (128-byte swizzle, so that the
-// fragment reads below hit all banks).  C q runs on mma.sync with C as two
-// bf16 terms (2^-16 of a product) taken apart as its fragments are read; warp
-// w has 16 rows and half of the columns.
+// A persistent CTA per SM takes 64 rows of an item at a time.  C q runs on
+// tcgen05 with C as two bf16 terms (2^-16 of a product), which the eight
+// worker warps take apart in registers: while they finish one job, the next
+// one is on the tensor core and C of the one after is on its way.
+//   warps 0-7  C to bf16 terms; outputs (a thread per row, warps of lane
+//              quarters 0 and 1) and q . mu_k (the other warps)
+//   warp 8     producer of q and the sums (TMA), warp 9 MMA issuer
 constexpr int kMomRows = 64;
-constexpr int kMomC = kD * kD * 4, kMomQ = kMomRows * kD * 2, kMomF = kMomRows * kD * 4;
-constexpr int kMomStage = kMomC + kMomQ + kMomF;
-constexpr size_t kMomDyn = 2 * (size_t)kMomStage;
+constexpr int kMomThreads = 320;
+constexpr int kMomQ = kMomRows * kD * 2, kMomF = kMomRows * kD * 4;
+struct MomSmem {
+    float muk[2][kD], muv[2][kD], z[2][kMomRows];
+    // (two of each: a wait for one job's phase is never two phases behind)
+    uint64_t ffull[2], fempty[2], pready[2], mdone[2], wsync;
+    int bad;
+    uint32_t tmem;
+};
+// the two terms of C, of two jobs | q of two jobs | sums of two jobs
+constexpr size_t kMomDyn = 4 * (size_t)kSlot + 2 * (kMomQ + kMomF) + sizeof(MomSmem);
+static_assert(kMomDyn <= 227 * 1024, "one block's shared memory");
 
-// Byte offset of columns (c, c + 1) of row r: boxes of 32 fp32 columns x kRows.
-template <int kRowsOfBox>
-__device__ __forceinline__ uint32_t mom_off(int r, int c)
+// One job: 64 rows of an item.  rows <= 0: nothing to do.
+struct MomJob {
+    int u, row0, rows, sid;       // unit, first row of it, rows, place of the sums
+    int r0;                       // first row of the item
+    float ne;
+};
+
+__device__ __forceinline__ MomJob mom_job(const JoinArgs &j, const LineCuts &cuts, int per, int job)
 {
-    return (uint32_t)((c >> 5) * kRowsOfBox * 128 + r * 128 + ((((c & 31) >> 2) ^ (r & 7)) << 4) +
-                      (c & 3) * 4);
+    const AttArgs &a = j.a;
+    MomJob m;
+    const int item = job / per;
+    m.u = a.by_rb(item);
+    const int rb = item - m.u * a.RB, n = a.len[m.u], live = a.live(m.u);
+    m.r0 = (job - item * per) * kMomRows;
+    m.row0 = rb * kRows + m.r0;
+    m.rows = n < 0 || n > a.max_len || live < 0
+                 ? 0 : min(kMomRows, min(kRows, (live << a.gshift) - rb * kRows) - m.r0);
+    m.ne = j.mn[m.u];
+    // the part that has the item's start (its place has the joined sums)
+    m.sid = m.rows > 0 ? item + cuts.part(a.whole ? item : a.first[item]) : 0;
+    return m;
 }
 
-__global__ void __launch_bounds__(256, 1)
+__global__ void __launch_bounds__(kMomThreads, 1)
 tree_moment_kernel(const __grid_constant__ JoinArgs j, const __grid_constant__ CUtensorMap tmQ,
-                   const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmF)
+                   const __grid_constant__ CUtensorMap tmF)
 {
     const AttArgs &a = j.a;
     extern __shared__ __align__(1024) unsigned char dyn[];
-    __shared__ uint64_t full[2];
-    __shared__ int bad;
+    unsigned char *planes = dyn, *qs = planes + 4 * kSlot, *fs = qs + 2 * kMomQ;
+    MomSmem &S = *reinterpret_cast<MomSmem *>(fs + 2 * kMomF);
     if (smem_u32(dyn) & 1023) {
         if (threadIdx.x == 0) record_status(a.status, KVC_ERR_CUDA);
         return;
     }
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int g = lane >> 2, t = lane & 3, n0 = 64 * (warp & 1), m0 = 16 * (warp >> 1);
-    const int items = a.U * a.RB, per = (a.rows + kMomRows - 1) / kMomRows;
-    const float sd = rsqrtf((float)kD);
+    const int items = a.U * a.RB, per = (a.rows + kMomRows - 1) / kMomRows, jobs = items * per;
     if (tid == 0) {
-        bad = 0;
-        mbar_init(&full[0], 1);
-        mbar_init(&full[1], 1);
+        S.bad = 0;
+        mbar_init(&S.wsync, 8);
+        for (int i = 0; i < 2; i++) {
+            mbar_init(&S.ffull[i], 1);
+            mbar_init(&S.fempty[i], 8);
+            mbar_init(&S.pready[i], 8);
+            mbar_init(&S.mdone[i], 1);
+        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    const int W = a.whole ? 0 : a.first[items];
-    const LineCuts cuts(j.grid, a.whole ? items : W);
-    // job -> item, first row, rows; 0 rows: nothing to do
-    auto job_of = [&](int job, int &item, int &u, int &r0, int &nr, int &sid) {
-        item = job / per;
-        u = a.by_rb(item);
-        const int rb = item - u * a.RB;
-        r0 = (job - item * per) * kMomRows;
-        const int n = a.len[u], live = a.live(u);
-        nr = n < 0 || n > a.max_len || live < 0
-                 ? 0 : min(kMomRows, min(kRows, (live << a.gshift) - rb * kRows) - r0);
-        // the part that has the item's start (its place has the joined sums)
-        if (nr > 0) sid = item + cuts.part(a.whole ? item : a.first[item]);
-    };
-    auto load = [&](int job, int st) {
-        int item, u, r0, nr, sid;
-        job_of(job, item, u, r0, nr, sid);
-        if (nr <= 0) {
-            mbar_arrive(&full[st]);
-            return;
-        }
-        const bool mix = j.mn[u] > 0.f, c = mix && j.first_order;
-        unsigned char *d = dyn + st * kMomStage;
-        mbar_expect_tx(&full[st], kMomF + (mix ? kMomQ : 0) + (c ? kMomC : 0));
-        if (c)
-            for (int i = 0; i < 4; i++) tma_3d(d + i * (kMomC / 4), &tmC, 32 * i, 0, u, &full[st]);
-        if (mix)
-            for (int i = 0; i < 2; i++)
-                tma_3d(d + kMomC + i * (kMomQ / 2), &tmQ, 64 * i, (item - u * a.RB) * kRows + r0, u, &full[st]);
-        for (int i = 0; i < 4; i++)
-            tma_3d(d + kMomC + kMomQ + i * (kMomF / 4), &tmF, 32 * i, r0, sid, &full[st]);
-    };
+    if (warp == 9) tmem_alloc(&S.tmem, 256);
     __syncthreads();
-    const int jobs = items * per;
-    if (tid == 0)
-        for (int i = 0; i < 2; i++)
-            if ((int)(blockIdx.x + i * gridDim.x) < jobs) load(blockIdx.x + i * gridDim.x, i);
-    int k = 0;
-    for (int job = blockIdx.x; job < jobs; job += gridDim.x, k++) {
-        const int st = k & 1;
-        int item, u, r0, nr, sid;
-        job_of(job, item, u, r0, nr, sid);
-        const unsigned char *cs = dyn + st * kMomStage, *qs = cs + kMomC, *fs = qs + kMomQ;
-        const float ne = nr > 0 ? j.mn[u] : 0.f;
-        const bool mix = ne > 0.f;
-        float2 ml[2];
-        float z[2] = {0.f, 0.f}, mk[8][4], mv[8][2];
-        if (nr > m0) {
-#pragma unroll
-            for (int h = 0; h < 2; h++)
-                ml[h] = a.ml[(size_t)sid * a.rows + r0 + min(m0 + g + 8 * h, nr - 1)];
-            if (mix) {
-#pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    const float *v = j.mu_v + (size_t)u * kD + n0 + 8 * i + 2 * t;
-                    mv[i][0] = v[0];
-                    mv[i][1] = v[1];
-                    const float *mu = j.mu_k + (size_t)u * kD + 16 * i + 2 * t;
-                    mk[i][0] = mu[0];
-                    mk[i][1] = mu[1];
-                    mk[i][2] = mu[8];
-                    mk[i][3] = mu[9];
-                }
+    tc_fence_after();
+    const uint32_t tmem = S.tmem;
+    const LineCuts cuts(j.grid, a.whole ? items : a.first[items]);
+    if (warp == 8) {
+        if (elect_one()) {
+            bool ok = true;
+            int kf = 0;                          // jobs with rows
+            for (int job = blockIdx.x; ok && job < jobs; job += gridDim.x) {
+                const MomJob m = mom_job(j, cuts, per, job);
+                if (m.rows <= 0) continue;
+                const bool mix = m.ne > 0.f;
+                const int st = kf & 1;
+                if (kf >= 2) ok = tree_wait(&S.fempty[st], (kf / 2 - 1) & 1, &S.bad);
+                if (!ok) break;
+                mbar_expect_tx(&S.ffull[st], kMomF + (mix ? kMomQ : 0));
+                for (int i = 0; i < 4; i++)
+                    tma_3d(fs + st * kMomF + i * (kMomF / 4), &tmF, 32 * i, m.r0, m.sid, &S.ffull[st]);
+                if (mix)
+                    for (int i = 0; i < 2; i++)
+                        tma_3d(qs + st * kMomQ + i * (kMomQ / 2), &tmQ, 64 * i, m.row0, m.u, &S.ffull[st]);
+                kf++;
+            }
+            if (!ok) {
+                S.bad = 1;
+                // the copies in flight land before the block ends
+                for (int i = max(0, kf - 2); i < kf; i++) mbar_wait(&S.ffull[i & 1], (i / 2) & 1);
             }
         }
-        if (!tree_wait(&full[st], (k >> 1) & 1, &bad)) bad = 1;
-        if (nr > m0) {
-            float d[8][4];
+        __syncwarp();
+    } else if (warp == 9) {
+        if (elect_one()) {
+            bool ok = true;
+            int kf = 0, kc = 0;
+            const uint64_t c0 = umma_sdesc(smem_u32(planes));
+            for (int job = blockIdx.x; ok && job < jobs; job += gridDim.x) {
+                const MomJob m = mom_job(j, cuts, per, job);
+                if (m.rows <= 0) continue;
+                const int st = kf & 1;
+                if (m.ne > 0.f && j.first_order) {
+                    ok = tree_wait(&S.ffull[st], (kf / 2) & 1, &S.bad);
+                    ok = ok && tree_wait(&S.pready[kc & 1], (kc >> 1) & 1, &S.bad);
+                    if (!ok) break;
+                    tc_fence_after();
+                    // rows 64 .. 127 of the operand are whatever lies behind: their lanes
+                    // are not read
+                    const uint64_t q0 = umma_sdesc(smem_u32(qs + st * kMomQ));
+                    const uint32_t d = tmem + 128 * (kc & 1);
 #pragma unroll
-            for (int i = 0; i < 8; i++) d[i][0] = d[i][1] = d[i][2] = d[i][3] = 0.f;
-            if (mix) {
-                uint32_t q[8][4];
-#pragma unroll
-                for (int ks = 0; ks < 8; ks++) {
-                    // ldmatrix: rows m0 .. m0 + 15 in the two 8-column chunks of the step
-                    const int row = m0 + (lane & 15), ch = 2 * ks + (lane >> 4);
-                    ldsm_x4(smem_u32(qs) + sw_off_t<64>(row, ch), q[ks][0], q[ks][1], q[ks][2], q[ks][3]);
-                    // q . mu_k of rows g and g + 8
-#pragma unroll
-                    for (int h = 0; h < 4; h++)
-                        z[h & 1] += bf_lo(q[ks][h]) * mk[ks][h & 2] + bf_hi(q[ks][h]) * mk[ks][(h & 2) + 1];
-                }
-                if (j.first_order) {
-#pragma unroll
-                    for (int ks = 0; ks < 8; ks++)
-#pragma unroll
-                        for (int i = 0; i < 8; i++) {
-                            uint32_t hi[2], lo[2];
-#pragma unroll
-                            for (int h = 0; h < 2; h++) {
-                                const float2 x = *reinterpret_cast<const float2 *>(
-                                    cs + mom_off<kD>(n0 + 8 * i + g, 16 * ks + 8 * h + 2 * t));
-                                hi[h] = pack_bf16(x.x, x.y);
-                                lo[h] = pack_bf16(x.x - bf_lo(hi[h]), x.y - bf_hi(hi[h]));
-                            }
-                            mma16816(d[i], q[ks][0], q[ks][1], q[ks][2], q[ks][3], lo[0], lo[1]);
-                            mma16816(d[i], q[ks][0], q[ks][1], q[ks][2], q[ks][3], hi[0], hi[1]);
-                        }
-                }
-            }
-            const size_t ubase = (size_t)u * a.TG + (size_t)(item - u * a.RB) * kRows + r0;
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-                const int row = m0 + g + 8 * h;
-                const float lse = ml[h].y == 0.f ? -INFINITY : (ml[h].x + log2f(ml[h].y)) * 0.6931471805599453f;
-                float w = 1.f;
-                if (mix) {
-                    float x = z[h];
-                    x += __shfl_xor_sync(kFull, x, 1);
-                    x += __shfl_xor_sync(kFull, x, 2);
-                    w = 1.f / (1.f + expf(logf(ne) + sd * x - lse));
-                }
-                const float wf = ml[h].y == 0.f ? 0.f : w / ml[h].y, we = 1.f - w;
-                uint32_t *o = reinterpret_cast<uint32_t *>(a.o + (ubase + row) * kD + n0 + 2 * t);
-                if (row < nr && !bad) {
-#pragma unroll
-                    for (int i = 0; i < 8; i++) {
-                        const float2 x = *reinterpret_cast<const float2 *>(
-                            fs + mom_off<kMomRows>(row, n0 + 8 * i + 2 * t));
-                        float f0 = wf * x.x, f1 = wf * x.y;
-                        if (mix) {
-                            f0 += we * (mv[i][0] + sd * d[i][2 * h]);
-                            f1 += we * (mv[i][1] + sd * d[i][2 * h + 1]);
-                        }
-                        o[4 * i] = pack_bf16(f0, f1);
+                    for (int x = 0; x < 16; x++) {
+                        const int ks = x & 7;
+                        umma_bf16(d, q0 + (uint64_t)((ks >> 2) * (kMomQ / 2 >> 4) + (ks & 3) * 2),
+                                  umma_sdesc_step(c0 + (uint64_t)((2 * (kc & 1) + (x >> 3)) * (kSlot >> 4)), ks),
+                                  kIdescS, x > 0);
                     }
-                    if (t == 0 && n0 == 0) a.lse[ubase + row] = lse;
+                    umma_commit(&S.mdone[kc & 1]);
+                    kc++;
                 }
+                kf++;
+            }
+            // (a wait that ran out: the MMAs issued before are done when mdone says so)
+            if (!ok) {
+                S.bad = 1;
+                if (kc > 0) mbar_wait(&S.mdone[(kc - 1) & 1], ((kc - 1) >> 1) & 1);
             }
         }
-        __syncthreads();                                     // the stage is read
-        if (bad) {
-            // the copies in flight land before the block ends
-            if (tid == 0) mbar_wait(&full[st ^ 1], ((k + 1) >> 1) & 1);
-            break;
+        __syncwarp();
+    } else {
+        const float sd = rsqrtf((float)kD);
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const int col0 = 64 * (warp >> 2);
+        bool ok = true;
+        int kf = 0, kc = 0;
+        uint32_t wph = 0;
+        auto wait = [&](uint64_t *b, uint32_t ph) { ok = __all_sync(kFull, tree_wait(b, ph, &S.bad)) && ok; };
+        auto sync = [&] {                                    // the eight warps
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.wsync);
+            wait(&S.wsync, wph);
+            wph ^= 1;
+        };
+        // C of a unit: 16-byte chunks of eight elements, on their way in registers
+        float4 cr[16];
+        auto fetch = [&](int u) {
+            const float4 *C = reinterpret_cast<const float4 *>(j.C + (size_t)u * kD * kD);
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                cr[2 * i] = C[2 * (i * 256 + tid)];
+                cr[2 * i + 1] = C[2 * (i * 256 + tid) + 1];
+            }
+        };
+        // what was fetched into its two terms; c: the count of products before
+        auto terms = [&](int c) {
+            if (c > 1) wait(&S.mdone[c & 1], ((c >> 1) - 1) & 1);   // the terms of two jobs ago are used up
+            if (!ok) return;
+            unsigned char *to = planes + (c & 1) * 2 * kSlot;
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const int e = i * 256 + tid, row = e >> 4, ch = e & 15;
+                const float4 x = cr[2 * i], y = cr[2 * i + 1];
+                const uint4 hi = make_uint4(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w), pack_bf16(y.x, y.y),
+                                            pack_bf16(y.z, y.w));
+                const uint4 lo = make_uint4(pack_bf16(x.x - bf_lo(hi.x), x.y - bf_hi(hi.x)),
+                                            pack_bf16(x.z - bf_lo(hi.y), x.w - bf_hi(hi.y)),
+                                            pack_bf16(y.x - bf_lo(hi.z), y.y - bf_hi(hi.z)),
+                                            pack_bf16(y.z - bf_lo(hi.w), y.w - bf_hi(hi.w)));
+                unsigned char *d = to + sw_off_t<128>(row, ch);
+                *reinterpret_cast<uint4 *>(d) = hi;
+                *reinterpret_cast<uint4 *>(d + kSlot) = lo;
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.pready[c & 1]);
+        };
+        // the rows of a job; f, c: counts of jobs and of products before it; the
+        // thread's dimension of the means
+        auto finish = [&](const MomJob &m, int f, int c, float mk1, float mv1, float2 ml) {
+            const int st = f & 1;
+            const bool mix = m.ne > 0.f, prod = mix && j.first_order;
+            wait(&S.ffull[st], (f / 2) & 1);
+            if (prod) wait(&S.mdone[c & 1], (c >> 1) & 1);
+            if (mix && tid < kD) {
+                S.muk[st][tid] = mk1;
+                S.muv[st][tid] = mv1;
+            }
+            if (ok) sync();
+            if (!ok) return;
+            tc_fence_after();
+            if (mix && (warp & 2)) {
+                // q . mu_k: these four warps have 16 rows each, eight lanes a row of
+                // 16 dimensions (two 16-byte chunks)
+                const int q = 16 * (2 * (warp >> 2) + (warp & 1));
+                const float ln = logf(m.ne);
+                float z[4];
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const int r = q + 4 * i + (lane >> 3);
+                    z[i] = 0.f;
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        const int ch = (lane & 7) + 8 * h;
+                        float f[8];
+                        unpack8(lds_v4(qs + st * kMomQ + sw_off_t<64>(r, ch)), f);
+#pragma unroll
+                        for (int e = 0; e < 8; e++) z[i] = fmaf(f[e], S.muk[st][8 * ch + e], z[i]);
+                    }
+                }
+#pragma unroll
+                for (int d = 1; d < 8; d <<= 1)
+#pragma unroll
+                    for (int i = 0; i < 4; i++) z[i] += __shfl_xor_sync(kFull, z[i], d);
+                if ((lane & 7) == 0)
+#pragma unroll
+                    for (int i = 0; i < 4; i++) S.z[st][q + 4 * i + (lane >> 3)] = ln + sd * z[i];
+            }
+            sync();
+            if (!ok) return;
+            const int row = 32 * (warp & 3) + lane;
+            if (!(warp & 2) && row - lane < m.rows) {
+                const float lse = ml.y == 0.f ? -INFINITY : (ml.x + log2f(ml.y)) * 0.6931471805599453f;
+                const float w = mix ? 1.f / (1.f + expf(S.z[st][row] - lse)) : 1.f;
+                const float wf = ml.y == 0.f ? 0.f : w / ml.y, we = 1.f - w, ws = we * sd;
+                const size_t orow = (size_t)m.u * a.TG + (size_t)(m.row0 + row);
+#pragma unroll 2
+                for (int h = 0; h < 4; h++) {
+                    const int c0 = col0 + 16 * h;
+                    uint32_t y[16];
+                    if (prod) {
+                        tmem_ld16_async(tmem + lanes + 128 * (c & 1) + c0, y);
+                        tmem_wait_ld();
+                        tmem_bind16(y);
+                    }
+                    float o[16];
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const float4 x = *reinterpret_cast<const float4 *>(
+                            fs + st * kMomF + (c0 >> 5) * (kMomF / 4) + row * 128 +
+                            (((((c0 & 31) >> 2) + i) ^ (row & 7)) << 4));
+                        o[4 * i] = wf * x.x;
+                        o[4 * i + 1] = wf * x.y;
+                        o[4 * i + 2] = wf * x.z;
+                        o[4 * i + 3] = wf * x.w;
+                        if (mix) {
+                            const float4 v = *reinterpret_cast<const float4 *>(&S.muv[st][c0 + 4 * i]);
+                            o[4 * i] = fmaf(we, v.x, o[4 * i]);
+                            o[4 * i + 1] = fmaf(we, v.y, o[4 * i + 1]);
+                            o[4 * i + 2] = fmaf(we, v.z, o[4 * i + 2]);
+                            o[4 * i + 3] = fmaf(we, v.w, o[4 * i + 3]);
+                        }
+                    }
+                    if (prod)
+#pragma unroll
+                        for (int i = 0; i < 16; i++) o[i] = fmaf(ws, __uint_as_float(y[i]), o[i]);
+                    if (row < m.rows) {
+                        uint4 *d = reinterpret_cast<uint4 *>(a.o + orow * kD + c0);
+                        d[0] = make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]),
+                                          pack_bf16(o[6], o[7]));
+                        d[1] = make_uint4(pack_bf16(o[8], o[9]), pack_bf16(o[10], o[11]),
+                                          pack_bf16(o[12], o[13]), pack_bf16(o[14], o[15]));
+                    }
+                }
+                if (row < m.rows && col0 == 0) a.lse[orow] = lse;
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.fempty[st]);
+        };
+        // the next job with rows from `job` on (jobs: there is none)
+        auto next = [&](int job, MomJob &m) {
+            for (; job < jobs; job += gridDim.x) {
+                m = mom_job(j, cuts, per, job);
+                if (m.rows > 0) break;
+            }
+            return min(job, jobs);
+        };
+        MomJob last, m;
+        last.rows = 0;
+        int lc = 0;
+        float mk1 = 0.f, mv1 = 0.f, mk2 = 0.f, mv2 = 0.f;
+        float2 ml1 = make_float2(0.f, 0.f), ml2 = ml1;
+        auto ahead = [&](const MomJob &x) {
+            if (x.ne > 0.f) {
+                if (j.first_order) fetch(x.u);
+                if (tid < kD) {
+                    mk2 = j.mu_k[(size_t)x.u * kD + tid];
+                    mv2 = j.mu_v[(size_t)x.u * kD + tid];
+                }
+            }
+            ml2 = a.ml[(size_t)x.sid * a.rows + x.r0 + min(32 * (warp & 1) + lane, x.rows - 1)];
+        };
+        int job = next(blockIdx.x, m);
+        if (job < jobs) ahead(m);
+        while (ok && job < jobs) {
+            const int c = kc;
+            if (m.ne > 0.f && j.first_order) terms(kc++);
+            const float mk3 = mk2, mv3 = mv2;
+            const float2 ml3 = ml2;
+            MomJob n;
+            job = next(job + gridDim.x, n);
+            if (job < jobs) ahead(n);
+            if (ok && last.rows > 0) finish(last, kf - 1, lc, mk1, mv1, ml1);
+            last = m;
+            m = n;
+            lc = c;
+            mk1 = mk3;
+            mv1 = mv3;
+            ml1 = ml3;
+            kf++;
         }
-        if (tid == 0 && job + 2 * (int)gridDim.x < jobs) load(job + 2 * gridDim.x, st);
+        if (ok && last.rows > 0) finish(last, kf - 1, lc, mk1, mv1, ml1);
+        if (!ok && lane == 0) S.bad = 1;
     }
-    if (tid == 0 && bad) record_status(a.status, KVC_ERR_TIMEOUT);
+    __syncthreads();
+    if (warp == 9) tmem_dealloc(tmem, 256);
+    if (tid == 0 && S.bad) record_status(a.status, KVC_ERR_TIMEOUT);
 }
 
 struct TreeWs {
@@ -1235,7 +1383,7 @@ cudaError_t launch_tree_attend(const kvc_params &p, int max_len, const TreeArgs 
     kernel<<<(int)grid, kThreads, kDyn, st>>>(a, mk, mv, mq, mkt, mvt);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (m == nullptr && whole) return cudaSuccess;
-    JoinArgs j{a, m ? m->n : nullptr, m ? m->mu_k : nullptr, m ? m->mu_v : nullptr,
+    JoinArgs j{a, m ? m->n : nullptr, m ? m->mu_k : nullptr, m ? m->mu_v : nullptr, m ? m->C : nullptr,
                p.correction == KVC_CORR_FIRST_ORDER, (int)grid};
     if (!whole) {
         const dim3 g((unsigned)grid, (a.rows + 8 * kJoinRows - 1) / (8 * kJoinRows));
@@ -1244,15 +1392,13 @@ cudaError_t launch_tree_attend(const kvc_params &p, int max_len, const TreeArgs 
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     if (m) {
-        CUtensorMap mc, mf;
-        if (!make_f32_map(&mc, m->C, p.U, kD, kD) ||
-            !make_f32_map(&mf, w.part, items + kGrid, a.rows, kMomRows))
-            return cudaErrorInvalidValue;
+        CUtensorMap mf;
+        if (!make_f32_map(&mf, w.part, items + kGrid, a.rows, kMomRows)) return cudaErrorInvalidValue;
         e = cudaFuncSetAttribute(tree_moment_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)kMomDyn);
         if (e != cudaSuccess) return e;
         const long long jobs = items * ((a.rows + kMomRows - 1) / kMomRows);
-        tree_moment_kernel<<<(int)(jobs < kGrid ? jobs : kGrid), 256, kMomDyn, st>>>(j, mq, mc, mf);
+        tree_moment_kernel<<<(int)(jobs < kGrid ? jobs : kGrid), kMomThreads, kMomDyn, st>>>(j, mq, mf);
     }
     return cudaGetLastError();
 }
