@@ -273,28 +273,30 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float sca
     uint32_t c[32], d[32];
     {
         uint32_t a[32], b[32];
+        float mx[2] = {-INFINITY, -INFINITY};
+        auto top_of = [&](uint32_t (&y)[32], uint32_t keep) {
+            hide32<kMask>(y, keep);
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+                mx[0] = fmaxf(fmaxf(mx[0], __uint_as_float(y[j])), __uint_as_float(y[j + 1]));
+                mx[1] = fmaxf(fmaxf(mx[1], __uint_as_float(y[j + 2])), __uint_as_float(y[j + 3]));
+            }
+        };
         tmem_ld32_async(tS, a);
         tmem_ld32_async(tS + 32, b);
-        tmem_ld32_async(tS + 64, c);
-        tmem_ld32_async(tS + 96, d);
         tmem_wait_ld();
         tmem_bind(a);
         tmem_bind(b);
+        tmem_ld32_async(tS + 64, c);
+        top_of(a, (uint32_t)keep0);
+        tmem_ld32_async(tS + 96, d);
+        top_of(b, (uint32_t)(keep0 >> 32));
+        tmem_wait_ld();
         tmem_bind(c);
         tmem_bind(d);
-        hide32<kMask>(a, (uint32_t)keep0);
-        hide32<kMask>(b, (uint32_t)(keep0 >> 32));
-        hide32<kMask>(c, (uint32_t)keep1);
-        hide32<kMask>(d, (uint32_t)(keep1 >> 32));
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-            mx[0] = fmaxf(fmaxf(mx[0], __uint_as_float(a[j])), __uint_as_float(a[j + 1]));
-            mx[1] = fmaxf(fmaxf(mx[1], __uint_as_float(b[j])), __uint_as_float(b[j + 1]));
-            mx[2] = fmaxf(fmaxf(mx[2], __uint_as_float(c[j])), __uint_as_float(c[j + 1]));
-            mx[3] = fmaxf(fmaxf(mx[3], __uint_as_float(d[j])), __uint_as_float(d[j + 1]));
-        }
-        top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+        top_of(c, (uint32_t)keep1);
+        top_of(d, (uint32_t)(keep1 >> 32));
+        top = fmaxf(mx[0], mx[1]) * scale;
     }
     const bool move = top > m + kSlack || (m == -INFINITY && top > m);
     if (__any_sync(kFull, move)) {
@@ -348,16 +350,17 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float sca
         tmem_st16(at, p);
     };
     uint32_t a[32], b[32];
-    tmem_ld32_async(tS, a);
     weights(c, tS + 64, vote + 64);
-    tmem_ld32_async(tS + 32, b);
+    tmem_ld32_async(tS, a);
     weights(d, tS + 80, vote + 96);
     tmem_wait_ld();
     tmem_bind(a);
-    tmem_bind(b);
+    tmem_ld32_async(tS + 32, b);
     hide32<kMask>(a, (uint32_t)keep0);
-    hide32<kMask>(b, (uint32_t)(keep0 >> 32));
     weights(a, tS, vote);
+    tmem_wait_ld();
+    tmem_bind(b);
+    hide32<kMask>(b, (uint32_t)(keep0 >> 32));
     weights(b, tS + 16, vote + 32);
     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
     tmem_wait_st();
@@ -719,36 +722,35 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
             float m = -INFINITY, l = 0.f;
             bool begun = false;                              // O has a tile's product
             uint64_t see = 0;                                // drafted tokens the row sees
-            int vote_next = 0;                               // votes: loaded two tiles ahead,
-                                                             // in shared memory one ahead
             {
                 const int live = s.live, u = s.u;
                 if (row < rows)
                     see = a.t.mask[(size_t)a.by_units(u) * a.t.T + ((s.rb * kRows + row) >> a.gshift)] &
                           (live >= 64 ? ~0ull : (1ull << live) - 1);
-                // (a group without a tile here must not write: the maxima and sums of the
-                // item's end share the space, and only tiles order the group's warps)
+                // the first tile's votes (a group without a tile here must not write: the
+                // maxima and sums of the item's end share the space)
                 if (kVotes && s.t0 + (dual ? 0 : w) < s.t1) {
                     const int at = (s.t0 + (dual ? 0 : w)) * kTile + r;
-                    const int32_t *v = a.votes + (size_t)u * a.cap + at;
-                    S.g[w].vote[job & 1][r] = at < s.n ? (float)v[0] : 1.f;
-                    if (at + step * kTile < s.n) vote_next = v[step * kTile];
+                    S.g[w].vote[job & 1][r] = at < s.n ? (float)a.votes[(size_t)u * a.cap + at] : 1.f;
+                    group_sync();
+                    if (!ok) break;
                 }
             }
             for (int tile = s.t0 + (dual ? 0 : w); tile < s.t1; tile += step) {
                 const bool tree = tile == s.nt - 1;
                 const int nv = tree ? s.live : min(kTile, s.n - tile * kTile);
+                // the next tile's votes, on their way while S is waited for
+                int vote_next = 1;
                 if (kVotes) {
-                    group_sync();        // this tile's votes are there, the last one's are read
-                    if (!ok) break;
                     const int at = (tile + step) * kTile + r;
-                    S.g[w].vote[(job + 1) & 1][r] = at < s.n ? (float)vote_next : 1.f;
-                    if (at + step * kTile < s.n)
-                        vote_next = a.votes[(size_t)s.u * a.cap + at + step * kTile];
+                    if (at < s.n) vote_next = a.votes[(size_t)s.u * a.cap + at];
                 }
                 wait(&S.sfull[w], job & 1);
                 if (!ok) break;
                 tc_fence_after();
+                // S was issued when all four warps had handed over the group's last weights:
+                // they are done with the other buffer, and this one has been written
+                if (kVotes) S.g[w].vote[(job + 1) & 1][r] = (float)vote_next;
                 // value rows the MMA reads that are no slot: zero.  (After S: the issuer has
                 // then taken the ring entry that used the slot before, so that the parity
                 // below cannot be that of an earlier phase.)
