@@ -175,6 +175,31 @@ inline bool make_unit_map(CUtensorMap *m, const void *base, uint64_t units, uint
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A kernel that follows another of the same call: its launch overlaps the end of
+// the one before (programmatic dependent launch), and it calls follow() before
+// it touches anything that one wrote or reads.
+__device__ __forceinline__ void follow() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// In the kernel before: the next may be launched (it waits in follow()).
+__device__ __forceinline__ void lead() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_following(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st,
+                             const A &...args)
+{
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid;
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, kernel, P(args)...);
+}
+
 cudaError_t launch_tree_attend(const kvc_params &p, int max_len, const TreeArgs &t,
                                const uint16_t *q, const uint16_t *kt, const uint16_t *vt,
                                const kvc_cache &c, const kvc_moments *m, uint16_t *o, float *lse,

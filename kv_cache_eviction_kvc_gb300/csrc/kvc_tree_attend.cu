@@ -411,6 +411,7 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kMma) tmem_alloc(&S.tmem, 512);
+    lead();
 
     // this CTA's items [item0, item1) and tiles [lo, hi) of the line
     int item0, item1, base0, lo, hi;
@@ -934,6 +935,8 @@ template <bool kKeep>
 __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ JoinArgs j)
 {
     const AttArgs &a = j.a;
+    lead();
+    follow();
     const int4 cut = a.cut[blockIdx.x];                     // item, first and last part, rows
     const int lane = threadIdx.x & 31, r0 = kJoinRows * (blockIdx.y * 8 + (threadIdx.x >> 5));
     if (cut.x < 0 || r0 >= cut.w) return;
@@ -1068,6 +1071,7 @@ tree_moment_kernel(const __grid_constant__ JoinArgs j, const __grid_constant__ C
     if (warp == 9) tmem_alloc(&S.tmem, 256);
     __syncthreads();
     tc_fence_after();
+    follow();
     const uint32_t tmem = S.tmem;
     const LineCuts cuts(j.grid, a.whole ? items : a.first[items]);
     if (warp == 8) {
@@ -1389,9 +1393,8 @@ cudaError_t launch_tree_attend(const kvc_params &p, int max_len, const TreeArgs 
                p.correction == KVC_CORR_FIRST_ORDER, (int)grid};
     if (!whole) {
         const dim3 g((unsigned)grid, (a.rows + 8 * kJoinRows - 1) / (8 * kJoinRows));
-        if (m) tree_join_kernel<true><<<g, 256, 0, st>>>(j);
-        else tree_join_kernel<false><<<g, 256, 0, st>>>(j);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        e = launch_following(m ? tree_join_kernel<true> : tree_join_kernel<false>, g, 256, 0, st, j);
+        if (e != cudaSuccess) return e;
     }
     if (m) {
         CUtensorMap mf;
@@ -1400,7 +1403,9 @@ cudaError_t launch_tree_attend(const kvc_params &p, int max_len, const TreeArgs 
                                  (int)kMomDyn);
         if (e != cudaSuccess) return e;
         const long long jobs = items * ((a.rows + kMomRows - 1) / kMomRows);
-        tree_moment_kernel<<<(int)(jobs < kGrid ? jobs : kGrid), kMomThreads, kMomDyn, st>>>(j, mq, mf);
+        e = launch_following(tree_moment_kernel, dim3((unsigned)(jobs < kGrid ? jobs : kGrid)), kMomThreads,
+                             kMomDyn, st, j, mq, mf);
+        if (e != cudaSuccess) return e;
     }
     return cudaGetLastError();
 }
