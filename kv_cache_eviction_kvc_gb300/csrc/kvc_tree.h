@@ -26,28 +26,6 @@ struct PathArgs {
     int A;
 };
 
-// Live drafted tokens of unit u's tree, or -1 when outside [0, T].
-__device__ __forceinline__ int tree_live(const TreeArgs &t, int u)
-{
-    const int n = t.n ? t.n[u / t.units] : t.T;
-    return n < 0 || n > t.T ? -1 : n;
-}
-
-// Accepted tokens of unit u's path, or -1 when the path is not one: a count
-// outside [0, A] or a token that is not live.  Warp-wide; every lane gets the
-// answer.
-__device__ __forceinline__ int path_count(const TreeArgs &t, const PathArgs &p, int u, int lane)
-{
-    const int b = u / t.units, live = tree_live(t, u), a = p.n[b];
-    if (live < 0 || a < 0 || a > p.A) return -1;
-    bool bad = false;
-    for (int j = lane; j < a; j += 32) {
-        const int c = p.token[(size_t)b * p.A + j];
-        bad |= c < 0 || c >= live;
-    }
-    return __any_sync(kFull, bad) ? -1 : a;
-}
-
 // x / d for 0 <= x < 2^31 as a multiplication (Granlund and Montgomery, 1994)
 struct FastDiv {
     uint32_t mul, shift;

@@ -17,7 +17,7 @@
 // with the evicted set's estimate.  The drafted tokens are the item's last
 // tile.
 //
-// 352 threads:
+// 384 threads:
 //   warps 0-3, 4-7  two softmax groups, each with its own S, P and O in tensor
 //                   memory.  Items of more than 128 rows give each group 128
 //                   of them; otherwise the groups take alternate tiles of the
@@ -26,6 +26,7 @@
 //   warp 9          tensor-memory owner and MMA issuer
 //   warp 10         walks the CTA's items ahead of the others and tells them
 //                   through a ring in shared memory
+//   warp 11         mends value tiles before their MMA (see below)
 // (168 registers a thread: spills would go through the few KB of L1 that the
 // tiles leave, to L2.)
 // Tensor memory: O of group w at column 128 w, S at 256 + 128 w; P (bf16)
@@ -38,6 +39,8 @@
 // value rows behind len are zeroed in shared memory up to the next multiple of
 // 16 (the MMA reads 16 slots at a time).  Drafted tokens whose value is not
 // finite are zeroed as well and added afterwards to the rows that see them.
+// A warp of its own does it while the tile's S and softmax run: by the softmax
+// threads it was 4000 of the 30000 clocks of a unit of 1024 slots.
 // Every wait is bounded (~2 s); a wait that ran out records KVC_ERR_TIMEOUT.
 #include "kvc_tree.h"
 #include "kvc_umma.cuh"
@@ -52,8 +55,8 @@ constexpr int kRows = 256;                       // query rows per item
 constexpr int kSlot = kTile * kD * 2;            // 32 KB: a tile of keys or values
 constexpr int kHalf = kSlot / 2;                 // its 64-column half
 constexpr int kRing = 5;
-constexpr int kThreads = 352;
-constexpr int kProd = 8, kMma = 9, kWalk = 10;
+constexpr int kThreads = 384;
+constexpr int kProd = 8, kMma = 9, kWalk = 10, kMend = 11;
 constexpr int kSegs = 4;                         // items told ahead
 constexpr int kGrid = 152;                       // CTAs: one per SM
 constexpr uint32_t kColS = 256;
@@ -93,8 +96,7 @@ struct __align__(16) Seg {
     int item, u, rb, n, live, nt;   // nt: tiles of the item
     int t0, t1;                     // this CTA's tiles of it
     int rows;                       // live rows of the item
-    int k0;                         // the CTA's tiles before
-    int trees;                      // drafted tokens' tiles before
+    int mends;                      // value tiles to mend before the drafted tokens'
 };
 
 struct AttSmem {
@@ -104,11 +106,13 @@ struct AttSmem {
     } g[2];
     Seg seg[kSegs];
     int4 cut;
+    int4 mend[4];           // a value tile to mend: ring entry (-1: no more), phase, valid slots, drafted tokens'
     uint64_t full[kRing], empty[kRing];
     uint64_t segfull[kSegs], segempty[kSegs];
     uint64_t qfull[2], qempty[2], sfull[2], pready[2], pvdone[2];
     uint64_t gsync[2], xsync, drain;
-    uint64_t odd[2];        // drafted tokens with a value that is not finite
+    uint64_t armed[4], mended[4];
+    uint64_t odd[4];        // drafted tokens with a value that is not finite
     int scan[kThreads / 32];
     int start_item, start_base;
     int bad;
@@ -223,6 +227,13 @@ __device__ __forceinline__ void check_unit(const AttArgs &a, int u)
     else if (n < 0 || n > a.max_len) record_status(a.status, KVC_ERR_SHAPE);
 }
 
+// Value rows that the MMA reads (16 at a time) and that are no slot, or drafted
+// tokens: the tile is mended first.
+__device__ __forceinline__ bool needs_mend(const Seg &s, int t)
+{
+    return t == s.nt - 1 || (t == s.nt - 2 && (s.n & 15));
+}
+
 // valid slots of tile t (the drafted tokens' tile: the live ones)
 __device__ __forceinline__ int tile_valid(const Seg &s, int t)
 {
@@ -257,47 +268,10 @@ __device__ __forceinline__ void hide32(uint32_t (&y)[32], uint32_t keep)
         for (int j = 0; j < 32; j++) y[j] = keep >> j & 1 ? y[j] : 0xff800000u;
 }
 
-// One tile of the thread's row: the row's maximum so far, the weights, which
-// replace S as bf16 pairs, and their sum.  A slot's vote multiplies its weight
-// (exp(x + ln p) = p exp(x)).  All 128 columns are read for the maximum (a
-// read takes about 140 clocks and 10 more per 16 columns); the upper 64 stay
-// in registers for the weights and the lower 64 are read again meanwhile, which
-// is what fits without spills.  So P takes 32 columns at the start of each
-// half of S.
-template <bool kMask, bool kVotes>
-__device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float scale,
-                                             const float *vote, uint64_t keep0, uint64_t keep1,
-                                             bool rescale, float &m, float &l)
+// A new maximum of the row: m, l and (rescale) the row of O follow it once it
+// is above m by kSlack.
+__device__ __forceinline__ void move_max(float top, uint32_t tO, bool rescale, float &m, float &l)
 {
-    float top;
-    uint32_t c[32], d[32];
-    {
-        uint32_t a[32], b[32];
-        float mx[2] = {-INFINITY, -INFINITY};
-        auto top_of = [&](uint32_t (&y)[32], uint32_t keep) {
-            hide32<kMask>(y, keep);
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-                mx[0] = fmaxf(fmaxf(mx[0], __uint_as_float(y[j])), __uint_as_float(y[j + 1]));
-                mx[1] = fmaxf(fmaxf(mx[1], __uint_as_float(y[j + 2])), __uint_as_float(y[j + 3]));
-            }
-        };
-        tmem_ld32_async(tS, a);
-        tmem_ld32_async(tS + 32, b);
-        tmem_wait_ld();
-        tmem_bind(a);
-        tmem_bind(b);
-        tmem_ld32_async(tS + 64, c);
-        top_of(a, (uint32_t)keep0);
-        tmem_ld32_async(tS + 96, d);
-        top_of(b, (uint32_t)(keep0 >> 32));
-        tmem_wait_ld();
-        tmem_bind(c);
-        tmem_bind(d);
-        top_of(c, (uint32_t)keep1);
-        top_of(d, (uint32_t)(keep1 >> 32));
-        top = fmaxf(mx[0], mx[1]) * scale;
-    }
     const bool move = top > m + kSlack || (m == -INFINITY && top > m);
     if (__any_sync(kFull, move)) {
         float f = 1.f;
@@ -319,35 +293,92 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float sca
             }
         }
     }
+}
+
+// The weights of 32 raw products, added to sum and written to P as bf16 pairs.
+template <bool kVotes>
+__device__ __forceinline__ void weights32(const uint32_t (&y)[32], uint32_t at, const float *v, float2 c2,
+                                          float2 r2, float2 (&sum)[2])
+{
+            uint32_t p[16];
+    #pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+                float2 e[2];
+    #pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    const float2 x = make_float2(__uint_as_float(y[2 * (j + i)]),
+                                                 __uint_as_float(y[2 * (j + i) + 1]));
+                    const float2 t = fma2(x, c2, r2);
+                    e[i] = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+                }
+                if (kVotes) {
+                    const float4 w = *reinterpret_cast<const float4 *>(v + 2 * j);
+                    e[0].x *= w.x;
+                    e[0].y *= w.y;
+                    e[1].x *= w.z;
+                    e[1].y *= w.w;
+                }
+    #pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    sum[i] = add2(sum[i], e[i]);
+                    p[j + i] = pack_bf16(e[i].x, e[i].y);
+                }
+            }
+            tmem_st16(at, p);
+}
+
+// The largest of 32 raw products (hidden ones: -inf), kept in mx.
+template <bool kMask>
+__device__ __forceinline__ void top32(uint32_t (&y)[32], uint32_t keep, float (&mx)[2])
+{
+    hide32<kMask>(y, keep);
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+        mx[0] = fmaxf(fmaxf(mx[0], __uint_as_float(y[j])), __uint_as_float(y[j + 1]));
+        mx[1] = fmaxf(fmaxf(mx[1], __uint_as_float(y[j + 2])), __uint_as_float(y[j + 3]));
+    }
+}
+
+// One tile of the thread's row: the row's maximum so far, the weights, which
+// replace S as bf16 pairs, and their sum.  A slot's vote multiplies its weight
+// (exp(x + ln p) = p exp(x)).  All 128 columns are read for the maximum (a
+// read takes about 140 clocks and 10 more per 16 columns); the upper 64 stay
+// in registers for the weights and the lower 64 are read again meanwhile, which
+// is what fits without spills.  So P takes 32 columns at the start of each
+// half of S.
+template <bool kMask, bool kVotes>
+__device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float scale,
+                                             const float *vote, uint64_t keep0, uint64_t keep1,
+                                             bool rescale, float &m, float &l)
+{
+    float top;
+    uint32_t c[32], d[32];
+    {
+        uint32_t a[32], b[32];
+        float mx[2] = {-INFINITY, -INFINITY};
+        auto top_of = [&](uint32_t (&y)[32], uint32_t keep) { top32<kMask>(y, keep, mx); };
+        tmem_ld32_async(tS, a);
+        tmem_ld32_async(tS + 32, b);
+        tmem_wait_ld();
+        tmem_bind(a);
+        tmem_bind(b);
+        tmem_ld32_async(tS + 64, c);
+        top_of(a, (uint32_t)keep0);
+        tmem_ld32_async(tS + 96, d);
+        top_of(b, (uint32_t)(keep0 >> 32));
+        tmem_wait_ld();
+        tmem_bind(c);
+        tmem_bind(d);
+        top_of(c, (uint32_t)keep1);
+        top_of(d, (uint32_t)(keep1 >> 32));
+        top = fmaxf(mx[0], mx[1]) * scale;
+    }
+    move_max(top, tO, rescale, m, l);
     const float nref = m == -INFINITY ? 0.f : -m;
     const float2 c2 = make_float2(scale, scale), r2 = make_float2(nref, nref);
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     auto weights = [&](uint32_t (&y)[32], uint32_t at, const float *v) {
-        uint32_t p[16];
-#pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-            float2 e[2];
-#pragma unroll
-            for (int i = 0; i < 2; i++) {
-                const float2 x = make_float2(__uint_as_float(y[2 * (j + i)]),
-                                             __uint_as_float(y[2 * (j + i) + 1]));
-                const float2 t = fma2(x, c2, r2);
-                e[i] = make_float2(ex2_approx(t.x), ex2_approx(t.y));
-            }
-            if (kVotes) {
-                const float4 w = *reinterpret_cast<const float4 *>(v + 2 * j);
-                e[0].x *= w.x;
-                e[0].y *= w.y;
-                e[1].x *= w.z;
-                e[1].y *= w.w;
-            }
-#pragma unroll
-            for (int i = 0; i < 2; i++) {
-                sum[i] = add2(sum[i], e[i]);
-                p[j + i] = pack_bf16(e[i].x, e[i].y);
-            }
-        }
-        tmem_st16(at, p);
+        weights32<kVotes>(y, at, v, c2, r2, sum);
     };
     uint32_t a[32], b[32];
     weights(c, tS + 64, vote + 64);
@@ -362,6 +393,31 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float sca
     tmem_bind(b);
     hide32<kMask>(b, (uint32_t)(keep0 >> 32));
     weights(b, tS + 16, vote + 32);
+    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+    tmem_wait_st();
+}
+
+// The same for a tile of at most 64 slots: all of it stays in registers, the
+// upper half of P is not read.
+template <bool kVotes>
+__device__ __forceinline__ void softmax_half(uint32_t tS, uint32_t tO, float scale, const float *vote,
+                                             uint64_t keep, bool rescale, float &m, float &l)
+{
+    uint32_t a[32], b[32];
+    float mx[2] = {-INFINITY, -INFINITY};
+    tmem_ld32_async(tS, a);
+    tmem_ld32_async(tS + 32, b);
+    tmem_wait_ld();
+    tmem_bind(a);
+    tmem_bind(b);
+    top32<true>(a, (uint32_t)keep, mx);
+    top32<true>(b, (uint32_t)(keep >> 32), mx);
+    move_max(fmaxf(mx[0], mx[1]) * scale, tO, rescale, m, l);
+    const float nref = m == -INFINITY ? 0.f : -m;
+    const float2 c2 = make_float2(scale, scale), r2 = make_float2(nref, nref);
+    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    weights32<kVotes>(a, tS, vote, c2, r2, sum);
+    weights32<kVotes>(b, tS + 16, vote + 32, c2, r2, sum);
     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
     tmem_wait_st();
 }
@@ -404,6 +460,10 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
             mbar_init(&S.pready[i], 4);
             mbar_init(&S.pvdone[i], 1);
             mbar_init(&S.gsync[i], 4);
+        }
+        for (int i = 0; i < 4; i++) {
+            mbar_init(&S.armed[i], 1);
+            mbar_init(&S.mended[i], 1);
         }
         mbar_init(&S.xsync, 8);
         mbar_init(&S.drain, 1);
@@ -477,7 +537,7 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
     if (warp == kWalk) {
         // --------------------------------------------------------- walker
         if (elect_one()) {
-            int item = item0, base = base0, k0 = 0, trees = 0, n = 0, live = 0;
+            int item = item0, base = base0, mends = 0, n = 0, live = 0;
             bool ok = true;
             if (item < item1) {
                 n = a.len[a.by_rb(item)];
@@ -495,8 +555,6 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                     s.nt = item_tiles(a, n, live, s.rb);
                     s.t0 = max(0, lo - base);
                     s.t1 = min(s.nt, hi - base);
-                    s.k0 = k0;
-                    s.trees = trees;
                     base += a.whole ? 0 : s.nt;
                     if (++item < item1) {
                         n = a.len[a.by_rb(item)];
@@ -504,8 +562,9 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                     }
                     if (s.t1 <= s.t0) continue;
                     s.rows = min(kRows, (s.live << a.gshift) - s.rb * kRows);
-                    k0 += s.t1 - s.t0;
-                    trees += s.t1 == s.nt;
+                    mends += s.t0 <= s.nt - 2 && s.t1 >= s.nt - 1 && (s.n & 15);
+                    s.mends = mends;
+                    mends += s.t1 == s.nt;
                 }
                 if (i >= kSegs) ok = tree_wait(&S.segempty[i % kSegs], (i / kSegs - 1) & 1, &S.bad);
                 if (!ok) break;
@@ -519,7 +578,7 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
     } else if (warp == kProd) {
         // ------------------------------------------------------- producer
         if (elect_one()) {
-            int k = 0, slot = 0, qn[2] = {0, 0};
+            int k = 0, slot = 0, mends = 0, qn[2] = {0, 0};
             uint32_t ph = 1;                     // phase of the slot's last release
             bool ok = true;
             const uint64_t pol = l2_policy_evict_first();
@@ -539,6 +598,15 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                 k++;
                 if (++slot == kRing) { slot = 0; ph ^= 1; }
             };
+            // Told once the entry's phase has begun, so that the wait for it cannot end
+            // with an earlier one.  At most three value tiles are in the ring: the fourth
+            // place is free when it is needed.
+            auto tell = [&](int entry, int nv, bool tree) {
+                if (!ok) return;
+                S.mend[mends & 3] = make_int4(entry, (k - 1) / kRing & 1, nv, tree);
+                mbar_arrive(&S.armed[mends & 3]);
+                mends++;
+            };
             auto load_q = [&](int half, int u, int row, int rows) {
                 if (qn[half] > 0) ok = ok && tree_wait(&S.qempty[half], (qn[half] - 1) & 1, &S.bad);
                 if (!ok) return;
@@ -556,7 +624,10 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                 if (!ok) break;
                 const Seg s = S.seg[i % kSegs];
                 mbar_arrive(&S.segempty[i % kSegs]);
-                if (s.rows == 0) break;
+                if (s.rows == 0) {
+                    tell(-1, 0, false);
+                    break;
+                }
                 const int qrow = s.rb * kRows;
                 if (s.rows > 128) {
                     load_q(0, s.u, qrow, 128);
@@ -569,8 +640,10 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                 auto load_tile = [&](bool keys, int t) {
                     const bool tree = t == s.nt - 1;
                     const int nv = tree ? 64 : s.n - t * kTile, row = tree ? 0 : t * kTile;
+                    const int entry = slot;
                     load(keys ? (tree ? &tmKt : &tmK) : (tree ? &tmVt : &tmV), s.u, row, nv,
                          !tree && a.RB == 1);
+                    if (!keys && needs_mend(s, t)) tell(entry, tile_valid(s, t), tree);
                 };
                 // in the order of their use, so that no tile waits in the ring for
                 // one behind it: alternate tiles have two S before the first O
@@ -596,7 +669,7 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
         if (elect_one()) {
             bool ok = true;
             // next ring entry and its phase; the entries in use by S and by O
-            int slot = 0, ks_slot = 0, vs_slot = 0;
+            int slot = 0, ks_slot = 0, vs_slot = 0, mends = 0;
             uint32_t ph = 0, q_ph = 0, p_ph = 0;             // phases; the groups' as bits
             const uint64_t q0 = umma_sdesc(smem_u32(qbuf)), k0 = umma_sdesc(smem_u32(ring));
             const uint64_t v0 = v_desc(smem_u32(ring));
@@ -622,8 +695,12 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                 if (last) umma_commit(&S.empty[ks_slot]);
                 if (last_q) umma_commit(&S.qempty[half]);
             };
-            auto issue_o = [&](uint32_t w, int nv, bool first, bool last, bool keep) {
+            auto issue_o = [&](uint32_t w, int nv, bool mend, bool first, bool last, bool keep) {
                 if (first) take(vs_slot);
+                if (first && mend) {
+                    ok = ok && tree_wait(&S.mended[mends & 3], mends >> 2 & 1, &S.bad);
+                    mends++;
+                }
                 ok = ok && tree_wait(&S.pready[w], p_ph >> w & 1, &S.bad);
                 p_ph ^= 1u << w;
                 if (!ok) return;
@@ -666,8 +743,8 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                 for (uint32_t j = 0; ok && j < jobs + 2; j++) {
                     const uint32_t w = j & 1, first = !dual || !w, last = !dual || w;
                     if (j >= 2) {
-                        const int t = (int)((j - 2) >> dual);
-                        issue_o(w, tile_valid(s, s.t0 + t), first, last, j - 2 >= 2);
+                        const int t = s.t0 + (int)((j - 2) >> dual);
+                        issue_o(w, tile_valid(s, t), needs_mend(s, t), first, last, j - 2 >= 2);
                     }
                     if (j < jobs) {
                         const int t = (int)(j >> dual);
@@ -684,6 +761,46 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
             }
         }
         __syncwarp();
+    } else if (warp == kMend) {
+        // --------------------------------------------------------- mender
+        bool ok = true;
+        for (int x = 0; ok; x++) {
+            ok = __all_sync(kFull, tree_wait(&S.armed[x & 3], x >> 2 & 1, &S.bad));
+            if (!ok) break;
+            const int4 f = S.mend[x & 3];
+            if (f.x < 0) break;
+            ok = __all_sync(kFull, tree_wait(&S.full[f.x], f.y, &S.bad));
+            if (!ok) break;
+            unsigned char *v = ring + f.x * kSlot;
+            const int nv = f.z, stop = (nv + 15) & ~15;
+            uint64_t odd = 0;
+            // two rows of 16 chunks at a time: rows that are no slot become zero; of a
+            // drafted token, what is not finite does, and is added to the rows that see
+            // it at the end
+#pragma unroll 4
+            for (int r0 = f.w ? 0 : nv & ~1; r0 < stop; r0 += 2) {
+                const int c = lane & 15, r = r0 + (lane >> 4);
+                uint4 *p = reinterpret_cast<uint4 *>(v + (c >> 3) * kHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+                const uint4 y = *p;
+                uint32_t w[4] = {y.x, y.y, y.z, y.w};
+                bool hit = false;
+                if (f.w)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        if ((w[e] & 0x7f80u) == 0x7f80u) { w[e] &= 0xffff0000u; hit = true; }
+                        if ((w[e] & 0x7f800000u) == 0x7f800000u) { w[e] &= 0x0000ffffu; hit = true; }
+                    }
+                if (r >= nv) *p = make_uint4(0, 0, 0, 0);
+                else if (hit) *p = make_uint4(w[0], w[1], w[2], w[3]);
+                const unsigned bits = __ballot_sync(kFull, hit && r < nv);
+                if (bits) odd |= (uint64_t)((bits & 0xffffu ? 1 : 0) | (bits >> 16 ? 2 : 0)) << r0;
+            }
+            if (lane == 0) S.odd[x & 3] = odd;
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.mended[x & 3]);
+        }
+        if (!ok && lane == 0) S.bad = 1;
     } else {
         // --------------------------------------------------------- softmax
         const int w = warp >> 2, r = tid & 127;              // group, row of its 128
@@ -710,9 +827,26 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
             xph ^= 1;
             tc_fence_after();
         };
-        for (int i = 0; ok; i++) {
+        // what a thread needs of the next item from global memory: the drafted tokens its
+        // row sees, the first votes
+        uint64_t see_next = 0;
+        int vote_first = 1;
+        auto peek = [&](int i) {
             wait(&S.segfull[i % kSegs], (i / kSegs) & 1);
-            if (!ok) break;
+            if (!ok) return;
+            const volatile Seg &s = S.seg[i % kSegs];
+            const int rows = s.rows, live = s.live, u = s.u, row = (rows > 128 ? 128 * w : 0) + r;
+            see_next = 0;
+            if (row < rows)
+                see_next = a.t.mask[(size_t)a.by_units(u) * a.t.T + ((s.rb * kRows + row) >> a.gshift)] &
+                           (live >= 64 ? ~0ull : (1ull << live) - 1);
+            if (kVotes) {
+                const int at = (s.t0 + (rows > 128 ? 0 : w)) * kTile + r;
+                vote_first = rows > 0 && at < s.n ? a.votes[(size_t)u * a.cap + at] : 1;
+            }
+        };
+        peek(0);
+        for (int i = 0; ok; i++) {
             const volatile Seg &s = S.seg[i % kSegs];
             const int rows = s.rows;
             if (rows == 0) break;
@@ -720,22 +854,15 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
             const int step = dual ? 1 : 2;
             const int row = (dual ? 128 * w : 0) + r;        // row of the item
             const bool busy = row - lane < rows;             // the warp has rows
+            const uint64_t see = see_next;
             float m = -INFINITY, l = 0.f;
             bool begun = false;                              // O has a tile's product
-            uint64_t see = 0;                                // drafted tokens the row sees
-            {
-                const int live = s.live, u = s.u;
-                if (row < rows)
-                    see = a.t.mask[(size_t)a.by_units(u) * a.t.T + ((s.rb * kRows + row) >> a.gshift)] &
-                          (live >= 64 ? ~0ull : (1ull << live) - 1);
-                // the first tile's votes (a group without a tile here must not write: the
-                // maxima and sums of the item's end share the space)
-                if (kVotes && s.t0 + (dual ? 0 : w) < s.t1) {
-                    const int at = (s.t0 + (dual ? 0 : w)) * kTile + r;
-                    S.g[w].vote[job & 1][r] = at < s.n ? (float)a.votes[(size_t)u * a.cap + at] : 1.f;
-                    group_sync();
-                    if (!ok) break;
-                }
+            // the first tile's votes (a group without a tile here must not write: the
+            // maxima and sums of the item's end share the space)
+            if (kVotes && s.t0 + (dual ? 0 : w) < s.t1) {
+                S.g[w].vote[job & 1][r] = (float)vote_first;
+                group_sync();
+                if (!ok) break;
             }
             for (int tile = s.t0 + (dual ? 0 : w); tile < s.t1; tile += step) {
                 const bool tree = tile == s.nt - 1;
@@ -752,47 +879,6 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                 // S was issued when all four warps had handed over the group's last weights:
                 // they are done with the other buffer, and this one has been written
                 if (kVotes) S.g[w].vote[(job + 1) & 1][r] = (float)vote_next;
-                // value rows the MMA reads that are no slot: zero.  (After S: the issuer has
-                // then taken the ring entry that used the slot before, so that the parity
-                // below cannot be that of an earlier phase.)
-                if ((tree || nv & 15) && (!dual || w == 0)) {
-                    const int t = tile - s.t0;
-                    const int kv = 2 * s.k0 + t + (dual ? t + 1 : min(t + 2, s.t1 - s.t0));
-                    const int slot = kv % kRing;
-                    wait(&S.full[slot], (kv / kRing) & 1);
-                    if (!ok) break;
-                    unsigned char *v = ring + slot * kSlot;
-                    const int stop = (nv + 15) & ~15;
-                    bool odd = false;
-                    if (r < stop && (tree || r >= nv)) {
-                        // thread r has slot r; of a drafted token, what is not finite is
-                        // zeroed here and added to the rows that see it at the end
-#pragma unroll 2
-                        for (int c = 0; c < 16; c++) {
-                            uint4 *p = reinterpret_cast<uint4 *>(
-                                v + (c >> 3) * kHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-                            uint32_t x[4] = {0, 0, 0, 0};
-                            if (r < nv) {
-                                const uint4 y = *p;
-                                x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
-                            }
-                            bool hit = r >= nv;
-#pragma unroll
-                            for (int e = 0; e < 4; e++) {
-                                if ((x[e] & 0x7f80u) == 0x7f80u) { x[e] &= 0xffff0000u; hit = true; }
-                                if ((x[e] & 0x7f800000u) == 0x7f800000u) { x[e] &= 0x0000ffffu; hit = true; }
-                            }
-                            if (hit) *p = make_uint4(x[0], x[1], x[2], x[3]);
-                            odd |= hit;
-                        }
-                    }
-                    if (tree && warp - 4 * w < 2) {
-                        const uint32_t bits = __ballot_sync(kFull, odd && r < nv);
-                        if (lane == 0)
-                            reinterpret_cast<uint32_t *>(&S.odd[s.trees & 1])[warp - 4 * w] = bits;
-                    }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                }
                 if (busy) {
                     if (tree || nv < kTile) {
                         uint64_t keep0 = see, keep1 = 0;     // the slots the row may see
@@ -800,7 +886,10 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                             keep0 = nv >= 64 ? ~0ull : (1ull << nv) - 1;
                             keep1 = nv <= 64 ? 0ull : (1ull << (nv - 64)) - 1;
                         }
-                        softmax_tile<true, kVotes>(tS, tO, a.scale, S.g[w].vote[job & 1], keep0, keep1, begun, m, l);
+                        if (nv <= 64)
+                            softmax_half<kVotes>(tS, tO, a.scale, S.g[w].vote[job & 1], keep0, begun, m, l);
+                        else
+                            softmax_tile<true, kVotes>(tS, tO, a.scale, S.g[w].vote[job & 1], keep0, keep1, begun, m, l);
                     } else {
                         softmax_tile<false, kVotes>(tS, tO, a.scale, S.g[w].vote[job & 1], 0, 0, begun, m, l);
                     }
@@ -812,7 +901,9 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                 if (lane == 0) mbar_arrive(&S.pready[w]);
             }
             // ------------------------------------------------------ outputs
+            if (ok) peek(i + 1);
             if (ok && begun) wait(&S.pvdone[w], (job - 1) & 1);
+            if (ok && s.t1 == s.nt) wait(&S.mended[s.mends & 3], s.mends >> 2 & 1);   // S.odd is written
             if (!ok) break;
             tc_fence_after();
             const int u = s.u, nq = s.t1 - s.t0;
@@ -820,11 +911,9 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
             const bool has_tree = s.t1 == s.nt;
             float c0 = 1.f, c1 = 0.f, M = m, L = l;          // weights of the groups' sums
             if (!dual) S.g[w].ml[r] = make_float2(m, l);
-            if (!dual || has_tree) {                         // has_tree: S.odd is written
+            if (!dual) {
                 all_sync();
                 if (!ok) break;
-            }
-            if (!dual) {
                 const float2 p0 = S.g[0].ml[r], p1 = S.g[1].ml[r];
                 M = fmaxf(p0.x, p1.x);
                 const float ref = M == -INFINITY ? 0.f : M;
@@ -839,7 +928,7 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                 c0 *= inv;
                 c1 *= inv;
             }
-            const uint64_t by_hand = has_tree ? S.odd[s.trees & 1] & see : 0;
+            const uint64_t by_hand = has_tree ? S.odd[s.mends & 3] & see : 0;
             // a group writes its rows whole, or (alternate tiles) half of the columns
             const int q0 = dual ? 0 : 2 * w, q1 = dual ? 4 : q0 + 2;
             const bool two = !dual && nq > 1, mine = row < rows;
@@ -847,36 +936,44 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                 // 32 columns of 16 rows at a time, in the layout that gives a thread two
                 // columns of every eight; a transposition in each quad of lanes leaves it
                 // eight in a row, so that a store covers whole lines
-                const uint32_t t0 = tmem + lanes + (dual ? 128 * w : 0);
+                uint32_t y[16], z[16];
+                auto fetch = [&](int q) {
+                    const uint32_t at = tmem + lanes + ((uint32_t)(16 * (q & 1)) << 16) + 32 * (q >> 1);
+                    tmem_ld_16x256(at + (dual ? 128 * w : 0), y);
+                    if (two) tmem_ld_16x256(at + 128, z);
+                };
+                fetch(2 * q0);
 #pragma unroll 1
                 for (int q = 2 * q0; q < 2 * q1; q++) {
                     const int h = q & 1, col = 32 * (q >> 1) + 8 * (lane & 3);
-                    uint32_t y[16], z[16];
-                    tmem_ld_16x256(t0 + ((uint32_t)(16 * h) << 16) + 32 * (q >> 1), y);
-                    if (two) tmem_ld_16x256(tmem + lanes + 128 + ((uint32_t)(16 * h) << 16) + 32 * (q >> 1), z);
+                    float f[2][8];
                     tmem_wait_ld();
                     tmem_bind16(y);
                     if (two) tmem_bind16(z);
 #pragma unroll
                     for (int k = 0; k < 2; k++) {            // rows (lane / 4) and 8 more
-                        const int of = 16 * h + 8 * k + (lane >> 2), r2 = row - lane + of;
+                        const int of = 16 * h + 8 * k + (lane >> 2);
                         const float a0 = __shfl_sync(kFull, c0, of), a1 = __shfl_sync(kFull, c1, of);
-                        float f[8];
 #pragma unroll
                         for (int j = 0; j < 4; j++)
 #pragma unroll
                             for (int e = 0; e < 2; e++) {
-                                f[2 * j + e] = __uint_as_float(y[4 * j + 2 * k + e]) * a0;
-                                if (two) f[2 * j + e] = fmaf(__uint_as_float(z[4 * j + 2 * k + e]), a1, f[2 * j + e]);
+                                f[k][2 * j + e] = __uint_as_float(y[4 * j + 2 * k + e]) * a0;
+                                if (two) f[k][2 * j + e] = fmaf(__uint_as_float(z[4 * j + 2 * k + e]), a1, f[k][2 * j + e]);
                             }
-                        quad_transpose(f, lane);
+                    }
+                    if (q + 1 < 2 * q1) fetch(q + 1);
+#pragma unroll
+                    for (int k = 0; k < 2; k++) {
+                        const int of = 16 * h + 8 * k + (lane >> 2), r2 = row - lane + of;
+                        quad_transpose(f[k], lane);
                         if (r2 >= rows) continue;
                         if (direct) {
                             *reinterpret_cast<uint4 *>(a.o + (orow - lane + of) * kD + col) =
-                                make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
-                                           pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+                                make_uint4(pack_bf16(f[k][0], f[k][1]), pack_bf16(f[k][2], f[k][3]),
+                                           pack_bf16(f[k][4], f[k][5]), pack_bf16(f[k][6], f[k][7]));
                         } else {
-                            st_v8(a.part + (part - lane + of) * kD + col, reinterpret_cast<const uint32_t *>(f));
+                            st_v8(a.part + (part - lane + of) * kD + col, reinterpret_cast<const uint32_t *>(f[k]));
                         }
                     }
                 }
