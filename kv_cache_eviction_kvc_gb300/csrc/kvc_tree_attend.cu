@@ -240,6 +240,11 @@ __device__ __forceinline__ int tile_valid(const Seg &s, int t)
     return t == s.nt - 1 ? s.live : min(kTile, s.n - t * kTile);
 }
 
+// The value of a load is used from here on (the compiler would convert it, and
+// so wait for it, right behind the load).
+__device__ __forceinline__ void late(int &x) { asm volatile("" : "+r"(x)); }
+__device__ __forceinline__ void late(uint64_t &x) { asm volatile("" : "+l"(x)); }
+
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
 {
     float2 d;
@@ -835,11 +840,10 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
             wait(&S.segfull[i % kSegs], (i / kSegs) & 1);
             if (!ok) return;
             const volatile Seg &s = S.seg[i % kSegs];
-            const int rows = s.rows, live = s.live, u = s.u, row = (rows > 128 ? 128 * w : 0) + r;
+            const int rows = s.rows, u = s.u, row = (rows > 128 ? 128 * w : 0) + r;
             see_next = 0;
             if (row < rows)
-                see_next = a.t.mask[(size_t)a.by_units(u) * a.t.T + ((s.rb * kRows + row) >> a.gshift)] &
-                           (live >= 64 ? ~0ull : (1ull << live) - 1);
+                see_next = a.t.mask[(size_t)a.by_units(u) * a.t.T + ((s.rb * kRows + row) >> a.gshift)];
             if (kVotes) {
                 const int at = (s.t0 + (rows > 128 ? 0 : w)) * kTile + r;
                 vote_first = rows > 0 && at < s.n ? a.votes[(size_t)u * a.cap + at] : 1;
@@ -854,7 +858,10 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
             const int step = dual ? 1 : 2;
             const int row = (dual ? 128 * w : 0) + r;        // row of the item
             const bool busy = row - lane < rows;             // the warp has rows
-            const uint64_t see = see_next;
+            late(see_next);
+            late(vote_first);
+            const int live = s.live;
+            const uint64_t see = see_next & (live >= 64 ? ~0ull : (1ull << live) - 1);
             float m = -INFINITY, l = 0.f;
             bool begun = false;                              // O has a tile's product
             // the first tile's votes (a group without a tile here must not write: the
@@ -878,7 +885,10 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                 tc_fence_after();
                 // S was issued when all four warps had handed over the group's last weights:
                 // they are done with the other buffer, and this one has been written
-                if (kVotes) S.g[w].vote[(job + 1) & 1][r] = (float)vote_next;
+                if (kVotes) {
+                    late(vote_next);
+                    S.g[w].vote[(job + 1) & 1][r] = (float)vote_next;
+                }
                 if (busy) {
                     if (tree || nv < kTile) {
                         uint64_t keep0 = see, keep1 = 0;     // the slots the row may see
@@ -964,9 +974,10 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                     }
                     if (q + 1 < 2 * q1) fetch(q + 1);
 #pragma unroll
+                    for (int k = 0; k < 2; k++) quad_transpose(f[k], lane);
+#pragma unroll
                     for (int k = 0; k < 2; k++) {
                         const int of = 16 * h + 8 * k + (lane >> 2), r2 = row - lane + of;
-                        quad_transpose(f[k], lane);
                         if (r2 >= rows) continue;
                         if (direct) {
                             *reinterpret_cast<uint4 *>(a.o + (orow - lane + of) * kD + col) =
