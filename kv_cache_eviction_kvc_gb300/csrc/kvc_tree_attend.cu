@@ -1107,19 +1107,21 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
 // The normalization correction: every row's sum normalised and mixed with the
 // evicted set's estimate.  Bound by bytes: 64 KB of C per unit, 1 KB per row.
 // A persistent CTA per SM takes 64 rows of an item at a time.  C q runs on
-// tcgen05 with C as two bf16 terms (2^-16 of a product), which the eight
-// worker warps take apart in registers: while they finish one job, the next
-// one is on the tensor core and C of the one after is on its way.
-//   warps 0-7  C to bf16 terms; outputs (a thread per row, warps of lane
-//              quarters 0 and 1) and q . mu_k (the other warps)
-//   warp 8     producer of q and the sums (TMA), warp 9 MMA issuer
+// tcgen05 with C as two bf16 terms (2^-16 of a product), which warps of their
+// own take apart in registers.  The roles are apart so that C of the jobs to
+// come keeps loading; each knows 32 jobs ahead of their use (a lane each).
+//   warps 0, 1, 4, 5    outputs: a thread per row (the tensor-memory lanes of
+//                       64 rows), half of the columns each
+//   warps 2, 3, 6, 7    q . mu_k of the rows, mu_v
+//   warps 8-15          C to bf16 terms, loaded half a job ahead
+//   warp 16             producer of q and the sums (TMA), warp 17 MMA issuer
 constexpr int kMomRows = 64;
-constexpr int kMomThreads = 320;
+constexpr int kMomThreads = 576;
 constexpr int kMomQ = kMomRows * kD * 2, kMomF = kMomRows * kD * 4;
 struct MomSmem {
-    float muk[2][kD], muv[2][kD], z[2][kMomRows];
+    float muv[2][kD], z[2][kMomRows];
     // (two of each: a wait for one job's phase is never two phases behind)
-    uint64_t ffull[2], fempty[2], pready[2], mdone[2], wsync;
+    uint64_t ffull[2], fempty[2], zready[2], pready[2], mdone[2], dfree[2];
     int bad;
     uint32_t tmem;
 };
@@ -1151,6 +1153,39 @@ __device__ __forceinline__ MomJob mom_job(const JoinArgs &j, const LineCuts &cut
     return m;
 }
 
+// A CTA's jobs with rows, one after another, for a whole warp.
+struct MomJobs {
+    const JoinArgs &j;
+    const LineCuts &cuts;
+    int per, jobs, k;             // k: the next one, in steps of the grid
+    MomJob mine;                  // lane i: job k - k % 32 + i
+
+    __device__ __forceinline__ MomJobs(const JoinArgs &j, const LineCuts &cuts, int per, int jobs)
+        : j(j), cuts(cuts), per(per), jobs(jobs), k(0)
+    {
+    }
+    __device__ __forceinline__ bool next(MomJob &m)
+    {
+        for (;; k++) {
+            if ((long long)k * gridDim.x + blockIdx.x >= jobs) return false;
+            if ((k & 31) == 0) {
+                const long long job = (long long)(k + (threadIdx.x & 31)) * gridDim.x + blockIdx.x;
+                mine.rows = 0;
+                if (job < jobs) mine = mom_job(j, cuts, per, (int)job);
+            }
+            m.rows = __shfl_sync(kFull, mine.rows, k & 31);
+            if (m.rows > 0) break;
+        }
+        m.u = __shfl_sync(kFull, mine.u, k & 31);
+        m.row0 = __shfl_sync(kFull, mine.row0, k & 31);
+        m.sid = __shfl_sync(kFull, mine.sid, k & 31);
+        m.r0 = __shfl_sync(kFull, mine.r0, k & 31);
+        m.ne = __shfl_sync(kFull, mine.ne, k & 31);
+        k++;
+        return true;
+    }
+};
+
 __global__ void __launch_bounds__(kMomThreads, 1)
 tree_moment_kernel(const __grid_constant__ JoinArgs j, const __grid_constant__ CUtensorMap tmQ,
                    const __grid_constant__ CUtensorMap tmF)
@@ -1164,154 +1199,163 @@ tree_moment_kernel(const __grid_constant__ JoinArgs j, const __grid_constant__ C
         return;
     }
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int items = a.U * a.RB, per = (a.rows + kMomRows - 1) / kMomRows, jobs = items * per;
+    const int items = a.U * a.RB, per = (a.rows + kMomRows - 1) / kMomRows;
     if (tid == 0) {
         S.bad = 0;
-        mbar_init(&S.wsync, 8);
         for (int i = 0; i < 2; i++) {
             mbar_init(&S.ffull[i], 1);
             mbar_init(&S.fempty[i], 8);
+            mbar_init(&S.zready[i], 4);
             mbar_init(&S.pready[i], 8);
             mbar_init(&S.mdone[i], 1);
+            mbar_init(&S.dfree[i], 4);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 9) tmem_alloc(&S.tmem, 256);
+    if (warp == 17) tmem_alloc(&S.tmem, 256);
     __syncthreads();
     tc_fence_after();
     follow();
     const uint32_t tmem = S.tmem;
     const LineCuts cuts(j.grid, a.whole ? items : a.first[items]);
-    if (warp == 8) {
-        if (elect_one()) {
-            bool ok = true;
-            int kf = 0;                          // jobs with rows
-            for (int job = blockIdx.x; ok && job < jobs; job += gridDim.x) {
-                const MomJob m = mom_job(j, cuts, per, job);
-                if (m.rows <= 0) continue;
-                const bool mix = m.ne > 0.f;
-                const int st = kf & 1;
-                if (kf >= 2) ok = tree_wait(&S.fempty[st], (kf / 2 - 1) & 1, &S.bad);
-                if (!ok) break;
+    MomJobs list(j, cuts, per, items * per);
+    MomJob m;
+    const float sd = rsqrtf((float)kD);
+    bool ok = true;
+    int kf = 0, kc = 0;                                      // jobs and products before
+    auto wait = [&](uint64_t *b, uint32_t ph) { ok = ok && __all_sync(kFull, tree_wait(b, ph, &S.bad)); };
+    auto arrive = [&](uint64_t *b) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b);
+    };
+    if (warp == 16) {
+        // -------------------------------------------------------- producer
+        for (; ok && list.next(m); kf++) {
+            const bool mix = m.ne > 0.f;
+            const int st = kf & 1;
+            if (kf >= 2) wait(&S.fempty[st], (kf / 2 - 1) & 1);
+            if (!ok) break;
+            if (elect_one()) {
                 mbar_expect_tx(&S.ffull[st], kMomF + (mix ? kMomQ : 0));
                 for (int i = 0; i < 4; i++)
                     tma_3d(fs + st * kMomF + i * (kMomF / 4), &tmF, 32 * i, m.r0, m.sid, &S.ffull[st]);
                 if (mix)
                     for (int i = 0; i < 2; i++)
                         tma_3d(qs + st * kMomQ + i * (kMomQ / 2), &tmQ, 64 * i, m.row0, m.u, &S.ffull[st]);
-                kf++;
             }
-            if (!ok) {
-                S.bad = 1;
-                // the copies in flight land before the block ends
-                for (int i = max(0, kf - 2); i < kf; i++) mbar_wait(&S.ffull[i & 1], (i / 2) & 1);
-            }
-        }
-        __syncwarp();
-    } else if (warp == 9) {
-        if (elect_one()) {
-            bool ok = true;
-            int kf = 0, kc = 0;
-            const uint64_t c0 = umma_sdesc(smem_u32(planes));
-            for (int job = blockIdx.x; ok && job < jobs; job += gridDim.x) {
-                const MomJob m = mom_job(j, cuts, per, job);
-                if (m.rows <= 0) continue;
-                const int st = kf & 1;
-                if (m.ne > 0.f && j.first_order) {
-                    ok = tree_wait(&S.ffull[st], (kf / 2) & 1, &S.bad);
-                    ok = ok && tree_wait(&S.pready[kc & 1], (kc >> 1) & 1, &S.bad);
-                    if (!ok) break;
-                    tc_fence_after();
-                    // rows 64 .. 127 of the operand are whatever lies behind: their lanes
-                    // are not read
-                    const uint64_t q0 = umma_sdesc(smem_u32(qs + st * kMomQ));
-                    const uint32_t d = tmem + 128 * (kc & 1);
-#pragma unroll
-                    for (int x = 0; x < 16; x++) {
-                        const int ks = x & 7;
-                        umma_bf16(d, q0 + (uint64_t)((ks >> 2) * (kMomQ / 2 >> 4) + (ks & 3) * 2),
-                                  umma_sdesc_step(c0 + (uint64_t)((2 * (kc & 1) + (x >> 3)) * (kSlot >> 4)), ks),
-                                  kIdescS, x > 0);
-                    }
-                    umma_commit(&S.mdone[kc & 1]);
-                    kc++;
-                }
-                kf++;
-            }
-            // (a wait that ran out: the MMAs issued before are done when mdone says so)
-            if (!ok) {
-                S.bad = 1;
-                if (kc > 0) mbar_wait(&S.mdone[(kc - 1) & 1], ((kc - 1) >> 1) & 1);
-            }
-        }
-        __syncwarp();
-    } else {
-        const float sd = rsqrtf((float)kD);
-        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const int col0 = 64 * (warp >> 2);
-        bool ok = true;
-        int kf = 0, kc = 0;
-        uint32_t wph = 0;
-        auto wait = [&](uint64_t *b, uint32_t ph) { ok = __all_sync(kFull, tree_wait(b, ph, &S.bad)) && ok; };
-        auto sync = [&] {                                    // the eight warps
             __syncwarp();
-            if (lane == 0) mbar_arrive(&S.wsync);
-            wait(&S.wsync, wph);
-            wph ^= 1;
-        };
-        // C of a unit: 16-byte chunks of eight elements, on their way in registers
-        float4 cr[16];
-        auto fetch = [&](int u) {
+        }
+        // (after a wait that ran out: the copies in flight land before the block ends)
+        if (!ok)
+            for (int i = max(0, kf - 2); i < kf; i++) mbar_wait(&S.ffull[i & 1], (i / 2) & 1);
+    } else if (warp == 17) {
+        // ------------------------------------------------------ MMA issuer
+        const uint64_t c0 = umma_sdesc(smem_u32(planes));
+        for (; ok && list.next(m); kf++) {
+            const int st = kf & 1;
+            if (m.ne <= 0.f || !j.first_order) continue;
+            wait(&S.ffull[st], (kf / 2) & 1);
+            wait(&S.pready[kc & 1], (kc >> 1) & 1);
+            if (kc >= 2) wait(&S.dfree[kc & 1], ((kc >> 1) - 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+                // rows 64 .. 127 of the operand are whatever lies behind: their lanes
+                // are not read
+                const uint64_t q0 = umma_sdesc(smem_u32(qs + st * kMomQ));
+                const uint32_t d = tmem + 128 * (kc & 1);
+#pragma unroll
+                for (int x = 0; x < 16; x++) {
+                    const int ks = x & 7;
+                    umma_bf16(d, q0 + (uint64_t)((ks >> 2) * (kMomQ / 2 >> 4) + (ks & 3) * 2),
+                              umma_sdesc_step(c0 + (uint64_t)((2 * (kc & 1) + (x >> 3)) * (kSlot >> 4)), ks),
+                              kIdescS, x > 0);
+                }
+                umma_commit(&S.mdone[kc & 1]);
+            }
+            __syncwarp();
+            kc++;
+        }
+        // (after a wait that ran out: the MMAs issued before are done when mdone says so)
+        if (!ok && kc > 0) mbar_wait(&S.mdone[(kc - 1) & 1], ((kc - 1) >> 1) & 1);
+    } else if (warp >= 8) {
+        // ------------------------------------------------- C to bf16 terms
+        // 16-byte chunks of eight elements; half of a unit's are taken apart while the
+        // other half is on its way
+        const int t = tid - 256;
+        float4 x[8], y[8];
+        auto fetch = [&](float4 (&r)[8], int u, int half) {
             const float4 *C = reinterpret_cast<const float4 *>(j.C + (size_t)u * kD * kD);
 #pragma unroll
-            for (int i = 0; i < 8; i++) {
-                cr[2 * i] = C[2 * (i * 256 + tid)];
-                cr[2 * i + 1] = C[2 * (i * 256 + tid) + 1];
+            for (int i = 0; i < 4; i++) {
+                const int e = 2 * ((4 * half + i) * 256 + t);
+                r[2 * i] = C[e];
+                r[2 * i + 1] = C[e + 1];
             }
         };
-        // what was fetched into its two terms; c: the count of products before
-        auto terms = [&](int c) {
-            if (c > 1) wait(&S.mdone[c & 1], ((c >> 1) - 1) & 1);   // the terms of two jobs ago are used up
-            if (!ok) return;
-            unsigned char *to = planes + (c & 1) * 2 * kSlot;
+        auto terms = [&](const float4 (&r)[8], int half) {
+            unsigned char *to = planes + (kc & 1) * 2 * kSlot;
 #pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const int e = i * 256 + tid, row = e >> 4, ch = e & 15;
-                const float4 x = cr[2 * i], y = cr[2 * i + 1];
+            for (int i = 0; i < 4; i++) {
+                const int e = (4 * half + i) * 256 + t;
+                const float4 x = r[2 * i], y = r[2 * i + 1];
                 const uint4 hi = make_uint4(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w), pack_bf16(y.x, y.y),
                                             pack_bf16(y.z, y.w));
                 const uint4 lo = make_uint4(pack_bf16(x.x - bf_lo(hi.x), x.y - bf_hi(hi.x)),
                                             pack_bf16(x.z - bf_lo(hi.y), x.w - bf_hi(hi.y)),
                                             pack_bf16(y.x - bf_lo(hi.z), y.y - bf_hi(hi.z)),
                                             pack_bf16(y.z - bf_lo(hi.w), y.w - bf_hi(hi.w)));
-                unsigned char *d = to + sw_off_t<128>(row, ch);
+                unsigned char *d = to + sw_off_t<128>(e >> 4, e & 15);
                 *reinterpret_cast<uint4 *>(d) = hi;
                 *reinterpret_cast<uint4 *>(d + kSlot) = lo;
             }
+        };
+        auto next = [&] {                                    // the next job with a product
+            while (list.next(m))
+                if (m.ne > 0.f) return true;
+            return false;
+        };
+        bool more = j.first_order && next();
+        if (more) {
+            fetch(x, m.u, 0);
+            fetch(y, m.u, 1);
+        }
+        for (; more && ok; kc++) {
+            more = next();
+            if (kc > 1) wait(&S.mdone[kc & 1], ((kc >> 1) - 1) & 1);   // the terms of two jobs ago are used up
+            if (!ok) break;
+            terms(x, 0);
+            if (more) fetch(x, m.u, 0);
+            terms(y, 1);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&S.pready[c & 1]);
+            arrive(&S.pready[kc & 1]);
+            if (more) fetch(y, m.u, 1);
+        }
+    } else if (warp & 2) {
+        // ------------------------------------------------- q . mu_k, mu_v
+        // 16 rows a warp, eight lanes a row of 16 dimensions (two 16-byte chunks)
+        const int q = 16 * (2 * (warp >> 2) + (warp & 1)), dim = 32 * (q >> 4) + lane;
+        float k0[16], k1[16];                                // the lane's part of mu_k, and of the next job's
+        float v0 = 0.f, v1 = 0.f;
+        auto fetch = [&](float (&k)[16], float &v) {
+            if (m.ne <= 0.f) return;
+            const float *mk = j.mu_k + (size_t)m.u * kD + 8 * (lane & 7);
+#pragma unroll
+            for (int i = 0; i < 16; i++) k[i] = mk[64 * (i >> 3) + (i & 7)];
+            v = j.mu_v[(size_t)m.u * kD + dim];
         };
-        // the rows of a job; f, c: counts of jobs and of products before it; the
-        // thread's dimension of the means
-        auto finish = [&](const MomJob &m, int f, int c, float mk1, float mv1, float2 ml) {
-            const int st = f & 1;
-            const bool mix = m.ne > 0.f, prod = mix && j.first_order;
-            wait(&S.ffull[st], (f / 2) & 1);
-            if (prod) wait(&S.mdone[c & 1], (c >> 1) & 1);
-            if (mix && tid < kD) {
-                S.muk[st][tid] = mk1;
-                S.muv[st][tid] = mv1;
-            }
-            if (ok) sync();
-            if (!ok) return;
-            tc_fence_after();
-            if (mix && (warp & 2)) {
-                // q . mu_k: these four warps have 16 rows each, eight lanes a row of
-                // 16 dimensions (two 16-byte chunks)
-                const int q = 16 * (2 * (warp >> 2) + (warp & 1));
-                const float ln = logf(m.ne);
+        bool more = list.next(m);
+        if (more) fetch(k0, v0);
+        for (; more && ok; kf++) {
+            const int st = kf & 1;
+            const float ne = m.ne;
+            more = list.next(m);
+            if (more) fetch(k1, v1);
+            wait(&S.ffull[st], (kf / 2) & 1);
+            if (!ok) break;
+            if (ne > 0.f) {
+                const float ln = logf(ne);
                 float z[4];
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
@@ -1319,11 +1363,10 @@ tree_moment_kernel(const __grid_constant__ JoinArgs j, const __grid_constant__ C
                     z[i] = 0.f;
 #pragma unroll
                     for (int h = 0; h < 2; h++) {
-                        const int ch = (lane & 7) + 8 * h;
                         float f[8];
-                        unpack8(lds_v4(qs + st * kMomQ + sw_off_t<64>(r, ch)), f);
+                        unpack8(lds_v4(qs + st * kMomQ + sw_off_t<64>(r, (lane & 7) + 8 * h)), f);
 #pragma unroll
-                        for (int e = 0; e < 8; e++) z[i] = fmaf(f[e], S.muk[st][8 * ch + e], z[i]);
+                        for (int e = 0; e < 8; e++) z[i] = fmaf(f[e], k0[8 * h + e], z[i]);
                     }
                 }
 #pragma unroll
@@ -1333,15 +1376,41 @@ tree_moment_kernel(const __grid_constant__ JoinArgs j, const __grid_constant__ C
                 if ((lane & 7) == 0)
 #pragma unroll
                     for (int i = 0; i < 4; i++) S.z[st][q + 4 * i + (lane >> 3)] = ln + sd * z[i];
+                S.muv[st][dim] = v0;
             }
-            sync();
-            if (!ok) return;
-            const int row = 32 * (warp & 3) + lane;
-            if (!(warp & 2) && row - lane < m.rows) {
-                const float lse = ml.y == 0.f ? -INFINITY : (ml.x + log2f(ml.y)) * 0.6931471805599453f;
+            arrive(&S.zready[st]);
+            arrive(&S.fempty[st]);
+#pragma unroll
+            for (int i = 0; i < 16; i++) k0[i] = k1[i];
+            v0 = v1;
+        }
+    } else {
+        // --------------------------------------------------------- outputs
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const int col0 = 64 * (warp >> 2), row = 32 * (warp & 3) + lane;
+        auto fetch = [&] { return a.ml[(size_t)m.sid * a.rows + m.r0 + min(row, m.rows - 1)]; };
+        float2 ml0 = make_float2(0.f, 0.f), ml1 = ml0;
+        bool more = list.next(m);
+        if (more) ml0 = fetch();
+        for (; more && ok; kf++) {
+            const int st = kf & 1, c = kc;
+            const MomJob g = m;
+            const bool mix = g.ne > 0.f, prod = mix && j.first_order;
+            more = list.next(m);
+            if (more) ml1 = fetch();
+            wait(&S.ffull[st], (kf / 2) & 1);
+            wait(&S.zready[st], (kf / 2) & 1);
+            if (prod) {
+                wait(&S.mdone[c & 1], (c >> 1) & 1);
+                kc++;
+            }
+            if (!ok) break;
+            tc_fence_after();
+            if (row - lane < g.rows) {
+                const float lse = ml0.y == 0.f ? -INFINITY : (ml0.x + log2f(ml0.y)) * 0.6931471805599453f;
                 const float w = mix ? 1.f / (1.f + expf(S.z[st][row] - lse)) : 1.f;
-                const float wf = ml.y == 0.f ? 0.f : w / ml.y, we = 1.f - w, ws = we * sd;
-                const size_t orow = (size_t)m.u * a.TG + (size_t)(m.row0 + row);
+                const float wf = ml0.y == 0.f ? 0.f : w / ml0.y, we = 1.f - w, ws = we * sd;
+                const size_t orow = (size_t)g.u * a.TG + (size_t)(g.row0 + row);
 #pragma unroll 2
                 for (int h = 0; h < 4; h++) {
                     const int c0 = col0 + 16 * h;
@@ -1372,67 +1441,26 @@ tree_moment_kernel(const __grid_constant__ JoinArgs j, const __grid_constant__ C
                     if (prod)
 #pragma unroll
                         for (int i = 0; i < 16; i++) o[i] = fmaf(ws, __uint_as_float(y[i]), o[i]);
-                    if (row < m.rows) {
+                    uint32_t b[8];
+#pragma unroll
+                    for (int i = 0; i < 8; i++) b[i] = pack_bf16(o[2 * i], o[2 * i + 1]);
+                    if (row < g.rows) {
                         uint4 *d = reinterpret_cast<uint4 *>(a.o + orow * kD + c0);
-                        d[0] = make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]),
-                                          pack_bf16(o[6], o[7]));
-                        d[1] = make_uint4(pack_bf16(o[8], o[9]), pack_bf16(o[10], o[11]),
-                                          pack_bf16(o[12], o[13]), pack_bf16(o[14], o[15]));
+                        d[0] = make_uint4(b[0], b[1], b[2], b[3]);
+                        d[1] = make_uint4(b[4], b[5], b[6], b[7]);
                     }
                 }
-                if (row < m.rows && col0 == 0) a.lse[orow] = lse;
+                if (row < g.rows && col0 == 0) a.lse[orow] = lse;
             }
             tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&S.fempty[st]);
-        };
-        // the next job with rows from `job` on (jobs: there is none)
-        auto next = [&](int job, MomJob &m) {
-            for (; job < jobs; job += gridDim.x) {
-                m = mom_job(j, cuts, per, job);
-                if (m.rows > 0) break;
-            }
-            return min(job, jobs);
-        };
-        MomJob last, m;
-        last.rows = 0;
-        int lc = 0;
-        float mk1 = 0.f, mv1 = 0.f, mk2 = 0.f, mv2 = 0.f;
-        float2 ml1 = make_float2(0.f, 0.f), ml2 = ml1;
-        auto ahead = [&](const MomJob &x) {
-            if (x.ne > 0.f) {
-                if (j.first_order) fetch(x.u);
-                if (tid < kD) {
-                    mk2 = j.mu_k[(size_t)x.u * kD + tid];
-                    mv2 = j.mu_v[(size_t)x.u * kD + tid];
-                }
-            }
-            ml2 = a.ml[(size_t)x.sid * a.rows + x.r0 + min(32 * (warp & 1) + lane, x.rows - 1)];
-        };
-        int job = next(blockIdx.x, m);
-        if (job < jobs) ahead(m);
-        while (ok && job < jobs) {
-            const int c = kc;
-            if (m.ne > 0.f && j.first_order) terms(kc++);
-            const float mk3 = mk2, mv3 = mv2;
-            const float2 ml3 = ml2;
-            MomJob n;
-            job = next(job + gridDim.x, n);
-            if (job < jobs) ahead(n);
-            if (ok && last.rows > 0) finish(last, kf - 1, lc, mk1, mv1, ml1);
-            last = m;
-            m = n;
-            lc = c;
-            mk1 = mk3;
-            mv1 = mv3;
-            ml1 = ml3;
-            kf++;
+            if (prod) arrive(&S.dfree[c & 1]);
+            arrive(&S.fempty[st]);
+            ml0 = ml1;
         }
-        if (ok && last.rows > 0) finish(last, kf - 1, lc, mk1, mv1, ml1);
-        if (!ok && lane == 0) S.bad = 1;
     }
+    if (!ok && lane == 0) S.bad = 1;
     __syncthreads();
-    if (warp == 9) tmem_dealloc(tmem, 256);
+    if (warp == 17) tmem_dealloc(tmem, 256);
     if (tid == 0 && S.bad) record_status(a.status, KVC_ERR_TIMEOUT);
 }
 
