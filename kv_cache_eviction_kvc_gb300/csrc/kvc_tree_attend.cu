@@ -1136,7 +1136,8 @@ struct MomJob {
     float ne;
 };
 
-__device__ __forceinline__ MomJob mom_job(const JoinArgs &j, const LineCuts &cuts, int per, int job)
+// sums: the place of the sums is wanted, which is known after the attention.
+__device__ __forceinline__ MomJob mom_job(const JoinArgs &j, bool sums, int per, int job)
 {
     const AttArgs &a = j.a;
     MomJob m;
@@ -1149,19 +1150,24 @@ __device__ __forceinline__ MomJob mom_job(const JoinArgs &j, const LineCuts &cut
                  ? 0 : min(kMomRows, min(kRows, (live << a.gshift) - rb * kRows) - m.r0);
     m.ne = j.mn[m.u];
     // the part that has the item's start (its place has the joined sums)
-    m.sid = m.rows > 0 ? item + cuts.part(a.whole ? item : a.first[item]) : 0;
+    m.sid = 0;
+    if (sums && m.rows > 0) {
+        const int items = a.U * a.RB;
+        const LineCuts cuts(j.grid, a.whole ? items : a.first[items]);
+        m.sid = item + cuts.part(a.whole ? item : a.first[item]);
+    }
     return m;
 }
 
 // A CTA's jobs with rows, one after another, for a whole warp.
 struct MomJobs {
     const JoinArgs &j;
-    const LineCuts &cuts;
+    bool sums;
     int per, jobs, k;             // k: the next one, in steps of the grid
     MomJob mine;                  // lane i: job k - k % 32 + i
 
-    __device__ __forceinline__ MomJobs(const JoinArgs &j, const LineCuts &cuts, int per, int jobs)
-        : j(j), cuts(cuts), per(per), jobs(jobs), k(0)
+    __device__ __forceinline__ MomJobs(const JoinArgs &j, bool sums, int per, int jobs)
+        : j(j), sums(sums), per(per), jobs(jobs), k(0)
     {
     }
     __device__ __forceinline__ bool next(MomJob &m)
@@ -1171,7 +1177,7 @@ struct MomJobs {
             if ((k & 31) == 0) {
                 const long long job = (long long)(k + (threadIdx.x & 31)) * gridDim.x + blockIdx.x;
                 mine.rows = 0;
-                if (job < jobs) mine = mom_job(j, cuts, per, (int)job);
+                if (job < jobs) mine = mom_job(j, sums, per, (int)job);
             }
             m.rows = __shfl_sync(kFull, mine.rows, k & 31);
             if (m.rows > 0) break;
@@ -1215,10 +1221,12 @@ tree_moment_kernel(const __grid_constant__ JoinArgs j, const __grid_constant__ C
     if (warp == 17) tmem_alloc(&S.tmem, 256);
     __syncthreads();
     tc_fence_after();
-    follow();
     const uint32_t tmem = S.tmem;
-    const LineCuts cuts(j.grid, a.whole ? items : a.first[items]);
-    MomJobs list(j, cuts, per, items * per);
+    // the sums, the place they are at and the outputs wait for the kernels before; the
+    // rest of this one reads what they only read
+    const bool sums = warp == 16 || (warp < 8 && !(warp & 2));
+    if (sums) follow();
+    MomJobs list(j, sums, per, items * per);
     MomJob m;
     const float sd = rsqrtf((float)kD);
     bool ok = true;
