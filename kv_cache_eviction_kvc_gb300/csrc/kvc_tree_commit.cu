@@ -25,6 +25,7 @@
 // candidate: then the bound is taken again over whole (utility, position,
 // slot) keys, which are distinct; and if the lowest keys sit in so few sets
 // that even these are too many, the k lowest are found one after another.
+#include "kvc_soft64.h"
 #include "kvc_tree.h"
 
 #include <stddef.h>
@@ -78,6 +79,7 @@ struct ComArgs {
     uint64_t *gmin;                      // [U][cap] lowest key of every 32 slots (long units)
     double alpha, beta;                  // EMA: alpha util + beta weight
     int cap, L, rule, kmax, max_len;
+    bool soft;                           // EMA: alpha and beta are ones soft_fma takes
     FastDiv by_units;
 };
 
@@ -86,7 +88,7 @@ struct ComSmem {
     Key set[128];
     Key bound;
     double fresh[kTreeMax];              // utilities of the accepted tokens
-    float bar[2][kD], del[2][kD];        // batch means; their distance from the moments'
+    float del[2][kD];                    // the batch means' distance from the moments'
     float w[kTreeMax];
     int32_t tok[kTreeMax];
     int vic[kTreeMax], src[kTreeMax], gone[kTreeMax];
@@ -94,8 +96,7 @@ struct ComSmem {
     int n_cand, n_hole;
     alignas(16) float kv[4];             // [2][kmax][kD]: the victims' keys and values
 };
-static_assert(offsetof(ComSmem, kv) % 16 == 0 && offsetof(ComSmem, bar) % 16 == 0 &&
-                  offsetof(ComSmem, del) % 16 == 0, "read as float4");
+static_assert(offsetof(ComSmem, kv) % 16 == 0 && offsetof(ComSmem, del) % 16 == 0, "read as float4");
 
 // What a unit does: its lengths and counts, or why it is refused.  Warp-wide.
 struct Plan {
@@ -127,23 +128,25 @@ __device__ __forceinline__ Plan plan_unit(const ComArgs &a, int u, int lane)
     return p;
 }
 
-// An fp32 as fp64 by integer operations: conversions run on the fp64 pipe,
-// which is narrow on this part (about one operation a clock per SM) and the
-// bound of step 1.  Zeros and normal numbers; the rest is converted.
-__device__ __forceinline__ double widen(float x)
-{
-    const uint32_t b = __float_as_uint(x), e = b >> 23 & 255;
-    if (e - 1u < 254u)
-        return __hiloint2double((int)((b & 0x80000000u) | ((b & 0x7fffffffu) >> 3) + (896u << 20)), (int)(b << 29));
-    return (b & 0x7fffffffu) == 0 ? __hiloint2double((int)b, 0) : (double)x;
-}
-
+// fp64 by integer operations where the operands are the usual ones: the fp64
+// pipe is the bound of step 1 otherwise (a warp's addition every 88 clocks of
+// an SM; a million slots: 14.5 us with it, SOFT_US without).
 __device__ __forceinline__ double new_util(const ComArgs &a, double m, float weight)
 {
-    const double s = widen(weight);
     const uint64_t b = (uint64_t)__double_as_longlong(m);
-    if ((b & 0x7fffffffffffffffull) == 0x7ff0000000000000ull || a.rule == KVC_RULE_SINGLE) return s;
-    return a.rule == KVC_RULE_CUMULATIVE ? m + s : fma(a.alpha, m, a.beta * s);
+    const uint32_t w = __float_as_uint(weight);
+    const bool zero = w == 0, usual = zero || (w >> 23) - 1u < 254u;
+    if ((b & 0x7fffffffffffffffull) == 0x7ff0000000000000ull || a.rule == KVC_RULE_SINGLE)
+        return !usual ? (double)weight : __longlong_as_double(zero ? 0ll : (long long)soft_widen(w));
+    if (a.rule == KVC_RULE_CUMULATIVE) {
+        if (!usual || !(b == 0 || soft_normal(b))) return m + (double)weight;
+        if (zero) return m;
+        const uint64_t s = soft_widen(w);
+        return __longlong_as_double((long long)(b == 0 ? s : soft_add(b, s)));
+    }
+    if (!usual || !a.soft || !(b == 0 || soft_normal(b))) return fma(a.alpha, m, a.beta * (double)weight);
+    const uint64_t s = zero ? 0 : soft_mul((uint64_t)__double_as_longlong(a.beta), w);
+    return __longlong_as_double((long long)(b == 0 ? s : soft_fma((uint64_t)__double_as_longlong(a.alpha), b, s)));
 }
 
 // Long units: the utilities of kChunk slots, and the lowest key of every 32.
@@ -184,23 +187,22 @@ __global__ void __launch_bounds__(kThreads) tree_update_kernel(ComArgs a)
 // k sets have a key); `mine` is the thread's own minimum.
 __device__ __forceinline__ void rank_utils(ComSmem &s, uint64_t mine, int k)
 {
-    const int tid = threadIdx.x, fold = k <= 16 ? 8 : 2, sets = kThreads / fold;
+    const int tid = threadIdx.x, fold = k <= 16 ? 8 : 2, sets = kThreads / fold, own = tid / fold;
     uint64_t *set = reinterpret_cast<uint64_t *>(s.set);
     for (int d = 1; d < fold; d <<= 1)
         mine = min((unsigned long long)mine, __shfl_xor_sync(kFull, (unsigned long long)mine, d));
-    if (tid % fold == 0) set[tid / fold] = mine;
+    if (tid % fold == 0) set[own] = mine;
     if (tid == 0) s.n_cand = 0;
     __syncthreads();
-    if (tid < sets) {
-        const uint64_t x = set[tid];
-        int r = 0;
+    // a set's rank, counted by its threads together
+    int r = 0;
 #pragma unroll 8
-        for (int j = 0; j < sets; j++) {
-            const uint64_t y = set[j];
-            r += y < x || (y == x && j < tid);
-        }
-        if (r == k - 1) s.bound = Key{x, kNone};
+    for (int j = tid % fold; j < sets; j += fold) {
+        const uint64_t y = set[j];
+        r += y < mine || (y == mine && j < own);
     }
+    for (int d = 1; d < fold; d <<= 1) r += __shfl_xor_sync(kFull, r, d);
+    if (r == k - 1 && tid % fold == 0) s.bound = Key{mine, kNone};
     __syncthreads();
 }
 
@@ -265,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 4) tree_commit_kernel(ComArgs a)
     // 1. the lowest key of the thread's slots (long units: of its groups of 32)
     uint64_t mine = kNone;
     if (kSplit) {
-#pragma unroll 4
+#pragma unroll 8
         for (int g = tid; g < groups; g += kThreads) mine = min((unsigned long long)mine, (unsigned long long)gmin[g]);
     } else {
         for (int i0 = tid; i0 < n; i0 += 4 * kThreads) {
@@ -310,24 +312,32 @@ __global__ void __launch_bounds__(kThreads, 4) tree_commit_kernel(ComArgs a)
             const uint64_t x = util_key(s.fresh[tid]);
             if (x != kNone) add_candidate(s, Key{x, tie_key(pos0 + tid, n + tid)});
         }
+        auto look = [&](int i) {                             // (both loads in flight together)
+            const double m = i < n ? util[i] : __longlong_as_double(0x7ff0000000000000ll);
+            const int32_t at = i < n ? pos[i] : 0;
+            const uint64_t x = util_key(m);
+            if (x != kNone && x <= top) add_candidate(s, Key{x, tie_key(at, i)});
+        };
         if (kSplit) {
             // a warp looks through the groups that one of its threads found low
-            for (int g0 = 32 * warp; g0 < groups; g0 += kThreads) {
-                const int g = g0 + lane;
-                const uint64_t x = g < groups ? gmin[g] : kNone;
-                for (unsigned todo = __ballot_sync(kFull, x != kNone && x <= top); todo; todo &= todo - 1) {
-                    const int i = 32 * (g0 + __ffs(todo) - 1) + lane;
-                    const uint64_t y = i < n ? util_key(util[i]) : kNone;
-                    if (y != kNone && y <= top) add_candidate(s, Key{y, tie_key(pos[i], i)});
+            constexpr int kAt = 8;                           // loads in flight
+            for (int g0 = 32 * warp; g0 < groups; g0 += kAt * kThreads) {
+                uint64_t x[kAt];
+#pragma unroll
+                for (int j = 0; j < kAt; j++) {
+                    const int g = g0 + j * kThreads + lane;
+                    x[j] = g < groups ? gmin[g] : kNone;
                 }
+#pragma unroll
+                for (int j = 0; j < kAt; j++)
+                    for (unsigned todo = __ballot_sync(kFull, x[j] != kNone && x[j] <= top); todo; todo &= todo - 1)
+                        look(32 * (g0 + j * kThreads + __ffs(todo) - 1) + lane);
             }
         } else {
             // a warp looks through the slots of each of its threads that found one low
             // (every kThreads-th slot: at most 32 of them)
             for (unsigned todo = __ballot_sync(kFull, mine != kNone && mine <= top); todo; todo &= todo - 1) {
-                const int i = 32 * warp + __ffs(todo) - 1 + kThreads * lane;
-                const uint64_t x = i < n ? util_key(util[i]) : kNone;
-                if (x != kNone && x <= top) add_candidate(s, Key{x, tie_key(pos[i], i)});
+                look(32 * warp + __ffs(todo) - 1 + kThreads * lane);
             }
         }
         __syncthreads();
@@ -400,6 +410,7 @@ __global__ void __launch_bounds__(kThreads, 4) tree_commit_kernel(ComArgs a)
         __syncthreads();
         // the victims' rows, before any of them is overwritten
         if (a.C)
+#pragma unroll 4
             for (int e = tid; e < k * 32; e += kThreads) {
                 const int j = e >> 5, ch = e & 15, which = e >> 4 & 1, i = s.vic[j];
                 const uint16_t *row = i < n ? (which ? a.V : a.K) + (cb + i) * kD
@@ -449,22 +460,22 @@ __global__ void __launch_bounds__(kThreads, 4) tree_commit_kernel(ComArgs a)
     // the moments: the batch's weighted means and co-moment, merged (Chan,
     // Golub and LeVeque, 1979)
     const int which = tid >> 7, d = tid & 127;
-    const float *kv = s.kv, *vv = s.kv + a.kmax * kD;
+    float *kv = s.kv, *vv = s.kv + a.kmax * kD, *own = (which ? vv : kv) + d;
     float *mu = (which ? a.mu_v : a.mu_k) + (size_t)u * kD + d;
     const float mu0 = *mu, n0 = a.mn[u];
     float nb = 0.f, x = 0.f;
     for (int j = 0; j < k; j++) {
         nb += s.w[j];
-        x += s.w[j] * (which ? vv : kv)[j * kD + d];
+        x += s.w[j] * own[j * kD];
     }
     const float n1 = n0 + nb;
     x /= nb;
-    s.bar[which][d] = x;
     s.del[which][d] = x - mu0;
+    // the batch about its means, values weighted
+    for (int j = 0; j < k; j++) own[j * kD] = which ? s.w[j] * (own[j * kD] - x) : own[j * kD] - x;
     *mu = mu0 + (x - mu0) * (nb / n1);
     __syncthreads();
     // warp w: rows (value dimensions) 16 w .., four columns a lane
-    const float4 kb = reinterpret_cast<const float4 *>(s.bar[0])[lane];
     const float4 dk = reinterpret_cast<const float4 *>(s.del[0])[lane];
     const float cross = n0 * (nb / n1) / n1, keep = n0 / n1, inv = 1.f / n1;
 #pragma unroll 1
@@ -477,17 +488,11 @@ __global__ void __launch_bounds__(kThreads, 4) tree_commit_kernel(ComArgs a)
             old[i] = c[i * (kD / 4)];
             m[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        const float4 vb = *reinterpret_cast<const float4 *>(&s.bar[1][row]);
 #pragma unroll 2
         for (int j = 0; j < k; j++) {
-            float4 y = reinterpret_cast<const float4 *>(kv + j * kD)[lane];
+            const float4 y = reinterpret_cast<const float4 *>(kv + j * kD)[lane];
             const float4 x4 = *reinterpret_cast<const float4 *>(vv + j * kD + row);
-            const float w = s.w[j];
-            y.x -= kb.x;
-            y.y -= kb.y;
-            y.z -= kb.z;
-            y.w -= kb.w;
-            const float v[4] = {w * (x4.x - vb.x), w * (x4.y - vb.y), w * (x4.z - vb.z), w * (x4.w - vb.w)};
+            const float v[4] = {x4.x, x4.y, x4.z, x4.w};
 #pragma unroll
             for (int i = 0; i < 4; i++) {
                 m[i].x = fmaf(v[i], y.x, m[i].x);
@@ -520,7 +525,7 @@ cudaError_t launch_tree_commit(const kvc_params &p, int max_len, const TreeArgs 
               m ? m->n : nullptr, m ? m->mu_k : nullptr, m ? m->mu_v : nullptr, m ? m->C : nullptr,
               evict_idx, evict_pos, n_evict, ws.status, ws.pend,
               reinterpret_cast<uint64_t *>(ws.probs), (double)p.alpha, 1.0 - (double)p.alpha, p.cap, p.L, p.rule, kmax,
-              max_len, FastDiv(t.units)};
+              max_len, p.alpha > 1e-30f && p.alpha < 1.f, FastDiv(t.units)};
     const bool split = max_len > kLong;
     const size_t smem = sizeof(ComSmem) + (m ? 2 * (size_t)kmax * kD * sizeof(float) : 0);
     auto *kernel = split ? tree_commit_kernel<true> : tree_commit_kernel<false>;

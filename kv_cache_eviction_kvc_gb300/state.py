@@ -153,22 +153,12 @@ class DecodeState:
         """Attention of a tree of drafted tokens over the cache (the cache
         does not change): q [U][T][G][d], k_tree / v_tree [U][T][d].  Returns
         (o [U][T][G][d] bf16, lse [U][T][G] fp32), buffers of the state that
-        the next call with the same T writes again."""
-        T = tree.T
-        if getattr(self, "tree_T", 0) != T:
-            nbytes = K_.kvc_tree_workspace_size(self.params, T)
-            if nbytes == 0:
-                raise K_.KvcError(K_.KVC_ERR_INVALID_ARG, f"no trees of T = {T} tokens")
-            dev = self.device
-            self.tree_T = T
-            self.tree_ws = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
-            self.tree_o = torch.zeros(self.U, T, self.G, self.d, dtype=torch.bfloat16, device=dev)
-            self.tree_lse = torch.zeros(self.U, T, self.G, dtype=torch.float32, device=dev)
-            self.tree_S = torch.zeros(self.U, self.cap, dtype=torch.float32, device=dev)
-            self.tree_evict = torch.full((2, self.U, K_.TREE_MAX), -1, dtype=torch.int32, device=dev)
+        the next call with the same T writes again.  The first call with a T
+        allocates: make it before capturing one into a graph."""
+        b = self._tree_buffers(tree.T, make=True)
         K_.kvc_tree_attend(self.params, max_len, tree, q, k_tree, v_tree, self.cache, self.moments,
-                           self.tree_o, self.tree_lse, self.tree_ws, stream)
-        return self.tree_o, self.tree_lse
+                           b["o"], b["lse"], b["ws"], stream)
+        return b["o"], b["lse"]
 
     def accept(self, tree: K_.kvc_tree, path: K_.kvc_path, q, k_tree, v_tree, max_len: int,
                row_weight=None, refresh=True, stream=None):
@@ -177,14 +167,40 @@ class DecodeState:
         (row_weight: fp32 [trees][A] or None); the lowest go until every unit
         is at its budget.  self.n_evict has the counts, self.tree_evict the
         slots and positions."""
+        b = self._tree_buffers(tree.T, make=False)
         S = None
         if refresh:
             S = self.tree_S
             K_.kvc_tree_weights(self.params, max_len, tree, path, row_weight, q, k_tree,
-                                self.tree_lse, self.cache, S, self.tree_ws, stream)
+                                b["lse"], self.cache, S, b["ws"], stream)
         K_.kvc_tree_commit(self.params, max_len, tree, path, k_tree, v_tree, S, self.cache,
                            self.moments, K_.TREE_MAX, self.tree_evict[0], self.tree_evict[1],
                            self.n_evict, self.ws, stream)
 
+    def _tree_buffers(self, T, make):
+        """What verify and accept of trees of T tokens use; kept for each T
+        (a captured graph goes on using them)."""
+        trees = self.__dict__.setdefault("_trees", {})
+        if T not in trees:
+            if not make:
+                raise ValueError(f"no tree of T = {T} tokens has been verified")
+            nbytes = K_.kvc_tree_workspace_size(self.params, T)
+            if nbytes == 0:
+                raise ValueError(f"no trees of T = {T} tokens")
+            dev = self.device
+            if not trees:
+                self.tree_S = torch.zeros(self.U, self.cap, dtype=torch.float32, device=dev)
+                self.tree_evict = torch.full((2, self.U, K_.TREE_MAX), -1, dtype=torch.int32, device=dev)
+            trees[T] = dict(
+                ws=torch.zeros(nbytes, dtype=torch.uint8, device=dev),
+                o=torch.zeros(self.U, T, self.G, self.d, dtype=torch.bfloat16, device=dev),
+                lse=torch.zeros(self.U, T, self.G, dtype=torch.float32, device=dev))
+        return trees[T]
+
     def tree_status(self) -> int:
-        return K_.kvc_get_device_status(self.tree_ws)
+        """The first error that a verify or accept recorded (0: none)."""
+        for b in self.__dict__.get("_trees", {}).values():
+            status = K_.kvc_get_device_status(b["ws"])
+            if status:
+                return status
+        return 0

@@ -3,6 +3,8 @@ kvc_tree_commit) against their definitions in 64 bits (tree_ref.py): head
 layouts, lengths from zero on, ragged trees and budgets, masks that leave rows
 empty, NaN where nothing looks, ties, every rule; then runs of the three
 together against the one-token calls, streams and graphs."""
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -402,6 +404,8 @@ COMMIT = [
     (1, 3, [5, 5], [3, 3], 3, dict(L=9), True),                        # room left: nothing goes
     (4, 24, [100, 200, 300, 400] * 45, [i % 7 for i in range(45)], 6,
      dict(budget=[100, 200, 300, 400] * 45, L=400), True),
+    (1, 30, [9000, 8193, 40], [20, 3, 30], 30,                         # long units, more than 16 victims
+     dict(budget=[9000, 8180, 50], L=9000, votes=True, moments=True, unscored=True), True),
 ]
 
 
@@ -430,6 +434,96 @@ def test_commit_ties(n, ties):
         S[:, ::512] = 0.25
         S[:, 1:3000:3] = 0.5
     check_commit(c, S, 40)
+
+
+@pytest.mark.parametrize("n", [300, 9000])
+@pytest.mark.parametrize("rule", ["cumulative", "ema"])
+def test_commit_utilities_to_the_bit(rule, n):
+    """The new utilities are what IEEE arithmetic gives (a multiply-add of the
+    rounded product under EMA), for operands all over the range."""
+    c = Case(13, 1, 1, 2, [n], cap=n + 4, rule=rule)
+    c.path([1], 1)
+    rng = c.rng
+    m = np.exp2(rng.uniform(-60, 20, n)) * (1 + rng.integers(0, 4, n) * 2.0 ** -52)
+    s = np.exp2(rng.uniform(-60, 20, n)).astype(np.float32)
+    m[:200:2] = np.exp2(rng.integers(-30, 3, 100).astype(np.float64))          # ties of the rounding
+    s[:200:2] = (np.exp2(rng.integers(-40, 3, 100)) * rng.integers(1, 4, 100)).astype(np.float32)
+    odd = [(0.0, 0.0), (0.0, 1.5), (0.25, 0.0), (5e-324, 1e-45), (1e-310, 0.0), (1e300, 1.0),
+           (1e-300, 1e-38), (2.0 ** -699, 0.0), (-1.5, 1.5), (-1.5, 0.25), (1.0, 1e-45),
+           (1.0, 3e38), (0.0, 1e-42), (1.0, 2.0 ** -53), (1 + 2.0 ** -52, 2.0 ** -53),
+           (2 - 2.0 ** -52, 2.0 ** -53), (2.0 ** -53, 2.0 ** 60)]
+    for i, (x, y) in enumerate(odd):
+        m[201 + i], s[201 + i] = x, np.float32(y)
+    c.t["util"][0, :n] = torch.from_numpy(m).to(DEV)
+    S = np.ones((1, c.cap), np.float32)
+    S[0, :n] = s
+    run_commit(c, S, 1)
+    got = f64(c.t["util"])[0, :n]
+    if rule == "cumulative":
+        want = m + s.astype(np.float64)
+    else:
+        want = np.array([float(Fraction(0.75) * Fraction(x) + Fraction(0.25 * float(y)))
+                         for x, y in zip(m, s)])
+    assert np.array_equal(got, want), np.flatnonzero(got != want)[:10]
+
+
+def test_commit_of_a_token_named_twice():
+    """A path is a list of live tokens; one that is named twice is appended
+    twice, and its weights count twice."""
+    c = Case(14, 1, 2, 4, [70, 40], cap=80, L=70, kind="chain", moments=True)
+    c.path([3, 4], 4)
+    c.tok[:] = [[2, 0, 2, 0], [1, 1, 1, 3]]
+    c.t["tok"].copy_(torch.from_numpy(c.tok))
+    o, lse = c.run_attend()
+    S = torch.full((c.U, c.cap), -3.0, device=DEV)
+    K.kvc_tree_weights(c.p, c.max_len, c.tree, c.accept, None, c.t["q"], c.t["kt"], lse, c.cache, S, c.ws)
+    assert K.kvc_get_device_status(c.ws) == 0
+    for u in range(c.U):
+        n, a = c.lens[u], c.counts[u]
+        rs, bs = R.weights(c.q[u], c.K[u], None, n, c.kt[u], c.mask[u], [int(x) for x in c.tok[u, :a]],
+                           np.ones(4), f64(lse[u]))
+        assert (np.abs(f64(S[u, :n + a]) - rs) <= bs).all()
+    check_commit(c, S.cpu().numpy(), 3)
+
+
+def test_commit_in_a_graph():
+    """Weights and commit captured once and replayed from two states: what
+    the calls give."""
+    def make(seed):
+        c = Case(seed, 2, 4, 9, [700, 90, 33, 400], votes=True, moments=True,
+                 budget=[700, 88, 33, 398], L=700)
+        c.path([4, 2], 4)
+        c.run_attend()
+        return c
+
+    def call(c):
+        K.kvc_tree_weights(c.p, c.max_len, c.tree, c.accept, None, c.t["q"], c.t["kt"], c.lse, c.cache,
+                           c.S, c.ws)
+        K.kvc_tree_commit(c.p, c.max_len, c.tree, c.accept, c.t["kt"], c.t["vt"], c.S, c.cache,
+                          c.moments, 6, None, None, c.ne, c.dws)
+
+    def state(c):
+        return [c.t[n] for n in ("K", "V", "votes", "pos", "util", "len")] + c.t["mom"] + [c.ne]
+
+    c = make(31)
+    c.S = torch.zeros(c.U, c.cap, device=DEV)
+    c.ne = torch.zeros(c.U, dtype=torch.int32, device=DEV)
+    first = [x.clone() for x in state(c)]
+    call(c)
+    want = [x.clone() for x in state(c)]
+    for x, y in zip(state(c), first):
+        x.copy_(y)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(c)
+    for _ in range(3):
+        for x, y in zip(state(c), first):
+            x.copy_(y)
+        g.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(state(c), want):
+            assert torch.equal(x.contiguous().view(torch.uint8), y.contiguous().view(torch.uint8))
+    assert K.kvc_get_device_status(c.dws) == 0 and K.kvc_get_device_status(c.ws) == 0
 
 
 def test_commit_same_position_and_weight_goes_by_slot():
@@ -608,6 +702,57 @@ def test_graphs_that_share_a_workspace_and_another_stream():
             torch.cuda.synchronize()
             for x, y in zip((c.o, c.lse, c.S), w):
                 assert torch.equal(x, y)               # the same bits, run after run
+
+
+def test_calls_at_once_on_two_streams():
+    """Two verifications in flight together, a workspace each: the bits that
+    each gives alone."""
+    cases = [_graph_case(41), _graph_case(42)]
+    for c in cases:
+        c.call()
+    want = [[x.clone() for x in (c.o, c.lse, c.S)] for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        for c, s in zip(cases, streams):
+            c.call(s)
+    torch.cuda.synchronize()
+    for c, w in zip(cases, want):
+        for x, y in zip((c.o, c.lse, c.S), w):
+            assert torch.equal(x, y)
+        assert K.kvc_get_device_status(c.ws) == 0
+
+
+def test_state_keeps_buffers_of_every_tree_size():
+    """A graph of a verification stays valid when the same state verifies
+    trees of another size in between."""
+    U, G, L = 4, 4, 80
+    st, rnd = _stream(5, U, G, L, L + 20, L, 1)
+    trees, args = {}, {}
+    for T in (3, 7):
+        mask = tree_masks(np.random.default_rng(T), 1, T, "chain")
+        trees[T] = K.make_tree(T, U, torch.from_numpy(mask.view(np.int64)).to(DEV))
+        args[T] = (rnd(U, T, G, 128).bfloat16(), rnd(U, T, 128).bfloat16(), rnd(U, T, 128).bfloat16())
+    path = K.make_path(2, torch.tensor([[0, 1]], dtype=torch.int32, device=DEV),
+                       torch.tensor([2], dtype=torch.int32, device=DEV),
+                       torch.tensor([500], dtype=torch.int32, device=DEV))
+    with pytest.raises(ValueError):
+        st.accept(trees[3], path, *args[3], L)          # nothing verified yet
+    o, lse = st.verify(trees[3], *args[3], L)
+    want = o.clone(), lse.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        st.verify(trees[3], *args[3], L)
+    o7 = [x.clone() for x in st.verify(trees[7], *args[7], L)]
+    o.zero_(), lse.zero_()
+    g.replay()
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    again = st.verify(trees[7], *args[7], L)
+    assert torch.equal(again[0], o7[0]) and torch.equal(again[1], o7[1])
+    assert st.verify(trees[3], *args[3], L)[0].data_ptr() == o.data_ptr()
+    st.accept(trees[3], path, *args[3], L)
+    assert st.tree_status() == 0 and st.device_status() == 0
+    assert st.len.tolist() == [L] * U and st.n_evict.tolist() == [2] * U
 
 
 def test_offsets_past_32_bits():
