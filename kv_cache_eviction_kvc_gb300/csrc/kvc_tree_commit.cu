@@ -76,7 +76,8 @@ struct ComArgs {
     const int32_t *budget;
     float *mn, *mu_k, *mu_v, *C;
     int32_t *evict_idx, *evict_pos, *n_evict, *status, *pend;
-    uint64_t *gmin;                      // [U][cap] lowest key of every 32 slots (long units)
+    uint64_t *gmin;                      // [U][gstride] lowest keys of 32 slots each (long units)
+    int gstride;
     double alpha, beta;                  // EMA: alpha util + beta weight
     int cap, L, rule, kmax, max_len;
     FastDiv by_units;
@@ -92,7 +93,7 @@ struct ComSmem {
     int32_t tok[kTreeMax];
     int vic[kTreeMax], src[kTreeMax], gone[kTreeMax];
     int scan[40];
-    int n_cand, n_hole;
+    int n_cand, n_low, n_hole;
     alignas(16) float kv[4];             // [2][kmax][kD]: the victims' keys and values
 };
 static_assert(offsetof(ComSmem, kv) % 16 == 0 && offsetof(ComSmem, del) % 16 == 0, "read as float4");
@@ -153,8 +154,16 @@ __device__ __forceinline__ double new_util(const ComArgs &a, double m, float wei
     return fma(a.alpha, m, a.beta * __longlong_as_double((long long)s));
 }
 
-// Long units: the utilities of kChunk slots, and the lowest key of every 32.
-// grid (chunks, U)
+// Long units: the utilities of kChunk slots, and the lowest keys of 32 slots
+// each.  A group is what four neighbouring threads have (eight slots each, every
+// kThreads-th), so that little goes between lanes.  grid (chunks, U)
+constexpr int kGroups = kChunk / 32;     // groups of a chunk
+
+__device__ __forceinline__ int group_slot(int g, int i)          // the i-th slot of a group
+{
+    return g / kGroups * kChunk + 4 * (g % kGroups) + (i & 3) + kThreads * (i >> 2);
+}
+
 __global__ void __launch_bounds__(kThreads) tree_update_kernel(ComArgs a)
 {
     const int u = blockIdx.y, lane = threadIdx.x & 31;
@@ -162,6 +171,7 @@ __global__ void __launch_bounds__(kThreads) tree_update_kernel(ComArgs a)
     if (p.err != KVC_OK) return;
     const size_t cb = (size_t)u * a.cap;
     const int i0 = blockIdx.x * kChunk + threadIdx.x;
+    uint64_t low = kNone;
     if (i0 - (int)threadIdx.x >= p.n) return;
     constexpr int kPer = kChunk / kThreads;
     double m[kPer];
@@ -179,12 +189,11 @@ __global__ void __launch_bounds__(kThreads) tree_update_kernel(ComArgs a)
             m[j] = new_util(a, m[j], s[j]);
             a.util[cb + i] = m[j];
         }
-        uint64_t x = util_key(m[j]);
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1)
-            x = min((unsigned long long)x, __shfl_xor_sync(kFull, (unsigned long long)x, d));
-        if (lane == 0 && i < p.n) a.gmin[cb / 32 + u + (i >> 5)] = x;
+        low = min((unsigned long long)low, (unsigned long long)util_key(m[j]));
     }
+#pragma unroll
+    for (int d = 1; d < 4; d <<= 1) low = min((unsigned long long)low, __shfl_xor_sync(kFull, (unsigned long long)low, d));
+    if ((lane & 3) == 0) a.gmin[(size_t)u * a.gstride + blockIdx.x * kGroups + (threadIdx.x >> 2)] = low;
 }
 
 // The k-th smallest of the sets' minima into s.bound.u (kNone when fewer than
@@ -196,7 +205,7 @@ __device__ __forceinline__ void rank_utils(ComSmem &s, uint64_t mine, int k)
     for (int d = 1; d < fold; d <<= 1)
         mine = min((unsigned long long)mine, __shfl_xor_sync(kFull, (unsigned long long)mine, d));
     if (tid % fold == 0) set[own] = mine;
-    if (tid == 0) s.n_cand = 0;
+    if (tid == 0) s.n_cand = s.n_low = 0;
     __syncthreads();
     // a set's rank, counted by its threads together
     int r = 0;
@@ -238,7 +247,7 @@ __device__ __forceinline__ void add_candidate(ComSmem &s, const Key &k)
 }
 
 template <bool kSplit>
-__global__ void __launch_bounds__(kThreads, 4) tree_commit_kernel(ComArgs a)
+__global__ void __launch_bounds__(kThreads, kSplit ? 2 : 4) tree_commit_kernel(ComArgs a)
 {
     extern __shared__ __align__(16) unsigned char raw[];
     ComSmem &s = *reinterpret_cast<ComSmem *>(raw);
@@ -270,8 +279,8 @@ __global__ void __launch_bounds__(kThreads, 4) tree_commit_kernel(ComArgs a)
     const int n = p.n, acc = p.acc, total = p.total, k = p.k, b = a.by_units(u);
     const size_t tb = (size_t)u * a.t.T;
     int32_t *pos = a.pos + cb;
-    const uint64_t *gmin = a.gmin + cb / 32 + u;
-    const int pos0 = a.p.pos[b], groups = (n + 31) >> 5;
+    const uint64_t *gmin = a.gmin + (size_t)u * a.gstride;
+    const int pos0 = a.p.pos[b], groups = (n + kChunk - 1) / kChunk * kGroups;
     float *C = a.C + (size_t)u * kD * kD;
     if (a.C && k > 0) {
 #pragma unroll
@@ -328,32 +337,50 @@ __global__ void __launch_bounds__(kThreads, 4) tree_commit_kernel(ComArgs a)
             const uint64_t x = util_key(s.fresh[tid]);
             if (x != kNone) add_candidate(s, Key{x, tie_key(pos0 + tid, n + tid)});
         }
-        auto look = [&](int i) {                             // (both loads in flight together)
-            const double m = i < n ? util[i] : __longlong_as_double(0x7ff0000000000000ll);
-            const int32_t at = i < n ? pos[i] : 0;
-            const uint64_t x = util_key(m);
-            if (x != kNone && x <= top) add_candidate(s, Key{x, tie_key(at, i)});
+        // the groups of slots (long units: of 32; else: a thread's own) that have a low one
+        int *low = reinterpret_cast<int *>(s.set);           // (the sets are done with)
+        constexpr int kLow = sizeof(s.set) / sizeof(int);
+        auto found = [&](int g) {
+            const int c = atomicAdd(&s.n_low, 1);
+            if (c < kLow) low[c] = g;
         };
         if (kSplit) {
-            // a warp looks through the groups that one of its threads found low
             constexpr int kAt = 8;                           // loads in flight
-            for (int g0 = 32 * warp; g0 < groups; g0 += kAt * kThreads) {
+            for (int g0 = tid; g0 < groups; g0 += kAt * kThreads) {
                 uint64_t x[kAt];
 #pragma unroll
                 for (int j = 0; j < kAt; j++) {
-                    const int g = g0 + j * kThreads + lane;
+                    const int g = g0 + j * kThreads;
                     x[j] = g < groups ? gmin[g] : kNone;
                 }
 #pragma unroll
                 for (int j = 0; j < kAt; j++)
-                    for (unsigned todo = __ballot_sync(kFull, x[j] != kNone && x[j] <= top); todo; todo &= todo - 1)
-                        look(32 * (g0 + j * kThreads + __ffs(todo) - 1) + lane);
+                    if (x[j] != kNone && x[j] <= top) found(g0 + j * kThreads);
             }
-        } else {
-            // a warp looks through the slots of each of its threads that found one low
-            // (every kThreads-th slot: at most 32 of them)
-            for (unsigned todo = __ballot_sync(kFull, mine != kNone && mine <= top); todo; todo &= todo - 1) {
-                look(32 * warp + __ffs(todo) - 1 + kThreads * lane);
+        } else if (mine != kNone && mine <= top) {
+            found(tid);
+        }
+        __syncthreads();
+        // their slots, a lane each and four groups at once (more groups than places: every
+        // slot is looked at below)
+        const int n_low = s.n_low;
+        if (n_low > kLow && tid == 0) s.n_cand = kCand + 1;
+        for (int e0 = warp; n_low <= kLow && e0 < n_low; e0 += 4 * kThreads / 32) {
+            double m[4];
+            int32_t at[4];
+            int slot[4];
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const int e = e0 + j * kThreads / 32, g = low[min(e, n_low - 1)];
+                slot[j] = kSplit ? group_slot(g, lane) : g + kThreads * lane;
+                const bool in = e < n_low && slot[j] < n;
+                m[j] = in ? util[slot[j]] : __longlong_as_double(0x7ff0000000000000ll);
+                at[j] = in ? pos[slot[j]] : 0;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const uint64_t x = util_key(m[j]);
+                if (x != kNone && x <= top) add_candidate(s, Key{x, tie_key(at[j], slot[j])});
             }
         }
         __syncthreads();
@@ -426,16 +453,27 @@ __global__ void __launch_bounds__(kThreads, 4) tree_commit_kernel(ComArgs a)
         __syncthreads();
         // the victims' rows, before any of them is overwritten
         if (a.C)
-#pragma unroll 4
-            for (int e = tid; e < k * 32; e += kThreads) {
-                const int j = e >> 5, ch = e & 15, which = e >> 4 & 1, i = s.vic[j];
-                const uint16_t *row = i < n ? (which ? a.V : a.K) + (cb + i) * kD
-                                            : (which ? a.vt : a.kt) + (tb + s.tok[i - n]) * kD;
-                float f[8];
-                unpack8(reinterpret_cast<const uint4 *>(row)[ch], f);
-                float4 *d = reinterpret_cast<float4 *>(s.kv + (which * a.kmax + j) * kD + ch * 8);
-                d[0] = make_float4(f[0], f[1], f[2], f[3]);
-                d[1] = make_float4(f[4], f[5], f[6], f[7]);
+            for (int e0 = tid; e0 < k * 32; e0 += 4 * kThreads) {
+                uint4 v[4];
+#pragma unroll
+                for (int x = 0; x < 4; x++) {
+                    const int e = e0 + x * kThreads, j = e >> 5, ch = e & 15, which = e >> 4 & 1;
+                    if (e >= k * 32) break;
+                    const int i = s.vic[j];
+                    const uint16_t *row = i < n ? (which ? a.V : a.K) + (cb + i) * kD
+                                                : (which ? a.vt : a.kt) + (tb + s.tok[i - n]) * kD;
+                    v[x] = reinterpret_cast<const uint4 *>(row)[ch];
+                }
+#pragma unroll
+                for (int x = 0; x < 4; x++) {
+                    const int e = e0 + x * kThreads, j = e >> 5, ch = e & 15, which = e >> 4 & 1;
+                    if (e >= k * 32) break;
+                    float f[8];
+                    unpack8(v[x], f);
+                    float4 *d = reinterpret_cast<float4 *>(s.kv + (which * a.kmax + j) * kD + ch * 8);
+                    d[0] = make_float4(f[0], f[1], f[2], f[3]);
+                    d[1] = make_float4(f[4], f[5], f[6], f[7]);
+                }
             }
     } else if (tid == 0) {
         s.n_hole = 0;
@@ -504,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 4) tree_commit_kernel(ComArgs a)
             old[i] = c[i * (kD / 4)];
             m[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-#pragma unroll 2
+#pragma unroll kSplit ? 4 : 2
         for (int j = 0; j < k; j++) {
             const float4 y = reinterpret_cast<const float4 *>(kv + j * kD)[lane];
             const float4 x4 = *reinterpret_cast<const float4 *>(vv + j * kD + row);
@@ -540,7 +578,7 @@ cudaError_t launch_tree_commit(const kvc_params &p, int max_len, const TreeArgs 
     ComArgs a{t, pa, kt, vt, S, c.K, c.V, c.votes, c.pos, c.len, c.util, p.budget,
               m ? m->n : nullptr, m ? m->mu_k : nullptr, m ? m->mu_v : nullptr, m ? m->C : nullptr,
               evict_idx, evict_pos, n_evict, ws.status, ws.pend,
-              reinterpret_cast<uint64_t *>(ws.probs), (double)p.alpha, 1.0 - (double)p.alpha, p.cap, p.L, p.rule, kmax,
+              reinterpret_cast<uint64_t *>(ws.probs), (p.cap + kChunk - 1) / kChunk * kGroups, (double)p.alpha, 1.0 - (double)p.alpha, p.cap, p.L, p.rule, kmax,
               max_len, FastDiv(t.units)};
     const bool split = max_len > kLong;
     const size_t smem = sizeof(ComSmem) + (m ? 2 * (size_t)kmax * kD * sizeof(float) : 0);
