@@ -79,12 +79,17 @@ __device__ __forceinline__ int unit_acc(const WtArgs &a, int u, int n, int32_t *
 {
     const int b = a.by_units(u);
     const int live = a.t.n ? a.t.n[b] : a.t.T, acc = a.p.n[b];
+    // (no token's load waits for another's: one by one they were 9 us of a call)
+    const int32_t *tok = a.p.token + (size_t)b * a.p.A;
+    bool bad = false;
+    for (int j0 = 0; j0 < a.p.A; j0 += 8)
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            const int c = j0 + e < a.p.A ? tok[j0 + e] : 0;
+            bad |= j0 + e < acc && (c < 0 || c >= live);
+        }
     *err = KVC_ERR_INVALID_ARG;
-    if (live < 0 || live > a.t.T || acc < 0 || acc > a.p.A) return -1;
-    for (int j = 0; j < acc; j++) {
-        const int c = a.p.token[(size_t)b * a.p.A + j];
-        if (c < 0 || c >= live) return -1;
-    }
+    if (live < 0 || live > a.t.T || acc < 0 || acc > a.p.A || bad) return -1;
     *err = KVC_ERR_SHAPE;
     if (n < 0 || n > a.max_len || n + acc > a.cap) return -1;
     return acc;
@@ -95,6 +100,14 @@ __device__ __forceinline__ int unit_tiles(const WtArgs &a, int u)
     int32_t err;
     const int n = a.len[u];
     return unit_acc(a, u, n, &err) < 0 ? 0 : (n + kTile - 1) >> 7;
+}
+
+// 16 bytes to shared memory, zeros when the source is not to be read.
+__device__ __forceinline__ void cp_async16(void *dst, const void *src, bool read)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+                 "r"(read ? 16 : 0)
+                 : "memory");
 }
 
 // c_row: a row that weighs nothing (or saw nothing) has +inf.
@@ -320,29 +333,20 @@ tree_weights_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CU
             const int rows = s.acc * a.G, cols = max(16, (rows + 15) & ~15);
             unsigned char *d = qbuf + qb * qbytes;
             const int32_t *tok = a.p.token + (size_t)s.b * a.p.A;
-            // two rows of 16 chunks a step, four steps in flight
-            for (int r0 = 0; r0 < cols; r0 += 8) {
-                uint4 v[4];
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const int r = r0 + 2 * e + (lane >> 4), j = r / a.G;
-                    v[e] = make_uint4(0, 0, 0, 0);
-                    if (r < rows)
-                        v[e] = reinterpret_cast<const uint4 *>(
-                            a.q + (((size_t)s.u * a.t.T + tok[j]) * a.G + (r - j * a.G)) * kD)[lane & 15];
-                }
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const int r = r0 + 2 * e + (lane >> 4), c = lane & 15;
-                    *reinterpret_cast<uint4 *>(d + (c >> 3) * (a.rows * 128) + r * 128 +
-                                               (((c & 7) ^ (r & 7)) << 4)) = v[e];
-                }
+            // two rows of 16 chunks a step, all of them in flight together; rows past the
+            // last are zero
+            for (int r0 = 0; r0 < cols; r0 += 2) {
+                const int r = r0 + (lane >> 4), c = lane & 15, j = r < rows ? r / a.G : 0;
+                const uint16_t *from =
+                    a.q + (((size_t)s.u * a.t.T + (rows ? tok[j] : 0)) * a.G + (r < rows ? r - j * a.G : 0)) * kD + 8 * c;
+                cp_async16(d + (c >> 3) * (a.rows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4), from, r < rows);
             }
             for (int r = lane; r < cols; r += 32) {
                 const int j = r / a.G;
                 S.c[qb][r] = r < rows ? row_c(a, ((size_t)s.u * a.t.T + tok[j]) * a.G + (r - j * a.G), s.b, j)
                                       : INFINITY;
             }
+            asm volatile("cp.async.wait_all;" ::: "memory");
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(&S.qfull[qb]);
