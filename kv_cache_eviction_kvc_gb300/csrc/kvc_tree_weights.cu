@@ -49,7 +49,7 @@ struct WtArgs {
     const int32_t *votes, *len;
     float *S;
     int32_t *status;
-    int U, G, cap, max_len;
+    int U, G, gshift, cap, max_len;
     int rows, qbufs, ring, dbufs, dcols;   // rows of q per buffer (a multiple of 16); tiles in flight
     FastDiv by_units;
     float scale;                           // log2(e) / sqrt(d)
@@ -111,11 +111,9 @@ __device__ __forceinline__ void cp_async16(void *dst, const void *src, bool read
 }
 
 // c_row: a row that weighs nothing (or saw nothing) has +inf.
-__device__ __forceinline__ float row_c(const WtArgs &a, size_t qrow, int b, int j)
+__device__ __forceinline__ float row_c(const WtArgs &a, float lse, float w)
 {
-    const float lse = a.lse[qrow];
-    const float w = (a.w ? a.w[(size_t)b * a.p.A + j] : 1.f) / (float)a.G;
-    return lse == -INFINITY ? INFINITY : lse * kLog2e - log2f(w);
+    return lse == -INFINITY ? INFINITY : lse * kLog2e - log2f(w / (float)a.G);
 }
 
 // exp2(x - c_row); nothing for a row of c = +inf, whatever its product is.
@@ -333,18 +331,33 @@ tree_weights_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CU
             const int rows = s.acc * a.G, cols = max(16, (rows + 15) & ~15);
             unsigned char *d = qbuf + qb * qbytes;
             const int32_t *tok = a.p.token + (size_t)s.b * a.p.A;
-            // two rows of 16 chunks a step, all of them in flight together; rows past the
-            // last are zero
-            for (int r0 = 0; r0 < cols; r0 += 2) {
-                const int r = r0 + (lane >> 4), c = lane & 15, j = r < rows ? r / a.G : 0;
-                const uint16_t *from =
-                    a.q + (((size_t)s.u * a.t.T + (rows ? tok[j] : 0)) * a.G + (r < rows ? r - j * a.G : 0)) * kD + 8 * c;
-                cp_async16(d + (c >> 3) * (a.rows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4), from, r < rows);
-            }
-            for (int r = lane; r < cols; r += 32) {
-                const int j = r / a.G;
-                S.c[qb][r] = r < rows ? row_c(a, ((size_t)s.u * a.t.T + tok[j]) * a.G + (r - j * a.G), s.b, j)
-                                      : INFINITY;
+            const int t0 = lane < s.acc ? tok[lane] : 0, t1 = lane + 32 < s.acc ? tok[lane + 32] : 0;
+            auto token = [&](int j) {                        // the j-th, for every lane its own j
+                const int x = __shfl_sync(kFull, t0, j & 31), y = __shfl_sync(kFull, t1, j & 31);
+                return j < 32 ? x : y;
+            };
+            // two rows of 16 chunks a step, all of them in flight together with what c_row
+            // needs; rows past the last are zero
+            for (int b0 = 0; b0 < cols; b0 += 128) {
+                float lse[4], w[4];
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const int r = b0 + 32 * e + lane, j = min(r, rows - 1) >> a.gshift, t = token(max(j, 0));
+                    lse[e] = -INFINITY;
+                    w[e] = 1.f;
+                    if (r < rows) {
+                        lse[e] = a.lse[((size_t)s.u * a.t.T + t) * a.G + (r & (a.G - 1))];
+                        if (a.w) w[e] = a.w[(size_t)s.b * a.p.A + j];
+                    }
+                }
+                for (int r0 = b0; r0 < min(cols, b0 + 128); r0 += 2) {
+                    const int r = r0 + (lane >> 4), c = lane & 15, t = token(min(r, max(rows - 1, 0)) >> a.gshift);
+                    const uint16_t *from = a.q + (((size_t)s.u * a.t.T + t) * a.G + (r & (a.G - 1))) * kD + 8 * c;
+                    cp_async16(d + (c >> 3) * (a.rows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4), from, r < rows);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    if (b0 + 32 * e + lane < cols) S.c[qb][b0 + 32 * e + lane] = row_c(a, lse[e], w[e]);
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -375,19 +388,20 @@ tree_weights_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CU
                 }
                 float sum[2] = {0.f, 0.f};
                 for (int r0 = 0; r0 < rows; r0 += 8) {       // eight rows of q
-                    const int r = min(r0 + g, rows - 1), j = r / a.G;
+                    const int r = min(r0 + g, rows - 1), j = r >> a.gshift;
                     const uint32_t *p = reinterpret_cast<const uint32_t *>(
-                        a.q + (((size_t)u * a.t.T + tok[j]) * a.G + (r - j * a.G)) * kD) + t;
+                        a.q + (((size_t)u * a.t.T + tok[j]) * a.G + (r & (a.G - 1))) * kD) + t;
                     float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int ks = 0; ks < 8; ks++)
                         mma16816(d, ka[ks][0], ka[ks][1], ka[ks][2], ka[ks][3], p[8 * ks], p[8 * ks + 4]);
 #pragma unroll
                     for (int e = 0; e < 2; e++) {            // the columns of the thread
-                        const int rr = r0 + 2 * t + e, jj = rr / a.G;
+                        const int rr = r0 + 2 * t + e, jj = rr >> a.gshift;
                         if (rr >= rows) continue;
                         const int ct = tok[jj];
-                        const float cr = row_c(a, ((size_t)u * a.t.T + ct) * a.G + (rr - jj * a.G), b, jj);
+                        const float cr = row_c(a, a.lse[((size_t)u * a.t.T + ct) * a.G + (rr & (a.G - 1))],
+                                               a.w ? a.w[(size_t)b * a.p.A + jj] : 1.f);
                         const uint64_t see = a.t.mask[(size_t)b * a.t.T + ct];
 #pragma unroll
                         for (int h = 0; h < 2; h++)
@@ -473,7 +487,7 @@ cudaError_t launch_tree_weights(const kvc_params &p, int max_len, const TreeArgs
     CUtensorMap mk;
     if (!make_unit_map(&mk, c.K, p.U, p.cap)) return cudaErrorInvalidValue;
     WtArgs a{t, pa, row_weight, q, kt, lse, c.votes, c.len, S, static_cast<int32_t *>(ws), p.U, p.G,
-             p.cap, max_len};
+             p.G == 1 ? 0 : p.G == 2 ? 1 : p.G == 4 ? 2 : 3, p.cap, max_len};
     a.rows = (pa.A * p.G + 15) & ~15;
     a.qbufs = a.rows <= 128 ? 2 : 1;
     a.dcols = a.rows <= 128 ? 128 : a.rows <= 256 ? 256 : 512;
