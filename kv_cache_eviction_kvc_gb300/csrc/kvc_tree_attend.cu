@@ -476,6 +476,7 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kMma) tmem_alloc(&S.tmem, 512);
+    follow();
     lead();
 
     // this CTA's items [item0, item1) and tiles [lo, hi) of the line
@@ -1468,6 +1469,7 @@ tree_moment_kernel(const __grid_constant__ JoinArgs j, const __grid_constant__ C
     }
     if (!ok && lane == 0) S.bad = 1;
     __syncthreads();
+    lead();
     if (warp == 17) tmem_dealloc(tmem, 256);
     if (tid == 0 && S.bad) record_status(a.status, KVC_ERR_TIMEOUT);
 }
@@ -1530,8 +1532,8 @@ cudaError_t launch_tree_attend(const kvc_params &p, int max_len, const TreeArgs 
     auto *kernel = c.votes ? tree_attend_kernel<true> : tree_attend_kernel<false>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDyn);
     if (e != cudaSuccess) return e;
-    kernel<<<(int)grid, kThreads, kDyn, st>>>(a, mk, mv, mq, mkt, mvt);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch_following(kernel, dim3((unsigned)grid), kThreads, kDyn, st, a, mk, mv, mq, mkt, mvt);
+    if (e != cudaSuccess) return e;
     if (m == nullptr && whole) return cudaSuccess;
     JoinArgs j{a, m ? m->n : nullptr, m ? m->mu_k : nullptr, m ? m->mu_v : nullptr, m ? m->C : nullptr,
                p.correction == KVC_CORR_FIRST_ORDER, (int)grid};
@@ -1551,7 +1553,7 @@ cudaError_t launch_tree_attend(const kvc_params &p, int max_len, const TreeArgs 
                              kMomDyn, st, j, mq, mf);
         if (e != cudaSuccess) return e;
     }
-    return cudaGetLastError();
+    return cudaSuccess;
 }
 
 }  // namespace kvc

@@ -167,6 +167,7 @@ __device__ __forceinline__ int group_slot(int g, int i)          // the i-th slo
 __global__ void __launch_bounds__(kThreads) tree_update_kernel(ComArgs a)
 {
     const int u = blockIdx.y, lane = threadIdx.x & 31;
+    follow();
     const Plan p = plan_unit(a, u, lane);
     if (p.err != KVC_OK) return;
     const size_t cb = (size_t)u * a.cap;
@@ -253,6 +254,7 @@ __global__ void __launch_bounds__(kThreads, kSplit ? 2 : 4) tree_commit_kernel(C
     extern __shared__ __align__(16) unsigned char raw[];
     ComSmem &s = *reinterpret_cast<ComSmem *>(raw);
     const int u = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (!kSplit) follow();
     const size_t cb = (size_t)u * a.cap;
     double *util = a.util + cb;
     const float *S = a.S ? a.S + cb : nullptr;
@@ -567,6 +569,7 @@ __global__ void __launch_bounds__(kThreads, kSplit ? 2 : 4) tree_commit_kernel(C
         }
     }
     if (tid == 0) a.mn[u] = n1;
+    lead();
 }
 
 }  // namespace
@@ -589,12 +592,10 @@ cudaError_t launch_tree_commit(const kvc_params &p, int max_len, const TreeArgs 
     if (e != cudaSuccess) return e;
     if (split) {
         if (p.U > 65535) return cudaErrorInvalidValue;
-        tree_update_kernel<<<dim3((max_len + kChunk - 1) / kChunk, p.U), kThreads, 0, st>>>(a);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        e = launch_following(tree_update_kernel, dim3((max_len + kChunk - 1) / kChunk, p.U), kThreads, 0, st, a);
+        if (e != cudaSuccess) return e;
     }
-    if (split) return launch_following(kernel, dim3(p.U), kThreads, smem, st, a);
-    kernel<<<p.U, kThreads, smem, st>>>(a);
-    return cudaGetLastError();
+    return launch_following(kernel, dim3(p.U), kThreads, smem, st, a);
 }
 
 }  // namespace kvc

@@ -159,6 +159,7 @@ tree_weights_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CU
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kMma) tmem_alloc(&S.tmem, 512);
+    follow();
 
     // the line of tiles: every CTA counts it and finds where its part starts
     int lo, hi;
@@ -471,6 +472,7 @@ tree_weights_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CU
         }
     }
     __syncthreads();
+    lead();
     if (warp == kMma) tmem_dealloc(tmem, 512);
     if (tid == 0 && S.bad) record_status(a.status, KVC_ERR_TIMEOUT);
 }
@@ -502,8 +504,7 @@ cudaError_t launch_tree_weights(const kvc_params &p, int max_len, const TreeArgs
     if (e != cudaSuccess) return e;
     long long grid = tiles > p.U ? tiles : p.U;
     if (grid > kGrid) grid = kGrid;
-    tree_weights_kernel<<<(int)grid, kThreads, smem, st>>>(a, mk);
-    return cudaGetLastError();
+    return launch_following(tree_weights_kernel, dim3((unsigned)grid), kThreads, smem, st, a, mk);
 }
 
 }  // namespace kvc

@@ -704,6 +704,38 @@ def test_graphs_that_share_a_workspace_and_another_stream():
                 assert torch.equal(x, y)               # the same bits, run after run
 
 
+def test_graph_with_copies_and_branches():
+    """Captured behind copies and fills, and on two branches that meet again."""
+    cases = [_graph_case(51), _graph_case(52)]
+    for c in cases:
+        c.call()
+    want = [[x.clone() for x in (c.o, c.lse, c.S)] for c in cases]
+    src = [c.t["q"].clone() for c in cases]
+    side = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            cases[1].t["q"].copy_(src[1])
+            cases[1].o.zero_()
+            cases[1].call()
+        cases[0].o.zero_()
+        cases[0].t["q"].copy_(src[0])
+        cases[0].call()
+        main.wait_stream(side)
+        cases[0].call()                                # behind both branches
+    for _ in range(3):
+        for c in cases:
+            c.t["q"].zero_()
+            c.S.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for c, w in zip(cases, want):
+            for x, y in zip((c.o, c.lse, c.S), w):
+                assert torch.equal(x, y)
+
+
 def test_calls_at_once_on_two_streams():
     """Two verifications in flight together, a workspace each: the bits that
     each gives alone."""
