@@ -80,7 +80,7 @@ struct AttArgs {
     int *first;             // [items + 1] tiles before each item
     int4 *cut;              // [CTAs] the item a part begins inside of: item, first and last part, rows
     int32_t *status;
-    int U, RB, TG, gshift, cap, max_len, rows, whole, join_all;
+    int U, RB, TG, gshift, cap, max_len, rows, whole, split, join_all;
     FastDiv by_rb, by_units;
     float scale;            // log2(e) / sqrt(d)
 
@@ -481,7 +481,24 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
 
     // this CTA's items [item0, item1) and tiles [lo, hi) of the line
     int item0, item1, base0, lo, hi;
-    if (a.whole) {
+    if (a.split) {
+        // each item in as many parts, a CTA each (fewer when it has fewer tiles)
+        const int item = blockIdx.x / a.split, sub = blockIdx.x - item * a.split;
+        const int u = a.by_rb(item), rb = item - u * a.RB, live = a.live(u);
+        const int nt = item_tiles(a, a.len[u], live, rb), parts = min(a.split, nt);
+        item0 = item;
+        item1 = item + 1;
+        base0 = 0;
+        lo = sub < parts ? nt * sub / parts : 0;
+        hi = sub < parts ? nt * (sub + 1) / parts : 0;
+        if (tid == 0) {
+            if (sub == 1 && parts > 1)
+                S.cut = make_int4(item, blockIdx.x - 1, blockIdx.x + parts - 2,
+                                  min(kRows, (live << a.gshift) - rb * kRows));
+            a.cut[blockIdx.x] = S.cut;
+            if (sub == 0 && rb == 0) check_unit(a, u);
+        }
+    } else if (a.whole) {
         // parts of whole items: nothing to count, nothing to join
         const LineCuts c(gridDim.x, items);
         item0 = c.start(blockIdx.x);
@@ -1154,8 +1171,8 @@ __device__ __forceinline__ MomJob mom_job(const JoinArgs &j, bool sums, int per,
     m.sid = 0;
     if (sums && m.rows > 0) {
         const int items = a.U * a.RB;
-        const LineCuts cuts(j.grid, a.whole ? items : a.first[items]);
-        m.sid = item + cuts.part(a.whole ? item : a.first[item]);
+        const LineCuts cuts(j.grid, a.whole ? items : a.split ? 0 : a.first[items]);
+        m.sid = item + (a.split ? item * a.split : cuts.part(a.whole ? item : a.first[item]));
     }
     return m;
 }
@@ -1506,6 +1523,33 @@ TreeWs tree_ws(const kvc_params &p, int T, void *base)
 
 }  // namespace
 
+// How the items go to the CTAs: whole, each cut into `split` parts of its own,
+// or (neither) the line of all tiles cut into kGrid parts.
+struct Cut {
+    bool whole;
+    int split;
+};
+
+// In units of one tile's bytes at the whole device's bandwidth (9.4 ns): a CTA
+// takes 80 of them for a tile (170 with two halves of rows) however little else
+// runs, and 152 when all of them load.  A join is 320 and the sums' way to
+// memory and back.  Measured, whole against cut: 8 units of 512 slots 10.5 and
+// 11.1 us, of 1024 slots 13.8 and 12.1, 128 of up to 3277 slots 37 and 43, 160
+// of 1920 slots 44 and 33, 80 of 1408 slots and 240 rows 28 and 39.
+Cut choose_cut(long long items, long long tiles, int rows)
+{
+    const long long lat = rows > 128 ? 170 : 80, full = items / kGrid, rem = items % kGrid;
+    auto larger = [](long long x, long long y) { return x > y ? x : y; };
+    const long long whole = tiles * (full * larger(kGrid, lat) + (rem ? larger(lat, rem) : 0));
+    // at least two tiles a part
+    long long split = kGrid / items < (tiles + 1) / 2 ? kGrid / items : (tiles + 1) / 2;
+    if (split < 2) split = 0;
+    const long long parts = split ? items * split : items + kGrid;
+    const long long each = split ? (tiles + split - 1) / split : (items * tiles + kGrid - 1) / kGrid;
+    const long long cut = larger(items * tiles * 15 / 16, lat * each) + 320 + parts * rows / 64;
+    return whole <= cut ? Cut{true, 0} : Cut{false, (int)split};
+}
+
 size_t tree_ws_bytes(const kvc_params &p, int T) { return tree_ws(p, T, nullptr).bytes; }
 
 cudaError_t launch_tree_attend(const kvc_params &p, int max_len, const TreeArgs &t,
@@ -1522,22 +1566,21 @@ cudaError_t launch_tree_attend(const kvc_params &p, int max_len, const TreeArgs 
         !make_unit_map(&mq, q, p.U, TG) || !make_unit_map(&mkt, kt, p.U, t.T) ||
         !make_unit_map(&mvt, vt, p.U, t.T))
         return cudaErrorInvalidValue;
-    const bool whole = tmax <= 4 || items >= 6 * kGrid;
-    long long grid = whole ? items : (items * tmax + 3) / 4;
-    if (grid < items) grid = items;
-    if (grid > kGrid) grid = kGrid;
+    const int rows = TG < kRows ? TG : kRows;
+    const Cut cut = choose_cut(items, tmax, rows);
+    const long long grid = cut.split ? items * cut.split : cut.whole && items < kGrid ? items : kGrid;
     AttArgs a{t, c.votes, c.len, vt, o, lse, w.part, w.ml, w.first, w.cut, w.status, p.U, RB, TG,
-              p.G == 1 ? 0 : p.G == 2 ? 1 : p.G == 4 ? 2 : 3, p.cap, max_len, TG < kRows ? TG : kRows,
-              whole, m != nullptr, FastDiv(RB), FastDiv(t.units), kLog2e / sqrtf((float)kD)};
+              p.G == 1 ? 0 : p.G == 2 ? 1 : p.G == 4 ? 2 : 3, p.cap, max_len, rows,
+              cut.whole, cut.split, m != nullptr, FastDiv(RB), FastDiv(t.units), kLog2e / sqrtf((float)kD)};
     auto *kernel = c.votes ? tree_attend_kernel<true> : tree_attend_kernel<false>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDyn);
     if (e != cudaSuccess) return e;
     e = launch_following(kernel, dim3((unsigned)grid), kThreads, kDyn, st, a, mk, mv, mq, mkt, mvt);
     if (e != cudaSuccess) return e;
-    if (m == nullptr && whole) return cudaSuccess;
+    if (m == nullptr && cut.whole) return cudaSuccess;
     JoinArgs j{a, m ? m->n : nullptr, m ? m->mu_k : nullptr, m ? m->mu_v : nullptr, m ? m->C : nullptr,
                p.correction == KVC_CORR_FIRST_ORDER, (int)grid};
-    if (!whole) {
+    if (!cut.whole) {
         const dim3 g((unsigned)grid, (a.rows + 8 * kJoinRows - 1) / (8 * kJoinRows));
         e = launch_following(m ? tree_join_kernel<true> : tree_join_kernel<false>, g, 256, 0, st, j);
         if (e != cudaSuccess) return e;

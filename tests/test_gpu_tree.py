@@ -173,6 +173,13 @@ ATTEND = [
     (1, 4, 6, [0, 0, 5], dict(kind="none", moments=True)),
     (1, 8, 17, [900, 1000, 3], dict(q_scale=30.0)),          # sharp attention
     (4, 1, 24, [100, 200, 300, 400] * 45, dict()),           # more units than SMs
+    # parts of the line of all tiles, which begin and end inside of units
+    (4, 2, 12, [(37 * i * i) % 2100 for i in range(160)], dict(votes=True, moments=True)),
+    (4, 1, 5, [(53 * i * i) % 2100 for i in range(160)], dict(kind="any", live=[i % 6 for i in range(40)])),
+    (2, 8, 40, [(41 * i * i) % 2900 for i in range(80)], dict(kind="any")),
+    # parts of single units, some of fewer tiles than parts
+    (1, 2, 12, [4000, 130, 5, 0, 2050], dict(votes=True, moments=True)),
+    (1, 8, 40, [2900, 1, 260], dict(moments=True)),
 ]
 
 
