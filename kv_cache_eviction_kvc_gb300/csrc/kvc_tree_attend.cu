@@ -1533,9 +1533,11 @@ struct Cut {
 // In units of one tile's bytes at the whole device's bandwidth (9.4 ns): a CTA
 // takes 80 of them for a tile (170 with two halves of rows) however little else
 // runs, and 152 when all of them load.  A join is 320 and the sums' way to
-// memory and back.  Measured, whole against cut: 8 units of 512 slots 10.5 and
-// 11.1 us, of 1024 slots 13.8 and 12.1, 128 of up to 3277 slots 37 and 43, 160
-// of 1920 slots 44 and 33, 80 of 1408 slots and 240 rows 28 and 39.
+// memory and back.  Measured (us), whole / parts of their own / line: 8 units
+// of 512 slots 10.5 / 10.9 / -, of 1024 slots 13.9 / 11.2 / -, of 4096 slots
+// - / 14.6 / 20.2; 40 of 2432 slots 23.3 / 17.5 / 20.6; 80 of 1408 slots 17.8 /
+// - / 22.1, with 240 rows 28.9 / - / 38.9; 128 of up to 3277 slots 37 / - / 43;
+// 160 of 1152 slots 30.3 / - / 26.2; 1024 of 1024 slots 144 / - / 161.
 Cut choose_cut(long long items, long long tiles, int rows)
 {
     const long long lat = rows > 128 ? 170 : 80, full = items / kGrid, rem = items % kGrid;

@@ -17,9 +17,8 @@
 //      against one another;
 //   4. rows move, C is read and written in whole lines (prefetched to L2 at
 //      the start).
-// Units of more than kLong slots are updated by a kernel of their own over
-// the whole grid, which leaves the lowest utility of every 32 slots; step 1 is
-// then a pass over those.
+// Long units are updated by a kernel of their own over the whole grid, which
+// leaves the lowest utility of every 32 slots; step 1 is then a pass over those.
 //
 // Many equal utilities (weights that underflow to 0) can make every slot a
 // candidate: then the bound is taken again over whole (utility, position,
@@ -35,7 +34,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kCand = 1024;              // candidates held
-constexpr int kLong = 32 * kThreads;     // slots of a unit that one CTA updates
+constexpr int kLong = 32 * kThreads;     // slots of a unit that one CTA can update
+constexpr int kSms = 152;
 constexpr int kChunk = 2048;             // slots per CTA of the update kernel
 
 struct Key {
@@ -585,7 +585,10 @@ cudaError_t launch_tree_commit(const kvc_params &p, int max_len, const TreeArgs 
               evict_idx, evict_pos, n_evict, ws.status, ws.pend,
               reinterpret_cast<uint64_t *>(ws.probs), (p.cap + kChunk - 1) / kChunk * kGroups, (double)p.alpha, 1.0 - (double)p.alpha, p.cap, p.L, p.rule, kmax,
               max_len, FastDiv(t.units)};
-    const bool split = max_len > kLong;
+    // Half a device of units or fewer leaves SMs to the update kernel: 8 units of 8192
+    // slots take 16.6 us in one kernel and 12.9 in two, 64 units 17.3 and 14.7, but 128
+    // units 17.9 and 18.9; of 4096 slots 8 units take the same.
+    const bool split = max_len > kLong || (max_len > kLong / 2 && p.U <= kSms / 2);
     const size_t smem = sizeof(ComSmem) + (m ? 2 * (size_t)kmax * kD * sizeof(float) : 0);
     auto *kernel = split ? tree_commit_kernel<true> : tree_commit_kernel<false>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);

@@ -413,6 +413,8 @@ COMMIT = [
      dict(budget=[100, 200, 300, 400] * 45, L=400), True),
     (1, 30, [9000, 8193, 40], [20, 3, 30], 30,                         # long units, more than 16 victims
      dict(budget=[9000, 8180, 50], L=9000, votes=True, moments=True, unscored=True), True),
+    (20, 4, [5000 + 37 * i for i in range(80)], [3, 0, 4, 2], 4,       # many units, no kernel of their own
+     dict(budget=[5000 + 37 * i for i in range(80)], L=7925, rule="cumulative"), True),
 ]
 
 
