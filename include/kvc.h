@@ -507,7 +507,8 @@ KVC_API kvc_status kvc_decode_attend_noalloc(const kvc_params *p, int32_t t,
  * is this library's own extension of their definitions, cited per call.
  * A tree belongs to a sequence: `units` consecutive units (NL * Hkv of one
  * call, Hkv when the layers are called one by one) share its mask and path.
- * The calls may alternate with kvc_decode_step on the same cache.
+ * The calls may alternate with kvc_decode_step on the same cache.  Outputs do
+ * not overlap inputs.
  */
 typedef struct {
     int32_t T;              /* drafted tokens per tree, 1..64: the row stride of
@@ -527,7 +528,9 @@ typedef struct {
 typedef struct {
     int32_t A;              /* row stride of token and row_weight, 1..T      */
     const int32_t *token;   /* DEVICE [U/units][A] the accepted tokens, in the
-                               order they are appended (root first)          */
+                               order they are appended (root first); any
+                               live tokens (one that is named twice counts
+                               and is appended twice)                        */
     const int32_t *n;       /* DEVICE [U/units] accepted tokens, 0..A        */
     const int32_t *pos;     /* DEVICE [U/units] position of the first of them;
                                the j-th has pos + j                          */

@@ -9,13 +9,22 @@
 // clocks per tile against about 2800 for its bytes at one SM's share of the
 // bandwidth), so everything else is laid out to keep the loads going.
 //
-// Work split: the tiles of all (unit, block of 256 rows) items form one line
-// that is cut into equal parts, one per CTA (a persistent CTA per SM).  An
-// item inside one part is finished there; an item that a cut crosses leaves
-// partial sums (maximum, sum, output) per part, which tree_join_kernel adds.
-// With moments every item leaves its sums, and tree_moment_kernel mixes them
-// with the evicted set's estimate.  The drafted tokens are the item's last
-// tile.
+// Work split: an item is a unit's block of 256 rows.  Items go to the CTAs (one
+// per SM) whole, or each in parts of its own, or the tiles of all items form one
+// line that is cut into equal parts (choose_cut has the rule).  An item inside
+// one part is finished there; one that a cut crosses leaves partial sums
+// (maximum, sum, output) per part, which tree_join_kernel adds.  With moments
+// every item leaves its sums, and tree_moment_kernel mixes them with the evicted
+// set's estimate.  The drafted tokens are the item's last tile.
+//
+// Measured (bf16, d = 128, G = 4; a call among others): 128 units of 2623 slots
+// on average, 24 tokens: 37 us, 4.8 TB/s; 1024 units of 1024 slots, 16 tokens,
+// votes and moments: 144 us, 4.5 TB/s; 8 units of 131071 slots, 63 tokens (252
+// rows): 118 us, 4.6 TB/s and 1.15 PFLOP/s, 31 tokens: 91 us, 5.9 TB/s.  With
+// two halves of rows a tile takes 3600 clocks for its 2048 of the tensor core:
+// S overwrites P, so a group's product, softmax and next product follow one
+// another.  1024-slot units spend 6000 of 25000 clocks on their ends (sums of the
+// two groups, outputs, the next unit's first S).
 //
 // 384 threads:
 //   warps 0-3, 4-7  two softmax groups, each with its own S, P and O in tensor
@@ -349,7 +358,7 @@ __device__ __forceinline__ void top32(uint32_t (&y)[32], uint32_t keep, float (&
 // (exp(x + ln p) = p exp(x)).  All 128 columns are read for the maximum (a
 // read takes about 140 clocks and 10 more per 16 columns); the upper 64 stay
 // in registers for the weights and the lower 64 are read again meanwhile, which
-// is what fits without spills.  So P takes 32 columns at the start of each
+// is what fits with few spills.  So P takes 32 columns at the start of each
 // half of S.
 template <bool kMask, bool kVotes>
 __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float scale,
@@ -1044,6 +1053,7 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
     if (tid == 0 && S.bad) record_status(a.status, KVC_ERR_TIMEOUT);
 }
 
+// The kernels behind the attention.
 struct JoinArgs {
     AttArgs a;
     const float *mn, *mu_k, *mu_v, *C;
@@ -1054,7 +1064,8 @@ struct JoinArgs {
 // their columns; the loads of four parts are in flight together.  The result
 // is the output, or (kKeep, when the moments follow) the first part's place
 // takes it.  grid (CTAs of the attention, rows / 16): block x takes the item
-// whose first cut is the start of part x.
+// whose first cut is the start of part x.  Bound by latency: about 5 us behind
+// the attention for 8 units of 131071 slots (152 parts of 252 rows, 20 MB).
 constexpr int kJoinRows = 2;
 
 template <bool kKeep>
@@ -1128,6 +1139,9 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
 // tcgen05 with C as two bf16 terms (2^-16 of a product), which warps of their
 // own take apart in registers.  The roles are apart so that C of the jobs to
 // come keeps loading; each knows 32 jobs ahead of their use (a lane each).
+// 1024 units of 64 rows: 33 us behind the attention (134 MB, 4 TB/s; 24 us of
+// it with the inputs that load before the attention ends).  One group of warps
+// for everything took 36 us and began at the attention's end.
 //   warps 0, 1, 4, 5    outputs: a thread per row (the tensor-memory lanes of
 //                       64 rows), half of the columns each
 //   warps 2, 3, 6, 7    q . mu_k of the rows, mu_v
