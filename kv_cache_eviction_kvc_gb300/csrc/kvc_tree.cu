@@ -24,6 +24,7 @@ static bool misaligned(const void *p, unsigned a) { return ((uintptr_t)p & (a - 
 static kvc_status tr_cuda(cudaError_t e, const char *what)
 {
     if (e == cudaSuccess) return KVC_OK;
+    (void)cudaGetLastError();                    // it is reported here, not by the next call
     set_error("%s: %s", what, cudaGetErrorString(e));
     return KVC_ERR_CUDA;
 }

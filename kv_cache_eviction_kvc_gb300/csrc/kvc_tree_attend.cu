@@ -118,7 +118,8 @@ struct AttSmem {
     int4 mend[4];           // a value tile to mend: ring entry (-1: no more), phase, valid slots, drafted tokens'
     uint64_t full[kRing], empty[kRing];
     uint64_t segfull[kSegs], segempty[kSegs];
-    uint64_t qfull[2], qempty[2], sfull[2], pready[2], pvdone[2];
+    uint64_t qfull[2], qempty[2];
+    uint64_t sfull[2], pready[2][2], pvdone[2][2];   // by group; by group and half of the tile
     uint64_t gsync[2], xsync, drain;
     uint64_t armed[4], mended[4];
     uint64_t odd[4];        // drafted tokens with a value that is not finite
@@ -284,7 +285,8 @@ __device__ __forceinline__ void hide32(uint32_t (&y)[32], uint32_t keep)
 
 // A new maximum of the row: m, l and (rescale) the row of O follow it once it
 // is above m by kSlack.
-__device__ __forceinline__ void move_max(float top, uint32_t tO, bool rescale, float &m, float &l)
+template <typename F>
+__device__ __forceinline__ void move_max(float top, uint32_t tO, bool rescale, float &m, float &l, F before_o)
 {
     const bool move = top > m + kSlack || (m == -INFINITY && top > m);
     if (__any_sync(kFull, move)) {
@@ -295,6 +297,7 @@ __device__ __forceinline__ void move_max(float top, uint32_t tO, bool rescale, f
             l *= f;
         }
         if (rescale) {
+            before_o();
 #pragma unroll 1
             for (int h = 0; h < 8; h++) {
                 uint32_t z[16];
@@ -353,69 +356,13 @@ __device__ __forceinline__ void top32(uint32_t (&y)[32], uint32_t keep, float (&
     }
 }
 
-// One tile of the thread's row: the row's maximum so far, the weights, which
-// replace S as bf16 pairs, and their sum.  A slot's vote multiplies its weight
-// (exp(x + ln p) = p exp(x)).  All 128 columns are read for the maximum (a
-// read takes about 140 clocks and 10 more per 16 columns); the upper 64 stay
-// in registers for the weights and the lower 64 are read again meanwhile, which
-// is what fits with few spills.  So P takes 32 columns at the start of each
-// half of S.
-template <bool kMask, bool kVotes>
-__device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float scale,
-                                             const float *vote, uint64_t keep0, uint64_t keep1,
-                                             bool rescale, float &m, float &l)
-{
-    float top;
-    uint32_t c[32], d[32];
-    {
-        uint32_t a[32], b[32];
-        float mx[2] = {-INFINITY, -INFINITY};
-        auto top_of = [&](uint32_t (&y)[32], uint32_t keep) { top32<kMask>(y, keep, mx); };
-        tmem_ld32_async(tS, a);
-        tmem_ld32_async(tS + 32, b);
-        tmem_wait_ld();
-        tmem_bind(a);
-        tmem_bind(b);
-        tmem_ld32_async(tS + 64, c);
-        top_of(a, (uint32_t)keep0);
-        tmem_ld32_async(tS + 96, d);
-        top_of(b, (uint32_t)(keep0 >> 32));
-        tmem_wait_ld();
-        tmem_bind(c);
-        tmem_bind(d);
-        top_of(c, (uint32_t)keep1);
-        top_of(d, (uint32_t)(keep1 >> 32));
-        top = fmaxf(mx[0], mx[1]) * scale;
-    }
-    move_max(top, tO, rescale, m, l);
-    const float nref = m == -INFINITY ? 0.f : -m;
-    const float2 c2 = make_float2(scale, scale), r2 = make_float2(nref, nref);
-    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-    auto weights = [&](uint32_t (&y)[32], uint32_t at, const float *v) {
-        weights32<kVotes>(y, at, v, c2, r2, sum);
-    };
-    uint32_t a[32], b[32];
-    weights(c, tS + 64, vote + 64);
-    tmem_ld32_async(tS, a);
-    weights(d, tS + 80, vote + 96);
-    tmem_wait_ld();
-    tmem_bind(a);
-    tmem_ld32_async(tS + 32, b);
-    hide32<kMask>(a, (uint32_t)keep0);
-    weights(a, tS, vote);
-    tmem_wait_ld();
-    tmem_bind(b);
-    hide32<kMask>(b, (uint32_t)(keep0 >> 32));
-    weights(b, tS + 16, vote + 32);
-    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-    tmem_wait_st();
-}
-
-// The same for a tile of at most 64 slots: all of it stays in registers, the
-// upper half of P is not read.
-template <bool kVotes>
+// 64 slots of the thread's row: the row's maximum so far, the weights, which
+// replace S as bf16 pairs in the first 32 of the columns, and their sum.  A slot's
+// vote multiplies its weight (exp(x + ln p) = p exp(x)).  All 64 products stay in
+// registers meanwhile.  before_o() is called before O is rescaled.
+template <bool kMask, bool kVotes, typename F>
 __device__ __forceinline__ void softmax_half(uint32_t tS, uint32_t tO, float scale, const float *vote,
-                                             uint64_t keep, bool rescale, float &m, float &l)
+                                             uint64_t keep, bool rescale, float &m, float &l, F before_o)
 {
     uint32_t a[32], b[32];
     float mx[2] = {-INFINITY, -INFINITY};
@@ -424,16 +371,15 @@ __device__ __forceinline__ void softmax_half(uint32_t tS, uint32_t tO, float sca
     tmem_wait_ld();
     tmem_bind(a);
     tmem_bind(b);
-    top32<true>(a, (uint32_t)keep, mx);
-    top32<true>(b, (uint32_t)(keep >> 32), mx);
-    move_max(fmaxf(mx[0], mx[1]) * scale, tO, rescale, m, l);
+    top32<kMask>(a, (uint32_t)keep, mx);
+    top32<kMask>(b, (uint32_t)(keep >> 32), mx);
+    move_max(fmaxf(mx[0], mx[1]) * scale, tO, rescale, m, l, before_o);
     const float nref = m == -INFINITY ? 0.f : -m;
     const float2 c2 = make_float2(scale, scale), r2 = make_float2(nref, nref);
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     weights32<kVotes>(a, tS, vote, c2, r2, sum);
     weights32<kVotes>(b, tS + 16, vote + 32, c2, r2, sum);
     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-    tmem_wait_st();
 }
 
 template <bool kVotes>
@@ -471,8 +417,10 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
             mbar_init(&S.qfull[i], 1);
             mbar_init(&S.qempty[i], 1);
             mbar_init(&S.sfull[i], 1);
-            mbar_init(&S.pready[i], 4);
-            mbar_init(&S.pvdone[i], 1);
+            for (int h = 0; h < 2; h++) {
+                mbar_init(&S.pready[i][h], 4);
+                mbar_init(&S.pvdone[i][h], 1);
+            }
             mbar_init(&S.gsync[i], 4);
         }
         for (int i = 0; i < 4; i++) {
@@ -700,57 +648,61 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
         // ------------------------------------------------------ MMA issuer
         if (elect_one()) {
             bool ok = true;
-            // next ring entry and its phase; the entries in use by S and by O
-            int slot = 0, ks_slot = 0, vs_slot = 0, mends = 0;
-            uint32_t ph = 0, q_ph = 0, p_ph = 0;             // phases; the groups' as bits
+            // next ring entry and its phase; the entries in use by S and by O (a byte of each
+            // group)
+            int slot = 0, mends = 0;
+            uint32_t k_at = 0, v_at = 0;
+            uint32_t ph = 0, q_ph = 0, p_ph = 0;             // phases; by half of q, by group and half as bits
             const uint64_t q0 = umma_sdesc(smem_u32(qbuf)), k0 = umma_sdesc(smem_u32(ring));
             const uint64_t v0 = v_desc(smem_u32(ring));
             constexpr uint32_t kStep = kSlot >> 4;           // a slot in descriptor units
-            auto take = [&](int &of) {                       // the next entry, once it is there
+            auto take = [&](uint32_t &at, uint32_t g) {      // the next entry, once it is there
                 ok = ok && tree_wait(&S.full[slot], ph, &S.bad);
-                of = slot;
+                at = (at & ~(0xffu << 8 * g)) | (uint32_t)slot << 8 * g;
                 if (++slot == kRing) { slot = 0; ph ^= 1; }
             };
-            // S of group w; the key tile is waited for by its first reader
-            // and given back by its last
-            auto issue_s = [&](uint32_t w, uint32_t half, bool small, bool first, bool last,
-                               bool last_q) {
-                if (first) take(ks_slot);
+            // S of group w; the key tile is waited for by its first reader and given back by
+            // its last; g: whose entry it is (two halves of rows share theirs)
+            auto issue_s = [&](uint32_t w, uint32_t half, uint32_t g, int nv, bool first, bool last) {
+                if (first) take(k_at, g);
                 if (!ok) return;
+                const uint32_t entry = k_at >> 8 * g & 0xff, idesc = nv <= 64 ? kIdescS64 : kIdescS;
                 tc_fence_after();
-                const uint32_t idesc = small ? kIdescS64 : kIdescS, d = tmem + kColS + 128 * w;
-                const uint64_t qd = q0 + half * kStep, kd = k0 + (uint32_t)ks_slot * kStep;
+                const uint32_t d = tmem + kColS + 128 * w;
+                const uint64_t qd = q0 + half * kStep, kd = k0 + entry * kStep;
 #pragma unroll
                 for (int ks = 0; ks < 8; ks++)
                     umma_bf16(d, umma_sdesc_step(qd, ks), umma_sdesc_step(kd, ks), idesc, ks > 0);
                 umma_commit(&S.sfull[w]);
-                if (last) umma_commit(&S.empty[ks_slot]);
-                if (last_q) umma_commit(&S.qempty[half]);
+                if (last) umma_commit(&S.empty[entry]);
             };
-            auto issue_o = [&](uint32_t w, int nv, bool mend, bool first, bool last, bool keep) {
-                if (first) take(vs_slot);
+            // O of group w from the 16-slot steps [ks, ks1)
+            auto issue_o = [&](uint32_t w, uint32_t h, uint32_t g, int ks, int ks1, bool mend, bool first,
+                               bool last, bool keep) {
+                if (first) take(v_at, g);
                 if (first && mend) {
                     ok = ok && tree_wait(&S.mended[mends & 3], mends >> 2 & 1, &S.bad);
                     mends++;
                 }
-                ok = ok && tree_wait(&S.pready[w], p_ph >> w & 1, &S.bad);
-                p_ph ^= 1u << w;
+                ok = ok && tree_wait(&S.pready[w][h], p_ph >> (2 * w + h) & 1, &S.bad);
+                p_ph ^= 1u << (2 * w + h);
                 if (!ok) return;
                 tc_fence_after();
-                const uint64_t vd = v0 + (uint32_t)vs_slot * kStep;
+                const uint32_t entry = v_at >> 8 * g & 0xff;
+                const uint64_t vd = v0 + entry * kStep;
                 const uint32_t d = tmem + 128 * w, p = tmem + kColS + 128 * w;
-                if (nv > kTile - 16) {
+                auto step = [&](int ks) {
+                    umma_ts(d, p + 8 * ks + 32 * (ks >> 2), vd + (uint64_t)(ks * (2048 >> 4)), kIdescO, keep);
+                    keep = true;
+                };
+                if (ks1 - ks == 4) {
 #pragma unroll
-                    for (int ks = 0; ks < 8; ks++)
-                        umma_ts(d, p + 8 * ks + 32 * (ks >> 2), vd + (uint64_t)(ks * (2048 >> 4)),
-                                kIdescO, ks > 0 || keep);
+                    for (int x = 0; x < 4; x++) step(ks + x);
                 } else {
-                    for (int ks = 0; 16 * ks < nv; ks++)
-                        umma_ts(d, p + 8 * ks + 32 * (ks >> 2), vd + (uint64_t)(ks * (2048 >> 4)),
-                                kIdescO, ks > 0 || keep);
+                    for (; ks < ks1; ks++) step(ks);
                 }
-                umma_commit(&S.pvdone[w]);
-                if (last) umma_commit(&S.empty[vs_slot]);
+                umma_commit(&S.pvdone[w][h]);
+                if (last) umma_commit(&S.empty[entry]);
             };
             auto wait_q = [&](uint32_t half) {
                 ok = ok && tree_wait(&S.qfull[half], q_ph >> half & 1, &S.bad);
@@ -763,25 +715,31 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                 mbar_arrive(&S.segempty[i % kSegs]);
                 if (s.rows == 0) break;
                 const int nq = s.t1 - s.t0;
-                const uint32_t dual = s.rows > 128, jobs = nq << dual;
-                // job j: tile j of the group j & 1, or with two halves of rows
-                // tile j / 2 of the half j & 1
+                const uint32_t dual = s.rows > 128;
+                // job j: tile j of the group j & 1, or with two halves of rows tile j / 2 of the
+                // half j & 1.  S comes whole, O in halves: the first runs under the softmax of
+                // the second.
+                const int jobs = nq << dual;
                 if (dual) {
                     wait_q(0);
                     wait_q(1);
                 } else {
                     wait_q(i & 1);
                 }
-                for (uint32_t j = 0; ok && j < jobs + 2; j++) {
-                    const uint32_t w = j & 1, first = !dual || !w, last = !dual || w;
+                for (int j = 0; ok && j < jobs + 2; j++) {
+                    const uint32_t w = j & 1, g = dual ? 0 : w, first = !dual || !w, last = !dual || w;
+                    const int before = (j - 2) >> dual, now = j >> dual;
                     if (j >= 2) {
-                        const int t = s.t0 + (int)((j - 2) >> dual);
-                        issue_o(w, tile_valid(s, t), needs_mend(s, t), first, last, j - 2 >= 2);
+                        const int nv = tile_valid(s, s.t0 + before);
+                        for (int h = 0; h < 2; h++)
+                            if (nv > 64 * h)
+                                issue_o(w, h, g, 4 * h, min(4 * h + 4, (nv + 15) >> 4), needs_mend(s, s.t0 + before),
+                                        first && !h, last && nv <= 64 * h + 64, j - 2 >= 2 || h);
                     }
-                    if (j < jobs) {
-                        const int t = (int)(j >> dual);
-                        issue_s(w, dual ? w : i & 1, tile_valid(s, s.t0 + t) <= 64, first, last,
-                                dual ? t == nq - 1 : j == jobs - 1);
+                    if (j < jobs) issue_s(w, dual ? w : i & 1, g, tile_valid(s, s.t0 + now), first, last);
+                    if (j == jobs - 1) {
+                        if (dual || !(i & 1)) umma_commit(&S.qempty[0]);
+                        if (dual || (i & 1)) umma_commit(&S.qempty[1]);
                     }
                 }
             }
@@ -838,7 +796,9 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
         const int w = warp >> 2, r = tid & 127;              // group, row of its 128
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lanes + kColS + 128 * w, tO = tmem + lanes + 128 * w;
-        uint32_t job = 0, gph = 0, xph = 0;                  // jobs so far; barrier phases
+        uint32_t tiles = 0, gph = 0, xph = 0;                // tiles so far; barrier phases
+        // by half as bits: the phase of its last O, and whether there is one
+        uint32_t o_ph = 0, o_any = 0;
         bool ok = true;
         auto wait = [&](uint64_t *b, uint32_t ph) {
             const bool x = tree_wait(b, ph, &S.bad);
@@ -894,7 +854,7 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
             // the first tile's votes (a group without a tile here must not write: the
             // maxima and sums of the item's end share the space)
             if (kVotes && s.t0 + (dual ? 0 : w) < s.t1) {
-                S.g[w].vote[job & 1][r] = (float)vote_first;
+                S.g[w].vote[tiles & 1][r] = (float)vote_first;
                 group_sync();
                 if (!ok) break;
             }
@@ -907,39 +867,50 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                     const int at = (tile + step) * kTile + r;
                     if (at < s.n) vote_next = a.votes[(size_t)s.u * a.cap + at];
                 }
-                wait(&S.sfull[w], job & 1);
+                wait(&S.sfull[w], tiles & 1);
                 if (!ok) break;
                 tc_fence_after();
                 // S was issued when all four warps had handed over the group's last weights:
                 // they are done with the other buffer, and this one has been written
                 if (kVotes) {
                     late(vote_next);
-                    S.g[w].vote[(job + 1) & 1][r] = (float)vote_next;
+                    S.g[w].vote[(tiles + 1) & 1][r] = (float)vote_next;
                 }
-                if (busy) {
-                    if (tree || nv < kTile) {
-                        uint64_t keep0 = see, keep1 = 0;     // the slots the row may see
-                        if (!tree) {
-                            keep0 = nv >= 64 ? ~0ull : (1ull << nv) - 1;
-                            keep1 = nv <= 64 ? 0ull : (1ull << (nv - 64)) - 1;
+                // half by half: O of the first is made under the softmax of the second
+#pragma unroll 1
+                for (int h = 0; h < 2 && 64 * h < nv; h++) {
+                    if (busy) {
+                        const float *vote = S.g[w].vote[tiles & 1] + 64 * h;
+                        // O must not be in the making when it is rescaled.  What came before
+                        // this S is done (MMAs are in order); the first half's O need not be.
+                        // The one before that is, so the parity is not an earlier phase's.
+                        auto before_o = [&] {
+                            if (h == 0) return;
+                            wait(&S.pvdone[w][0], o_ph & 1);
+                            tc_fence_after();
+                        };
+                        if (tree || nv < 64 * h + 64) {
+                            const uint64_t keep = tree ? see : (1ull << (nv - 64 * h)) - 1;
+                            softmax_half<true, kVotes>(tS + 64 * h, tO, a.scale, vote, keep, begun, m, l, before_o);
+                        } else {
+                            softmax_half<false, kVotes>(tS + 64 * h, tO, a.scale, vote, 0, begun, m, l, before_o);
                         }
-                        if (nv <= 64)
-                            softmax_half<kVotes>(tS, tO, a.scale, S.g[w].vote[job & 1], keep0, begun, m, l);
-                        else
-                            softmax_tile<true, kVotes>(tS, tO, a.scale, S.g[w].vote[job & 1], keep0, keep1, begun, m, l);
-                    } else {
-                        softmax_tile<false, kVotes>(tS, tO, a.scale, S.g[w].vote[job & 1], 0, 0, begun, m, l);
+                        tmem_wait_st();
                     }
+                    begun = true;
+                    o_ph = o_any >> h & 1 ? o_ph ^ 1u << h : o_ph;
+                    o_any |= 1u << h;
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&S.pready[w][h]);
                 }
-                begun = true;
-                job++;
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&S.pready[w]);
+                if (!ok) break;
+                tiles++;
             }
             // ------------------------------------------------------ outputs
             if (ok) peek(i + 1);
-            if (ok && begun) wait(&S.pvdone[w], (job - 1) & 1);
+            for (int h = 0; h < 2; h++)
+                if (ok && begun && (o_any >> h & 1)) wait(&S.pvdone[w][h], o_ph >> h & 1);
             if (ok && s.t1 == s.nt) wait(&S.mended[s.mends & 3], s.mends >> 2 & 1);   // S.odd is written
             if (!ok) break;
             tc_fence_after();
