@@ -119,7 +119,8 @@ struct AttSmem {
     uint64_t full[kRing], empty[kRing];
     uint64_t segfull[kSegs], segempty[kSegs];
     uint64_t qfull[2], qempty[2];
-    uint64_t sfull[2], pready[2][2], pvdone[2][2];   // by group; by group and half of the tile
+    uint64_t sfull[2], pready[2][2];    // by group; by group and half of the tile
+    uint64_t ohalf[2], odone[2];        // O of a tile's first half; of the group's last tile
     uint64_t gsync[2], xsync, drain;
     uint64_t armed[4], mended[4];
     uint64_t odd[4];        // drafted tokens with a value that is not finite
@@ -417,10 +418,10 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
             mbar_init(&S.qfull[i], 1);
             mbar_init(&S.qempty[i], 1);
             mbar_init(&S.sfull[i], 1);
-            for (int h = 0; h < 2; h++) {
-                mbar_init(&S.pready[i][h], 4);
-                mbar_init(&S.pvdone[i][h], 1);
-            }
+            mbar_init(&S.pready[i][0], 4);
+            mbar_init(&S.pready[i][1], 4);
+            mbar_init(&S.ohalf[i], 1);
+            mbar_init(&S.odone[i], 1);
             mbar_init(&S.gsync[i], 4);
         }
         for (int i = 0; i < 4; i++) {
@@ -676,33 +677,46 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                 umma_commit(&S.sfull[w]);
                 if (last) umma_commit(&S.empty[entry]);
             };
-            // O of group w from the 16-slot steps [ks, ks1)
-            auto issue_o = [&](uint32_t w, uint32_t h, uint32_t g, int ks, int ks1, bool mend, bool first,
-                               bool last, bool keep) {
+            // O of group w from a tile's nv slots, 16 a step, its second half once the softmax
+            // has handed that over too; end: the group's last tile of the item
+            auto issue_o = [&](uint32_t w, uint32_t g, int nv, bool mend, bool first, bool last, bool keep,
+                               bool end) {
                 if (first) take(v_at, g);
                 if (first && mend) {
                     ok = ok && tree_wait(&S.mended[mends & 3], mends >> 2 & 1, &S.bad);
                     mends++;
                 }
-                ok = ok && tree_wait(&S.pready[w][h], p_ph >> (2 * w + h) & 1, &S.bad);
-                p_ph ^= 1u << (2 * w + h);
-                if (!ok) return;
-                tc_fence_after();
+                auto half = [&](uint32_t h) {
+                    ok = ok && tree_wait(&S.pready[w][h], p_ph >> (2 * h + w) & 1, &S.bad);
+                    p_ph ^= 1u << (2 * h + w);
+                    tc_fence_after();
+                    return ok;
+                };
                 const uint32_t entry = v_at >> 8 * g & 0xff;
                 const uint64_t vd = v0 + entry * kStep;
                 const uint32_t d = tmem + 128 * w, p = tmem + kColS + 128 * w;
                 auto step = [&](int ks) {
-                    umma_ts(d, p + 8 * ks + 32 * (ks >> 2), vd + (uint64_t)(ks * (2048 >> 4)), kIdescO, keep);
-                    keep = true;
+                    umma_ts(d, p + 8 * ks + 32 * (ks >> 2), vd + (uint64_t)(ks * (2048 >> 4)), kIdescO, keep || ks > 0);
                 };
-                if (ks1 - ks == 4) {
+                if (!half(0)) return;
+                if (nv > kTile - 16) {
 #pragma unroll
-                    for (int x = 0; x < 4; x++) step(ks + x);
+                    for (int ks = 0; ks < 4; ks++) step(ks);
+                    umma_commit(&S.ohalf[w]);
+                    if (!half(1)) return;
+#pragma unroll
+                    for (int ks = 4; ks < 8; ks++) step(ks);
                 } else {
-                    for (; ks < ks1; ks++) step(ks);
+                    for (int ks = 0; 16 * ks < nv; ks++) {
+                        if (ks == 4) {
+                            umma_commit(&S.ohalf[w]);
+                            if (!half(1)) return;
+                        }
+                        step(ks);
+                    }
                 }
-                umma_commit(&S.pvdone[w][h]);
                 if (last) umma_commit(&S.empty[entry]);
+                if (end) umma_commit(&S.odone[w]);
             };
             auto wait_q = [&](uint32_t half) {
                 ok = ok && tree_wait(&S.qfull[half], q_ph >> half & 1, &S.bad);
@@ -730,11 +744,8 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                     const uint32_t w = j & 1, g = dual ? 0 : w, first = !dual || !w, last = !dual || w;
                     const int before = (j - 2) >> dual, now = j >> dual;
                     if (j >= 2) {
-                        const int nv = tile_valid(s, s.t0 + before);
-                        for (int h = 0; h < 2; h++)
-                            if (nv > 64 * h)
-                                issue_o(w, h, g, 4 * h, min(4 * h + 4, (nv + 15) >> 4), needs_mend(s, s.t0 + before),
-                                        first && !h, last && nv <= 64 * h + 64, j - 2 >= 2 || h);
+                        issue_o(w, g, tile_valid(s, s.t0 + before), needs_mend(s, s.t0 + before), first, last,
+                                j - 2 >= 2, j >= jobs);
                     }
                     if (j < jobs) issue_s(w, dual ? w : i & 1, g, tile_valid(s, s.t0 + now), first, last);
                     if (j == jobs - 1) {
@@ -797,8 +808,7 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lanes + kColS + 128 * w, tO = tmem + lanes + 128 * w;
         uint32_t tiles = 0, gph = 0, xph = 0;                // tiles so far; barrier phases
-        // by half as bits: the phase of its last O, and whether there is one
-        uint32_t o_ph = 0, o_any = 0;
+        uint32_t half_ph = 0, done_ph = 0;                   // phases of ohalf and odone
         bool ok = true;
         auto wait = [&](uint64_t *b, uint32_t ph) {
             const bool x = tree_wait(b, ph, &S.bad);
@@ -886,7 +896,7 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                         // The one before that is, so the parity is not an earlier phase's.
                         auto before_o = [&] {
                             if (h == 0) return;
-                            wait(&S.pvdone[w][0], o_ph & 1);
+                            wait(&S.ohalf[w], half_ph);
                             tc_fence_after();
                         };
                         if (tree || nv < 64 * h + 64) {
@@ -898,19 +908,20 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                         tmem_wait_st();
                     }
                     begun = true;
-                    o_ph = o_any >> h & 1 ? o_ph ^ 1u << h : o_ph;
-                    o_any |= 1u << h;
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&S.pready[w][h]);
                 }
                 if (!ok) break;
                 tiles++;
+                half_ph ^= nv > 64;
             }
             // ------------------------------------------------------ outputs
             if (ok) peek(i + 1);
-            for (int h = 0; h < 2; h++)
-                if (ok && begun && (o_any >> h & 1)) wait(&S.pvdone[w][h], o_ph >> h & 1);
+            if (ok && begun) {
+                wait(&S.odone[w], done_ph);
+                done_ph ^= 1;
+            }
             if (ok && s.t1 == s.nt) wait(&S.mended[s.mends & 3], s.mends >> 2 & 1);   // S.odd is written
             if (!ok) break;
             tc_fence_after();
