@@ -734,6 +734,9 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                 // half j & 1.  S comes whole, O in halves: the first runs under the softmax of
                 // the second.
                 const int jobs = nq << dual;
+                // whole tiles need no closer look (the issuer's instructions are what a tile
+                // of two halves of rows waits for)
+                const int whole = min(s.t1, s.n >> 7) - s.t0;
                 if (dual) {
                     wait_q(0);
                     wait_q(1);
@@ -744,10 +747,12 @@ tree_attend_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ CU
                     const uint32_t w = j & 1, g = dual ? 0 : w, first = !dual || !w, last = !dual || w;
                     const int before = (j - 2) >> dual, now = j >> dual;
                     if (j >= 2) {
-                        issue_o(w, g, tile_valid(s, s.t0 + before), needs_mend(s, s.t0 + before), first, last,
-                                j - 2 >= 2, j >= jobs);
+                        const bool easy = before < whole;
+                        issue_o(w, g, easy ? kTile : tile_valid(s, s.t0 + before),
+                                !easy && needs_mend(s, s.t0 + before), first, last, j - 2 >= 2, j >= jobs);
                     }
-                    if (j < jobs) issue_s(w, dual ? w : i & 1, g, tile_valid(s, s.t0 + now), first, last);
+                    if (j < jobs)
+                        issue_s(w, dual ? w : i & 1, g, now < whole ? kTile : tile_valid(s, s.t0 + now), first, last);
                     if (j == jobs - 1) {
                         if (dual || !(i & 1)) umma_commit(&S.qempty[0]);
                         if (dual || (i & 1)) umma_commit(&S.qempty[1]);
