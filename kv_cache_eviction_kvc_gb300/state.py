@@ -166,15 +166,20 @@ class DecodeState:
         With refresh the utilities take the weight the accepted tokens gave
         (row_weight: fp32 [trees][A] or None); the lowest go until every unit
         is at its budget.  self.n_evict has the counts, self.tree_evict the
-        slots and positions."""
+        slots and positions ([2][U][most victims of this call])."""
         b = self._tree_buffers(tree.T, make=False)
         S = None
         if refresh:
             S = self.tree_S
             K_.kvc_tree_weights(self.params, max_len, tree, path, row_weight, q, k_tree,
                                 b["lse"], self.cache, S, b["ws"], stream)
+        # as many victims as there can be: fewer leave room for more units at once
+        kmax = K_.TREE_MAX
+        if self.budget is None:
+            kmax = min(kmax, max(1, max_len + path.A - self.L))
+        self.tree_evict = self._tree_evict[:2 * self.U * kmax].view(2, self.U, kmax)
         K_.kvc_tree_commit(self.params, max_len, tree, path, k_tree, v_tree, S, self.cache,
-                           self.moments, K_.TREE_MAX, self.tree_evict[0], self.tree_evict[1],
+                           self.moments, kmax, self.tree_evict[0], self.tree_evict[1],
                            self.n_evict, self.ws, stream)
 
     def _tree_buffers(self, T, make):
@@ -190,7 +195,8 @@ class DecodeState:
             dev = self.device
             if not trees:
                 self.tree_S = torch.zeros(self.U, self.cap, dtype=torch.float32, device=dev)
-                self.tree_evict = torch.full((2, self.U, K_.TREE_MAX), -1, dtype=torch.int32, device=dev)
+                self._tree_evict = torch.full((2 * self.U * K_.TREE_MAX,), -1, dtype=torch.int32,
+                                              device=dev)
             trees[T] = dict(
                 ws=torch.zeros(nbytes, dtype=torch.uint8, device=dev),
                 o=torch.zeros(self.U, T, self.G, self.d, dtype=torch.bfloat16, device=dev),

@@ -415,6 +415,9 @@ COMMIT = [
      dict(budget=[9000, 8180, 50], L=9000, votes=True, moments=True, unscored=True), True),
     (20, 4, [5000 + 37 * i for i in range(80)], [3, 0, 4, 2], 4,       # many units, no kernel of their own
      dict(budget=[5000 + 37 * i for i in range(80)], L=7925, rule="cumulative"), True),
+    # more units than fit at once
+    (10, 6, [(29 * i) % 400 for i in range(650)], [i % 7 for i in range(65)], 6,
+     dict(L=400, budget=[max(1, (29 * i) % 400) for i in range(650)], votes=True, moments=True), True),
 ]
 
 
