@@ -323,11 +323,15 @@ def kvc_decode_attend_noalloc(p, t, new_pos, max_len, q, k_new, v_new, cache: kv
 
 # ------------------------------------------------------------------ drafted tokens
 
+_BF16, _F32, _I32, _U8, _Tensor = (torch.bfloat16, torch.float32, torch.int32, torch.uint8,
+                                    torch.Tensor)
+
+
 def _sized(t, dtype, name, numel, device, optional=False):
     """The address of a tensor, as _ptr, with the element count and the device
     checked too: a row stride or a unit count that does not fit the tensor is
     an error here, not a read out of range on the device."""
-    if (type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == device
+    if (type(t) is _Tensor and t.dtype is dtype and t.get_device() == device
             and t.is_contiguous() and t.numel() >= numel):
         return t.data_ptr()
     ptr = _ptr(t, dtype, name, optional)
@@ -339,6 +343,8 @@ def _sized(t, dtype, name, numel, device, optional=False):
     return ptr
 
 
+# the current device and stream without what torch.cuda's functions do around them
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
@@ -347,6 +353,9 @@ def _stream_on(stream, device):
     if stream is None and _raw_stream is not None:
         return _raw_stream(device)
     return _stream(stream)
+
+
+_ref = ctypes.byref
 
 
 def make_tree(T, units, mask, n=None) -> kvc_tree:
@@ -378,14 +387,14 @@ def make_path(A, token, n, pos) -> kvc_path:
     return pa
 
 
-def _tree_device(p, tree, path=None):
+def _tree_device(U, tree, path=None):
     """The current device; the tree (and path) must live there and cover the units."""
-    dev = torch.cuda.current_device()
+    dev = _device()
     if tree.keep[0].get_device() != dev or (path is not None and path.keep[0].get_device() != dev):
         raise ValueError(f"the tree and path must live on the current device cuda:{dev}")
-    if tree.units < 1 or tree.trees * tree.units < p.U or (
-            path is not None and path.trees * tree.units < p.U):
-        raise ValueError(f"the trees of {tree.units} units do not cover U = {p.U}")
+    units = tree.units
+    if units < 1 or tree.trees * units < U or (path is not None and path.trees * units < U):
+        raise ValueError(f"the trees of {units} units do not cover U = {U}")
     return dev
 
 
@@ -396,28 +405,33 @@ def kvc_tree_workspace_size(p: kvc_params, T: int) -> int:
 def kvc_tree_attend(p, max_len, tree: kvc_tree, q, k_tree, v_tree, cache: kvc_cache, mom, o, lse,
                     ws, stream=None):
     """mom: kvc_moments or None (no correction)."""
-    bf, dev = torch.bfloat16, _tree_device(p, tree)
-    rows = p.U * tree.T
+    U, G, d = p.U, p.G, p.d
+    dev = _tree_device(U, tree)
+    rows = U * tree.T
+    n, heads = rows * d, rows * G
     _check(load().kvc_tree_attend(
-        ctypes.byref(p), int(max_len), ctypes.byref(tree),
-        _sized(q, bf, "q", rows * p.G * p.d, dev), _sized(k_tree, bf, "k_tree", rows * p.d, dev),
-        _sized(v_tree, bf, "v_tree", rows * p.d, dev), ctypes.byref(cache),
-        None if mom is None else ctypes.byref(mom), _sized(o, bf, "o", rows * p.G * p.d, dev),
-        _sized(lse, torch.float32, "lse", rows * p.G, dev), _sized(ws, torch.uint8, "ws", 0, dev),
+        _ref(p), int(max_len), _ref(tree),
+        _sized(q, _BF16, "q", heads * d, dev), _sized(k_tree, _BF16, "k_tree", n, dev),
+        _sized(v_tree, _BF16, "v_tree", n, dev), _ref(cache),
+        None if mom is None else _ref(mom), _sized(o, _BF16, "o", heads * d, dev),
+        _sized(lse, _F32, "lse", heads, dev), _sized(ws, _U8, "ws", 0, dev),
         ws.numel(), _stream_on(stream, dev)))
 
 
 def kvc_tree_weights(p, max_len, tree: kvc_tree, path: kvc_path, row_weight, q, k_tree, lse,
                      cache: kvc_cache, S, ws, stream=None):
     """row_weight: fp32 [trees][A] or None (all 1)."""
-    bf, f32, dev = torch.bfloat16, torch.float32, _tree_device(p, tree, path)
-    rows = p.U * tree.T
+    U, G, d = p.U, p.G, p.d
+    dev = _tree_device(U, tree, path)
+    rows = U * tree.T
+    weights = None
+    if row_weight is not None:
+        weights = _sized(row_weight, _F32, "row_weight", U // tree.units * path.A, dev)
     _check(load().kvc_tree_weights(
-        ctypes.byref(p), int(max_len), ctypes.byref(tree), ctypes.byref(path),
-        _sized(row_weight, f32, "row_weight", p.U // tree.units * path.A, dev, optional=True),
-        _sized(q, bf, "q", rows * p.G * p.d, dev), _sized(k_tree, bf, "k_tree", rows * p.d, dev),
-        _sized(lse, f32, "lse", rows * p.G, dev), ctypes.byref(cache),
-        _sized(S, f32, "S", p.U * p.cap, dev), _sized(ws, torch.uint8, "ws", 0, dev), ws.numel(),
+        _ref(p), int(max_len), _ref(tree), _ref(path), weights,
+        _sized(q, _BF16, "q", rows * G * d, dev), _sized(k_tree, _BF16, "k_tree", rows * d, dev),
+        _sized(lse, _F32, "lse", rows * G, dev), _ref(cache),
+        _sized(S, _F32, "S", U * p.cap, dev), _sized(ws, _U8, "ws", 0, dev), ws.numel(),
         _stream_on(stream, dev)))
 
 
@@ -425,17 +439,17 @@ def kvc_tree_commit(p, max_len, tree: kvc_tree, path: kvc_path, k_tree, v_tree, 
                     cache: kvc_cache, mom, kmax, evict_idx, evict_pos, n_evict, ws, stream=None):
     """S: fp32 [U][cap] from kvc_tree_weights or None (no refresh); mom:
     kvc_moments or None; evict_idx, evict_pos: int32 [U][kmax] or None."""
-    bf, i32, dev = torch.bfloat16, torch.int32, _tree_device(p, tree, path)
-    rows = p.U * tree.T
+    U, kmax = p.U, int(kmax)
+    dev = _tree_device(U, tree, path)
+    n = U * tree.T * p.d
     _check(load().kvc_tree_commit(
-        ctypes.byref(p), int(max_len), ctypes.byref(tree), ctypes.byref(path),
-        _sized(k_tree, bf, "k_tree", rows * p.d, dev),
-        _sized(v_tree, bf, "v_tree", rows * p.d, dev),
-        _sized(S, torch.float32, "S", p.U * p.cap, dev, optional=True), ctypes.byref(cache),
-        None if mom is None else ctypes.byref(mom), int(kmax),
-        _sized(evict_idx, i32, "evict_idx", p.U * int(kmax), dev, optional=True),
-        _sized(evict_pos, i32, "evict_pos", p.U * int(kmax), dev, optional=True),
-        _sized(n_evict, i32, "n_evict", p.U, dev), _sized(ws, torch.uint8, "ws", 0, dev),
+        _ref(p), int(max_len), _ref(tree), _ref(path),
+        _sized(k_tree, _BF16, "k_tree", n, dev), _sized(v_tree, _BF16, "v_tree", n, dev),
+        None if S is None else _sized(S, _F32, "S", U * p.cap, dev), _ref(cache),
+        None if mom is None else _ref(mom), kmax,
+        None if evict_idx is None else _sized(evict_idx, _I32, "evict_idx", U * kmax, dev),
+        None if evict_pos is None else _sized(evict_pos, _I32, "evict_pos", U * kmax, dev),
+        _sized(n_evict, _I32, "n_evict", U, dev), _sized(ws, _U8, "ws", 0, dev),
         ws.numel(), _stream_on(stream, dev)))
 
 
