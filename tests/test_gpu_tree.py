@@ -498,6 +498,50 @@ def test_commit_of_a_token_named_twice():
     check_commit(c, S.cpu().numpy(), 3)
 
 
+def test_commit_of_many_long_units_is_as_of_few():
+    """160 units in one call and 80 at a time: the same bits (the number of
+    units chooses how the work is laid out)."""
+    U, n, cap, T, A = 160, 8250, 8300, 3, 2
+    g = torch.Generator(device=DEV)
+    g.manual_seed(3)
+
+    def rnd(*s, dtype=torch.bfloat16):
+        return torch.randn(*s, generator=g, device=DEV).to(dtype)
+
+    start = dict(K=rnd(U, cap, 128), V=rnd(U, cap, 128), util=rnd(U, cap, dtype=torch.float64).exp(),
+                 pos=torch.randperm(cap, device=DEV, dtype=torch.int32).repeat(U, 1),
+                 len=torch.full((U,), n, dtype=torch.int32, device=DEV),
+                 n=torch.full((U,), 5.0, device=DEV), mu_k=rnd(U, 128, dtype=torch.float32),
+                 mu_v=rnd(U, 128, dtype=torch.float32), C=rnd(U, 128, 128, dtype=torch.float32))
+    kt, vt, S = rnd(U, T, 128), rnd(U, T, 128), rnd(U, cap, dtype=torch.float32).exp()
+    mask = torch.tensor([[1, 3, 7]] * 4, dtype=torch.int64, device=DEV)
+    tok = torch.tensor([[0, 1], [0, 2], [1, 2], [0, 1]], dtype=torch.int32, device=DEV)
+    counts = torch.tensor([2, 1, 2, 0], dtype=torch.int32, device=DEV)
+    first = torch.full((4,), 9000, dtype=torch.int32, device=DEV)
+
+    def run(units):
+        c = {k: v.clone() for k, v in start.items()}
+        ne = torch.zeros(U, dtype=torch.int32, device=DEV)
+        ev = torch.full((2, U, A), -9, dtype=torch.int32, device=DEV)
+        for a in range(0, U, units):
+            z, b = slice(a, a + units), slice(a // 40, (a + units) // 40)
+            p = K.make_params(units, 1, cap, n, rule=K.RULE_CUMULATIVE)
+            dws = torch.empty(K.kvc_decode_workspace_size(p), dtype=torch.uint8, device=DEV)
+            K.kvc_decode_workspace_init(p, dws)
+            K.kvc_tree_commit(p, n, K.make_tree(T, 40, mask[b]), K.make_path(A, tok[b], counts[b], first[b]),
+                              kt[z], vt[z], S[z], K.make_cache(c["K"][z], c["V"][z], None, c["pos"][z],
+                                                               c["util"][z], c["len"][z]),
+                              K.make_moments(c["n"][z], c["mu_k"][z], c["mu_v"][z], c["C"][z]), A,
+                              ev[0, z], ev[1, z], ne[z], dws)
+            assert K.kvc_get_device_status(dws) == 0
+        return [*c.values(), ne, ev]
+
+    many, few = run(160), run(80)
+    assert many[-2].tolist() == [2] * 40 + [1] * 40 + [2] * 40 + [0] * 40
+    for x, y in zip(many, few):
+        assert torch.equal(x, y)
+
+
 def test_commit_in_a_graph():
     """Weights and commit captured once and replayed from two states: what
     the calls give."""
