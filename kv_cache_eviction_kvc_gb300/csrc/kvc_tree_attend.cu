@@ -1050,12 +1050,13 @@ struct JoinArgs {
 };
 
 // The sums of a cut item's parts added.  A warp has two rows, a lane four of
-// their columns; the loads of four parts are in flight together.  The result
+// their columns; the loads of eight parts are in flight together (four: 8 units
+// of 4096 slots 14.7 us and not 13.4; of 240 rows 23.3 and not 23.9).  The result
 // is the output, or (kKeep, when the moments follow) the first part's place
 // takes it.  grid (CTAs of the attention, rows / 16): block x takes the item
 // whose first cut is the start of part x.  Bound by latency: about 5 us behind
 // the attention for 8 units of 131071 slots (152 parts of 252 rows, 20 MB).
-constexpr int kJoinRows = 2;
+constexpr int kJoinRows = 2, kJoinAt = 8;
 
 template <bool kKeep>
 __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ JoinArgs j)
@@ -1076,12 +1077,12 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
         L[i] = 0.f;
         f[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    for (int k0 = 0; k0 < np; k0 += 4) {
+    for (int k0 = 0; k0 < np; k0 += kJoinAt) {
         // places past the last part or row are read again and weigh nothing
-        float2 ml[4][kJoinRows];
-        float4 p[4][kJoinRows];
+        float2 ml[kJoinAt][kJoinRows];
+        float4 p[kJoinAt][kJoinRows];
 #pragma unroll
-        for (int k = 0; k < 4; k++)
+        for (int k = 0; k < kJoinAt; k++)
 #pragma unroll
             for (int i = 0; i < kJoinRows; i++) {
                 const size_t x = at + min(k0 + k, np - 1) * step + min(i, nr - 1);
@@ -1089,7 +1090,7 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
                 p[k][i] = reinterpret_cast<const float4 *>(a.part + x * kD)[lane];
             }
 #pragma unroll
-        for (int k = 0; k < 4; k++)
+        for (int k = 0; k < kJoinAt; k++)
 #pragma unroll
             for (int i = 0; i < kJoinRows; i++) {
                 if (k0 + k >= np) continue;
@@ -1538,7 +1539,7 @@ struct Cut {
 // runs, and 152 when all of them load.  A join is 320 and the sums' way to
 // memory and back.  Measured (us), whole / parts of their own / line: 8 units
 // of 512 slots 10.5 / 10.9 / -, of 1024 slots 13.9 / 11.2 / -, of 4096 slots
-// - / 14.6 / 20.2; 40 of 2432 slots 23.3 / 17.5 / 20.6; 80 of 1408 slots 17.8 /
+// - / 13.4 / 20.2; 40 of 2432 slots 23.3 / 17.5 / 20.6; 80 of 1408 slots 17.8 /
 // - / 22.1, with 240 rows 28.9 / - / 38.9; 128 of up to 3277 slots 37 / - / 43;
 // 160 of 1152 slots 30.3 / - / 26.2; 1024 of 1024 slots 144 / - / 161.
 Cut choose_cut(long long items, long long tiles, int rows)
