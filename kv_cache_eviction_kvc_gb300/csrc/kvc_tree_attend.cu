@@ -20,7 +20,7 @@
 // Measured (bf16, d = 128, G = 4; a call among others): 128 units of 2623 slots
 // on average, 24 tokens: 36.5 us, 4.9 TB/s; 1024 units of 1024 slots, 16 tokens,
 // votes and moments: 140 us, 4.6 TB/s; 8 units of 131071 slots, 63 tokens (252
-// rows): 118 us, 4.6 TB/s and 1.15 PFLOP/s, 31 tokens: 91 us, 5.9 TB/s.  With
+// rows): 118 to 122 us, 4.5 TB/s and 1.13 PFLOP/s, 31 tokens: 91 us, 5.9 TB/s.  With
 // two halves of rows a tile takes 3600 clocks for its 2048 of the tensor core:
 // S overwrites P, so a group's product, softmax and next product follow one
 // another.  (S in two halves of 64 slots, each made under the softmax of the

@@ -13,8 +13,8 @@
 // about 1200 of one SM's share of the bandwidth).  The 128-slot tiles of all
 // units form one line, cut into equal parts for a persistent CTA per SM; every
 // tile stands alone, so nothing is joined.  Measured (G = 4; a call among
-// others): 128 units of 2623 slots on average, up to 6 accepted tokens: 18.7 us,
-// 4.7 TB/s; 1024 units of 1024 slots, 5 accepted, votes: 51 us, 5.5 TB/s; 8 units
+// others): 128 units of 2623 slots on average, up to 6 accepted tokens: 18.6 us,
+// 4.7 TB/s; 1024 units of 1024 slots, 5 accepted, votes: 50 us, 5.6 TB/s; 8 units
 // of 131071 slots, 17 accepted: 50 us, 5.5 TB/s.  In between a tile takes 1320
 // clocks, the bandwidth's; what is left is the start (about 6 us until the first
 // product: lengths, paths, query rows).

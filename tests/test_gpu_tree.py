@@ -180,6 +180,8 @@ ATTEND = [
     # parts of single units, some of fewer tiles than parts
     (1, 2, 12, [4000, 130, 5, 0, 2050], dict(votes=True, moments=True)),
     (1, 8, 40, [2900, 1, 260], dict(moments=True)),
+    (1, 8, 3, [20000], dict(votes=True, moments=True)),      # one unit on every SM
+    (1, 1, 1, [1], dict(moments=True)),
 ]
 
 
