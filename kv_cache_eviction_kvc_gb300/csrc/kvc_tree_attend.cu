@@ -1156,6 +1156,10 @@ struct MomJob {
     int u, row0, rows, sid;       // unit, first row of it, rows, place of the sums
     int r0;                       // first row of the item
     float ne;
+
+    // The unit has evicted tokens to mix in.  All roles ask this, so that none is a job
+    // ahead of another; a count that is NaN mixes (as in kvc_correct) and stays in its unit.
+    __device__ __forceinline__ bool mixes() const { return !(ne <= 0.f); }
 };
 
 // sums: the place of the sums is wanted, which is known after the attention.
@@ -1261,7 +1265,7 @@ tree_moment_kernel(const __grid_constant__ JoinArgs j, const __grid_constant__ C
     if (warp == 16) {
         // -------------------------------------------------------- producer
         for (; ok && list.next(m); kf++) {
-            const bool mix = m.ne > 0.f;
+            const bool mix = m.mixes();
             const int st = kf & 1;
             if (kf >= 2) wait(&S.fempty[st], (kf / 2 - 1) & 1);
             if (!ok) break;
@@ -1283,7 +1287,7 @@ tree_moment_kernel(const __grid_constant__ JoinArgs j, const __grid_constant__ C
         const uint64_t c0 = umma_sdesc(smem_u32(planes));
         for (; ok && list.next(m); kf++) {
             const int st = kf & 1;
-            if (m.ne <= 0.f || !j.first_order) continue;
+            if (!m.mixes() || !j.first_order) continue;
             wait(&S.ffull[st], (kf / 2) & 1);
             wait(&S.pready[kc & 1], (kc >> 1) & 1);
             if (kc >= 2) wait(&S.dfree[kc & 1], ((kc >> 1) - 1) & 1);
@@ -1342,7 +1346,7 @@ tree_moment_kernel(const __grid_constant__ JoinArgs j, const __grid_constant__ C
         };
         auto next = [&] {                                    // the next job with a product
             while (list.next(m))
-                if (m.ne > 0.f) return true;
+                if (m.mixes()) return true;
             return false;
         };
         bool more = j.first_order && next();
@@ -1369,7 +1373,7 @@ tree_moment_kernel(const __grid_constant__ JoinArgs j, const __grid_constant__ C
         float k0[16], k1[16];                                // the lane's part of mu_k, and of the next job's
         float v0 = 0.f, v1 = 0.f;
         auto fetch = [&](float (&k)[16], float &v) {
-            if (m.ne <= 0.f) return;
+            if (!m.mixes()) return;
             const float *mk = j.mu_k + (size_t)m.u * kD + 8 * (lane & 7);
 #pragma unroll
             for (int i = 0; i < 16; i++) k[i] = mk[64 * (i >> 3) + (i & 7)];
@@ -1380,11 +1384,12 @@ tree_moment_kernel(const __grid_constant__ JoinArgs j, const __grid_constant__ C
         for (; more && ok; kf++) {
             const int st = kf & 1;
             const float ne = m.ne;
+            const bool mix = m.mixes();
             more = list.next(m);
             if (more) fetch(k1, v1);
             wait(&S.ffull[st], (kf / 2) & 1);
             if (!ok) break;
-            if (ne > 0.f) {
+            if (mix) {
                 const float ln = logf(ne);
                 float z[4];
 #pragma unroll
@@ -1425,7 +1430,7 @@ tree_moment_kernel(const __grid_constant__ JoinArgs j, const __grid_constant__ C
         for (; more && ok; kf++) {
             const int st = kf & 1, c = kc;
             const MomJob g = m;
-            const bool mix = g.ne > 0.f, prod = mix && j.first_order;
+            const bool mix = g.mixes(), prod = mix && j.first_order;
             more = list.next(m);
             if (more) ml1 = fetch();
             wait(&S.ffull[st], (kf / 2) & 1);

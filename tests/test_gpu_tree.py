@@ -892,3 +892,31 @@ def test_offsets_past_32_bits():
                    f64(k[-1]), f64(v[-1]), [0, 1], 9000, None)
     assert np.array_equal(f64(Kc[-1, :n]), ref["K"]) and np.array_equal(f64(Vc[-1, :n]), ref["V"])
     assert ne.tolist() == [2] * U
+
+
+# ------------------------------------------------------- one unit does not reach another
+
+@pytest.mark.parametrize("correction", [K.CORR_FIRST_ORDER, K.CORR_ZERO_ORDER])
+@pytest.mark.parametrize("n", [NAN, -3.0, 0.0])
+def test_attend_moment_count_stays_in_its_unit(n, correction):
+    """A count of evicted tokens that is NaN (or not above zero) is its unit's
+    own matter: three units of a CTA's list have it, the others are as they
+    were to the bit.  NaN gives NaN as in the one-token correction; without
+    evicted tokens the output is the attention's."""
+    U, odd = 480, [3, 156, 307]
+    c = Case(61, 4, 2, 5, [10 + i % 7 for i in range(U)], moments=True, correction=correction)
+    c.t["mom"][0].copy_(1 + torch.arange(U, device=DEV) % 9)
+    o, lse = (x.clone() for x in c.run_attend())
+    c.t["mom"][0][odd] = n
+    got, got_lse = c.run_attend()
+    assert K.kvc_get_device_status(c.ws) == 0
+    rest = [u for u in range(U) if u not in odd]
+    assert torch.equal(got[rest], o[rest]) and torch.equal(got_lse, lse)
+    if n != n:
+        assert torch.isnan(got[odd]).all()
+        return
+    c.p.correction = K.CORR_OFF
+    plain = c.run_attend()[0]
+    # the groups' sums are normalised before or after they are added: a few half steps of
+    # fp32 on values of order 1 (2^-20), then bf16 roundings that are at most a step apart
+    assert torch.allclose(got[odd].double(), plain[odd].double(), rtol=2.0 ** -7, atol=2.0 ** -20)
