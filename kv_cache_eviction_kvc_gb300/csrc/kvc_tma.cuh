@@ -217,19 +217,38 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
     return fn;
 }
 
+// A tensor map of `rank` dimensions, 128-byte swizzle, what lies outside reads as
+// zero.  The encoder needs a current context, which a host thread has only from its
+// first runtime call on that makes one (a launch does): the device's is made current
+// then.
+inline bool encode_map(CUtensorMap *m, CUtensorMapDataType type, int rank, const void *base,
+                       const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint32_t estr[3] = {1u, 1u, 1u};
+    auto encode = [&] {
+        return enc(m, type, (cuuint32_t)rank, const_cast<void *>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    CUresult r = encode();
+    if (r == CUDA_ERROR_INVALID_CONTEXT || r == CUDA_ERROR_NOT_INITIALIZED) {
+        int device = 0;
+        if (cudaGetDevice(&device) != cudaSuccess || cudaSetDevice(device) != cudaSuccess) return false;
+        r = encode();
+    }
+    return r == CUDA_SUCCESS;
+}
+
 // [rows][128] bf16 rows of 256 bytes, loaded as boxes of 64 columns x
 // box_rows rows with the 128-byte swizzle.  Rows past the end read as zero.
 inline bool make_row_map(CUtensorMap *m, const void *base, uint64_t rows, int box_rows)
 {
-    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-    if (!enc) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)128, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)256};
     const cuuint32_t box[2] = {64u, (cuuint32_t)box_rows};
-    const cuuint32_t estr[2] = {1u, 1u};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box,
-               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box);
 }
 
 // cluster barrier split into its two halves (any thread may arrive early and

@@ -128,14 +128,10 @@ __device__ __forceinline__ void tma_3d_hint(void *dst, const CUtensorMap *map, i
 // the 128-byte swizzle.
 inline bool make_f32_map(CUtensorMap *m, const void *base, uint64_t units, uint64_t rows, int box_rows)
 {
-    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-    if (!enc) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)kD, (cuuint64_t)rows, (cuuint64_t)units};
     const cuuint64_t strides[2] = {(cuuint64_t)(kD * 4), (cuuint64_t)(rows * kD * 4)};
-    const cuuint32_t box[3] = {32u, (cuuint32_t)box_rows, 1u}, estr[3] = {1u, 1u, 1u};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void *>(base), dims, strides, box,
-               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint32_t box[3] = {32u, (cuuint32_t)box_rows, 1u};
+    return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, box);
 }
 
 // [units][rows][128] bf16, boxes of 64 columns x 64 rows of a unit with the
@@ -143,14 +139,10 @@ inline bool make_f32_map(CUtensorMap *m, const void *base, uint64_t units, uint6
 // row index fit 32 bits where their product does not.
 inline bool make_unit_map(CUtensorMap *m, const void *base, uint64_t units, uint64_t rows)
 {
-    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-    if (!enc) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)kD, (cuuint64_t)rows, (cuuint64_t)units};
     const cuuint64_t strides[2] = {(cuuint64_t)(kD * 2), (cuuint64_t)(rows * kD * 2)};
-    const cuuint32_t box[3] = {64u, 64u, 1u}, estr[3] = {1u, 1u, 1u};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
-               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint32_t box[3] = {64u, 64u, 1u};
+    return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box);
 }
 
 // Programmatic dependent launch: a kernel's launch and set-up overlap the end of

@@ -3,6 +3,8 @@ kvc_tree_commit) against their definitions in 64 bits (tree_ref.py): head
 layouts, lengths from zero on, ragged trees and budgets, masks that leave rows
 empty, NaN where nothing looks, ties, every rule; then runs of the three
 together against the one-token calls, streams and graphs."""
+import ctypes
+import threading
 from fractions import Fraction
 
 import numpy as np
@@ -920,3 +922,55 @@ def test_attend_moment_count_stays_in_its_unit(n, correction):
     # the groups' sums are normalised before or after they are added: a few half steps of
     # fp32 on values of order 1 (2^-20), then bf16 roundings that are at most a step apart
     assert torch.allclose(got[odd].double(), plain[odd].double(), rtol=2.0 ** -7, atol=2.0 ** -20)
+
+
+@pytest.mark.parametrize("call", ["attend", "weights", "step"])
+def test_first_call_of_a_host_thread(call):
+    """The first thing a host thread does is a call: it is not refused (the
+    thread has no context of its own yet), gives the bits that it gives
+    elsewhere, and a one-token step takes the same kernels (their bits)."""
+    lib, ref = K.load(), ctypes.byref
+    c = Case(73, 1, 4, 6, [300, 64], kind="chain", moments=True, L=300)
+    c.path([3, 2], 3)
+    c.run_attend()
+    S = torch.zeros(c.U, c.cap, device=DEV)
+    at = {n: x.data_ptr() for n, x in c.t.items() if isinstance(x, torch.Tensor)}
+    st, rnd = _stream(4, 2, 4, 65, 70, 64, 1)
+    st.step_calls(1, 65, rnd(2, 4, 128).bfloat16(), rnd(2, 128).bfloat16(), rnd(2, 128).bfloat16(), 66)
+    st.set_kmax(1)
+    q, k, v = rnd(2, 4, 128).bfloat16(), rnd(2, 128).bfloat16(), rnd(2, 128).bfloat16()
+    out, state, args = {
+        "attend": ([c.o, c.lse], [],
+                   (ref(c.p), c.max_len, ref(c.tree), at["q"], at["kt"], at["vt"], ref(c.cache),
+                    ref(c.moments), c.o.data_ptr(), c.lse.data_ptr(), c.ws.data_ptr(), c.ws.numel(), None)),
+        "weights": ([S], [],
+                    (ref(c.p), c.max_len, ref(c.tree), ref(c.accept), None, at["q"], at["kt"],
+                     c.lse.data_ptr(), ref(c.cache), S.data_ptr(), c.ws.data_ptr(), c.ws.numel(), None)),
+        "step": ([st.o, st.util, st.C], [st.K, st.V, st.pos, st.util, st.len, st.n, st.mu_k, st.mu_v, st.C],
+                 (ref(st.params), 2, 66, 65, q.data_ptr(), k.data_ptr(), v.data_ptr(), ref(st.cache),
+                  ref(st.moments), st.o.data_ptr(), None, 1, st.evict_idx.data_ptr(), None,
+                  st.n_evict.data_ptr(), st.ws.data_ptr(), st.ws.numel(), None)),
+    }[call]
+    name = {"attend": "kvc_tree_attend", "weights": "kvc_tree_weights", "step": "kvc_decode_step"}[call]
+    first = [x.clone() for x in state]
+    torch.cuda.synchronize()
+    assert getattr(lib, name)(*args) == 0
+    torch.cuda.synchronize()
+    want = [x.clone() for x in out]
+    for x, y in zip(state, first):
+        x.copy_(y)
+    for x in out if not state else [st.o]:
+        x.zero_()
+    torch.cuda.synchronize()
+    got = []
+
+    def run():
+        got.append((getattr(lib, name)(*args), K.kvc_last_error()))
+
+    thread = threading.Thread(target=run)
+    thread.start()
+    thread.join()
+    torch.cuda.synchronize()
+    assert got[0][0] == 0, got
+    for x, y in zip(out, want):
+        assert torch.equal(x, y)
