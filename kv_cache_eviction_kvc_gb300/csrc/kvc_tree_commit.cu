@@ -620,12 +620,17 @@ cudaError_t launch_tree_commit(const kvc_params &p, int max_len, const TreeArgs 
     // units 17.9 and 18.9; of 4096 slots 8 units take the same.
     const bool split = max_len > kLong || (max_len > kLong / 2 && p.U <= kSms / 2);
     const size_t smem = sizeof(ComSmem) + (m ? 2 * (size_t)kmax * kD * sizeof(float) : 0);
+    // The attribute is the kernel's, shared by the host's threads: every call allows the
+    // most that any call takes (a call that allowed its own size could take another
+    // thread's away between that one's setting and its launch).
+    constexpr size_t kMost = sizeof(ComSmem) + 2 * (size_t)kTreeMax * kD * sizeof(float);
+    static_assert(kMost <= 227 * 1024, "one block's shared memory");
     // A unit that has an SM to itself gets twice the threads: 128 units of 2623 slots on
     // average 12.1 us with 256 and 11.7 with 512, 8 of 131071 19.8 and 18.8.
     const bool wide = p.U <= kSms;
     auto *kernel = wide ? split ? tree_commit_kernel<2 * kThreads, true> : tree_commit_kernel<2 * kThreads, false>
                    : split ? tree_commit_kernel<kThreads, true> : tree_commit_kernel<kThreads, false>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
     if (e != cudaSuccess) return e;
     if (split) {
         if (p.U > 65535) return cudaErrorInvalidValue;

@@ -78,6 +78,7 @@ struct WtSmem {
     uint32_t tmem;
 };
 constexpr size_t kCtl = sizeof(WtSmem) + 1024;
+constexpr int kMostSmem = 227 * 1024;            // of one block
 
 // Accepted tokens of unit u, or -1 when the unit is refused.
 __device__ __forceinline__ int unit_acc(const WtArgs &a, int u, int n, int32_t *err)
@@ -499,13 +500,14 @@ cudaError_t launch_tree_weights(const kvc_params &p, int max_len, const TreeArgs
     a.qbufs = a.rows <= 128 ? 2 : 1;
     a.dcols = a.rows <= 128 ? 128 : a.rows <= 256 ? 256 : 512;
     a.dbufs = 512 / a.dcols;
-    a.ring = (int)((227 * 1024 - kCtl - (size_t)a.qbufs * a.rows * 256) / kSlot);
+    a.ring = (int)((kMostSmem - kCtl - (size_t)a.qbufs * a.rows * 256) / kSlot);
     if (a.ring > kMaxRing) a.ring = kMaxRing;
     a.by_units = FastDiv(t.units);
     a.scale = kLog2e / sqrtf((float)kD);
     const size_t smem = (size_t)a.ring * kSlot + (size_t)a.qbufs * a.rows * 256 + sizeof(WtSmem);
-    cudaError_t e = cudaFuncSetAttribute(tree_weights_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // (the attribute is the kernel's, shared by the host's threads: never one call's size)
+    cudaError_t e = cudaFuncSetAttribute(tree_weights_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kMostSmem);
     if (e != cudaSuccess) return e;
     long long grid = tiles > p.U ? tiles : p.U;
     if (grid > kGrid) grid = kGrid;

@@ -4,6 +4,7 @@ layouts, lengths from zero on, ragged trees and budgets, masks that leave rows
 empty, NaN where nothing looks, ties, every rule; then runs of the three
 together against the one-token calls, streams and graphs."""
 import ctypes
+import sys
 import threading
 from fractions import Fraction
 
@@ -974,3 +975,65 @@ def test_first_call_of_a_host_thread(call):
     assert got[0][0] == 0, got
     for x, y in zip(out, want):
         assert torch.equal(x, y)
+
+
+def test_calls_of_two_host_threads():
+    """Two host threads with a stream, a state and sizes of their own (one
+    accepted token and no moments; 64 and moments, 512 rows of q) call at
+    once, as fast as they can: no call is refused, and what they leave is what
+    the same calls leave one thread after the other."""
+    lib, ref, calls = K.load(), ctypes.byref, 3000
+
+    def make(seed, G, T, A, moments):
+        c = Case(seed, 1, G, T, [300, 200], kind="chain", moments=moments, budget=[300, 200], L=300)
+        c.path([A, A], A)
+        c.run_attend()
+        c.S = torch.zeros(c.U, c.cap, device=DEV)
+        ne = torch.zeros(c.U, dtype=torch.int32, device=DEV)
+        c.stream = torch.cuda.Stream()
+        at = {n: x.data_ptr() for n, x in c.t.items() if isinstance(x, torch.Tensor)}
+        mom = ref(c.moments) if moments else None
+        side = ctypes.c_void_p(c.stream.cuda_stream)
+        c.weights = (ref(c.p), c.max_len, ref(c.tree), ref(c.accept), None, at["q"], at["kt"],
+                     c.lse.data_ptr(), ref(c.cache), c.S.data_ptr(), c.ws.data_ptr(), c.ws.numel(), side)
+        c.commit = (ref(c.p), c.max_len, ref(c.tree), ref(c.accept), at["kt"], at["vt"], c.S.data_ptr(),
+                    ref(c.cache), mom, A, None, None, ne.data_ptr(), c.dws.data_ptr(), c.dws.numel(), side)
+        c.state = [c.t[n] for n in ("K", "V", "pos", "util", "len")] + (c.t["mom"] or []) + [c.S, ne]
+        return c
+
+    cases = [make(71, 1, 4, 1, False), make(72, 8, 64, 64, True)]
+    first = [[x.clone() for x in c.state] for c in cases]
+    refused = []
+
+    def loop(c):
+        for _ in range(calls):
+            status = lib.kvc_tree_weights(*c.weights) or lib.kvc_tree_commit(*c.commit)
+            if status:
+                refused.append((status, K.kvc_last_error()))     # (the thread's own message)
+                return
+
+    torch.cuda.synchronize()
+    want = []
+    for c, f in zip(cases, first):
+        loop(c)
+        torch.cuda.synchronize()
+        want.append([x.clone() for x in c.state])
+        for x, y in zip(c.state, f):
+            x.copy_(y)
+    torch.cuda.synchronize()
+    before = sys.getswitchinterval()
+    sys.setswitchinterval(1e-6)
+    try:
+        threads = [threading.Thread(target=loop, args=(c,)) for c in cases]
+        for x in threads:
+            x.start()
+        for x in threads:
+            x.join()
+    finally:
+        sys.setswitchinterval(before)
+    torch.cuda.synchronize()
+    assert not refused, refused
+    for c, w in zip(cases, want):
+        assert K.kvc_get_device_status(c.ws) == 0 and K.kvc_get_device_status(c.dws) == 0
+        for x, y in zip(c.state, w):
+            assert torch.equal(x.contiguous().view(torch.uint8), y.contiguous().view(torch.uint8))
