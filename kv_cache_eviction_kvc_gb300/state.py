@@ -204,9 +204,13 @@ class DecodeState:
         return trees[T]
 
     def tree_status(self) -> int:
-        """The first error that a verify or accept recorded (0: none)."""
-        for b in self.__dict__.get("_trees", {}).values():
-            status = K_.kvc_get_device_status(b["ws"])
+        """The first error that a verify or accept recorded and that has not
+        been read yet (0: none).  accept's commit records in the decode
+        stream's workspace, as the steps do: an error there is returned here
+        or by device_status(), whichever is asked first."""
+        trees = self.__dict__.get("_trees", {})
+        for ws in [b["ws"] for b in trees.values()] + ([self.ws] if trees else []):
+            status = K_.kvc_get_device_status(ws)
             if status:
                 return status
         return 0

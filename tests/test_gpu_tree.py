@@ -1037,3 +1037,32 @@ def test_calls_of_two_host_threads():
         assert K.kvc_get_device_status(c.ws) == 0 and K.kvc_get_device_status(c.dws) == 0
         for x, y in zip(c.state, w):
             assert torch.equal(x.contiguous().view(torch.uint8), y.contiguous().view(torch.uint8))
+
+
+# ------------------------------------------------------------------ the state's calls
+
+def _chain(T, U, tok, count, pos):
+    """A chain of T tokens of one sequence, and a path of it."""
+    mask = torch.tensor([[(2 << i) - 1 for i in range(T)]], dtype=torch.int64, device=DEV)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)
+    return K.make_tree(T, U, mask), K.make_path(len(tok), i32([tok]), i32([count]), i32([pos]))
+
+
+@pytest.mark.parametrize("refused", ["a dead token", "too many victims", "too few scored"])
+def test_state_reports_what_only_the_commit_refuses(refused):
+    """Without a refresh only the commit looks at the path, and only it
+    counts victims: tree_status() has its refusal, once."""
+    U, G, L, T = 4, 2, 80, 5
+    st, rnd = _stream(6, U, G, L, L + 80, L, 1)
+    tree, path = _chain(T, U, [0, 5 if refused == "a dead token" else 1], 2, 500)
+    args = rnd(U, T, G, 128).bfloat16(), rnd(U, T, 128).bfloat16(), rnd(U, T, 128).bfloat16()
+    if refused == "too many victims":
+        st.len.fill_(L + 70)                           # 70 slots over the budget
+    if refused != "too few scored":
+        st.util.fill_(1.0)
+    max_len = int(st.len[0])
+    st.verify(tree, *args, max_len)
+    st.accept(tree, path, *args, max_len, refresh=False)
+    assert st.n_evict.tolist() == [0] * U and st.len.tolist() == [max_len] * U
+    assert st.tree_status() == (2 if refused == "too many victims" else 1)
+    assert st.tree_status() == 0 and st.device_status() == 0
