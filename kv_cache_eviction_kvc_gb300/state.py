@@ -155,7 +155,7 @@ class DecodeState:
         (o [U][T][G][d] bf16, lse [U][T][G] fp32), buffers of the state that
         the next call with the same T writes again.  The first call with a T
         allocates: make it before capturing one into a graph."""
-        b = self._tree_buffers(tree.T, make=True)
+        b = self._tree_buffers(tree.T, True, stream)
         K_.kvc_tree_attend(self.params, max_len, tree, q, k_tree, v_tree, self.cache, self.moments,
                            b["o"], b["lse"], b["ws"], stream)
         return b["o"], b["lse"]
@@ -167,7 +167,7 @@ class DecodeState:
         (row_weight: fp32 [trees][A] or None); the lowest go until every unit
         is at its budget.  self.n_evict has the counts, self.tree_evict the
         slots and positions ([2][U][most victims of this call])."""
-        b = self._tree_buffers(tree.T, make=False)
+        b = self._tree_buffers(tree.T, False)
         S = None
         if refresh:
             S = self.tree_S
@@ -182,7 +182,7 @@ class DecodeState:
                            self.moments, kmax, self.tree_evict[0], self.tree_evict[1],
                            self.n_evict, self.ws, stream)
 
-    def _tree_buffers(self, T, make):
+    def _tree_buffers(self, T, make, stream=None):
         """What verify and accept of trees of T tokens use; kept for each T
         (a captured graph goes on using them)."""
         trees = self.__dict__.setdefault("_trees", {})
@@ -201,6 +201,11 @@ class DecodeState:
                 ws=torch.zeros(nbytes, dtype=torch.uint8, device=dev),
                 o=torch.zeros(self.U, T, self.G, self.d, dtype=torch.bfloat16, device=dev),
                 lse=torch.zeros(self.U, T, self.G, dtype=torch.float32, device=dev))
+            if stream is not None:
+                # the fills above are on the current stream: the call's waits for them
+                if not hasattr(stream, "wait_stream"):
+                    stream = torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream), dev)
+                stream.wait_stream(torch.cuda.current_stream(dev))
         return trees[T]
 
     def tree_status(self) -> int:

@@ -1066,3 +1066,31 @@ def test_state_reports_what_only_the_commit_refuses(refused):
     assert st.n_evict.tolist() == [0] * U and st.len.tolist() == [max_len] * U
     assert st.tree_status() == (2 if refused == "too many victims" else 1)
     assert st.tree_status() == 0 and st.device_status() == 0
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_first_verify_on_another_stream(handle):
+    """The first call with a T makes its buffers: a call on another stream
+    than the current one, which is busy, does not run ahead of their fills."""
+    U, G, L, T = 4, 4, 3000, 9
+    st, rnd = _stream(7, U, G, L, L + 20, L, 1)
+    tree, path = _chain(T, U, [0, 1], 2, 5000)
+    args = rnd(U, T, G, 128).bfloat16(), rnd(U, T, 128).bfloat16(), rnd(U, T, 128).bfloat16()
+    st.util.copy_(torch.rand(U, L + 20, device=DEV, dtype=torch.float64))
+    side = torch.cuda.Stream()
+    room = torch.empty(256 << 20, dtype=torch.uint8, device=DEV)
+    del room                                           # the buffers come without a device call
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)                     # about 0.1 s of the current stream
+    on = side.cuda_stream if handle else side
+    o, lse = st.verify(tree, *args, L, stream=on)
+    st.accept(tree, path, *args, L, stream=on)
+    torch.cuda.synchronize()
+    S, got = st.tree_S.clone(), (o.clone(), lse.clone())
+    ev = st.tree_evict.clone()
+    again, _ = _stream(7, U, G, L, L + 20, L, 1)
+    again.util.copy_(st.util)
+    want = again.verify(tree, *args, L)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    again.accept(tree, path, *args, L)
+    assert torch.equal(S, again.tree_S) and (ev[0] >= 0).all()
