@@ -57,7 +57,7 @@
 extern "C" {
 #endif
 
-#define KVC_VERSION 10200  /* major*10000 + minor*100 + patch */
+#define KVC_VERSION 10300  /* major*10000 + minor*100 + patch */
 
 /* Exported symbols (the library is built with hidden default visibility). */
 #if defined(__GNUC__)
@@ -591,10 +591,13 @@ KVC_API kvc_status kvc_tree_attend(const kvc_params *p, int32_t max_len, const k
  * (where kvc_tree_commit appends c_r).  Entries from n + a on are left as
  * they were; a = 0 gives S = 0 on [0, n).  Rows with lse = -inf give nothing.
  * row_weight: DEVICE [U/units][A] fp32, >= 0 (a negative weight gives NaN).
- * S [U][cap] fp32; a weight below fp32's range is 0.  The logits are formed
- * again from the keys (256 bytes per slot): which rows count is known only
- * after the verification, and keeping all T G logits per slot would move
- * more.  max_len >= len[u].  Device-side errors, which leave the unit's
+ * S [U][cap] fp32: a weight below fp32's range is 0, so over sharp attention
+ * (logits further apart than about 87) slots tie that the method orders.  With
+ * S in fp64 (kvc_tree_weights_f64) they do not: a weight has the one-token
+ * calls' range and is held to fp32's precision.  The logits are formed again
+ * from the keys (256 bytes per slot): which rows count is known only after the
+ * verification, and keeping all T G logits per slot would move more.
+ * max_len >= len[u].  Device-side errors, which leave the unit's
  * entries untouched: KVC_ERR_SHAPE (len[u] outside [0, max_len], or len[u] +
  * a > cap), KVC_ERR_INVALID_ARG (a outside [0, A], an accepted token that is
  * not live, live tokens outside [0, T]).
@@ -604,6 +607,13 @@ KVC_API kvc_status kvc_tree_weights(const kvc_params *p, int32_t max_len, const 
                                     const uint16_t *q, const uint16_t *k_tree, const float *lse,
                                     const kvc_cache *cache, float *S, void *ws, size_t ws_bytes,
                                     void *stream);
+/* The same with S in fp64 (8-byte aligned), read by kvc_tree_commit_f64. */
+KVC_API kvc_status kvc_tree_weights_f64(const kvc_params *p, int32_t max_len,
+                                        const kvc_tree *tree, const kvc_path *path,
+                                        const float *row_weight, const uint16_t *q,
+                                        const uint16_t *k_tree, const float *lse,
+                                        const kvc_cache *cache, double *S, void *ws,
+                                        size_t ws_bytes, void *stream);
 
 /*
  * kvc_tree_commit -- append the accepted tokens and evict by accumulated
@@ -648,6 +658,14 @@ KVC_API kvc_status kvc_tree_commit(const kvc_params *p, int32_t max_len, const k
                                    const kvc_cache *cache, const kvc_moments *mom, int32_t kmax,
                                    int32_t *evict_idx, int32_t *evict_pos, int32_t *n_evict,
                                    void *ws, size_t ws_bytes, void *stream);
+/* The same with S in fp64 (8-byte aligned; NULL: no refresh). */
+KVC_API kvc_status kvc_tree_commit_f64(const kvc_params *p, int32_t max_len,
+                                       const kvc_tree *tree, const kvc_path *path,
+                                       const uint16_t *k_tree, const uint16_t *v_tree,
+                                       const double *S, const kvc_cache *cache,
+                                       const kvc_moments *mom, int32_t kmax, int32_t *evict_idx,
+                                       int32_t *evict_pos, int32_t *n_evict, void *ws,
+                                       size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------------ */
 /* prefill -> decode hand-off                                           */

@@ -180,13 +180,14 @@ cudaError_t launch_tree_attend(const kvc_params &p, int max_len, const TreeArgs 
                                void *ws, cudaStream_t st);
 cudaError_t launch_tree_weights(const kvc_params &p, int max_len, const TreeArgs &t,
                                 const PathArgs &a, const float *row_weight, const uint16_t *q,
-                                const uint16_t *kt, const float *lse, const kvc_cache &c, float *S,
-                                void *ws, cudaStream_t st);
+                                const uint16_t *kt, const float *lse, const kvc_cache &c, void *S,
+                                bool wide, void *ws, cudaStream_t st);
 cudaError_t launch_tree_commit(const kvc_params &p, int max_len, const TreeArgs &t,
                                const PathArgs &a, const uint16_t *kt, const uint16_t *vt,
-                               const float *S, const kvc_cache &c, const kvc_moments *m, int kmax,
-                               int32_t *evict_idx, int32_t *evict_pos, int32_t *n_evict,
+                               const void *S, bool wide, const kvc_cache &c, const kvc_moments *m,
+                               int kmax, int32_t *evict_idx, int32_t *evict_pos, int32_t *n_evict,
                                const DecodeWs &ws, cudaStream_t st);
+// (S: fp64 when wide, else fp32)
 size_t tree_ws_bytes(const kvc_params &p, int T);
 
 }  // namespace kvc

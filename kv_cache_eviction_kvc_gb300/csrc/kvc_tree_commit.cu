@@ -75,7 +75,7 @@ struct ComArgs {
     TreeArgs t;
     PathArgs p;
     const uint16_t *kt, *vt;
-    const float *S;
+    const void *S;                       // float, or (wide) double
     uint16_t *K, *V;
     int32_t *votes, *pos, *len;
     double *util;
@@ -160,6 +160,21 @@ __device__ __forceinline__ double new_util(const ComArgs &a, double m, float wei
     return fma(a.alpha, m, a.beta * __longlong_as_double((long long)s));
 }
 
+// The same with a weight in fp64, below fp32's range too.
+__device__ __noinline__ double odd_util(int rule, double alpha, double beta, double m, double s)
+{
+    return rule == KVC_RULE_CUMULATIVE ? m + s : fma(alpha, m, beta * s);
+}
+
+__device__ __forceinline__ double new_util(const ComArgs &a, double m, double s)
+{
+    const uint64_t b = (uint64_t)__double_as_longlong(m), w = (uint64_t)__double_as_longlong(s);
+    if (a.rule == KVC_RULE_SINGLE || (b & 0x7fffffffffffffffull) == 0x7ff0000000000000ull) return s;
+    if (a.rule == KVC_RULE_EMA) return fma(a.alpha, m, a.beta * s);
+    if (soft_normal(b) && soft_normal(w)) return __longlong_as_double((long long)soft_add(b, w));
+    return odd_util(a.rule, a.alpha, a.beta, m, s);
+}
+
 // Long units: the utilities of kChunk slots, and the lowest keys of 32 slots
 // each.  A group is what four neighbouring threads have (eight slots each, every
 // kThreads-th), so that little goes between lanes.  grid (chunks, U)
@@ -170,8 +185,10 @@ __device__ __forceinline__ int group_slot(int g, int i)          // the i-th slo
     return g / kGroups * kChunk + 4 * (g % kGroups) + (i & 3) + kThreads * (i >> 2);
 }
 
+template <typename W>
 __global__ void __launch_bounds__(kThreads) tree_update_kernel(ComArgs a)
 {
+    const W *S = static_cast<const W *>(a.S);
     const int u = blockIdx.y, lane = threadIdx.x & 31;
     follow();
     const Plan p = plan_unit(a, u, lane);
@@ -182,17 +199,17 @@ __global__ void __launch_bounds__(kThreads) tree_update_kernel(ComArgs a)
     if (i0 - (int)threadIdx.x >= p.n) return;
     constexpr int kPer = kChunk / kThreads;
     double m[kPer];
-    float s[kPer];
+    W s[kPer];
 #pragma unroll
     for (int j = 0; j < kPer; j++) {
         const int i = i0 + j * kThreads;
         m[j] = i < p.n ? a.util[cb + i] : __longlong_as_double(0x7ff0000000000000ll);
-        s[j] = a.S && i < p.n ? a.S[cb + i] : 0.f;
+        s[j] = S && i < p.n ? S[cb + i] : W(0);
     }
 #pragma unroll
     for (int j = 0; j < kPer; j++) {
         const int i = i0 + j * kThreads;
-        if (a.S && i < p.n) {
+        if (S && i < p.n) {
             m[j] = new_util(a, m[j], s[j]);
             a.util[cb + i] = m[j];
         }
@@ -258,7 +275,7 @@ __device__ __forceinline__ void add_candidate(ComSmem &s, const Key &k)
     if (c < kCand) s.cand[c] = k;
 }
 
-template <int kT, bool kSplit>
+template <int kT, bool kSplit, typename W>
 __global__ void __launch_bounds__(kT, kT > kThreads ? 1 : kSplit ? 2 : 4) tree_commit_kernel(ComArgs a)
 {
     extern __shared__ __align__(16) unsigned char raw[];
@@ -267,17 +284,17 @@ __global__ void __launch_bounds__(kT, kT > kThreads ? 1 : kSplit ? 2 : 4) tree_c
     if (!kSplit) follow();
     const size_t cb = (size_t)u * a.cap;
     double *util = a.util + cb;
-    const float *S = a.S ? a.S + cb : nullptr;
+    const W *S = a.S ? static_cast<const W *>(a.S) + cb : nullptr;
     // four slots a thread on their way while the four before are updated, the first
     // of them before it is known how many there are (what lies behind is not used)
     double m_next[4];
-    float x_next[4];
+    W x_next[4];
     auto load = [&](int i0) {
 #pragma unroll
         for (int j = 0; j < 4; j++) {
             const int i = i0 + j * kT;
             m_next[j] = i < a.cap ? util[i] : 0.;
-            x_next[j] = S && i < a.cap ? S[i] : 0.f;
+            x_next[j] = S && i < a.cap ? S[i] : W(0);
         }
     };
     if (!kSplit) load(tid);
@@ -323,7 +340,7 @@ __global__ void __launch_bounds__(kT, kT > kThreads ? 1 : kSplit ? 2 : 4) tree_c
     } else {
         for (int i0 = tid; i0 < n; i0 += 4 * kT) {
             double m[4];
-            float x[4];
+            W x[4];
 #pragma unroll
             for (int j = 0; j < 4; j++) {
                 m[j] = m_next[j];
@@ -602,13 +619,11 @@ __global__ void __launch_bounds__(kT, kT > kThreads ? 1 : kSplit ? 2 : 4) tree_c
     lead();
 }
 
-}  // namespace
-
-cudaError_t launch_tree_commit(const kvc_params &p, int max_len, const TreeArgs &t,
-                               const PathArgs &pa, const uint16_t *kt, const uint16_t *vt,
-                               const float *S, const kvc_cache &c, const kvc_moments *m, int kmax,
-                               int32_t *evict_idx, int32_t *evict_pos, int32_t *n_evict,
-                               const DecodeWs &ws, cudaStream_t st)
+template <typename W>
+cudaError_t launch(const kvc_params &p, int max_len, const TreeArgs &t, const PathArgs &pa,
+                   const uint16_t *kt, const uint16_t *vt, const void *S, const kvc_cache &c,
+                   const kvc_moments *m, int kmax, int32_t *evict_idx, int32_t *evict_pos,
+                   int32_t *n_evict, const DecodeWs &ws, cudaStream_t st)
 {
     ComArgs a{t, pa, kt, vt, S, c.K, c.V, c.votes, c.pos, c.len, c.util, p.budget,
               m ? m->n : nullptr, m ? m->mu_k : nullptr, m ? m->mu_v : nullptr, m ? m->C : nullptr,
@@ -628,16 +643,28 @@ cudaError_t launch_tree_commit(const kvc_params &p, int max_len, const TreeArgs 
     // A unit that has an SM to itself gets twice the threads: 128 units of 2623 slots on
     // average 12.1 us with 256 and 11.7 with 512, 8 of 131071 19.8 and 18.8.
     const bool wide = p.U <= kSms;
-    auto *kernel = wide ? split ? tree_commit_kernel<2 * kThreads, true> : tree_commit_kernel<2 * kThreads, false>
-                   : split ? tree_commit_kernel<kThreads, true> : tree_commit_kernel<kThreads, false>;
+    auto *kernel = wide ? split ? tree_commit_kernel<2 * kThreads, true, W> : tree_commit_kernel<2 * kThreads, false, W>
+                   : split ? tree_commit_kernel<kThreads, true, W> : tree_commit_kernel<kThreads, false, W>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
     if (e != cudaSuccess) return e;
     if (split) {
         if (p.U > 65535) return cudaErrorInvalidValue;
-        e = launch_following(tree_update_kernel, dim3((max_len + kChunk - 1) / kChunk, p.U), kThreads, 0, st, a);
+        e = launch_following(tree_update_kernel<W>, dim3((max_len + kChunk - 1) / kChunk, p.U), kThreads, 0, st, a);
         if (e != cudaSuccess) return e;
     }
     return launch_following(kernel, dim3(p.U), wide ? 2 * kThreads : kThreads, smem, st, a);
+}
+
+}  // namespace
+
+cudaError_t launch_tree_commit(const kvc_params &p, int max_len, const TreeArgs &t,
+                               const PathArgs &pa, const uint16_t *kt, const uint16_t *vt,
+                               const void *S, bool wide, const kvc_cache &c, const kvc_moments *m,
+                               int kmax, int32_t *evict_idx, int32_t *evict_pos, int32_t *n_evict,
+                               const DecodeWs &ws, cudaStream_t st)
+{
+    return (wide ? launch<double> : launch<float>)(p, max_len, t, pa, kt, vt, S, c, m, kmax, evict_idx,
+                                                   evict_pos, n_evict, ws, st);
 }
 
 }  // namespace kvc

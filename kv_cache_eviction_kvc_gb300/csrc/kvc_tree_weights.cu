@@ -26,8 +26,9 @@
 //   warp 10     walks the CTA's units ahead of the others
 //   warp 11     gathers a unit's accepted rows of q (two buffers when they fit)
 //   warp 12     the accepted tokens' own entries, a few dot products per unit
-//               (mma.sync), unit by unit over the grid
+//               (mma.sync), 16 tokens of a unit at a time over the grid
 // Every wait is bounded (~2 s); a wait that ran out records KVC_ERR_TIMEOUT.
+#include "kvc_soft64.h"
 #include "kvc_tree.h"
 #include "kvc_umma.cuh"
 
@@ -42,6 +43,7 @@ constexpr int kHalf = kSlot / 2;
 constexpr int kMaxRing = 6, kSegs = 3, kMaxRows = kTreeMax * 8;
 constexpr int kThreads = 416;
 constexpr int kProd = 8, kMma = 9, kWalk = 10, kGather = 11, kTail = 12;
+constexpr int kTails = kThreads / 32 - kTail;
 constexpr int kGrid = 152;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -52,10 +54,11 @@ struct WtArgs {
     const uint16_t *q, *kt;
     const float *lse;
     const int32_t *votes, *len;
-    float *S;
+    void *S;                               // float, or (wide) double
     int32_t *status;
     int U, G, gshift, cap, max_len;
     int rows, qbufs, ring, dbufs, dcols;   // rows of q per buffer (a multiple of 16); tiles in flight
+    int blocks;                            // of 16 accepted tokens
     FastDiv by_units;
     float scale;                           // log2(e) / sqrt(d)
 };
@@ -129,6 +132,36 @@ __device__ __forceinline__ float weight(uint32_t x, float scale, float c)
     return c == INFINITY ? 0.f : e;
 }
 
+// S in fp64 holds weights below fp32's range, which a method that orders the slots
+// tells apart.  A sum of fp32 terms above kSmall is good as it is: a term that fp32
+// loses is below 2^-126, 512 of them below 2^-27 of such a sum.  Below it the sum is
+// formed again in units of 2^ref, the whole power of two below its largest term.
+constexpr float kSmall = 0x1p-90f;
+constexpr float kLeast = -1300.f;        // exponents from here down are 0 in fp64
+
+// log2 of a term
+__device__ __forceinline__ float weight_log(uint32_t x, float scale, float c)
+{
+    return c == INFINITY ? -INFINITY : fmaf(__uint_as_float(x), scale, -c);
+}
+
+// v as fp64 (by integer operations: fp64 ones are scarce).
+__device__ __forceinline__ double widen(float v)
+{
+    const uint32_t b = __float_as_uint(v);
+    return (b >> 23) - 1u < 254u ? __longlong_as_double((long long)soft_widen(b)) : (double)v;
+}
+
+// v 2^e for e < 0
+__device__ __forceinline__ double widen(float v, int e)
+{
+    const uint64_t b = soft_widen(__float_as_uint(v));
+    if (v >= 1.f && v < 0x1p100f && (int)(b >> 52) + e >= 1)
+        return __longlong_as_double((long long)b + ((long long)e << 52));
+    return ldexp((double)v, e);
+}
+
+template <bool kWide>
 __global__ void __launch_bounds__(kThreads, 1)
 tree_weights_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CUtensorMap tmK)
 {
@@ -371,56 +404,107 @@ tree_weights_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CU
             __syncwarp();
             if (lane == 0) mbar_arrive(&S.qfull[qb]);
         }
-    } else if (warp == kTail) {
+    } else if (warp >= kTail) {
         // --------------------------------- the accepted tokens' own entries
-        for (int u = blockIdx.x; u < a.U; u += gridDim.x) {
+        // a job: 16 of a unit's accepted tokens
+        for (long long job = blockIdx.x + (long long)gridDim.x * (warp - kTail); job < (long long)a.U * a.blocks;
+             job += (long long)gridDim.x * kTails) {
+            const int u = (int)(job / a.blocks), m0 = 16 * (int)(job - (long long)u * a.blocks);
             int32_t err;
             const int n = a.len[u], acc = unit_acc(a, u, n, &err), b = a.by_units(u);
-            if (acc <= 0) continue;
+            if (acc <= m0) continue;
             const int32_t *tok = a.p.token + (size_t)b * a.p.A;
             const int g = lane >> 2, t = lane & 3, rows = acc * a.G;
-            for (int m0 = 0; m0 < acc; m0 += 16) {           // 16 accepted tokens' keys
-                uint32_t ka[8][4];
-                int c[2];
+            const int t0 = lane < acc ? tok[lane] : 0, t1 = lane + 32 < acc ? tok[lane + 32] : 0;
+            auto token = [&](int j) {                        // the j-th, for every lane its own j
+                const int x = __shfl_sync(kFull, t0, j & 31), y = __shfl_sync(kFull, t1, j & 31);
+                return j < 32 ? x : y;
+            };
+            // eight rows of q: the thread's part of one, and what it needs of its two columns
+            struct Rows {
+                uint32_t q[16];
+                float lse[2], w[2];
+                uint64_t see[2];
+            };
+            auto fetch = [&](Rows &x, int r0) {
+                const int r = min(r0 + g, rows - 1);
+                const uint32_t *p = reinterpret_cast<const uint32_t *>(
+                    a.q + (((size_t)u * a.t.T + token(r >> a.gshift)) * a.G + (r & (a.G - 1))) * kD) + t;
 #pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    c[h] = tok[min(m0 + g + 8 * h, acc - 1)];
-                    const uint32_t *p = reinterpret_cast<const uint32_t *>(
-                        a.kt + ((size_t)u * a.t.T + c[h]) * kD) + t;
+                for (int ks = 0; ks < 16; ks++) x.q[ks] = p[4 * ks];
 #pragma unroll
-                    for (int ks = 0; ks < 8; ks++) {
-                        ka[ks][h] = p[8 * ks];
-                        ka[ks][2 + h] = p[8 * ks + 4];
-                    }
+                for (int e = 0; e < 2; e++) {
+                    const int rr = min(r0 + 2 * t + e, rows - 1), jj = rr >> a.gshift, ct = token(jj);
+                    x.lse[e] = a.lse[((size_t)u * a.t.T + ct) * a.G + (rr & (a.G - 1))];
+                    x.w[e] = a.w ? a.w[(size_t)b * a.p.A + jj] : 1.f;
+                    x.see[e] = r0 + 2 * t + e < rows ? a.t.mask[(size_t)b * a.t.T + ct] : 0;
                 }
-                float sum[2] = {0.f, 0.f};
-                for (int r0 = 0; r0 < rows; r0 += 8) {       // eight rows of q
-                    const int r = min(r0 + g, rows - 1), j = r >> a.gshift;
-                    const uint32_t *p = reinterpret_cast<const uint32_t *>(
-                        a.q + (((size_t)u * a.t.T + tok[j]) * a.G + (r & (a.G - 1))) * kD) + t;
+            };
+            // the 16 tokens' keys
+            uint32_t ka[8][4];
+            int c[2];
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                c[h] = token(min(m0 + g + 8 * h, acc - 1));
+                const uint32_t *p = reinterpret_cast<const uint32_t *>(
+                    a.kt + ((size_t)u * a.t.T + c[h]) * kD) + t;
+#pragma unroll
+                for (int ks = 0; ks < 8; ks++) {
+                    ka[ks][h] = p[8 * ks];
+                    ka[ks][2 + h] = p[8 * ks + 4];
+                }
+            }
+            float sum[2] = {0.f, 0.f}, top[2] = {kLeast, kLeast}, ref[2], low[2] = {0.f, 0.f};
+            // (a second time where a sum is small, in units of its largest term)
+            for (int pass = 0; pass < (kWide ? 2 : 1); pass++) {
+                Rows x, next;
+                fetch(next, 0);
+                for (int r0 = 0; r0 < rows; r0 += 8) {
+                    x = next;
+                    if (r0 + 8 < rows) fetch(next, r0 + 8);
                     float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int ks = 0; ks < 8; ks++)
-                        mma16816(d, ka[ks][0], ka[ks][1], ka[ks][2], ka[ks][3], p[8 * ks], p[8 * ks + 4]);
+                        mma16816(d, ka[ks][0], ka[ks][1], ka[ks][2], ka[ks][3], x.q[2 * ks], x.q[2 * ks + 1]);
 #pragma unroll
-                    for (int e = 0; e < 2; e++) {            // the columns of the thread
-                        const int rr = r0 + 2 * t + e, jj = rr >> a.gshift;
-                        if (rr >= rows) continue;
-                        const int ct = tok[jj];
-                        const float cr = row_c(a, a.lse[((size_t)u * a.t.T + ct) * a.G + (rr & (a.G - 1))],
-                                               a.w ? a.w[(size_t)b * a.p.A + jj] : 1.f);
-                        const uint64_t see = a.t.mask[(size_t)b * a.t.T + ct];
+                    for (int e = 0; e < 2; e++) {
+                        const float cr = row_c(a, x.lse[e], x.w[e]);
 #pragma unroll
-                        for (int h = 0; h < 2; h++)
-                            if (see >> c[h] & 1) sum[h] += weight(__float_as_uint(d[2 * h + e]), a.scale, cr);
+                        for (int h = 0; h < 2; h++) {
+                            if (!(x.see[e] >> c[h] & 1)) continue;
+                            const uint32_t y = __float_as_uint(d[2 * h + e]);
+                            if (!kWide || pass == 0) sum[h] += weight(y, a.scale, cr);
+                            if (kWide && pass == 0) top[h] = fmaxf(top[h], weight_log(y, a.scale, cr));
+                            if (kWide && pass == 1) low[h] += ex2_approx(weight_log(y, a.scale, cr) - ref[h]);
+                        }
                     }
                 }
+                if (!kWide) break;
+                bool again = false;
 #pragma unroll
                 for (int h = 0; h < 2; h++) {
-                    sum[h] += __shfl_xor_sync(kFull, sum[h], 1);
-                    sum[h] += __shfl_xor_sync(kFull, sum[h], 2);
-                    if (t == 0 && m0 + g + 8 * h < acc) a.S[(size_t)u * a.cap + n + m0 + g + 8 * h] = sum[h];
+                    if (pass == 1) continue;
+                    for (int x = 1; x < 4; x <<= 1) {
+                        sum[h] += __shfl_xor_sync(kFull, sum[h], x);
+                        top[h] = fmaxf(top[h], __shfl_xor_sync(kFull, top[h], x));
+                    }
+                    ref[h] = floorf(top[h]);
+                    again |= m0 + g + 8 * h < acc && sum[h] < kSmall;
                 }
+                if (!__any_sync(kFull, again)) break;
+            }
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                float &of = kWide ? low[h] : sum[h];
+                of += __shfl_xor_sync(kFull, of, 1);
+                of += __shfl_xor_sync(kFull, of, 2);
+                if (t != 0 || m0 + g + 8 * h >= acc) continue;
+                const size_t to = (size_t)u * a.cap + n + m0 + g + 8 * h;
+                if (kWide)
+                    static_cast<double *>(a.S)[to] =
+                        sum[h] < kSmall ? widen(low[h], (int)ref[h]) : widen(sum[h]);
+                else
+                    static_cast<float *>(a.S)[to] = sum[h];
             }
         }
     } else {
@@ -449,7 +533,7 @@ tree_weights_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CU
                 ok = __all_sync(kFull, tree_wait(&S.dfull[db], (kk / a.dbufs) & 1, &S.bad));
                 if (!ok) break;
                 tc_fence_after();
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                float sum[4] = {0.f, 0.f, 0.f, 0.f}, top[2] = {kLeast, kLeast};
 #pragma unroll 1
                 for (int c0 = 0; c0 < cols; c0 += 16) {
                     uint32_t y[16];
@@ -465,12 +549,38 @@ tree_weights_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CU
                         sum[1] += weight(y[4 * j + 1], a.scale, c[j].y);
                         sum[2] += weight(y[4 * j + 2], a.scale, c[j].z);
                         sum[3] += weight(y[4 * j + 3], a.scale, c[j].w);
+                        if (kWide) {
+                            top[0] = fmaxf(fmaxf(top[0], weight_log(y[4 * j], a.scale, c[j].x)),
+                                           weight_log(y[4 * j + 1], a.scale, c[j].y));
+                            top[1] = fmaxf(fmaxf(top[1], weight_log(y[4 * j + 2], a.scale, c[j].z)),
+                                           weight_log(y[4 * j + 3], a.scale, c[j].w));
+                        }
                     }
                 }
+                const float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                const float ref = floorf(fmaxf(top[0], top[1]));
+                float low = 0.f;
+                if (kWide && __any_sync(kFull, at < s.n && all < kSmall))
+#pragma unroll 1
+                    for (int c0 = 0; c0 < cols; c0 += 16) {
+                        uint32_t y[16];
+                        tmem_ld16_async(tmem + lanes + db * a.dcols + c0, y);
+                        tmem_wait_ld();
+                        tmem_bind16(y);
+#pragma unroll
+                        for (int j = 0; j < 16; j++)
+                            low += ex2_approx(weight_log(y[j], a.scale, S.c[qb][c0 + j]) - ref);
+                    }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&S.dempty[db]);
-                if (at < s.n) a.S[slot] = ((sum[0] + sum[1]) + (sum[2] + sum[3])) * vote;
+                if (at < s.n) {
+                    if (kWide)
+                        static_cast<double *>(a.S)[slot] =
+                            all < kSmall ? widen(low * vote, (int)ref) : widen(all * vote);
+                    else
+                        static_cast<float *>(a.S)[slot] = all * vote;
+                }
             }
             k += s.tiles;
             __syncwarp();
@@ -487,8 +597,8 @@ tree_weights_kernel(const __grid_constant__ WtArgs a, const __grid_constant__ CU
 
 cudaError_t launch_tree_weights(const kvc_params &p, int max_len, const TreeArgs &t,
                                 const PathArgs &pa, const float *row_weight, const uint16_t *q,
-                                const uint16_t *kt, const float *lse, const kvc_cache &c, float *S,
-                                void *ws, cudaStream_t st)
+                                const uint16_t *kt, const float *lse, const kvc_cache &c, void *S,
+                                bool wide, void *ws, cudaStream_t st)
 {
     const long long tmax = (max_len + kTile - 1) / kTile, tiles = p.U * tmax;
     if (tiles > 0x7fffffffll) return cudaErrorInvalidValue;
@@ -497,6 +607,7 @@ cudaError_t launch_tree_weights(const kvc_params &p, int max_len, const TreeArgs
     WtArgs a{t, pa, row_weight, q, kt, lse, c.votes, c.len, S, static_cast<int32_t *>(ws), p.U, p.G,
              p.G == 1 ? 0 : p.G == 2 ? 1 : p.G == 4 ? 2 : 3, p.cap, max_len};
     a.rows = (pa.A * p.G + 15) & ~15;
+    a.blocks = (pa.A + 15) / 16;
     a.qbufs = a.rows <= 128 ? 2 : 1;
     a.dcols = a.rows <= 128 ? 128 : a.rows <= 256 ? 256 : 512;
     a.dbufs = 512 / a.dcols;
@@ -506,12 +617,12 @@ cudaError_t launch_tree_weights(const kvc_params &p, int max_len, const TreeArgs
     a.scale = kLog2e / sqrtf((float)kD);
     const size_t smem = (size_t)a.ring * kSlot + (size_t)a.qbufs * a.rows * 256 + sizeof(WtSmem);
     // (the attribute is the kernel's, shared by the host's threads: never one call's size)
-    cudaError_t e = cudaFuncSetAttribute(tree_weights_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kMostSmem);
+    auto *kernel = wide ? tree_weights_kernel<true> : tree_weights_kernel<false>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
     if (e != cudaSuccess) return e;
     long long grid = tiles > p.U ? tiles : p.U;
     if (grid > kGrid) grid = kGrid;
-    return launch_following(tree_weights_kernel, dim3((unsigned)grid), kThreads, smem, st, a, mk);
+    return launch_following(kernel, dim3((unsigned)grid), kThreads, smem, st, a, mk);
 }
 
 }  // namespace kvc

@@ -33,6 +33,7 @@ EXPORTED = (
     "kvc_prefill_workspace_size", "kvc_prefill_score", "kvc_prefill_window_attention",
     "kvc_prefill_snapkv", "kvc_prefill_handoff_workspace_size", "kvc_prefill_handoff",
     "kvc_tree_workspace_size", "kvc_tree_attend", "kvc_tree_weights", "kvc_tree_commit",
+    "kvc_tree_weights_f64", "kvc_tree_commit_f64",
 )
 
 
@@ -124,6 +125,8 @@ def load(build: bool = True):
         "kvc_tree_weights": (I32, [PP, I32, PT, PA, P, P, P, P, PC, P, P, SZ, P]),
         "kvc_tree_commit": (I32, [PP, I32, PT, PA, P, P, P, PC, PM, I32, P, P, P, P, SZ, P]),
     }
+    for name in ("kvc_tree_weights", "kvc_tree_commit"):
+        sigs[name + "_f64"] = sigs[name]
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
         fn.restype = res
@@ -323,8 +326,8 @@ def kvc_decode_attend_noalloc(p, t, new_pos, max_len, q, k_new, v_new, cache: kv
 
 # ------------------------------------------------------------------ drafted tokens
 
-_BF16, _F32, _I32, _U8, _Tensor = (torch.bfloat16, torch.float32, torch.int32, torch.uint8,
-                                    torch.Tensor)
+_BF16, _F32, _F64, _I32, _U8, _Tensor = (torch.bfloat16, torch.float32, torch.float64, torch.int32,
+                                          torch.uint8, torch.Tensor)
 
 
 def _sized(t, dtype, name, numel, device, optional=False):
@@ -420,32 +423,35 @@ def kvc_tree_attend(p, max_len, tree: kvc_tree, q, k_tree, v_tree, cache: kvc_ca
 
 def kvc_tree_weights(p, max_len, tree: kvc_tree, path: kvc_path, row_weight, q, k_tree, lse,
                      cache: kvc_cache, S, ws, stream=None):
-    """row_weight: fp32 [trees][A] or None (all 1)."""
+    """row_weight: fp32 [trees][A] or None (all 1).  S: fp64 [U][cap], or fp32
+    (weights below its range are 0)."""
     U, G, d = p.U, p.G, p.d
     dev = _tree_device(U, tree, path)
     rows = U * tree.T
     weights = None
     if row_weight is not None:
         weights = _sized(row_weight, _F32, "row_weight", U // tree.units * path.A, dev)
-    _check(load().kvc_tree_weights(
+    lib, wide = load(), getattr(S, "dtype", None) is _F64
+    _check((lib.kvc_tree_weights_f64 if wide else lib.kvc_tree_weights)(
         _ref(p), int(max_len), _ref(tree), _ref(path), weights,
         _sized(q, _BF16, "q", rows * G * d, dev), _sized(k_tree, _BF16, "k_tree", rows * d, dev),
         _sized(lse, _F32, "lse", rows * G, dev), _ref(cache),
-        _sized(S, _F32, "S", U * p.cap, dev), _sized(ws, _U8, "ws", 0, dev), ws.numel(),
+        _sized(S, _F64 if wide else _F32, "S", U * p.cap, dev), _sized(ws, _U8, "ws", 0, dev), ws.numel(),
         _stream_on(stream, dev)))
 
 
 def kvc_tree_commit(p, max_len, tree: kvc_tree, path: kvc_path, k_tree, v_tree, S,
                     cache: kvc_cache, mom, kmax, evict_idx, evict_pos, n_evict, ws, stream=None):
-    """S: fp32 [U][cap] from kvc_tree_weights or None (no refresh); mom:
+    """S: [U][cap] from kvc_tree_weights (fp64 or fp32) or None (no refresh); mom:
     kvc_moments or None; evict_idx, evict_pos: int32 [U][kmax] or None."""
     U, kmax = p.U, int(kmax)
     dev = _tree_device(U, tree, path)
     n = U * tree.T * p.d
-    _check(load().kvc_tree_commit(
+    lib, wide = load(), getattr(S, "dtype", None) is _F64
+    _check((lib.kvc_tree_commit_f64 if wide else lib.kvc_tree_commit)(
         _ref(p), int(max_len), _ref(tree), _ref(path),
         _sized(k_tree, _BF16, "k_tree", n, dev), _sized(v_tree, _BF16, "v_tree", n, dev),
-        None if S is None else _sized(S, _F32, "S", U * p.cap, dev), _ref(cache),
+        None if S is None else _sized(S, _F64 if wide else _F32, "S", U * p.cap, dev), _ref(cache),
         None if mom is None else _ref(mom), kmax,
         None if evict_idx is None else _sized(evict_idx, _I32, "evict_idx", U * kmax, dev),
         None if evict_pos is None else _sized(evict_pos, _I32, "evict_pos", U * kmax, dev),

@@ -194,7 +194,9 @@ class DecodeState:
                 raise ValueError(f"no trees of T = {T} tokens")
             dev = self.device
             if not trees:
-                self.tree_S = torch.zeros(self.U, self.cap, dtype=torch.float32, device=dev)
+                # fp64, as the utilities: over sharp attention most weights are below
+                # fp32's range, and the victims go by their order
+                self.tree_S = torch.zeros(self.U, self.cap, dtype=torch.float64, device=dev)
                 self._tree_evict = torch.full((2 * self.U * K_.TREE_MAX,), -1, dtype=torch.int32,
                                               device=dev)
             trees[T] = dict(

@@ -1094,3 +1094,162 @@ def test_first_verify_on_another_stream(handle):
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     again.accept(tree, path, *args, L)
     assert torch.equal(S, again.tree_S) and (ev[0] >= 0).all()
+
+
+# ------------------------------------------------------- weights below fp32's range
+
+def wide_weights(c, u, w):
+    """R.weights' sums and their bound without what fp32's range takes: every
+    error is relative to its term (the logit's, the logarithms', and 16 half
+    steps for the powers of two that the sum is held in)."""
+    b, a, n, G = u // c.per, c.counts[u // c.per], c.lens[u], c.G
+    path = [int(x) for x in c.tok[b, :a]]
+    S, e_S = np.zeros(n + a), np.zeros(n + a)
+    keys, lse = np.concatenate([c.K[u, :n], c.kt[u, path]]), f64(c.lse[u])
+    for j, t in enumerate(path):
+        see = [int(c.mask[b, t]) >> r & 1 for r in path]
+        for h in range(G):
+            if lse[t, h] == -np.inf:
+                continue
+            x = keys @ c.q[u, t, h] * R.SCALE
+            e = np.exp(x - lse[t, h])
+            if c.votes is not None:
+                e[:n] *= c.votes[u, :n]
+            e[n:] = np.where(see, e[n:], 0.0)
+            e *= w[j] / G
+            S += e
+            e_S += e * (R.logit_error(c.q[u, t, h], keys) + 8 * R.E32 * (
+                np.abs(x) + abs(lse[t, h]) + 2 + abs(np.log(w[j] / G))))
+    return S, e_S + (a * G + 32) * R.E32 * S
+
+
+WIDE = [
+    # per, G, T, lens, counts, A, keywords
+    (1, 1, 1, [0, 1, 2], [1, 1, 0], 1, {}),
+    (2, 4, 7, [127, 128, 129, 0], [3, 2], 3, dict(q_scale=30.0)),
+    (2, 8, 5, [255, 256, 257, 300], [5, 1], 5, dict(votes=True, q_scale=25.0)),
+    (1, 2, 64, [130, 1, 400], [64, 64, 7], 64, dict(kind="chain", q_scale=12.0)),
+    (1, 8, 64, [200, 129], [64, 30], 64, dict(kind="chain", q_scale=40.0)),
+    (1, 4, 6, [0, 0, 5], [2, 3, 1], 3, dict(kind="none")),
+    (4, 1, 24, [100, 200, 300, 400] * 45, [i % 7 for i in range(45)], 6, dict(q_scale=60.0)),
+    (1, 4, 9, [700], [5], 5, dict(q_scale=90.0, votes=True)),
+]
+
+
+@pytest.mark.parametrize("given", [False, True])
+@pytest.mark.parametrize("i", range(len(WIDE)))
+def test_weights_f64(i, given):
+    """Logits up to several hundred apart: every weight down to 2^-1000 is
+    there, to fp32's precision of its logit."""
+    per, G, T, lens, counts, A, kw = WIDE[i]
+    c = Case(500 + i, per, G, T, lens, **kw)
+    c.path(counts, A)
+    c.run_attend()
+    w = (2.0 ** c.rng.uniform(-40, 1, (c.B, A))).astype(np.float32) if given else np.ones((c.B, A), np.float32)
+    S = torch.full((c.U, c.cap), -3.0, device=DEV, dtype=torch.float64)
+    K.kvc_tree_weights(c.p, c.max_len, c.tree, c.accept, torch.from_numpy(w).to(DEV) if given else None,
+                       c.t["q"], c.t["kt"], c.lse, c.cache, S, c.ws)
+    assert K.kvc_get_device_status(c.ws) == 0
+    S = f64(S)
+    for u in range(c.U):
+        b = u // per
+        n = lens[u] + counts[b]
+        ref, bound = wide_weights(c, u, w[b].astype(np.float64))
+        there = ref > 2.0 ** -1000
+        assert (np.abs(S[u, :n] - ref)[there] <= bound[there]).all(), (
+            u, (np.abs(S[u, :n] - ref)[there] / bound[there]).max())
+        assert (S[u, :n][~there] <= 2.0 ** -999).all() and (S[u, :n][~there] >= 0).all()
+        assert (S[u, n:] == -3).all()
+    if kw.get("q_scale", 0) >= 60:
+        assert (S[(S > 0)] < 2.0 ** -150).any()
+
+
+def test_weights_f64_are_the_fp32_ones_where_those_hold():
+    c = Case(520, 2, 4, 9, [700, 90, 33, 400], votes=True)
+    c.path([4, 2], 4)
+    c.run_attend()
+    S = [torch.full((c.U, c.cap), -3.0, device=DEV, dtype=t) for t in (torch.float32, torch.float64)]
+    for x in S:
+        K.kvc_tree_weights(c.p, c.max_len, c.tree, c.accept, None, c.t["q"], c.t["kt"], c.lse, c.cache,
+                           x, c.ws)
+    assert (S[0] != 0).all() and torch.equal(S[0].double(), S[1])
+
+
+@pytest.mark.parametrize("n,U", [(300, 2), (9000, 2), (5000, 1), (257, 400), (8300, 160)])
+@pytest.mark.parametrize("rule", ["single", "cumulative", "ema"])
+def test_commit_f64(rule, n, U):
+    """Weights all over fp64's range, every way the work is cut: utilities as
+    IEEE arithmetic gives them, and the victims that follow from them."""
+    rng = np.random.default_rng(530)
+    cap = n + 6
+    S = np.exp2(rng.uniform(-800, 4, (U, cap)))
+    old = np.exp2(rng.uniform(-800, 4, (U, cap)))
+    old[rng.random(old.shape) < 0.1] = np.inf
+    odd = [(0.0, 0.0), (0.0, 1.5), (0.25, 0.0), (5e-324, 5e-324), (1e-310, 1e-320), (1e300, 1.0),
+           (-1.5, 1.5), (-1.5, 0.25), (1.0, 5e-324), (1.0, 3e38), (1.0, 2.0 ** -53),
+           (1 + 2.0 ** -52, 2.0 ** -53), (2 - 2.0 ** -52, 2.0 ** -53), (2.0 ** -53, 2.0 ** 60)]
+    for i, (x, y) in enumerate(odd):
+        old[:, 200 + i], S[:, 200 + i] = x, y
+    pos = np.stack([rng.permutation(cap) for _ in range(U)]).astype(np.int32)
+    util, dpos = torch.from_numpy(old).to(DEV), torch.from_numpy(pos).to(DEV)
+    rows = torch.zeros(U, cap, 128, dtype=torch.bfloat16, device=DEV)
+    length = torch.full((U,), n, dtype=torch.int32, device=DEV)
+    code = {"single": K.RULE_SINGLE, "cumulative": K.RULE_CUMULATIVE, "ema": K.RULE_EMA}[rule]
+    p = K.make_params(U, 1, cap, n, rule=code, alpha=0.75)
+    tree, path = _chain(4, U, [0, 1, 2], 3, cap)
+    new = torch.zeros(U, 4, 128, dtype=torch.bfloat16, device=DEV)
+    ei, ep = (torch.full((U, 3), -9, dtype=torch.int32, device=DEV) for _ in range(2))
+    ne = torch.full((U,), -9, dtype=torch.int32, device=DEV)
+    dws = torch.empty(K.kvc_decode_workspace_size(p), dtype=torch.uint8, device=DEV)
+    K.kvc_decode_workspace_init(p, dws)
+    K.kvc_tree_commit(p, n, tree, path, new, new, torch.from_numpy(S).to(DEV),
+                      K.make_cache(rows, rows, None, dpos, util, length), None, 3, ei, ep, ne, dws)
+    assert K.kvc_get_device_status(dws) == 0 and (ne == 3).all() and (length == n).all()
+    m, s, R_ = old[:, :n], S[:, :n], U
+    with np.errstate(invalid="ignore"):
+        if rule == "ema":
+            # alpha and 1 - alpha are exact: the product of the weight is rounded, then the whole
+            R_ = min(U, 2)
+            upd = np.array([[float(Fraction(0.75) * Fraction(x) + Fraction(0.25 * y)) if np.isfinite(x)
+                             else y for x, y in zip(a, b)] for a, b in zip(m[:R_], s[:R_])])
+        else:
+            upd = s if rule == "single" else np.where(np.isinf(m), s, m + s)
+    every = np.concatenate([upd, S[:R_, n:n + 3]], 1)
+    where = np.concatenate([pos[:R_, :n], np.tile(cap + np.arange(3), (R_, 1))], 1)
+    low = np.sort(np.lexsort((where, every))[:, :3], 1)
+    assert np.array_equal(low, ei[:R_].cpu().numpy())
+    assert np.array_equal(np.take_along_axis(where, low, 1), ep[:R_].cpu().numpy())
+    keep = np.ones((R_, n + 3), dtype=bool)
+    np.put_along_axis(keep, low, False, 1)                 # a victim's place is another's now
+    keep = keep[:, :n]
+    assert np.array_equal(f64(util)[:R_, :n][keep], upd[keep])
+
+
+@pytest.mark.parametrize("rule", [K.RULE_SINGLE, K.RULE_CUMULATIVE, K.RULE_EMA])
+def test_sharp_attention_evicts_what_decode_steps_evict(rule):
+    """Logits some hundred apart: the weights of most slots are far below
+    fp32's range, and verify / accept of one token at a time evict the same
+    positions as the one-token calls, which order them."""
+    U, G, n, L = 6, 4, 300, 280
+    a, rnd = _stream(8, U, G, n, n + 4, L, 8)
+    b, _ = _stream(8, U, G, n, n + 4, L, 8)
+    a.params.rule = b.params.rule = rule
+    one = torch.ones(1, 1, dtype=torch.int64, device=DEV)
+    zero = torch.zeros(1, 1, dtype=torch.int32, device=DEV)
+    low = 0
+    for t in range(1, 13):
+        q, k, v = (60 * rnd(U, G, 128)).bfloat16(), rnd(U, 128).bfloat16(), rnd(U, 128).bfloat16()
+        max_len = n + 1 if t == 1 else L + 1
+        b.step_calls(t, n + t - 1, q, k, v, max_len)
+        if t == 1:
+            a.step_calls(t, n + t - 1, q, k, v, max_len)
+            continue
+        tree = K.make_tree(1, U, one)
+        path = K.make_path(1, zero, torch.ones(1, dtype=torch.int32, device=DEV),
+                           torch.full((1,), n + t - 1, dtype=torch.int32, device=DEV))
+        a.verify(tree, q, k, v, L)
+        a.accept(tree, path, q, k, v, L)
+        assert a.tree_status() == 0 and a.device_status() == 0
+        low += int((b.probs[:, :L] < 2.0 ** -150).sum())
+        assert torch.equal(a.tree_evict[1][:, 0], b.evict_pos[:, 0]), t
+    assert low > U * L                                     # one in eleven of the weights at least

@@ -103,3 +103,33 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         K.make_tree(8, 2, None)
     with pytest.raises(ValueError):
         K.make_path(3, torch.zeros(2, 4, dtype=torch.int32), mask, mask)
+
+
+def wide(call, name):
+    """The fp64 form takes what the fp32 form takes: its refusals by the same arguments."""
+    lib = K.load()
+    old = getattr(lib, name)
+    setattr(lib, name, getattr(lib, name + "_f64"))
+    try:
+        return call()
+    finally:
+        setattr(lib, name, old)
+
+
+@pytest.mark.parametrize("kw,code", [
+    ({"d": 64}, 5), ({"G": 3}, 5), ({"U": 0}, 1), ({"L": 100}, 1), ({"K": None}, 1), ({"max_len": 0}, 2),
+    ({"max_len": 101}, 2), ({"T": 65}, 5), ({"units": 3}, 1), ({"mask": None}, 1), ({"kt": 264}, 1),
+    ({"A": 9}, 1), ({"token": None}, 1), ({"ws": None}, 6), ({"ws_bytes": 255}, 6)])
+@pytest.mark.parametrize("call,name", [(weights, "kvc_tree_weights"), (commit, "kvc_tree_commit")])
+def test_f64_forms_refuse_the_same(call, name, kw, code):
+    assert wide(lambda: call(**kw), name) == code
+    assert name + "_f64" in K.kvc_last_error() or code in (1, 5)
+
+
+def test_f64_weights_must_be_aligned():
+    assert wide(lambda: weights(S=260), "kvc_tree_weights") == 1
+    p, c, t, a, m = _args()
+    assert K.load().kvc_tree_commit_f64(
+        ctypes.byref(p), 10, ctypes.byref(t), ctypes.byref(a), 256, 256, 260, ctypes.byref(c),
+        ctypes.byref(m), 3, None, None, 256, 256, BIG, None) == 1
+    assert "S must be" in K.kvc_last_error()
