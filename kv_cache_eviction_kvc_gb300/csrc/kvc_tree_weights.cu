@@ -19,13 +19,13 @@
 // clocks, the bandwidth's; what is left is the start (about 6 us until the first
 // product: lengths, paths, query rows).
 //
-// 416 threads:
+// 512 threads:
 //   warps 0-7   two groups on alternate tiles, a thread per slot
 //   warp 8      producer (TMA, a ring of 32 KB key tiles)
 //   warp 9      tensor-memory owner and MMA issuer (up to four tiles ahead)
 //   warp 10     walks the CTA's units ahead of the others
 //   warp 11     gathers a unit's accepted rows of q (two buffers when they fit)
-//   warp 12     the accepted tokens' own entries, a few dot products per unit
+//   warps 12-15 the accepted tokens' own entries, a few dot products per unit
 //               (mma.sync), 16 tokens of a unit at a time over the grid
 // Every wait is bounded (~2 s); a wait that ran out records KVC_ERR_TIMEOUT.
 #include "kvc_soft64.h"
@@ -41,7 +41,7 @@ constexpr int kTile = 128;
 constexpr int kSlot = kTile * kD * 2;            // 32 KB: a tile of keys
 constexpr int kHalf = kSlot / 2;
 constexpr int kMaxRing = 6, kSegs = 3, kMaxRows = kTreeMax * 8;
-constexpr int kThreads = 416;
+constexpr int kThreads = 512;
 constexpr int kProd = 8, kMma = 9, kWalk = 10, kGather = 11, kTail = 12;
 constexpr int kTails = kThreads / 32 - kTail;
 constexpr int kGrid = 152;
