@@ -1253,3 +1253,89 @@ def test_sharp_attention_evicts_what_decode_steps_evict(rule):
         low += int((b.probs[:, :L] < 2.0 ** -150).sum())
         assert torch.equal(a.tree_evict[1][:, 0], b.evict_pos[:, 0]), t
     assert low > U * L                                     # one in eleven of the weights at least
+
+
+# ---------------------------------------------------- ways of the work seldom taken
+
+LAYOUTS = {
+    "whole, both groups": (2, 4, 9, [300, 45, 128, 700] * 2, dict(live=[9, 4, 9, 2])),
+    "whole, moments": (2, 4, 9, [300, 45, 128, 700] * 2, dict(live=[9, 4, 9, 2], moments=True, votes=True)),
+    "two halves of rows": (1, 4, 63, [300, 0, 130], {}),
+    "two halves, moments": (1, 4, 63, [300, 0, 130], dict(moments=True)),
+    "parts of a unit": (1, 2, 12, [4000, 130, 5, 0, 2050], {}),
+    "parts of a unit, moments": (1, 2, 12, [4000, 130, 5, 0, 2050], dict(votes=True, moments=True)),
+    "parts, two halves, two blocks": (1, 8, 40, [2900, 1, 260], dict(moments=True)),
+    "line": (4, 2, 12, [(37 * i * i) % 2100 for i in range(160)], {}),
+    "line, moments": (4, 2, 12, [(37 * i * i) % 2100 for i in range(160)], dict(votes=True, moments=True)),
+}
+
+
+@pytest.mark.parametrize("value", [NAN, float("inf"), -float("inf")])
+@pytest.mark.parametrize("layout", list(LAYOUTS))
+def test_attend_masked_branch_in_every_layout(layout, value):
+    """One value (then one key) of every tree's token 1 is not finite: what a
+    row that sees the token gets is not finite in that dimension (for a key,
+    in any), everything else is as it was to the bit."""
+    per, G, T, lens, kw = LAYOUTS[layout]
+    c = Case(600, per, G, T, lens, kind="tree", **kw)
+    o, lse = (x.clone() for x in c.run_attend())
+    see = torch.zeros(c.U, T, dtype=torch.bool, device=DEV)
+    for u in range(c.U):
+        for t in range(c.live[u // per]):
+            see[u, t] = bool(int(c.mask[u // per, t]) >> 1 & 1)
+    assert see.any() and not see.all()
+    hit = torch.zeros_like(o, dtype=torch.bool)
+    hit[..., 5] = see[:, :, None]
+    keep = c.t["vt"][:, 1, 5].clone()
+    c.t["vt"][:, 1, 5] = value
+    got, got_lse = c.run_attend()
+    assert K.kvc_get_device_status(c.ws) == 0
+    assert torch.equal(got_lse, lse) and torch.equal(got[~hit], o[~hit])
+    assert not torch.isfinite(got[hit]).any()
+    c.t["vt"][:, 1, 5] = keep
+    c.t["kt"][:, 1, 5] = NAN
+    got, got_lse = c.run_attend()
+    assert K.kvc_get_device_status(c.ws) == 0
+    assert torch.equal(got[~see], o[~see]) and torch.equal(got_lse[~see], lse[~see])
+    assert torch.isnan(got[see]).all() and torch.isnan(got_lse[see]).all()
+
+
+@pytest.mark.parametrize("n,U", [(20000, 2), (20000, 60), (1500, 160), (9000, 160), (20000, 153)])
+@pytest.mark.parametrize("ties", ["zero", "few", "stride", "one group"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float64])
+def test_commit_ties_of_long_and_of_many_units(ties, n, U, dtype):
+    """More slots at the bound than there are places for, in long units and
+    where a unit has half the threads: the lowest (weight, position, slot)."""
+    rng = np.random.default_rng(640)
+    k, cap = 40, n + 41
+    S = np.zeros((U, cap))
+    if ties == "few":
+        S = rng.integers(0, 3, S.shape).astype(np.float64)
+    elif ties == "stride":
+        S = 1 + rng.integers(0, 1000, S.shape) / 1024
+        S[:, ::512] = 0.25
+        S[:, 1:3000:3] = 0.5
+    elif ties == "one group":                              # the lowest sit side by side
+        S = 1 + rng.integers(0, 1000, S.shape) / 1024
+        S[:, 256:290] = 0.25
+        S[:, 1000:1003] = 0.125
+    pos = np.stack([rng.permutation(cap) for _ in range(U)]).astype(np.int32)
+    pos[:, 5] = pos[:, 3]                                  # a tie of the positions too
+    util = torch.zeros(U, cap, dtype=torch.float64, device=DEV)
+    rows = torch.zeros(U, cap, 128, dtype=torch.bfloat16, device=DEV)
+    length = torch.full((U,), n, dtype=torch.int32, device=DEV)
+    p = K.make_params(U, 1, cap, n, rule=K.RULE_SINGLE)
+    tree, path = _chain(k, U, list(range(k)), k, cap)
+    new = torch.zeros(U, k, 128, dtype=torch.bfloat16, device=DEV)
+    ei, ep = (torch.full((U, k), -9, dtype=torch.int32, device=DEV) for _ in range(2))
+    ne = torch.full((U,), -9, dtype=torch.int32, device=DEV)
+    dws = torch.empty(K.kvc_decode_workspace_size(p), dtype=torch.uint8, device=DEV)
+    K.kvc_decode_workspace_init(p, dws)
+    K.kvc_tree_commit(p, n, tree, path, new, new, torch.from_numpy(S).to(DEV, dtype),
+                      K.make_cache(rows, rows, None, torch.from_numpy(pos).to(DEV), util, length), None,
+                      k, ei, ep, ne, dws)
+    assert K.kvc_get_device_status(dws) == 0 and (ne == k).all() and (length == n).all()
+    where = np.concatenate([pos[:, :n], np.tile(cap + np.arange(k), (U, 1))], 1)
+    low = np.sort(np.lexsort((where, S[:, :n + k]))[:, :k], 1)
+    assert np.array_equal(low, ei.cpu().numpy())
+    assert np.array_equal(np.take_along_axis(where, low, 1), ep.cpu().numpy())
