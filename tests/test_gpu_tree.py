@@ -1339,3 +1339,95 @@ def test_commit_ties_of_long_and_of_many_units(ties, n, U, dtype):
     low = np.sort(np.lexsort((where, S[:, :n + k]))[:, :k], 1)
     assert np.array_equal(low, ei.cpu().numpy())
     assert np.array_equal(np.take_along_axis(where, low, 1), ep.cpu().numpy())
+
+
+def test_lazy_steps_around_a_commit():
+    """Between lazy steps a commit moves the lowest slots about: the victims
+    that the refresh step queued are dropped, and the fused step takes the
+    ones that the call sequence takes."""
+    U, G, n, L, T = 6, 4, 90, 64, 6
+    a, rnd = _stream(9, U, G, n, n + 12, L, 8)
+    b, _ = _stream(9, U, G, n, n + 12, L, 8)
+    a.params.refresh_period = b.params.refresh_period = 6
+    pos = n
+    for t in range(1, 25):
+        q, k, v = rnd(U, G, 128).bfloat16(), rnd(U, 128).bfloat16(), rnd(U, 128).bfloat16()
+        max_len = n + 1 if t == 1 else L + 1
+        (a.step_calls if t == 1 else a.step)(t, pos, q, k, v, max_len)
+        b.step_calls(t, pos, q, k, v, max_len)
+        pos += 1
+        assert torch.equal(a.n_evict, b.n_evict)
+        assert torch.equal(a.evict_pos, b.evict_pos), t
+        if t % 3 == 0:
+            tree, path = _chain(T, U, [0, 1, 2], 1 + t % 2, pos)
+            args = rnd(U, T, G, 128).bfloat16(), rnd(U, T, 128).bfloat16(), rnd(U, T, 128).bfloat16()
+            for x in (a, b):
+                x.verify(tree, *args, L)
+                x.accept(tree, path, *args, L, refresh=t % 2 == 0)
+                assert x.tree_status() == 0
+            pos += 1 + t % 2
+            assert torch.equal(a.tree_evict, b.tree_evict)
+        assert a.device_status() == 0 and b.device_status() == 0
+        assert torch.equal(a.pos[:, :L].sort(1)[0], b.pos[:, :L].sort(1)[0])
+
+
+@pytest.mark.parametrize("budgets", [False, True])
+def test_state_run_in_a_graph(budgets):
+    """verify and accept captured once, replayed over new inputs and new
+    paths: what the calls give outside a graph, with a budget of the state
+    and with one per unit."""
+    U, per, G, L, T, A = 8, 4, 4, 200, 7, 4
+    rng = np.random.default_rng(3)
+
+    def make():
+        st, rnd = _stream(10, U, G, L, L + 12, L, 1, budgets=budgets)
+        if budgets:
+            lens = torch.tensor([L, 150, 3, 77, L - 1, 128, 129, 1], dtype=torch.int32, device=DEV)
+            st.len.copy_(lens)
+            st.budget.copy_(lens)
+        st.util.copy_(torch.rand(U, L + 12, dtype=torch.float64, device=DEV,
+                                 generator=torch.Generator(device=DEV).manual_seed(5)))
+        i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device=DEV)
+        ins = dict(q=torch.zeros(U, T, G, 128, dtype=torch.bfloat16, device=DEV),
+                   k=torch.zeros(U, T, 128, dtype=torch.bfloat16, device=DEV),
+                   v=torch.zeros(U, T, 128, dtype=torch.bfloat16, device=DEV),
+                   mask=torch.zeros(2, T, dtype=torch.int64, device=DEV), tok=i32(2, A), n=i32(2),
+                   pos=i32(2), live=i32(2), w=torch.zeros(2, A, device=DEV))
+        tree = K.make_tree(T, per, ins["mask"], ins["live"])
+        path = K.make_path(A, ins["tok"], ins["n"], ins["pos"])
+        return st, ins, tree, path, rnd
+
+    def call(st, ins, tree, path):
+        st.verify(tree, ins["q"], ins["k"], ins["v"], L)
+        st.accept(tree, path, ins["q"], ins["k"], ins["v"], L, row_weight=ins["w"])
+
+    def state(st):
+        o, lse = st._trees[T]["o"], st._trees[T]["lse"]
+        return [st.K, st.V, st.pos, st.util, st.len, st.n, st.mu_k, st.mu_v, st.C, st.n_evict, o, lse, st.tree_S]
+
+    a, b = make(), make()
+    a[0].verify(a[2], a[1]["q"], a[1]["k"], a[1]["v"], L)      # (no live token: makes the buffers)
+    b[0].verify(b[2], b[1]["q"], b[1]["k"], b[1]["v"], L)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(*b[:4])
+    for step in range(5):
+        rnd = a[4]
+        new = dict(q=rnd(U, T, G, 128).bfloat16(), k=rnd(U, T, 128).bfloat16(), v=rnd(U, T, 128).bfloat16(),
+                   mask=torch.from_numpy(tree_masks(rng, 2, T, "chain").view(np.int64)).to(DEV),
+                   tok=torch.from_numpy(np.tile(np.arange(A, dtype=np.int32), (2, 1))).to(DEV),
+                   n=torch.tensor([step % (A + 1), 3], dtype=torch.int32, device=DEV),
+                   pos=torch.full((2,), 1000 + 10 * step, dtype=torch.int32, device=DEV),
+                   live=torch.tensor([T, 5], dtype=torch.int32, device=DEV),
+                   w=torch.rand(2, A, device=DEV))
+        for s in (a, b):
+            for name, x in new.items():
+                s[1][name].copy_(x)
+        call(*a[:4])
+        g.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(state(a[0]), state(b[0])):
+            assert torch.equal(x.contiguous().view(torch.uint8), y.contiguous().view(torch.uint8))
+        for s in (a, b):
+            assert s[0].tree_status() == 0
+            assert torch.equal(s[0].len, s[0].budget if budgets else torch.full_like(s[0].len, L))
