@@ -4,6 +4,9 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <mutex>
+#include <unordered_map>
+
 #include <cuda_runtime.h>
 
 #include "kvc_common.cuh"
@@ -21,6 +24,18 @@ void set_error(const char *fmt, ...)
     va_start(ap, fmt);
     vsnprintf(g_err, sizeof g_err, fmt, ap);
     va_end(ap);
+}
+
+cudaError_t allow_smem(const void *kernel, size_t bytes)
+{
+    static std::mutex lock;
+    static std::unordered_map<const void *, size_t> most;
+    std::lock_guard<std::mutex> hold(lock);
+    size_t &m = most[kernel];
+    const size_t want = bytes > m ? bytes : m;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)want);
+    if (e == cudaSuccess) m = want;
+    return e;
 }
 
 DecodeWs decode_ws_layout(const kvc_params &p, void *base)

@@ -887,8 +887,7 @@ cudaError_t launch_aggregate(const kvc_params &p, int t, const double *probs,
         aggregate_chained_kernel<<<p.U / per, 512, 0, st>>>(a, p.chain_layers, p.chain_heads);
     } else if (kmax > 16 && p.cap <= kAggKeysMax) {
         const size_t smem = (size_t)p.cap * 4;
-        cudaError_t e = cudaFuncSetAttribute(aggregate_keys_kernel,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaError_t e = allow_smem((const void *)aggregate_keys_kernel, smem);
         if (e != cudaSuccess) return e;
         aggregate_keys_kernel<<<p.U, 1024, smem, st>>>(a);
     } else {
@@ -1376,8 +1375,7 @@ static cudaError_t launch_correct_g(const CorrArgs &a, int U, int cap, cudaStrea
 {
     const size_t smem = (size_t)((cap + 31) / 32) * 4;
     if (smem > 16384) {
-        cudaError_t e = cudaFuncSetAttribute(correct_kernel<G>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaError_t e = allow_smem((const void *)correct_kernel<G>, smem);
         if (e != cudaSuccess) return e;
     }
     correct_kernel<G><<<U, 256, smem, st>>>(a);
@@ -1543,8 +1541,7 @@ cudaError_t launch_compact(const kvc_params &p, const kvc_cache &c, int kmax,
 {
     const size_t smem = (size_t)((p.cap + 31) / 32) * 8;
     if (smem > 16384) {
-        cudaError_t e = cudaFuncSetAttribute(compact_kernel,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaError_t e = allow_smem((const void *)compact_kernel, smem);
         if (e != cudaSuccess) return e;
     }
     CompactArgs a{c.K, c.V, c.votes, c.pos, c.util, c.len, evict_idx, n_evict,

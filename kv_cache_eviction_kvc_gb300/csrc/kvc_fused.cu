@@ -1477,7 +1477,7 @@ static cudaError_t launch_fused_g(const FusedArgs &a0, int U, int CS, cudaStream
     auto kern = fused_step_kernel<G, false>;
     if constexpr (G == 2 || G == 4)
         if (a.merge && a.R >= 1) kern = fused_step_kernel<G, true>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dyn);
+    cudaError_t e = allow_smem((const void *)kern, dyn);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     (void)e;

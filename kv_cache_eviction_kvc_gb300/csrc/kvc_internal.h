@@ -37,6 +37,11 @@ constexpr int kPendStride = 72;  // [0] refresh step, [1] count, [2..] slots
 
 DecodeWs decode_ws_layout(const kvc_params &p, void *base);
 
+// Allows the kernel `bytes` of dynamic shared memory, for kernels whose calls differ in
+// it.  The limit is the kernel's, shared by the host's threads, so it only grows: a
+// call's launch is not refused for what another thread allowed in between.
+cudaError_t allow_smem(const void *kernel, size_t bytes);
+
 // thread-local error message
 void set_error(const char *fmt, ...);
 

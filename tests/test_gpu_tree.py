@@ -1431,3 +1431,47 @@ def test_state_run_in_a_graph(budgets):
         for s in (a, b):
             assert s[0].tree_status() == 0
             assert torch.equal(s[0].len, s[0].budget if budgets else torch.full_like(s[0].len, L))
+
+
+def test_steps_of_two_host_threads():
+    """One-token steps of two states from two host threads at once, whose
+    caches differ in size (and so the kernel's shared memory): no step is
+    refused."""
+    lib, ref, calls = K.load(), ctypes.byref, 4000
+
+    def make(seed, L):
+        st, rnd = _stream(seed, 2, 4, L + 1, L + 4, L, 1)
+        q, k, v = rnd(2, 4, 128).bfloat16(), rnd(2, 128).bfloat16(), rnd(2, 128).bfloat16()
+        st.step_calls(1, L + 1, q, k, v, L + 2)
+        st.set_kmax(1)
+        stream = torch.cuda.Stream()
+        args = (L + 1, q.data_ptr(), k.data_ptr(), v.data_ptr(), ref(st.cache), ref(st.moments),
+                st.o.data_ptr(), None, 1, st.evict_idx.data_ptr(), None, st.n_evict.data_ptr(),
+                st.ws.data_ptr(), st.ws.numel(), ctypes.c_void_p(stream.cuda_stream))
+        return st, args, (q, k, v, stream)
+
+    states = [make(81, 64), make(82, 15000)]
+    refused = []
+
+    def loop(st, args):
+        for i in range(calls):
+            status = lib.kvc_decode_step(ref(st.params), 2 + i, 20000 + i, *args)
+            if status:
+                refused.append((status, K.kvc_last_error()))
+                return
+
+    torch.cuda.synchronize()
+    before = sys.getswitchinterval()
+    sys.setswitchinterval(1e-6)
+    try:
+        threads = [threading.Thread(target=loop, args=x[:2]) for x in states]
+        for x in threads:
+            x.start()
+        for x in threads:
+            x.join()
+    finally:
+        sys.setswitchinterval(before)
+    torch.cuda.synchronize()
+    assert not refused, refused
+    for st, _, _ in states:
+        assert st.device_status() == 0 and st.n_evict.tolist() == [1, 1]
