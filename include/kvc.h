@@ -562,8 +562,10 @@ KVC_API size_t kvc_tree_workspace_size(const kvc_params *p, int32_t T);
  *   o = fhat with moments).
  * What a row does not see does not reach it, NaN and infinities included.
  * q [U][T][G][d], k_tree, v_tree [U][T][d] bf16; o [U][T][G][d] bf16 (the
- * type the output projection reads; fp32 until that one rounding, the
- * softmax weights rounded to bf16 for the tensor cores), lse [U][T][G] fp32.
+ * type the output projection reads; fp32 until that one rounding, but the
+ * softmax weights are rounded to bf16 for the tensor cores and C enters as two
+ * bf16 terms, 2^-16 of each product), lse [U][T][G] fp32.  A count n_e that is
+ * NaN gives that unit NaN, as in kvc_correct.
  * Reads K, V, votes and len of the cache.  max_len >= len[u] bounds the
  * launch.  Device-side errors, which leave the unit's outputs untouched:
  * KVC_ERR_SHAPE (len[u] outside [0, max_len]), KVC_ERR_INVALID_ARG (live

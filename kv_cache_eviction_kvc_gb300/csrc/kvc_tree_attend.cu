@@ -20,7 +20,8 @@
 // Measured (bf16, d = 128, G = 4; a call among others): 128 units of 2623 slots
 // on average, 24 tokens: 36.5 us, 4.9 TB/s; 1024 units of 1024 slots, 16 tokens,
 // votes and moments: 140 us, 4.6 TB/s; 8 units of 131071 slots, 63 tokens (252
-// rows): 118 to 122 us, 4.5 TB/s and 1.13 PFLOP/s, 31 tokens: 91 us, 5.9 TB/s.  With
+// rows): 115 to 122 us, 4.5 TB/s and 1.13 PFLOP/s, 31 tokens: 91 us, 5.9 TB/s, 64
+// tokens of 8 heads (512 rows, two blocks that read the slots once each): 210 us.  With
 // two halves of rows a tile takes 3600 clocks for its 2048 of the tensor core:
 // S overwrites P, so a group's product, softmax and next product follow one
 // another.  (S in two halves of 64 slots, each made under the softmax of the
@@ -315,7 +316,11 @@ __device__ __forceinline__ void move_max(float top, uint32_t tO, bool rescale, f
     }
 }
 
-// The weights of 32 raw products, added to sum and written to P as bf16 pairs.
+// The weights of 32 raw products, added to sum and written to P as bf16 pairs.  The
+// sum is of the weights before that rounding; each product of O is off by at most
+// half a step of bf16, which is what o is rounded to itself (a second term for the
+// rest would cost O's product a second time, 1024 of a tile's 3600 clocks with two
+// halves of rows).
 template <bool kVotes>
 __device__ __forceinline__ void weights32(const uint32_t (&y)[32], uint32_t at, const float *v, float2 c2,
                                           float2 r2, float2 (&sum)[2])
@@ -1539,14 +1544,14 @@ struct Cut {
     int split;
 };
 
-// In units of one tile's bytes at the whole device's bandwidth (9.4 ns): a CTA
+// In units of one tile's bytes at the whole device's bandwidth (9.65 ns): a CTA
 // takes 80 of them for a tile (170 with two halves of rows) however little else
 // runs, and 152 when all of them load.  A join is 320 and the sums' way to
 // memory and back.  Measured (us), whole / parts of their own / line: 8 units
-// of 512 slots 10.5 / 10.9 / -, of 1024 slots 13.9 / 11.2 / -, of 4096 slots
-// - / 13.4 / 20.2; 40 of 2432 slots 23.3 / 17.5 / 20.6; 80 of 1408 slots 17.8 /
-// - / 22.1, with 240 rows 28.9 / - / 38.9; 128 of up to 3277 slots 37 / - / 43;
-// 160 of 1152 slots 30.3 / - / 26.2; 1024 of 1024 slots 144 / - / 161.
+// of 512 slots 10.8 / 11.0 / -, of 1024 slots 14.1 / 11.1 / -, of 4096 slots
+// - / 13.6 / 18.6; 40 of 2432 slots 23.8 / 17.6 / 21.3; 80 of 1408 slots 18.5 /
+// - / 22.3, with 240 rows 30.9 / - / 41.4; 128 of up to 3277 slots 36.7 / - / 43.8;
+// 160 of 1152 slots 30.5 / - / 26.5; 1024 of 1024 slots 140 / - / 147.
 Cut choose_cut(long long items, long long tiles, int rows)
 {
     const long long lat = rows > 128 ? 170 : 80, full = items / kGrid, rem = items % kGrid;

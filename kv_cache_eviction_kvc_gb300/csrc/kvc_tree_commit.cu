@@ -2,8 +2,8 @@
 // the weight every slot gathered, evict the lowest (utility, position) pairs
 // down to the budget into the moments, close the gaps.
 //
-// Bound by bytes: 20 per slot (utility read and written, weight read), 128 KB
-// per unit for C, and the rows that go and come.  One CTA per unit, of
+// Its bytes: 20 per slot (utility read and written, weight read; 24 with weights in
+// fp64), 128 KB per unit for C, and the rows that go and come.  One CTA per unit, of
 // 256 threads and several per SM, so that one's loads run under another's
 // selection, or of 512 when it has the SM to itself:
 //   1. the utilities are updated in place; every thread keeps the lowest of
@@ -23,8 +23,11 @@
 //
 // Measured (a call among others): 128 units of 2623 slots on average, up to 6
 // accepted, EMA, moments: 11.7 us (a chain of about ten dependent steps, most of
-// them a trip to L2); 1024 units of 1024 slots, cumulative, votes, moments: 35 us,
-// 4.6 TB/s; 8 units of 131071 slots, 17 accepted: 18.8 us (update 7.9).
+// them a trip to L2); 1024 units of 1024 slots, cumulative, votes, moments: 35 us for
+// 162 MB (1.7 waves of four CTAs an SM, each such a chain: DRAM is a third busy); 8
+// units of 131071 slots, 17 accepted: 18.7 us (update 7.9).  With kmax = 64 the rows of
+// 64 victims leave room for two CTAs an SM: the 1024 units take 47 us without votes,
+// 31 with kmax = 5.  Weights in fp64: 32.4 for 31.3 us.
 //
 // Many equal utilities (weights that underflow to 0) can make every slot a
 // candidate: then the bound is taken again over whole (utility, position,

@@ -13,11 +13,15 @@
 // about 1200 of one SM's share of the bandwidth).  The 128-slot tiles of all
 // units form one line, cut into equal parts for a persistent CTA per SM; every
 // tile stands alone, so nothing is joined.  Measured (G = 4; a call among
-// others): 128 units of 2623 slots on average, up to 6 accepted tokens: 18.6 us,
-// 4.7 TB/s; 1024 units of 1024 slots, 5 accepted, votes: 50 us, 5.6 TB/s; 8 units
-// of 131071 slots, 17 accepted: 50 us, 5.5 TB/s.  In between a tile takes 1320
+// others): 128 units of 2623 slots on average, up to 6 accepted tokens: 18.8 us,
+// 4.7 TB/s; 1024 units of 1024 slots, 5 accepted, votes: 47 us, 6.0 TB/s; 8 units
+// of 131071 slots, 17 accepted: 45 us, 6.0 TB/s.  In between a tile takes 1320
 // clocks, the bandwidth's; what is left is the start (about 6 us until the first
 // product: lengths, paths, query rows).
+//
+// S in fp64 (kWide) takes the same times while the weights are in fp32's range
+// (1024 units 47, 8 units 46 us).  Logits some hundred apart: 48 and 64 us, a tile's
+// sums are then formed twice.
 //
 // 512 threads:
 //   warps 0-7   two groups on alternate tiles, a thread per slot
@@ -26,7 +30,9 @@
 //   warp 10     walks the CTA's units ahead of the others
 //   warp 11     gathers a unit's accepted rows of q (two buffers when they fit)
 //   warps 12-15 the accepted tokens' own entries, a few dot products per unit
-//               (mma.sync), 16 tokens of a unit at a time over the grid
+//               (mma.sync), 16 tokens of a unit at a time over the grid: a chain of
+//               loads per eight rows (1024 units, G = 8, 24 accepted: one warp
+//               284 us a call, four 144)
 // Every wait is bounded (~2 s); a wait that ran out records KVC_ERR_TIMEOUT.
 #include "kvc_soft64.h"
 #include "kvc_tree.h"

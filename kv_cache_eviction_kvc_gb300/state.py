@@ -154,7 +154,10 @@ class DecodeState:
         does not change): q [U][T][G][d], k_tree / v_tree [U][T][d].  Returns
         (o [U][T][G][d] bf16, lse [U][T][G] fp32), buffers of the state that
         the next call with the same T writes again.  The first call with a T
-        allocates: make it before capturing one into a graph."""
+        allocates (make it before capturing one into a graph) what the state
+        then keeps: o and lse, and a workspace of 520 bytes for each of
+        (U ceil(T G / 256) + 152) min(T G, 256) rows (1024 units, G = 4,
+        T = 16: 17 and 39 MB).  A loop over many T keeps buffers of each."""
         b = self._tree_buffers(tree.T, True, stream)
         K_.kvc_tree_attend(self.params, max_len, tree, q, k_tree, v_tree, self.cache, self.moments,
                            b["o"], b["lse"], b["ws"], stream)
@@ -164,9 +167,11 @@ class DecodeState:
                row_weight=None, refresh=True, stream=None):
         """After verify of the same tree: the accepted path joins the cache.
         With refresh the utilities take the weight the accepted tokens gave
-        (row_weight: fp32 [trees][A] or None); the lowest go until every unit
-        is at its budget.  self.n_evict has the counts, self.tree_evict the
-        slots and positions ([2][U][most victims of this call])."""
+        (row_weight: fp32 [trees][A] or None; held in fp64, as a step's
+        probabilities are); the lowest go until every unit is at its budget.
+        self.n_evict has the counts, self.tree_evict the slots and positions
+        ([2][U][most victims of this call]); tree_status() has the errors of
+        both calls."""
         b = self._tree_buffers(tree.T, False)
         S = None
         if refresh:
