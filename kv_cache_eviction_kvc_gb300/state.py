@@ -210,8 +210,10 @@ class DecodeState:
                 lse=torch.zeros(self.U, T, self.G, dtype=torch.float32, device=dev))
             if stream is not None:
                 # the fills above are on the current stream: the call's waits for them
-                if not hasattr(stream, "wait_stream"):
-                    stream = torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream), dev)
+                if not hasattr(stream, "wait_stream"):       # a handle; 0: the default stream
+                    handle = int(getattr(stream, "cuda_stream", stream))
+                    stream = (torch.cuda.ExternalStream(handle, dev) if handle
+                              else torch.cuda.default_stream(dev))
                 stream.wait_stream(torch.cuda.current_stream(dev))
         return trees[T]
 

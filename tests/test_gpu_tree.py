@@ -1068,7 +1068,7 @@ def test_state_reports_what_only_the_commit_refuses(refused):
     assert st.tree_status() == 0 and st.device_status() == 0
 
 
-@pytest.mark.parametrize("handle", [False, True])
+@pytest.mark.parametrize("handle", [False, True, "default"])
 def test_first_verify_on_another_stream(handle):
     """The first call with a T makes its buffers: a call on another stream
     than the current one, which is busy, does not run ahead of their fills."""
@@ -1081,10 +1081,12 @@ def test_first_verify_on_another_stream(handle):
     room = torch.empty(256 << 20, dtype=torch.uint8, device=DEV)
     del room                                           # the buffers come without a device call
     torch.cuda.synchronize()
-    torch.cuda._sleep(200_000_000)                     # about 0.1 s of the current stream
-    on = side.cuda_stream if handle else side
-    o, lse = st.verify(tree, *args, L, stream=on)
-    st.accept(tree, path, *args, L, stream=on)
+    # (the default stream's handle is 0: the current one is another then)
+    on = 0 if handle == "default" else side.cuda_stream if handle else side
+    with torch.cuda.stream(side if handle == "default" else torch.cuda.current_stream()):
+        torch.cuda._sleep(200_000_000)                 # about 0.1 s of the current stream
+        o, lse = st.verify(tree, *args, L, stream=on)
+        st.accept(tree, path, *args, L, stream=on)
     torch.cuda.synchronize()
     S, got = st.tree_S.clone(), (o.clone(), lse.clone())
     ev = st.tree_evict.clone()
