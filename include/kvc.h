@@ -57,7 +57,7 @@
 extern "C" {
 #endif
 
-#define KVC_VERSION 10300  /* major*10000 + minor*100 + patch */
+#define KVC_VERSION 10400  /* major*10000 + minor*100 + patch */
 
 /* Exported symbols (the library is built with hidden default visibility). */
 #if defined(__GNUC__)
@@ -668,6 +668,174 @@ KVC_API kvc_status kvc_tree_commit_f64(const kvc_params *p, int32_t max_len,
                                        const kvc_moments *mom, int32_t kmax, int32_t *evict_idx,
                                        int32_t *evict_pos, int32_t *n_evict, void *ws,
                                        size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------ */
+/* in front of the cache: norms and rotation of a step's heads          */
+/* ------------------------------------------------------------------ */
+
+/*
+ * What the calls around the cache need of the projection: the pages begin at
+ * q, k_new and v_new; these are their definitions here.
+ */
+typedef struct {
+    int32_t Hq, Hkv;        /* query and KV heads of a row; Hq = G Hkv, G in
+                               {1, 2, 4, 8}, Hkv <= 4096                     */
+    int32_t d;              /* head dimension (128)                          */
+    int32_t rot;            /* leading dimensions of a head that are rotated:
+                               0 (none) or a multiple of 16 up to d          */
+    int32_t interleaved;    /* 0: pairs (i, i + rot/2); 1: (2i, 2i + 1)      */
+    float eps;              /* of the norms, >= 0                            */
+    float scale;            /* factor of cosine and sine (1; the length
+                               extensions that scale attention have another) */
+    const uint16_t *q_weight;   /* DEVICE [d] bf16: the norm's weights of the
+                               query heads, or NULL: they are not normed     */
+    const uint16_t *k_weight;   /* the same of the key heads                 */
+    const double *inv_freq;     /* DEVICE [rot/2] radians per position, finite
+                               (8-byte aligned; NULL with rot = 0)           */
+    int32_t units;          /* units from one sequence to the next in the
+                               outputs (NL Hkv; Hkv when the layers are
+                               called one by one)                            */
+    int32_t first_unit;     /* unit of KV head 0 within a sequence:
+                               first_unit + Hkv <= units                     */
+} kvc_rope;
+
+/*
+ * kvc_qk_norm_rope -- norms and rotation of the query and key heads of B
+ * sequences of T tokens, in one pass, from the projection's rows to the unit
+ * layouts of the other calls.
+ *
+ * Row (b, t) of qkv, at (b T + t) * row_stride elements, holds Hq query heads,
+ * Hkv key heads and Hkv value heads of d elements each.  For a query or key
+ * head x with weights w, position p = pos[b][t]:
+ *   y = x w / sqrt(mean(x^2) + eps)                 (y = x without weights)
+ *   pair i of the rotated dimensions, a_i = p inv_freq[i]:
+ *     (y_1, y_2) -> scale (y_1 cos a_i - y_2 sin a_i, y_2 cos a_i + y_1 sin a_i)
+ *   rounded once, to bf16; value heads are copied.
+ * KV head g of sequence b is unit u = b units + first_unit + g, and query head
+ * h belongs to KV head h / G: q [U][T][G][d], k and v [U][T][d] bf16, as
+ * kvc_decode_step (T = 1), the drafted-token calls and the prefill calls take
+ * them.  Any of q, k, v may be NULL (not written), one at least is not.
+ * All in fp32 but the angles: these are fixed-point fractions of a turn, with
+ * the product by the position exact modulo a turn (inv_freq / 2 pi rounded to
+ * 53 bits), so far positions lose nothing.  A normed row whose squares sum
+ * past fp32's range gives zeros (NaN where it was infinite).
+ * pos [B][T] int32 (any value).  n: DEVICE [B] live tokens of each sequence,
+ * taken as within [0, T], or NULL = T: rows of the outputs at or behind it are
+ * left as they were, rows of the inputs there are not used.
+ * qkv, q, k, v and the weights are 16-byte aligned; row_stride >= (Hq + 2 Hkv)
+ * d, a multiple of 8.  Outputs do not overlap inputs.
+ */
+KVC_API kvc_status kvc_qk_norm_rope(const kvc_rope *r, int32_t B, int32_t T, const uint16_t *qkv,
+                                    int64_t row_stride, const int32_t *pos, const int32_t *n,
+                                    uint16_t *q, uint16_t *k, uint16_t *v, void *stream);
+
+/* ------------------------------------------------------------------ */
+/* beside the budgeted cache: a cache in pages                          */
+/* ------------------------------------------------------------------ */
+
+/*
+ * A prompt before its selection, or a layer that keeps all of its tokens, lives
+ * in pages of a pool that sequences share: no rows are reserved, and a row may
+ * be held in 8 bits.  kvc_page_write puts rows in, kvc_page_attend appends one
+ * token and attends over the pages, kvc_page_read gives rows back in bf16 (the
+ * prompt for the prefill scorer, or what a selection keeps for the budgeted
+ * cache).
+ */
+enum {
+    KVC_PAGE_BF16 = 0,      /* rows of d bf16                                */
+    KVC_PAGE_E4M3 = 1       /* rows of d e4m3 values with an fp32 scale each:
+                               scale = max(max |x| / 448, 2^-126),
+                               value = e4m3(x (1 / scale)), nearest even,
+                               at most 448 in magnitude; a row that holds a
+                               NaN or an infinity is NaN when read           */
+};
+
+typedef struct {
+    int32_t U;              /* units                                         */
+    int32_t d;              /* head dimension (128)                          */
+    int32_t type;           /* KVC_PAGE_*                                    */
+    int32_t heads;          /* units that share a table and a length: unit u
+                               is head u % heads of sequence u / heads; 1: a
+                               table per unit (a budget of its own).  Divides
+                               U; S = U / heads                              */
+    int32_t page;           /* slots per page: 16, 32, 64 or 128             */
+    int32_t n_pages;        /* pages of the pool                             */
+    int32_t stride;         /* entries per row of the table: a sequence has
+                               room for stride * page slots (< 2^31 - 128)   */
+    void *K, *V;            /* DEVICE [n_pages][heads][page][d]              */
+    float *k_scale, *v_scale;   /* DEVICE [n_pages][heads][page]; NULL with
+                               KVC_PAGE_BF16                                 */
+    const int32_t *table;   /* DEVICE [S][stride]: slot i of a sequence is row
+                               i % page of page table[i / page].  Entries
+                               behind a call's last slot are not read        */
+    const int32_t *len;     /* DEVICE [S] slots in use.  No call changes it:
+                               one array may serve every layer of a step, and
+                               the caller advances it once                   */
+} kvc_pages;
+
+/* Bytes of workspace the calls below need with G query heads per KV head
+ * (kvc_page_write and kvc_page_read: the first 256).  Zero it once before the
+ * first call; its first 256 bytes hold the status word kvc_get_device_status
+ * reads.  Calls that overlap on the GPU need a workspace each.  0: invalid
+ * parameters. */
+KVC_API size_t kvc_page_workspace_size(const kvc_pages *pg, int32_t G);
+
+/*
+ * kvc_page_write -- rows into pages, quantised as they are written.
+ *
+ * k, v [U][T][d] bf16 (16-byte aligned): of every unit of sequence s, rows
+ * t < count[s] go to slots first[s] + t.  first: DEVICE [S] or NULL (0);
+ * count: DEVICE [S] or NULL (T).  len is not used (first may be it).  A slot
+ * is written by one row of one sequence; pages shared by sequences (a common
+ * prefix) are written through one of them.
+ * Device-side errors: KVC_ERR_SHAPE (count outside [0, T], slots outside
+ * [0, stride * page)), which leaves the sequence as it was;
+ * KVC_ERR_INVALID_ARG (a page outside the pool), whose rows are not written.
+ */
+KVC_API kvc_status kvc_page_write(const kvc_pages *pg, int32_t T, const int32_t *first,
+                                  const int32_t *count, const uint16_t *k, const uint16_t *v,
+                                  void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * kvc_page_read -- rows out of pages, in bf16 (value * scale, rounded once).
+ *
+ * For unit u and i < count[u], rows k_out[u][i], v_out[u][i] receive slot
+ * slots[u][i] (any order, repeats allowed), or slot i where slots is NULL.
+ * slots: DEVICE [U][M] or NULL; count: DEVICE [U] or NULL (M; without slots the
+ * lesser of M and the length).  k_out, v_out [U][ld][d] bf16 (16-byte aligned),
+ * ld >= M: with ld = cap the rows of a budgeted cache.  Rows at or behind the
+ * count are left as they were.
+ * Device-side errors: KVC_ERR_SHAPE (count outside [0, M], which leaves the
+ * unit's rows as they were; a slot outside [0, len), whose row is left),
+ * KVC_ERR_INVALID_ARG (a page outside the pool, whose rows are left).
+ */
+KVC_API kvc_status kvc_page_read(const kvc_pages *pg, int32_t M, int32_t ld, const int32_t *slots,
+                                 const int32_t *count, uint16_t *k_out, uint16_t *v_out, void *ws,
+                                 size_t ws_bytes, void *stream);
+
+/*
+ * kvc_page_attend -- append one token, then its attention over the pages.
+ *
+ * Defined by: MomentKV sec 2 as in kvc_decode_attend (append before the
+ * attention), without votes.  For unit u of sequence s, n = len[s]:
+ *   with k_new, v_new [U][d] bf16, slot n receives them (quantised) and n
+ *   below is n + 1; with both NULL nothing is appended;
+ *   x_i = q_h . k_i / sqrt(d), i in [0, n), over the values as they are held;
+ *   lse = log sum_i exp(x_i), o = sum_i exp(x_i - lse) v_i.
+ *   n = 0: lse = -inf, o = 0.
+ * q [U][G][d] bf16; o [U][G][d] bf16 (the type the output projection reads),
+ * lse [U][G] fp32.  q, o, k_new, v_new are 16-byte aligned.  Logits, sums and
+ * outputs are fp32 until that one rounding, weights enter the products as two
+ * 16-bit terms.  max_len bounds n with the appended token, 1 <= max_len <=
+ * stride * page, and the launch.
+ * Device-side errors, which leave the outputs of the units concerned as they
+ * were: KVC_ERR_SHAPE (len[s] < 0, or n with the appended token above
+ * max_len), KVC_ERR_INVALID_ARG (a page outside the pool).
+ */
+KVC_API kvc_status kvc_page_attend(const kvc_pages *pg, int32_t G, int32_t max_len,
+                                   const uint16_t *q, const uint16_t *k_new,
+                                   const uint16_t *v_new, uint16_t *o, float *lse, void *ws,
+                                   size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------------ */
 /* prefill -> decode hand-off                                           */

@@ -23,6 +23,7 @@ STATUS_NAMES = {0: "KVC_OK", 1: "KVC_ERR_INVALID_ARG", 2: "KVC_ERR_SHAPE",
 RULE_SINGLE, RULE_CUMULATIVE, RULE_EMA, RULE_MI, RULE_EMA_CHAINED = 0, 1, 2, 3, 4
 CORR_OFF, CORR_ZERO_ORDER, CORR_FIRST_ORDER = 0, 1, 2
 ALLOC_GLOBAL, ALLOC_LAYER, ALLOC_HEAD = 0, 1, 2
+PAGE_BF16, PAGE_E4M3 = 0, 1
 TREE_MAX = 64      # most drafted tokens per tree, most victims per commit
 
 EXPORTED = (
@@ -34,6 +35,8 @@ EXPORTED = (
     "kvc_prefill_snapkv", "kvc_prefill_handoff_workspace_size", "kvc_prefill_handoff",
     "kvc_tree_workspace_size", "kvc_tree_attend", "kvc_tree_weights", "kvc_tree_commit",
     "kvc_tree_weights_f64", "kvc_tree_commit_f64",
+    "kvc_qk_norm_rope", "kvc_page_workspace_size", "kvc_page_write", "kvc_page_read",
+    "kvc_page_attend",
 )
 
 
@@ -72,6 +75,22 @@ class kvc_path(ctypes.Structure):
                 ("pos", ctypes.c_void_p)]
 
 
+class kvc_rope(ctypes.Structure):
+    _fields_ = [("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("scale", ctypes.c_float), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p),
+                ("units", ctypes.c_int32), ("first_unit", ctypes.c_int32)]
+
+
+class kvc_pages(ctypes.Structure):
+    _fields_ = [("U", ctypes.c_int32), ("d", ctypes.c_int32), ("type", ctypes.c_int32),
+                ("heads", ctypes.c_int32), ("page", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("stride", ctypes.c_int32), ("K", ctypes.c_void_p), ("V", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("len", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -93,6 +112,7 @@ def load(build: bool = True):
     PC = ctypes.POINTER(kvc_cache)
     PM = ctypes.POINTER(kvc_moments)
     PT, PA = ctypes.POINTER(kvc_tree), ctypes.POINTER(kvc_path)
+    PR, PG = ctypes.POINTER(kvc_rope), ctypes.POINTER(kvc_pages)
     sigs = {
         "kvc_version": (I32, []),
         "kvc_last_error": (ctypes.c_char_p, []),
@@ -124,6 +144,11 @@ def load(build: bool = True):
         "kvc_tree_attend": (I32, [PP, I32, PT, P, P, P, PC, PM, P, P, P, SZ, P]),
         "kvc_tree_weights": (I32, [PP, I32, PT, PA, P, P, P, P, PC, P, P, SZ, P]),
         "kvc_tree_commit": (I32, [PP, I32, PT, PA, P, P, P, PC, PM, I32, P, P, P, P, SZ, P]),
+        "kvc_qk_norm_rope": (I32, [PR, I32, I32, P, I64, P, P, P, P, P, P]),
+        "kvc_page_workspace_size": (SZ, [PG, I32]),
+        "kvc_page_write": (I32, [PG, I32, P, P, P, P, P, SZ, P]),
+        "kvc_page_read": (I32, [PG, I32, I32, P, P, P, P, P, SZ, P]),
+        "kvc_page_attend": (I32, [PG, I32, I32, P, P, P, P, P, P, SZ, P]),
     }
     for name in ("kvc_tree_weights", "kvc_tree_commit"):
         sigs[name + "_f64"] = sigs[name]
@@ -457,6 +482,144 @@ def kvc_tree_commit(p, max_len, tree: kvc_tree, path: kvc_path, k_tree, v_tree, 
         None if evict_pos is None else _sized(evict_pos, _I32, "evict_pos", U * kmax, dev),
         _sized(n_evict, _I32, "n_evict", U, dev), _sized(ws, _U8, "ws", 0, dev),
         ws.numel(), _stream_on(stream, dev)))
+
+
+# ------------------------------------------------------------------ norms and rotation
+
+def make_rope(Hq, Hkv, inv_freq, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
+              scale=1.0, units=None, first_unit=0, d=128) -> kvc_rope:
+    """Norms and rotation of Hq query and Hkv KV heads.  inv_freq: float64 [rot/2]
+    radians per position, or None (nothing is rotated); q_weight, k_weight: bf16
+    [d] or None (not normed).  units: units from one sequence to the next in the
+    outputs (None: Hkv), KV head 0 being unit first_unit of them.  The tensors
+    are kept alive with the structure."""
+    tensors = [t for t in (inv_freq, q_weight, k_weight) if t is not None]
+    dev = tensors[0].device.index if tensors else None
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    r = kvc_rope(Hq, Hkv, d, rot, int(bool(interleaved)), eps, scale,
+                 _sized(q_weight, _BF16, "q_weight", d, dev, optional=True),
+                 _sized(k_weight, _BF16, "k_weight", d, dev, optional=True),
+                 _sized(inv_freq, _F64, "inv_freq", rot // 2, dev, optional=True),
+                 Hkv if units is None else units, first_unit)
+    r.dev, r.keep = dev, (inv_freq, q_weight, k_weight)
+    return r
+
+
+def kvc_qk_norm_rope(r: kvc_rope, qkv, pos, n, q, k, v, stream=None):
+    """qkv: bf16 [B][T][row], a row of at least (Hq + 2 Hkv) d elements; rows may be
+    further apart (a slice of wider ones), sequences follow one another.  pos:
+    int32 [B][T]; n: int32 [B] or None.  q [U][T][G][d], k, v [U][T][d] bf16,
+    each of them or None."""
+    dev = _device()
+    if r.dev is not None and r.dev != dev:
+        raise ValueError(f"the weights and frequencies must live on the current device cuda:{dev}")
+    if qkv is None or qkv.dim() != 3:
+        raise ValueError("qkv must be [B][T][row]")
+    B, T, width = qkv.shape
+    row, Hq, Hkv, d = qkv.stride(1) if T > 1 else qkv.stride(0), r.Hq, r.Hkv, r.d
+    if B * T == 1:
+        row = width
+    if (width < (Hq + 2 * Hkv) * d or qkv.stride(2) != 1
+            or (T > 1 and B > 1 and qkv.stride(0) != T * row)):
+        raise ValueError(f"qkv must hold rows of (Hq + 2 Hkv) d = {(Hq + 2 * Hkv) * d} elements, "
+                         "evenly apart")
+    if qkv.dtype is not _BF16 or qkv.get_device() != dev:
+        raise TypeError(f"qkv must be bf16 on the current device cuda:{dev}")
+    # units the outputs hold at least: all of the last sequence's that are written
+    rows = ((B - 1) * r.units + r.first_unit + Hkv) * T
+    _check(load().kvc_qk_norm_rope(
+        _ref(r), B, T, qkv.data_ptr(), row, _sized(pos, _I32, "pos", B * T, dev),
+        None if n is None else _sized(n, _I32, "n", B, dev),
+        None if q is None else _sized(q, _BF16, "q", rows * (Hq // Hkv) * d, dev),
+        None if k is None else _sized(k, _BF16, "k", rows * d, dev),
+        None if v is None else _sized(v, _BF16, "v", rows * d, dev), _stream_on(stream, dev)))
+
+
+# ------------------------------------------------------------------ a cache in pages
+
+def make_pages(K, V, k_scale, v_scale, table, length) -> kvc_pages:
+    """A cache in pages: K, V [n_pages][heads][page][d] bf16, or float8_e4m3fn with
+    k_scale, v_scale fp32 [n_pages][heads][page]; table: int32 [S][stride]
+    (sequences of `heads` units; heads = 1: a table per unit), length: int32 [S].
+    The tensors are kept alive with the structure."""
+    if K is None or K.dim() != 4 or V is None or V.shape != K.shape:
+        raise ValueError("K and V must be [n_pages][heads][page][d]")
+    if table is None or table.dim() != 2:
+        raise ValueError("table must be [S][stride]")
+    n_pages, heads, page, d = K.shape
+    S, stride = table.shape
+    dev, rows = K.device.index, n_pages * heads * page
+    e4m3 = K.dtype is torch.float8_e4m3fn
+    dtype = torch.float8_e4m3fn if e4m3 else _BF16
+    if not e4m3 and (k_scale is not None or v_scale is not None):
+        raise ValueError("bf16 pages have no scales")
+    pg = kvc_pages(S * heads, d, PAGE_E4M3 if e4m3 else PAGE_BF16, heads, page, n_pages, stride,
+                   _sized(K, dtype, "K", rows * d, dev), _sized(V, dtype, "V", rows * d, dev),
+                   _sized(k_scale, _F32, "k_scale", rows, dev) if e4m3 else None,
+                   _sized(v_scale, _F32, "v_scale", rows, dev) if e4m3 else None,
+                   _sized(table, _I32, "table", S * stride, dev),
+                   _sized(length, _I32, "length", S, dev))
+    pg.S, pg.dev, pg.keep = S, dev, (K, V, k_scale, v_scale, table, length)
+    return pg
+
+
+def _pages_device(pg):
+    dev = _device()
+    if pg.dev != dev:
+        raise ValueError(f"the pages must live on the current device cuda:{dev}")
+    return dev
+
+
+def kvc_page_workspace_size(pg: kvc_pages, G: int) -> int:
+    return int(load().kvc_page_workspace_size(_ref(pg), int(G)))
+
+
+def kvc_page_write(pg: kvc_pages, first, count, k, v, ws, stream=None):
+    """k, v: bf16 [U][T][d]; first, count: int32 [S] or None (0, T)."""
+    dev = _pages_device(pg)
+    if k is None or k.dim() != 3:
+        raise ValueError("k must be [U][T][d]")
+    T = k.shape[1]
+    n = pg.U * T * pg.d
+    _check(load().kvc_page_write(
+        _ref(pg), T, None if first is None else _sized(first, _I32, "first", pg.S, dev),
+        None if count is None else _sized(count, _I32, "count", pg.S, dev),
+        _sized(k, _BF16, "k", n, dev), _sized(v, _BF16, "v", n, dev), _sized(ws, _U8, "ws", 0, dev),
+        ws.numel(), _stream_on(stream, dev)))
+
+
+def kvc_page_read(pg: kvc_pages, slots, count, k_out, v_out, ws, stream=None, M=None):
+    """slots: int32 [U][M] or None (slot i; M, else all rows of k_out); count: int32
+    [U] or None; k_out, v_out: bf16 [U][ld][d], ld >= M."""
+    dev = _pages_device(pg)
+    if k_out is None or k_out.dim() != 3:
+        raise ValueError("k_out must be [U][ld][d]")
+    if slots is not None and slots.dim() != 2:
+        raise ValueError("slots must be [U][M]")
+    U, ld = pg.U, k_out.shape[1]
+    M = slots.shape[1] if slots is not None else ld if M is None else int(M)
+    n = U * ld * pg.d
+    _check(load().kvc_page_read(
+        _ref(pg), M, ld, None if slots is None else _sized(slots, _I32, "slots", U * M, dev),
+        None if count is None else _sized(count, _I32, "count", U, dev),
+        _sized(k_out, _BF16, "k_out", n, dev), _sized(v_out, _BF16, "v_out", n, dev),
+        _sized(ws, _U8, "ws", 0, dev), ws.numel(), _stream_on(stream, dev)))
+
+
+def kvc_page_attend(pg: kvc_pages, max_len, q, k_new, v_new, o, lse, ws, stream=None):
+    """q, o: bf16 [U][G][d]; k_new, v_new: bf16 [U][d], or both None; lse: fp32 [U][G]."""
+    dev = _pages_device(pg)
+    U, d = pg.U, pg.d
+    if q is None or q.dim() != 3:
+        raise ValueError("q must be [U][G][d]")
+    G = q.shape[1]
+    n, heads = U * d, U * G
+    _check(load().kvc_page_attend(
+        _ref(pg), G, int(max_len), _sized(q, _BF16, "q", heads * d, dev),
+        None if k_new is None else _sized(k_new, _BF16, "k_new", n, dev),
+        None if v_new is None else _sized(v_new, _BF16, "v_new", n, dev),
+        _sized(o, _BF16, "o", heads * d, dev), _sized(lse, _F32, "lse", heads, dev),
+        _sized(ws, _U8, "ws", 0, dev), ws.numel(), _stream_on(stream, dev)))
 
 
 # ------------------------------------------------------------------ prefill

@@ -228,3 +228,111 @@ class DecodeState:
             if status:
                 return status
         return 0
+
+
+class PagedState:
+    """A cache in pages of `seqs` sequences of `heads` units (heads = 1: a table
+    and a length per unit), with the pool's bookkeeping: pages are taken from a
+    free list on the host as sequences grow and go back when they end.  Calls run
+    on the current stream."""
+
+    def __init__(self, seqs: int, heads: int, G: int, max_len: int, *, page: int = 64,
+                 e4m3: bool = True, n_pages: int | None = None, device="cuda", d: int = 128):
+        self.seqs, self.heads, self.G, self.page, self.d = seqs, heads, G, page, d
+        self.device = dev = torch.device(device)
+        stride = -(-max_len // page)
+        n_pages = seqs * stride if n_pages is None else n_pages
+        shape = (n_pages, heads, page, d)
+        dtype = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+        self.K = torch.zeros(shape, dtype=dtype, device=dev)
+        self.V = torch.zeros(shape, dtype=dtype, device=dev)
+        self.k_scale = torch.zeros(shape[:3], device=dev) if e4m3 else None
+        self.v_scale = torch.zeros(shape[:3], device=dev) if e4m3 else None
+        self.table = torch.full((seqs, stride), -1, dtype=torch.int32, device=dev)
+        self.len = torch.zeros(seqs, dtype=torch.int32, device=dev)
+        self.pages = K_.make_pages(self.K, self.V, self.k_scale, self.v_scale, self.table, self.len)
+        nbytes = K_.kvc_page_workspace_size(self.pages, G)
+        if nbytes == 0:
+            raise K_.KvcError(1, K_.kvc_last_error() or "invalid page parameters")
+        self.ws = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+        self.o = torch.zeros(seqs * heads, G, d, dtype=torch.bfloat16, device=dev)
+        self.lse = torch.zeros(seqs * heads, G, dtype=torch.float32, device=dev)
+        self._free = list(range(n_pages - 1, -1, -1))
+        self._held = [[] for _ in range(seqs)]
+
+    # --------------------------------------------------------------- pages
+    def reserve(self, lengths):
+        """Pages for lengths[s] slots of every sequence (a host list; what a
+        sequence has already stays).  A pool without enough raises and nothing
+        changes."""
+        if len(lengths) != self.seqs:
+            raise ValueError(f"{len(lengths)} lengths for {self.seqs} sequences")
+        want = [max(0, -(-int(n) // self.page) - len(h)) for n, h in zip(lengths, self._held)]
+        for n, h, w in zip(lengths, self._held, want):
+            if len(h) + w > self.table.shape[1]:
+                raise ValueError(f"{n} slots are more than a table of {self.table.shape[1]} pages holds")
+        if sum(want) > len(self._free):
+            raise RuntimeError(f"the pool has {len(self._free)} free pages, {sum(want)} are needed")
+        at, value = [], []
+        for s, w in enumerate(want):
+            for _ in range(w):
+                at.append(s * self.table.shape[1] + len(self._held[s]))
+                self._held[s].append(self._free.pop())
+                value.append(self._held[s][-1])
+        if at:
+            i = torch.tensor([at, value], dtype=torch.int64).to(self.device)
+            self.table.view(-1).index_copy_(0, i[0], i[1].to(torch.int32))
+
+    def release(self, s: int):
+        """The pages of sequence s go back to the pool; its length becomes 0."""
+        self._free += reversed(self._held[s])
+        self._held[s] = []
+        self.table[s].fill_(-1)
+        self.len[s:s + 1].zero_()
+
+    # --------------------------------------------------------------- calls
+    def write(self, k, v, count=None):
+        """Rows k, v [U][T][d] behind what the sequences hold (count: int32
+        [seqs], None: T rows each); the lengths advance.  Reserve their pages
+        before."""
+        K_.kvc_page_write(self.pages, self.len, count, k, v, self.ws)
+        self.len.add_(k.shape[1] if count is None else count)
+
+    def step(self, q, k_new, v_new, max_len: int):
+        """One token per sequence: k_new, v_new [U][d] join the cache, q [U][G][d]
+        attends over it; the lengths advance.  max_len bounds the new lengths.
+        Returns (o [U][G][d] bf16, lse [U][G] fp32), written again by the next
+        call."""
+        K_.kvc_page_attend(self.pages, max_len, q, k_new, v_new, self.o, self.lse, self.ws)
+        self.len.add_(1)
+        return self.o, self.lse
+
+    def read(self, M: int, slots=None, count=None):
+        """bf16 rows (k, v [U][M][d]) of slots [U][M] (None: the first M), the first
+        count[u] of each (None: M; without slots what there is).  Rows behind the
+        count are zero."""
+        U = self.seqs * self.heads
+        k = torch.zeros(U, M, self.d, dtype=torch.bfloat16, device=self.device)
+        v = torch.zeros_like(k)
+        K_.kvc_page_read(self.pages, slots, count, k, v, self.ws, M=M)
+        return k, v
+
+    def hand_over(self, st: DecodeState, slots, count):
+        """The budgeted cache st of the same units takes count[u] (int32 [U]) of the
+        slots listed in slots[u] (int32 [U][M], M <= cap): rows, positions and
+        lengths; utilities and moments start anew, as in load_prefill."""
+        if st.U != self.seqs * self.heads or slots.shape[1] > st.cap:
+            raise ValueError(f"{slots.shape[1]} slots of {self.seqs * self.heads} units for a cache "
+                             f"of {st.U} units of {st.cap}")
+        K_.kvc_page_read(self.pages, slots, count, st.K, st.V, self.ws)
+        st.pos[:, :slots.shape[1]].copy_(slots)
+        if st.votes is not None:
+            st.votes.fill_(1)
+        st.util.fill_(float("inf"))
+        st.len.copy_(count)
+        for t in (st.n, st.mu_k, st.mu_v, st.C):
+            t.zero_()
+
+    def status(self) -> int:
+        """The first error a call recorded and that has not been read yet (0: none)."""
+        return K_.kvc_get_device_status(self.ws)
