@@ -115,9 +115,8 @@ kvc_status kvc_qk_norm_rope(const kvc_rope *r, int32_t B, int32_t T, const uint1
              "%s: units %d .. %lld of a sequence's %d", fn, r->first_unit,
              (long long)r->first_unit + r->Hkv, r->units);
     PG_CHECK(B >= 1 && T >= 1, KVC_ERR_INVALID_ARG, "%s: B = %d and T = %d must be >= 1", fn, B, T);
-    PG_CHECK((int64_t)B * r->units < (1ll << 31) && (int64_t)B * T < (1ll << 31) &&
-                 launchable((int64_t)B * T, (r->Hq + 2ll * r->Hkv + 15) / 16),
-             KVC_ERR_UNSUPPORTED, "%s: B = %d sequences of T = %d tokens unsupported", fn, B, T);
+    PG_CHECK((int64_t)B * r->units < (1ll << 31) && (int64_t)B * T <= (1ll << 30), KVC_ERR_UNSUPPORTED,
+             "%s: B = %d sequences of T = %d tokens unsupported", fn, B, T);
     PG_CHECK(qkv && pos && (q || k || v), KVC_ERR_INVALID_ARG,
              "%s: qkv, pos and one of q, k, v must be non-NULL", fn);
     PG_CHECK(!misaligned(qkv, 16) && !misaligned(q, 16) && !misaligned(k, 16) && !misaligned(v, 16) &&

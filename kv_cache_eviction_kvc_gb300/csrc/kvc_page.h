@@ -38,20 +38,17 @@ struct PageArgs {
 
 PageArgs page_args(const kvc_pages &pg);
 
-// Largest magnitude of eight bf16 and m; a NaN stays.
-__device__ __forceinline__ float max_nan(float a, float b)
-{
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
+// Magnitudes of two bf16, which order as whole numbers; a NaN is above infinity.
+__device__ __forceinline__ uint32_t magnitudes(uint32_t w) { return w & 0x7fff7fffu; }
 
+// The scale of a row from its largest magnitude, and what its values are multiplied by.
 __device__ __forceinline__ float row_scale(float amax)
 {
-    return max_nan(__fdiv_rn(amax, kE4m3Max), kLeastScale);
+    const float s = __fdiv_rn(amax, kE4m3Max);
+    return s < kLeastScale ? kLeastScale : s;    // a NaN stays
 }
 
-// four e4m3 values of x * inv, nearest even, at most 448
+// four e4m3 values, nearest even, at most 448
 __device__ __forceinline__ uint32_t to_e4m3(float a, float b, float c, float d)
 {
     const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
@@ -73,6 +70,40 @@ __device__ __forceinline__ uint32_t to_bf16x2(float lo, float hi)
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+// packed fp32 pairs: one instruction for two
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z)
+{
+    float2 r;
+    asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+        " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}\n"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
+    return r;
+}
+
+__device__ __forceinline__ float2 mul2(float2 x, float2 y)
+{
+    float2 r;
+    asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mul.rn.f32x2 d, a, b;\n"
+        " mov.b64 {%0, %1}, d;\n}\n"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+    return r;
+}
+
+// two bf16 times f
+__device__ __forceinline__ float2 scaled2(uint32_t w, float f)
+{
+    return mul2(make_float2(bf_lo(w), bf_hi(w)), make_float2(f, f));
+}
+
+// four bf16 times inv as e4m3
+__device__ __forceinline__ uint32_t quantise4(uint32_t w0, uint32_t w1, float inv)
+{
+    const float2 a = scaled2(w0, inv), b = scaled2(w1, inv);
+    return to_e4m3(a.x, a.y, b.x, b.y);
 }
 
 size_t page_ws_bytes(const kvc_pages &pg, int G);

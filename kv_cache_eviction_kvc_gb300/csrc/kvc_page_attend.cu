@@ -295,14 +295,11 @@ __global__ void __launch_bounds__(kThreads, 3) attend_kernel(const __grid_consta
                 const uint2 w = *reinterpret_cast<const uint2 *>((i ? a.v_new : a.k_new) + (size_t)u * kD + lane * 4);
                 uint8_t *pool = i ? a.pg.V : a.pg.K;
                 if (kE4m3) {
-                    const float x[4] = {bf_lo(w.x), bf_hi(w.x), bf_lo(w.y), bf_hi(w.y)};
-                    float amax = 0.f;
+                    uint32_t top = __vmaxu2(magnitudes(w.x), magnitudes(w.y));
 #pragma unroll
-                    for (int j = 0; j < 4; j++) amax = max_nan(amax, fabsf(x[j]));
-#pragma unroll
-                    for (int j = 16; j; j >>= 1) amax = max_nan(amax, __shfl_xor_sync(kFull, amax, j));
-                    const float scale = row_scale(amax), inv = __fdiv_rn(1.f, scale);
-                    const uint32_t v = to_e4m3(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+                    for (int j = 16; j; j >>= 1) top = __vmaxu2(top, __shfl_xor_sync(kFull, top, j));
+                    const float scale = row_scale(__uint_as_float(max(top << 16, top & 0xffff0000u)));
+                    const uint32_t v = quantise4(w.x, w.y, __fdiv_rn(1.f, scale));
                     reinterpret_cast<uint32_t *>(sm.row[i])[lane] = v;
                     if (lane == 0) sm.row_scale[i] = scale;
                     if (ok) {

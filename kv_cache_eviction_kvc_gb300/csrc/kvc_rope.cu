@@ -11,13 +11,27 @@
 // product with the integer position, modulo 2^64, is the angle modulo a turn
 // without rounding.  The only rounding is F's (53 bits of f / 2 pi), so position
 // 2^20 at f = 1 is off by 2^-36 turns where an fp32 product would be off by 2^-7.
+//
+// Bound by the bytes, 512 per head read and written, with the instructions close
+// behind (141 for two heads took 80 % of the issue slots of the time of the bytes):
+// weights, cosine and sine are one 2x2 of a pair, formed once per token and kind of
+// head, applied in packed fp32 pairs.  Measured: one token of 48 heads 6.8 us (the
+// host's part of the call), 16 x 24 tokens 7.6, 32768 tokens 137 (5.9 TB/s; a block
+// per token without the 2x2 took 319).  Four blocks of 64 registers and four rows in
+// flight per team: 139; two rows 150, three 146; three blocks 152; two of 100 181.
 #include "kvc_page.h"
+
+#include <algorithm>
 
 namespace kvc {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTeams = kThreads / 16;            // of sixteen lanes: a head each
+constexpr int kTok = 4;                          // tokens of a tile
+constexpr int kPer = kTeams / kTok;              // teams of a token
+constexpr int kAhead = 4;                        // rows a team has in flight
+constexpr int kResident = 4;                     // blocks per SM
 
 struct RopeArgs {
     const uint16_t *qkv;
@@ -26,7 +40,7 @@ struct RopeArgs {
     const uint16_t *qw, *kw;
     const double *inv_freq;
     uint16_t *q, *k, *v;
-    int T, Hkv, G, rot, units, first_unit;
+    int T, Hkv, gshift, rot, units, first_unit;
     float eps, scale;
     FastDiv by_T;
 };
@@ -46,95 +60,143 @@ __device__ __forceinline__ void unpack4(uint2 w, float *f)
     f[3] = bf_hi(w.y);
 }
 
-// One block: kTok tokens, `rows` of their heads.
-template <int kTok, bool kInter>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a, int tokens,
-                                                        int rows_per_block)
+// Tiles of four tokens: their turns to shared memory (a thread each), then their
+// rows [y rows, (y + 1) rows), four teams a token.
+template <bool kInter>
+__global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const __grid_constant__ RopeArgs a, int tokens,
+                                                        int rows)
 {
-    __shared__ float4 turns[kTok][2][16];        // (c, s, c, s) of pairs 4l .. 4l + 3
+    __shared__ float4 turns[2][kTok][2][16];     // (c, s, c, s) of pairs 4l .. 4l + 3
     follow();
     lead();
     const int tid = threadIdx.x, lane = tid & 15, team = tid >> 4;
-    const int tok0 = blockIdx.x * kTok;
+    const unsigned mates = team & 1 ? 0xffff0000u : 0x0000ffffu;
     const int half = a.rot >> 1;
-    for (int i = tid; i < kTok * half; i += kThreads) {
-        const int j = i / half, p = i - j * half, tok = tok0 + j;
-        if (tok >= tokens) break;
-        const uint64_t at = (uint64_t)(int64_t)a.pos[tok] * turn_fraction(a.inv_freq[p]);
-        float s, c;
-        sincospif(__ll2float_rn((long long)at) * 1.0842021724855044e-19f, &s, &c);   // 2^-63
-        float2 *to = reinterpret_cast<float2 *>(&turns[j][(p >> 1) & 1][p >> 2]) + (p & 1);
-        *to = make_float2(c * a.scale, s * a.scale);
-    }
-    __syncthreads();
-
-    constexpr int kPer = kTeams / kTok;          // teams of a token
-    const int j = team / kPer, tok = tok0 + j;
-    if (tok >= tokens) return;
-    const int b = a.by_T(tok), t = tok - b * a.T;
-    if (a.n && t >= a.n[b]) return;
     const bool turned = lane * 8 < a.rot;
     // the lane's two groups of four dimensions
     const int d0 = kInter || !turned ? lane * 8 : lane * 4;
     const int d1 = kInter || !turned ? d0 + 4 : half + d0;
-    float cs[8];
-    if (turned) {
-        *reinterpret_cast<float4 *>(cs) = turns[j][0][lane];
-        *reinterpret_cast<float4 *>(cs + 4) = turns[j][1][lane];
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; i++) cs[2 * i] = 1.f, cs[2 * i + 1] = 0.f;
-    }
-    const unsigned mates = team & 1 ? 0xffff0000u : 0x0000ffffu;
-    const int G = a.G, nq = a.Hkv * G, all = nq + 2 * a.Hkv;
-    const int end = min(all, (int)(blockIdx.y + 1) * rows_per_block);
-    const uint16_t *src = a.qkv + (int64_t)tok * a.row_stride;
-    const int64_t unit = (int64_t)b * a.units + a.first_unit;
-    for (int r = blockIdx.y * rows_per_block + team % kPer; r < end; r += kPer) {
-        const int kind = r < nq ? 0 : r < nq + a.Hkv ? 1 : 2;
-        uint16_t *dst;
-        if (kind == 0) {
-            const int g = r / G;
-            dst = a.q ? a.q + (((unit + g) * a.T + t) * G + (r - g * G)) * kD : nullptr;
-        } else {
-            dst = kind == 1 ? a.k : a.v;
-            if (dst) dst += ((unit + (r - nq) % a.Hkv) * a.T + t) * kD;
+    // a thread has one pair's turns: of token tid / 64 of the tile
+    const int pair = tid & 63, pair_tok = tid >> 6;
+    const bool turns_it = pair < half;
+    const uint64_t fraction = turns_it ? turn_fraction(a.inv_freq[pair]) : 0;
+    const int G = 1 << a.gshift, nq = a.Hkv << a.gshift, nk = nq + a.Hkv;
+    const int r0 = blockIdx.y * rows, r1 = min(nk + a.Hkv, r0 + rows);
+    const int turn0 = max(r0, a.q ? 0 : nq), turn1 = min(r1, a.k ? nk : nq);    // rows that turn
+    const int copy0 = a.v ? max(r0, nk) : r1;                                   // rows that do not
+
+    int buf = 0;
+    for (int tok0 = blockIdx.x * kTok; tok0 < tokens; tok0 += gridDim.x * kTok, buf ^= 1) {
+        if (turns_it && tok0 + pair_tok < tokens) {
+            const uint64_t at = (uint64_t)(int64_t)a.pos[tok0 + pair_tok] * fraction;
+            float s, c;
+            sincospif(__ll2float_rn((long long)at) * 1.0842021724855044e-19f, &s, &c);   // 2^-63
+            float2 *to = reinterpret_cast<float2 *>(&turns[buf][pair_tok][(pair >> 1) & 1][pair >> 2]);
+            to[pair & 1] = make_float2(c * a.scale, s * a.scale);
         }
-        if (!dst) continue;
-        const uint16_t *x = src + r * kD;
-        const uint2 w0 = __ldg(reinterpret_cast<const uint2 *>(x + d0));
-        const uint2 w1 = __ldg(reinterpret_cast<const uint2 *>(x + d1));
-        if (kind == 2) {
-            *reinterpret_cast<uint2 *>(dst + d0) = w0;
-            *reinterpret_cast<uint2 *>(dst + d1) = w1;
-            continue;
+        __syncthreads();
+        const int j = team / kPer, tok = tok0 + j;
+        if (tok >= tokens) continue;
+        const int b = a.by_T(tok), t = tok - b * a.T;
+        if (a.n && t >= a.n[b]) continue;
+        const uint16_t *src = a.qkv + (int64_t)tok * a.row_stride;
+        const int64_t row = ((int64_t)b * a.units + a.first_unit) * a.T + t;   // of KV head 0 in k and v
+        const int first = team % kPer;
+#pragma unroll 1
+        for (int keys = 0; keys < 2; keys++) {
+            const int from = keys ? max(turn0, nq) : turn0, upto = keys ? turn1 : min(turn1, nq);
+            if (from + first >= upto) continue;
+            // a turn after the weights: (y_1, y_2) -> (A y_1 - B y_2, C y_2 + D y_1)
+            const uint16_t *weight = keys ? a.kw : a.qw;
+            float A[4], B[4], C[4], E[4];
+            {
+                float g[8];
+#pragma unroll
+                for (int i = 0; i < 8; i++) g[i] = 1.f;
+                if (weight) {
+                    unpack4(__ldg(reinterpret_cast<const uint2 *>(weight + d0)), g);
+                    unpack4(__ldg(reinterpret_cast<const uint2 *>(weight + d1)), g + 4);
+                }
+                float cs[8];
+                if (turned) {
+                    *reinterpret_cast<float4 *>(cs) = turns[buf][j][0][lane];
+                    *reinterpret_cast<float4 *>(cs + 4) = turns[buf][j][1][lane];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; i++) cs[2 * i] = 1.f, cs[2 * i + 1] = 0.f;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const float g1 = g[kInter ? 2 * e : e], g2 = g[kInter ? 2 * e + 1 : e + 4];
+                    A[e] = g1 * cs[2 * e], B[e] = -(g2 * cs[2 * e + 1]);
+                    C[e] = g2 * cs[2 * e], E[e] = g1 * cs[2 * e + 1];
+                }
+            }
+            for (int r = from + first; r < upto; r += kPer * kAhead) {
+                uint2 w[kAhead][2];
+#pragma unroll
+                for (int i = 0; i < kAhead; i++) {
+                    const uint16_t *x = src + min(r + i * kPer, upto - 1) * kD;
+                    w[i][0] = __ldg(reinterpret_cast<const uint2 *>(x + d0));
+                    w[i][1] = __ldg(reinterpret_cast<const uint2 *>(x + d1));
+                }
+                float inv[kAhead];
+                if (weight) {
+#pragma unroll
+                    for (int i = 0; i < kAhead; i++) {
+                        float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int e = 0; e < 4; e++) {
+                            const uint32_t v = e == 0 ? w[i][0].x : e == 1 ? w[i][0].y : e == 2 ? w[i][1].x : w[i][1].y;
+                            const float2 y = make_float2(bf_lo(v), bf_hi(v));
+                            s = fma2(y, y, s);
+                        }
+                        inv[i] = s.x + s.y;
+                    }
+#pragma unroll
+                    for (int m = 8; m; m >>= 1)
+#pragma unroll
+                        for (int i = 0; i < kAhead; i++) inv[i] += __shfl_xor_sync(mates, inv[i], m, 16);
+#pragma unroll
+                    for (int i = 0; i < kAhead; i++) inv[i] = rsqrtf(inv[i] * (1.f / kD) + a.eps);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kAhead; i++) inv[i] = 1.f;
+                }
+#pragma unroll
+                for (int i = 0; i < kAhead; i++) {
+                    const int at = r + i * kPer;
+                    if (at >= upto) break;
+                    const float2 n2 = make_float2(inv[i], inv[i]);
+                    float2 y[4], z[4];
+                    y[0] = mul2(make_float2(bf_lo(w[i][0].x), bf_hi(w[i][0].x)), n2);
+                    y[1] = mul2(make_float2(bf_lo(w[i][0].y), bf_hi(w[i][0].y)), n2);
+                    y[2] = mul2(make_float2(bf_lo(w[i][1].x), bf_hi(w[i][1].x)), n2);
+                    y[3] = mul2(make_float2(bf_lo(w[i][1].y), bf_hi(w[i][1].y)), n2);
+                    if (kInter) {
+#pragma unroll
+                        for (int e = 0; e < 4; e++)
+                            z[e] = fma2(make_float2(B[e], E[e]), make_float2(y[e].y, y[e].x),
+                                        mul2(make_float2(A[e], C[e]), y[e]));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 2; e++) {
+                            z[e] = fma2(make_float2(B[2 * e], B[2 * e + 1]), y[e + 2],
+                                        mul2(make_float2(A[2 * e], A[2 * e + 1]), y[e]));
+                            z[e + 2] = fma2(make_float2(E[2 * e], E[2 * e + 1]), y[e],
+                                            mul2(make_float2(C[2 * e], C[2 * e + 1]), y[e + 2]));
+                        }
+                    }
+                    uint16_t *dst = keys ? a.k + (row + (int64_t)(at - nq) * a.T) * kD
+                                         : a.q + (((row + (int64_t)(at >> a.gshift) * a.T) << a.gshift) + (at & (G - 1))) * kD;
+                    *reinterpret_cast<uint2 *>(dst + d0) = make_uint2(to_bf16x2(z[0].x, z[0].y), to_bf16x2(z[1].x, z[1].y));
+                    *reinterpret_cast<uint2 *>(dst + d1) = make_uint2(to_bf16x2(z[2].x, z[2].y), to_bf16x2(z[3].x, z[3].y));
+                }
+            }
         }
-        float y[8];
-        unpack4(w0, y);
-        unpack4(w1, y + 4);
-        const uint16_t *weight = kind == 0 ? a.qw : a.kw;
-        if (weight) {
-            float s = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; i++) s = fmaf(y[i], y[i], s);
-#pragma unroll
-            for (int m = 8; m; m >>= 1) s += __shfl_xor_sync(mates, s, m, 16);
-            const float inv = 1.f / sqrtf(s * (1.f / kD) + a.eps);
-            float w[8];
-            unpack4(__ldg(reinterpret_cast<const uint2 *>(weight + d0)), w);
-            unpack4(__ldg(reinterpret_cast<const uint2 *>(weight + d1)), w + 4);
-#pragma unroll
-            for (int i = 0; i < 8; i++) y[i] *= inv * w[i];
-        }
-        float z[8];
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const int i1 = kInter ? 2 * i : i, i2 = kInter ? 2 * i + 1 : i + 4;
-            z[i1] = y[i1] * cs[2 * i] - y[i2] * cs[2 * i + 1];
-            z[i2] = y[i2] * cs[2 * i] + y[i1] * cs[2 * i + 1];
-        }
-        *reinterpret_cast<uint2 *>(dst + d0) = make_uint2(to_bf16x2(z[0], z[1]), to_bf16x2(z[2], z[3]));
-        *reinterpret_cast<uint2 *>(dst + d1) = make_uint2(to_bf16x2(z[4], z[5]), to_bf16x2(z[6], z[7]));
+        for (int r = copy0 + first; r < r1; r += kPer)
+            *reinterpret_cast<uint4 *>(a.v + (row + (int64_t)(r - nk) * a.T) * kD + lane * 8) =
+                __ldg(reinterpret_cast<const uint4 *>(src + r * kD + lane * 8));
     }
 }
 
@@ -157,7 +219,7 @@ cudaError_t launch_qk_norm_rope(const kvc_rope &r, int B, int T, const uint16_t 
     a.v = v;
     a.T = T;
     a.Hkv = r.Hkv;
-    a.G = r.Hq / r.Hkv;
+    while (r.Hkv << a.gshift < r.Hq) a.gshift++;
     a.rot = r.rot;
     a.units = r.units;
     a.first_unit = r.first_unit;
@@ -165,9 +227,15 @@ cudaError_t launch_qk_norm_rope(const kvc_rope &r, int B, int T, const uint16_t 
     a.scale = r.scale;
     a.by_T = FastDiv((uint32_t)T);
     const int tokens = B * T, rows = r.Hq + 2 * r.Hkv;
-    const dim3 grid(tokens, (rows + kTeams - 1) / kTeams);
-    return r.interleaved ? launch_following(rope_kernel<1, true>, grid, kThreads, 0, st, a, tokens, kTeams)
-                         : launch_following(rope_kernel<1, false>, grid, kThreads, 0, st, a, tokens, kTeams);
+    // Persistent blocks, four per SM (16 or 54 per SM in turn: within 3 %).  Few tokens: a token's
+    // rows go to several blocks, as many as fill the device (384 tokens of 48 rows: three blocks
+    // 10.2, one 12.3 us; 1024: two 12.5, three 14.3, one 14.3; 4096: one 26.6, three 28.8)
+    const int tiles = (tokens - 1) / kTok + 1, fill = 152 * kResident;
+    const int cuts = std::max(1, std::min((rows + kTeams - 1) / kTeams, fill / tiles));
+    const int each = ((rows - 1) / cuts / kTeams + 1) * kTeams;
+    const dim3 grid(std::min(tiles, fill), (rows - 1) / each + 1);
+    return r.interleaved ? launch_following(rope_kernel<true>, grid, kThreads, 0, st, a, tokens, each)
+                         : launch_following(rope_kernel<false>, grid, kThreads, 0, st, a, tokens, each);
 }
 
 }  // namespace kvc
