@@ -181,7 +181,7 @@ kvc_status kvc_page_attend(const kvc_pages *pg, int32_t G, int32_t max_len, cons
     PG_CHECK(max_len >= 1 && max_len <= (int64_t)pg->stride * pg->page, KVC_ERR_SHAPE,
              "%s: max_len = %d must satisfy 1 <= max_len <= stride * page = %lld", fn, max_len,
              (long long)pg->stride * pg->page);
-    PG_CHECK(launchable(pg->U, (max_len + 63ll) / 64), KVC_ERR_UNSUPPORTED,
+    PG_CHECK(launchable(pg->U, (max_len + 15ll) / 16), KVC_ERR_UNSUPPORTED,
              "%s: max_len = %d of U = %d units unsupported", fn, max_len, pg->U);
     PG_CHECK(q && o && lse, KVC_ERR_INVALID_ARG, "%s: q, o and lse must be non-NULL", fn);
     PG_CHECK((k_new == nullptr) == (v_new == nullptr), KVC_ERR_INVALID_ARG,

@@ -24,13 +24,14 @@
 // not the largest weight, is near 1 in f16: a row of huge values that weighs
 // nothing does not push the others below f16's range.
 //
-// The reference moves only when a logit passes it by 2^8: one vote per tile in
-// place of six exchanges, and the sums are rarely scaled.
+// The reference moves only when a weight passes 2^8: one vote per tile in place of
+// six exchanges, and the sums are rarely scaled.
 //
-// Work: tiles of all units form one line, cut into equal parts for a fixed number
-// of persistent CTAs (three per SM), whatever bound the caller gives for the
-// lengths.  A unit that is cut leaves its parts in the workspace; the CTA that
-// comes last joins them in the order of the line, so results do not depend on it.
+// Work: tiles of 16 (bf16) or 32 slots of all units form one line, cut into equal
+// parts for a fixed number of warps, whatever bound the caller gives for the
+// lengths.  A warp walks its part alone, without a barrier, the next tile's rows
+// on their way in registers across the ends of units.  A unit that is cut leaves
+// its parts in the workspace, which a second kernel joins in the order of the line.
 #include "kvc_page.h"
 
 #include <cuda_fp16.h>
@@ -39,10 +40,9 @@
 namespace kvc {
 namespace {
 
-constexpr int kThreads = 128, kWarps = kThreads / 32;
-constexpr int kGrid = 152 * 3;
+constexpr int kThreads = 128, kWarps = kThreads / 32, kJoin = 256;
+constexpr int kResident = 3, kGrid = 152 * kResident, kWorkers = kGrid * kWarps;
 constexpr int kHeads = 8;                        // columns of the products
-constexpr int kPad = kD + 2;                     // row of a head in shared memory
 constexpr float kSlack = 8.f;                    // log2 that a logit may pass the reference by
 
 struct AttendArgs {
@@ -50,8 +50,9 @@ struct AttendArgs {
     const uint16_t *q, *k_new, *v_new;
     uint16_t *o;
     float *lse;
-    int32_t *status, *arrived, *part_bad;        // [U], [2 kGrid]
-    float *part_o, *part_ml;                     // [2 kGrid][G][d], [2 kGrid][G][2]
+    int32_t *status, *part_bad;                  // [2 kWorkers]
+    int2 *cuts;                                  // [U] the first and the last worker that has a part
+    float *part_o, *part_ml;                     // [2 kWorkers][G][d], [2 kWorkers][G][2]
     int S, G, max_len;
 };
 
@@ -63,6 +64,14 @@ __device__ __forceinline__ uint4 ldg16(const void *p)
                  : "l"(p));
     return r;
 }
+
+// 16 bytes to shared memory in the background
+__device__ __forceinline__ void copy16(void *dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t word(const uint4 &r, int i)
 {
@@ -108,6 +117,14 @@ __device__ __forceinline__ void two_terms(float a, float b, uint32_t &hi, uint32
     }
 }
 
+// 2^x; results below fp32's normal range are zero
+__device__ __forceinline__ float pow2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // log2 of a power of two above the scale, at least -100: weights over the reference
 // are then at most 2^100, and their sum stays in range
 __device__ __forceinline__ float scale_log2(float s)
@@ -115,13 +132,20 @@ __device__ __forceinline__ float scale_log2(float s)
     return fmaxf((float)((int)(__float_as_uint(s) >> 23) - 126), -100.f);
 }
 
+// four e4m3 values as f16 (exact): the low two, the high two
+__device__ __forceinline__ void e4m3_to_f16x4(uint32_t w, uint32_t &lo, uint32_t &hi)
+{
+    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+
 struct Shared {
-    float o[kWarps][kHeads * kPad];
-    float m[kWarps][kHeads], l[kWarps][kHeads];
-    __align__(16) uint8_t row[2][kD * 2];        // the new token's key and value as held
-    float row_scale[2];
+    __align__(16) uint16_t q[kWarps][2][kHeads * kD];      // queries of the unit at hand and of the next
+    __align__(16) uint16_t fresh[kWarps][2][kD];           // the new token's key and value
+    __align__(16) uint8_t row[kWarps][2][kD * 2];          // as they are held
     int scratch[33];
-    int seq, at, last;
+    int seq[kWarps], at[kWarps];
 };
 
 // What a lane holds of the slots a warp has of a tile: kBlocks blocks of 16.
@@ -129,61 +153,248 @@ template <bool kE4m3>
 struct Frags {
     static constexpr int kBlocks = kE4m3 ? 2 : 1;
     static constexpr int kSlots = 16 * kBlocks;
-    uint4 k[8], v[8];
-    float ks[4], vs[4];
+    static constexpr int kRow = kE4m3 ? kD : kD * 2;       // bytes
+    static constexpr int kK = kRow / 64, kV = kRow / 128;  // a lane's pieces of a key, of a value
+    uint4 k[kBlocks * 2 * kK], v[kBlocks * 4 * kV];
+    float ks[kBlocks * 2], vs[kBlocks * 2];
 };
 
-template <bool kE4m3>
-__global__ void __launch_bounds__(kThreads, 3) attend_kernel(const __grid_constant__ AttendArgs a)
+// A walk along the line, a tile at a time.
+struct Walk {
+    int s, h, n, tiles, tile;                    // sequence, head, its length, a unit's tiles, the tile
+    int ahead;                                   // the next sequence's length
+};
+
+// The parts of units that were cut, joined in the order of the line.  kWide: a block
+// per row (unit and head), its warps a share of the parts each; else a warp per row.
+// Four dimensions a lane; weights of 32 parts are formed in the lanes, their sums
+// added up with 8 loads in flight.
+template <bool kWide>
+__global__ void __launch_bounds__(kJoin) join_kernel(const __grid_constant__ AttendArgs a)
+{
+    __shared__ float4 sums[kJoin / 32][32];
+    __shared__ float part_l[kJoin / 32];
+    follow();
+    lead();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = a.G, rows = a.S * a.pg.heads * G;
+    constexpr int kRows = kWide ? 1 : kJoin / 32, kShares = kWide ? kJoin / 32 : 1;
+    const int share = kWide ? warp : 0;
+    for (int i = blockIdx.x * kRows + (kWide ? 0 : warp); i < rows; i += gridDim.x * kRows) {
+        const int u = i / G, hh = i - u * G;
+        const int2 cut = a.cuts[u];
+        const int n = a.pg.len[a.pg.by_heads(u)];
+        // a unit that was refused has no parts, and what stands in cuts is another call's
+        if (n < 0 || n > a.max_len - (a.k_new != nullptr) || cut.x >= cut.y) continue;
+        const int parts = cut.y - cut.x + 1;
+        auto slot = [&](int p) { return 2 * (cut.x + p) + (p == 0); };
+        float M = -INFINITY, L = 0.f;
+        bool wrong = false;
+        for (int p = lane; p < parts; p += 32) {
+            M = fmaxf(M, a.part_ml[((size_t)slot(p) * G + hh) * 2]);
+            wrong |= a.part_bad[slot(p)] != 0;
+        }
+        M = warp_max(M);
+        if (__any_sync(kFull, wrong)) {
+            if (lane == 0) record_status(a.status, KVC_ERR_INVALID_ARG);
+            continue;
+        }
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int mine = (parts - 1) / kShares + 1, end = min(parts, (share + 1) * mine);
+        for (int p0 = share * mine; p0 < end; p0 += 32) {
+            float2 ml = make_float2(-INFINITY, 0.f);
+            if (p0 + lane < end)
+                ml = *reinterpret_cast<const float2 *>(a.part_ml + ((size_t)slot(p0 + lane) * G + hh) * 2);
+            const float r = ml.x == -INFINITY ? 0.f : pow2(ml.x - M);       // 0 keeps a NaN
+            L += warp_sum(r * ml.y);
+            const int some = min(32, end - p0);
+            for (int j0 = 0; j0 < some; j0 += 8) {
+                float4 x[8];
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+                    if (j0 + j < some)
+                        x[j] = *reinterpret_cast<const float4 *>(
+                            a.part_o + ((size_t)slot(p0 + j0 + j) * G + hh) * kD + lane * 4);
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    const float f = __shfl_sync(kFull, r, j0 + j);
+                    if (j0 + j < some)
+                        o = make_float4(fmaf(f, x[j].x, o.x), fmaf(f, x[j].y, o.y), fmaf(f, x[j].z, o.z),
+                                        fmaf(f, x[j].w, o.w));
+                }
+            }
+        }
+        if (kWide) {
+            sums[warp][lane] = o;
+            if (lane == 0) part_l[warp] = L;
+            __syncthreads();
+            if (warp == 0) {
+#pragma unroll
+                for (int w = 1; w < kShares; w++) {
+                    const float4 x = sums[w][lane];
+                    o = make_float4(o.x + x.x, o.y + x.y, o.z + x.z, o.w + x.w);
+                    L += part_l[w];
+                }
+            }
+            __syncthreads();
+        }
+        if (share == 0) {
+            const float inv = M == -INFINITY && L == 0.f ? 0.f : 1.f / L;
+            *reinterpret_cast<uint2 *>(a.o + (size_t)i * kD + lane * 4) =
+                make_uint2(to_bf16x2(o.x * inv, o.y * inv), to_bf16x2(o.z * inv, o.w * inv));
+            if (lane == 0) a.lse[i] = (M + log2f(L)) * 0.6931471805599453f;
+        }
+    }
+}
+
+// kFew: at most four heads, whose weights' two terms are columns h and h + 4 of one
+// product.
+template <bool kE4m3, bool kFew>
+__global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __grid_constant__ AttendArgs a)
 {
     using F = Frags<kE4m3>;
-    constexpr int kTile = kWarps * F::kSlots;
-    constexpr int kBytes = kE4m3 ? kD : kD * 2;
+    constexpr int kBlocks = F::kBlocks, kTile = F::kSlots, kRow = F::kRow;
     __shared__ Shared sm;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kFull, tid >> 5, 0);   // uniform
     const int g = lane >> 2, c = lane & 3;
     const int app = a.k_new != nullptr, heads = a.pg.heads, G = a.G;
     follow();
     lead();
 
-    // the line: tiles of every sequence's units in order
-    auto tiles_of = [&](int s) {
-        const int n = a.pg.len[s];
-        if (n < 0 || n > a.max_len - app) return 0;
-        return max(1, (n + app + kTile - 1) / kTile);
-    };
+    // the line: tiles of every sequence's units in order, cut into equal parts for the warps
+    auto length = [&](int s) { return s < a.S ? a.pg.len[s] : 0; };
+    auto tiles_of = [&](int n) { return n < 0 || n > a.max_len - app ? 0 : max(1, (n + app + kTile - 1) / kTile); };
     const int each = (a.S + kThreads - 1) / kThreads;
     const int s0 = min(a.S, tid * each), s1 = min(a.S, s0 + each);
-    int mine = 0;
+    int mine = 0, refused = 0;
+#pragma unroll 8
     for (int s = s0; s < s1; s++) {
-        const int t = tiles_of(s);
-        if (t == 0 && blockIdx.x == 0) record_status(a.status, KVC_ERR_SHAPE);
+        const int t = tiles_of(a.pg.len[s]);
+        refused |= t == 0;
         mine += t * heads;
     }
+    if (refused && blockIdx.x == 0) record_status(a.status, KVC_ERR_SHAPE);
     int total;
     const int before = block_exscan(mine, sm.scratch, &total);
-    const LineCuts cuts(gridDim.x, total);
-    if ((int)blockIdx.x >= cuts.parts) return;
-    int t = cuts.start(blockIdx.x);
-    const int t_end = cuts.start(blockIdx.x + 1);
-    if (t >= before && t < before + mine) {
-        int at = before, s = s0, w;
-        while (at + (w = tiles_of(s) * heads) <= t) at += w, s++;
-        sm.seq = s;
-        sm.at = at;
+    const LineCuts cuts(gridDim.x * kWarps, total);
+#pragma unroll
+    for (int w = 0; w < kWarps; w++) {
+        const int id = w * gridDim.x + blockIdx.x, t = cuts.start(id);
+        if (id < cuts.parts && t >= before && t < before + mine) {
+            int at = before, s = s0, size;
+            while (at + (size = tiles_of(a.pg.len[s]) * heads) <= t) at += size, s++;
+            sm.seq[w] = s;
+            sm.at[w] = at;
+        }
     }
     __syncthreads();
-    int s = sm.seq, unit_at = sm.at, tiles = tiles_of(s);
-    int h = (t - unit_at) / tiles;
-    unit_at += h * tiles;
+    const int id = warp * gridDim.x + blockIdx.x;          // few tiles go to as many SMs as there are
+    if (id >= cuts.parts) return;
+    int t = cuts.start(id);
+    const int t_end = cuts.start(id + 1);
+    Walk cur;                                    // the unit at hand
+    cur.s = sm.seq[warp];
+    cur.n = length(cur.s);
+    cur.ahead = length(cur.s + 1);
+    cur.tiles = tiles_of(cur.n);
+    int unit_at = sm.at[warp];                   // the unit's first tile on the line
+    cur.h = (t - unit_at) / cur.tiles;
+    unit_at += cur.h * cur.tiles;
+    cur.tile = t - unit_at;
+    auto next_unit = [&](Walk &w) {
+        w.tile = 0;
+        if (++w.h < heads) return;
+        w.h = 0;
+        do {
+            w.s++;
+            w.n = w.ahead;
+            w.ahead = length(w.s + 1);
+            w.tiles = tiles_of(w.n);
+        } while (w.tiles == 0 && w.s < a.S);
+    };
 
+    // the tile after the one at hand is on its way, its successor's pages are known
+    Walk far = cur;
+    int far_left = t_end - t;
+    int far_h = 0, far_slot = 0, far_live = 0, ids[kBlocks];       // of what is loaded next
+    bool far_bad = false;
+    F f;
+    auto look_up = [&]() {
+        far_h = far.h;
+        far_slot = far.tile * kTile;
+        far_live = far_left > 0 ? far.n - far_slot : 0;           // slots from far_slot on that hold a row
+#pragma unroll
+        for (int b = 0; b < kBlocks; b++) ids[b] = far_live > 16 * b ? a.pg.entry(far.s, far_slot + 16 * b) : 0;
+        if (--far_left > 0 && ++far.tile == far.tiles) next_unit(far);
+    };
+    auto load = [&](bool keys) {
+#pragma unroll
+        for (int b = 0; b < kBlocks; b++) {
+            int live = far_live - 16 * b;
+            const bool ok = a.pg.in_pool(ids[b]);
+            if (live > 0 && !ok) far_bad = true, live = 0;
+            const size_t row = live > 0 ? a.pg.row(ids[b], far_h, far_slot + 16 * b) : 0;
+            if (keys) {
+                const uint8_t *p = a.pg.K + (row + g) * kRow + c * 16;
+                const float *ps = a.pg.ks + row + g, *pv = a.pg.vs + row + g;
+                if (live >= 16) {
+#pragma unroll
+                    for (int r = 0; r < 2; r++) {
+#pragma unroll
+                        for (int j = 0; j < F::kK; j++) f.k[(b * 2 + r) * F::kK + j] = ldg16(p + r * 8 * kRow + j * 64);
+                        if (kE4m3) f.ks[b * 2 + r] = ps[8 * r], f.vs[b * 2 + r] = pv[8 * r];
+                    }
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 2; r++) {
+                        const bool on = g + 8 * r < live;
+#pragma unroll
+                        for (int j = 0; j < F::kK; j++)
+                            f.k[(b * 2 + r) * F::kK + j] = on ? ldg16(p + r * 8 * kRow + j * 64) : make_uint4(0, 0, 0, 0);
+                        if (kE4m3) f.ks[b * 2 + r] = on ? ps[8 * r] : 0.f, f.vs[b * 2 + r] = on ? pv[8 * r] : 0.f;
+                    }
+                }
+            } else {
+                const uint8_t *p = a.pg.V + (row + 2 * c) * kRow + g * 16;
+                if (live >= 16) {
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+#pragma unroll
+                        for (int j = 0; j < F::kV; j++)
+                            f.v[(b * 4 + i) * F::kV + j] = ldg16(p + ((i & 1) + 8 * (i >> 1)) * kRow + j * 128);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const int r = (i & 1) + 8 * (i >> 1);
+#pragma unroll
+                        for (int j = 0; j < F::kV; j++)
+                            f.v[(b * 4 + i) * F::kV + j] =
+                                2 * c + r < live ? ldg16(p + r * kRow + j * 128) : make_uint4(0, 0, 0, 0);
+                    }
+                }
+            }
+        }
+    };
+    // the queries of a unit to shared memory
+    auto fetch_q = [&](int buf, int u) {
+        for (int i = lane; i < G * 16; i += 32) copy16(sm.q[warp][buf] + i * 8, a.q + (size_t)u * G * kD + i * 8);
+    };
+    int qbuf = 0;
+    fetch_q(0, cur.s * heads + cur.h);
+    look_up();
+    load(true);
+    load(false);
+    look_up();
+
+    const int head = kFew ? g & 3 : g;           // of the column that the lane's queries are
     const float log2e_d = 0.08838834764831845f * 1.4426950408889634f;   // log2(e) / sqrt(128)
     while (t < t_end) {
-        const int u = s * heads + h, n = a.pg.len[s];
-        const int first = t - unit_at, end = min(t_end - unit_at, tiles);
-        const bool has_new = app && end == tiles;
+        const int u = cur.s * heads + cur.h, n = cur.n, tiles = cur.tiles;
+        const int first = cur.tile, end = min(t_end - unit_at, tiles);
+        const bool has_new = app && end == tiles;          // the new token's slot is in the last tile
+        copies_wait();
+        __syncwarp();
 
-        // queries: the lane's 32 dimensions of head g, in the order of the keys' loads
+        // queries: the lane's 32 dimensions of a head, in the order of the keys' loads
         uint32_t q[8][2];
         float ch0 = log2e_d, ch1 = log2e_d;      // what a product becomes a logit (base 2) by
         {
@@ -191,36 +402,31 @@ __global__ void __launch_bounds__(kThreads, 3) attend_kernel(const __grid_consta
 #pragma unroll
             for (int j = 0; j < 4; j++) {
                 const int d = kE4m3 ? ((j >> 1) * 4 + c) * 16 + (j & 1) * 8 : (j * 4 + c) * 8;
-                w[j] = g < G ? *reinterpret_cast<const uint4 *>(a.q + ((size_t)u * G + g) * kD + d)
-                             : make_uint4(0, 0, 0, 0);
+                w[j] = head < G ? *reinterpret_cast<const uint4 *>(sm.q[warp][qbuf] + head * kD + d) : make_uint4(0, 0, 0, 0);
             }
             if (kE4m3) {
-                float amax = 0.f;
+                uint32_t top = 0;                // magnitudes order as whole numbers
 #pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    float f[8];
-                    unpack8(w[j], f);
-#pragma unroll
-                    for (int i = 0; i < 8; i++) amax = fmaxf(amax, fabsf(f[i]));
-                }
-                amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
-                amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
+                for (int j = 0; j < 4; j++)
+                    top = __vmaxu2(top, __vmaxu2(__vmaxu2(magnitudes(w[j].x), magnitudes(w[j].y)),
+                                                 __vmaxu2(magnitudes(w[j].z), magnitudes(w[j].w))));
+                top = __vmaxu2(top, __shfl_xor_sync(kFull, top, 1));
+                top = __vmaxu2(top, __shfl_xor_sync(kFull, top, 2));
+                top = max(top & 0xffffu, top >> 16) >> 7;      // the exponent
                 // 2^e takes the largest to [2^13, 2^14)
-                const int e = min(13 + 127 - (int)(__float_as_uint(amax) >> 23), 120);
+                const int e = min(13 + 127 - (int)top, 120);
                 const float f2 = __uint_as_float((uint32_t)(e + 127) << 23);
                 const float back = __uint_as_float((uint32_t)(127 - e) << 23);
                 ch0 *= __shfl_sync(kFull, back, 8 * c);
                 ch1 *= __shfl_sync(kFull, back, 8 * c + 4);
 #pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    float f[8];
-                    unpack8(w[j], f);
+                for (int j = 0; j < 4; j++)
 #pragma unroll
                     for (int i = 0; i < 4; i++) {
-                        const __half2 x = __floats2half2_rn(f[2 * i] * f2, f[2 * i + 1] * f2);
+                        const float2 y = scaled2(word(w[j], i), f2);
+                        const __half2 x = __floats2half2_rn(y.x, y.y);
                         q[j * 2 + (i >> 1)][i & 1] = *reinterpret_cast<const uint32_t *>(&x);
                     }
-                }
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
@@ -229,141 +435,108 @@ __global__ void __launch_bounds__(kThreads, 3) attend_kernel(const __grid_consta
                 }
             }
         }
-
-        float acc[8][4] = {}, m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-        F f;
-        int ids[F::kBlocks];
-        bool bad = false;
-        const int mine_end = end + (has_new && warp == 0);   // one turn more, for the new token
-        auto look_up = [&](int tile) {
-#pragma unroll
-            for (int b = 0; b < F::kBlocks; b++) {
-                const int slot = tile * kTile + warp * F::kSlots + 16 * b;
-                ids[b] = tile < end && slot < n ? a.pg.entry(s, slot) : 0;
-            }
-        };
-        // slots of the tile that hold a row, from the lane's point of view: limit - 16 b
-        auto load = [&](int tile, bool keys) {
-#pragma unroll
-            for (int b = 0; b < F::kBlocks; b++) {
-                const int slot = tile * kTile + warp * F::kSlots + 16 * b;
-                int live = tile < end ? n - slot : 0;         // rows of the block
-                const bool ok = a.pg.in_pool(ids[b]);
-                if (live > 0 && !ok) bad = true, live = 0;
-                const size_t row = live > 0 ? a.pg.row(ids[b], h, slot) : 0;
-                if (keys) {
-                    const uint8_t *p = a.pg.K + (row + g) * kBytes + c * 16;
-#pragma unroll
-                    for (int r = 0; r < 2; r++) {
-                        const bool on = g + 8 * r < live;
-#pragma unroll
-                        for (int j = 0; j < 4 / F::kBlocks; j++)
-                            f.k[(b * 2 + r) * (4 / F::kBlocks) + j] =
-                                on ? ldg16(p + r * 8 * kBytes + j * 64) : make_uint4(0, 0, 0, 0);
-                        if (kE4m3) {
-                            f.ks[b * 2 + r] = on ? a.pg.ks[row + g + 8 * r] : 0.f;
-                            f.vs[b * 2 + r] = on ? a.pg.vs[row + g + 8 * r] : 0.f;
-                        }
-                    }
-                } else {
-                    const uint8_t *p = a.pg.V + (row + 2 * c) * kBytes + g * 16;
-#pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        const int r = (i & 1) + 8 * (i >> 1);
-                        const bool on = 2 * c + r < live;
-#pragma unroll
-                        for (int j = 0; j < 2 / F::kBlocks; j++)
-                            f.v[(b * 4 + i) * (2 / F::kBlocks) + j] =
-                                on ? ldg16(p + r * kBytes + j * 128) : make_uint4(0, 0, 0, 0);
-                    }
-                }
-            }
-        };
-
-        look_up(first);
-        load(first, true);
-        load(first, false);
-        look_up(first + 1);
-        if (has_new && warp == 0) {
-            // the new token's row: to its page, and to shared memory for the turn behind the last
-            const int page = a.pg.entry(s, n);
-            const bool ok = a.pg.in_pool(page);
-            bad |= !ok;
-            const size_t row = ok ? a.pg.row(page, h, n) : 0;
-#pragma unroll
-            for (int i = 0; i < 2; i++) {
-                const uint2 w = *reinterpret_cast<const uint2 *>((i ? a.v_new : a.k_new) + (size_t)u * kD + lane * 4);
-                uint8_t *pool = i ? a.pg.V : a.pg.K;
-                if (kE4m3) {
-                    uint32_t top = __vmaxu2(magnitudes(w.x), magnitudes(w.y));
-#pragma unroll
-                    for (int j = 16; j; j >>= 1) top = __vmaxu2(top, __shfl_xor_sync(kFull, top, j));
-                    const float scale = row_scale(__uint_as_float(max(top << 16, top & 0xffff0000u)));
-                    const uint32_t v = quantise4(w.x, w.y, __fdiv_rn(1.f, scale));
-                    reinterpret_cast<uint32_t *>(sm.row[i])[lane] = v;
-                    if (lane == 0) sm.row_scale[i] = scale;
-                    if (ok) {
-                        *reinterpret_cast<uint32_t *>(pool + row * kBytes + lane * 4) = v;
-                        if (lane == 0) (i ? a.pg.vs : a.pg.ks)[row] = scale;
-                    }
-                } else {
-                    reinterpret_cast<uint2 *>(sm.row[i])[lane] = w;
-                    if (ok) *reinterpret_cast<uint2 *>(pool + row * kBytes + lane * 8) = w;
-                }
-            }
-            __syncwarp();
+        // what the unit's end and the next unit need comes in the background
+        int fresh_page = 0;
+        if (has_new) {
+            copy16(sm.fresh[warp][lane >> 4] + (lane & 15) * 8,
+                   (lane < 16 ? a.k_new : a.v_new) + (size_t)u * kD + (lane & 15) * 8);
+            fresh_page = a.pg.entry(cur.s, n);
+        }
+        if (unit_at + tiles < t_end) {
+            Walk then = cur;
+            next_unit(then);
+            fetch_q(qbuf ^ 1, then.s * heads + then.h);
         }
 
-        for (int tile = first; tile < mine_end; tile++) {
-            const bool extra = tile == end;
-            int live = extra ? 1 : n - (tile * kTile + warp * F::kSlots);
-            if (extra) {
-                // the new token alone: row 0 of the block
-                const uint4 none = make_uint4(0, 0, 0, 0);
+        float acc[8][4] = {}, m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+        bool bad = false;
+        for (int tile = first; tile < end; tile++) {
+            int live = n - tile * kTile;
+            bad |= far_bad;
+            far_bad = false;
+            if (has_new && tile + 1 == end) {
+                // the new token's row: to its page, and into the registers as it is held
+                const bool ok = a.pg.in_pool(fresh_page);
+                bad |= !ok;
+                const size_t row = ok ? a.pg.row(fresh_page, cur.h, n) : 0;
+                copies_wait();
+                __syncwarp();
+                float sc[2] = {};
 #pragma unroll
-                for (int j = 0; j < 8; j++) f.k[j] = f.v[j] = none;
-                if (g == 0)
+                for (int i = 0; i < 2; i++) {
+                    const uint2 w = reinterpret_cast<const uint2 *>(sm.fresh[warp][i])[lane];
+                    uint8_t *pool = i ? a.pg.V : a.pg.K;
+                    if (kE4m3) {
+                        uint32_t top = __vmaxu2(magnitudes(w.x), magnitudes(w.y));
 #pragma unroll
-                    for (int j = 0; j < 4 / F::kBlocks; j++) f.k[j] = lds_v4(sm.row[0] + c * 16 + j * 64);
-                if (c == 0)
+                        for (int j = 16; j; j >>= 1) top = __vmaxu2(top, __shfl_xor_sync(kFull, top, j));
+                        sc[i] = row_scale(__uint_as_float(max(top << 16, top & 0xffff0000u)));
+                        const uint32_t v = quantise4(w.x, w.y, __fdiv_rn(1.f, sc[i]));
+                        reinterpret_cast<uint32_t *>(sm.row[warp][i])[lane] = v;
+                        if (ok) {
+                            *reinterpret_cast<uint32_t *>(pool + row * kRow + lane * 4) = v;
+                            if (lane == 0) (i ? a.pg.vs : a.pg.ks)[row] = sc[i];
+                        }
+                    } else {
+                        reinterpret_cast<uint2 *>(sm.row[warp][i])[lane] = w;
+                        if (ok) *reinterpret_cast<uint2 *>(pool + row * kRow + lane * 8) = w;
+                    }
+                }
+                __syncwarp();
 #pragma unroll
-                    for (int j = 0; j < 2 / F::kBlocks; j++) f.v[j] = lds_v4(sm.row[1] + g * 16 + j * 128);
-                f.ks[0] = sm.row_scale[0], f.vs[0] = sm.row_scale[1];
+                for (int b = 0; b < kBlocks; b++) {
+                    const int at = live - 16 * b;                  // its place in the block
+#pragma unroll
+                    for (int r = 0; r < 2; r++)
+                        if (at == g + 8 * r) {
+#pragma unroll
+                            for (int j = 0; j < F::kK; j++) f.k[(b * 2 + r) * F::kK + j] = lds_v4(sm.row[warp][0] + c * 16 + j * 64);
+                            f.ks[b * 2 + r] = sc[0], f.vs[b * 2 + r] = sc[1];
+                        }
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        if (at == 2 * c + (i & 1) + 8 * (i >> 1))
+#pragma unroll
+                            for (int j = 0; j < F::kV; j++) f.v[(b * 4 + i) * F::kV + j] = lds_v4(sm.row[warp][1] + g * 16 + j * 128);
+                }
+                live++;
             }
             // S' = K Q'
-            float x[F::kBlocks][4];
+            float x[kBlocks][4];
 #pragma unroll
-            for (int b = 0; b < F::kBlocks; b++) {
+            for (int b = 0; b < kBlocks; b++) {
                 float y[4] = {};
                 x[b][0] = x[b][1] = x[b][2] = x[b][3] = 0.f;
 #pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    float *to = i & 1 ? y : x[b];
+                for (int j = 0; j < F::kK; j++) {
+                    const uint4 &r0 = f.k[b * 2 * F::kK + j], &r1 = f.k[(b * 2 + 1) * F::kK + j];
                     if (kE4m3) {
-                        const uint32_t r0 = word(f.k[b * 4 + (i >> 2)], i & 3);
-                        const uint32_t r1 = word(f.k[b * 4 + 2 + (i >> 2)], i & 3);
-                        mma<true>(to, e4m3_to_f16x2(r0), e4m3_to_f16x2(r1), e4m3_to_f16x2(r0 >> 16),
-                                  e4m3_to_f16x2(r1 >> 16), q[i][0], q[i][1]);
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            uint32_t a0, a1, a2, a3;
+                            e4m3_to_f16x4(word(r0, i), a0, a2);
+                            e4m3_to_f16x4(word(r1, i), a1, a3);
+                            mma<true>(i & 1 ? y : x[b], a0, a1, a2, a3, q[j * 4 + i][0], q[j * 4 + i][1]);
+                        }
                     } else {
-                        const uint4 &r0 = f.k[i >> 1], &r1 = f.k[4 + (i >> 1)];
-                        mma<false>(to, word(r0, 2 * (i & 1)), word(r1, 2 * (i & 1)), word(r0, 2 * (i & 1) + 1),
-                                   word(r1, 2 * (i & 1) + 1), q[i][0], q[i][1]);
+                        mma<false>(x[b], r0.x, r1.x, r0.y, r1.y, q[2 * j][0], q[2 * j][1]);
+                        mma<false>(y, r0.z, r1.z, r0.w, r1.w, q[2 * j + 1][0], q[2 * j + 1][1]);
                     }
                 }
 #pragma unroll
                 for (int j = 0; j < 4; j++) x[b][j] += y[j];
             }
             // logits in base 2, what is not there at -inf; the reference's candidates
-            float top0 = -INFINITY, top1 = -INFINITY, vs[4];
+            float top0 = -INFINITY, top1 = -INFINITY, vs[2 * kBlocks];
 #pragma unroll
-            for (int b = 0; b < F::kBlocks; b++)
+            for (int b = 0; b < kBlocks; b++)
 #pragma unroll
                 for (int r = 0; r < 2; r++) {
                     const bool on = 16 * b + 8 * r + g < live;
                     float c0 = ch0, c1 = ch1, up = 0.f;
                     if (kE4m3) {
                         c0 *= f.ks[b * 2 + r], c1 *= f.ks[b * 2 + r];
-                        vs[b * 2 + r] = on ? f.vs[b * 2 + r] : 0.f;
+                        vs[b * 2 + r] = f.vs[b * 2 + r];
                         up = scale_log2(f.vs[b * 2 + r]);
                     }
                     x[b][2 * r] = on ? x[b][2 * r] * c0 : -INFINITY;
@@ -371,9 +544,7 @@ __global__ void __launch_bounds__(kThreads, 3) attend_kernel(const __grid_consta
                     top0 = fmaxf(top0, x[b][2 * r] + up);
                     top1 = fmaxf(top1, x[b][2 * r + 1] + up);
                 }
-            if (!extra) {
-                if (tile + 1 < end) load(tile + 1, true);
-            }
+            load(true);
             if (__any_sync(kFull, top0 > m0 + kSlack || top1 > m1 + kSlack)) {
 #pragma unroll
                 for (int i = 4; i < 32; i <<= 1) {
@@ -381,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 3) attend_kernel(const __grid_consta
                     top1 = fmaxf(top1, __shfl_xor_sync(kFull, top1, i));
                 }
                 const float n0 = fmaxf(m0, top0), n1 = fmaxf(m1, top1);
-                const float r0 = m0 == n0 ? 1.f : exp2f(m0 - n0), r1 = m1 == n1 ? 1.f : exp2f(m1 - n1);
+                const float r0 = m0 == n0 ? 1.f : pow2(m0 - n0), r1 = m1 == n1 ? 1.f : pow2(m1 - n1);
                 m0 = n0, m1 = n1;
                 l0 *= r0, l1 *= r1;
 #pragma unroll
@@ -390,10 +561,10 @@ __global__ void __launch_bounds__(kThreads, 3) attend_kernel(const __grid_consta
             const float ref0 = m0 == -INFINITY ? 0.f : m0, ref1 = m1 == -INFINITY ? 0.f : m1;
             // weights, O' += V' P'
 #pragma unroll
-            for (int b = 0; b < F::kBlocks; b++) {
+            for (int b = 0; b < kBlocks; b++) {
                 float p[4];
 #pragma unroll
-                for (int j = 0; j < 4; j++) p[j] = exp2f(x[b][j] - (j & 1 ? ref1 : ref0));
+                for (int j = 0; j < 4; j++) p[j] = pow2(x[b][j] - (j & 1 ? ref1 : ref0));
                 l0 += p[0] + p[2];
                 l1 += p[1] + p[3];
                 if (kE4m3) {
@@ -403,137 +574,87 @@ __global__ void __launch_bounds__(kThreads, 3) attend_kernel(const __grid_consta
                 uint32_t hi0, lo0, hi1, lo1;
                 two_terms<kE4m3>(p[0], p[1], hi0, lo0);
                 two_terms<kE4m3>(p[2], p[3], hi1, lo1);
+                if (kFew && c >= 2) hi0 = lo0, hi1 = lo1;
                 hi0 = transpose8x8(hi0), hi1 = transpose8x8(hi1);
-                lo0 = transpose8x8(lo0), lo1 = transpose8x8(lo1);
+                if (!kFew) lo0 = transpose8x8(lo0), lo1 = transpose8x8(lo1);
+                // a product's 16 rows are two dimensions of each lane's
 #pragma unroll
                 for (int i = 0; i < 8; i++) {
                     uint32_t a0, a1, a2, a3;
                     if (kE4m3) {
-                        // bytes of two slots side by side, the lane's dimensions 16 g + 2 i, + 1
+                        // bytes of two slots side by side, dimensions 16 g + 2 i, + 1
                         const uint32_t sel = i & 1 ? 0x7362 : 0x5140;
-                        const uint32_t w0 = __byte_perm(word(f.v[b * 4], i >> 1), word(f.v[b * 4 + 1], i >> 1), sel);
-                        const uint32_t w1 =
-                            __byte_perm(word(f.v[b * 4 + 2], i >> 1), word(f.v[b * 4 + 3], i >> 1), sel);
-                        a0 = e4m3_to_f16x2(w0), a1 = e4m3_to_f16x2(w0 >> 16);
-                        a2 = e4m3_to_f16x2(w1), a3 = e4m3_to_f16x2(w1 >> 16);
+                        e4m3_to_f16x4(__byte_perm(word(f.v[b * 4], i >> 1), word(f.v[b * 4 + 1], i >> 1), sel), a0, a1);
+                        e4m3_to_f16x4(__byte_perm(word(f.v[b * 4 + 2], i >> 1), word(f.v[b * 4 + 3], i >> 1), sel), a2, a3);
                     } else {
-                        // the lane's dimensions 8 g + 2 i, + 1 (and 64 on from the fourth)
+                        // dimensions 8 g + 2 i, + 1 (and 64 on from the fourth)
                         const int j = i >> 2, w = i & 3;
-                        a0 = __byte_perm(word(f.v[j], w), word(f.v[2 + j], w), 0x5410);
-                        a1 = __byte_perm(word(f.v[j], w), word(f.v[2 + j], w), 0x7632);
-                        a2 = __byte_perm(word(f.v[4 + j], w), word(f.v[6 + j], w), 0x5410);
-                        a3 = __byte_perm(word(f.v[4 + j], w), word(f.v[6 + j], w), 0x7632);
+                        a0 = __byte_perm(word(f.v[j], w), word(f.v[F::kV + j], w), 0x5410);
+                        a1 = __byte_perm(word(f.v[j], w), word(f.v[F::kV + j], w), 0x7632);
+                        a2 = __byte_perm(word(f.v[2 * F::kV + j], w), word(f.v[3 * F::kV + j], w), 0x5410);
+                        a3 = __byte_perm(word(f.v[2 * F::kV + j], w), word(f.v[3 * F::kV + j], w), 0x7632);
                     }
                     mma<kE4m3>(acc[i], a0, a1, a2, a3, hi0, hi1);
-                    mma<kE4m3>(acc[i], a0, a1, a2, a3, lo0, lo1);
+                    if (!kFew) mma<kE4m3>(acc[i], a0, a1, a2, a3, lo0, lo1);
                 }
             }
-            if (tile + 1 < end) {
-                load(tile + 1, false);
-                look_up(tile + 2);
-            }
+            load(false);
+            look_up();
         }
 
-        // the warps' sums meet in shared memory
+        // the warp's sums: o and lse of a whole unit, else a part
+        bad = __any_sync(kFull, bad);
 #pragma unroll
         for (int i = 4; i < 32; i <<= 1) {
             l0 += __shfl_xor_sync(kFull, l0, i);
             l1 += __shfl_xor_sync(kFull, l1, i);
         }
-        if (g == 0) {
-            sm.m[warp][2 * c] = m0, sm.m[warp][2 * c + 1] = m1;
-            sm.l[warp][2 * c] = l0, sm.l[warp][2 * c + 1] = l1;
-        }
+        if (kFew)
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const int d = kE4m3 ? 16 * g + 2 * i : 8 * g + 2 * (i & 3) + 64 * (i >> 2);
-            *reinterpret_cast<float2 *>(&sm.o[warp][2 * c * kPad + d]) = make_float2(acc[i][0], acc[i][2]);
-            *reinterpret_cast<float2 *>(&sm.o[warp][(2 * c + 1) * kPad + d]) = make_float2(acc[i][1], acc[i][3]);
-        }
-        const bool any_bad = __syncthreads_or(bad);
-
-        // thread: head hh, eight dimensions
-        const int hh = tid >> 4, d = (tid & 15) * 8;
-        float M = -INFINITY, L = 0.f, O[8] = {};
+            for (int i = 0; i < 8; i++)
 #pragma unroll
-        for (int w = 0; w < kWarps; w++) M = fmaxf(M, sm.m[w][hh]);
+                for (int j = 0; j < 4; j++) acc[i][j] += __shfl_xor_sync(kFull, acc[i][j], 2);
+        const bool whole = first == 0 && end == tiles;
+        const size_t part = 2 * id + (first == 0);
 #pragma unroll
-        for (int w = 0; w < kWarps; w++) {
-            const float r = sm.m[w][hh] == -INFINITY ? 0.f : exp2f(sm.m[w][hh] - M);   // 0 keeps a NaN
-            L = fmaf(r, sm.l[w][hh], L);
+        for (int j = 0; j < 2; j++) {
+            const int hh = 2 * c + j;
+            if (hh >= G || (whole && bad)) continue;
+            const float M = j ? m1 : m0, L = j ? l1 : l0;
+            if (whole) {
+                const size_t to = (size_t)u * G + hh;
+                const float inv = M == -INFINITY && L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
-            for (int i = 0; i < 8; i++) O[i] = fmaf(r, sm.o[w][hh * kPad + d + i], O[i]);
-        }
-        auto write = [&]() {
-            if (hh >= G) return;
-            const float inv = M == -INFINITY && L == 0.f ? 0.f : 1.f / L;
-            const size_t to = (size_t)u * G + hh;
-            *reinterpret_cast<uint4 *>(a.o + to * kD + d) =
-                make_uint4(to_bf16x2(O[0] * inv, O[1] * inv), to_bf16x2(O[2] * inv, O[3] * inv),
-                           to_bf16x2(O[4] * inv, O[5] * inv), to_bf16x2(O[6] * inv, O[7] * inv));
-            if (d == 0) a.lse[to] = (M + log2f(L)) * 0.6931471805599453f;
-        };
-        const int from = cuts.part(unit_at), upto = cuts.part(unit_at + tiles - 1);
-        if (from == upto) {
-            if (!any_bad) write();
-            else if (tid == 0) record_status(a.status, KVC_ERR_INVALID_ARG);
-        } else {
-            // a part of the unit; the last to come joins them all
-            const int slot = 2 * blockIdx.x + (first == 0);
-            if (hh < G) {
-                float *to = a.part_o + ((size_t)slot * G + hh) * kD + d;
-                *reinterpret_cast<float4 *>(to) = make_float4(O[0], O[1], O[2], O[3]);
-                *reinterpret_cast<float4 *>(to + 4) = make_float4(O[4], O[5], O[6], O[7]);
-                if (d == 0) *reinterpret_cast<float2 *>(a.part_ml + ((size_t)slot * G + hh) * 2) = make_float2(M, L);
-            }
-            if (tid == 0) a.part_bad[slot] = any_bad;
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) sm.last = atomicAdd(a.arrived + u, 1) == upto - from;
-            __syncthreads();
-            if (sm.last) {
-                __threadfence();
-                bool wrong = false;
-                M = -INFINITY, L = 0.f;
-#pragma unroll
-                for (int i = 0; i < 8; i++) O[i] = 0.f;
-                for (int p = from; p <= upto; p++) wrong |= __ldcg(a.part_bad + 2 * p + (p == from)) != 0;
-                if (hh < G) {
-                    for (int p = from; p <= upto; p++)
-                        M = fmaxf(M, __ldcg(a.part_ml + ((size_t)(2 * p + (p == from)) * G + hh) * 2));
-#pragma unroll 4
-                    for (int p = from; p <= upto; p++) {
-                        const size_t at = (size_t)(2 * p + (p == from)) * G + hh;
-                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.part_ml + at * 2));
-                        const float r = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-                        const float4 x = __ldcg(reinterpret_cast<const float4 *>(a.part_o + at * kD + d));
-                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(a.part_o + at * kD + d + 4));
-                        L = fmaf(r, ml.y, L);
-                        O[0] = fmaf(r, x.x, O[0]), O[1] = fmaf(r, x.y, O[1]);
-                        O[2] = fmaf(r, x.z, O[2]), O[3] = fmaf(r, x.w, O[3]);
-                        O[4] = fmaf(r, y.x, O[4]), O[5] = fmaf(r, y.y, O[5]);
-                        O[6] = fmaf(r, y.z, O[6]), O[7] = fmaf(r, y.w, O[7]);
-                    }
+                for (int i = 0; i < 8; i += 4) {
+                    const int d = kE4m3 ? 16 * g + 2 * i : 8 * g + 16 * i;
+                    *reinterpret_cast<uint4 *>(a.o + to * kD + d) =
+                        make_uint4(to_bf16x2(acc[i][j] * inv, acc[i][2 + j] * inv),
+                                   to_bf16x2(acc[i + 1][j] * inv, acc[i + 1][2 + j] * inv),
+                                   to_bf16x2(acc[i + 2][j] * inv, acc[i + 2][2 + j] * inv),
+                                   to_bf16x2(acc[i + 3][j] * inv, acc[i + 3][2 + j] * inv));
                 }
-                if (!wrong) write();
-                if (tid == 0) {
-                    if (wrong) record_status(a.status, KVC_ERR_INVALID_ARG);
-                    a.arrived[u] = 0;            // for the next call
+                if (g == 0) a.lse[to] = (M + log2f(L)) * 0.6931471805599453f;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    const int d = kE4m3 ? 16 * g + 2 * i : 8 * g + 2 * (i & 3) + 16 * (i & 4);
+                    *reinterpret_cast<float4 *>(a.part_o + (part * G + hh) * kD + d) =
+                        make_float4(acc[i][j], acc[i][2 + j], acc[i + 1][j], acc[i + 1][2 + j]);
                 }
+                if (g == 0) *reinterpret_cast<float2 *>(a.part_ml + (part * G + hh) * 2) = make_float2(M, L);
             }
         }
-        __syncthreads();
+        if (lane == 0) {
+            if (whole && bad) record_status(a.status, KVC_ERR_INVALID_ARG);
+            if (!whole) a.part_bad[part] = bad;
+            if (first == 0) a.cuts[u] = make_int2(id, cuts.part(unit_at + tiles - 1));
+        }
 
         // the next unit
         t = unit_at + end;
-        if (t < t_end) {
-            unit_at += tiles;
-            if (++h == heads) {
-                h = 0;
-                do tiles = tiles_of(++s);
-                while (tiles == 0);
-            }
-        }
+        unit_at += tiles;
+        if (t < t_end) next_unit(cur);
+        qbuf ^= 1;
     }
 }
 
@@ -541,8 +662,8 @@ __global__ void __launch_bounds__(kThreads, 3) attend_kernel(const __grid_consta
 
 size_t page_ws_bytes(const kvc_pages &pg, int G)
 {
-    return kAlign + align_up((size_t)pg.U * 4) + align_up(2 * kGrid * 4) +
-           align_up((size_t)2 * kGrid * G * 2 * 4) + align_up((size_t)2 * kGrid * G * kD * 4);
+    return kAlign + align_up((size_t)pg.U * 8) + align_up(2 * kWorkers * 4) +
+           align_up((size_t)2 * kWorkers * G * 2 * 4) + align_up((size_t)2 * kWorkers * G * kD * 4);
 }
 
 cudaError_t launch_page_attend(const kvc_pages &pg, int G, int max_len, const uint16_t *q,
@@ -559,22 +680,29 @@ cudaError_t launch_page_attend(const kvc_pages &pg, int G, int max_len, const ui
     uint8_t *at = static_cast<uint8_t *>(ws);
     a.status = &reinterpret_cast<WsHeader *>(at)->status;
     at += kAlign;
-    a.arrived = reinterpret_cast<int32_t *>(at);
-    at += align_up((size_t)pg.U * 4);
+    a.cuts = reinterpret_cast<int2 *>(at);
+    at += align_up((size_t)pg.U * 8);
     a.part_bad = reinterpret_cast<int32_t *>(at);
-    at += align_up(2 * kGrid * 4);
+    at += align_up(2 * kWorkers * 4);
     a.part_ml = reinterpret_cast<float *>(at);
-    at += align_up((size_t)2 * kGrid * G * 2 * 4);
+    at += align_up((size_t)2 * kWorkers * G * 2 * 4);
     a.part_o = reinterpret_cast<float *>(at);
     a.S = pg.U / pg.heads;
     a.G = G;
     a.max_len = max_len;
     // no more CTAs than there can be tiles
-    const int tile = kWarps * (pg.type == KVC_PAGE_E4M3 ? 32 : 16);
-    const int64_t tiles = (int64_t)pg.U * ((max_len + tile - 1) / tile);
+    const bool e4m3 = pg.type == KVC_PAGE_E4M3, few = G <= 4;
+    const int tile = e4m3 ? Frags<true>::kSlots : Frags<false>::kSlots;
+    const int64_t tiles = (int64_t)pg.U * ((max_len - 1) / tile + 1);
     const dim3 grid((unsigned)(tiles < kGrid ? tiles : kGrid));
-    return pg.type == KVC_PAGE_E4M3 ? launch_following(attend_kernel<true>, grid, kThreads, 0, st, a)
-                                    : launch_following(attend_kernel<false>, grid, kThreads, 0, st, a);
+    void (*kernel)(AttendArgs) = e4m3 ? (few ? attend_kernel<true, true> : attend_kernel<true, false>)
+                                      : (few ? attend_kernel<false, true> : attend_kernel<false, false>);
+    const cudaError_t err = launch_following(kernel, grid, kThreads, 0, st, a);
+    if (err != cudaSuccess || max_len <= tile) return err;       // a tile is never cut
+    const int64_t rows = (int64_t)pg.U * G, fill = 152 * 4;
+    if (rows <= fill) return launch_following(join_kernel<true>, dim3((unsigned)rows), kJoin, 0, st, a);
+    const int64_t blocks = (rows - 1) / (kJoin / 32) + 1;
+    return launch_following(join_kernel<false>, dim3((unsigned)(blocks < fill ? blocks : fill)), kJoin, 0, st, a);
 }
 
 }  // namespace kvc
