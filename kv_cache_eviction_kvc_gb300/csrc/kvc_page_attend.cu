@@ -140,12 +140,16 @@ __device__ __forceinline__ void e4m3_to_f16x4(uint32_t w, uint32_t &lo, uint32_t
         : "r"(w));
 }
 
+template <bool kWhole>
 struct Shared {
-    __align__(16) uint16_t q[kWarps][2][kHeads * kD];      // queries of the unit at hand and of the next
+    __align__(16) uint16_t q[kWarps][kWhole ? 1 : 2][kHeads * kD];      // queries of the unit at hand and of the next
     __align__(16) uint16_t fresh[kWarps][2][kD];           // the new token's key and value
     __align__(16) uint8_t row[kWarps][2][kD * 2];          // as they are held
     int scratch[33];
     int seq[kWarps], at[kWarps];
+    // kWhole: the warps' sums
+    __align__(16) float o[kWhole ? kWarps : 1][kHeads][kD + 4];
+    float m[kWarps][kHeads], l[kWarps][kHeads];
 };
 
 // What a lane holds of the slots a warp has of a tile: kBlocks blocks of 16.
@@ -164,6 +168,15 @@ struct Walk {
     int s, h, n, tiles, tile;                    // sequence, head, its length, a unit's tiles, the tile
     int ahead;                                   // the next sequence's length
 };
+
+// o and lse of row i (unit and head), four dimensions a lane, of sums o and L over 2^M
+__device__ __forceinline__ void store_row(const AttendArgs &a, size_t i, int lane, float M, float L, float4 o)
+{
+    const float inv = M == -INFINITY && L == 0.f ? 0.f : 1.f / L;
+    *reinterpret_cast<uint2 *>(a.o + i * kD + lane * 4) =
+        make_uint2(to_bf16x2(o.x * inv, o.y * inv), to_bf16x2(o.z * inv, o.w * inv));
+    if (lane == 0) a.lse[i] = (M + log2f(L)) * 0.6931471805599453f;
+}
 
 // The parts of units that were cut, joined in the order of the line.  kWide: a block
 // per row (unit and head), its warps a share of the parts each; else a warp per row.
@@ -237,23 +250,21 @@ __global__ void __launch_bounds__(kJoin) join_kernel(const __grid_constant__ Att
             }
             __syncthreads();
         }
-        if (share == 0) {
-            const float inv = M == -INFINITY && L == 0.f ? 0.f : 1.f / L;
-            *reinterpret_cast<uint2 *>(a.o + (size_t)i * kD + lane * 4) =
-                make_uint2(to_bf16x2(o.x * inv, o.y * inv), to_bf16x2(o.z * inv, o.w * inv));
-            if (lane == 0) a.lse[i] = (M + log2f(L)) * 0.6931471805599453f;
-        }
+        if (share == 0) store_row(a, i, lane, M, L, o);
     }
 }
 
 // kFew: at most four heads, whose weights' two terms are columns h and h + 4 of one
 // product.
-template <bool kE4m3, bool kFew>
+// kWhole: a unit goes whole to a CTA, whose warps take every fourth tile and meet in
+// shared memory: neither the line nor a second kernel is needed.
+template <bool kE4m3, bool kFew, bool kWhole>
 __global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __grid_constant__ AttendArgs a)
 {
     using F = Frags<kE4m3>;
     constexpr int kBlocks = F::kBlocks, kTile = F::kSlots, kRow = F::kRow;
-    __shared__ Shared sm;
+    constexpr int kStep = kWhole ? kWarps : 1;
+    __shared__ Shared<kWhole> sm;
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kFull, tid >> 5, 0);   // uniform
     const int g = lane >> 2, c = lane & 3;
     const int app = a.k_new != nullptr, heads = a.pg.heads, G = a.G;
@@ -263,43 +274,60 @@ __global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __gri
     // the line: tiles of every sequence's units in order, cut into equal parts for the warps
     auto length = [&](int s) { return s < a.S ? a.pg.len[s] : 0; };
     auto tiles_of = [&](int n) { return n < 0 || n > a.max_len - app ? 0 : max(1, (n + app + kTile - 1) / kTile); };
-    const int each = (a.S + kThreads - 1) / kThreads;
-    const int s0 = min(a.S, tid * each), s1 = min(a.S, s0 + each);
-    int mine = 0, refused = 0;
-#pragma unroll 8
-    for (int s = s0; s < s1; s++) {
-        const int t = tiles_of(a.pg.len[s]);
-        refused |= t == 0;
-        mine += t * heads;
-    }
-    if (refused && blockIdx.x == 0) record_status(a.status, KVC_ERR_SHAPE);
-    int total;
-    const int before = block_exscan(mine, sm.scratch, &total);
-    const LineCuts cuts(gridDim.x * kWarps, total);
-#pragma unroll
-    for (int w = 0; w < kWarps; w++) {
-        const int id = w * gridDim.x + blockIdx.x, t = cuts.start(id);
-        if (id < cuts.parts && t >= before && t < before + mine) {
-            int at = before, s = s0, size;
-            while (at + (size = tiles_of(a.pg.len[s]) * heads) <= t) at += size, s++;
-            sm.seq[w] = s;
-            sm.at[w] = at;
-        }
-    }
-    __syncthreads();
-    const int id = warp * gridDim.x + blockIdx.x;          // few tiles go to as many SMs as there are
-    if (id >= cuts.parts) return;
-    int t = cuts.start(id);
-    const int t_end = cuts.start(id + 1);
     Walk cur;                                    // the unit at hand
-    cur.s = sm.seq[warp];
-    cur.n = length(cur.s);
-    cur.ahead = length(cur.s + 1);
-    cur.tiles = tiles_of(cur.n);
-    int unit_at = sm.at[warp];                   // the unit's first tile on the line
-    cur.h = (t - unit_at) / cur.tiles;
-    unit_at += cur.h * cur.tiles;
-    cur.tile = t - unit_at;
+    int id = 0, t, t_end, unit_at = 0;           // the worker, its part of the line, the unit's first tile
+    LineCuts cuts(1, 0);
+    if (kWhole) {
+        const int u = blockIdx.x;
+        cur.s = a.pg.by_heads(u);
+        cur.h = u - cur.s * heads;
+        cur.n = a.pg.len[cur.s];
+        cur.tiles = tiles_of(cur.n);
+        cur.tile = cur.ahead = 0;
+        t = 0, t_end = cur.tiles;
+        if (t_end == 0) {
+            if (tid == 0) record_status(a.status, KVC_ERR_SHAPE);
+            return;
+        }
+        cur.tile = warp;
+    } else {
+        const int each = (a.S + kThreads - 1) / kThreads;
+        const int s0 = min(a.S, tid * each), s1 = min(a.S, s0 + each);
+        int mine = 0, refused = 0;
+#pragma unroll 8
+        for (int s = s0; s < s1; s++) {
+            const int t = tiles_of(a.pg.len[s]);
+            refused |= t == 0;
+            mine += t * heads;
+        }
+        if (refused && blockIdx.x == 0) record_status(a.status, KVC_ERR_SHAPE);
+        int total;
+        const int before = block_exscan(mine, sm.scratch, &total);
+        cuts = LineCuts(gridDim.x * kWarps, total);
+#pragma unroll
+        for (int w = 0; w < kWarps; w++) {
+            const int id = w * gridDim.x + blockIdx.x, t = cuts.start(id);
+            if (id < cuts.parts && t >= before && t < before + mine) {
+                int at = before, s = s0, size;
+                while (at + (size = tiles_of(a.pg.len[s]) * heads) <= t) at += size, s++;
+                sm.seq[w] = s;
+                sm.at[w] = at;
+            }
+        }
+        __syncthreads();
+        id = warp * gridDim.x + blockIdx.x;          // few tiles go to as many SMs as there are
+        if (id >= cuts.parts) return;
+        t = cuts.start(id);
+        t_end = cuts.start(id + 1);
+        cur.s = sm.seq[warp];
+        cur.n = length(cur.s);
+        cur.ahead = length(cur.s + 1);
+        cur.tiles = tiles_of(cur.n);
+        unit_at = sm.at[warp];
+        cur.h = (t - unit_at) / cur.tiles;
+        unit_at += cur.h * cur.tiles;
+        cur.tile = t - unit_at;
+    }
     auto next_unit = [&](Walk &w) {
         w.tile = 0;
         if (++w.h < heads) return;
@@ -314,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __gri
 
     // the tile after the one at hand is on its way, its successor's pages are known
     Walk far = cur;
-    int far_left = t_end - t;
+    int far_left = kWhole ? (t_end - warp + kWarps - 1) / kWarps : t_end - t;
     int far_h = 0, far_slot = 0, far_live = 0, ids[kBlocks];       // of what is loaded next
     bool far_bad = false;
     F f;
@@ -324,7 +352,9 @@ __global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __gri
         far_live = far_left > 0 ? far.n - far_slot : 0;           // slots from far_slot on that hold a row
 #pragma unroll
         for (int b = 0; b < kBlocks; b++) ids[b] = far_live > 16 * b ? a.pg.entry(far.s, far_slot + 16 * b) : 0;
-        if (--far_left > 0 && ++far.tile == far.tiles) next_unit(far);
+        --far_left;
+        far.tile += kStep;
+        if (!kWhole && far_left > 0 && far.tile == far.tiles) next_unit(far);
     };
     auto load = [&](bool keys) {
 #pragma unroll
@@ -390,7 +420,8 @@ __global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __gri
     while (t < t_end) {
         const int u = cur.s * heads + cur.h, n = cur.n, tiles = cur.tiles;
         const int first = cur.tile, end = min(t_end - unit_at, tiles);
-        const bool has_new = app && end == tiles;          // the new token's slot is in the last tile
+        // the new token's slot is in the last tile
+        const bool has_new = app && end == tiles && (!kWhole || (tiles - 1) % kWarps == warp);
         copies_wait();
         __syncwarp();
 
@@ -442,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __gri
                    (lane < 16 ? a.k_new : a.v_new) + (size_t)u * kD + (lane & 15) * 8);
             fresh_page = a.pg.entry(cur.s, n);
         }
-        if (unit_at + tiles < t_end) {
+        if (!kWhole && unit_at + tiles < t_end) {
             Walk then = cur;
             next_unit(then);
             fetch_q(qbuf ^ 1, then.s * heads + then.h);
@@ -450,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __gri
 
         float acc[8][4] = {}, m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
         bool bad = false;
-        for (int tile = first; tile < end; tile++) {
+        for (int tile = first; tile < end; tile += kStep) {
             int live = n - tile * kTile;
             bad |= far_bad;
             far_bad = false;
@@ -614,6 +645,40 @@ __global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __gri
             for (int i = 0; i < 8; i++)
 #pragma unroll
                 for (int j = 0; j < 4; j++) acc[i][j] += __shfl_xor_sync(kFull, acc[i][j], 2);
+        if (kWhole) {
+            if (g == 0) {
+                sm.m[warp][2 * c] = m0, sm.m[warp][2 * c + 1] = m1;
+                sm.l[warp][2 * c] = l0, sm.l[warp][2 * c + 1] = l1;
+            }
+#pragma unroll
+            for (int j = 0; j < 2; j++)
+                if (2 * c + j < G)
+#pragma unroll
+                    for (int i = 0; i < 8; i += 2) {
+                        const int d = kE4m3 ? 16 * g + 2 * i : 8 * g + 2 * (i & 3) + 16 * (i & 4);
+                        *reinterpret_cast<float4 *>(&sm.o[warp][2 * c + j][d]) =
+                            make_float4(acc[i][j], acc[i][2 + j], acc[i + 1][j], acc[i + 1][2 + j]);
+                    }
+            if (__syncthreads_or(bad)) {
+                if (tid == 0) record_status(a.status, KVC_ERR_INVALID_ARG);
+                return;
+            }
+            for (int hh = warp; hh < G; hh += kWarps) {
+                float M = -INFINITY, L = 0.f;
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < kWarps; w++) M = fmaxf(M, sm.m[w][hh]);
+#pragma unroll
+                for (int w = 0; w < kWarps; w++) {
+                    const float r = sm.m[w][hh] == -INFINITY ? 0.f : pow2(sm.m[w][hh] - M);   // 0 keeps a NaN
+                    const float4 x = *reinterpret_cast<const float4 *>(&sm.o[w][hh][lane * 4]);
+                    L = fmaf(r, sm.l[w][hh], L);
+                    o = make_float4(fmaf(r, x.x, o.x), fmaf(r, x.y, o.y), fmaf(r, x.z, o.z), fmaf(r, x.w, o.w));
+                }
+                store_row(a, (size_t)u * G + hh, lane, M, L, o);
+            }
+            return;
+        }
         const bool whole = first == 0 && end == tiles;
         const size_t part = 2 * id + (first == 0);
 #pragma unroll
@@ -690,15 +755,24 @@ cudaError_t launch_page_attend(const kvc_pages &pg, int G, int max_len, const ui
     a.S = pg.U / pg.heads;
     a.G = G;
     a.max_len = max_len;
-    // no more CTAs than there can be tiles
     const bool e4m3 = pg.type == KVC_PAGE_E4M3, few = G <= 4;
+    // Short units that all fit at once go whole to a CTA each (a cold call, 8 / 64 / 128 units of
+    // 64 slots in bf16: 8.2 / 8.2 / 9.5 us, the line 12.3 / 13 / 16.4; of 512 slots 15.7 / 16.4 /
+    // 16.4 and 14.0 / 16.4 / 20.5; of 1024 22.5 / 24.6 / 24.6 and 14.3 / 18.4 / 24.6; 4096 units of
+    // 64 in e4m3: 51 and 33)
+    if (max_len <= 512 && pg.U <= kGrid) {
+        void (*kernel)(AttendArgs) = e4m3 ? (few ? attend_kernel<true, true, true> : attend_kernel<true, false, true>)
+                                          : (few ? attend_kernel<false, true, true> : attend_kernel<false, false, true>);
+        return launch_following(kernel, dim3(pg.U), kThreads, 0, st, a);
+    }
+    // no more CTAs than there can be tiles
     const int tile = e4m3 ? Frags<true>::kSlots : Frags<false>::kSlots;
     const int64_t tiles = (int64_t)pg.U * ((max_len - 1) / tile + 1);
     const dim3 grid((unsigned)(tiles < kGrid ? tiles : kGrid));
-    void (*kernel)(AttendArgs) = e4m3 ? (few ? attend_kernel<true, true> : attend_kernel<true, false>)
-                                      : (few ? attend_kernel<false, true> : attend_kernel<false, false>);
+    void (*kernel)(AttendArgs) = e4m3 ? (few ? attend_kernel<true, true, false> : attend_kernel<true, false, false>)
+                                      : (few ? attend_kernel<false, true, false> : attend_kernel<false, false, false>);
     const cudaError_t err = launch_following(kernel, grid, kThreads, 0, st, a);
-    if (err != cudaSuccess || max_len <= tile) return err;       // a tile is never cut
+    if (err != cudaSuccess) return err;
     const int64_t rows = (int64_t)pg.U * G, fill = 152 * 4;
     if (rows <= fill) return launch_following(join_kernel<true>, dim3((unsigned)rows), kJoin, 0, st, a);
     const int64_t blocks = (rows - 1) / (kJoin / 32) + 1;
