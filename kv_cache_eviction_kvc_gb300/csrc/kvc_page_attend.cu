@@ -200,6 +200,16 @@ __global__ void __launch_bounds__(kJoin) join_kernel(const __grid_constant__ Att
         if (n < 0 || n > a.max_len - (a.k_new != nullptr) || cut.x >= cut.y) continue;
         const int parts = cut.y - cut.x + 1;
         auto slot = [&](int p) { return 2 * (cut.x + p) + (p == 0); };
+        const int mine = (parts - 1) / kShares + 1, end = min(parts, (share + 1) * mine);
+        // the first sums load beside the maxima: most units have two or three parts
+        float4 x[8];
+        auto load = [&](int p) {
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                if (p + j < end)
+                    x[j] = *reinterpret_cast<const float4 *>(a.part_o + ((size_t)slot(p + j) * G + hh) * kD + lane * 4);
+        };
+        load(share * mine);
         float M = -INFINITY, L = 0.f;
         bool wrong = false;
         for (int p = lane; p < parts; p += 32) {
@@ -212,28 +222,21 @@ __global__ void __launch_bounds__(kJoin) join_kernel(const __grid_constant__ Att
             continue;
         }
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        const int mine = (parts - 1) / kShares + 1, end = min(parts, (share + 1) * mine);
         for (int p0 = share * mine; p0 < end; p0 += 32) {
             float2 ml = make_float2(-INFINITY, 0.f);
             if (p0 + lane < end)
                 ml = *reinterpret_cast<const float2 *>(a.part_ml + ((size_t)slot(p0 + lane) * G + hh) * 2);
             const float r = ml.x == -INFINITY ? 0.f : pow2(ml.x - M);       // 0 keeps a NaN
             L += warp_sum(r * ml.y);
-            const int some = min(32, end - p0);
-            for (int j0 = 0; j0 < some; j0 += 8) {
-                float4 x[8];
-#pragma unroll
-                for (int j = 0; j < 8; j++)
-                    if (j0 + j < some)
-                        x[j] = *reinterpret_cast<const float4 *>(
-                            a.part_o + ((size_t)slot(p0 + j0 + j) * G + hh) * kD + lane * 4);
+            for (int j0 = 0; j0 < 32 && p0 + j0 < end; j0 += 8) {
 #pragma unroll
                 for (int j = 0; j < 8; j++) {
                     const float f = __shfl_sync(kFull, r, j0 + j);
-                    if (j0 + j < some)
+                    if (p0 + j0 + j < end)
                         o = make_float4(fmaf(f, x[j].x, o.x), fmaf(f, x[j].y, o.y), fmaf(f, x[j].z, o.z),
                                         fmaf(f, x[j].w, o.w));
                 }
+                load(p0 + j0 + 8);
             }
         }
         if (kWide) {
