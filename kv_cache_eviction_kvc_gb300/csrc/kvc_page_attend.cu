@@ -125,11 +125,11 @@ __device__ __forceinline__ float pow2(float x)
     return r;
 }
 
-// log2 of a power of two above the scale, at least -100: weights over the reference
-// are then at most 2^100, and their sum stays in range
+// log2 of a power of two above the scale, at least -96: exponentials over the reference
+// are then at most 2^104 (the slack among them), and sums of 2^23 of them stay in range
 __device__ __forceinline__ float scale_log2(float s)
 {
-    return fmaxf((float)((int)(__float_as_uint(s) >> 23) - 126), -100.f);
+    return fmaxf((float)((int)(__float_as_uint(s) >> 23) - 126), -96.f);
 }
 
 // four e4m3 values as f16 (exact): the low two, the high two

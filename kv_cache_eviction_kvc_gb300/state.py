@@ -288,7 +288,7 @@ class PagedState:
         self._free += reversed(self._held[s])
         self._held[s] = []
         self.table[s].fill_(-1)
-        self.len[s:s + 1].zero_()
+        self.len[s].zero_()
 
     # --------------------------------------------------------------- calls
     def write(self, k, v, count=None):

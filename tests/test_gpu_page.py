@@ -300,6 +300,38 @@ def test_bound_above_the_lengths_changes_nothing(e4m3):
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("G,lens", [(8, [131071]), (1, [60001]), (8, [20000, 9, 0]), (8, [4000, 3999] * 40),
+                                    (1, [700] * 700), (4, [511] * 456), (4, [512] * 456), (4, [511] * 457),
+                                    (2, [0] * 500), (4, [513, 0])])
+def test_attend_every_way_the_work_is_cut(e4m3, G, lens):
+    """One unit over all warps, units of many and of few parts, whole units up to the number that
+    fits at once and one more, empty units only."""
+    p = Pool(len(lens) + G, 1, lens, 64 if max(lens) > 1000 else 16, e4m3, more=1)
+    some = sorted({0, 1, len(lens) // 2, len(lens) - 2, len(lens) - 1} & set(range(len(lens))))
+    check_attend(p, G, units=some)
+    check_attend(p, G, append=False, units=some)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_every_sequence_refused(e4m3):
+    for n in (20, 5000):
+        p = Pool(67, 2, [n, n], 16, e4m3, more=1)
+        p.t["len"].fill_(n + 1)
+        _, _, _, o, lse = attend(p, 4, max_len=n + 1)
+        assert p.status() == 2 and (o == 7).all() and (lse == 7).all()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_long_unit_of_zeros(e4m3):
+    """Values (and then keys) of zeros, whose e4m3 scale is the least there is: the sums stay in range."""
+    p = Pool(69, 1, [100000, 3], 128, e4m3, more=1, v_scale=0.0)
+    check_attend(p, 4, v=torch.zeros(2, D, dtype=torch.bfloat16, device=DEV),
+                 k=bf(p.rng.standard_normal((2, D))).to(DEV))
+    p = Pool(70, 1, [100000, 3], 128, e4m3, more=1, v_scale=0.0, k_scale=0.0)
+    check_attend(p, 4)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
 def test_same_call_same_bits(e4m3):
     p = Pool(59, 2, [9000, 100, 33], 16, e4m3, more=1)
     q, k, v, o, lse = attend(p, 4)
@@ -705,6 +737,9 @@ def test_prompt_steps_and_selection(e4m3):
     assert all(torch.equal(a, b) for a, b in zip(*outs))
     assert st.status() == 0
     # a sequence ends, another takes its pages
+    st.release(-1)
+    assert st.len.tolist()[-1] == 0 and (st.table[-1] == -1).all()
+    st.reserve([n[0], n[1], 3])
     st.release(0)
     assert st.len.tolist()[0] == 0
     st.reserve([120, n[1], n[2]])

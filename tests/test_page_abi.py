@@ -2,11 +2,16 @@
 refuse bad arguments on the host, before any launch (no GPU: the pointers are
 fake and never read)."""
 import ctypes
+import os
+import shutil
+import subprocess
 
 import pytest
 import torch
 
 from kv_cache_eviction_kvc_gb300 import kvc as K
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 BIG = 1 << 40
 
@@ -109,3 +114,22 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
             K.make_pages(*bad)
     with pytest.raises(ValueError):
         K.make_rope(32, 8, torch.zeros(64, dtype=torch.float64))    # host memory
+
+
+@pytest.mark.skipif(shutil.which("gcc") is None, reason="needs gcc")
+def test_struct_layouts(tmp_path):
+    """The header's structures and the binding's agree field by field."""
+    lines = []
+    for name, cls in (("kvc_rope", K.kvc_rope), ("kvc_pages", K.kvc_pages)):
+        lines += [f'printf("%zu ", offsetof({name}, {f}));' for f, _ in cls._fields_]
+        lines.append(f'printf("%zu ", sizeof({name}));')
+    src = tmp_path / "l.c"
+    src.write_text('#include <stdio.h>\n#include "kvc.h"\nint main(void){' + "".join(lines) + "return 0;}")
+    subprocess.run(["gcc", "-std=c99", "-pedantic", "-Werror", "-I", os.path.join(ROOT, "include"), str(src),
+                    "-o", str(tmp_path / "l")], check=True)
+    got = [int(x) for x in subprocess.run([str(tmp_path / "l")], capture_output=True, text=True,
+                                          check=True).stdout.split()]
+    want = []
+    for cls in (K.kvc_rope, K.kvc_pages):
+        want += [getattr(cls, f).offset for f, _ in cls._fields_] + [ctypes.sizeof(cls)]
+    assert got == want
