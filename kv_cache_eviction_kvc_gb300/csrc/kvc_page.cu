@@ -43,6 +43,7 @@ static kvc_status check_pages(const char *fn, const kvc_pages *pg)
              "%s: pages of %d slots unsupported (16, 32, 64 or 128)", fn, pg->page);
     PG_CHECK(pg->U >= 1 && pg->heads >= 1 && pg->U % pg->heads == 0, KVC_ERR_INVALID_ARG,
              "%s: heads = %d must divide U = %d", fn, pg->heads, pg->U);
+    PG_CHECK(pg->U <= 1 << 27, KVC_ERR_UNSUPPORTED, "%s: U = %d unsupported (at most 2^27)", fn, pg->U);
     PG_CHECK(pg->n_pages >= 1 && pg->stride >= 1, KVC_ERR_INVALID_ARG,
              "%s: n_pages = %d and stride = %d must be >= 1", fn, pg->n_pages, pg->stride);
     PG_CHECK((int64_t)pg->stride * pg->page < (1ll << 31) - 128, KVC_ERR_UNSUPPORTED,

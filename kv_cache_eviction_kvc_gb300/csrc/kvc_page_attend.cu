@@ -32,6 +32,15 @@
 // lengths.  A warp walks its part alone, without a barrier, the next tile's rows
 // on their way in registers across the ends of units.  A unit that is cut leaves
 // its parts in the workspace, which a second kernel joins in the order of the line.
+//
+// Measured, calls replayed as a graph: 8 units x 131071 slots bf16 87 us (6.2 TB/s;
+// 81.7 without the join), 128 units x <= 32768 e4m3 140 us (6.5; 138), 1024 units x
+// <= 1024 e4m3 41 us (5.1; 37.5), 128 x <= 3277 bf16 with 8 heads 33.4 us (5.3; 29.6),
+// 8 x 64 3.6 us.  What is left is a chain of waits at either end: lengths, pages,
+// first rows (about 4 us), the join (2 to 5 us).  Tried and slower: the next tiles
+// in a ring of shared memory filled by cp.async (8 x 131071: 115); a tile of a CTA's
+// four warps with a barrier per unit (1024 units: 48); e4m3 tiles of 16 slots (47, and
+// 44.5 with four CTAs per SM); joins by the last CTA or warp to come (registers spill).
 #include "kvc_page.h"
 
 #include <cuda_fp16.h>
@@ -40,7 +49,7 @@
 namespace kvc {
 namespace {
 
-constexpr int kThreads = 128, kWarps = kThreads / 32, kJoin = 256;
+constexpr int kThreads = 128, kWarps = kThreads / 32;
 constexpr int kResident = 3, kGrid = 152 * kResident, kWorkers = kGrid * kWarps;
 constexpr int kHeads = 8;                        // columns of the products
 constexpr float kSlack = 8.f;                    // log2 that a logit may pass the reference by
@@ -178,82 +187,91 @@ __device__ __forceinline__ void store_row(const AttendArgs &a, size_t i, int lan
     if (lane == 0) a.lse[i] = (M + log2f(L)) * 0.6931471805599453f;
 }
 
-// The parts of units that were cut, joined in the order of the line.  kWide: a block
-// per row (unit and head), its warps a share of the parts each; else a warp per row.
-// Four dimensions a lane; weights of 32 parts are formed in the lanes, their sums
-// added up with 8 loads in flight.
-template <bool kWide>
-__global__ void __launch_bounds__(kJoin) join_kernel(const __grid_constant__ AttendArgs a)
+// A share of the parts of row i (unit and head) over the maximum of all: sums o and L.
+// False where there are none, or none to be written.
+template <int kShares>
+__device__ __forceinline__ bool sum_parts(const AttendArgs &a, int i, int share, int lane, float &M, float &L, float4 &o)
 {
-    __shared__ float4 sums[kJoin / 32][32];
-    __shared__ float part_l[kJoin / 32];
+    const int G = a.G;
+    const int u = i / G, hh = i - u * G;
+    const int2 cut = a.cuts[u];
+    const int n = a.pg.len[a.pg.by_heads(u)];
+    // a unit that was refused has no parts, and what stands in cuts is another call's
+    if (n < 0 || n > a.max_len - (a.k_new != nullptr) || cut.x >= cut.y) return false;
+    const int parts = cut.y - cut.x + 1;
+    auto slot = [&](int p) { return 2 * (cut.x + p) + (p == 0); };
+    const int mine = (parts - 1) / kShares + 1, end = min(parts, (share + 1) * mine);
+    // the first sums load beside the maxima: most units have two or three parts
+    float4 x[8];
+    auto load = [&](int p) {
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            if (p + j < end)
+                x[j] = *reinterpret_cast<const float4 *>(a.part_o + ((size_t)slot(p + j) * G + hh) * kD + lane * 4);
+    };
+    load(share * mine);
+    bool wrong = false;
+    for (int p = lane; p < parts; p += 32) {
+        M = fmaxf(M, a.part_ml[((size_t)slot(p) * G + hh) * 2]);
+        wrong |= a.part_bad[slot(p)] != 0;
+    }
+    M = warp_max(M);
+    if (__any_sync(kFull, wrong)) {
+        if (lane == 0) record_status(a.status, KVC_ERR_INVALID_ARG);
+        return false;
+    }
+    for (int p0 = share * mine; p0 < end; p0 += 32) {
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (p0 + lane < end)
+            ml = *reinterpret_cast<const float2 *>(a.part_ml + ((size_t)slot(p0 + lane) * G + hh) * 2);
+        const float r = ml.x == -INFINITY ? 0.f : pow2(ml.x - M);       // 0 keeps a NaN
+        L += warp_sum(r * ml.y);
+        for (int j0 = 0; j0 < 32 && p0 + j0 < end; j0 += 8) {
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const float f = __shfl_sync(kFull, r, j0 + j);
+                if (p0 + j0 + j < end)
+                    o = make_float4(fmaf(f, x[j].x, o.x), fmaf(f, x[j].y, o.y), fmaf(f, x[j].z, o.z),
+                                    fmaf(f, x[j].w, o.w));
+            }
+            load(p0 + j0 + 8);
+        }
+    }
+    return true;
+}
+
+// The parts of units that were cut, joined in the order of the line: kShares warps
+// per row (unit and head), each a share of the parts.  Four dimensions a lane; weights
+// of 32 parts are formed in the lanes, their sums added up with 8 loads in flight.
+template <int kShares>
+__global__ void __launch_bounds__(kShares < 8 ? 256 : 32 * kShares) join_kernel(const __grid_constant__ AttendArgs a)
+{
+    constexpr int kJoinWarps = kShares < 8 ? 8 : kShares, kRows = kJoinWarps / kShares;
+    __shared__ float4 sums[kJoinWarps][32];
+    __shared__ float part_l[kJoinWarps];
     follow();
     lead();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = a.G, rows = a.S * a.pg.heads * G;
-    constexpr int kRows = kWide ? 1 : kJoin / 32, kShares = kWide ? kJoin / 32 : 1;
-    const int share = kWide ? warp : 0;
-    for (int i = blockIdx.x * kRows + (kWide ? 0 : warp); i < rows; i += gridDim.x * kRows) {
-        const int u = i / G, hh = i - u * G;
-        const int2 cut = a.cuts[u];
-        const int n = a.pg.len[a.pg.by_heads(u)];
-        // a unit that was refused has no parts, and what stands in cuts is another call's
-        if (n < 0 || n > a.max_len - (a.k_new != nullptr) || cut.x >= cut.y) continue;
-        const int parts = cut.y - cut.x + 1;
-        auto slot = [&](int p) { return 2 * (cut.x + p) + (p == 0); };
-        const int mine = (parts - 1) / kShares + 1, end = min(parts, (share + 1) * mine);
-        // the first sums load beside the maxima: most units have two or three parts
-        float4 x[8];
-        auto load = [&](int p) {
-#pragma unroll
-            for (int j = 0; j < 8; j++)
-                if (p + j < end)
-                    x[j] = *reinterpret_cast<const float4 *>(a.part_o + ((size_t)slot(p + j) * G + hh) * kD + lane * 4);
-        };
-        load(share * mine);
+    const int share = warp % kShares;
+    for (int i0 = blockIdx.x * kRows; i0 < rows; i0 += gridDim.x * kRows) {
+        const int i = i0 + warp / kShares;
         float M = -INFINITY, L = 0.f;
-        bool wrong = false;
-        for (int p = lane; p < parts; p += 32) {
-            M = fmaxf(M, a.part_ml[((size_t)slot(p) * G + hh) * 2]);
-            wrong |= a.part_bad[slot(p)] != 0;
-        }
-        M = warp_max(M);
-        if (__any_sync(kFull, wrong)) {
-            if (lane == 0) record_status(a.status, KVC_ERR_INVALID_ARG);
-            continue;
-        }
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int p0 = share * mine; p0 < end; p0 += 32) {
-            float2 ml = make_float2(-INFINITY, 0.f);
-            if (p0 + lane < end)
-                ml = *reinterpret_cast<const float2 *>(a.part_ml + ((size_t)slot(p0 + lane) * G + hh) * 2);
-            const float r = ml.x == -INFINITY ? 0.f : pow2(ml.x - M);       // 0 keeps a NaN
-            L += warp_sum(r * ml.y);
-            for (int j0 = 0; j0 < 32 && p0 + j0 < end; j0 += 8) {
-#pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    const float f = __shfl_sync(kFull, r, j0 + j);
-                    if (p0 + j0 + j < end)
-                        o = make_float4(fmaf(f, x[j].x, o.x), fmaf(f, x[j].y, o.y), fmaf(f, x[j].z, o.z),
-                                        fmaf(f, x[j].w, o.w));
-                }
-                load(p0 + j0 + 8);
-            }
-        }
-        if (kWide) {
+        const bool done = i < rows && sum_parts<kShares>(a, i, share, lane, M, L, o);
+        if (kShares > 1) {
             sums[warp][lane] = o;
             if (lane == 0) part_l[warp] = L;
             __syncthreads();
-            if (warp == 0) {
-#pragma unroll
+            if (share == 0)
+#pragma unroll 8
                 for (int w = 1; w < kShares; w++) {
-                    const float4 x = sums[w][lane];
+                    const float4 x = sums[warp + w][lane];
                     o = make_float4(o.x + x.x, o.y + x.y, o.z + x.z, o.w + x.w);
-                    L += part_l[w];
+                    L += part_l[warp + w];
                 }
-            }
             __syncthreads();
         }
-        if (share == 0) store_row(a, i, lane, M, L, o);
+        if (done && share == 0) store_row(a, i, lane, M, L, o);
     }
 }
 
@@ -777,9 +795,17 @@ cudaError_t launch_page_attend(const kvc_pages &pg, int G, int max_len, const ui
     const cudaError_t err = launch_following(kernel, grid, kThreads, 0, st, a);
     if (err != cudaSuccess) return err;
     const int64_t rows = (int64_t)pg.U * G, fill = 152 * 4;
-    if (rows <= fill) return launch_following(join_kernel<true>, dim3((unsigned)rows), kJoin, 0, st, a);
-    const int64_t blocks = (rows - 1) / (kJoin / 32) + 1;
-    return launch_following(join_kernel<false>, dim3((unsigned)(blocks < fill ? blocks : fill)), kJoin, 0, st, a);
+    auto join = [&](void (*f)(AttendArgs), int per_block, int threads) {
+        const int64_t blocks = (rows - 1) / per_block + 1;
+        return launch_following(f, dim3((unsigned)(blocks < fill ? blocks : fill)), threads, 0, st, a);
+    };
+    // as many warps per row as keep a unit's parts in about one round of loads (8 units of 131071
+    // slots, 171 parts each: 8 warps 87.5 us a call, 32 87.2; 1024 units, two or three parts each:
+    // one warp 41.0, four 48.5)
+    const int parts = kWorkers / pg.U + 2;
+    if (parts <= 8) return join(join_kernel<1>, 8, 256);
+    if (parts <= 32) return join(join_kernel<4>, 2, 256);
+    return join(join_kernel<32>, 1, 1024);
 }
 
 }  // namespace kvc
