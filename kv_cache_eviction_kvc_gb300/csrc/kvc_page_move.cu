@@ -2,9 +2,10 @@
 // with an fp32 scale per row) and out of it (kvc_page_read).
 //
 // Sixteen lanes hold a row: 16 bytes each of its bf16 form, 8 of its e4m3 form.
-// Both calls are bound by the bytes (a slot: 1024 in bf16, 264 in e4m3) once there
-// are rows enough; before that by a chain of loads (count, slot, table, row, each
-// waiting for the one before), of which a team has two rows in flight.
+// Both calls are bound by the bytes (a slot read and written: 1024 in bf16, 776 to
+// or from e4m3) once there are rows enough; before that by a chain of loads (count,
+// slot, table, row, each waiting for the one before), of which a team has two rows
+// in flight.
 //
 // Written in e4m3 the arithmetic is nearly as long as the bytes, so magnitudes are
 // compared as 16-bit whole numbers, both rows' in one word (four exchanges for the
@@ -12,7 +13,9 @@
 //
 // Measured: 8 units x 32768 rows to e4m3 33.6 us (6.1 TB/s), 8 x 131071 rows back
 // 125 us (6.5 TB/s), 32 units x <= 3277 listed rows of 32768 back 14.1 us (4.7 TB/s:
-// the chain of loads and the launch are half).  Rows in flight per team, the same
+// the scale of a listed row brings 64 bytes from memory, 15 % more in all, and the
+// chain of loads starts and ends it; loading the next rows' slots and pages ahead in
+// longer-lived blocks took 14.5 to 16).  Rows in flight per team, the same
 // three: one 35.2, 148, 18.6 us; two 33.6, 125, 14.1; three 33.3, 125, 14.2; four
 // 35.7, 126, 14.6.
 #include "kvc_page.h"
