@@ -502,6 +502,8 @@ def make_rope(Hq, Hkv, inv_freq, q_weight=None, k_weight=None, eps=1e-6, interle
                  _sized(inv_freq, _F64, "inv_freq", rot // 2, dev, optional=True),
                  Hkv if units is None else units, first_unit)
     r.dev, r.keep = dev, (inv_freq, q_weight, k_weight)
+    # what a call checks sizes by: a row, a sequence's units, the units of the last one, heads
+    r.sizes = ((Hq + 2 * Hkv) * d, r.units, r.first_unit + Hkv, Hq // max(1, Hkv), d)
     return r
 
 
@@ -513,26 +515,32 @@ def kvc_qk_norm_rope(r: kvc_rope, qkv, pos, n, q, k, v, stream=None):
     dev = _device()
     if r.dev is not None and r.dev != dev:
         raise ValueError(f"the weights and frequencies must live on the current device cuda:{dev}")
-    if qkv is None or qkv.dim() != 3:
+    if not isinstance(qkv, _Tensor) or qkv.dim() != 3:
         raise ValueError("qkv must be [B][T][row]")
+    least, units, mine, G, d = r.sizes
     B, T, width = qkv.shape
-    row, Hq, Hkv, d = qkv.stride(1) if T > 1 else qkv.stride(0), r.Hq, r.Hkv, r.d
-    if B * T == 1:
+    if qkv.is_contiguous():
         row = width
-    if (width < (Hq + 2 * Hkv) * d or qkv.stride(2) != 1
-            or (T > 1 and B > 1 and qkv.stride(0) != T * row)):
-        raise ValueError(f"qkv must hold rows of (Hq + 2 Hkv) d = {(Hq + 2 * Hkv) * d} elements, "
-                         "evenly apart")
+    else:
+        apart, row, one = qkv.stride()
+        if T == 1:
+            row = apart if B > 1 else width
+        elif B > 1 and apart != T * row:
+            row = -1
+        if row < width or one != 1:
+            raise ValueError("qkv must hold rows evenly apart")
+    if width < least:
+        raise ValueError(f"qkv must hold rows of (Hq + 2 Hkv) d = {least} elements")
     if qkv.dtype is not _BF16 or qkv.get_device() != dev:
         raise TypeError(f"qkv must be bf16 on the current device cuda:{dev}")
-    # units the outputs hold at least: all of the last sequence's that are written
-    rows = ((B - 1) * r.units + r.first_unit + Hkv) * T
+    # elements the outputs hold at least: up to the last sequence's last unit that is written
+    size = ((B - 1) * units + mine) * T * d
     _check(load().kvc_qk_norm_rope(
         _ref(r), B, T, qkv.data_ptr(), row, _sized(pos, _I32, "pos", B * T, dev),
         None if n is None else _sized(n, _I32, "n", B, dev),
-        None if q is None else _sized(q, _BF16, "q", rows * (Hq // Hkv) * d, dev),
-        None if k is None else _sized(k, _BF16, "k", rows * d, dev),
-        None if v is None else _sized(v, _BF16, "v", rows * d, dev), _stream_on(stream, dev)))
+        None if q is None else _sized(q, _BF16, "q", size * G, dev),
+        None if k is None else _sized(k, _BF16, "k", size, dev),
+        None if v is None else _sized(v, _BF16, "v", size, dev), _stream_on(stream, dev)))
 
 
 # ------------------------------------------------------------------ a cache in pages
@@ -560,6 +568,7 @@ def make_pages(K, V, k_scale, v_scale, table, length) -> kvc_pages:
                    _sized(table, _I32, "table", S * stride, dev),
                    _sized(length, _I32, "length", S, dev))
     pg.S, pg.dev, pg.keep = S, dev, (K, V, k_scale, v_scale, table, length)
+    pg.units, pg.dim = S * heads, d          # U and d, as plain numbers
     return pg
 
 
@@ -570,6 +579,14 @@ def _pages_device(pg):
     return dev
 
 
+def _rows(t, message):
+    """The second of three dimensions."""
+    shape = t.shape if isinstance(t, _Tensor) else ()
+    if len(shape) != 3:
+        raise ValueError(message)
+    return shape[1]
+
+
 def kvc_page_workspace_size(pg: kvc_pages, G: int) -> int:
     return int(load().kvc_page_workspace_size(_ref(pg), int(G)))
 
@@ -577,10 +594,8 @@ def kvc_page_workspace_size(pg: kvc_pages, G: int) -> int:
 def kvc_page_write(pg: kvc_pages, first, count, k, v, ws, stream=None):
     """k, v: bf16 [U][T][d]; first, count: int32 [S] or None (0, T)."""
     dev = _pages_device(pg)
-    if k is None or k.dim() != 3:
-        raise ValueError("k must be [U][T][d]")
-    T = k.shape[1]
-    n = pg.U * T * pg.d
+    T = _rows(k, "k must be [U][T][d]")
+    n = pg.units * T * pg.dim
     _check(load().kvc_page_write(
         _ref(pg), T, None if first is None else _sized(first, _I32, "first", pg.S, dev),
         None if count is None else _sized(count, _I32, "count", pg.S, dev),
@@ -592,13 +607,11 @@ def kvc_page_read(pg: kvc_pages, slots, count, k_out, v_out, ws, stream=None, M=
     """slots: int32 [U][M] or None (slot i; M, else all rows of k_out); count: int32
     [U] or None; k_out, v_out: bf16 [U][ld][d], ld >= M."""
     dev = _pages_device(pg)
-    if k_out is None or k_out.dim() != 3:
-        raise ValueError("k_out must be [U][ld][d]")
     if slots is not None and slots.dim() != 2:
         raise ValueError("slots must be [U][M]")
-    U, ld = pg.U, k_out.shape[1]
+    U, ld = pg.units, _rows(k_out, "k_out must be [U][ld][d]")
     M = slots.shape[1] if slots is not None else ld if M is None else int(M)
-    n = U * ld * pg.d
+    n = U * ld * pg.dim
     _check(load().kvc_page_read(
         _ref(pg), M, ld, None if slots is None else _sized(slots, _I32, "slots", U * M, dev),
         None if count is None else _sized(count, _I32, "count", U, dev),
@@ -609,10 +622,7 @@ def kvc_page_read(pg: kvc_pages, slots, count, k_out, v_out, ws, stream=None, M=
 def kvc_page_attend(pg: kvc_pages, max_len, q, k_new, v_new, o, lse, ws, stream=None):
     """q, o: bf16 [U][G][d]; k_new, v_new: bf16 [U][d], or both None; lse: fp32 [U][G]."""
     dev = _pages_device(pg)
-    U, d = pg.U, pg.d
-    if q is None or q.dim() != 3:
-        raise ValueError("q must be [U][G][d]")
-    G = q.shape[1]
+    U, d, G = pg.units, pg.dim, _rows(q, "q must be [U][G][d]")
     n, heads = U * d, U * G
     _check(load().kvc_page_attend(
         _ref(pg), G, int(max_len), _sized(q, _BF16, "q", heads * d, dev),

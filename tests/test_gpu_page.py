@@ -660,6 +660,17 @@ def test_rope_rows_further_apart():
         K.kvc_qk_norm_rope(r, wide[..., :2 * D], i32([[0, 1, 2], [7, 8, 9]]), None, q, k, v)
     with pytest.raises(ValueError):
         K.kvc_qk_norm_rope(r, wide.transpose(0, 1), i32([[0, 1, 2], [7, 8, 9]]), None, q, k, v)
+    with pytest.raises(ValueError):
+        K.kvc_qk_norm_rope(r, wide[:, :2], i32([[0, 1], [7, 8]]), None, q, k, v)
+    with pytest.raises(ValueError):
+        K.kvc_qk_norm_rope(r, x[0], i32([[0, 1, 2]]), None, q, k, v)
+    # one token each of sequences further apart, and one token alone
+    for src, at in ((wide[:, 1:2, D:4 * D], [[1], [8]]), (wide[1:, 1:2, D:4 * D], [[8]])):
+        B = len(at)
+        q1, k1, v1 = (torch.zeros(B, 1, *s, D, dtype=torch.bfloat16, device=DEV) for s in ((1,), (), ()))
+        K.kvc_qk_norm_rope(r, src, i32(at), None, q1, k1, v1)
+        for have, all_ in ((q1, q), (k1, k), (v1, v)):
+            assert torch.equal(have[:, 0], all_[2 - B:, 1])
 
 
 # ---------------------------------------------------------------------- together
@@ -806,6 +817,37 @@ def test_graph_advances_with_the_lengths(e4m3):
         outs.append(got)
     for (a, b), (c, d) in zip(*outs):
         assert torch.equal(a, c) and torch.equal(b, d)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_write_and_read_in_a_graph(e4m3):
+    """Captured on a side stream and replayed with other rows, places and counts."""
+    p = Pool(108, 2, [0, 0], 16, e4m3, more=90)
+    k, v = (torch.zeros(4, 40, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    ko, vo = (torch.zeros(4, 90, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    count, s = i32([40, 40]), torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        K.kvc_page_write(p.pages, p.t["len"], count, k, v, p.ws)
+        p.t["len"].add_(count)
+        K.kvc_page_read(p.pages, None, None, ko, vo, p.ws)
+    held = [[np.zeros((0, D)), np.zeros((0, D))] for _ in range(4)]
+    for counts in ([40, 3], [0, 40], [17, 1]):
+        count.copy_(i32(counts))
+        for i, x in enumerate((k, v)):
+            x.copy_(bf(p.rng.standard_normal((4, 40, D))))
+            for u in range(4):
+                row = f64(x[u, :counts[u // 2]])
+                if e4m3 and len(row):
+                    val, sc = R.quantise(row)
+                    row = f64(bf(f64(val) * sc.astype(np.float64)[:, None]))
+                held[u][i] = np.concatenate([held[u][i], row])
+        g.replay()
+        for u in range(4):
+            n = len(held[u][0])
+            assert np.array_equal(f64(ko[u, :n]), held[u][0]) and np.array_equal(f64(vo[u, :n]), held[u][1])
+    assert p.status() == 0
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
