@@ -674,8 +674,8 @@ KVC_API kvc_status kvc_tree_commit_f64(const kvc_params *p, int32_t max_len,
 /* ------------------------------------------------------------------ */
 
 /*
- * What the calls around the cache need of the projection: the pages begin at
- * q, k_new and v_new; these are their definitions here.
+ * The method's sources begin at q, k_new and v_new of a step; these calls, which
+ * the sources do not describe, make them of a projection's rows.
  */
 typedef struct {
     int32_t Hq, Hkv;        /* query and KV heads of a row; Hq = G Hkv, G in
@@ -734,6 +734,7 @@ KVC_API kvc_status kvc_qk_norm_rope(const kvc_rope *r, int32_t B, int32_t T, con
 /* ------------------------------------------------------------------ */
 
 /*
+ * (Here a page is a piece of memory, not a source.)
  * A prompt before its selection, or a layer that keeps all of its tokens, lives
  * in pages of a pool that sequences share: no rows are reserved, and a row may
  * be held in 8 bits.  kvc_page_write puts rows in, kvc_page_attend appends one

@@ -32,6 +32,8 @@
 // lengths.  A warp walks its part alone, without a barrier, the next tile's rows
 // on their way in registers across the ends of units.  A unit that is cut leaves
 // its parts in the workspace, which a second kernel joins in the order of the line.
+// Short units that all fit at once go whole to a cluster each, whose warps take its
+// tiles in turn and join over distributed shared memory: no line, no second kernel.
 //
 // Measured, calls replayed as a graph: 8 units x 131071 slots bf16 87 us (6.2 TB/s;
 // 81.7 without the join), 128 units x <= 32768 e4m3 140 us (6.5; 138), 1024 units x
@@ -62,7 +64,7 @@ struct AttendArgs {
     int32_t *status, *part_bad;                  // [2 kWorkers]
     int2 *cuts;                                  // [U] the first and the last worker that has a part
     float *part_o, *part_ml;                     // [2 kWorkers][G][d], [2 kWorkers][G][2]
-    int S, G, max_len;
+    int S, G, max_len, cluster;
 };
 
 __device__ __forceinline__ uint4 ldg16(const void *p)
@@ -156,10 +158,46 @@ struct Shared {
     __align__(16) uint8_t row[kWarps][2][kD * 2];          // as they are held
     int scratch[33];
     int seq[kWarps], at[kWarps];
-    // kWhole: the warps' sums
+    // kWhole: the warps' sums, whether a page was bad
     __align__(16) float o[kWhole ? kWarps : 1][kHeads][kD + 4];
-    float m[kWarps][kHeads], l[kWarps][kHeads];
+    __align__(8) float2 ml[kWhole ? kWarps : 1][kHeads];
+    int bad;
 };
+
+// what stands at the same place of CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t far_address(const void *p, uint32_t rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ int far_int(const int *p, uint32_t rank)
+{
+    int r;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(r) : "r"(far_address(p, rank)) : "memory");
+    return r;
+}
+
+__device__ __forceinline__ float2 far_float2(const float2 *p, uint32_t rank)
+{
+    float2 r;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                 : "=f"(r.x), "=f"(r.y)
+                 : "r"(far_address(p, rank))
+                 : "memory");
+    return r;
+}
+
+__device__ __forceinline__ float4 far_float4(const float *p, uint32_t rank)
+{
+    float4 r;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w)
+                 : "r"(far_address(p, rank))
+                 : "memory");
+    return r;
+}
 
 // What a lane holds of the slots a warp has of a tile: kBlocks blocks of 16.
 template <bool kE4m3>
@@ -277,14 +315,14 @@ __global__ void __launch_bounds__(kShares < 8 ? 256 : 32 * kShares) join_kernel(
 
 // kFew: at most four heads, whose weights' two terms are columns h and h + 4 of one
 // product.
-// kWhole: a unit goes whole to a CTA, whose warps take every fourth tile and meet in
-// shared memory: neither the line nor a second kernel is needed.
+// kWhole: a unit goes whole to a cluster of a.cluster CTAs (1 to 8), whose warps take
+// its tiles in turn and meet in shared memory: neither the line nor a second kernel is
+// needed.
 template <bool kE4m3, bool kFew, bool kWhole>
 __global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __grid_constant__ AttendArgs a)
 {
     using F = Frags<kE4m3>;
     constexpr int kBlocks = F::kBlocks, kTile = F::kSlots, kRow = F::kRow;
-    constexpr int kStep = kWhole ? kWarps : 1;
     __shared__ Shared<kWhole> sm;
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kFull, tid >> 5, 0);   // uniform
     const int g = lane >> 2, c = lane & 3;
@@ -298,8 +336,10 @@ __global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __gri
     Walk cur;                                    // the unit at hand
     int id = 0, t, t_end, unit_at = 0;           // the worker, its part of the line, the unit's first tile
     LineCuts cuts(1, 0);
+    const int step = kWhole ? a.cluster * kWarps : 1;      // tiles from one of a warp to its next
     if (kWhole) {
-        const int u = blockIdx.x;
+        const int u = blockIdx.x / (unsigned)a.cluster;
+        id = (blockIdx.x - u * a.cluster) * kWarps + warp;
         cur.s = a.pg.by_heads(u);
         cur.h = u - cur.s * heads;
         cur.n = a.pg.len[cur.s];
@@ -308,9 +348,9 @@ __global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __gri
         t = 0, t_end = cur.tiles;
         if (t_end == 0) {
             if (tid == 0) record_status(a.status, KVC_ERR_SHAPE);
-            return;
+            return;                              // the whole cluster
         }
-        cur.tile = warp;
+        cur.tile = id;
     } else {
         const int each = (a.S + kThreads - 1) / kThreads;
         const int s0 = min(a.S, tid * each), s1 = min(a.S, s0 + each);
@@ -363,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __gri
 
     // the tile after the one at hand is on its way, its successor's pages are known
     Walk far = cur;
-    int far_left = kWhole ? (t_end - warp + kWarps - 1) / kWarps : t_end - t;
+    int far_left = kWhole ? (t_end - id + step - 1) / step : t_end - t;
     int far_h = 0, far_slot = 0, far_live = 0, ids[kBlocks];       // of what is loaded next
     bool far_bad = false;
     F f;
@@ -374,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __gri
 #pragma unroll
         for (int b = 0; b < kBlocks; b++) ids[b] = far_live > 16 * b ? a.pg.entry(far.s, far_slot + 16 * b) : 0;
         --far_left;
-        far.tile += kStep;
+        far.tile += step;
         if (!kWhole && far_left > 0 && far.tile == far.tiles) next_unit(far);
     };
     auto load = [&](bool keys) {
@@ -442,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __gri
         const int u = cur.s * heads + cur.h, n = cur.n, tiles = cur.tiles;
         const int first = cur.tile, end = min(t_end - unit_at, tiles);
         // the new token's slot is in the last tile
-        const bool has_new = app && end == tiles && (!kWhole || (tiles - 1) % kWarps == warp);
+        const bool has_new = app && end == tiles && (!kWhole || (tiles - 1) % step == id);
         copies_wait();
         __syncwarp();
 
@@ -502,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __gri
 
         float acc[8][4] = {}, m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
         bool bad = false;
-        for (int tile = first; tile < end; tile += kStep) {
+        for (int tile = first; tile < end; tile += step) {
             int live = n - tile * kTile;
             bad |= far_bad;
             far_bad = false;
@@ -668,8 +708,8 @@ __global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __gri
                 for (int j = 0; j < 4; j++) acc[i][j] += __shfl_xor_sync(kFull, acc[i][j], 2);
         if (kWhole) {
             if (g == 0) {
-                sm.m[warp][2 * c] = m0, sm.m[warp][2 * c + 1] = m1;
-                sm.l[warp][2 * c] = l0, sm.l[warp][2 * c + 1] = l1;
+                sm.ml[warp][2 * c] = make_float2(m0, l0);
+                sm.ml[warp][2 * c + 1] = make_float2(m1, l1);
             }
 #pragma unroll
             for (int j = 0; j < 2; j++)
@@ -680,24 +720,50 @@ __global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __gri
                         *reinterpret_cast<float4 *>(&sm.o[warp][2 * c + j][d]) =
                             make_float4(acc[i][j], acc[i][2 + j], acc[i + 1][j], acc[i + 1][2 + j]);
                     }
-            if (__syncthreads_or(bad)) {
-                if (tid == 0) record_status(a.status, KVC_ERR_INVALID_ARG);
+            const int any_bad = __syncthreads_or(bad);
+            // a warp per head; lane w has the weight of the cluster's warp w
+            auto join = [&](auto read_ml, auto read_o) {
+                for (int hh = id; hh < G; hh += step) {
+                    float2 ml = make_float2(-INFINITY, 0.f);
+                    if (lane < step) ml = read_ml(hh);
+                    const float M = warp_max(ml.x);
+                    const float r = ml.x == -INFINITY ? 0.f : pow2(ml.x - M);       // 0 keeps a NaN
+                    const float L = warp_sum(r * ml.y);
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int w0 = 0; w0 < step; w0 += kWarps) {
+                        float4 x[kWarps];
+#pragma unroll
+                        for (int w = 0; w < kWarps; w++) x[w] = read_o(w0, w, hh);
+#pragma unroll
+                        for (int w = 0; w < kWarps; w++) {
+                            const float f = __shfl_sync(kFull, r, w0 + w);
+                            o = make_float4(fmaf(f, x[w].x, o.x), fmaf(f, x[w].y, o.y), fmaf(f, x[w].z, o.z),
+                                            fmaf(f, x[w].w, o.w));
+                        }
+                    }
+                    store_row(a, (size_t)u * G + hh, lane, M, L, o);
+                }
+            };
+            if (a.cluster == 1) {                // without the cluster's barriers (1 us of 4.6)
+                if (!any_bad)
+                    join([&](int hh) { return sm.ml[lane][hh]; },
+                         [&](int, int w, int hh) { return *reinterpret_cast<const float4 *>(&sm.o[w][hh][lane * 4]); });
+                else if (tid == 0)
+                    record_status(a.status, KVC_ERR_INVALID_ARG);
                 return;
             }
-            for (int hh = warp; hh < G; hh += kWarps) {
-                float M = -INFINITY, L = 0.f;
-                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int w = 0; w < kWarps; w++) M = fmaxf(M, sm.m[w][hh]);
-#pragma unroll
-                for (int w = 0; w < kWarps; w++) {
-                    const float r = sm.m[w][hh] == -INFINITY ? 0.f : pow2(sm.m[w][hh] - M);   // 0 keeps a NaN
-                    const float4 x = *reinterpret_cast<const float4 *>(&sm.o[w][hh][lane * 4]);
-                    L = fmaf(r, sm.l[w][hh], L);
-                    o = make_float4(fmaf(r, x.x, o.x), fmaf(r, x.y, o.y), fmaf(r, x.z, o.z), fmaf(r, x.w, o.w));
-                }
-                store_row(a, (size_t)u * G + hh, lane, M, L, o);
-            }
+            if (tid == 0) sm.bad = any_bad;
+            cluster_arrive();
+            cluster_wait();
+            const uint32_t there = lane / kWarps;
+            if (!__any_sync(kFull, lane < step && far_int(&sm.bad, there) != 0))
+                join([&](int hh) { return far_float2(&sm.ml[lane % kWarps][hh], there); },
+                     [&](int w0, int w, int hh) { return far_float4(&sm.o[w][hh][lane * 4], w0 / kWarps); });
+            else if (id == 0 && lane == 0)
+                record_status(a.status, KVC_ERR_INVALID_ARG);
+            // no CTA ends while another reads its sums
+            cluster_arrive();
+            cluster_wait();
             return;
         }
         const bool whole = first == 0 && end == tiles;
@@ -752,6 +818,25 @@ size_t page_ws_bytes(const kvc_pages &pg, int G)
            align_up((size_t)2 * kWorkers * G * 2 * 4) + align_up((size_t)2 * kWorkers * G * kD * 4);
 }
 
+// as launch_following, in clusters
+static cudaError_t launch_clusters(void (*kernel)(AttendArgs), int ctas, int cluster, cudaStream_t st,
+                                   const AttendArgs &a)
+{
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3(ctas);
+    c.blockDim = dim3(kThreads);
+    c.stream = st;
+    cudaLaunchAttribute at[2] = {};
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    c.attrs = at;
+    c.numAttrs = 2;
+    return cudaLaunchKernelEx(&c, kernel, a);
+}
+
 cudaError_t launch_page_attend(const kvc_pages &pg, int G, int max_len, const uint16_t *q,
                                const uint16_t *k_new, const uint16_t *v_new, uint16_t *o, float *lse,
                                void *ws, cudaStream_t st)
@@ -777,18 +862,26 @@ cudaError_t launch_page_attend(const kvc_pages &pg, int G, int max_len, const ui
     a.G = G;
     a.max_len = max_len;
     const bool e4m3 = pg.type == KVC_PAGE_E4M3, few = G <= 4;
-    // Short units that all fit at once go whole to a CTA each (a cold call, 8 / 64 / 128 units of
-    // 64 slots in bf16: 8.2 / 8.2 / 9.5 us, the line 12.3 / 13 / 16.4; of 512 slots 15.7 / 16.4 /
-    // 16.4 and 14.0 / 16.4 / 20.5; of 1024 22.5 / 24.6 / 24.6 and 14.3 / 18.4 / 24.6; 4096 units of
-    // 64 in e4m3: 51 and 33)
-    if (max_len <= 512 && pg.U <= kGrid) {
+    const int tile = e4m3 ? Frags<true>::kSlots : Frags<false>::kSlots;
+    // Units that are all at work at once, and short, go whole to a cluster each: as many CTAs as
+    // there are SMs for, four tiles at least for each, at most ten for a warp.  In a graph, cluster /
+    // line (8 units in clusters of 8, 32 of 4, 64 of 2, 128 and 456 alone): e4m3, 512 slots 6.6 /
+    // 8.9, 6.8 / 9.4, 7.5 / 9.6, 8.2 / 11.4, 12.9 / 18.2 us; 1024 slots 7.3 / 9.5, 7.8 / 10.3, 9.5 /
+    // 11.6, 13.9 / 14.3, 21.3 / 25.0; 4096 slots 10.1 / 11.5, 15.1 / 14.8, 25.7 / 18.7, 45 / 27;
+    // bf16, 4096 slots 10.7 / 14.2, 21.1 / 17.6.  Larger clusters: 64 units of 512 slots in e4m3 8.9
+    // in 4, 14.5 in 8.
+    const int tiles_each = (max_len - 1) / tile + 1;
+    int cluster = 8;
+    while (cluster > 1 && ((int64_t)pg.U * cluster > 152 || 4 * cluster > tiles_each)) cluster /= 2;
+    a.cluster = cluster;
+    if (pg.U <= kGrid && tiles_each <= 10 * kWarps * cluster) {
         void (*kernel)(AttendArgs) = e4m3 ? (few ? attend_kernel<true, true, true> : attend_kernel<true, false, true>)
                                           : (few ? attend_kernel<false, true, true> : attend_kernel<false, false, true>);
-        return launch_following(kernel, dim3(pg.U), kThreads, 0, st, a);
+        return cluster == 1 ? launch_following(kernel, dim3(pg.U), kThreads, 0, st, a)
+                            : launch_clusters(kernel, pg.U * cluster, cluster, st, a);
     }
     // no more CTAs than there can be tiles
-    const int tile = e4m3 ? Frags<true>::kSlots : Frags<false>::kSlots;
-    const int64_t tiles = (int64_t)pg.U * ((max_len - 1) / tile + 1);
+    const int64_t tiles = (int64_t)pg.U * tiles_each;
     const dim3 grid((unsigned)(tiles < kGrid ? tiles : kGrid));
     void (*kernel)(AttendArgs) = e4m3 ? (few ? attend_kernel<true, true, false> : attend_kernel<true, false, false>)
                                       : (few ? attend_kernel<false, true, false> : attend_kernel<false, false, false>);
