@@ -15,10 +15,13 @@
 // Bound by the bytes, 512 per head read and written, with the instructions close
 // behind (141 for two heads took 80 % of the issue slots of the time of the bytes):
 // weights, cosine and sine are one 2x2 of a pair, formed once per token and kind of
-// head, applied in packed fp32 pairs.  Measured: one token of 48 heads 6.8 us (the
-// host's part of the call), 16 x 24 tokens 7.6, 32768 tokens 137 (5.9 TB/s; a block
-// per token without the 2x2 took 319).  Four blocks of 64 registers and four rows in
-// flight per team: 139; two rows 150, three 146; three blocks 152; two of 100 181.
+// head, applied in packed fp32 pairs.  Value heads go along with the key heads, so
+// that a tile waits for memory three times and not four (135.6 -> 133.2 us).
+// Measured: one token of 48 heads 6.5 us (3.2 in a graph), 16 x 24 tokens 7.0 (4.2),
+// 32768 tokens 133 (6.0 TB/s; a block per token without the 2x2 took 319).  Four
+// blocks of 64 registers and four rows in flight per team, against (with value heads
+// by themselves): two rows 150, three 146, three blocks 152, two of 100 registers 181;
+// loads and stores marked as streaming 141; the next position loaded ahead 146.
 #include "kvc_page.h"
 
 #include <algorithm>
@@ -82,8 +85,9 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const __grid_
     const uint64_t fraction = turns_it ? turn_fraction(a.inv_freq[pair]) : 0;
     const int G = 1 << a.gshift, nq = a.Hkv << a.gshift, nk = nq + a.Hkv;
     const int r0 = blockIdx.y * rows, r1 = min(nk + a.Hkv, r0 + rows);
-    const int turn0 = max(r0, a.q ? 0 : nq), turn1 = min(r1, a.k ? nk : nq);    // rows that turn
-    const int copy0 = a.v ? max(r0, nk) : r1;                                   // rows that do not
+    // the rows of queries, and of keys with the values behind them, that are written
+    const int q0 = a.q ? r0 : nq, q1 = min(r1, nq);
+    const int kv0 = max(r0, a.k ? nq : nk), kv1 = min(r1, a.v ? nk + a.Hkv : nk);
 
     int buf = 0;
     for (int tok0 = blockIdx.x * kTok; tok0 < tokens; tok0 += gridDim.x * kTok, buf ^= 1) {
@@ -104,7 +108,7 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const __grid_
         const int first = team % kPer;
 #pragma unroll 1
         for (int keys = 0; keys < 2; keys++) {
-            const int from = keys ? max(turn0, nq) : turn0, upto = keys ? turn1 : min(turn1, nq);
+            const int from = keys ? kv0 : q0, upto = keys ? kv1 : q1;
             if (from + first >= upto) continue;
             // a turn after the weights: (y_1, y_2) -> (A y_1 - B y_2, C y_2 + D y_1)
             const uint16_t *weight = keys ? a.kw : a.qw;
@@ -167,6 +171,12 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const __grid_
                 for (int i = 0; i < kAhead; i++) {
                     const int at = r + i * kPer;
                     if (at >= upto) break;
+                    if (at >= nk) {              // a value head goes as it is
+                        uint16_t *dst = a.v + (row + (int64_t)(at - nk) * a.T) * kD;
+                        *reinterpret_cast<uint2 *>(dst + d0) = w[i][0];
+                        *reinterpret_cast<uint2 *>(dst + d1) = w[i][1];
+                        continue;
+                    }
                     const float2 n2 = make_float2(inv[i], inv[i]);
                     float2 y[4], z[4];
                     y[0] = mul2(make_float2(bf_lo(w[i][0].x), bf_hi(w[i][0].x)), n2);
@@ -194,9 +204,6 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const __grid_
                 }
             }
         }
-        for (int r = copy0 + first; r < r1; r += kPer)
-            *reinterpret_cast<uint4 *>(a.v + (row + (int64_t)(r - nk) * a.T) * kD + lane * 8) =
-                __ldg(reinterpret_cast<const uint4 *>(src + r * kD + lane * 8));
     }
 }
 
