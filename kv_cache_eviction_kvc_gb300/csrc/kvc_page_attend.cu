@@ -46,6 +46,7 @@
 #include "kvc_page.h"
 
 #include <cuda_fp16.h>
+#include <limits.h>
 #include <math.h>
 
 namespace kvc {
@@ -225,20 +226,24 @@ __device__ __forceinline__ void store_row(const AttendArgs &a, size_t i, int lan
     if (lane == 0) a.lse[i] = (M + log2f(L)) * 0.6931471805599453f;
 }
 
+enum { kNothing, kDone, kTooMany };
+
 // A share of the parts of row i (unit and head) over the maximum of all: sums o and L.
-// False where there are none, or none to be written.
-template <int kShares>
-__device__ __forceinline__ bool sum_parts(const AttendArgs &a, int i, int share, int lane, float &M, float &L, float4 &o)
+// kNothing where there are none, or none to be written; kTooMany, and nothing done,
+// where there are more than `most`.
+__device__ __forceinline__ int sum_parts(const AttendArgs &a, int i, int share, int shares, int lane, int most,
+                                         float &M, float &L, float4 &o)
 {
     const int G = a.G;
     const int u = i / G, hh = i - u * G;
     const int2 cut = a.cuts[u];
     const int n = a.pg.len[a.pg.by_heads(u)];
     // a unit that was refused has no parts, and what stands in cuts is another call's
-    if (n < 0 || n > a.max_len - (a.k_new != nullptr) || cut.x >= cut.y) return false;
+    if (n < 0 || n > a.max_len - (a.k_new != nullptr) || cut.x >= cut.y) return kNothing;
     const int parts = cut.y - cut.x + 1;
+    if (parts > most) return kTooMany;
     auto slot = [&](int p) { return 2 * (cut.x + p) + (p == 0); };
-    const int mine = (parts - 1) / kShares + 1, end = min(parts, (share + 1) * mine);
+    const int mine = (uint32_t)(parts - 1) / (uint32_t)shares + 1, end = min(parts, (share + 1) * mine);
     // the first sums load beside the maxima: most units have two or three parts
     float4 x[8];
     auto load = [&](int p) {
@@ -256,7 +261,7 @@ __device__ __forceinline__ bool sum_parts(const AttendArgs &a, int i, int share,
     M = warp_max(M);
     if (__any_sync(kFull, wrong)) {
         if (lane == 0) record_status(a.status, KVC_ERR_INVALID_ARG);
-        return false;
+        return kNothing;
     }
     for (int p0 = share * mine; p0 < end; p0 += 32) {
         float2 ml = make_float2(-INFINITY, 0.f);
@@ -275,41 +280,58 @@ __device__ __forceinline__ bool sum_parts(const AttendArgs &a, int i, int share,
             load(p0 + j0 + 8);
         }
     }
-    return true;
+    return kDone;
 }
 
 // The parts of units that were cut, joined in the order of the line: kShares warps
 // per row (unit and head), each a share of the parts.  Four dimensions a lane; weights
 // of 32 parts are formed in the lanes, their sums added up with 8 loads in flight.
+// With one warp per row, rows of many parts (a long unit among short ones) are taken
+// by the whole block; a unit's rows belong to different blocks.
 template <int kShares>
-__global__ void __launch_bounds__(kShares < 8 ? 256 : 32 * kShares) join_kernel(const __grid_constant__ AttendArgs a)
+__global__ void __launch_bounds__(kShares < 8 ? 256 : 32 * kShares, kShares < 8 ? 4 : 1) join_kernel(const __grid_constant__ AttendArgs a)
 {
     constexpr int kJoinWarps = kShares < 8 ? 8 : kShares, kRows = kJoinWarps / kShares;
+    constexpr int kMost = 24;                    // parts that a warp takes alone
     __shared__ float4 sums[kJoinWarps][32];
     __shared__ float part_l[kJoinWarps];
+    __shared__ int many[kJoinWarps];
     follow();
     lead();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = a.G, rows = a.S * a.pg.heads * G;
-    const int share = warp % kShares;
-    for (int i0 = blockIdx.x * kRows; i0 < rows; i0 += gridDim.x * kRows) {
-        const int i = i0 + warp / kShares;
-        float M = -INFINITY, L = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        const bool done = i < rows && sum_parts<kShares>(a, i, share, lane, M, L, o);
-        if (kShares > 1) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rows = a.S * a.pg.heads * a.G;
+    for (int i0 = blockIdx.x; i0 < rows; i0 += gridDim.x * kRows) {
+        // kShares = 1: first every warp its own row, then the block row after row of those left over
+        constexpr int kTurns = kShares == 1 ? 1 + kRows : 1;
+#pragma unroll 1
+        for (int turn = 0; turn < kTurns; turn++) {
+            const bool alone = kShares == 1 && turn == 0;
+            if (turn > 0 && !many[turn - 1]) continue;
+            const int shares = alone ? 1 : kShares == 1 ? kJoinWarps : kShares, share = warp % shares;
+            const int i = i0 + (turn > 0 ? turn - 1 : warp / shares) * gridDim.x;
+            float M = -INFINITY, L = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            const int done = i < rows ? sum_parts(a, i, share, shares, lane, alone ? kMost : INT_MAX, M, L, o) : kNothing;
+            if (alone) {
+                if (done == kDone) store_row(a, i, lane, M, L, o);
+                if (lane == 0) many[warp] = done == kTooMany;
+                __syncthreads();
+                continue;
+            }
             sums[warp][lane] = o;
             if (lane == 0) part_l[warp] = L;
             __syncthreads();
-            if (share == 0)
+            if (share == 0 && done == kDone) {
 #pragma unroll 8
-                for (int w = 1; w < kShares; w++) {
+                for (int w = 1; w < shares; w++) {
                     const float4 x = sums[warp + w][lane];
                     o = make_float4(o.x + x.x, o.y + x.y, o.z + x.z, o.w + x.w);
                     L += part_l[warp + w];
                 }
+                store_row(a, i, lane, M, L, o);
+            }
             __syncthreads();
         }
-        if (done && share == 0) store_row(a, i, lane, M, L, o);
+        if (kShares == 1) __syncthreads();       // many is written again
     }
 }
 

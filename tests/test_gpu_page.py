@@ -304,12 +304,14 @@ def test_bound_above_the_lengths_changes_nothing(e4m3):
                                     (1, [700] * 700), (4, [511] * 456), (4, [512] * 456), (4, [511] * 457),
                                     (2, [0] * 500), (4, [513, 0]), (8, [4094, 100, 0, 2049] * 2), (1, [4095]),
                                     (4, [8190, 1]), (4, [10239, 1]), (4, [10241, 1]), (2, [5119, 60]), (2, [5121, 60]), (2, [1023, 7] * 16), (8, [30, 40]),
+                                    (4, [70000] + [5, 0, 33] * 100), (1, [1] * 700 + [40000, 3000]),
                                     (4, [260] * 77), (4, [1023, 300, 0] * 50)])
 def test_attend_every_way_the_work_is_cut(e4m3, G, lens):
     """One unit over all warps, units of many and of few parts, whole units in clusters of every
     size, up to the number and the length that go so and one more, empty units only."""
     p = Pool(len(lens) + G, 1, lens, 64 if max(lens) > 1000 else 16, e4m3, more=1)
     some = sorted({0, 1, len(lens) // 2, len(lens) - 2, len(lens) - 1} & set(range(len(lens))))
+    # (a long unit among many short ones is joined by a block)
     check_attend(p, G, units=some)
     check_attend(p, G, append=False, units=some)
 
