@@ -18,7 +18,7 @@
 // head, applied in packed fp32 pairs.  Value heads go along with the key heads, so
 // that a tile waits for memory three times and not four (135.6 -> 133.2 us).
 // Measured: one token of 48 heads 6.5 us (3.2 in a graph), 16 x 24 tokens 7.0 (4.2),
-// 32768 tokens 133 (6.0 TB/s; a block per token without the 2x2 took 319).  Four
+// 32768 tokens 131 (6.2 TB/s; a block per token without the 2x2 took 319).  Four
 // blocks of 64 registers and four rows in flight per team, against (with value heads
 // by themselves): two rows 150, three 146, three blocks 152, two of 100 registers 181;
 // loads and stores marked as streaming 141; the next position loaded ahead 146.
@@ -31,8 +31,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTeams = kThreads / 16;            // of sixteen lanes: a head each
-constexpr int kTok = 4;                          // tokens of a tile
-constexpr int kPer = kTeams / kTok;              // teams of a token
 constexpr int kAhead = 4;                        // rows a team has in flight
 constexpr int kResident = 4;                     // blocks per SM
 
@@ -63,12 +61,13 @@ __device__ __forceinline__ void unpack4(uint2 w, float *f)
     f[3] = bf_hi(w.y);
 }
 
-// Tiles of four tokens: their turns to shared memory (a thread each), then their
-// rows [y rows, (y + 1) rows), four teams a token.
-template <bool kInter>
+// Tiles of kTok tokens: their turns to shared memory (a thread per pair), then their
+// rows [y rows, (y + 1) rows), 16 / kTok teams a token.
+template <int kTok, bool kInter>
 __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const __grid_constant__ RopeArgs a, int tokens,
-                                                        int rows)
+                                                                   int rows)
 {
+    constexpr int kPer = kTeams / kTok;          // teams of a token
     __shared__ float4 turns[2][kTok][2][16];     // (c, s, c, s) of pairs 4l .. 4l + 3
     follow();
     lead();
@@ -91,13 +90,15 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const __grid_
 
     int buf = 0;
     for (int tok0 = blockIdx.x * kTok; tok0 < tokens; tok0 += gridDim.x * kTok, buf ^= 1) {
-        if (turns_it && tok0 + pair_tok < tokens) {
-            const uint64_t at = (uint64_t)(int64_t)a.pos[tok0 + pair_tok] * fraction;
-            float s, c;
-            sincospif(__ll2float_rn((long long)at) * 1.0842021724855044e-19f, &s, &c);   // 2^-63
-            float2 *to = reinterpret_cast<float2 *>(&turns[buf][pair_tok][(pair >> 1) & 1][pair >> 2]);
-            to[pair & 1] = make_float2(c * a.scale, s * a.scale);
-        }
+#pragma unroll
+        for (int j = 0; j < kTok; j += kThreads / 64)
+            if (turns_it && tok0 + pair_tok + j < tokens) {
+                const uint64_t at = (uint64_t)(int64_t)a.pos[tok0 + pair_tok + j] * fraction;
+                float s, c;
+                sincospif(__ll2float_rn((long long)at) * 1.0842021724855044e-19f, &s, &c);   // 2^-63
+                float2 *to = reinterpret_cast<float2 *>(&turns[buf][pair_tok + j][(pair >> 1) & 1][pair >> 2]);
+                to[pair & 1] = make_float2(c * a.scale, s * a.scale);
+            }
         __syncthreads();
         const int j = team / kPer, tok = tok0 + j;
         if (tok >= tokens) continue;
@@ -234,15 +235,23 @@ cudaError_t launch_qk_norm_rope(const kvc_rope &r, int B, int T, const uint16_t 
     a.scale = r.scale;
     a.by_T = FastDiv((uint32_t)T);
     const int tokens = B * T, rows = r.Hq + 2 * r.Hkv;
+    // Tokens of a tile: enough rows for its 16 teams, not so many that few tiles have the work (4, 8
+    // and 16 tokens, tiles of much work: 6 rows a token 445 / 297 / 184 us, 24 rows 161 / 131 / 133,
+    // 48 rows 133 / 131 / 144, 80 rows 129 / 134 / 152; 1024 tokens of 24 rows 7.7 / 5.9 / 7.2; 64 of
+    // 48 rows 3.6 / 4.7 / 7.0)
+    int tok = 16;
+    while (tok > 4 && (tok * rows > 384 || tokens < 128 * tok)) tok /= 2;
     // Persistent blocks, four per SM (16 or 54 per SM in turn: within 3 %).  Few tokens: a token's
-    // rows go to several blocks, as many as fill the device (384 tokens of 48 rows: three blocks
-    // 10.2, one 12.3 us; 1024: two 12.5, three 14.3, one 14.3; 4096: one 26.6, three 28.8)
-    const int tiles = (tokens - 1) / kTok + 1, fill = 152 * kResident;
+    // rows go to several blocks, as many as fill the device (384 tokens of 48 rows in tiles of 4: three
+    // blocks 10.2, one 12.3 us; 1024: two 12.5, three 14.3, one 14.3; 4096: one 26.6, three 28.8)
+    const int tiles = (tokens - 1) / tok + 1, fill = 152 * kResident;
     const int cuts = std::max(1, std::min((rows + kTeams - 1) / kTeams, fill / tiles));
     const int each = ((rows - 1) / cuts / kTeams + 1) * kTeams;
     const dim3 grid(std::min(tiles, fill), (rows - 1) / each + 1);
-    return r.interleaved ? launch_following(rope_kernel<true>, grid, kThreads, 0, st, a, tokens, each)
-                         : launch_following(rope_kernel<false>, grid, kThreads, 0, st, a, tokens, each);
+    void (*kernel)(RopeArgs, int, int) = tok == 4 ? (r.interleaved ? rope_kernel<4, true> : rope_kernel<4, false>)
+                                       : tok == 8 ? (r.interleaved ? rope_kernel<8, true> : rope_kernel<8, false>)
+                                                  : (r.interleaved ? rope_kernel<16, true> : rope_kernel<16, false>);
+    return launch_following(kernel, grid, kThreads, 0, st, a, tokens, each);
 }
 
 }  // namespace kvc

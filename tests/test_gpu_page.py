@@ -617,6 +617,36 @@ def test_rope_many_tokens():
     rope_case(17, B, T, Hkv, G, n=[1700, 1699, 1], rot=64)
 
 
+@pytest.mark.parametrize("Hkv,G,B,T", [(1, 1, 2, 1100), (1, 4, 1, 2100), (8, 1, 1, 1030), (2, 8, 3, 700)])
+def test_rope_tiles_of_every_size(Hkv, G, B, T):
+    """Tiles of 16, 8 and 4 tokens, more of them than blocks and a last one that is not full: every
+    row against a call of single tokens, which has tiles of 4, and some against the definition."""
+    rng = np.random.default_rng(T)
+    x = bf(2 * rng.standard_normal((B, T, Hkv * (G + 2) * D))).to(DEV)
+    w = bf(1 + 0.3 * rng.standard_normal(D)).to(DEV)
+    f = torch.from_numpy(1e4 ** (-np.arange(64) / 64)).to(DEV)
+    r = K.make_rope(Hkv * G, Hkv, f, w, w)
+    pos = i32(rng.integers(0, 5000, (B, T)).tolist())
+    big, small = ([torch.zeros(B * Hkv, T, *s, D, dtype=torch.bfloat16, device=DEV) for s in ((G,), (), ())]
+                  for _ in range(2))
+    K.kvc_qk_norm_rope(r, x, pos, None, *big)
+    step = 100
+    for b in range(B):
+        for t in range(0, T, step):
+            m = min(step, T - t)
+            part = [torch.zeros(Hkv, m, *s, D, dtype=torch.bfloat16, device=DEV) for s in ((G,), (), ())]
+            K.kvc_qk_norm_rope(r, x[b:b + 1, t:t + m], pos[b:b + 1, t:t + m].contiguous(), None, *part)
+            for a, p in zip(small, part):
+                a[b * Hkv:(b + 1) * Hkv, t:t + m] = p
+    for a, b in zip(big, small):
+        assert torch.equal(a, b)
+    for t in (0, T // 2, T - 1):
+        for name, at, out in (("q", 0, big[0][(B - 1) * Hkv, t, 0]), ("k", Hkv * G, big[1][(B - 1) * Hkv, t])):
+            want, bound = R.norm_rope(f64(x[B - 1, t, at * D:(at + 1) * D]), f64(w), int(pos[B - 1, t]),
+                                      f.cpu().tolist(), float(np.float32(1e-6)), False, 1.0)
+            assert (np.abs(f64(out) - want) <= bound + R.BF * np.abs(want)).all(), (name, t)
+
+
 def test_rope_positions():
     far = [0, 1, -1, -7, 1000003, 2 ** 20, 2 ** 24 + 1, 2 ** 31 - 1, -2 ** 31, 131071]
     rope_case(5, 1, len(far), 1, 2, pos=far)
