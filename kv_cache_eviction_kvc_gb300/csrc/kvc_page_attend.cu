@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kShares < 8 ? 256 : 32 * kShares, kShares < 8 
             if (alone) {
                 if (done == kDone) store_row(a, i, lane, M, L, o);
                 if (lane == 0) many[warp] = done == kTooMany;
-                __syncthreads();
+                if (!__syncthreads_or(done == kTooMany)) break;
                 continue;
             }
             sums[warp][lane] = o;
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kShares < 8 ? 256 : 32 * kShares, kShares < 8 
             }
             __syncthreads();
         }
-        if (kShares == 1) __syncthreads();       // many is written again
+        if (kShares == 1 && i0 + (int)gridDim.x * kRows < rows) __syncthreads();     // many is written again
     }
 }
 
@@ -885,18 +885,23 @@ cudaError_t launch_page_attend(const kvc_pages &pg, int G, int max_len, const ui
     a.max_len = max_len;
     const bool e4m3 = pg.type == KVC_PAGE_E4M3, few = G <= 4;
     const int tile = e4m3 ? Frags<true>::kSlots : Frags<false>::kSlots;
-    // Units that are all at work at once, and short, go whole to a cluster each: as many CTAs as
-    // there are SMs for, four tiles at least for each, at most ten for a warp.  In a graph, cluster /
-    // line (8 units in clusters of 8, 32 of 4, 64 of 2, 128 and 456 alone): e4m3, 512 slots 6.6 /
-    // 8.9, 6.8 / 9.4, 7.5 / 9.6, 8.2 / 11.4, 12.9 / 18.2 us; 1024 slots 7.3 / 9.5, 7.8 / 10.3, 9.5 /
-    // 11.6, 13.9 / 14.3, 21.3 / 25.0; 4096 slots 10.1 / 11.5, 15.1 / 14.8, 25.7 / 18.7, 45 / 27;
-    // bf16, 4096 slots 10.7 / 14.2, 21.1 / 17.6.  Larger clusters: 64 units of 512 slots in e4m3 8.9
-    // in 4, 14.5 in 8.
+    // Short units go whole to a cluster each: as many CTAs as there are SMs for, four tiles at least
+    // for each, at most ten for a warp.  In a graph, cluster / line (8 units in clusters of 8, 32 of
+    // 4, 64 of 2, 128 and 456 alone): e4m3, 512 slots 6.6 / 8.9, 6.8 / 9.4, 7.5 / 9.6, 8.2 / 11.4,
+    // 12.9 / 18.2 us; 1024 slots 7.3 / 9.5, 7.8 / 10.3, 9.5 / 11.6, 13.9 / 14.3, 21.3 / 25.0; 4096
+    // slots 10.1 / 11.5, 15.1 / 14.8, 25.7 / 18.7, 45 / 27; bf16, 4096 slots 10.7 / 14.2, 21.1 /
+    // 17.6.  Larger clusters: 64 units of 512 slots in e4m3 8.9 in 4, 14.5 in 8.  Up to two CTAs'
+    // worth of units: 768 of 256 slots 16.2 / 18.8 in e4m3, 18.6 / 22.1 in bf16; 1024 of them 20.8 /
+    // 20.6 and 24.6 / 25.7.  With many units the line's warps lose about 1 us at the end of each,
+    // which other CTAs hide: in bf16, of 128 slots on, 2048 units of 512 slots 70.7 / 77.3, 4096
+    // 132 / 148, of 1024 slots 131 / 140 (4096 of 64 40.7 / 36.5; in e4m3 no gain: 2048 of 512 49.9 /
+    // 48.8, 4096 of 256 63 / 56).
     const int tiles_each = (max_len - 1) / tile + 1;
     int cluster = 8;
     while (cluster > 1 && ((int64_t)pg.U * cluster > 152 || 4 * cluster > tiles_each)) cluster /= 2;
     a.cluster = cluster;
-    if (pg.U <= kGrid && tiles_each <= 10 * kWarps * cluster) {
+    if ((pg.U <= 2 * kGrid && tiles_each <= 10 * kWarps * cluster) ||
+        (!e4m3 && pg.U >= 4 * kGrid && tiles_each >= 8 && tiles_each <= 20 * kWarps)) {
         void (*kernel)(AttendArgs) = e4m3 ? (few ? attend_kernel<true, true, true> : attend_kernel<true, false, true>)
                                           : (few ? attend_kernel<false, true, true> : attend_kernel<false, false, true>);
         return cluster == 1 ? launch_following(kernel, dim3(pg.U), kThreads, 0, st, a)

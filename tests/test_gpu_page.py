@@ -301,7 +301,8 @@ def test_bound_above_the_lengths_changes_nothing(e4m3):
 
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("G,lens", [(8, [131071]), (1, [60001]), (8, [20000, 9, 0]), (8, [4000, 3999] * 40),
-                                    (1, [700] * 700), (4, [511] * 456), (4, [512] * 456), (4, [511] * 457),
+                                    (1, [700] * 700), (4, [511] * 456), (4, [640] * 456), (4, [511] * 457),
+                                    (4, [300, 17] * 456), (4, [300] * 913), (2, [200, 3, 126] * 608), (2, [100] * 1824),
                                     (2, [0] * 500), (4, [513, 0]), (8, [4094, 100, 0, 2049] * 2), (1, [4095]),
                                     (4, [8190, 1]), (4, [10239, 1]), (4, [10241, 1]), (2, [5119, 60]), (2, [5121, 60]), (2, [1023, 7] * 16), (8, [30, 40]),
                                     (4, [70000] + [5, 0, 33] * 100), (1, [1] * 700 + [40000, 3000]),
@@ -601,8 +602,6 @@ def test_rope_head_layouts(G, Hkv):
 @pytest.mark.parametrize("rot", [0, 16, 32, 48, 96, 112, 128])
 @pytest.mark.parametrize("normed", [(True, True), (False, False), (True, False), (False, True)])
 def test_rope_forms(interleaved, rot, normed):
-    if rot == 0 and normed == (False, False):
-        normed = (False, True)
     rope_case(rot + 3, 1, 4, 2, 2, rot=rot, interleaved=interleaved, normed=normed)
 
 
