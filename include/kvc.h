@@ -826,10 +826,12 @@ KVC_API kvc_status kvc_page_read(const kvc_pages *pg, int32_t M, int32_t ld, con
  *   n = 0: lse = -inf, o = 0.
  * q [U][G][d] bf16; o [U][G][d] bf16 (the type the output projection reads),
  * lse [U][G] fp32.  q, o, k_new, v_new are 16-byte aligned.  Logits, sums and
- * outputs are fp32 until that one rounding, weights enter the products as two
- * 16-bit terms.  max_len bounds n with the appended token, 1 <= max_len <=
- * stride * page; a bound far above the lengths costs short units a few
- * microseconds, no more.  Outputs do not overlap inputs.
+ * outputs are fp32 until that one rounding; weights enter the products as two
+ * 16-bit terms (2^-17 of a weight is left out with bf16 values; with e4m3 ones
+ * 2^-22, and 2^-24 of the largest contribution).  max_len bounds n with the
+ * appended token, 1 <= max_len <= stride * page; a bound far above the lengths
+ * costs short units a few microseconds, no more.  Outputs do not overlap inputs;
+ * calls that append to the same units are ordered by the caller.
  * Device-side errors, which leave the outputs of the units concerned as they
  * were: KVC_ERR_SHAPE (len[s] < 0, or n with the appended token above
  * max_len), KVC_ERR_INVALID_ARG (a page outside the pool).
