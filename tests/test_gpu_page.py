@@ -84,7 +84,8 @@ class Pool:
         x = f64(self.t[name].view(torch.uint8 if self.e4m3 else torch.bfloat16).cpu()[b, h, r]
                 .view(self.t[name].dtype))
         if self.e4m3:
-            x = x * self.scale[name].cpu()[b, h, r].numpy().astype(np.float64)[:, None]
+            with np.errstate(invalid="ignore"):
+                x = x * self.scale[name].cpu()[b, h, r].numpy().astype(np.float64)[:, None]
         return x
 
     def status(self):
