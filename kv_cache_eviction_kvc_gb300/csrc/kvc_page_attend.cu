@@ -226,11 +226,11 @@ __device__ __forceinline__ void store_row(const AttendArgs &a, size_t i, int lan
     if (lane == 0) a.lse[i] = (M + log2f(L)) * 0.6931471805599453f;
 }
 
-enum { kNothing, kDone, kTooMany };
+enum { kNothing, kDone, kTooMany, kBad };
 
-// A share of the parts of row i (unit and head) over the maximum of all: sums o and L.
-// kNothing where there are none, or none to be written; kTooMany, and nothing done,
-// where there are more than `most`.
+// A share of the parts of row i (unit and head): sums o and L over 2^M, M the largest
+// of the share.  kNothing where there are none; kTooMany, and nothing done, where there
+// are more than `most`; kBad where one has a page outside the pool.
 __device__ __forceinline__ int sum_parts(const AttendArgs &a, int i, int share, int shares, int lane, int most,
                                          float &M, float &L, float4 &o)
 {
@@ -243,8 +243,8 @@ __device__ __forceinline__ int sum_parts(const AttendArgs &a, int i, int share, 
     const int parts = cut.y - cut.x + 1;
     if (parts > most) return kTooMany;
     auto slot = [&](int p) { return 2 * (cut.x + p) + (p == 0); };
-    const int mine = (uint32_t)(parts - 1) / (uint32_t)shares + 1, end = min(parts, (share + 1) * mine);
-    // the first sums load beside the maxima: most units have two or three parts
+    const int mine = (uint32_t)(parts - 1) / (uint32_t)shares + 1, begin = share * mine, end = min(parts, begin + mine);
+    // the first sums load beside their maxima: one wait for a share of up to eight parts
     float4 x[8];
     auto load = [&](int p) {
 #pragma unroll
@@ -252,22 +252,22 @@ __device__ __forceinline__ int sum_parts(const AttendArgs &a, int i, int share, 
             if (p + j < end)
                 x[j] = *reinterpret_cast<const float4 *>(a.part_o + ((size_t)slot(p + j) * G + hh) * kD + lane * 4);
     };
-    load(share * mine);
+    load(begin);
     bool wrong = false;
-    for (int p = lane; p < parts; p += 32) {
-        M = fmaxf(M, a.part_ml[((size_t)slot(p) * G + hh) * 2]);
-        wrong |= a.part_bad[slot(p)] != 0;
-    }
-    M = warp_max(M);
-    if (__any_sync(kFull, wrong)) {
-        if (lane == 0) record_status(a.status, KVC_ERR_INVALID_ARG);
-        return kNothing;
-    }
-    for (int p0 = share * mine; p0 < end; p0 += 32) {
+    for (int p0 = begin; p0 < end; p0 += 32) {
         float2 ml = make_float2(-INFINITY, 0.f);
-        if (p0 + lane < end)
+        if (p0 + lane < end) {
             ml = *reinterpret_cast<const float2 *>(a.part_ml + ((size_t)slot(p0 + lane) * G + hh) * 2);
-        const float r = ml.x == -INFINITY ? 0.f : pow2(ml.x - M);       // 0 keeps a NaN
+            wrong |= a.part_bad[slot(p0 + lane)] != 0;
+        }
+        const float top = fmaxf(M, warp_max(ml.x));
+        if (p0 > begin) {
+            const float c = M == -INFINITY ? 0.f : pow2(M - top);           // 0 keeps a NaN
+            L *= c;
+            o = make_float4(o.x * c, o.y * c, o.z * c, o.w * c);
+        }
+        M = top;
+        const float r = ml.x == -INFINITY ? 0.f : pow2(ml.x - M);
         L += warp_sum(r * ml.y);
         for (int j0 = 0; j0 < 32 && p0 + j0 < end; j0 += 8) {
 #pragma unroll
@@ -280,58 +280,70 @@ __device__ __forceinline__ int sum_parts(const AttendArgs &a, int i, int share, 
             load(p0 + j0 + 8);
         }
     }
-    return kDone;
+    return __any_sync(kFull, wrong) ? kBad : kDone;
 }
 
 // The parts of units that were cut, joined in the order of the line: kShares warps
-// per row (unit and head), each a share of the parts.  Four dimensions a lane; weights
-// of 32 parts are formed in the lanes, their sums added up with 8 loads in flight.
-// With one warp per row, rows of many parts (a long unit among short ones) are taken
-// by the whole block; a unit's rows belong to different blocks.
+// per row (unit and head), each a share of the parts, whose sums meet in shared
+// memory.  Four dimensions a lane; weights of 32 parts are formed in the lanes.  With
+// one warp per row, rows of many parts (a long unit among short ones) are taken by the
+// whole block; a unit's rows belong to different blocks.
 template <int kShares>
 __global__ void __launch_bounds__(kShares < 8 ? 256 : 32 * kShares, kShares < 8 ? 4 : 1) join_kernel(const __grid_constant__ AttendArgs a)
 {
     constexpr int kJoinWarps = kShares < 8 ? 8 : kShares, kRows = kJoinWarps / kShares;
     constexpr int kMost = 24;                    // parts that a warp takes alone
     __shared__ float4 sums[kJoinWarps][32];
-    __shared__ float part_l[kJoinWarps];
-    __shared__ int many[kJoinWarps];
+    __shared__ float part_m[kJoinWarps], part_l[kJoinWarps];
+    __shared__ int got[kJoinWarps];
     follow();
     lead();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rows = a.S * a.pg.heads * a.G;
     for (int i0 = blockIdx.x; i0 < rows; i0 += gridDim.x * kRows) {
         // kShares = 1: first every warp its own row, then the block row after row of those left over
         constexpr int kTurns = kShares == 1 ? 1 + kRows : 1;
+        uint32_t left = 0;                       // rows of the block that are left over
 #pragma unroll 1
         for (int turn = 0; turn < kTurns; turn++) {
             const bool alone = kShares == 1 && turn == 0;
-            if (turn > 0 && !many[turn - 1]) continue;
+            if (turn > 0 && !(left >> (turn - 1) & 1)) continue;
             const int shares = alone ? 1 : kShares == 1 ? kJoinWarps : kShares, share = warp % shares;
             const int i = i0 + (turn > 0 ? turn - 1 : warp / shares) * gridDim.x;
             float M = -INFINITY, L = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            const int done = i < rows ? sum_parts(a, i, share, shares, lane, alone ? kMost : INT_MAX, M, L, o) : kNothing;
+            int done = i < rows ? sum_parts(a, i, share, shares, lane, alone ? kMost : INT_MAX, M, L, o) : kNothing;
             if (alone) {
                 if (done == kDone) store_row(a, i, lane, M, L, o);
-                if (lane == 0) many[warp] = done == kTooMany;
+                if (done == kBad && lane == 0) record_status(a.status, KVC_ERR_INVALID_ARG);
+                if (lane == 0) got[warp] = done;
                 if (!__syncthreads_or(done == kTooMany)) break;
+                for (int w = 0; w < kRows; w++) left |= (uint32_t)(got[w] == kTooMany) << w;
+                __syncthreads();                 // got is written again
                 continue;
             }
             sums[warp][lane] = o;
-            if (lane == 0) part_l[warp] = L;
+            if (lane == 0) part_m[warp] = M, part_l[warp] = L, got[warp] = done;
             __syncthreads();
-            if (share == 0 && done == kDone) {
-#pragma unroll 8
+            if (share == 0 && done != kNothing) {
+                float top = M;
                 for (int w = 1; w < shares; w++) {
-                    const float4 x = sums[warp + w][lane];
-                    o = make_float4(o.x + x.x, o.y + x.y, o.z + x.z, o.w + x.w);
-                    L += part_l[warp + w];
+                    top = fmaxf(top, part_m[warp + w]);
+                    if (got[warp + w] == kBad) done = kBad;
                 }
-                store_row(a, i, lane, M, L, o);
+                L = 0.f;
+                o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                for (int w = 0; w < shares; w++) {
+                    const float m = part_m[warp + w], c = m == -INFINITY ? 0.f : pow2(m - top);   // 0 keeps a NaN
+                    const float4 x = sums[warp + w][lane];
+                    L = fmaf(c, part_l[warp + w], L);
+                    o = make_float4(fmaf(c, x.x, o.x), fmaf(c, x.y, o.y), fmaf(c, x.z, o.z), fmaf(c, x.w, o.w));
+                }
+                if (done == kDone) store_row(a, i, lane, top, L, o);
+                else if (lane == 0) record_status(a.status, KVC_ERR_INVALID_ARG);
             }
             __syncthreads();
         }
-        if (kShares == 1 && i0 + (int)gridDim.x * kRows < rows) __syncthreads();     // many is written again
     }
 }
 
@@ -920,8 +932,8 @@ cudaError_t launch_page_attend(const kvc_pages &pg, int G, int max_len, const ui
         return launch_following(f, dim3((unsigned)(blocks < fill ? blocks : fill)), threads, 0, st, a);
     };
     // as many warps per row as keep a unit's parts in about one round of loads (8 units of 131071
-    // slots, 171 parts each: 8 warps 87.5 us a call, 32 87.2; 1024 units, two or three parts each:
-    // one warp 41.0, four 48.5)
+    // slots, 171 parts each: 8 warps 87.5 us a call, 32 87.2, and 85.5 since a warp looks at the maxima
+    // of its share alone; 1024 units, two or three parts each: one warp 41.0, four 48.5)
     const int parts = kWorkers / pg.U + 2;
     if (parts <= 8) return join(join_kernel<1>, 8, 256);
     if (parts <= 32) return join(join_kernel<4>, 2, 256);
