@@ -35,14 +35,16 @@
 // Short units that all fit at once go whole to a cluster each, whose warps take its
 // tiles in turn and join over distributed shared memory: no line, no second kernel.
 //
-// Measured, calls replayed as a graph: 8 units x 131071 slots bf16 87 us (6.2 TB/s;
-// 81.7 without the join), 128 units x <= 32768 e4m3 140 us (6.5; 138), 1024 units x
-// <= 1024 e4m3 41 us (5.1; 37.5), 128 x <= 3277 bf16 with 8 heads 33.4 us (5.3; 29.6),
-// 8 x 64 3.6 us.  What is left is a chain of waits at either end: lengths, pages,
-// first rows (about 4 us), the join (2 to 5 us).  Tried and slower: the next tiles
-// in a ring of shared memory filled by cp.async (8 x 131071: 115); a tile of a CTA's
-// four warps with a barrier per unit (1024 units: 48); e4m3 tiles of 16 slots (47, and
-// 44.5 with four CTAs per SM); joins by the last CTA or warp to come (registers spill).
+// Measured, calls replayed as a graph: 8 units x 131071 slots bf16 85.5 us (6.3 TB/s;
+// 80.8 without the join), 128 units x <= 32768 e4m3 139 us (6.5; 135.8), 1024 units x
+// <= 1024 e4m3 41.7 us (5.1; 37.2), 128 x <= 3277 bf16 with 8 heads 34 us (5.2; 29.9),
+// 8 x 64 3.8 us.  What is left is a chain of waits at either end: lengths, pages,
+// first rows (about 3 us), the join (4 us, of which an empty kernel is 0.5 and reading
+// the cuts 0.9).  Tried and slower: the next tiles in a ring of shared memory filled by
+// cp.async (8 x 131071: 115); a tile of a CTA's four warps with a barrier per unit (1024
+// units: 48); e4m3 tiles of 16 slots (47, and 44.5 with four CTAs per SM); joins by the
+// last CTA or warp to come (registers spill); a CTA's parts joined in shared memory
+// first (1024 units 43.9, 128 x <= 3277 37.1: the CTA waits for its slowest warp).
 #include "kvc_page.h"
 
 #include <cuda_fp16.h>
