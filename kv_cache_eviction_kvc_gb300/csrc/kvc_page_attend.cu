@@ -35,8 +35,8 @@
 // Short units that all fit at once go whole to a cluster each, whose warps take its
 // tiles in turn and join over distributed shared memory: no line, no second kernel.
 //
-// Measured, calls replayed as a graph: 8 units x 131071 slots bf16 85.5 us (6.3 TB/s;
-// 80.8 without the join), 128 units x <= 32768 e4m3 139 us (6.5; 135.8), 1024 units x
+// Measured, calls replayed as a graph: 8 units x 131071 slots bf16 84 us (6.4 TB/s;
+// 80.8 without the join), 128 units x <= 32768 e4m3 138 us (6.6; 135.8), 1024 units x
 // <= 1024 e4m3 41.7 us (5.1; 37.2), 128 x <= 3277 bf16 with 8 heads 34 us (5.2; 29.9),
 // 8 x 64 3.8 us.  What is left is a chain of waits at either end: lengths, pages,
 // first rows (about 3 us), the join (4 us, of which an empty kernel is 0.5 and reading
@@ -934,12 +934,12 @@ cudaError_t launch_page_attend(const kvc_pages &pg, int G, int max_len, const ui
         return launch_following(f, dim3((unsigned)(blocks < fill ? blocks : fill)), threads, 0, st, a);
     };
     // as many warps per row as keep a unit's parts in about one round of loads (8 units of 131071
-    // slots, 171 parts each: 8 warps 87.5 us a call, 32 87.2, and 85.5 since a warp looks at the maxima
-    // of its share alone; 1024 units, two or three parts each: one warp 41.0, four 48.5)
+    // slots, 171 parts each: 16 warps 83.6 us a call, 32 84.6; 128 units, 16 parts of 8 heads: two
+    // warps 34.4, four 33.7, eight 37.8; 1024 units, two or three parts: one warp 41.6, two 43.1)
     const int parts = kWorkers / pg.U + 2;
     if (parts <= 8) return join(join_kernel<1>, 8, 256);
     if (parts <= 32) return join(join_kernel<4>, 2, 256);
-    return join(join_kernel<32>, 1, 1024);
+    return join(join_kernel<16>, 1, 512);
 }
 
 }  // namespace kvc
