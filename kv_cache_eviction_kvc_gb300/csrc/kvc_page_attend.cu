@@ -21,8 +21,9 @@
 // power of two per head puts the largest at 2^13: bf16's 8 bits fit f16's 11 down
 // to 2^-27 of it.  With e4m3 the reference of the exponentials is the maximum of
 // x + (a power of two above the value's scale), so that the largest contribution,
-// not the largest weight, is near 1 in f16: a row of huge values that weighs
-// nothing does not push the others below f16's range.
+// not the largest weight, is near 2^7 in f16: a row of huge values that weighs
+// nothing does not push the others below f16's range, whose steps (2^-24) are 2^-31
+// of the largest contribution.
 //
 // The reference moves only when a weight passes 2^8: one vote per tile in place of
 // six exchanges, and the sums are rarely scaled.
@@ -139,11 +140,12 @@ __device__ __forceinline__ float pow2(float x)
     return r;
 }
 
-// log2 of a power of two above the scale, at least -96: exponentials over the reference
-// are then at most 2^104 (the slack among them), and sums of 2^23 of them stay in range
+// log2 of a power of two above the scale, less seven octaves, so that contributions go
+// up to 2^15 (the slack among them), near the top of f16; at least -96: exponentials over
+// the reference are then at most 2^104, and sums of 2^23 of them stay in range
 __device__ __forceinline__ float scale_log2(float s)
 {
-    return fmaxf((float)((int)(__float_as_uint(s) >> 23) - 126), -96.f);
+    return fmaxf((float)((int)(__float_as_uint(s) >> 23) - 133), -96.f);
 }
 
 // four e4m3 values as f16 (exact): the low two, the high two

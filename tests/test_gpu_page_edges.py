@@ -1,0 +1,55 @@
+"""GPU tests of the cache in pages, and of the norms and rotation in front of it,
+where the numbers are at an edge: contributions far apart, values that are not
+finite or near the ends of fp32, lengths at which a tile could be lost, places of
+a batch that are free.  Against the definitions in 64 bits (page_ref.py)."""
+import numpy as np
+import pytest
+import torch
+
+import page_ref as R
+from test_gpu_page import DEV, D, NAN, K, Pool, attend, bf, check_attend, f64, i32
+
+pytestmark = pytest.mark.gpu
+
+
+def put(p, name, u, slots, x):
+    """Rows x [len(slots)][D] of a unit of the pool."""
+    s, h = u // p.heads, u % p.heads
+    slots = np.asarray(slots)
+    b = torch.from_numpy(p.tab[s][slots // p.page].astype(np.int64)).to(DEV)
+    r = torch.from_numpy(slots % p.page).to(DEV)
+    if p.e4m3:
+        v, sc = R.quantise(f64(bf(x)))
+        p.t[name].view(torch.uint8)[b, h, r] = v.view(torch.uint8).to(DEV)
+        p.scale[name][b, h, r] = torch.from_numpy(sc).to(DEV)
+    else:
+        p.t[name][b, h, r] = bf(x).to(DEV)
+
+
+def spike(at, width=1):
+    """A row of ones in dimensions [at, at + width), zeros elsewhere."""
+    x = np.zeros(D)
+    x[at:at + width] = 1.0
+    return x
+
+
+# ---------------------------------------------------------------------- contributions far apart
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("lens", [[200, 40], [2000] * 130])
+def test_small_contributions_beside_a_large_one(e4m3, lens):
+    """One slot has nearly all of the weight and values in half of the dimensions; the others weigh
+    2^-18 to 2^-21 of it and have the other half to themselves, where each of them counts in full."""
+    p = Pool(211, 1, lens, 16, e4m3)
+    q = p.rng.standard_normal((p.U, 4, D))
+    q[:, :, 0] = 4 * np.array([18, 19, 20, 21]) / 18
+    b = -18 * np.log(2) * np.sqrt(D) / 4                   # logits of -18 octaves for the first head
+    some = [0, 1, p.U - 1]
+    for u in range(p.U) if p.U < 10 else some:
+        n = p.lens[u]
+        at = 5 + 11 * u % (n - 5)
+        put(p, "K", u, range(n), np.tile(b * spike(0), (n, 1)))
+        put(p, "K", u, [at], np.zeros((1, D)))
+        put(p, "V", u, range(n), np.tile(0.8 * spike(64, 64), (n, 1)))
+        put(p, "V", u, [at], spike(0, 64)[None])
+    check_attend(p, 4, append=False, q=bf(q).to(DEV), units=some)
