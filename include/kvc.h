@@ -824,6 +824,9 @@ KVC_API kvc_status kvc_page_read(const kvc_pages *pg, int32_t M, int32_t ld, con
  *   x_i = q_h . k_i / sqrt(d), i in [0, n), over the values as they are held;
  *   lse = log sum_i exp(x_i), o = sum_i exp(x_i - lse) v_i.
  *   n = 0: lse = -inf, o = 0.
+ * A NaN or an infinity of a value row reaches o alone, not lse; one in a key row
+ * makes the logits it enters NaN or infinite, and where one is NaN or +infinite
+ * lse and o of the head are NaN (all of them -infinite: as n = 0).
  * q [U][G][d] bf16; o [U][G][d] bf16 (the type the output projection reads),
  * lse [U][G] fp32.  q, o, k_new, v_new are 16-byte aligned.  Logits, sums and
  * outputs are fp32 until that one rounding; weights enter the products as two

@@ -142,10 +142,13 @@ __device__ __forceinline__ float pow2(float x)
 
 // log2 of a power of two above the scale, less seven octaves, so that contributions go
 // up to 2^15 (the slack among them), near the top of f16; at least -96: exponentials over
-// the reference are then at most 2^104, and sums of 2^23 of them stay in range
+// the reference are then at most 2^104, and sums of 2^23 of them stay in range.  A NaN or
+// an infinity moves no reference (the product with it is NaN all the same): lse does not
+// depend on the values
 __device__ __forceinline__ float scale_log2(float s)
 {
-    return fmaxf((float)((int)(__float_as_uint(s) >> 23) - 133), -96.f);
+    const int e = __float_as_uint(s) >> 23 & 0xff;
+    return e == 0xff ? -96.f : fmaxf((float)(e - 133), -96.f);
 }
 
 // four e4m3 values as f16 (exact): the low two, the high two

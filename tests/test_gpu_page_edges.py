@@ -53,3 +53,44 @@ def test_small_contributions_beside_a_large_one(e4m3, lens):
         put(p, "V", u, range(n), np.tile(0.8 * spike(64, 64), (n, 1)))
         put(p, "V", u, [at], spike(0, 64)[None])
     check_attend(p, 4, append=False, q=bf(q).to(DEV), units=some)
+
+
+# ---------------------------------------------------------------------- values that are not finite
+
+def lse_of(q, k):
+    """log sum exp of the logits of q [G][D] over k [n][D], and the bound of page_ref.attend."""
+    _, lse, _, bl = R.attend(q, k, np.zeros_like(k))
+    return lse, bl
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("lens", [[300, 300, 20], [40000, 3, 700], [500] * 1000])
+@pytest.mark.parametrize("bad", [NAN, -NAN, np.inf, -np.inf])
+def test_lse_beside_values_that_are_not_finite(e4m3, lens, bad):
+    """lse goes by the keys alone: a value row with a NaN or an infinity makes o NaN (in e4m3 the whole
+    row is NaN, in bf16 the dimension), and leaves lse and the other units."""
+    p = Pool(223, 1, lens, 16, e4m3)
+    x = p.rng.standard_normal((1, D))
+    x[0, 7] = bad
+    put(p, "V", 0, [len(lens) % 7 + 9], x)
+    q, _, _, o, lse = attend(p, 4, append=False)
+    assert p.status() == 0
+    for u in (0, 1, p.U - 1):
+        want, bound = lse_of(f64(q[u]), p.held("K", u, range(lens[u])))
+        assert (np.abs(f64(lse[u]) - want) <= bound).all(), (u, f64(lse[u]), want)
+    assert (o[0].isnan() if e4m3 else ~o[0, :, 7].isfinite()).all()
+    assert not o[1:].isnan().any() and (e4m3 or not o[0, :, 8:].isnan().any())
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("n", [20, 4000])
+def test_lse_with_an_appended_value_that_is_not_finite(e4m3, n):
+    p = Pool(227, 1, [n, n, n], 16, e4m3, more=1)
+    k, v = (bf(p.rng.standard_normal((3, D))) for _ in range(2))
+    v[0, 5], v[1, 5] = NAN, np.inf
+    q, _, _, o, lse = attend(p, 2, k=k.to(DEV), v=v.to(DEV))
+    assert p.status() == 0
+    for u in range(3):
+        want, bound = lse_of(f64(q[u]), p.held("K", u, range(n + 1)))
+        assert (np.abs(f64(lse[u]) - want) <= bound).all(), (u, f64(lse[u]), want)
+    assert not o[0, :, 5].isfinite().any() and not o[1, :, 5].isfinite().any() and o[2].isfinite().all()
