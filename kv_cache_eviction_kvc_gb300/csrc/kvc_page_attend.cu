@@ -19,14 +19,16 @@
 // 16-bit terms (bf16 beside bf16 values, 2^-17 of a weight left; f16 beside e4m3
 // values, which f16 holds exactly).  Queries beside e4m3 keys are f16 after a
 // power of two per head puts the largest at 2^13: bf16's 8 bits fit f16's 11 down
-// to 2^-27 of it.  With e4m3 the reference of the exponentials is the maximum of
-// x + (a power of two above the value's scale), so that the largest contribution,
-// not the largest weight, is near 2^7 in f16: a row of huge values that weighs
-// nothing does not push the others below f16's range, whose steps (2^-24) are 2^-31
-// of the largest contribution.
+// to 2^-27 of it.  With e4m3 values there are two references: the weights' sum has the
+// maximum of x, the contributions that of x + (the exponent of the value's scale), so
+// that the largest contribution, not the largest weight, is near 2^7 in f16, whose steps
+// (2^-24) are 2^-31 of it: a row of huge values that weighs nothing does not push the
+// others below f16's range, and values of any magnitude leave the weights' sum alone.
+// The second is held as its whole number of octaves above the first.
 //
-// The reference moves only when a weight passes 2^8: one vote per tile in place of
-// six exchanges, and the sums are rarely scaled.
+// A reference moves only when a weight or a contribution passes 2^8 of it: one vote per
+// tile in place of six exchanges, and the sums are rarely scaled.  What a warp, or a part
+// of a unit, gives to a join is its own o and the weights' maximum and sum.
 //
 // Work: tiles of 16 (bf16) or 32 slots of all units form one line, cut into equal
 // parts for a fixed number of warps, whatever bound the caller gives for the
@@ -140,15 +142,32 @@ __device__ __forceinline__ float pow2(float x)
     return r;
 }
 
-// log2 of a power of two above the scale, less seven octaves, so that contributions go
-// up to 2^15 (the slack among them), near the top of f16; at least -96: exponentials over
-// the reference are then at most 2^104, and sums of 2^23 of them stay in range.  A NaN or
-// an infinity moves no reference (the product with it is NaN all the same): lse does not
-// depend on the values
-__device__ __forceinline__ float scale_log2(float s)
+// 1 / x to an ulp; a NaN stays
+__device__ __forceinline__ float reciprocal(float x)
 {
-    const int e = __float_as_uint(s) >> 23 & 0xff;
-    return e == 0xff ? -96.f : fmaxf((float)(e - 133), -96.f);
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// The exponent field u of a value's scale 2^(u - 127) f, f in [1, 2).  A NaN or an infinity
+// moves no reference (the product with it is NaN all the same): lse does not depend on values.
+__device__ __forceinline__ float scale_exponent(float s)
+{
+    const uint32_t e = __float_as_uint(s) >> 23 & 0xff;
+    return e == 0xff ? 0.f : (float)(int)e;
+}
+
+// What sums of contributions over 2^(e - 127) of the weights' reference become o by: two
+// factors, neither past fp32's range, of the weights' sum l over its reference m (0 where
+// there is no weight: o is 0 then).
+template <bool kE4m3>
+__device__ __forceinline__ float2 to_mean(float m, float l, float e)
+{
+    const float inv = m == -INFINITY && l == 0.f ? 0.f : reciprocal(l);
+    if (!kE4m3) return make_float2(inv, 1.f);
+    const float h = floorf((e - 127.f) * 0.5f);
+    return make_float2(inv * pow2(h), pow2(e - 127.f - h));
 }
 
 // four e4m3 values as f16 (exact): the low two, the high two
@@ -224,19 +243,20 @@ struct Walk {
     int ahead;                                   // the next sequence's length
 };
 
-// o and lse of row i (unit and head), four dimensions a lane, of sums o and L over 2^M
+// o and lse of row i (unit and head), four dimensions a lane; L is the weights' sum over 2^M
 __device__ __forceinline__ void store_row(const AttendArgs &a, size_t i, int lane, float M, float L, float4 o)
 {
-    const float inv = M == -INFINITY && L == 0.f ? 0.f : 1.f / L;
-    *reinterpret_cast<uint2 *>(a.o + i * kD + lane * 4) =
-        make_uint2(to_bf16x2(o.x * inv, o.y * inv), to_bf16x2(o.z * inv, o.w * inv));
+    *reinterpret_cast<uint2 *>(a.o + i * kD + lane * 4) = make_uint2(to_bf16x2(o.x, o.y), to_bf16x2(o.z, o.w));
     if (lane == 0) a.lse[i] = (M + log2f(L)) * 0.6931471805599453f;
 }
 
 enum { kNothing, kDone, kTooMany, kBad };
 
-// A share of the parts of row i (unit and head): sums o and L over 2^M, M the largest
-// of the share.  kNothing where there are none; kTooMany, and nothing done, where there
+// 1 / L for sums of weights: 0 where there are none, and a NaN stays
+__device__ __forceinline__ float share_of(float L) { return L == 0.f ? 0.f : reciprocal(L); }
+
+// A share of the parts of row i (unit and head): its o, and the weights' sum L over 2^M, M
+// the largest of the share.  kNothing where there are none; kTooMany, and nothing done, where there
 // are more than `most`; kBad where one has a page outside the pool.
 __device__ __forceinline__ int sum_parts(const AttendArgs &a, int i, int share, int shares, int lane, int most,
                                          float &M, float &L, float4 &o)
@@ -268,14 +288,14 @@ __device__ __forceinline__ int sum_parts(const AttendArgs &a, int i, int share, 
             wrong |= a.part_bad[slot(p0 + lane)] != 0;
         }
         const float top = fmaxf(M, warp_max(ml.x));
-        if (p0 > begin) {
-            const float c = M == -INFINITY ? 0.f : pow2(M - top);           // 0 keeps a NaN
-            L *= c;
-            o = make_float4(o.x * c, o.y * c, o.z * c, o.w * c);
-        }
+        // weights of what there is and of the parts, as shares of their sum (0 keeps a NaN)
+        float c = p0 == begin ? 0.f : (M == -INFINITY ? 0.f : pow2(M - top)) * L;
+        float r = (ml.x == -INFINITY ? 0.f : pow2(ml.x - top)) * ml.y;
         M = top;
-        const float r = ml.x == -INFINITY ? 0.f : pow2(ml.x - M);
-        L += warp_sum(r * ml.y);
+        L = c + warp_sum(r);
+        const float inv = share_of(L);
+        c *= inv, r *= inv;
+        if (p0 > begin) o = make_float4(o.x * c, o.y * c, o.z * c, o.w * c);
         for (int j0 = 0; j0 < 32 && p0 + j0 < end; j0 += 8) {
 #pragma unroll
             for (int j = 0; j < 8; j++) {
@@ -337,13 +357,16 @@ __global__ void __launch_bounds__(kShares < 8 ? 256 : 32 * kShares, kShares < 8 
                     top = fmaxf(top, part_m[warp + w]);
                     if (got[warp + w] == kBad) done = kBad;
                 }
-                L = 0.f;
+                // lane w has the weight of share w (0 keeps a NaN)
+                float r = 0.f;
+                if (lane < shares) r = (part_m[warp + lane] == -INFINITY ? 0.f : pow2(part_m[warp + lane] - top)) * part_l[warp + lane];
+                L = warp_sum(r);
+                r *= share_of(L);
                 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
                 for (int w = 0; w < shares; w++) {
-                    const float m = part_m[warp + w], c = m == -INFINITY ? 0.f : pow2(m - top);   // 0 keeps a NaN
+                    const float c = __shfl_sync(kFull, r, w);
                     const float4 x = sums[warp + w][lane];
-                    L = fmaf(c, part_l[warp + w], L);
                     o = make_float4(fmaf(c, x.x, o.x), fmaf(c, x.y, o.y), fmaf(c, x.z, o.z), fmaf(c, x.w, o.w));
                 }
                 if (done == kDone) store_row(a, i, lane, top, L, o);
@@ -582,6 +605,7 @@ __global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __gri
         }
 
         float acc[8][4] = {}, m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+        float e0 = 1.f, e1 = 1.f;                // octaves of the contributions' reference over m, and 127
         bool bad = false;
         for (int tile = first; tile < end; tile += step) {
             int live = n - tile * kTile;
@@ -659,8 +683,9 @@ __global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __gri
 #pragma unroll
                 for (int j = 0; j < 4; j++) x[b][j] += y[j];
             }
-            // logits in base 2, what is not there at -inf; the reference's candidates
-            float top0 = -INFINITY, top1 = -INFINITY, vs[2 * kBlocks];
+            // logits in base 2, what is not there at -inf; the references' candidates
+            float top0 = -INFINITY, top1 = -INFINITY, out0 = -INFINITY, out1 = -INFINITY;
+            float vs[2 * kBlocks], high = 0.f;   // the values' scales, their largest exponent
 #pragma unroll
             for (int b = 0; b < kBlocks; b++)
 #pragma unroll
@@ -670,29 +695,52 @@ __global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __gri
                     if (kE4m3) {
                         c0 *= f.ks[b * 2 + r], c1 *= f.ks[b * 2 + r];
                         vs[b * 2 + r] = f.vs[b * 2 + r];
-                        up = scale_log2(f.vs[b * 2 + r]);
+                        up = scale_exponent(f.vs[b * 2 + r]);
+                        high = fmaxf(high, up);
                     }
                     x[b][2 * r] = on ? x[b][2 * r] * c0 : -INFINITY;
                     x[b][2 * r + 1] = on ? x[b][2 * r + 1] * c1 : -INFINITY;
-                    top0 = fmaxf(top0, x[b][2 * r] + up);
-                    top1 = fmaxf(top1, x[b][2 * r + 1] + up);
+                    top0 = fmaxf(top0, x[b][2 * r]);
+                    top1 = fmaxf(top1, x[b][2 * r + 1]);
+                    if (kE4m3) {
+                        out0 = fmaxf(out0, x[b][2 * r] + up);
+                        out1 = fmaxf(out1, x[b][2 * r + 1] + up);
+                    }
                 }
             load(true);
-            if (__any_sync(kFull, top0 > m0 + kSlack || top1 > m1 + kSlack)) {
+            // contributions are at most 2^7 where their reference is met, 2^15 with the slack
+            constexpr float kUp = 6.f;
+            bool past = top0 > m0 + kSlack || top1 > m1 + kSlack;
+            if (kE4m3) past |= out0 > m0 + e0 + (kUp + kSlack) || out1 > m1 + e1 + (kUp + kSlack);
+            if (__any_sync(kFull, past)) {
 #pragma unroll
                 for (int i = 4; i < 32; i <<= 1) {
                     top0 = fmaxf(top0, __shfl_xor_sync(kFull, top0, i));
                     top1 = fmaxf(top1, __shfl_xor_sync(kFull, top1, i));
+                    if (kE4m3) {
+                        out0 = fmaxf(out0, __shfl_xor_sync(kFull, out0, i));
+                        out1 = fmaxf(out1, __shfl_xor_sync(kFull, out1, i));
+                    }
                 }
                 const float n0 = fmaxf(m0, top0), n1 = fmaxf(m1, top1);
-                const float r0 = m0 == n0 ? 1.f : pow2(m0 - n0), r1 = m1 == n1 ? 1.f : pow2(m1 - n1);
+                float d0 = m0 == n0 ? 0.f : m0 - n0, d1 = m1 == n1 ? 0.f : m1 - n1;
+                l0 *= pow2(d0), l1 *= pow2(d1);
                 m0 = n0, m1 = n1;
-                l0 *= r0, l1 *= r1;
+                if (kE4m3) {
+                    d0 += e0, d1 += e1;          // the old reference over the new m
+                    e0 = fmaxf(ceilf(fmaxf(d0, out0 - n0 - kUp)), 1.f), e1 = fmaxf(ceilf(fmaxf(d1, out1 - n1 - kUp)), 1.f);
+                    d0 -= e0, d1 -= e1;
+                }
+                const float r0 = pow2(d0), r1 = pow2(d1);
 #pragma unroll
                 for (int i = 0; i < 8; i++) acc[i][0] *= r0, acc[i][1] *= r1, acc[i][2] *= r0, acc[i][3] *= r1;
             }
             const float ref0 = m0 == -INFINITY ? 0.f : m0, ref1 = m1 == -INFINITY ? 0.f : m1;
             // weights, O' += V' P'
+            const float s0 = pow2(127.f - e0), s1 = pow2(127.f - e1);
+            // a value 2^100 above its reference, of a weight that fp32 may not hold: the
+            // contribution is an exponential of its own
+            const bool apart = kE4m3 && high - fminf(e0, e1) > 100.f;
 #pragma unroll
             for (int b = 0; b < kBlocks; b++) {
                 float p[4];
@@ -701,8 +749,15 @@ __global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __gri
                 l0 += p[0] + p[2];
                 l1 += p[1] + p[3];
                 if (kE4m3) {
-                    p[0] *= vs[b * 2], p[1] *= vs[b * 2];
-                    p[2] *= vs[b * 2 + 1], p[3] *= vs[b * 2 + 1];
+#pragma unroll
+                    for (int j = 0; j < 4; j++) p[j] *= vs[b * 2 + (j >> 1)] * (j & 1 ? s1 : s0);
+                    if (apart)
+#pragma unroll
+                        for (int j = 0; j < 4; j++) {
+                            const float v = vs[b * 2 + (j >> 1)], up = scale_exponent(v);
+                            p[j] = pow2(x[b][j] - (j & 1 ? ref1 : ref0) + (up - (j & 1 ? e1 : e0))) *
+                                   (up == 0.f ? v : __uint_as_float((__float_as_uint(v) & 0x807fffff) | 0x3f800000));
+                        }
                 }
                 uint32_t hi0, lo0, hi1, lo1;
                 two_terms<kE4m3>(p[0], p[1], hi0, lo0);
@@ -747,6 +802,11 @@ __global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __gri
             for (int i = 0; i < 8; i++)
 #pragma unroll
                 for (int j = 0; j < 4; j++) acc[i][j] += __shfl_xor_sync(kFull, acc[i][j], 2);
+        const float2 f0 = to_mean<kE4m3>(m0, l0, e0), f1 = to_mean<kE4m3>(m1, l1, e1);
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+#pragma unroll
+            for (int j = 0; j < 4; j++) acc[i][j] = acc[i][j] * (j & 1 ? f1.x : f0.x) * (j & 1 ? f1.y : f0.y);
         if (kWhole) {
             if (g == 0) {
                 sm.ml[warp][2 * c] = make_float2(m0, l0);
@@ -768,8 +828,9 @@ __global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __gri
                     float2 ml = make_float2(-INFINITY, 0.f);
                     if (lane < step) ml = read_ml(hh);
                     const float M = warp_max(ml.x);
-                    const float r = ml.x == -INFINITY ? 0.f : pow2(ml.x - M);       // 0 keeps a NaN
-                    const float L = warp_sum(r * ml.y);
+                    float r = (ml.x == -INFINITY ? 0.f : pow2(ml.x - M)) * ml.y;    // 0 keeps a NaN
+                    const float L = warp_sum(r);
+                    r *= share_of(L);
                     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
                     for (int w0 = 0; w0 < step; w0 += kWarps) {
                         float4 x[kWarps];
@@ -816,15 +877,13 @@ __global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __gri
             const float M = j ? m1 : m0, L = j ? l1 : l0;
             if (whole) {
                 const size_t to = (size_t)u * G + hh;
-                const float inv = M == -INFINITY && L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
                 for (int i = 0; i < 8; i += 4) {
                     const int d = kE4m3 ? 16 * g + 2 * i : 8 * g + 16 * i;
                     *reinterpret_cast<uint4 *>(a.o + to * kD + d) =
-                        make_uint4(to_bf16x2(acc[i][j] * inv, acc[i][2 + j] * inv),
-                                   to_bf16x2(acc[i + 1][j] * inv, acc[i + 1][2 + j] * inv),
-                                   to_bf16x2(acc[i + 2][j] * inv, acc[i + 2][2 + j] * inv),
-                                   to_bf16x2(acc[i + 3][j] * inv, acc[i + 3][2 + j] * inv));
+                        make_uint4(to_bf16x2(acc[i][j], acc[i][2 + j]), to_bf16x2(acc[i + 1][j], acc[i + 1][2 + j]),
+                                   to_bf16x2(acc[i + 2][j], acc[i + 2][2 + j]),
+                                   to_bf16x2(acc[i + 3][j], acc[i + 3][2 + j]));
                 }
                 if (g == 0) a.lse[to] = (M + log2f(L)) * 0.6931471805599453f;
             } else {

@@ -94,3 +94,39 @@ def test_lse_with_an_appended_value_that_is_not_finite(e4m3, n):
         want, bound = lse_of(f64(q[u]), p.held("K", u, range(n + 1)))
         assert (np.abs(f64(lse[u]) - want) <= bound).all(), (u, f64(lse[u]), want)
     assert not o[0, :, 5].isfinite().any() and not o[1, :, 5].isfinite().any() and o[2].isfinite().all()
+
+
+# ---------------------------------------------------------------------- values of any magnitude
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("first,then", [(0.0, 1e12), (1e12, 0.0), (1e-30, 1e25), (1e25, 1e-30)])
+@pytest.mark.parametrize("lens", [[300, 40], [9000, 70, 700], [600] * 1000, [70000]])
+def test_weights_do_not_depend_on_the_order_of_values(e4m3, first, then, lens):
+    """A run of slots with small or no values before (behind) one with large ones: all have the same
+    weight, in one warp and across parts."""
+    p = Pool(229, 1, lens, 16, e4m3)
+    some = sorted({0, p.U // 2, p.U - 1})
+    for u in some:
+        n = lens[u]
+        i = np.arange(n)[:, None] >= n // 2
+        put(p, "V", u, range(n), np.where(i, then, first) * (1 + p.rng.random((n, D))))
+    check_attend(p, 4, append=False, q_scale=0.0, units=some)
+    check_attend(p, 4, append=False, q_scale=0.5, units=some)
+
+
+@pytest.mark.parametrize("lens", [[300, 40], [9000, 70, 700], [600] * 1000])
+@pytest.mark.parametrize("v_scale", [1e-36, 1e33, 4e37])
+def test_sharp_attention_over_values_near_the_ends_of_fp32(lens, v_scale):
+    """Values in e4m3 up to the largest fp32 holds: weights far below the largest count all the same
+    (their contributions, and their sum).  The least values are multiples of the least scale."""
+    p = Pool(233, 1, lens, 16, True, v_scale=v_scale, k_scale=2.0)
+    check_attend(p, 4, append=False, units=sorted({0, p.U // 2, p.U - 1}))
+    # one slot 20 octaves above all others, whose values have dimensions to themselves
+    n, some = lens[0], [0]
+    put(p, "K", 0, range(n), np.tile(-20 * np.log(2) * np.sqrt(D) / 4 * spike(0), (n, 1)))
+    put(p, "K", 0, [n // 2], np.zeros((1, D)))
+    put(p, "V", 0, range(n), np.tile(v_scale * spike(64, 64), (n, 1)))
+    put(p, "V", 0, [n // 2], v_scale * spike(0, 64)[None])
+    q = np.zeros((p.U, 4, D))
+    q[:, :, 0] = 4
+    check_attend(p, 4, append=False, q=bf(q).to(DEV), units=some)
