@@ -15,7 +15,11 @@
 // in shared memory, in one type for both operands (e4m3 rows against bf16
 // queries), for products that take a few percent of the time here.
 //
-// Precision.  Logits, maxima, sums and outputs are fp32.  Weights enter O' as two
+// Precision.  Logits, maxima, sums and outputs are fp32; the tensor core cuts its sums
+// off instead of rounding them, which adds up over a long run (3e-6 of o over 2300
+// slots of a warp), so it has the 16 slots of a product alone and those are added with
+// rounding (no cost but with eight heads over e4m3: 32 units x 16000 32.2 -> 33.3 us;
+// the 32 slots of a tile at once spill, 146.5 -> 149.2 for 128 units x <= 32768).  Weights enter O' as two
 // 16-bit terms (bf16 beside bf16 values, 2^-17 of a weight left; f16 beside e4m3
 // values, which f16 holds exactly).  Queries beside e4m3 keys are f16 after a
 // power of two per head puts the largest at 2^13: bf16's 8 bits fit f16's 11 down
@@ -765,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __gri
                 if (kFew && c >= 2) hi0 = lo0, hi1 = lo1;
                 hi0 = transpose8x8(hi0), hi1 = transpose8x8(hi1);
                 if (!kFew) lo0 = transpose8x8(lo0), lo1 = transpose8x8(lo1);
-                // a product's 16 rows are two dimensions of each lane's
+                // a product's 16 rows are two dimensions of each lane's; it is added with rounding
 #pragma unroll
                 for (int i = 0; i < 8; i++) {
                     uint32_t a0, a1, a2, a3;
@@ -782,8 +786,11 @@ __global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __gri
                         a2 = __byte_perm(word(f.v[2 * F::kV + j], w), word(f.v[3 * F::kV + j], w), 0x5410);
                         a3 = __byte_perm(word(f.v[2 * F::kV + j], w), word(f.v[3 * F::kV + j], w), 0x7632);
                     }
-                    mma<kE4m3>(acc[i], a0, a1, a2, a3, hi0, hi1);
-                    if (!kFew) mma<kE4m3>(acc[i], a0, a1, a2, a3, lo0, lo1);
+                    float sum[4] = {};
+                    mma<kE4m3>(sum, a0, a1, a2, a3, hi0, hi1);
+                    if (!kFew) mma<kE4m3>(sum, a0, a1, a2, a3, lo0, lo1);
+#pragma unroll
+                    for (int j = 0; j < 4; j++) acc[i][j] += sum[j];
                 }
             }
             load(false);

@@ -130,3 +130,33 @@ def test_sharp_attention_over_values_near_the_ends_of_fp32(lens, v_scale):
     q = np.zeros((p.U, 4, D))
     q[:, :, 0] = 4
     check_attend(p, 4, append=False, q=bf(q).to(DEV), units=some)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("G", [4, 8])
+def test_long_sums_are_rounded_not_cut_off(e4m3, G):
+    """Equal weights over runs of 8192 slots of values of 1.5 at most, and as many of the same negated: o is 0.
+    A sum that grows to 8192 and back is off by half its step (2^-11 at most) in each of 1024 additions
+    at most; rounded, these are either way alike, and 8 standard deviations of their sum are
+    8 2^-10 sqrt(1024 / 12) over 16384 slots, with parts (sums of 1/2, rounded to 2^-25) joined besides.
+    Cut off, they add up to 1024 2^-12 (2^-11 on the average, half of it as the sum grows)."""
+    page, runs = 128, 1824
+    x = 1 + (np.random.default_rng(5).random((page, D)) - 0.5)
+    x[1::2] /= 64                                          # bits below those that sums of the others keep
+    p = Pool(239, 1, [page, page], page, e4m3)
+    put(p, "V", 0, range(page), x)
+    put(p, "V", 1, range(page), x)
+    a, b = int(p.tab[0, 0]), int(p.tab[1, 0])
+    if e4m3:
+        p.t["V"].view(torch.uint8)[b] ^= 128
+    else:
+        p.t["V"][b].neg_()
+    n = runs * 128 * page
+    tab = torch.tensor(([a] * 64 + [b] * 64) * runs, dtype=torch.int32, device=DEV).view(1, -1)
+    p.t["table"], p.t["len"] = tab, i32([n])
+    p.U = 1
+    p.make()
+    _, _, _, o, lse = attend(p, G, append=False, max_len=n, q_scale=0.0)
+    assert p.status() == 0
+    assert np.abs(f64(o)).max() <= 8 * 2.0 ** -10 * np.sqrt(1024 / 12) / 16384 + 8 * 2.0 ** -24
+    assert np.abs(f64(lse) - np.log(n)).max() <= 8 * 2.0 ** -24 * np.log(n)
