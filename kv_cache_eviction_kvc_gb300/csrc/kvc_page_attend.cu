@@ -55,6 +55,7 @@
 #include "kvc_page.h"
 
 #include <cuda_fp16.h>
+#include <float.h>
 #include <limits.h>
 #include <math.h>
 
@@ -697,7 +698,8 @@ __global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __gri
                     const bool on = 16 * b + 8 * r + g < live;
                     float c0 = ch0, c1 = ch1, up = 0.f;
                     if (kE4m3) {
-                        c0 *= f.ks[b * 2 + r], c1 *= f.ks[b * 2 + r];
+                        // finite, so that a product of zero stays a logit of zero
+                        c0 = fminf(c0 * f.ks[b * 2 + r], FLT_MAX), c1 = fminf(c1 * f.ks[b * 2 + r], FLT_MAX);
                         vs[b * 2 + r] = f.vs[b * 2 + r];
                         up = scale_exponent(f.vs[b * 2 + r]);
                         high = fmaxf(high, up);

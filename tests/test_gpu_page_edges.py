@@ -160,3 +160,21 @@ def test_long_sums_are_rounded_not_cut_off(e4m3, G):
     assert p.status() == 0
     assert np.abs(f64(o)).max() <= 8 * 2.0 ** -10 * np.sqrt(1024 / 12) / 16384 + 8 * 2.0 ** -24
     assert np.abs(f64(lse) - np.log(n)).max() <= 8 * 2.0 ** -24 * np.log(n)
+
+
+# ---------------------------------------------------------------------- logits of any magnitude
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("lens", [[300, 40], [9000, 70], [600] * 1000])
+def test_large_queries_and_keys_that_do_not_meet(e4m3, lens):
+    """A query and keys near the ends of fp32 whose products are all zero: every logit is zero."""
+    p = Pool(241, 1, lens, 16, e4m3, more=1)
+    some = sorted({0, p.U // 2, p.U - 1})
+    for u in some:
+        put(p, "K", u, range(lens[u]), 3e37 * (1 + p.rng.random((lens[u], 1))) * spike(64, 64))
+    q = np.zeros((p.U, 4, D))
+    q[:, :, :64] = 1e38 * np.array([1, 2, 3, -3])[:, None]
+    k = bf(np.zeros((p.U, D))).to(DEV)
+    _, _, _, _, lse = check_attend(p, 4, q=bf(q).to(DEV), units=some, k=k, v=k + 1)
+    for u in some:
+        assert np.abs(f64(lse[u]) - np.log(lens[u] + 1)).max() <= 8 * 2.0 ** -24 * np.log(lens[u] + 1)
