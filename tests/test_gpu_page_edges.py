@@ -178,3 +178,46 @@ def test_large_queries_and_keys_that_do_not_meet(e4m3, lens):
     _, _, _, _, lse = check_attend(p, 4, q=bf(q).to(DEV), units=some, k=k, v=k + 1)
     for u in some:
         assert np.abs(f64(lse[u]) - np.log(lens[u] + 1)).max() <= 8 * 2.0 ** -24 * np.log(lens[u] + 1)
+
+
+# ---------------------------------------------------------------------- norms and rotation
+
+def rotated(x, w=None, pos=3, rot=128, interleaved=False, eps=1e-6, base=1e4, freq=None):
+    """One token's query and key head of x [D] through the call: [2][D], and the frequencies."""
+    f = base ** (-2.0 * np.arange(rot // 2) / rot) if rot else None
+    f = f if freq is None else np.asarray(freq, dtype=np.float64)
+    w = None if w is None else bf(w).to(DEV)
+    r = K.make_rope(1, 1, None if f is None else torch.from_numpy(f).to(DEV), w, w, eps=eps,
+                    interleaved=interleaved)
+    qkv = bf(np.concatenate([x, x, x]))[None, None].to(DEV)
+    q, k, v = (torch.zeros(1, 1, *s, D, dtype=torch.bfloat16, device=DEV) for s in ((1,), (), ()))
+    K.kvc_qk_norm_rope(r, qkv, i32([[pos]]), None, q, k, v)
+    assert torch.equal(v[0, 0].view(torch.int16), qkv[0, 0, 2 * D:].view(torch.int16))
+    return f64(torch.stack([q[0, 0, 0], k[0, 0]])), [] if f is None else f
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("rot", [0, 32, 64, 112])
+@pytest.mark.parametrize("normed", [False, True])
+@pytest.mark.parametrize("bad", [NAN, np.inf, -np.inf])
+def test_rope_of_a_row_that_is_not_finite(interleaved, rot, normed, bad):
+    """A dimension that is not turned is its own affair: y = x without a norm; with one, an infinity
+    leaves zeros elsewhere (its own place is NaN), a NaN makes the row NaN."""
+    rng = np.random.default_rng(rot)
+    w = 1 + 0.3 * rng.standard_normal(D) if normed else None
+    for at in sorted({rot, rot + 1, rot + 4, 120, 127}):
+        x = f64(bf(rng.standard_normal(D)))
+        x[at] = bad
+        got, f = rotated(x, w, rot=rot, interleaved=interleaved)
+        others = np.arange(D) != at
+        for y in got:
+            if not normed:
+                assert np.array_equal(y[at], bad, equal_nan=True)
+                clean = np.where(others, x, 0.0)
+                want, bound = R.norm_rope(clean, None, 3, f, 1e-6, interleaved, 1.0)
+                assert (np.abs(y - want)[others] <= (bound + R.BF * np.abs(want))[others]).all(), at
+                assert np.array_equal(y[rot:][others[rot:]], x[rot:][others[rot:]])
+            elif np.isnan(bad):
+                assert np.isnan(y).all()
+            else:
+                assert np.isnan(y[at]) and (y[others] == 0).all(), at
