@@ -718,8 +718,8 @@ typedef struct {
  * All in fp32 but the angles: these are fixed-point fractions of a turn, with
  * the product by the position exact modulo a turn (inv_freq / 2 pi rounded to
  * 53 bits), so far positions lose nothing.  A normed row whose squares sum
- * past fp32's range has y = 0 (NaN where it was infinite); a dimension that is
- * not turned reaches no other.
+ * past fp32's range has y = 0 (NaN where it was infinite), a row of zeros with
+ * eps = 0 is NaN; a dimension that is not turned reaches no other.
  * pos [B][T] int32 (any value).  n: DEVICE [B] live tokens of each sequence,
  * taken as within [0, T], or NULL = T: rows of the outputs at or behind it are
  * left as they were, rows of the inputs there are not used.

@@ -62,10 +62,31 @@ __device__ __forceinline__ void unpack4(uint2 w, float *f)
     f[3] = bf_hi(w.y);
 }
 
+// Where the sum of squares may have lost bits below fp32's range, and eps does not make up for
+// them, the row is taken times 2^100 (exact): what it is multiplied by then.
+constexpr float kLeastSquares = 0x1p-100f, kLeastEps = 0x1p-95f;
+
+__device__ __forceinline__ float rescaled(uint2 &w0, uint2 &w1, float eps, unsigned mates)
+{
+    constexpr float kUp = 0x1p100f;
+    float s = 0.f;
+    auto take = [&](uint32_t &w) {
+        const float2 y = scaled2(w, kUp);
+        w = to_bf16x2(y.x, y.y);
+        s = fmaf(y.x, y.x, fmaf(y.y, y.y, s));
+    };
+    take(w0.x), take(w0.y), take(w1.x), take(w1.y);
+#pragma unroll
+    for (int m = 8; m; m >>= 1) s += __shfl_xor_sync(mates, s, m, 16);
+    return rsqrtf(s * (1.f / kD) + eps * kUp * kUp);
+}
+
 // Tiles of kTok tokens: their turns to shared memory (a thread per pair), then their
 // rows [y rows, (y + 1) rows), 16 / kTok teams a token.  kAll: every dimension is turned,
-// and no lane tells itself apart (32768 tokens of 48 rows 129 us, with the test 134).
-template <int kTok, bool kInter, bool kAll>
+// and no lane tells itself apart (32768 tokens of 48 rows 129 us, with the test 134).  kTiny:
+// an eps below kLeastEps, so that rows of any magnitude keep their norm (the code for them
+// costs every row 10 to 28 %, so it is not in the others).
+template <int kTok, bool kInter, bool kAll, bool kTiny>
 __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const __grid_constant__ RopeArgs a, int tokens,
                                                                    int rows)
 {
@@ -165,7 +186,12 @@ __global__ void __launch_bounds__(kThreads, kResident) rope_kernel(const __grid_
 #pragma unroll
                         for (int i = 0; i < kAhead; i++) inv[i] += __shfl_xor_sync(mates, inv[i], m, 16);
 #pragma unroll
-                    for (int i = 0; i < kAhead; i++) inv[i] = rsqrtf(inv[i] * (1.f / kD) + a.eps);
+                    for (int i = 0; i < kAhead; i++) {
+                        if (kTiny && inv[i] < kLeastSquares && r + i * kPer < nk)
+                            inv[i] = rescaled(w[i][0], w[i][1], a.eps, mates);
+                        else
+                            inv[i] = rsqrtf(inv[i] * (1.f / kD) + a.eps);
+                    }
                 } else {
 #pragma unroll
                     for (int i = 0; i < kAhead; i++) inv[i] = 1.f;
@@ -245,7 +271,8 @@ cudaError_t launch_qk_norm_rope(const kvc_rope &r, int B, int T, const uint16_t 
     // and 16 tokens, tiles of much work: 6 rows a token 445 / 297 / 184 us, 24 rows 161 / 131 / 133,
     // 48 rows 133 / 131 / 144, 80 rows 129 / 134 / 152; 1024 tokens of 24 rows 7.7 / 5.9 / 7.2; 64 of
     // 48 rows 3.6 / 4.7 / 7.0)
-    int tok = 16;
+    const bool tiny = r.eps < kLeastEps && (r.q_weight || r.k_weight);
+    int tok = tiny ? 4 : 16;
     while (tok > 4 && (tok * rows > 384 || tokens < 128 * tok)) tok /= 2;
     // Persistent blocks, four per SM (16 or 54 per SM in turn: within 3 %).  Few tokens: a token's
     // rows go to several blocks, as many as fill the device (384 tokens of 48 rows in tiles of 4: three
@@ -256,12 +283,15 @@ cudaError_t launch_qk_norm_rope(const kvc_rope &r, int B, int T, const uint16_t 
     const dim3 grid(std::min(tiles, fill), (rows - 1) / each + 1);
     auto pick = [&](auto inter, auto all) {
         constexpr bool kInter = decltype(inter)::value, kAll = decltype(all)::value;
-        return tok == 4 ? rope_kernel<4, kInter, kAll> : tok == 8 ? rope_kernel<8, kInter, kAll> : rope_kernel<16, kInter, kAll>;
+        return tok == 4   ? rope_kernel<4, kInter, kAll, false>
+               : tok == 8 ? rope_kernel<8, kInter, kAll, false>
+                          : rope_kernel<16, kInter, kAll, false>;
     };
     const std::true_type yes;
     const std::false_type no;
-    void (*kernel)(RopeArgs, int, int) = r.interleaved ? (r.rot == kD ? pick(yes, yes) : pick(yes, no))
-                                                       : (r.rot == kD ? pick(no, yes) : pick(no, no));
+    void (*kernel)(RopeArgs, int, int) = tiny          ? (r.interleaved ? rope_kernel<4, true, false, true> : rope_kernel<4, false, false, true>)
+                                         : r.rot == kD ? (r.interleaved ? pick(yes, yes) : pick(no, yes))
+                                                       : (r.interleaved ? pick(yes, no) : pick(no, no));
     return launch_following(kernel, grid, kThreads, 0, st, a, tokens, each);
 }
 

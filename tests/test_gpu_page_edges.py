@@ -221,3 +221,30 @@ def test_rope_of_a_row_that_is_not_finite(interleaved, rot, normed, bad):
                 assert np.isnan(y).all()
             else:
                 assert np.isnan(y[at]) and (y[others] == 0).all(), at
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("eps", [0.0, 1e-40, 1e-30, 1e-6])
+@pytest.mark.parametrize("scale", [1e-38, 1e-30, 1e-23, 1e-20, 1e-16, 1e-3, 1e18])
+def test_rope_norm_of_any_magnitude(interleaved, eps, scale):
+    """Rows whose squares are below fp32's range, beside rows of its middle and of its upper end."""
+    rng = np.random.default_rng(31)
+    Hkv, G, T = 2, 4, 5
+    x = rng.standard_normal((T, Hkv * (G + 2), D)) * np.where(rng.random((T, Hkv * (G + 2), 1)) < 0.5, scale, 1.0)
+    qkv = bf(x).view(1, T, -1).to(DEV)
+    x = f64(qkv).reshape(T, -1, D)
+    w = bf(1 + 0.3 * rng.standard_normal(D))
+    f = 1e4 ** (-np.arange(64) / 64)
+    r = K.make_rope(Hkv * G, Hkv, torch.from_numpy(f).to(DEV), w.to(DEV), w.to(DEV), eps=eps,
+                    interleaved=interleaved)
+    q, k, v = (torch.zeros(Hkv, T, *s, D, dtype=torch.bfloat16, device=DEV) for s in ((G,), (), ()))
+    K.kvc_qk_norm_rope(r, qkv, i32([list(range(T))]), None, q, k, v)
+    for t in range(T):
+        for h in range(Hkv * (G + 2)):
+            y = (q[h // G, t, h % G] if h < Hkv * G else k[h - Hkv * G, t] if h < Hkv * (G + 1)
+                 else v[h - Hkv * (G + 1), t])
+            if h >= Hkv * (G + 1):
+                assert np.array_equal(f64(y), x[t, h])
+                continue
+            want, bound = R.norm_rope(x[t, h], f64(w), t, f, float(np.float32(eps)), interleaved, 1.0)
+            assert (np.abs(f64(y) - want) <= bound + R.BF * np.abs(want) + 1e-37).all(), (t, h)
