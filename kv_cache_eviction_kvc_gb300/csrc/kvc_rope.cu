@@ -49,9 +49,10 @@ struct RopeArgs {
 
 __device__ __forceinline__ uint64_t turn_fraction(double inv_freq)
 {
-    double t = inv_freq * 0.15915494309189533577;   // 1 / (2 pi)
+    double t = fabs(inv_freq) * 0.15915494309189533577;   // 1 / (2 pi)
     t -= floor(t);
-    return (uint64_t)(t * 18446744073709551616.0);
+    const uint64_t f = (uint64_t)(t * 18446744073709551616.0);
+    return inv_freq < 0 ? 0 - f : f;             // 1 - t would round a small t
 }
 
 __device__ __forceinline__ void unpack4(uint2 w, float *f)

@@ -248,3 +248,20 @@ def test_rope_norm_of_any_magnitude(interleaved, eps, scale):
                 continue
             want, bound = R.norm_rope(x[t, h], f64(w), t, f, float(np.float32(eps)), interleaved, 1.0)
             assert (np.abs(f64(y) - want) <= bound + R.BF * np.abs(want) + 1e-37).all(), (t, h)
+
+
+def test_rope_small_negative_frequencies():
+    """A negative frequency has the bits of the positive one: far positions at little angle."""
+    f = np.array([1e-13, 1e-11, 3e-10, 1e-9, 0.5, 7.5, 100.25, 1e-14])
+    x = np.zeros(D)
+    x[:len(f)] = 1.0                                       # y_2 of the pairs is then the sine
+    for pos in (2 ** 31 - 1, 123456789, -2 ** 31, 1):
+        up, _ = rotated(x, freq=f, pos=pos)
+        down, _ = rotated(x, freq=-f, pos=pos)
+        for y, sign in ((up, 1), (down, -1)):
+            want, bound = R.norm_rope(x, None, pos, sign * f, 0, False, 1.0)
+            for z in y:
+                small = np.abs(pos * f) < 1e-2             # where the angle is the sine: its own relative error
+                i = len(f) + np.arange(len(f))[small]
+                assert (np.abs(z - want)[i] <= (R.BF + 2.0 ** -20) * np.abs(want)[i]).all(), (pos, z[i], want[i])
+                assert (np.abs(z - want) <= bound + R.BF * np.abs(want)).all()
