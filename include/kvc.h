@@ -769,7 +769,8 @@ typedef struct {
                                KVC_PAGE_BF16                                 */
     const int32_t *table;   /* DEVICE [S][stride]: slot i of a sequence is row
                                i % page of page table[i / page].  Entries
-                               behind a call's last slot are not read        */
+                               behind a call's last slot are not read (but
+                               the first by kvc_page_attend)                 */
     const int32_t *len;     /* DEVICE [S] slots in use.  No call changes it:
                                one array may serve every layer of a step, and
                                the caller advances it once                   */
@@ -825,6 +826,9 @@ KVC_API kvc_status kvc_page_read(const kvc_pages *pg, int32_t M, int32_t ld, con
  *   x_i = q_h . k_i / sqrt(d), i in [0, n), over the values as they are held;
  *   lse = log sum_i exp(x_i), o = sum_i exp(x_i - lse) v_i.
  *   n = 0: lse = -inf, o = 0.
+ * A sequence of length 0 whose first entry of the table is -1 is a free place of
+ * the batch: a call that appends leaves its outputs as they were and records no
+ * error.
  * A NaN or an infinity of a value row reaches o alone, not lse; one in a key row
  * makes the logits it enters NaN or infinite, and where one is NaN or +infinite
  * lse and o of the head are NaN (all of them -infinite: as n = 0).

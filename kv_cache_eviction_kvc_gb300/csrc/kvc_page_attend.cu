@@ -801,6 +801,10 @@ __global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __gri
 
         // the warp's sums: o and lse of a whole unit, else a part
         bad = __any_sync(kFull, bad);
+        // a free place has no page for its token, which is no error
+        auto record_bad = [&]() {
+            if (!(app && n == 0 && a.pg.entry(cur.s, 0) == -1)) record_status(a.status, KVC_ERR_INVALID_ARG);
+        };
 #pragma unroll
         for (int i = 4; i < 32; i <<= 1) {
             l0 += __shfl_xor_sync(kFull, l0, i);
@@ -860,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __gri
                     join([&](int hh) { return sm.ml[lane][hh]; },
                          [&](int, int w, int hh) { return *reinterpret_cast<const float4 *>(&sm.o[w][hh][lane * 4]); });
                 else if (tid == 0)
-                    record_status(a.status, KVC_ERR_INVALID_ARG);
+                    record_bad();
                 return;
             }
             if (tid == 0) sm.bad = any_bad;
@@ -871,7 +875,7 @@ __global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __gri
                 join([&](int hh) { return far_float2(&sm.ml[lane % kWarps][hh], there); },
                      [&](int w0, int w, int hh) { return far_float4(&sm.o[w][hh][lane * 4], w0 / kWarps); });
             else if (id == 0 && lane == 0)
-                record_status(a.status, KVC_ERR_INVALID_ARG);
+                record_bad();
             // no CTA ends while another reads its sums
             cluster_arrive();
             cluster_wait();
@@ -906,7 +910,7 @@ __global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __gri
             }
         }
         if (lane == 0) {
-            if (whole && bad) record_status(a.status, KVC_ERR_INVALID_ARG);
+            if (whole && bad) record_bad();
             if (!whole) a.part_bad[part] = bad;
             if (first == 0) a.cuts[u] = make_int2(id, cuts.part(unit_at + tiles - 1));
         }

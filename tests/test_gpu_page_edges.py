@@ -265,3 +265,34 @@ def test_rope_small_negative_frequencies():
                 i = len(f) + np.arange(len(f))[small]
                 assert (np.abs(z - want)[i] <= (R.BF + 2.0 ** -20) * np.abs(want)[i]).all(), (pos, z[i], want[i])
                 assert (np.abs(z - want) <= bound + R.BF * np.abs(want)).all()
+
+
+# ---------------------------------------------------------------------- lengths, free places
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("n", [50, 300, 4000, 20000])
+def test_free_places_among_others(e4m3, n):
+    """However the work is cut: free places behind what another call left in the workspace."""
+    p = Pool(269, 2, [n, n, n, n, n], 16, e4m3, more=1)
+    check_attend(p, 4, units=[0, 9])
+    for free in ([0], [2, 3], [4], [0, 4], [0, 1, 2, 3, 4]):
+        tab = p.t["table"].clone()
+        lens = i32(p.lens)
+        for s in free:
+            p.t["len"][s] = 0
+            p.t["table"][s, 0] = -1
+        q, k, v, o, lse = attend(p, 4, max_len=n + 1)
+        assert p.status() == 0
+        for u in range(p.U):
+            if u // 2 in free:
+                assert (o[u] == 7).all() and (lse[u] == 7).all()
+            elif u in (1, 5, 8):
+                ro, rl, bo, bl = R.attend(f64(q[u]), p.held("K", u, range(n + 1)), p.held("V", u, range(n + 1)))
+                assert (np.abs(f64(o[u]) - ro) <= bo).all() and (np.abs(f64(lse[u]) - rl) <= bl).all(), (free, u)
+        # without a token to append, length 0 is nothing to attend over
+        _, _, _, o, lse = attend(p, 4, append=False, max_len=n + 1, q=q)
+        assert p.status() == 0
+        for s in free:
+            assert (o[2 * s] == 0).all() and (lse[2 * s] == -np.inf).all()
+        p.t["table"].copy_(tab)
+        p.t["len"].copy_(lens)
