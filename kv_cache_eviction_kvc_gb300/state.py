@@ -233,8 +233,11 @@ class DecodeState:
 class PagedState:
     """A cache in pages of `seqs` sequences of `heads` units (heads = 1: a table
     and a length per unit), with the pool's bookkeeping: pages are taken from a
-    free list on the host as sequences grow and go back when they end.  Calls run
-    on the current stream."""
+    free list on the host as sequences grow and go back when they end.  It holds
+    one layer, or all layers as units of a sequence.  Lengths advance by the rows
+    that were taken: a sequence that a call refuses (status()) keeps its length.
+    A place that holds no pages is free: steps leave it out.  Calls run on the
+    current stream."""
 
     def __init__(self, seqs: int, heads: int, G: int, max_len: int, *, page: int = 64,
                  e4m3: bool = True, n_pages: int | None = None, device="cuda", d: int = 128):
@@ -250,6 +253,7 @@ class PagedState:
         self.v_scale = torch.zeros(shape[:3], device=dev) if e4m3 else None
         self.table = torch.full((seqs, stride), -1, dtype=torch.int32, device=dev)
         self.len = torch.zeros(seqs, dtype=torch.int32, device=dev)
+        self.room = torch.zeros(seqs, dtype=torch.int32, device=dev)    # slots of the pages held
         self.pages = K_.make_pages(self.K, self.V, self.k_scale, self.v_scale, self.table, self.len)
         nbytes = K_.kvc_page_workspace_size(self.pages, G)
         if nbytes == 0:
@@ -282,29 +286,39 @@ class PagedState:
         if at:
             i = torch.tensor([at, value], dtype=torch.int64).to(self.device)
             self.table.view(-1).index_copy_(0, i[0], i[1].to(torch.int32))
+            self.room.copy_(torch.tensor([len(h) * self.page for h in self._held], dtype=torch.int32))
 
     def release(self, s: int):
-        """The pages of sequence s go back to the pool; its length becomes 0."""
+        """The pages of sequence s go back to the pool; its length becomes 0, its
+        place free."""
         self._free += reversed(self._held[s])
         self._held[s] = []
         self.table[s].fill_(-1)
         self.len[s].zero_()
+        self.room[s].zero_()
 
     # --------------------------------------------------------------- calls
     def write(self, k, v, count=None):
         """Rows k, v [U][T][d] behind what the sequences hold (count: int32
         [seqs], None: T rows each); the lengths advance.  Reserve their pages
-        before."""
+        before: a sequence without room for its rows keeps its length."""
         K_.kvc_page_write(self.pages, self.len, count, k, v, self.ws)
-        self.len.add_(k.shape[1] if count is None else count)
+        T = k.shape[1]
+        if count is None:
+            self.len.add_((self.len <= self.room - T) * T)
+        else:
+            taken = (count >= 0) & (count <= T) & (self.len + count <= self.room)
+            self.len.add_(torch.where(taken, count, 0))
 
     def step(self, q, k_new, v_new, max_len: int):
-        """One token per sequence: k_new, v_new [U][d] join the cache, q [U][G][d]
-        attends over it; the lengths advance.  max_len bounds the new lengths.
-        Returns (o [U][G][d] bf16, lse [U][G] fp32), written again by the next
-        call."""
+        """One token per sequence that holds pages: k_new, v_new [U][d] join the
+        cache, q [U][G][d] attends over it; the lengths advance.  max_len bounds
+        the new lengths; a sequence that has no slot left, or would pass max_len,
+        keeps its length.  Returns (o [U][G][d] bf16, lse [U][G] fp32), written
+        again by the next call (of free places and refused sequences: as they
+        were)."""
         K_.kvc_page_attend(self.pages, max_len, q, k_new, v_new, self.o, self.lse, self.ws)
-        self.len.add_(1)
+        self.len.add_(self.len < self.room.clamp(max=int(max_len)))
         return self.o, self.lse
 
     def read(self, M: int, slots=None, count=None):

@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import page_ref as R
+from kv_cache_eviction_kvc_gb300.state import PagedState
 from test_gpu_page import DEV, D, NAN, K, Pool, attend, bf, check_attend, f64, i32
 
 pytestmark = pytest.mark.gpu
@@ -268,6 +269,152 @@ def test_rope_small_negative_frequencies():
 
 
 # ---------------------------------------------------------------------- lengths, free places
+
+class Held:
+    """What the sequences of a PagedState hold, on the host, and steps against the definition."""
+
+    def __init__(self, st, seed):
+        self.st, self.rng = st, np.random.default_rng(seed)
+        self.U = st.seqs * st.heads
+        self.rows = [([], []) for _ in range(self.U)]
+        self.o, self.lse = st.o.clone(), st.lse.clone()
+
+    def store(self, x):
+        if self.st.K.dtype is torch.bfloat16:
+            return x
+        v, sc = R.quantise(x)
+        return f64(v) * sc.astype(np.float64)[..., None]
+
+    def write(self, T, count, taken):
+        k, v = (bf(self.rng.standard_normal((self.U, T, D))) for _ in range(2))
+        self.st.write(k.to(DEV), v.to(DEV), None if count is None else i32(count))
+        for u in range(self.U):
+            s = u // self.st.heads
+            if s in taken:
+                for have, x in zip(self.rows[u], (k, v)):
+                    have.extend(self.store(f64(x[u, :T if count is None else count[s]])))
+
+    def step(self, max_len, taken, call=None):
+        G = self.st.G
+        q = bf(self.rng.standard_normal((self.U, G, D))).to(DEV)
+        k, v = (bf(self.rng.standard_normal((self.U, D))).to(DEV) for _ in range(2))
+        o, lse = self.st.step(q, k, v, max_len) if call is None else call(q, k, v)
+        for u in range(self.U):
+            if u // self.st.heads not in taken:                # as it was, to the bit
+                assert torch.equal(o[u], self.o[u]) and torch.equal(lse[u], self.lse[u]), u
+                continue
+            for have, x in zip(self.rows[u], (k, v)):
+                have.append(self.store(f64(x[u])))
+            ro, rl, bo, bl = R.attend(f64(q[u]), *(np.array(x) for x in self.rows[u]))
+            assert (np.abs(f64(o[u]) - ro) <= bo).all() and (np.abs(f64(lse[u]) - rl) <= bl).all(), u
+        self.o, self.lse = o.clone(), lse.clone()
+        assert self.st.len.tolist() == self.lengths()
+
+    def release(self, s):
+        self.st.release(s)
+        for u in range(s * self.st.heads, (s + 1) * self.st.heads):
+            self.rows[u] = ([], [])
+
+    def lengths(self):
+        return [len(self.rows[s * self.st.heads][0]) for s in range(self.st.seqs)]
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("lens", [[40, 25, 33], [3000, 2500, 700], [17] * 500])
+def test_a_place_is_released_and_taken_again(e4m3, lens):
+    """The others step on; a free place records nothing, its outputs stay, and who takes it starts at
+    slot 0, over pages that held other rows."""
+    S, mine = len(lens), [0, 1, 2]
+    st = PagedState(S, 2, 4, max(lens) + 64, page=16, e4m3=e4m3)
+    h = Held(st, 251)
+    st.reserve([n + 20 for n in lens])
+    h.write(max(lens), lens, range(S))
+    every = set(range(S))
+    most = max(lens) + 40
+    h.step(most, every)
+    for s in (1, 2):
+        h.release(s)
+        every -= {s}
+        for _ in range(3):
+            h.step(most, every)
+            assert st.status() == 0
+    st.reserve([st.page * len(p) for p in st._held[:1]] + [22] + [0] * (S - 2))
+    h.write(20, [0, 20] + [0] * (S - 2), {1})
+    every |= {1}
+    assert st.status() == 0 and st.len.tolist()[1:3] == [20, 0]
+    h.step(most, every)
+    h.step(most, every)
+    assert st.status() == 0
+    k, v = st.read(most)
+    for u in (0, 2, 3, 4):
+        for out, rows in ((k, h.rows[u][0]), (v, h.rows[u][1])):
+            n = len(rows)
+            assert n == 0 or np.array_equal(f64(out[u, :n]), f64(bf(np.array(rows))))
+            assert (out[u, n:] == 0).all()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_refused_rows_do_not_count(e4m3):
+    """Past the pages, past max_len, and with counts that are none: lengths stay, the error is told,
+    and the next calls are right, rows that were written before it over the ones refused."""
+    st = PagedState(3, 2, 2, 128, page=16, e4m3=e4m3)
+    h = Held(st, 257)
+    st.reserve([32, 16, 48])
+    h.write(30, [30, 15, 30], {0, 1, 2})
+    h.step(64, {0, 1, 2})
+    assert st.status() == 0
+    h.step(64, {0, 2})                                     # sequence 1 has no slot left
+    assert st.status() == 1
+    h.step(64, {2})                                        # nor has 0
+    assert st.status() == 1
+    st.reserve([48, 32, 48])
+    h.step(33, {0, 1})                                     # 2 holds 33 already
+    assert st.status() == 2
+    h.step(64, {0, 1, 2})
+    assert st.status() == 0
+    h.write(14, [14, -1, 15], {0})
+    assert st.status() == 2 and st.len.tolist() == h.lengths()
+    h.write(15, [1, 15, 15], set())                        # they hold 48 of 48, 18 of 32 and 34 of 48
+    assert st.status() == 1 and st.len.tolist() == h.lengths()
+    h.write(15, [1, 14, 15], {1})
+    assert st.status() == 1 and st.len.tolist() == h.lengths()
+    st.reserve([64, 64, 64])
+    h.write(2, None, {0, 1, 2})
+    h.step(128, {0, 1, 2})
+    assert st.status() == 0
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_a_captured_step_follows_the_places(e4m3):
+    """A graph captured with every place taken, replayed with places free and taken again."""
+    lens = [900, 60, 300]
+    st = PagedState(3, 2, 4, 1024, page=16, e4m3=e4m3)
+    h = Held(st, 263)
+    st.reserve([n + 20 for n in lens])
+    h.write(max(lens), lens, {0, 1, 2})
+    h.step(1000, {0, 1, 2})
+    q, k, v = (torch.zeros(6, *s, D, dtype=torch.bfloat16, device=DEV) for s in ((4,), (), ()))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        st.step(q, k, v, 1000)
+
+    def call(*new):
+        for to, x in zip((q, k, v), new):
+            to.copy_(x)
+        g.replay()
+        return st.o, st.lse
+
+    h.step(1000, {0, 1, 2}, call)
+    h.release(0)
+    h.step(1000, {1, 2}, call)
+    h.step(1000, {1, 2}, call)
+    st.reserve([30, 0, 0])
+    h.write(10, [10, 0, 0], {0})
+    h.step(1000, {0, 1, 2}, call)
+    assert st.status() == 0
+
 
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("n", [50, 300, 4000, 20000])
