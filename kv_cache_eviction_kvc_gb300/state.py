@@ -334,7 +334,8 @@ class PagedState:
     def hand_over(self, st: DecodeState, slots, count):
         """The budgeted cache st of the same units takes count[u] (int32 [U]) of the
         slots listed in slots[u] (int32 [U][M], M <= cap): rows, positions and
-        lengths; utilities and moments start anew, as in load_prefill."""
+        lengths; utilities and moments start anew, as in load_prefill.  A unit
+        whose count or slots are refused (status()) is empty."""
         if st.U != self.seqs * self.heads or slots.shape[1] > st.cap:
             raise ValueError(f"{slots.shape[1]} slots of {self.seqs * self.heads} units for a cache "
                              f"of {st.U} units of {st.cap}")
@@ -343,7 +344,10 @@ class PagedState:
         if st.votes is not None:
             st.votes.fill_(1)
         st.util.fill_(float("inf"))
-        st.len.copy_(count)
+        behind = torch.arange(slots.shape[1], device=slots.device) >= count.unsqueeze(1)
+        held = self.len.repeat_interleave(self.heads).unsqueeze(1)
+        taken = (((slots >= 0) & (slots < held)) | behind).all(1) & (count >= 0) & (count <= slots.shape[1])
+        st.len.copy_(torch.where(taken, count, 0))
         for t in (st.n, st.mu_k, st.mu_v, st.C):
             t.zero_()
 

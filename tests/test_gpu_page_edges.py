@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import page_ref as R
-from kv_cache_eviction_kvc_gb300.state import PagedState
+from kv_cache_eviction_kvc_gb300.state import DecodeState, PagedState
 from test_gpu_page import DEV, D, NAN, K, Pool, attend, bf, check_attend, f64, i32
 
 pytestmark = pytest.mark.gpu
@@ -443,3 +443,35 @@ def test_free_places_among_others(e4m3, n):
             assert (o[2 * s] == 0).all() and (lse[2 * s] == -np.inf).all()
         p.t["table"].copy_(tab)
         p.t["len"].copy_(lens)
+
+
+def test_a_refused_selection_is_not_handed_over():
+    """Units whose count or slots the read refuses are empty in the budgeted cache, the others whole."""
+    lens = [40, 25, 33]
+    st = PagedState(3, 2, 4, 64, page=16, e4m3=False)
+    h = Held(st, 271)
+    st.reserve(lens)
+    h.write(40, lens, {0, 1, 2})
+    slots = torch.arange(20, dtype=torch.int32, device=DEV).repeat(6, 1)
+    ds = DecodeState(6, 4, 32, 24)
+    for bad in ("none", "long", "negative", "slot", "below", "behind"):
+        sl, count = slots.clone(), i32([20, 15, 0, 20, 1, 20])
+        if bad == "long":
+            count[1] = 21
+        elif bad == "negative":
+            count[1] = -1
+        elif bad == "slot":
+            sl[1, 14] = 40
+        elif bad == "below":
+            sl[1, 0] = -1
+        elif bad == "behind":                              # nobody asks for it
+            sl[1, 15] = 1 << 30
+        ds.K.fill_(7.0)
+        ds.len.fill_(5)
+        st.hand_over(ds, sl, count)
+        refused = bad in ("long", "negative", "slot", "below")
+        assert st.status() == (2 if refused else 0)
+        assert ds.len.tolist() == [20, 0 if refused else 15, 0, 20, 1, 20], bad
+        for u in range(6):
+            n = int(ds.len[u])
+            assert n == 0 or np.array_equal(f64(ds.K[u, :n]), f64(bf(np.array(h.rows[u][0][:n]))))
