@@ -475,3 +475,59 @@ def test_a_refused_selection_is_not_handed_over():
         for u in range(6):
             n = int(ds.len[u])
             assert n == 0 or np.array_equal(f64(ds.K[u, :n]), f64(bf(np.array(h.rows[u][0][:n]))))
+
+
+# ---------------------------------------------------------------------- long units
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("lens", [[131070], [131070, 65536], [100003] * 3, [70001] * 20, [65600, 3, 0] * 60])
+def test_every_slot_counts_once_in_a_long_unit(e4m3, lens):
+    """Equal weights: lse is log n to a fraction of 1/n, so no slot is missing or there twice.  The
+    values are zero but in slots around the places where the line of tiles is cut for the warps, each
+    with a dimension of its own: o is their value over n."""
+    p = Pool(277, 1, lens, 64, e4m3, more=1)
+    tile = 32 if e4m3 else 16
+    tiles = [-(-(n + 1) // tile) for n in lens]
+    total, warps = sum(tiles), 152 * 3 * 4
+    cuts = [c * (total // warps) + min(c, total % warps) for c in range(warps)]
+    some, want = sorted({0, len(lens) // 2, len(lens) - 1}), {}
+    v_new = np.zeros((p.U, D))
+    for u in some:
+        n, first = lens[u], sum(tiles[:u])
+        edges = [(c - first) * tile for c in cuts if first < c < first + tiles[u]]
+        at = {0, n - 1, 63, 64} | {int(e) + d for e in p.rng.permutation(edges)[:40] for d in (-1, 0)}
+        at |= {int(x) for x in p.rng.integers(0, max(n, 1), 30)}
+        at = sorted(x for x in at if 0 <= x < n)[:D - 1]
+        x = np.zeros((n, D))
+        x[at, range(len(at))] = 1000.0 + np.arange(len(at))
+        v_new[u, D - 1] = 555.0
+        if n:
+            put(p, "V", u, range(n), x)
+        want[u] = at
+    zero = bf(np.zeros((p.U, D))).to(DEV)
+    _, _, _, o, lse = attend(p, 4, q_scale=0.0, k=zero, v=bf(v_new).to(DEV))
+    assert p.status() == 0
+    for u, at in want.items():
+        n = lens[u] + 1
+        expect = np.zeros(D)
+        if at:
+            expect[:len(at)] = p.held("V", u, at)[range(len(at)), range(len(at))]
+        expect[D - 1] = p.held("V", u, [n - 1])[0, D - 1]
+        expect /= n
+        # the weights are 1 and their sum is exact: a quotient (2 ulp) and the rounding to bf16
+        assert (np.abs(f64(o[u]) - expect) <= (R.BF + 2.0 ** -20) * np.abs(expect)).all(), u
+        # a logarithm to base 2 to an ulp, its product with ln 2 (rounded to 2^-25 of itself)
+        y = np.log(n)
+        bound = np.spacing(np.float32(np.log2(n))) * np.log(2) + 2.0 ** -25 * y + np.spacing(np.float32(y)) / 2
+        assert n < 1000 or bound < 0.5 / n
+        assert np.abs(f64(lse[u]) - y).max() <= bound, u
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("G", [1, 8])
+@pytest.mark.parametrize("n,k_scale", [(131071, 4.0), (20011, 10.0), (131071, 30.0)])
+def test_sharp_attention_over_long_units(e4m3, G, n, k_scale):
+    """A few slots have nearly all of the weight, wherever they are; each head has others."""
+    p = Pool(n + G, 1, [n, n // 3, 40], 64, e4m3, more=1, k_scale=k_scale)
+    check_attend(p, G)
+    check_attend(p, G, append=False, units=[0])
