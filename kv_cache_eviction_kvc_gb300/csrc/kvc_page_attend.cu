@@ -1010,9 +1010,10 @@ cudaError_t launch_page_attend(const kvc_pages &pg, int G, int max_len, const ui
         const int64_t blocks = (rows - 1) / per_block + 1;
         return launch_following(f, dim3((unsigned)(blocks < fill ? blocks : fill)), threads, 0, st, a);
     };
-    // as many warps per row as keep a unit's parts in about one round of loads (8 units of 131071
-    // slots, 171 parts each: 16 warps 83.6 us a call, 32 84.6; 128 units, 16 parts of 8 heads: two
-    // warps 34.4, four 33.7, eight 37.8; 1024 units, two or three parts: one warp 41.6, two 43.1)
+    // warps per row by the parts that a unit may have, each with a share of them (8 units of 131071
+    // slots, 228 or 229 parts each: eight warps 85.4 us in a graph, 16 84.7, 32 85.4; 128 units, 16
+    // parts of 8 heads: two warps 35.3, four 34.4, eight 39.1; 1024 units, two or three parts: one warp
+    // 43.1, two 45.7)
     const int parts = kWorkers / pg.U + 2;
     if (parts <= 8) return join(join_kernel<1>, 8, 256);
     if (parts <= 32) return join(join_kernel<4>, 2, 256);

@@ -233,10 +233,11 @@ class DecodeState:
 class PagedState:
     """A cache in pages of `seqs` sequences of `heads` units (heads = 1: a table
     and a length per unit), with the pool's bookkeeping: pages are taken from a
-    free list on the host as sequences grow and go back when they end.  It holds
-    one layer, or all layers as units of a sequence.  Lengths advance by the rows
-    that were taken: a sequence that a call refuses (status()) keeps its length.
-    A place that holds no pages is free: steps leave it out.  Calls run on the
+    free list on the host as sequences grow and go back when they end.  It is
+    one layer's; the calls themselves leave the lengths alone, so that layers may
+    share a table and a length (kvc.make_pages).  Lengths advance by the rows that
+    were taken: a sequence that a call refuses (status()) keeps its length.  A
+    place that holds no pages is free: steps leave it out.  Calls run on the
     current stream."""
 
     def __init__(self, seqs: int, heads: int, G: int, max_len: int, *, page: int = 64,
