@@ -836,7 +836,10 @@ KVC_API kvc_status kvc_page_read(const kvc_pages *pg, int32_t M, int32_t ld, con
  * lse [U][G] fp32.  q, o, k_new, v_new are 16-byte aligned.  Logits, sums and
  * outputs are fp32 until that one rounding; weights enter the products as two
  * 16-bit terms (2^-17 of a weight is left out with bf16 values; with e4m3 ones
- * 2^-22, and 2^-31 of the largest contribution).  max_len bounds n with the
+ * 2^-22, and 2^-31 of the largest contribution); one below 2^-126 of the
+ * largest may count as none, and bf16 values whose sum, over weights of up to
+ * 2^8 each, passes fp32's range are infinite.  Beside e4m3 keys an element of q
+ * keeps its bits down to 2^-27 of its head's largest.  max_len bounds n with the
  * appended token, 1 <= max_len <= stride * page; a bound far above the lengths
  * costs short units a few microseconds, no more.  Outputs do not overlap inputs;
  * calls that append to the same units are ordered by the caller.

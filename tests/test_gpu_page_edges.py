@@ -531,3 +531,22 @@ def test_sharp_attention_over_long_units(e4m3, G, n, k_scale):
     p = Pool(n + G, 1, [n, n // 3, 40], 64, e4m3, more=1, k_scale=k_scale)
     check_attend(p, G)
     check_attend(p, G, append=False, units=[0])
+
+
+@pytest.mark.parametrize("G", [4, 8])
+@pytest.mark.parametrize("n", [20, 300, 9000])
+@pytest.mark.parametrize("octaves,ratio", [(100, 2.0 ** 100), (125, 2.0 ** 124), (138, 2.0 ** 138), (150, 2.0 ** 150),
+                                           (300, 2.0 ** 200), (2000, 2.0 ** 200)])
+def test_a_large_value_of_a_weight_below_fp32(G, n, octaves, ratio):
+    """In e4m3 a value 2^100 and more above the others counts by its contribution, whether or not its
+    weight is one that fp32 holds, and leaves the others theirs where it has none."""
+    p = Pool(281, 1, [n, n], 16, True)
+    q = np.zeros((2, G, D))
+    q[:, :, 0] = 4
+    low = 2.0 ** -100
+    for u, at in ((0, n // 3), (1, n - 1)):
+        put(p, "K", u, range(n), np.zeros((n, D)))
+        put(p, "K", u, [at], -octaves * np.log(2) * np.sqrt(D) / 4 * spike(0)[None])
+        put(p, "V", u, range(n), low * (1 + p.rng.random((n, D))))
+        put(p, "V", u, [at], low * ratio * spike(0, 64)[None])
+    check_attend(p, G, append=False, q=bf(q).to(DEV))
