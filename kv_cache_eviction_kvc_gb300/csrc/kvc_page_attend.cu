@@ -42,10 +42,10 @@
 // Short units that all fit at once go whole to a cluster each, whose warps take its
 // tiles in turn and join over distributed shared memory: no line, no second kernel.
 //
-// Measured, calls replayed as a graph: 8 units x 131071 slots bf16 84 us (6.4 TB/s;
-// 80.8 without the join), 128 units x <= 32768 e4m3 138 us (6.6; 135.8), 1024 units x
-// <= 1024 e4m3 41.7 us (5.1; 37.2), 128 x <= 3277 bf16 with 8 heads 34 us (5.2; 29.9),
-// 8 x 64 3.8 us.  What is left is a chain of waits at either end: lengths, pages,
+// Measured, calls replayed as a graph: 8 units x 131071 slots bf16 85 us (6.3 TB/s),
+// 128 units x <= 32768 e4m3 146.6 us (6.2; 145.4 with one reference for the weights' sum
+// and the contributions), 1024 units x <= 1024 e4m3 43.2 us (4.9; 42.7), 128 x <= 3277
+// bf16 with 8 heads 34.9 us (5.1), 8 x 64 3.7 us.  What is left is a chain of waits at either end: lengths, pages,
 // first rows (about 3 us), the join (4 us, of which an empty kernel is 0.5 and reading
 // the cuts 0.9).  Tried and slower: the next tiles in a ring of shared memory filled by
 // cp.async (8 x 131071: 115); a tile of a CTA's four warps with a barrier per unit (1024
@@ -978,15 +978,16 @@ cudaError_t launch_page_attend(const kvc_pages &pg, int G, int max_len, const ui
     const int tile = e4m3 ? Frags<true>::kSlots : Frags<false>::kSlots;
     // Short units go whole to a cluster each: as many CTAs as there are SMs for, four tiles at least
     // for each, at most ten for a warp.  In a graph, cluster / line (8 units in clusters of 8, 32 of
-    // 4, 64 of 2, 128 and 456 alone): e4m3, 512 slots 6.6 / 8.9, 6.8 / 9.4, 7.5 / 9.6, 8.2 / 11.4,
-    // 12.9 / 18.2 us; 1024 slots 7.3 / 9.5, 7.8 / 10.3, 9.5 / 11.6, 13.9 / 14.3, 21.3 / 25.0; 4096
-    // slots 10.1 / 11.5, 15.1 / 14.8, 25.7 / 18.7, 45 / 27; bf16, 4096 slots 10.7 / 14.2, 21.1 /
-    // 17.6.  Larger clusters: 64 units of 512 slots in e4m3 8.9 in 4, 14.5 in 8.  Up to two CTAs'
-    // worth of units: 768 of 256 slots 16.2 / 18.8 in e4m3, 18.6 / 22.1 in bf16; 1024 of them 20.8 /
-    // 20.6 and 24.6 / 25.7.  With many units the line's warps lose about 1 us at the end of each,
-    // which other CTAs hide: in bf16, of 128 slots on, 2048 units of 512 slots 70.7 / 77.3, 4096
-    // 132 / 148, of 1024 slots 131 / 140 (4096 of 64 40.7 / 36.5; in e4m3 no gain: 2048 of 512 49.9 /
-    // 48.8, 4096 of 256 63 / 56).
+    // 4, 64 of 2, 128 and 456 alone): e4m3, 512 slots 6.8 / 8.4, 7.1 / 9.2, 7.9 / 10.7, 9.4 / 13.4,
+    // 14.9 / 21.0 us; 1024 slots 7.4 / 8.6, 8.1 / 10.4, 10.7 / 13.7, 15.3 / 16.0, 23.5 / 29.5; 4096
+    // slots 11.2 / 10.7, 16.4 / 15.2, 26.4 / 21.1, 46 / 31 (the first two go whole all the same, for
+    // the lengths between); bf16, 1024 slots 6.7 / 7.7, 9.2 / 11.5, 4096 slots 12.9 / 12.3, 21.2 /
+    // 18.0.  Larger clusters: 64 units of 512 slots in e4m3 8.9 in 4, 14.5 in 8.  Up to two CTAs'
+    // worth of units: 768 of 256 slots 18.9 / 19.6 in e4m3, 21.1 / 24.1 in bf16; 1024 of them 25.5 /
+    // 22.5 and 29.5 / 29.0.  With many units the line's warps lose about 1 us at the end of each,
+    // which other CTAs hide: in bf16, of 128 slots on, 2048 units of 512 slots 88.3 / 91.5, 4096
+    // 166 / 179, of 1024 slots 164 / 172 (4096 of 64 45.2 / 36.9; in e4m3 no gain: 2048 of 512 62.5 /
+    // 57.2, 4096 of 256 78 / 64).
     const int tiles_each = (max_len - 1) / tile + 1;
     int cluster = 8;
     while (cluster > 1 && ((int64_t)pg.U * cluster > 152 || 4 * cluster > tiles_each)) cluster /= 2;

@@ -17,8 +17,10 @@
 // weights, cosine and sine are one 2x2 of a pair, formed once per token and kind of
 // head, applied in packed fp32 pairs.  Value heads go along with the key heads, so
 // that a tile waits for memory three times and not four (135.6 -> 133.2 us).
-// Measured: one token of 48 heads 6.5 us (3.2 in a graph), 16 x 24 tokens 7.0 (4.2),
-// 32768 tokens 131 (6.2 TB/s; a block per token without the 2x2 took 319).  Four
+// Measured: one token of 48 heads 6.5 us (3.0 in a graph), 16 x 24 tokens 7.0 (4.2),
+// 32768 tokens 129 (6.2 TB/s; a block per token without the 2x2 took 319), 262144 of
+// 6 rows 176 (floor 120): a tile's turns are formed before its rows are asked for,
+// though the rows do not depend on them.  Variants, measured at 131 to 133: four
 // blocks of 64 registers and four rows in flight per team, against (with value heads
 // by themselves): two rows 150, three 146, three blocks 152, two of 100 registers 181;
 // loads and stores marked as streaming 141; the next position loaded ahead 146.
