@@ -688,7 +688,10 @@ __global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __gri
 #pragma unroll
                 for (int j = 0; j < 4; j++) x[b][j] += y[j];
             }
-            // logits in base 2, what is not there at -inf; the references' candidates
+            // logits in base 2 over the reference, what is not there at -inf; how far the tile passes
+            // the references.  (The reference first: beside a large logit a scale's exponent is lost.
+            // Products are rounded before it, so that equal ones stay equal.)
+            const float ref0 = m0 == -INFINITY ? 0.f : m0, ref1 = m1 == -INFINITY ? 0.f : m1;
             float top0 = -INFINITY, top1 = -INFINITY, out0 = -INFINITY, out1 = -INFINITY;
             float vs[2 * kBlocks], high = 0.f;   // the values' scales, their largest exponent
 #pragma unroll
@@ -704,8 +707,8 @@ __global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __gri
                         up = scale_exponent(f.vs[b * 2 + r]);
                         high = fmaxf(high, up);
                     }
-                    x[b][2 * r] = on ? x[b][2 * r] * c0 : -INFINITY;
-                    x[b][2 * r + 1] = on ? x[b][2 * r + 1] * c1 : -INFINITY;
+                    x[b][2 * r] = on ? __fmul_rn(x[b][2 * r], c0) - ref0 : -INFINITY;
+                    x[b][2 * r + 1] = on ? __fmul_rn(x[b][2 * r + 1], c1) - ref1 : -INFINITY;
                     top0 = fmaxf(top0, x[b][2 * r]);
                     top1 = fmaxf(top1, x[b][2 * r + 1]);
                     if (kE4m3) {
@@ -716,32 +719,45 @@ __global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __gri
             load(true);
             // contributions are at most 2^7 where their reference is met, 2^15 with the slack
             constexpr float kUp = 6.f;
-            bool past = top0 > m0 + kSlack || top1 > m1 + kSlack;
-            if (kE4m3) past |= out0 > m0 + e0 + (kUp + kSlack) || out1 > m1 + e1 + (kUp + kSlack);
+            bool past = top0 > (m0 == -INFINITY ? -INFINITY : kSlack) || top1 > (m1 == -INFINITY ? -INFINITY : kSlack);
+            if (kE4m3) past |= out0 > e0 + (kUp + kSlack) || out1 > e1 + (kUp + kSlack);
             if (__any_sync(kFull, past)) {
 #pragma unroll
                 for (int i = 4; i < 32; i <<= 1) {
                     top0 = fmaxf(top0, __shfl_xor_sync(kFull, top0, i));
                     top1 = fmaxf(top1, __shfl_xor_sync(kFull, top1, i));
-                    if (kE4m3) {
+                }
+                // by how much m moves; from -inf the sums, which are zero, take no part
+                const bool new0 = m0 == -INFINITY, new1 = m1 == -INFINITY;
+                const float n0 = new0 ? top0 : m0 + fmaxf(top0, 0.f), n1 = new1 ? top1 : m1 + fmaxf(top1, 0.f);
+                const float by0 = n0 == -INFINITY ? 0.f : n0 - ref0, by1 = n1 == -INFINITY ? 0.f : n1 - ref1;
+                float d0 = new0 ? -INFINITY : -by0, d1 = new1 ? -INFINITY : -by1;
+                l0 *= pow2(d0), l1 *= pow2(d1);
+                m0 = n0, m1 = n1;
+#pragma unroll
+                for (int b = 0; b < kBlocks; b++) x[b][0] -= by0, x[b][1] -= by1, x[b][2] -= by0, x[b][3] -= by1;
+                if (kE4m3) {
+                    out0 = out1 = -INFINITY;
+#pragma unroll
+                    for (int b = 0; b < kBlocks; b++)
+#pragma unroll
+                        for (int r = 0; r < 2; r++) {
+                            const float up = scale_exponent(vs[b * 2 + r]);
+                            out0 = fmaxf(out0, x[b][2 * r] + up), out1 = fmaxf(out1, x[b][2 * r + 1] + up);
+                        }
+#pragma unroll
+                    for (int i = 4; i < 32; i <<= 1) {
                         out0 = fmaxf(out0, __shfl_xor_sync(kFull, out0, i));
                         out1 = fmaxf(out1, __shfl_xor_sync(kFull, out1, i));
                     }
-                }
-                const float n0 = fmaxf(m0, top0), n1 = fmaxf(m1, top1);
-                float d0 = m0 == n0 ? 0.f : m0 - n0, d1 = m1 == n1 ? 0.f : m1 - n1;
-                l0 *= pow2(d0), l1 *= pow2(d1);
-                m0 = n0, m1 = n1;
-                if (kE4m3) {
                     d0 += e0, d1 += e1;          // the old reference over the new m
-                    e0 = fmaxf(ceilf(fmaxf(d0, out0 - n0 - kUp)), 1.f), e1 = fmaxf(ceilf(fmaxf(d1, out1 - n1 - kUp)), 1.f);
+                    e0 = fmaxf(ceilf(fmaxf(d0, out0 - kUp)), 1.f), e1 = fmaxf(ceilf(fmaxf(d1, out1 - kUp)), 1.f);
                     d0 -= e0, d1 -= e1;
                 }
                 const float r0 = pow2(d0), r1 = pow2(d1);
 #pragma unroll
                 for (int i = 0; i < 8; i++) acc[i][0] *= r0, acc[i][1] *= r1, acc[i][2] *= r0, acc[i][3] *= r1;
             }
-            const float ref0 = m0 == -INFINITY ? 0.f : m0, ref1 = m1 == -INFINITY ? 0.f : m1;
             // weights, O' += V' P'
             const float s0 = pow2(127.f - e0), s1 = pow2(127.f - e1);
             // a value 2^100 above its reference, of a weight that fp32 may not hold: the
@@ -751,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __gri
             for (int b = 0; b < kBlocks; b++) {
                 float p[4];
 #pragma unroll
-                for (int j = 0; j < 4; j++) p[j] = pow2(x[b][j] - (j & 1 ? ref1 : ref0));
+                for (int j = 0; j < 4; j++) p[j] = pow2(x[b][j]);
                 l0 += p[0] + p[2];
                 l1 += p[1] + p[3];
                 if (kE4m3) {
@@ -761,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, kResident) attend_kernel(const __gri
 #pragma unroll
                         for (int j = 0; j < 4; j++) {
                             const float v = vs[b * 2 + (j >> 1)], up = scale_exponent(v);
-                            p[j] = pow2(x[b][j] - (j & 1 ? ref1 : ref0) + (up - (j & 1 ? e1 : e0))) *
+                            p[j] = pow2(x[b][j] + (up - (j & 1 ? e1 : e0))) *
                                    (up == 0.f ? v : __uint_as_float((__float_as_uint(v) & 0x807fffff) | 0x3f800000));
                         }
                 }

@@ -550,3 +550,65 @@ def test_a_large_value_of_a_weight_below_fp32(G, n, octaves, ratio):
         put(p, "V", u, range(n), low * (1 + p.rng.random((n, D))))
         put(p, "V", u, [at], low * ratio * spike(0, 64)[None])
     check_attend(p, G, append=False, q=bf(q).to(DEV))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("G,lens", [(4, [300, 40]), (8, [9000, 70]), (4, [600] * 1000)])
+@pytest.mark.parametrize("size", [1e9, 1e15, 1e30])
+@pytest.mark.parametrize("v_scale", [1e-20, 1.0, 1e30])
+def test_logits_of_any_size(e4m3, G, lens, size, v_scale):
+    """Logits of plus and minus `size`: the slots of the larger one share the weight, whatever their
+    values' scale, and lse is that logit and the logarithm of their number.  Slots of the smaller one
+    with the largest values weigh nothing."""
+    p = Pool(283, 1, lens, 16, e4m3)
+    some = sorted({0, p.U // 2, p.U - 1})
+    q = np.zeros((p.U, G, D))
+    q[:, :, 0] = np.sqrt(size)
+    first = {}
+    for u in some:
+        n = lens[u]
+        up = p.rng.random(n) < 0.3
+        up[p.rng.integers(n)] = True
+        first[u] = up
+        put(p, "K", u, range(n), np.where(up, 1.0, -1.0)[:, None] * np.sqrt(size) * spike(0))
+        put(p, "V", u, range(n), v_scale * np.where(up, 1.0, 1e3)[:, None] * (1 + p.rng.random((n, D))))
+    _, _, _, o, lse = attend(p, G, append=False, q=bf(q).to(DEV))
+    assert p.status() == 0
+    qh = f64(bf(q))
+    for u in some:
+        rows = np.nonzero(first[u])[0]
+        want = p.held("V", u, rows).mean(0)
+        # equal weights of 1: their sums of n terms, a quotient and the rounding to bf16
+        assert (np.abs(f64(o[u]) - want) <= (R.BF + (len(rows) + 16) * 2.0 ** -24) * want).all(), u
+        x = qh[u, 0, 0] * p.held("K", u, rows[:1])[0, 0] / np.sqrt(D)
+        assert (np.abs(f64(lse[u]) - (x + np.log(len(rows)))) <= 16 * 2.0 ** -24 * x).all(), u
+
+
+@pytest.mark.parametrize("lens", [[300, 40], [9000, 70, 700], [600] * 1000])
+def test_infinite_keys(lens):
+    """Keys with an infinity, in bf16: a logit of -inf weighs nothing, all of them are no slots at all,
+    one of +inf or a NaN makes lse and o of its head NaN."""
+    p = Pool(293, 1, lens, 16, False)
+    u, n = 1, lens[1]
+    q = p.rng.standard_normal((p.U, 4, D))
+    q[:, :, 0] = [1, -1, 0, -2]
+    q = bf(q)
+    k = p.rng.standard_normal((n, D))
+    k[:, 0] = 0.5
+    k[n // 2, 0] = np.inf
+    put(p, "K", u, range(n), k)
+    _, _, _, o, lse = attend(p, 4, append=False, q=q.to(DEV))
+    rest = [i for i in range(n) if i != n // 2]
+    for h in (1, 3):
+        ro, rl, bo, bl = R.attend(f64(q[u, h])[None], p.held("K", u, rest), p.held("V", u, rest))
+        assert (np.abs(f64(o[u, h]) - ro[0]) <= bo[0]).all() and abs(float(lse[u, h]) - rl[0]) <= bl[0]
+    for h in (0, 2):
+        assert o[u, h].isnan().all() and lse[u, h].isnan()
+    k[:, 0] = np.inf
+    put(p, "K", u, range(n), k)
+    _, _, _, o, lse = attend(p, 4, append=False, q=q.to(DEV))
+    for h in (1, 3):
+        assert (o[u, h] == 0).all() and lse[u, h] == -np.inf
+    for h in (0, 2):
+        assert o[u, h].isnan().all() and lse[u, h].isnan()
+    assert not o[0].isnan().any() and not lse[0].isnan().any() and p.status() == 0
