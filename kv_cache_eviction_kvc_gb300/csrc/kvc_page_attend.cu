@@ -19,8 +19,8 @@
 // off instead of rounding them, which adds up over a long run (3e-6 of o over 2300
 // slots of a warp), so it has the 16 slots of a product alone and those are added with
 // rounding (no cost but with eight heads over e4m3: 32 units x 16000 32.2 -> 33.3 us;
-// the 32 slots of a tile at once spill, 146.5 -> 149.2 for 128 units x <= 32768).  Weights enter O' as two
-// 16-bit terms (bf16 beside bf16 values, 2^-17 of a weight left; f16 beside e4m3
+// the 32 slots of a tile at once spill, 146.5 -> 149.2 for 128 units x <= 32768).
+// Weights enter O' as two 16-bit terms (bf16 beside bf16 values, 2^-17 of a weight left; f16 beside e4m3
 // values, which f16 holds exactly).  Queries beside e4m3 keys are f16 after a
 // power of two per head puts the largest at 2^13: bf16's 8 bits fit f16's 11 down
 // to 2^-27 of it.  With e4m3 values there are two references: the weights' sum has the
@@ -45,9 +45,9 @@
 // Measured, calls replayed as a graph: 8 units x 131071 slots bf16 85 us (6.3 TB/s),
 // 128 units x <= 32768 e4m3 146.6 us (6.2; 145.4 with one reference for the weights' sum
 // and the contributions), 1024 units x <= 1024 e4m3 43.2 us (4.9; 42.7), 128 x <= 3277
-// bf16 with 8 heads 34.9 us (5.1), 8 x 64 3.7 us.  What is left is a chain of waits at either end: lengths, pages,
-// first rows (about 3 us), the join (4 us, of which an empty kernel is 0.5 and reading
-// the cuts 0.9).  Tried and slower: the next tiles in a ring of shared memory filled by
+// bf16 with 8 heads 34.9 us (5.1), 8 x 64 3.7 us.  What is left is a chain of waits at
+// either end: lengths, pages, first rows (about 3 us), the join (4 us, of which an empty
+// kernel is 0.5 and reading the cuts 0.9).  Tried and slower: the next tiles in a ring of shared memory filled by
 // cp.async (8 x 131071: 115); a tile of a CTA's four warps with a barrier per unit (1024
 // units: 48); e4m3 tiles of 16 slots (47, and 44.5 with four CTAs per SM); joins by the
 // last CTA or warp to come (registers spill); a CTA's parts joined in shared memory
@@ -994,12 +994,12 @@ cudaError_t launch_page_attend(const kvc_pages &pg, int G, int max_len, const ui
     const int tile = e4m3 ? Frags<true>::kSlots : Frags<false>::kSlots;
     // Short units go whole to a cluster each: as many CTAs as there are SMs for, four tiles at least
     // for each, at most ten for a warp.  In a graph, cluster / line (8 units in clusters of 8, 32 of
-    // 4, 64 of 2, 128 and 456 alone): e4m3, 512 slots 6.8 / 8.4, 7.1 / 9.2, 7.9 / 10.7, 9.4 / 13.4,
-    // 14.9 / 21.0 us; 1024 slots 7.4 / 8.6, 8.1 / 10.4, 10.7 / 13.7, 15.3 / 16.0, 23.5 / 29.5; 4096
-    // slots 11.2 / 10.7, 16.4 / 15.2, 26.4 / 21.1, 46 / 31 (the first two go whole all the same, for
+    // 4, 64 of 2, 128 and 456 alone): e4m3, 512 slots 7.0 / 8.4, 7.3 / 9.2, 8.2 / 10.7, 9.7 / 13.4,
+    // 15.1 / 21.0 us; 1024 slots 7.7 / 8.6, 8.4 / 10.4, 11.0 / 13.7, 15.5 / 16.0, 23.7 / 29.5; 4096
+    // slots 11.6 / 10.7, 16.7 / 15.2, 26.4 / 21.1, 46 / 31 (the first two go whole all the same, for
     // the lengths between); bf16, 1024 slots 6.7 / 7.7, 9.2 / 11.5, 4096 slots 12.9 / 12.3, 21.2 /
     // 18.0.  Larger clusters: 64 units of 512 slots in e4m3 8.9 in 4, 14.5 in 8.  Up to two CTAs'
-    // worth of units: 768 of 256 slots 18.9 / 19.6 in e4m3, 21.1 / 24.1 in bf16; 1024 of them 25.5 /
+    // worth of units: 768 of 256 slots 19.4 / 19.6 in e4m3, 21.1 / 24.1 in bf16; 1024 of them 25.5 /
     // 22.5 and 29.5 / 29.0.  With many units the line's warps lose about 1 us at the end of each,
     // which other CTAs hide: in bf16, of 128 slots on, 2048 units of 512 slots 88.3 / 91.5, 4096
     // 166 / 179, of 1024 slots 164 / 172 (4096 of 64 45.2 / 36.9; in e4m3 no gain: 2048 of 512 62.5 /

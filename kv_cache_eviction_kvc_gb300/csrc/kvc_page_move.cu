@@ -13,7 +13,7 @@
 //
 // Measured: 8 units x 32768 rows to bf16 40.7 us (6.6 TB/s; 40.3 in a graph), to e4m3
 // 33.2 (6.1); 8 x 131071 rows back 157 (6.8, what fits L2 among it) and 124 (6.5); 32
-// units x <= 3277 listed rows of 32768 back from bf16 16.0 us (5.4); 32 units x <= 3277 listed rows of 32768 back 14.1 us (4.7 TB/s:
+// units x <= 3277 listed rows of 32768 back 16.0 us (5.4) and from e4m3 14.1 (4.7 TB/s:
 // the scale of a listed row brings 64 bytes from memory, 15 % more in all, and the
 // chain of loads starts and ends it; loading the next rows' slots and pages ahead in
 // longer-lived blocks took 14.5 to 16).  Rows in flight per team, the same
